@@ -98,6 +98,11 @@ _SIGS = {
                                       C.POINTER(C.c_int), C.POINTER(C.c_int)]),
     "coll_allreduce_static": (C.c_int, [C.c_int, C.c_int, _P, _P, C.c_uint64, C.c_int,
                                         C.c_int64, C.c_int, C.c_int64, _P, _P]),
+    # dense operators: a packed argument structure, the stream
+    **{name: (C.c_int, [C.c_char_p, _P]) for name in
+       ("coll_linear", "coll_linear_backward", "coll_gated_ffn", "coll_gated_ffn_backward")},
+    **{name + "_workspace": (C.c_int64, [C.c_char_p]) for name in
+       ("coll_linear", "coll_linear_backward", "coll_gated_ffn", "coll_gated_ffn_backward")},
 }
 
 _lib = None

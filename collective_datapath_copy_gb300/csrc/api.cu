@@ -570,6 +570,7 @@ extern "C" const char *coll_strerror(int code) {
     case COLL_EDEVICE: return "inconsistent device state";
     case COLL_ENOMEM: return "out of memory";
     case COLL_ETOOBIG: return "request exceeds the fixed static scratch array or co-residency";
+    case COLL_EWORKSPACE: return "workspace missing, unaligned or too small";
     default: return "unknown error";
   }
 }

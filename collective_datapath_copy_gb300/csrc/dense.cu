@@ -1,0 +1,409 @@
+// C ABI of the dense operators (include/coll.h): argument checks, workspace layout, and which
+// kernels a call launches.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dense.h"
+
+namespace {
+
+using coll::DenseActBwd;
+using coll::DenseJob;
+using coll::DenseMat;
+
+// Bump allocator over the caller's workspace. With base == nullptr it only counts.
+struct Ws {
+  char *base;
+  uint64_t used;
+  void *take(uint64_t bytes) {
+    const uint64_t at = used;
+    used += (bytes + 255) & ~(uint64_t)255;
+    return base ? base + at : nullptr;
+  }
+};
+
+int64_t round8(int64_t v) { return (v + 7) & ~(int64_t)7; }
+
+bool is_half(int64_t t) { return t == COLL_BF16 || t == COLL_F16; }
+int esize(int64_t t) { return t == COLL_F32 ? 4 : 2; }
+
+// A matrix with its extent, for the checks.
+struct View {
+  const void *p;
+  int64_t rows, cols, rs, cs;
+  int es;
+};
+
+View view(const coll_mat_t &m, int64_t rows, int64_t cols, int es) {
+  return View{m.ptr, rows, cols, m.rs, m.cs, es};
+}
+
+bool empty(const View &v) { return !v.p || v.rows <= 0 || v.cols <= 0; }
+
+void range(const View &v, uintptr_t &lo, uintptr_t &hi) {
+  const int64_t r = (v.rows - 1) * v.rs, c = (v.cols - 1) * v.cs;
+  const int64_t a = (r < 0 ? r : 0) + (c < 0 ? c : 0), b = (r > 0 ? r : 0) + (c > 0 ? c : 0);
+  lo = (uintptr_t)v.p + (intptr_t)(a * v.es);
+  hi = (uintptr_t)v.p + (intptr_t)((b + 1) * v.es);
+}
+
+// Do two views share memory? Exact for rows of the same stride (column slices of one buffer);
+// otherwise by their address ranges.
+bool shares(const View &a, const View &b) {
+  if (empty(a) || empty(b)) return false;
+  uintptr_t a0, a1, b0, b1;
+  range(a, a0, a1);
+  range(b, b0, b1);
+  if (a1 <= b0 || b1 <= a0) return false;
+  const int64_t ra = a.rs * a.es, rb = b.rs * b.es;
+  const int64_t wa = a.cols * a.es, wb = b.cols * b.es;
+  if (a.cs == 1 && b.cs == 1 && ra == rb && ra >= wa && ra >= wb) {
+    int64_t d = ((intptr_t)b.p - (intptr_t)a.p) % ra;
+    if (d < 0) d += ra;
+    return d < wa || d + wb > ra;
+  }
+  return true;
+}
+
+bool same(const View &a, const View &b) {
+  return a.p == b.p && (a.rs == b.rs || a.rows <= 1) && (a.cs == b.cs || a.cols <= 1) &&
+         a.es == b.es;
+}
+
+// Codes for one matrix: present where it has to be, its base a multiple of its element, and for
+// an output one element per address.
+int check_mat(const View &v, bool needed, bool output) {
+  if (!v.p) return needed && v.rows > 0 && v.cols > 0 ? COLL_EINVAL : COLL_OK;
+  if ((uintptr_t)v.p % (unsigned)v.es) return COLL_EALIGN;
+  const int64_t lim = (int64_t)1 << 40;
+  if (v.rs > lim || v.rs < -lim || v.cs > lim || v.cs < -lim) return COLL_EINVAL;
+  if (output && v.rows > 0 && v.cols > 0) {
+    if (v.cols > 1 && v.cs != 1) return COLL_EINVAL;
+    if (v.rows > 1 && v.rs < v.cols) return COLL_EINVAL;
+  }
+  return COLL_OK;
+}
+
+struct Check {
+  int code = COLL_OK;
+  View in[8], out[4];
+  int n_in = 0, n_out = 0;
+  void input(const View &v, bool needed = true) {
+    if (!code) code = check_mat(v, needed, false);
+    in[n_in++] = v;
+  }
+  void output(const View &v, bool needed = true) {
+    if (!code) code = check_mat(v, needed, true);
+    out[n_out++] = v;
+  }
+  // overlaps after every check above; `in_place`: an input that out[0] may equal
+  int finish(const View *in_place) {
+    if (code) return code;
+    for (int o = 0; o < n_out; ++o) {
+      for (int i = 0; i < n_in; ++i) {
+        if (!shares(out[o], in[i])) continue;
+        if (o == 0 && in_place && in[i].p == in_place->p && same(out[o], in[i]) &&
+            same(*in_place, in[i]))
+          continue;
+        return COLL_EOVERLAP;
+      }
+      for (int q = 0; q < o; ++q)
+        if (shares(out[o], out[q])) return COLL_EOVERLAP;
+    }
+    return COLL_OK;
+  }
+};
+
+int check_sizes(int64_t m, int64_t n, int64_t k, int64_t dtype) {
+  const int64_t most = 0x7FFFFFFF - 4096;
+  if (m < 0 || n < 0 || k < 0 || m > most || n > most || k > most) return COLL_EINVAL;
+  return is_half(dtype) ? COLL_OK : COLL_EINVAL;
+}
+
+bool linear_act(int64_t a) { return a >= COLL_ACT_NONE && a <= COLL_ACT_SILU; }
+bool gated_act(int64_t a) { return a >= COLL_ACT_RELU && a <= COLL_ACT_SIGMOID; }
+
+DenseMat mat(const coll_mat_t &m) { return DenseMat{m.ptr, m.rs, m.cs}; }
+DenseMat turned(const coll_mat_t &m) { return DenseMat{m.ptr, m.cs, m.rs}; }
+
+bool run8(const void *p, int64_t rs, int es) {
+  return !p || (((uintptr_t)p & 15u) == 0 && (rs * es) % 16 == 0);
+}
+
+// Eight-column accesses of the epilogue are 16-byte aligned in every array.
+void set_vec(DenseJob &j) {
+  const coll::DenseEpi &e = j.e;
+  const int oe = esize(e.out_type);
+  bool v = true;
+  for (int b = 0; b < j.nbatch; ++b) v = v && run8(e.out[b], e.out_rs[b], oe);
+  v = v && run8(e.pre, e.pre_rs, 2) && run8(e.gate, e.gate_rs, 2) && run8(e.up, e.up_rs, 2);
+  v = v && run8(e.bias, 0, 2) && (!e.bias || e.bias_stride == 1);
+  v = v && run8(e.res, e.res_rs, oe) && (!e.res || e.res_cs == 1);
+  j.e.vec = v;
+}
+
+DenseJob job(int64_t m, int64_t n, int64_t k, int64_t type, int32_t *status) {
+  DenseJob j = {};
+  j.m = m;
+  j.n = n;
+  j.k = k;
+  j.nseg = j.nbatch = 1;
+  j.e.type = j.e.out_type = (int32_t)type;
+  j.status = status;
+  return j;
+}
+
+void set_out(DenseJob &j, int b, const coll_mat_t &o) {
+  j.e.out[b] = o.ptr;
+  j.e.out_rs[b] = o.rs;
+}
+
+// One product; only counts its workspace where ws.base is null.
+int product(DenseJob &j, Ws &ws, bool dry, cudaStream_t s) {
+  if (j.m == 0 || j.n == 0 || dry) return COLL_OK;
+  set_vec(j);
+  return coll::dense_simple(j, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+}
+
+// Scratch matrices: rows of whole 16-byte runs.
+coll_mat_t scratch(Ws &ws, int64_t rows, int64_t cols) {
+  const int64_t ld = round8(cols);
+  return coll_mat_t{ws.take((uint64_t)rows * ld * 2), ld, 1};
+}
+
+// ---- y = act(x w^T + bias) + residual
+
+int check(const coll_linear_t &a) {
+  int c = check_sizes(a.m, a.n, a.k, a.dtype);
+  if (c) return c;
+  if (!linear_act(a.act) || (a.out_dtype != a.dtype && a.out_dtype != COLL_F32))
+    return COLL_EINVAL;
+  const int oe = esize(a.out_dtype);
+  Check k;
+  const View res = view(a.residual, a.m, a.n, oe);
+  k.output(view(a.y, a.m, a.n, oe));
+  k.output(view(a.pre, a.m, a.n, 2), false);
+  k.input(view(a.x, a.m, a.k, 2));
+  k.input(view(a.w, a.n, a.k, 2));
+  k.input(res, false);
+  k.input(View{a.bias, 1, a.n, 0, a.bias_stride, 2}, false);
+  return k.finish(a.residual.ptr ? &res : nullptr);
+}
+
+int run(const coll_linear_t &a, Ws &ws, bool dry, cudaStream_t s) {
+  DenseJob j = job(a.m, a.n, a.k, a.dtype, a.status);
+  j.a[0] = mat(a.x);
+  j.b[0] = mat(a.w);
+  j.e.out_type = (int32_t)a.out_dtype;
+  j.e.act = (int32_t)a.act;
+  set_out(j, 0, a.y);
+  j.e.pre = a.pre.ptr;
+  j.e.pre_rs = a.pre.rs;
+  j.e.bias = a.bias;
+  j.e.bias_stride = a.bias_stride;
+  j.e.res = a.residual.ptr;
+  j.e.res_rs = a.residual.rs;
+  j.e.res_cs = a.residual.cs;
+  return product(j, ws, dry, s);
+}
+
+// ---- its gradients
+
+int check(const coll_linear_bwd_t &a) {
+  int c = check_sizes(a.m, a.n, a.k, a.dtype);
+  if (c) return c;
+  if (!linear_act(a.act) || (a.grad_dtype != a.dtype && a.grad_dtype != COLL_F32))
+    return COLL_EINVAL;
+  const int ge = esize(a.grad_dtype);
+  Check k;
+  k.output(view(a.dx, a.m, a.k, 2), false);
+  k.output(view(a.dw, a.n, a.k, ge), false);
+  k.output(View{a.db, 1, a.n, a.n, 1, ge}, false);
+  k.input(view(a.dy, a.m, a.n, 2));
+  k.input(view(a.pre, a.m, a.n, 2), a.act != COLL_ACT_NONE);
+  k.input(view(a.x, a.m, a.k, 2), a.dw.ptr != nullptr);
+  k.input(view(a.w, a.n, a.k, 2), a.dx.ptr != nullptr);
+  return k.finish(nullptr);
+}
+
+int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
+  const bool products = a.dx.ptr || a.dw.ptr;
+  coll_mat_t dz = a.dy;
+  DenseActBwd b = {};
+  b.m = a.m;
+  b.n = a.n;
+  b.dy = mat(a.dy);
+  b.type = (int32_t)a.dtype;
+  b.db_type = (int32_t)a.grad_dtype;
+  b.act = (int32_t)a.act;
+  if (a.act != COLL_ACT_NONE) {
+    b.pre = mat(a.pre);
+    if (products) {
+      dz = scratch(ws, a.m, a.n);
+      b.dz = dz.ptr;
+      b.ld = dz.rs;
+    }
+  }
+  if (a.db) {
+    b.db = a.db;
+    const int64_t blocks = coll::dense_act_bwd_row_blocks(a.m, a.n);
+    if (blocks > 1) b.part = static_cast<float *>(ws.take((uint64_t)blocks * a.n * 4));
+  }
+  if ((b.db || (a.act != COLL_ACT_NONE && products && a.m > 0)) && a.n > 0 && !dry)
+    if (coll::dense_act_bwd(b, s) != cudaSuccess) return COLL_ECUDA;
+  if (a.dx.ptr) {  // dx(m, k) = sum over n of dz(m, n) w(n, k)
+    DenseJob j = job(a.m, a.k, a.n, a.dtype, a.status);
+    j.a[0] = mat(dz);
+    j.b[0] = turned(a.w);
+    set_out(j, 0, a.dx);
+    const int c = product(j, ws, dry, s);
+    if (c) return c;
+  }
+  if (a.dw.ptr) {  // dw(n, k) = sum over m of dz(m, n) x(m, k)
+    DenseJob j = job(a.n, a.k, a.m, a.dtype, a.status);
+    j.a[0] = turned(dz);
+    j.b[0] = turned(a.x);
+    j.e.out_type = (int32_t)a.grad_dtype;
+    set_out(j, 0, a.dw);
+    return product(j, ws, dry, s);
+  }
+  return COLL_OK;
+}
+
+// ---- h = act(x w_gate^T) (x w_up^T)
+
+int check(const coll_gated_t &a) {
+  int c = check_sizes(a.m, a.n, a.k, a.dtype);
+  if (c) return c;
+  if (!gated_act(a.act) || (a.gate.ptr == nullptr) != (a.up.ptr == nullptr)) return COLL_EINVAL;
+  Check k;
+  k.output(view(a.h, a.m, a.n, 2));
+  k.output(view(a.gate, a.m, a.n, 2), false);
+  k.output(view(a.up, a.m, a.n, 2), false);
+  k.input(view(a.x, a.m, a.k, 2));
+  k.input(view(a.w_gate, a.n, a.k, 2));
+  k.input(view(a.w_up, a.n, a.k, 2));
+  return k.finish(nullptr);
+}
+
+int run(const coll_gated_t &a, Ws &ws, bool dry, cudaStream_t s) {
+  DenseJob j = job(a.m, a.n, a.k, a.dtype, a.status);
+  j.gated = 1;
+  j.a[0] = mat(a.x);
+  j.b[0] = mat(a.w_gate);
+  j.b[1] = mat(a.w_up);
+  j.e.act = (int32_t)a.act;
+  set_out(j, 0, a.h);
+  j.e.gate = a.gate.ptr;
+  j.e.gate_rs = a.gate.rs;
+  j.e.up = a.up.ptr;
+  j.e.up_rs = a.up.rs;
+  return product(j, ws, dry, s);
+}
+
+// ---- its gradients
+
+int check(const coll_gated_bwd_t &a) {
+  int c = check_sizes(a.m, a.n, a.k, a.dtype);
+  if (c) return c;
+  if (!gated_act(a.act) || (a.grad_dtype != a.dtype && a.grad_dtype != COLL_F32) ||
+      (a.dw_gate.ptr == nullptr) != (a.dw_up.ptr == nullptr))
+    return COLL_EINVAL;
+  const int ge = esize(a.grad_dtype);
+  Check k;
+  k.output(view(a.dx, a.m, a.k, 2), false);
+  k.output(view(a.dw_gate, a.n, a.k, ge), false);
+  k.output(view(a.dw_up, a.n, a.k, ge), false);
+  k.input(view(a.dh, a.m, a.n, 2));
+  k.input(view(a.gate, a.m, a.n, 2));
+  k.input(view(a.up, a.m, a.n, 2));
+  k.input(view(a.x, a.m, a.k, 2), a.dw_gate.ptr != nullptr);
+  k.input(view(a.w_gate, a.n, a.k, 2), a.dx.ptr != nullptr);
+  k.input(view(a.w_up, a.n, a.k, 2), a.dx.ptr != nullptr);
+  return k.finish(nullptr);
+}
+
+int run(const coll_gated_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
+  if (!a.dx.ptr && !a.dw_gate.ptr) return COLL_OK;
+  const coll_mat_t dg = scratch(ws, a.m, a.n), du = scratch(ws, a.m, a.n);
+  if (a.m > 0 && a.n > 0 && !dry) {
+    DenseActBwd b = {};
+    b.m = a.m;
+    b.n = a.n;
+    b.dy = mat(a.dh);
+    b.pre = mat(a.gate);
+    b.up = mat(a.up);
+    b.dz = dg.ptr;
+    b.du = du.ptr;
+    b.ld = dg.rs;
+    b.type = (int32_t)a.dtype;
+    b.act = (int32_t)a.act;
+    b.gated = 1;
+    if (coll::dense_act_bwd(b, s) != cudaSuccess) return COLL_ECUDA;
+  }
+  if (a.dx.ptr) {  // dx = dg w_gate + du w_up: one sum over both
+    DenseJob j = job(a.m, a.k, a.n, a.dtype, a.status);
+    j.nseg = 2;
+    j.a[0] = mat(dg);
+    j.a[1] = mat(du);
+    j.b[0] = turned(a.w_gate);
+    j.b[1] = turned(a.w_up);
+    set_out(j, 0, a.dx);
+    const int c = product(j, ws, dry, s);
+    if (c) return c;
+  }
+  if (a.dw_gate.ptr) {  // dw_gate = dg^T x, dw_up = du^T x: one launch
+    DenseJob j = job(a.n, a.k, a.m, a.dtype, a.status);
+    j.nbatch = 2;
+    j.a[0] = turned(dg);
+    j.a[1] = turned(du);
+    j.b[0] = turned(a.x);
+    j.e.out_type = (int32_t)a.grad_dtype;
+    set_out(j, 0, a.dw_gate);
+    set_out(j, 1, a.dw_up);
+    return product(j, ws, dry, s);
+  }
+  return COLL_OK;
+}
+
+template <typename T>
+int64_t workspace(const T *a) {
+  if (!a) return COLL_EINVAL;
+  const int c = check(*a);
+  if (c) return c;
+  Ws ws = {};
+  const int r = run(*a, ws, true, nullptr);
+  return r ? r : (int64_t)ws.used;
+}
+
+template <typename T>
+int call(const T *a, void *stream) {
+  const int64_t need = workspace(a);
+  if (need < 0) return (int)need;
+  Ws ws = {};
+  if (need > 0) {
+    if (!a->workspace || ((uintptr_t)a->workspace & 15u) || a->workspace_bytes < (uint64_t)need)
+      return COLL_EWORKSPACE;
+    ws.base = static_cast<char *>(a->workspace);
+  }
+  return run(*a, ws, false, static_cast<cudaStream_t>(stream));
+}
+
+}  // namespace
+
+extern "C" int coll_linear(const coll_linear_t *a, void *stream) { return call(a, stream); }
+extern "C" int coll_linear_backward(const coll_linear_bwd_t *a, void *stream) {
+  return call(a, stream);
+}
+extern "C" int coll_gated_ffn(const coll_gated_t *a, void *stream) { return call(a, stream); }
+extern "C" int coll_gated_ffn_backward(const coll_gated_bwd_t *a, void *stream) {
+  return call(a, stream);
+}
+extern "C" int64_t coll_linear_workspace(const coll_linear_t *a) { return workspace(a); }
+extern "C" int64_t coll_linear_backward_workspace(const coll_linear_bwd_t *a) {
+  return workspace(a);
+}
+extern "C" int64_t coll_gated_ffn_workspace(const coll_gated_t *a) { return workspace(a); }
+extern "C" int64_t coll_gated_ffn_backward_workspace(const coll_gated_bwd_t *a) {
+  return workspace(a);
+}

@@ -1,0 +1,64 @@
+// Dense operators: what the host dispatch (dense.cu) hands to the kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "coll.h"
+
+namespace coll {
+
+// Element (i, j) at p + i * rs + j * cs elements.
+struct DenseMat {
+  const void *p;
+  int64_t rs, cs;
+};
+
+// What happens to a finished accumulator. One product: z = acc + bias, y = act(z) + residual,
+// z kept in `pre`. Gated: h = act(g) u, g and u kept in `gate` and `up`.
+struct DenseEpi {
+  void *out[2];       // per batch
+  int64_t out_rs[2];
+  void *pre;
+  int64_t pre_rs;
+  void *gate, *up;
+  int64_t gate_rs, up_rs;
+  const void *bias;
+  int64_t bias_stride;
+  const void *res;
+  int64_t res_rs, res_cs;
+  int32_t type;      // COLL_BF16 / COLL_F16: bias, pre, gate, up
+  int32_t out_type;  // type or COLL_F32: out, residual
+  int32_t act;
+  int32_t vec;       // 1: eight columns from a multiple of eight start on a 16-byte boundary in
+                     // every array above
+};
+
+// out[b](m, n) = epilogue(sum over s of sum over k of A[b or s](m, k) B[s](n, k)).
+//   nseg == 2: the sums of two products (A[0] B[0] + A[1] B[1]), one output
+//   nbatch == 2: two products A[0] B[0] and A[1] B[0], two outputs
+//   gated: g = A[0] B[0], u = A[0] B[1], one output
+struct DenseJob {
+  int64_t m, n, k;
+  int32_t nseg, nbatch, gated, pad;
+  DenseMat a[2], b[2];
+  DenseEpi e;
+  int32_t *status;
+};
+
+// Elementwise parts of the backward calls (dense_aux.cu).
+struct DenseActBwd {
+  int64_t m, n;
+  DenseMat dy, pre, up;  // up: gated only
+  void *dz, *du;         // [m][ld]; may be NULL when only db is wanted
+  int64_t ld;
+  void *db;              // NULL: no column sums
+  float *part;           // column sums of each row block, [row_blocks][n]
+  int32_t type, db_type, act, gated;
+};
+int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n);
+cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s);
+
+cudaError_t dense_simple(const DenseJob &j, cudaStream_t s);
+
+}  // namespace coll

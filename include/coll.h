@@ -48,6 +48,8 @@ extern "C" {
 #define COLL_ENOMEM (-10)   /* host or device allocation failed                         */
 #define COLL_ETOOBIG (-11)  /* coll_allreduce_static: the request needs more than its fixed
                                scratch array or more warps than can be co-resident       */
+#define COLL_EWORKSPACE (-12) /* a dense operator's workspace is missing, unaligned or smaller
+                               than its *_workspace call says                            */
 
 /* ------------------------------------------------------------------ enums */
 #define COLL_OP_COPY 0
@@ -56,6 +58,7 @@ extern "C" {
 #define COLL_BF16 0  /* 2-byte elements; sum accumulates in binary32          */
 #define COLL_F32 1   /* 4-byte elements                                       */
 #define COLL_BYTES 2 /* 1-byte elements; copy only                            */
+#define COLL_F16 3   /* 2-byte elements; dense operators only (no collective) */
 
 /* Stage/Notify/Consume protocols for staged plans (zero_copy == 0).
  * Source: SiFAR review, "What carries the argument" and abstract: oneshot with a top and a
@@ -335,6 +338,103 @@ int coll_allreduce_static(int R, int dtype, void *const *in, void *const *out, u
 
 /* Static string for a code. No counterpart on the pages. */
 const char *coll_strerror(int code);
+
+/* ------------------------------------------------------------- dense operators
+ * The products on either side of a tensor-parallel layer's collective: a gated block's two
+ * projections before it splits over the ranks (coll_gated_ffn), a row-parallel product whose
+ * partial the collective sums (coll_linear), and their gradients. No counterpart on the pages.
+ *
+ * Operands are COLL_BF16 or COLL_F16 (one type per call); products accumulate in binary32 and
+ * every output is rounded once, to nearest even, from the binary32 epilogue. The backward
+ * calls round dz (dg, du) to the operands' type once before the products that read them.
+ * Results do not depend on timing: every sum has a fixed order for given sizes and layouts.
+ *
+ * Calls enqueue on `stream` and return; they hold no state between calls and allocate nothing,
+ * so calls on different streams may overlap when their workspaces differ, and calls may be
+ * captured into a CUDA graph. Buffers must stay live and unmodified until the stream has
+ * passed the call. `status`: optional device int32 that receives COLL_ETIMEDOUT if a bounded
+ * device wait expires (never cleared by a call). The workspace must be 16-byte aligned and
+ * hold what the call's *_workspace function returns for the same arguments.
+ * Errors (synchronous, nothing enqueued): COLL_EINVAL (sizes, types, activation, a NULL that is
+ * not optional, outputs whose rows overlap), COLL_EALIGN (a base that is not a multiple of its
+ * element), COLL_EOVERLAP (an output that shares memory with an input or another output; only
+ * y == residual, the same view, is allowed), COLL_EWORKSPACE, COLL_ECUDA. */
+#define COLL_ACT_NONE 0
+#define COLL_ACT_RELU 1
+#define COLL_ACT_GELU 2      /* z/2 (1 + erf(z / sqrt 2))                                       */
+#define COLL_ACT_GELU_TANH 3 /* z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))                   */
+#define COLL_ACT_SILU 4      /* z / (1 + exp(-z))                                               */
+#define COLL_ACT_SIGMOID 5   /* 1 / (1 + exp(-z)); gated operators only                         */
+
+/* A matrix in device memory: element (i, j) at ptr + i * rs + j * cs elements. Inputs may have
+ * any strides (0 broadcasts); outputs need cs == 1 and rs >= columns. ptr NULL = absent. */
+typedef struct {
+  void *ptr;
+  int64_t rs, cs;
+} coll_mat_t;
+
+/* y = act(z) + residual, z = x w^T + bias.  x [m][k], w [n][k], bias [n], residual and y [m][n].
+ * pre (optional): receives z rounded to dtype, for the backward call. y is of out_dtype: dtype
+ * or COLL_F32 (the partial of a binary32 sum); bias, residual and pre are of dtype, a residual
+ * beside a binary32 y is binary32 too. k == 0 gives act(bias) + residual. */
+typedef struct {
+  int64_t m, n, k;
+  int64_t dtype, out_dtype, act;
+  coll_mat_t x, w, residual, pre, y;
+  const void *bias;
+  int64_t bias_stride;
+  void *workspace;
+  uint64_t workspace_bytes;
+  int32_t *status;
+} coll_linear_t;
+
+/* dz = dy act'(pre);  dx = dz w,  dw = dz^T x,  db = column sums of dz. dx, dw and db are each
+ * optional (ptr NULL). pre is needed unless act is COLL_ACT_NONE; the residual's gradient is dy
+ * itself. dx is of dtype; dw and db are of grad_dtype: dtype or COLL_F32. m == 0 gives zeros. */
+typedef struct {
+  int64_t m, n, k;
+  int64_t dtype, grad_dtype, act;
+  coll_mat_t dy, pre, x, w, dx, dw;
+  void *db; /* [n], contiguous */
+  void *workspace;
+  uint64_t workspace_bytes;
+  int32_t *status;
+} coll_linear_bwd_t;
+
+/* h = act(g) u,  g = x w_gate^T,  u = x w_up^T.  x [m][k], w_gate and w_up [n][k], h [m][n].
+ * gate and up (optional): receive g and u rounded to dtype, for the backward call. */
+typedef struct {
+  int64_t m, n, k;
+  int64_t dtype, act;
+  coll_mat_t x, w_gate, w_up, gate, up, h;
+  void *workspace;
+  uint64_t workspace_bytes;
+  int32_t *status;
+} coll_gated_t;
+
+/* dg = dh u act'(g),  du = dh act(g);  dx = dg w_gate + du w_up,  dw_gate = dg^T x,
+ * dw_up = du^T x. dx is optional; dw_gate and dw_up are optional together. gate and up are what
+ * the forward call stored. dx is of dtype, dw_gate and dw_up of grad_dtype (dtype or COLL_F32). */
+typedef struct {
+  int64_t m, n, k;
+  int64_t dtype, grad_dtype, act;
+  coll_mat_t dh, gate, up, x, w_gate, w_up, dx, dw_gate, dw_up;
+  void *workspace;
+  uint64_t workspace_bytes;
+  int32_t *status;
+} coll_gated_bwd_t;
+
+int coll_linear(const coll_linear_t *a, void *stream);
+int coll_linear_backward(const coll_linear_bwd_t *a, void *stream);
+int coll_gated_ffn(const coll_gated_t *a, void *stream);
+int coll_gated_ffn_backward(const coll_gated_bwd_t *a, void *stream);
+
+/* Workspace bytes of a call with these arguments (its workspace fields are not read; 0 = none
+ * needed), or the negative code the call would return. No device call is made. */
+int64_t coll_linear_workspace(const coll_linear_t *a);
+int64_t coll_linear_backward_workspace(const coll_linear_bwd_t *a);
+int64_t coll_gated_ffn_workspace(const coll_gated_t *a);
+int64_t coll_gated_ffn_backward_workspace(const coll_gated_bwd_t *a);
 
 #ifdef __cplusplus
 }
