@@ -11,6 +11,7 @@
 #include <vector>
 
 #include "coll_internal.h"
+#include "dense_tc.h"
 #include "engine.cuh"
 
 struct coll_plan_s {
@@ -48,6 +49,27 @@ struct coll_plan_s {
   std::vector<const void *> gmaps_wt;
   uint32_t gmaps_k = 0;
 };
+
+namespace coll {
+
+// The CUDA driver API's tensor-map encoder, looked up once through the runtime (no link to the
+// driver library).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                         &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess) {
+      cudaGetLastError();
+      p = nullptr;
+    }
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  }();
+  return fn;
+}
+
+}  // namespace coll
 
 namespace {
 
@@ -110,23 +132,6 @@ bool overlaps(uintptr_t a0, uintptr_t a1, uintptr_t b0, uintptr_t b1) {
   return a0 < b1 && b0 < a1;
 }
 
-// The CUDA driver API's tensor-map encoder, looked up once through the runtime (no link to the
-// driver library).
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
-  static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() {
-    void *p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess) {
-      cudaGetLastError();
-      p = nullptr;
-    }
-    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-  }();
-  return fn;
-}
-
 // Tensor maps of the fused run's weight matrices W_r ([k rows][in_len[r] bf16], rows
 // in_bytes[r] apart), boxes of one unit's columns (at most 256) x 64 rows; reused while the
 // run's matrices and k stay the same.
@@ -139,7 +144,7 @@ int gemv_maps(coll_plan_s *p, const void *const *wt, uint32_t k) {
   const coll_compiled &c = p->c;
   std::vector<const void *> key(wt, wt + c.R);
   if (p->gmaps && p->gmaps_k == k && p->gmaps_wt == key) return COLL_OK;
-  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = coll::tensor_map_encoder();
   if (!encode) return COLL_ECUDA;
   if (!p->gmaps) {
     p->gmaps.reset(new (std::nothrow) coll::GemvMaps());

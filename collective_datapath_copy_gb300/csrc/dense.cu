@@ -4,12 +4,14 @@
 #include <stdint.h>
 
 #include "dense.h"
+#include "dense_tc.h"
 
 namespace {
 
 using coll::DenseActBwd;
 using coll::DenseJob;
 using coll::DenseMat;
+using coll::TcOperand;
 
 // Bump allocator over the caller's workspace. With base == nullptr it only counts.
 struct Ws {
@@ -158,11 +160,82 @@ void set_out(DenseJob &j, int b, const coll_mat_t &o) {
   j.e.out_rs[b] = o.rs;
 }
 
-// One product; only counts its workspace where ws.base is null.
+// The operand as a tensor map takes it in place: one unit stride, the other a multiple of 16
+// bytes that is no shorter than the line, a 16-byte aligned base. False where it has to be
+// laid out first.
+bool in_place(const DenseMat &m, int64_t rows, int64_t k, TcOperand &o) {
+  const int64_t most = (int64_t)1 << 38;  // the maps' strides are below 2^40 bytes
+  if ((uintptr_t)m.p & 15u) return false;
+  const bool along_k = m.cs == 1 || k == 1, along_m = m.rs == 1 || rows == 1;
+  if (along_k && (rows == 1 || (m.rs % 8 == 0 && m.rs >= k && m.rs < most))) {
+    o = TcOperand{m.p, rows, k, rows == 1 ? round8(k) : m.rs, 0};
+    return true;
+  }
+  if (along_m && (k == 1 || (m.cs % 8 == 0 && m.cs >= rows && m.cs < most))) {
+    o = TcOperand{m.p, rows, k, k == 1 ? round8(rows) : m.cs, 1};
+    return true;
+  }
+  return false;
+}
+
+// Lay the operand out in the workspace along `mn` (0: k, 1: its rows).
+int lay_out(const DenseMat &m, int64_t rows, int64_t k, int mn, Ws &ws, bool dry, cudaStream_t s,
+            TcOperand &o) {
+  const DenseMat src = mn ? DenseMat{m.p, m.cs, m.rs} : m;
+  const int64_t lines = mn ? k : rows, len = mn ? rows : k, ld = round8(len);
+  void *dst = ws.take((uint64_t)lines * ld * 2);
+  o = TcOperand{dst, rows, k, ld, mn};
+  if (dry) return COLL_OK;
+  return coll::dense_pack(src, lines, len, dst, ld, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+}
+
+int operand(const DenseMat &m, int64_t rows, int64_t k, Ws &ws, bool dry, cudaStream_t s,
+            TcOperand &o) {
+  if (in_place(m, rows, k, o)) return COLL_OK;
+  return lay_out(m, rows, k, m.cs != 1 && m.rs == 1, ws, dry, s, o);
+}
+
+int sm_count(uint32_t &sms) {
+  int dev = 0, v = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return COLL_ECUDA;
+  sms = (uint32_t)v;
+  return COLL_OK;
+}
+
+// One product; only counts its workspace where `dry`.
 int product(DenseJob &j, Ws &ws, bool dry, cudaStream_t s) {
-  if (j.m == 0 || j.n == 0 || dry) return COLL_OK;
+  if (j.m == 0 || j.n == 0) return COLL_OK;
   set_vec(j);
-  return coll::dense_simple(j, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  if (j.k == 0)
+    return dry || coll::dense_empty_sum(j, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  TcOperand a[2], b[2];
+  const int na = j.nbatch == 2 || j.nseg == 2 ? 2 : 1, nb = j.gated || j.nseg == 2 ? 2 : 1;
+  for (int i = 0; i < na; ++i) {
+    const int c = operand(j.a[i], j.m, j.k, ws, dry, s, a[i]);
+    if (c) return c;
+  }
+  if (j.gated && in_place(j.b[0], j.n, j.k, b[0]) && in_place(j.b[1], j.n, j.k, b[1]) &&
+      b[0].mn != b[1].mn) {
+    // both halves of one instruction's B lie the same way
+    const int c = lay_out(j.b[1], j.n, j.k, b[0].mn, ws, dry, s, b[1]);
+    if (c) return c;
+  } else {
+    for (int i = 0; i < nb; ++i) {
+      int c = operand(j.b[i], j.n, j.k, ws, dry, s, b[i]);
+      if (!c && i == 1 && j.gated && b[1].mn != b[0].mn)
+        c = lay_out(j.b[i], j.n, j.k, b[0].mn, ws, dry, s, b[i]);
+      if (c) return c;
+    }
+  }
+  if (dry) return COLL_OK;
+  uint32_t sms = 0;
+  coll::TcParams p;
+  int c = sm_count(sms);
+  if (!c) c = coll::tc_plan(p, j, a, b, sms);
+  if (c) return c;
+  return coll::tc_run(p, j.gated != 0, sms, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
 }
 
 // Scratch matrices: rows of whole 16-byte runs.
@@ -236,20 +309,19 @@ int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
   b.type = (int32_t)a.dtype;
   b.db_type = (int32_t)a.grad_dtype;
   b.act = (int32_t)a.act;
-  if (a.act != COLL_ACT_NONE) {
-    b.pre = mat(a.pre);
-    if (products) {
-      dz = scratch(ws, a.m, a.n);
-      b.dz = dz.ptr;
-      b.ld = dz.rs;
-    }
+  if (a.act != COLL_ACT_NONE) b.pre = mat(a.pre);
+  TcOperand o;
+  if (products && (a.act != COLL_ACT_NONE || !in_place(mat(a.dy), a.m, a.n, o))) {
+    dz = scratch(ws, a.m, a.n);  // both products read it
+    b.dz = dz.ptr;
+    b.ld = dz.rs;
   }
   if (a.db) {
     b.db = a.db;
     const int64_t blocks = coll::dense_act_bwd_row_blocks(a.m, a.n);
     if (blocks > 1) b.part = static_cast<float *>(ws.take((uint64_t)blocks * a.n * 4));
   }
-  if ((b.db || (a.act != COLL_ACT_NONE && products && a.m > 0)) && a.n > 0 && !dry)
+  if ((b.db || (dz.ptr != a.dy.ptr && a.m > 0)) && a.n > 0 && !dry)
     if (coll::dense_act_bwd(b, s) != cudaSuccess) return COLL_ECUDA;
   if (a.dx.ptr) {  // dx(m, k) = sum over n of dz(m, n) w(n, k)
     DenseJob j = job(a.m, a.k, a.n, a.dtype, a.status);

@@ -59,6 +59,13 @@ struct DenseActBwd {
 int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n);
 cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s);
 
-cudaError_t dense_simple(const DenseJob &j, cudaStream_t s);
+
+// dst[i * ld + j] = src(i, j): an operand whose strides or base no tensor map takes, laid out in
+// rows of whole 16-byte runs.
+cudaError_t dense_pack(const DenseMat &src, int64_t rows, int64_t cols, void *dst, int64_t ld,
+                       cudaStream_t s);
+
+// The job's epilogue over accumulators of zero (nothing to sum over).
+cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s);
 
 }  // namespace coll

@@ -70,8 +70,8 @@ __global__ void __launch_bounds__(256) act_bwd_kernel(const DenseActBwd a, int64
       if (GATED) store8(a.du, r * a.ld + col, left, a.type, u);
     }
   }
-  if (GATED || !a.db) return;
   __shared__ float part[GROUPS][COLS];
+  if (!a.db) return;  // gated calls have none
 #pragma unroll
   for (int i = 0; i < 8; ++i) part[grp][lane * 8 + i] = sum[i];
   __syncthreads();
@@ -93,7 +93,54 @@ __global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t bl
   st_elem(db, c, s, type);
 }
 
+// A thread moves eight neighbouring elements: plain 2-byte loads (the rows start anywhere), one
+// 16-byte store.
+__global__ void __launch_bounds__(256) pack_kernel(const DenseMat src, int64_t rows, int64_t cols,
+                                                   uint16_t *dst, int64_t ld) {
+  const int64_t runs = ld / 8, total = rows * runs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / runs, c = (i - r * runs) * 8;
+    const uint16_t *p = static_cast<const uint16_t *>(src.p) + r * src.rs + c * src.cs;
+    uint32_t v[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) v[q] = c + q < cols ? p[q * src.cs] : 0u;
+    *reinterpret_cast<uint4 *>(dst + r * ld + c) =
+        make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
+}
+
+template <bool GATED>
+__global__ void __launch_bounds__(256) empty_sum_kernel(const DenseJob j) {
+  const int64_t runs = (j.n + 7) / 8, total = j.m * runs;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / runs, c = (i - r * runs) * 8;
+    float g[8] = {}, u[8] = {};
+    epilogue_run8<GATED>(j.e, blockIdx.y, r, c, j.n - c, g, u);
+  }
+}
+
+unsigned grid_for(int64_t threads) {
+  const int64_t b = (threads + 255) / 256;
+  return (unsigned)(b < 4864 ? b : 4864);  // four CTAs of eight warps on each of 152 SMs, 8 deep
+}
+
 }  // namespace
+
+cudaError_t dense_pack(const DenseMat &src, int64_t rows, int64_t cols, void *dst, int64_t ld,
+                       cudaStream_t s) {
+  pack_kernel<<<grid_for(rows * (ld / 8)), 256, 0, s>>>(src, rows, cols,
+                                                        static_cast<uint16_t *>(dst), ld);
+  return cudaGetLastError();
+}
+
+cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s) {
+  const dim3 grid(grid_for(j.m * ((j.n + 7) / 8)), (unsigned)j.nbatch);
+  if (j.gated) empty_sum_kernel<true><<<grid, 256, 0, s>>>(j);
+  else empty_sum_kernel<false><<<grid, 256, 0, s>>>(j);
+  return cudaGetLastError();
+}
 
 // Row blocks: enough CTAs for two waves of eight a multiprocessor, 64 rows a block at least.
 int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n) {

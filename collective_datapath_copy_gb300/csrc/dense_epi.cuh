@@ -100,6 +100,22 @@ __device__ __forceinline__ void st_elem(void *p, int64_t i, float v, int type) {
   else static_cast<uint16_t *>(p)[i] = f2h(v, type);
 }
 
+__device__ __forceinline__ void act_run8(float (&v)[8], int act) {
+  switch (act) {
+#define COLL_ACT_CASE(a)                                   \
+  case a:                                                  \
+    _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], a); \
+    return;
+    COLL_ACT_CASE(COLL_ACT_RELU)
+    COLL_ACT_CASE(COLL_ACT_GELU)
+    COLL_ACT_CASE(COLL_ACT_GELU_TANH)
+    COLL_ACT_CASE(COLL_ACT_SILU)
+    COLL_ACT_CASE(COLL_ACT_SIGMOID)
+#undef COLL_ACT_CASE
+    default: return;
+  }
+}
+
 __device__ __forceinline__ void ld_run8(const void *p, int64_t i, int type, float (&v)[8]) {
   if (type == COLL_F32) {
     const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
@@ -109,10 +125,14 @@ __device__ __forceinline__ void ld_run8(const void *p, int64_t i, int type, floa
     return;
   }
   const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-  h2f2(a.x, type, v[0], v[1]);
-  h2f2(a.y, type, v[2], v[3]);
-  h2f2(a.z, type, v[4], v[5]);
-  h2f2(a.w, type, v[6], v[7]);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+  if (type == COLL_BF16) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h2f2(w[q], COLL_BF16, v[2 * q], v[2 * q + 1]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) h2f2(w[q], COLL_F16, v[2 * q], v[2 * q + 1]);
+  }
 }
 
 __device__ __forceinline__ void st_run8(void *p, int64_t i, int type, const float (&v)[8]) {
@@ -122,12 +142,15 @@ __device__ __forceinline__ void st_run8(void *p, int64_t i, int type, const floa
     o[1] = make_float4(v[4], v[5], v[6], v[7]);
     return;
   }
-  uint4 a;
-  a.x = f2h2(v[0], v[1], type);
-  a.y = f2h2(v[2], v[3], type);
-  a.z = f2h2(v[4], v[5], type);
-  a.w = f2h2(v[6], v[7], type);
-  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = a;
+  uint32_t w[4];
+  if (type == COLL_BF16) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = f2h2(v[2 * q], v[2 * q + 1], COLL_BF16);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) w[q] = f2h2(v[2 * q], v[2 * q + 1], COLL_F16);
+  }
+  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 // Columns [col, col + 8) of one row; `left` = columns of the row from col on (>= 1). g holds the
@@ -143,8 +166,9 @@ __device__ __forceinline__ void epilogue_run8(const DenseEpi &e, int batch, int6
         st_run8(e.gate, row * e.gate_rs + col, e.type, g);
         st_run8(e.up, row * e.up_rs + col, e.type, u);
       }
+      act_run8(g, e.act);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] = act_value(g[i], e.act) * u[i];
+      for (int i = 0; i < 8; ++i) g[i] *= u[i];
     } else {
       float t[8];
       if (e.bias) {
@@ -153,10 +177,7 @@ __device__ __forceinline__ void epilogue_run8(const DenseEpi &e, int batch, int6
         for (int i = 0; i < 8; ++i) g[i] += t[i];
       }
       if (e.pre) st_run8(e.pre, row * e.pre_rs + col, e.type, g);
-      if (e.act != COLL_ACT_NONE) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = act_value(g[i], e.act);
-      }
+      act_run8(g, e.act);
       if (e.res) {
         ld_run8(e.res, row * e.res_rs + col, e.out_type, t);
 #pragma unroll

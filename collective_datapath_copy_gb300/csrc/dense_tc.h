@@ -1,0 +1,39 @@
+// Launch interface of the tensor-core products (dense_tc.cu).
+#pragma once
+
+#include <cuda.h>  // CUtensorMap (the type only; maps are encoded through the runtime)
+#include <cudaTypedefs.h>
+
+#include "dense.h"
+
+namespace coll {
+
+constexpr uint32_t kTcSmem = 226 * 1024;  // dynamic shared memory a CTA may ask for
+
+struct TcParams {
+  CUtensorMap a[2], b[2];
+  DenseEpi e;
+  int64_t m, n;
+  int32_t *status;
+  uint32_t tiles_m, tiles_n, tiles;
+  int32_t tile_rows, tile_cols;  // of the output
+  int32_t b_rows, b_chunks;      // rows of B per CTA and operand, and 64-row chunks of them
+  int32_t kblocks, nseg, nbatch, stages;
+  uint32_t stage_bytes, idesc;
+  int32_t a_mn[2], b_mn[2];      // 1: the operand's rows (not k) are contiguous
+};
+
+// An operand as the tensor maps take it: rows x k, k contiguous (mn == 0) or rows contiguous.
+struct TcOperand {
+  const void *p;
+  int64_t rows, k, ld;  // ld: elements between the lines of the contiguous axis, a multiple of 8
+  int32_t mn;
+};
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+// Fill shapes and maps of `p` for the job; operands a[nseg or nbatch], b[nseg, or 2 when gated].
+int tc_plan(TcParams &p, const DenseJob &j, const TcOperand *a, const TcOperand *b, uint32_t sms);
+cudaError_t tc_run(const TcParams &p, bool gated, uint32_t sms, cudaStream_t s);
+
+}  // namespace coll
