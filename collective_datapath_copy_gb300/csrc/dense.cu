@@ -128,19 +128,19 @@ bool gated_act(int64_t a) { return a >= COLL_ACT_RELU && a <= COLL_ACT_SIGMOID; 
 DenseMat mat(const coll_mat_t &m) { return DenseMat{m.ptr, m.rs, m.cs}; }
 DenseMat turned(const coll_mat_t &m) { return DenseMat{m.ptr, m.cs, m.rs}; }
 
-bool run8(const void *p, int64_t rs, int es) {
-  return !p || (((uintptr_t)p & 15u) == 0 && (rs * es) % 16 == 0);
+bool sectors(const void *p, int64_t rs, int es) {
+  return !p || (((uintptr_t)p & 31u) == 0 && (rs * es) % 32 == 0);
 }
 
-// Eight-column accesses of the epilogue are 16-byte aligned in every array.
+// Accesses of 32 bytes at columns that are multiples of 32 are aligned in every array.
 void set_vec(DenseJob &j) {
   const coll::DenseEpi &e = j.e;
   const int oe = esize(e.out_type);
   bool v = true;
-  for (int b = 0; b < j.nbatch; ++b) v = v && run8(e.out[b], e.out_rs[b], oe);
-  v = v && run8(e.pre, e.pre_rs, 2) && run8(e.gate, e.gate_rs, 2) && run8(e.up, e.up_rs, 2);
-  v = v && run8(e.bias, 0, 2) && (!e.bias || e.bias_stride == 1);
-  v = v && run8(e.res, e.res_rs, oe) && (!e.res || e.res_cs == 1);
+  for (int b = 0; b < j.nbatch; ++b) v = v && sectors(e.out[b], e.out_rs[b], oe);
+  v = v && sectors(e.pre, e.pre_rs, 2) && sectors(e.gate, e.gate_rs, 2) && sectors(e.up, e.up_rs, 2);
+  v = v && sectors(e.bias, 0, 2) && (!e.bias || e.bias_stride == 1);
+  v = v && sectors(e.res, e.res_rs, oe) && (!e.res || e.res_cs == 1);
   j.e.vec = v;
 }
 

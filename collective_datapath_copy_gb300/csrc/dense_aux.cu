@@ -13,75 +13,115 @@
 namespace coll {
 namespace {
 
-constexpr int COLS = 256;   // columns per CTA: 32 runs of eight
-constexpr int GROUPS = 8;   // row groups per CTA
+constexpr int COLS = 256;   // columns per CTA: 32 lanes of eight
+constexpr int GROUPS = 8;   // row groups per CTA, a warp each
 
-__device__ __forceinline__ void load8(const DenseMat &m, int64_t row, int64_t col, int64_t left,
-                                      int type, float (&v)[8]) {
+// eight columns of one row; VEC: all there and 16-byte aligned
+template <bool VEC>
+__device__ __forceinline__ uint4 load8(const DenseMat &m, int64_t row, int64_t col, int64_t left) {
   const uint16_t *p = static_cast<const uint16_t *>(m.p) + row * m.rs + col * m.cs;
-  if (m.cs == 1 && left >= 8 && ((uintptr_t)p & 15u) == 0) {
-    ld_run8(p, 0, type, v);
-    return;
-  }
+  if constexpr (VEC) {
+    return __ldcs(reinterpret_cast<const uint4 *>(p));
+  } else {
+    uint32_t v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = i < left ? h2f(p[i * m.cs], type) : 0.0f;
+    for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i * m.cs] : 0u;
+    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+  }
 }
 
-__device__ __forceinline__ void store8(void *base, int64_t off, int64_t left, int type,
-                                       const float (&v)[8]) {
-  if (left >= 8) {  // ld is a multiple of eight and the base 16-byte aligned
-    st_run8(base, off, type, v);
-    return;
-  }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < left) static_cast<uint16_t *>(base)[off + i] = f2h(v[i], type);
+__device__ __forceinline__ void widen8(const uint4 &a, int type, float (&v)[8]) {
+  h2f2(a.x, type, v[0], v[1]);
+  h2f2(a.y, type, v[2], v[3]);
+  h2f2(a.z, type, v[4], v[5]);
+  h2f2(a.w, type, v[6], v[7]);
 }
 
-template <bool GATED>
-__global__ void __launch_bounds__(256) act_bwd_kernel(const DenseActBwd a, int64_t rows_per_block) {
+// The scratch rows are padded to a multiple of eight columns, so a run is stored whole.
+__device__ __forceinline__ void store8(void *base, int64_t off, int type, const float (&v)[8]) {
+  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(base) + off) =
+      make_uint4(f2h2(v[0], v[1], type), f2h2(v[2], v[3], type), f2h2(v[4], v[5], type),
+                 f2h2(v[6], v[7], type));
+}
+
+// Two rows a turn keep six 16-byte loads of a lane in flight (one row where loads are single
+// elements, which are many already).
+template <bool GATED, int ACT, int TYPE, bool VEC>
+__global__ void __launch_bounds__(256, VEC ? 4 : 2) act_bwd_kernel(const DenseActBwd a,
+                                                         int64_t rows_per_block) {
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * COLS + lane * 8;
   const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
   const int64_t r1 = r0 + rows_per_block < a.m ? r0 + rows_per_block : a.m;
   const int64_t left = a.n - col;
   float sum[8] = {};
-  if (left > 0) {
-    for (int64_t r = r0 + grp; r < r1; r += GROUPS) {
-      float dy[8], z[8], u[8], dz[8];
-      load8(a.dy, r, col, left, a.type, dy);
-      if (a.pre.p) load8(a.pre, r, col, left, a.type, z);
-      if (GATED) load8(a.up, r, col, left, a.type, u);
+  auto one = [&](int64_t r, const uint4 &wy, const uint4 &wz, const uint4 &wu) {
+    float dy[8], z[8], u[8];
+    widen8(wy, TYPE, dy);
+    if (ACT != COLL_ACT_NONE) widen8(wz, TYPE, z);
+    if (GATED) widen8(wu, TYPE, u);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (GATED) {
-          float v, d;
-          act_value_slope(z[i], a.act, v, d);
-          dz[i] = dy[i] * u[i] * d;
-          u[i] = dy[i] * v;
-        } else {
-          float v, d = 1.0f;
-          if (a.pre.p) act_value_slope(z[i], a.act, v, d);
-          dz[i] = dy[i] * d;
-          sum[i] += dz[i];
-        }
+    for (int i = 0; i < 8; ++i) {
+      float v, d = 1.0f;
+      if (ACT != COLL_ACT_NONE) act_value_slope(z[i], ACT, v, d);
+      if (GATED) {
+        z[i] = dy[i] * v;
+        dy[i] = dy[i] * u[i] * d;
+      } else {
+        if (ACT != COLL_ACT_NONE) dy[i] *= d;
+        sum[i] += dy[i];
       }
-      if (a.dz) store8(a.dz, r * a.ld + col, left, a.type, dz);
-      if (GATED) store8(a.du, r * a.ld + col, left, a.type, u);
+    }
+    if (a.dz) store8(a.dz, r * a.ld + col, TYPE, dy);
+    if (GATED) store8(a.du, r * a.ld + col, TYPE, z);
+  };
+  if (left > 0) {
+    constexpr int AHEAD = VEC ? 2 : 1;
+    uint4 y[AHEAD], z[AHEAD] = {}, u[AHEAD] = {};
+    auto fetch = [&](int i, int64_t r) {
+      y[i] = load8<VEC>(a.dy, r, col, left);
+      if (ACT != COLL_ACT_NONE) z[i] = load8<VEC>(a.pre, r, col, left);
+      if (GATED) u[i] = load8<VEC>(a.up, r, col, left);
+    };
+    for (int64_t r = r0 + grp; r < r1; r += AHEAD * GROUPS) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (r + i * GROUPS < r1) fetch(i, r + i * GROUPS);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (r + i * GROUPS < r1) one(r + i * GROUPS, y[i], z[i], u[i]);
     }
   }
-  __shared__ float part[GROUPS][COLS];
-  if (!a.db) return;  // gated calls have none
+  if constexpr (!GATED) {
+    if (!a.db) return;
+    __shared__ float part[GROUPS][COLS];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) part[grp][lane * 8 + i] = sum[i];
-  __syncthreads();
-  const int64_t c = (int64_t)blockIdx.x * COLS + threadIdx.x;
-  if (c >= a.n) return;
-  float s = part[0][threadIdx.x];
+    for (int i = 0; i < 8; ++i) part[grp][lane * 8 + i] = sum[i];
+    __syncthreads();
+    const int64_t c = (int64_t)blockIdx.x * COLS + threadIdx.x;
+    if (c >= a.n) return;
+    float s = part[0][threadIdx.x];
 #pragma unroll
-  for (int g = 1; g < GROUPS; ++g) s += part[g][threadIdx.x];
-  if (gridDim.y == 1) st_elem(a.db, c, s, a.db_type);
-  else a.part[(int64_t)blockIdx.y * a.n + c] = s;
+    for (int g = 1; g < GROUPS; ++g) s += part[g][threadIdx.x];
+    if (gridDim.y == 1) st_elem(a.db, c, s, a.db_type);
+    else a.part[(int64_t)blockIdx.y * a.n + c] = s;
+  }
+}
+
+bool runs16(const DenseMat &m) {
+  return !m.p || (((uintptr_t)m.p & 15u) == 0 && m.cs == 1 && m.rs % 8 == 0);
+}
+
+template <bool GATED, int ACT>
+void launch_act_bwd(const DenseActBwd &a, dim3 grid, int64_t per, cudaStream_t s) {
+  const bool vec = a.n % 8 == 0 && runs16(a.dy) && runs16(a.pre) && runs16(a.up);
+  if (a.type == COLL_BF16) {
+    if (vec) act_bwd_kernel<GATED, ACT, COLL_BF16, true><<<grid, 256, 0, s>>>(a, per);
+    else act_bwd_kernel<GATED, ACT, COLL_BF16, false><<<grid, 256, 0, s>>>(a, per);
+  } else {
+    if (vec) act_bwd_kernel<GATED, ACT, COLL_F16, true><<<grid, 256, 0, s>>>(a, per);
+    else act_bwd_kernel<GATED, ACT, COLL_F16, false><<<grid, 256, 0, s>>>(a, per);
+  }
 }
 
 __global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t blocks, int64_t n,
@@ -112,12 +152,11 @@ __global__ void __launch_bounds__(256) pack_kernel(const DenseMat src, int64_t r
 
 template <bool GATED>
 __global__ void __launch_bounds__(256) empty_sum_kernel(const DenseJob j) {
-  const int64_t runs = (j.n + 7) / 8, total = j.m * runs;
+  const int64_t total = j.m * j.n;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / runs, c = (i - r * runs) * 8;
-    float g[8] = {}, u[8] = {};
-    epilogue_run8<GATED>(j.e, blockIdx.y, r, c, j.n - c, g, u);
+    const int64_t r = i / j.n, c = i - r * j.n;
+    epilogue_one<GATED>(j.e, blockIdx.y, r, c, 0.0f, 0.0f, GATED ? 0.0f : bias_at(j.e, c));
   }
 }
 
@@ -136,7 +175,7 @@ cudaError_t dense_pack(const DenseMat &src, int64_t rows, int64_t cols, void *ds
 }
 
 cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s) {
-  const dim3 grid(grid_for(j.m * ((j.n + 7) / 8)), (unsigned)j.nbatch);
+  const dim3 grid(grid_for(j.m * j.n), (unsigned)j.nbatch);
   if (j.gated) empty_sum_kernel<true><<<grid, 256, 0, s>>>(j);
   else empty_sum_kernel<false><<<grid, 256, 0, s>>>(j);
   return cudaGetLastError();
@@ -158,8 +197,20 @@ cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s) {
   const int64_t blocks = dense_act_bwd_row_blocks(a.m, a.n);
   const int64_t per = (a.m + blocks - 1) / blocks;
   const dim3 grid((unsigned)((a.n + COLS - 1) / COLS), (unsigned)blocks);
-  if (a.gated) act_bwd_kernel<true><<<grid, 256, 0, s>>>(a, per);
-  else act_bwd_kernel<false><<<grid, 256, 0, s>>>(a, per);
+  switch (a.act) {
+    case COLL_ACT_NONE: launch_act_bwd<false, COLL_ACT_NONE>(a, grid, per, s); break;
+#define COLL_ACT_CASE(act)                                     \
+  case act:                                                    \
+    if (a.gated) launch_act_bwd<true, act>(a, grid, per, s);   \
+    else launch_act_bwd<false, act>(a, grid, per, s);          \
+    break;
+    COLL_ACT_CASE(COLL_ACT_RELU)
+    COLL_ACT_CASE(COLL_ACT_GELU)
+    COLL_ACT_CASE(COLL_ACT_GELU_TANH)
+    COLL_ACT_CASE(COLL_ACT_SILU)
+#undef COLL_ACT_CASE
+    default: launch_act_bwd<true, COLL_ACT_SIGMOID>(a, grid, per, s);
+  }
   if (!a.gated && a.db && blocks > 1)
     join_kernel<<<(unsigned)((a.n + 255) / 256), 256, 0, s>>>(a.part, blocks, a.n, a.db,
                                                               a.db_type);

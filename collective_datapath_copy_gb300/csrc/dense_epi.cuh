@@ -40,10 +40,29 @@ constexpr float kRsqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
 
+// Phi(z), the standard normal distribution function, and exp(-z^2 / 2), by the polynomial
+// 7.1.26 of Abramowitz and Stegun for erfc(|z| / sqrt 2): absolute error below 1e-7, and the
+// factor exp(-z^2 / 2) keeps it small against the far negative values too. A reciprocal, an
+// exponential and eight multiply-adds.
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+  const float x = fabsf(z) * kRsqrt2;
+  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+  e = __expf(-x * x);
+  float p = fmaf(1.061405429f, t, -1.453152027f);
+  p = fmaf(p, t, 1.421413741f);
+  p = fmaf(p, t, -0.284496736f);
+  p = fmaf(p, t, 0.254829592f);
+  const float half = 0.5f * p * t * e;
+  return z < 0.0f ? half : 1.0f - half;
+}
+
 __device__ __forceinline__ float act_value(float z, int act) {
   switch (act) {
     case COLL_ACT_RELU: return z > 0.0f ? z : (z != z ? z : 0.0f);
-    case COLL_ACT_GELU: return 0.5f * z * (1.0f + erff(z * kRsqrt2));
+    case COLL_ACT_GELU: {
+      float e;
+      return z * normal_cdf(z, e);
+    }
     case COLL_ACT_GELU_TANH:
       // (1 + tanh(a)) / 2 = logistic(2 a)
       return z * logistic(2.0f * kTanhScale * fmaf(kTanhCubic * z * z, z, z));
@@ -61,9 +80,10 @@ __device__ __forceinline__ void act_value_slope(float z, int act, float &v, floa
       d = z > 0.0f ? 1.0f : 0.0f;
       return;
     case COLL_ACT_GELU: {
-      const float c = 0.5f * (1.0f + erff(z * kRsqrt2));
+      float e;
+      const float c = normal_cdf(z, e);
       v = z * c;
-      d = fmaf(z * kRsqrt2Pi, __expf(-0.5f * z * z), c);
+      d = fmaf(z * kRsqrt2Pi, e, c);
       return;
     }
     case COLL_ACT_GELU_TANH: {
@@ -100,11 +120,12 @@ __device__ __forceinline__ void st_elem(void *p, int64_t i, float v, int type) {
   else static_cast<uint16_t *>(p)[i] = f2h(v, type);
 }
 
-__device__ __forceinline__ void act_run8(float (&v)[8], int act) {
+template <int N>
+__device__ __forceinline__ void act_run(float (&v)[N], int act) {
   switch (act) {
-#define COLL_ACT_CASE(a)                                   \
-  case a:                                                  \
-    _Pragma("unroll") for (int i = 0; i < 8; ++i) v[i] = act_value(v[i], a); \
+#define COLL_ACT_CASE(a)                                                     \
+  case a:                                                                    \
+    _Pragma("unroll") for (int i = 0; i < N; ++i) v[i] = act_value(v[i], a); \
     return;
     COLL_ACT_CASE(COLL_ACT_RELU)
     COLL_ACT_CASE(COLL_ACT_GELU)
@@ -116,96 +137,196 @@ __device__ __forceinline__ void act_run8(float (&v)[8], int act) {
   }
 }
 
-__device__ __forceinline__ void ld_run8(const void *p, int64_t i, int type, float (&v)[8]) {
-  if (type == COLL_F32) {
-    const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-    const float4 b = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-    return;
-  }
-  const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+// ---- 32-byte accesses (sm_100 and later): one whole sector a lane
+
+__device__ __forceinline__ void ld_32b(const void *p, uint32_t *r) {
+  asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+}
+
+__device__ __forceinline__ void st_32b(void *p, const uint32_t *r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// v[0..32) += 32 neighbouring 16-bit elements held in r[16]
+__device__ __forceinline__ void add_halves(float (&v)[32], const uint32_t *r, int type) {
   if (type == COLL_BF16) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) h2f2(w[q], COLL_BF16, v[2 * q], v[2 * q + 1]);
+    for (int q = 0; q < 16; ++q) {
+      float lo, hi;
+      h2f2(r[q], COLL_BF16, lo, hi);
+      v[2 * q] += lo, v[2 * q + 1] += hi;
+    }
   } else {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) h2f2(w[q], COLL_F16, v[2 * q], v[2 * q + 1]);
+    for (int q = 0; q < 16; ++q) {
+      float lo, hi;
+      h2f2(r[q], COLL_F16, lo, hi);
+      v[2 * q] += lo, v[2 * q + 1] += hi;
+    }
   }
 }
 
-__device__ __forceinline__ void st_run8(void *p, int64_t i, int type, const float (&v)[8]) {
-  if (type == COLL_F32) {
-    float4 *o = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-    o[0] = make_float4(v[0], v[1], v[2], v[3]);
-    o[1] = make_float4(v[4], v[5], v[6], v[7]);
-    return;
-  }
-  uint32_t w[4];
-  if (type == COLL_BF16) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = f2h2(v[2 * q], v[2 * q + 1], COLL_BF16);
-  } else {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) w[q] = f2h2(v[2 * q], v[2 * q + 1], COLL_F16);
-  }
-  *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) = make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ void ld_halves(const void *p, int64_t i, uint32_t *r) {
+  const uint16_t *q = static_cast<const uint16_t *>(p) + i;
+  ld_32b(q, r);
+  ld_32b(q + 16, r + 8);
 }
 
-// Columns [col, col + 8) of one row; `left` = columns of the row from col on (>= 1). g holds the
-// product (gated: the gate's), u the up product.
+// 32 neighbouring elements from element i on, a multiple of 32 bytes
+__device__ __forceinline__ void st_run32(void *p, int64_t i, int type, const float (&v)[32]) {
+  if (type == COLL_F32) {
+    float *o = static_cast<float *>(p) + i;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t r[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) r[x] = __float_as_uint(v[8 * q + x]);
+      st_32b(o + 8 * q, r);
+    }
+    return;
+  }
+  uint32_t r[16];
+  if (type == COLL_BF16) {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) r[q] = f2h2(v[2 * q], v[2 * q + 1], COLL_BF16);
+  } else {
+#pragma unroll
+    for (int q = 0; q < 16; ++q) r[q] = f2h2(v[2 * q], v[2 * q + 1], COLL_F16);
+  }
+  uint16_t *o = static_cast<uint16_t *>(p) + i;
+  st_32b(o, r);
+  st_32b(o + 16, r + 8);
+}
+
+// ---- rows that start anywhere: 32 x 32 blocks through shared memory, so that neighbouring lanes
+// access neighbouring columns. `st` is the warp's own 32 x kPitch words (an odd pitch: a lane's
+// row and a row across the lanes are both free of bank conflicts); lane l holds row l of the
+// block; `rows` and `cols` say how much of the block there is. Elements are accessed in pairs
+// where rows start on 4 bytes.
+
+constexpr int kPitch = 17;
+
+__device__ __forceinline__ bool in_pairs(const void *p, int64_t rs) {
+  return ((uintptr_t)p & 3u) == 0 && (rs & 1) == 0;
+}
+
+// block element (r, c) at p[r * rs + c]
+__device__ __forceinline__ void staged_store(uint32_t *st, void *p, int64_t rs, int type, int rows,
+                                             int cols, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (type == COLL_F32) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) st[lane * kPitch + i] = __float_as_uint(v[16 * h + i]);
+      __syncwarp();
+      const int c = lane & 15;
+      if (16 * h + c < cols)
+#pragma unroll 4
+        for (int r = lane >> 4; r < rows; r += 2)
+          static_cast<uint32_t *>(p)[r * rs + 16 * h + c] = st[r * kPitch + c];
+    }
+    return;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    st[lane * kPitch + i] = type == COLL_BF16 ? f2h2(v[2 * i], v[2 * i + 1], COLL_BF16)
+                                              : f2h2(v[2 * i], v[2 * i + 1], COLL_F16);
+  __syncwarp();
+  uint16_t *const o = static_cast<uint16_t *>(p);
+  if (in_pairs(p, rs)) {
+    const int c = 2 * (lane & 15);
+#pragma unroll 4
+    for (int r = lane >> 4; r < rows; r += 2) {
+      const uint32_t w = st[r * kPitch + (lane & 15)];
+      if (c + 1 < cols) *reinterpret_cast<uint32_t *>(o + r * rs + c) = w;
+      else if (c < cols) o[r * rs + c] = (uint16_t)w;
+    }
+  } else if (lane < cols) {
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r)
+      o[r * rs + lane] = reinterpret_cast<const uint16_t *>(st + r * kPitch)[lane];
+  }
+}
+
+// v += the block with element (r, c) at p[r * rs + c * cs]
+__device__ __forceinline__ void staged_add(uint32_t *st, const void *p, int64_t rs, int64_t cs,
+                                           int type, int rows, int cols, float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (type == COLL_F32) {
+    const float *q = static_cast<const float *>(p);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      __syncwarp();
+      const int c = lane & 15;
+      if (16 * h + c < cols)
+#pragma unroll 8
+        for (int r = lane >> 4; r < rows; r += 2)
+          st[r * kPitch + c] = __float_as_uint(q[r * rs + (16 * h + c) * cs]);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[16 * h + i] += __uint_as_float(st[lane * kPitch + i]);
+    }
+    return;
+  }
+  const uint16_t *q = static_cast<const uint16_t *>(p);
+  __syncwarp();
+  if (cs == 1 && in_pairs(p, rs) && cols == 32) {
+#pragma unroll 8
+    for (int r = lane >> 4; r < rows; r += 2)
+      st[r * kPitch + (lane & 15)] =
+          *reinterpret_cast<const uint32_t *>(q + r * rs + 2 * (lane & 15));
+  } else if (lane < cols) {
+#pragma unroll 8
+    for (int r = 0; r < rows; ++r)
+      reinterpret_cast<uint16_t *>(st + r * kPitch)[lane] = q[r * rs + lane * cs];
+  }
+  __syncwarp();
+  uint32_t w[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) w[i] = st[lane * kPitch + i];
+  add_halves(v, w, type);
+}
+
+// v[i] += bias of column i, for every row
+__device__ __forceinline__ void add_bias(const DenseEpi &e, int64_t col, int cols,
+                                         float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  const float b =
+      lane < cols ? ld_elem(e.bias, (col + lane) * e.bias_stride, e.type) : 0.0f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(~0u, b, i);
+}
+
+// One element: g holds the product (gated: the gate's), u the up product; b the bias.
 template <bool GATED>
-__device__ __forceinline__ void epilogue_run8(const DenseEpi &e, int batch, int64_t row,
-                                              int64_t col, int64_t left, float (&g)[8],
-                                              float (&u)[8]) {
-  const int64_t o = row * e.out_rs[batch] + col;
-  if (e.vec && left >= 8) {
-    if (GATED) {
-      if (e.gate) {
-        st_run8(e.gate, row * e.gate_rs + col, e.type, g);
-        st_run8(e.up, row * e.up_rs + col, e.type, u);
-      }
-      act_run8(g, e.act);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) g[i] *= u[i];
-    } else {
-      float t[8];
-      if (e.bias) {
-        ld_run8(e.bias, col, e.type, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] += t[i];
-      }
-      if (e.pre) st_run8(e.pre, row * e.pre_rs + col, e.type, g);
-      act_run8(g, e.act);
-      if (e.res) {
-        ld_run8(e.res, row * e.res_rs + col, e.out_type, t);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] += t[i];
-      }
+__device__ __forceinline__ void epilogue_one(const DenseEpi &e, int batch, int64_t row, int64_t col,
+                                             float g, float u, float b) {
+  if (GATED) {
+    if (e.gate) {
+      st_elem(e.gate, row * e.gate_rs + col, g, e.type);
+      st_elem(e.up, row * e.up_rs + col, u, e.type);
     }
-    st_run8(e.out[batch], o, e.out_type, g);
-    return;
+    g = act_value(g, e.act) * u;
+  } else {
+    g += b;
+    if (e.pre) st_elem(e.pre, row * e.pre_rs + col, g, e.type);
+    g = act_value(g, e.act);
+    if (e.res) g += ld_elem(e.res, row * e.res_rs + col * e.res_cs, e.out_type);
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    if (i >= left) break;
-    const int64_t c = col + i;
-    float v = g[i];
-    if (GATED) {
-      if (e.gate) {
-        st_elem(e.gate, row * e.gate_rs + c, v, e.type);
-        st_elem(e.up, row * e.up_rs + c, u[i], e.type);
-      }
-      v = act_value(v, e.act) * u[i];
-    } else {
-      if (e.bias) v += ld_elem(e.bias, c * e.bias_stride, e.type);
-      if (e.pre) st_elem(e.pre, row * e.pre_rs + c, v, e.type);
-      v = act_value(v, e.act);
-      if (e.res) v += ld_elem(e.res, row * e.res_rs + c * e.res_cs, e.out_type);
-    }
-    st_elem(e.out[batch], o + i, v, e.out_type);
-  }
+  st_elem(e.out[batch], row * e.out_rs[batch] + col, g, e.out_type);
+}
+
+__device__ __forceinline__ float bias_at(const DenseEpi &e, int64_t col) {
+  return e.bias ? ld_elem(e.bias, col * e.bias_stride, e.type) : 0.0f;
 }
 
 }  // namespace coll

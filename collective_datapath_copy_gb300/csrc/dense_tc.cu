@@ -11,17 +11,20 @@
 // 64 multiply-adds. Gated: CTA 0 holds rows of the gate's weights and CTA 1 the same rows of the
 // up weights, and the accumulator's halves are g and u of the same columns.
 //
-// Warps: 0 loads (one thread), 1 issues the matrix instructions (the pair's first CTA only), 2
-// owns TMEM, 4-7 run the epilogue: TMEM -> registers (a row per lane) -> shared memory -> eight
-// consecutive columns per lane, so that global accesses are 16 bytes a lane and 64 contiguous
-// bytes a row. Two accumulators of 256 columns let the epilogue of one tile run beside the
-// products of the next. The grid is persistent; tiles are walked eight rows of tiles at a time,
+// Warps: 0 loads, 1 issues the matrix instructions (the pair's first CTA only), 2
+// owns TMEM, 4-11 run the epilogue, two warps for each 32 rows, 32 columns at a time: a lane holds
+// 32 columns of its row and reads and writes whole 32-byte sectors. Where an array's rows do not
+// start on 32 bytes, or the row ends inside the 32 columns, 16 columns at a time pass through
+// shared memory and neighbouring lanes take neighbouring columns. Two accumulators of 256 columns
+// let the epilogue of one tile run beside the products of the next. The grid is persistent; tiles are walked eight rows of tiles at a time,
 // which keeps the operands of the tiles in flight in L2.
 //
 // Every wait is bounded: a wait that runs out sets an abort flag, the CTA's roles leave their
 // loops, in-flight copies and products get time to land, TMEM is freed, and status says so.
 #include <cuda.h>
 #include <string.h>
+
+#include <type_traits>
 
 #include "dense.h"
 #include "dense_epi.cuh"
@@ -31,34 +34,20 @@
 namespace coll {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int CG = 2;                     // CTAs of a tile (cta_group::2)
 constexpr int kTileK = 64;                // elements of k per stage: one 128-byte swizzled row
 constexpr uint32_t kABytes = 128 * 128;   // 128 rows
 constexpr uint32_t kChunk = 64 * 128;     // MN-major: 64 k rows of 64 elements
 constexpr int kMaxStages = 12;
-constexpr int kPitch = 36;                // floats per staged row: 32 and a bank shift
-constexpr uint32_t kStageOut = 4 * 32 * kPitch * 4;
-constexpr uint64_t kLimitNs = 2000000000ull;
-constexpr uint64_t kDrainNs = 20000000ull;
+constexpr uint32_t kStageOut = kEpiWarps * 32 * kPitch * 4;
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
   uint32_t tmem;
   uint32_t abort;
 };
-
-// Wait for a phase; on failure raise the abort flag and the caller's status.
-__device__ __forceinline__ bool wait_bar(Shared *sh, uint64_t *bar, uint32_t parity,
-                                         int32_t *status) {
-  if (mbar_try_wait(bar, parity)) return true;
-  volatile uint32_t *flag = &sh->abort;
-  if (mbar_wait(bar, parity, kLimitNs, flag)) return true;
-  if (!*flag) {
-    *flag = 1u;
-    if (status) *status = COLL_ETIMEDOUT;
-  }
-  return false;
-}
 
 struct Tile {
   int batch;
@@ -77,15 +66,15 @@ __device__ __forceinline__ Tile tile_at(const TcParams &p, uint32_t t) {
   return r;
 }
 
-template <int CG, bool GATED>
+template <bool GATED>
 __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ TcParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ Shared sh;
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
-  float *const staged = reinterpret_cast<float *>(raw + (ring - smem_u32(raw)) +
-                                                  (size_t)p.stages * p.stage_bytes);
+  uint32_t *const staged = reinterpret_cast<uint32_t *>(raw + (ring - smem_u32(raw)) +
+                                                        (size_t)p.stages * p.stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = CG == 2 ? cluster_rank() : 0u;
+  const uint32_t rank = cluster_rank();
   const bool leader = rank == 0u;
   const uint32_t clusters = gridDim.x / CG, cluster = blockIdx.x / CG;
 
@@ -96,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
-      mbar_init(&sh.acc_empty[i], 4 * CG);
+      mbar_init(&sh.acc_empty[i], kEpiWarps * CG);
     }
     sh.abort = 0u;
     mbar_init_fence();
@@ -104,168 +93,208 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   if (warp == 2) tmem_alloc<CG>(&sh.tmem, 512);
   tc_fence_before();
   __syncthreads();
-  if (CG == 2) cluster_sync();
+  cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
 
+  const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
+  const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
+
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t s = 0, phase = 0;
-      bool ok = true;
-      for (uint32_t t = cluster; ok && t < p.tiles; t += clusters) {
-        const Tile tl = tile_at(p, t);
-        const int32_t m = (int32_t)tl.m0 + (int32_t)rank * 128;
-        for (int seg = 0; ok && seg < p.nseg; ++seg) {
-          const CUtensorMap *ma = &p.a[p.nbatch == 2 ? tl.batch : seg];
-          const CUtensorMap *mb = &p.b[GATED && CG == 2 ? rank : seg];
-          const int32_t n = (int32_t)tl.n0 + (GATED ? 0 : (int32_t)rank * p.b_rows);
-          const bool amn = p.a_mn[p.nbatch == 2 ? tl.batch : seg];
-          const bool bmn = p.b_mn[GATED && CG == 2 ? rank : seg];
-          // bytes a stage receives, boxes past the edges counted whole
-          const uint32_t kr = p.b_rows * 128, mr = p.b_chunks * kChunk;
-          const uint32_t bytes =
-              CG * kABytes + (GATED ? (p.b_mn[0] ? mr : kr) + (p.b_mn[1] ? mr : kr)
-                                    : CG * (bmn ? mr : kr));
-          for (int kb = 0; kb < p.kblocks; ++kb) {
-            if (!wait_bar(&sh, &sh.empty[s], phase ^ 1u, p.status)) {
-              ok = false;
-              break;
-            }
-            uint32_t bar = smem_u32(&sh.full[s]);
-            if (leader) mbar_expect_tx(&sh.full[s], bytes);
-            if (CG == 2) bar = map_rank(bar, 0);
-            const uint32_t da = ring + s * p.stage_bytes, db = da + kABytes;
-            const int32_t k = kb * kTileK;
-            auto load = [&](uint32_t d, const CUtensorMap *map, int32_t x, int32_t y) {
-              if (CG == 2) tma_box_pair(d, map, x, y, bar);
-              else tma_box(d, map, x, y, bar);
-            };
-            if (amn) {
-              load(da, ma, m, k);
-              load(da + kChunk, ma, m + 64, k);
-            } else {
-              load(da, ma, k, m);
-            }
-            if (bmn) {
-              for (int c = 0; c < p.b_chunks; ++c) load(db + c * kChunk, mb, n + 64 * c, k);
-            } else {
-              load(db, mb, k, n);
-            }
-            if (GATED && CG == 1) {
-              const uint32_t d2 = db + p.b_rows * 128;
-              if (p.b_mn[1]) {
-                for (int c = 0; c < p.b_chunks; ++c) load(d2 + c * kChunk, &p.b[1], n + 64 * c, k);
-              } else {
-                load(d2, &p.b[1], k, n);
-              }
-            }
-            if (++s == (uint32_t)p.stages) {
-              s = 0;
-              phase ^= 1u;
-            }
+    const bool one = elect_one();
+    const uint32_t arrive0 = map_rank(full0, 0);
+    // bytes a stage receives, boxes past the edges counted whole
+    const uint32_t kr = p.b_rows * 128, mr = p.b_chunks * kChunk;
+    uint32_t s = 0, phase = 0;
+    bool ok = true;
+    // k blocks of one segment; the operands' major axes are fixed within it
+    auto segment = [&](auto amn_c, auto bmn_c, const CUtensorMap *ma, const CUtensorMap *mb,
+                       int32_t m, int32_t n) {
+      constexpr bool amn = decltype(amn_c)::value, bmn = decltype(bmn_c)::value;
+      const uint32_t bytes = CG * (kABytes + (bmn ? mr : kr));
+      const int32_t end = p.kblocks * kTileK;
+      for (int32_t k = 0; k < end; k += kTileK) {
+        if (!wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status)) return false;
+        if (one) {
+          const uint32_t da = ring + s * stage_bytes, db = da + kABytes, bar = arrive0 + 8 * s;
+          if (leader) bar_expect(full0 + 8 * s, bytes);
+          if (amn) {
+            tma_box_pair(da, ma, m, k, bar);
+            tma_box_pair(da + kChunk, ma, m + 64, k, bar);
+          } else {
+            tma_box_pair(da, ma, k, m, bar);
+          }
+          if (bmn) {
+            tma_box_pair(db, mb, n, k, bar);
+            if (p.b_chunks > 1) tma_box_pair(db + kChunk, mb, n + 64, k, bar);
+          } else {
+            tma_box_pair(db, mb, k, n, bar);
           }
         }
-      }
-      // every slot's last products are done before this CTA may go away
-      for (int i = 0; ok && i < p.stages; ++i) {
-        ok = wait_bar(&sh, &sh.empty[s], phase ^ 1u, p.status);
-        if (++s == (uint32_t)p.stages) {
+        __syncwarp();
+        if (++s == stages) {
           s = 0;
           phase ^= 1u;
         }
       }
+      return true;
+    };
+    using Yes = std::integral_constant<bool, true>;
+    using No = std::integral_constant<bool, false>;
+    for (uint32_t t = cluster; ok && t < p.tiles; t += clusters) {
+      const Tile tl = tile_at(p, t);
+      const int32_t m = (int32_t)tl.m0 + (int32_t)rank * 128;
+      const int32_t n = (int32_t)tl.n0 + (GATED ? 0 : (int32_t)rank * p.b_rows);
+      for (int seg = 0; ok && seg < p.nseg; ++seg) {
+        const int ia = p.nbatch == 2 ? tl.batch : seg, ib = GATED ? (int)rank : seg;
+        const CUtensorMap *ma = &p.a[ia], *mb = &p.b[ib];
+        if (p.a_mn[ia])
+          ok = p.b_mn[ib] ? segment(Yes{}, Yes{}, ma, mb, m, n) : segment(Yes{}, No{}, ma, mb, m, n);
+        else
+          ok = p.b_mn[ib] ? segment(No{}, Yes{}, ma, mb, m, n) : segment(No{}, No{}, ma, mb, m, n);
+      }
+    }
+    // every slot's last products are done before this CTA may go away
+    for (uint32_t i = 0; ok && i < stages; ++i) {
+      ok = wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
+      if (++s == stages) {
+        s = 0;
+        phase ^= 1u;
+      }
     }
   } else if (warp == 1) {
-    if (leader && lane == 0) {
-      const uint64_t kd = smem_desc(16, 1024), md = smem_desc(kChunk, 1024);
-      uint32_t s = 0, phase = 0, it = 0;
+    if (leader) {
+      const bool one = elect_one();
+      const uint32_t hi = desc_hi(1024), step = stage_bytes >> 4;
+      const uint32_t acc_full0 = smem_u32(&sh.acc_full[0]), acc_empty0 = smem_u32(&sh.acc_empty[0]);
+      uint32_t s = 0, phase = 0, it = 0, at = 0;  // at: 16-byte units from the ring's start
       bool ok = true;
       for (uint32_t t = cluster; ok && t < p.tiles; t += clusters, ++it) {
         const uint32_t buf = it & 1u, d = tmem + buf * 256u;
-        if (!wait_bar(&sh, &sh.acc_empty[buf], ((it >> 1) & 1u) ^ 1u, p.status)) break;
+        if (!wait_bar(&sh.abort, acc_empty0 + 8 * buf, ((it >> 1) & 1u) ^ 1u, p.status)) break;
         tc_fence_after();
         const int batch = p.nbatch == 2 ? tile_at(p, t).batch : 0;
-        bool add = false;
+        uint32_t add = 0;
         for (int seg = 0; ok && seg < p.nseg; ++seg) {
           const int ia = p.nbatch == 2 ? batch : seg;
           const bool amn = p.a_mn[ia], bmn = p.b_mn[seg];
-          const uint64_t ad = amn ? md : kd, bd = bmn ? md : kd;
-          const uint32_t as = amn ? 2048u : 32u, bs = bmn ? 2048u : 32u;
+          // an MN-major operand's next 16 of k are 16 rows on, a K-major one's 32 bytes
+          const uint32_t as = amn ? 2048u >> 4 : 32u >> 4, bs = bmn ? 2048u >> 4 : 32u >> 4;
+          const uint32_t a0 = desc_lo(ring, amn ? kChunk : 16u);
+          const uint32_t b0 = desc_lo(ring + kABytes, bmn ? kChunk : 16u);
           const uint32_t idesc = p.idesc | ((uint32_t)amn << 15) | ((uint32_t)bmn << 16);
-          for (int kb = 0; kb < p.kblocks; ++kb) {
-            if (!wait_bar(&sh, &sh.full[s], phase, p.status)) {
+          for (int kb = p.kblocks; kb > 0; --kb) {
+            if (!wait_bar(&sh.abort, full0 + 8 * s, phase, p.status)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint32_t sa = ring + s * p.stage_bytes, sb = sa + kABytes;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              mma_f16<CG>(d, desc_at(ad, sa + q * as), desc_at(bd, sb + q * bs), idesc, add);
-              add = true;
+            if (one) {
+              const uint32_t a = a0 + at, b = b0 + at;
+              mma_f16<CG>(d, a, hi, b, hi, idesc, add);
+              mma_f16<CG>(d, a + as, hi, b + bs, hi, idesc, 1);
+              mma_f16<CG>(d, a + 2 * as, hi, b + 2 * bs, hi, idesc, 1);
+              mma_f16<CG>(d, a + 3 * as, hi, b + 3 * bs, hi, idesc, 1);
+              mma_commit<CG>(empty0 + 8 * s, 3);
             }
-            mma_commit<CG>(&sh.empty[s], 3);
-            if (++s == (uint32_t)p.stages) {
+            __syncwarp();
+            add = 1;
+            at += step;
+            if (++s == stages) {
               s = 0;
+              at = 0;
               phase ^= 1u;
             }
           }
         }
-        if (ok) mma_commit<CG>(&sh.acc_full[buf], 3);
+        if (ok && one) mma_commit<CG>(acc_full0 + 8 * buf, 3);
+        __syncwarp();
       }
     }
   } else if (warp >= 4) {
-    const int quad = warp & 3;
-    float *const st = staged + quad * 32 * kPitch;
+    const int quad = warp & 3, part = (warp - 4) >> 2;
+    uint32_t *const st = staged + (warp - 4) * 32 * kPitch;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const int rr = lane >> 2, cc = (lane & 3) * 8;
+    const DenseEpi &e = p.e;
+    const bool pre_res = !GATED && e.vec && e.res && e.out_type != COLL_F32;
     uint32_t it = 0;
     for (uint32_t t = cluster; t < p.tiles; t += clusters, ++it) {
       const Tile tl = tile_at(p, t);
       const uint32_t buf = it & 1u;
-      if (!__all_sync(~0u, wait_bar(&sh, &sh.acc_full[buf], (it >> 1) & 1u, p.status))) break;
-      tc_fence_after();
-      const int64_t row0 = tl.m0 + rank * 128 + quad * 32;
+      const int64_t row0 = tl.m0 + rank * 128 + quad * 32, row = row0 + lane;
+      const bool live = row < p.m;
       const int cols = (int)min((int64_t)p.tile_cols, p.n - tl.n0);
-      for (int c0 = 0; c0 < cols; c0 += 32) {
-        float v[32], g[4][8], u[4][8];
+      uint32_t r[16];  // the residual of the next 32 columns, asked for ahead
+      auto ask = [&](int c0) {
+        if (pre_res && live && c0 + 32 <= cols) ld_halves(e.res, row * e.res_rs + tl.n0 + c0, r);
+      };
+      ask(part * 32);
+      if (!__all_sync(~0u, wait_bar(&sh.abort, smem_u32(&sh.acc_full[buf]), (it >> 1) & 1u, p.status))) break;
+      tc_fence_after();
+      for (int c0 = part * 32; c0 < cols; c0 += 64) {
+        float g[32], u[GATED ? 32 : 1];
         const uint32_t at = lanes + buf * 256u + c0;
+        tmem_load32(at, g);
+        if constexpr (GATED) tmem_load32(at + p.tile_cols, u);
+        const int64_t col = tl.n0 + c0;
+        const bool vec = e.vec && c0 + 32 <= cols;
+        const int rows = (int)max((int64_t)0, min((int64_t)32, p.m - row0)), left = min(32, cols - c0);
+        auto store = [&](void *base, int64_t rs, int type, const float (&v)[32]) {
+          if (vec) {
+            if (live) st_run32(base, row * rs + col, type, v);
+          } else {
+            const int64_t at0 = row0 * rs + col;
+            staged_store(st, static_cast<char *>(base) + at0 * (type == COLL_F32 ? 4 : 2), rs, type,
+                         rows, left, v);
+          }
+        };
+        if constexpr (GATED) {
+          if (e.gate) {
+            store(e.gate, e.gate_rs, e.type, g);
+            store(e.up, e.up_rs, e.type, u);
+          }
+          act_run(g, e.act);
 #pragma unroll
-        for (int w = 0; w < (GATED ? 2 : 1); ++w) {
-          tmem_load32(at + w * p.tile_cols, v);
-          if (c0 + 32 >= cols && w == (GATED ? 1 : 0)) {  // the accumulator has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              if (CG == 2 && !leader) mbar_arrive_remote(map_rank(smem_u32(&sh.acc_empty[buf]), 0));
-              else mbar_arrive(&sh.acc_empty[buf]);
+          for (int i = 0; i < 32; ++i) g[i] *= u[i];
+        } else {
+          if (e.bias) {
+            if (vec) {
+              uint32_t b[16];
+              ld_halves(e.bias, col, b);
+              add_halves(g, b, e.type);
+            } else {
+              add_bias(e, col, left, g);
             }
           }
-          __syncwarp();
+          if (e.pre) store(e.pre, e.pre_rs, e.type, g);
+          act_run(g, e.act);
+          if (e.res) {
+            if (!vec) {
+              const int64_t at0 = row0 * e.res_rs + col * e.res_cs;
+              staged_add(st, static_cast<const char *>(e.res) + at0 * (e.out_type == COLL_F32 ? 4 : 2),
+                         e.res_rs, e.res_cs, e.out_type, rows, left, g);
+            } else if (pre_res) {
+              add_halves(g, r, e.type);
+              ask(c0 + 64);
+            } else if (live) {
+              const float *q = static_cast<const float *>(e.res) + row * e.res_rs + col;
 #pragma unroll
-          for (int q = 0; q < 8; ++q)
-            *reinterpret_cast<float4 *>(st + lane * kPitch + 4 * q) =
-                make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-          __syncwarp();
+              for (int i = 0; i < 32; i += 8) {
+                uint32_t x[8];
+                ld_32b(q + i, x);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 x = *reinterpret_cast<const float4 *>(st + (q * 8 + rr) * kPitch + cc);
-            const float4 y =
-                *reinterpret_cast<const float4 *>(st + (q * 8 + rr) * kPitch + cc + 4);
-            float *o = w ? u[q] : g[q];
-            o[0] = x.x, o[1] = x.y, o[2] = x.z, o[3] = x.w;
-            o[4] = y.x, o[5] = y.y, o[6] = y.z, o[7] = y.w;
+                for (int w = 0; w < 8; ++w) g[i + w] += __uint_as_float(x[w]);
+              }
+            }
           }
         }
-        const int64_t left = (int64_t)cols - c0 - cc;
-        if (left > 0) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int64_t row = row0 + q * 8 + rr;
-            if (row < p.m)
-              epilogue_run8<GATED>(p.e, tl.batch, row, tl.n0 + c0 + cc, left, g[q], u[q]);
-          }
-        }
+        store(e.out[tl.batch], e.out_rs[tl.batch], e.out_type, g);
+      }
+      tc_fence_before();  // this warp has read its part of the accumulator
+      __syncwarp();
+      if (lane == 0) {
+        if (!leader) mbar_arrive_remote(map_rank(smem_u32(&sh.acc_empty[buf]), 0));
+        else mbar_arrive(&sh.acc_empty[buf]);
       }
     }
   }
@@ -273,21 +302,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   __syncwarp();
   tc_fence_before();
   __syncthreads();
-  if (sh.abort) {  // let copies and products in flight land
-    const uint64_t t0 = globaltimer();
-    while (globaltimer() - t0 < kDrainNs) __nanosleep(1000);
-  }
-  if (CG == 2) cluster_sync();
+  if (sh.abort) drain();
+  cluster_sync();
   if (warp == 2) {
     tc_fence_after();
     tmem_free<CG>(tmem, 512);
   }
 }
 
-template <int CG, bool GATED>
+template <bool GATED>
 cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStream_t s) {
   static const cudaError_t ready = cudaFuncSetAttribute(
-      tc_kernel<CG, GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
+      tc_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
   if (ready != cudaSuccess) return ready;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(clusters * CG);
@@ -300,11 +326,15 @@ cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStre
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = CG == 2 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, tc_kernel<CG, GATED>, p);
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tc_kernel<GATED>, p);
 }
 
-int encode(CUtensorMap *map, const TcOperand &o, int64_t type, uint32_t rows) {
+uint32_t ceil_div(int64_t a, int64_t b) { return (uint32_t)((a + b - 1) / b); }
+
+}  // namespace
+
+int tc_encode(CUtensorMap *map, const TcOperand &o, int64_t type, uint32_t rows) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (!fn) return COLL_ECUDA;
   const cuuint64_t inner = (cuuint64_t)(o.mn ? o.rows : o.k);
@@ -321,10 +351,6 @@ int encode(CUtensorMap *map, const TcOperand &o, int64_t type, uint32_t rows) {
              : COLL_EINVAL;
 }
 
-uint32_t ceil_div(int64_t a, int64_t b) { return (uint32_t)((a + b - 1) / b); }
-
-}  // namespace
-
 int tc_plan(TcParams &p, const DenseJob &j, const TcOperand *a, const TcOperand *b,
             uint32_t sms) {
   memset(&p, 0, sizeof(p));
@@ -335,24 +361,25 @@ int tc_plan(TcParams &p, const DenseJob &j, const TcOperand *a, const TcOperand 
   p.nseg = j.nseg;
   p.nbatch = j.nbatch;
   p.kblocks = (int32_t)ceil_div(j.k, kTileK);
-  const uint32_t cg = 2, clusters = sms / cg;
-  p.tile_rows = 128 * cg;
+  const uint32_t clusters = sms / CG;
+  p.tile_rows = 128 * CG;
   p.tiles_m = ceil_div(j.m, p.tile_rows);
-  // Columns of the accumulator: the widest (least operand traffic) unless a narrower tile fills
-  // the last wave better. A tile costs its columns plus a fixed part of about 24 (its epilogue's
-  // tail and the ring's refill).
+  // Columns of the accumulator: those with the least rounds of tiles times the time of a tile's k
+  // block. Measured at 4096 x 4096 x 8192: 349 ns for 256 columns, 199 for 128 and 167 for 64,
+  // where issuing a block's copies and products is the limit.
   int best = 256;
   int64_t cost = INT64_MAX;
   for (int bn = 256; bn >= 64; bn -= j.gated ? 64 : 32) {
     const int64_t cols = j.gated ? bn / 2 : bn;
     const int64_t tiles = (int64_t)p.tiles_m * ceil_div(j.n, cols) * j.nbatch;
-    const int64_t c = (tiles + clusters - 1) / clusters * (bn + 24);
+    const int64_t block = 58 + bn * 73 / 64, c = (tiles + clusters - 1) / clusters *
+                                                (block > 167 ? block : 167);
     if (c < cost) {
       cost = c;
       best = bn;
     }
   }
-  p.b_rows = best / (int)cg;
+  p.b_rows = best / CG;
   p.tile_cols = j.gated ? best / 2 : best;
   p.b_chunks = (p.b_rows + 63) / 64;
   p.tiles_n = ceil_div(j.n, p.tile_cols);
@@ -363,27 +390,27 @@ int tc_plan(TcParams &p, const DenseJob &j, const TcOperand *a, const TcOperand 
   bool bmn = false;
   for (int i = 0; i < na; ++i) {
     p.a_mn[i] = a[i].mn;
-    const int c = encode(&p.a[i], a[i], j.e.type, 128);
+    const int c = tc_encode(&p.a[i], a[i], j.e.type, 128);
     if (c) return c;
   }
   for (int i = 0; i < nb; ++i) {
     p.b_mn[i] = b[i].mn;
     bmn = bmn || b[i].mn;
-    const int c = encode(&p.b[i], b[i], j.e.type, (uint32_t)p.b_rows);
+    const int c = tc_encode(&p.b[i], b[i], j.e.type, (uint32_t)p.b_rows);
     if (c) return c;
   }
   const uint32_t rows = bmn ? (uint32_t)p.b_chunks * 64u : (uint32_t)p.b_rows;
   p.stage_bytes = kABytes + ((rows * 128u + 1023u) & ~1023u);
   p.stages = (int32_t)((kTcSmem - 1024 - kStageOut) / p.stage_bytes);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.idesc = mma_desc(j.e.type == COLL_BF16, false, false, 128 * cg, (uint32_t)best);
+  p.idesc = mma_desc(j.e.type == COLL_BF16, false, false, 128 * CG, (uint32_t)best);
   return COLL_OK;
 }
 
 cudaError_t tc_run(const TcParams &p, bool gated, uint32_t sms, cudaStream_t s) {
-  const uint32_t most = sms / 2, clusters = p.tiles < most ? p.tiles : most;
+  const uint32_t most = sms / CG, clusters = p.tiles < most ? p.tiles : most;
   const uint32_t smem = 1024 + (uint32_t)p.stages * p.stage_bytes + kStageOut;
-  return gated ? launch<2, true>(p, clusters, smem, s) : launch<2, false>(p, clusters, smem, s);
+  return gated ? launch<true>(p, clusters, smem, s) : launch<false>(p, clusters, smem, s);
 }
 
 }  // namespace coll

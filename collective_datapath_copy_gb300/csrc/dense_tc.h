@@ -32,6 +32,9 @@ struct TcOperand {
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
+// Map of an operand in boxes of 64 of k by `rows` rows (k contiguous) or 64 rows by 64 of k.
+int tc_encode(CUtensorMap *map, const TcOperand &o, int64_t type, uint32_t rows);
+
 // Fill shapes and maps of `p` for the job; operands a[nseg or nbatch], b[nseg, or 2 when gated].
 int tc_plan(TcParams &p, const DenseJob &j, const TcOperand *a, const TcOperand *b, uint32_t sms);
 cudaError_t tc_run(const TcParams &p, bool gated, uint32_t sms, cudaStream_t s);
