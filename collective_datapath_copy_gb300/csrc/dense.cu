@@ -204,12 +204,26 @@ int sm_count(uint32_t &sms) {
   return COLL_OK;
 }
 
+// Products that the direct kernel takes: few rows, everything contiguous along k.
+bool few_tokens(const DenseJob &j) {
+  auto along_k = [&](const DenseMat &m) { return m.cs == 1 || j.k == 1; };
+  return j.m <= coll::kGemvMost && j.k <= (int64_t)1 << 30 && j.nseg == 1 && j.nbatch == 1 && along_k(j.a[0]) &&
+         along_k(j.b[0]) && (!j.gated || along_k(j.b[1]));
+}
+
 // One product; only counts its workspace where `dry`.
 int product(DenseJob &j, Ws &ws, bool dry, cudaStream_t s) {
   if (j.m == 0 || j.n == 0) return COLL_OK;
   set_vec(j);
   if (j.k == 0)
     return dry || coll::dense_empty_sum(j, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  uint32_t sms = 0;
+  if (few_tokens(j)) {
+    if (dry) return COLL_OK;
+    const int c = sm_count(sms);
+    if (c) return c;
+    return coll::gemv_run(j, sms, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  }
   TcOperand a[2], b[2];
   const int na = j.nbatch == 2 || j.nseg == 2 ? 2 : 1, nb = j.gated || j.nseg == 2 ? 2 : 1;
   for (int i = 0; i < na; ++i) {
@@ -230,10 +244,16 @@ int product(DenseJob &j, Ws &ws, bool dry, cudaStream_t s) {
     }
   }
   if (dry) return COLL_OK;
-  uint32_t sms = 0;
-  coll::TcParams p;
   int c = sm_count(sms);
-  if (!c) c = coll::tc_plan(p, j, a, b, sms);
+  if (c) return c;
+  if (j.m <= coll::kSkinnyMost && j.nseg == 1 && j.nbatch == 1) {
+    coll::SkinnyParams q;
+    c = coll::skinny_plan(q, j, b, a[0], sms);
+    if (c) return c;
+    return coll::skinny_run(q, j.gated != 0, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  }
+  coll::TcParams p;
+  c = coll::tc_plan(p, j, a, b, sms);
   if (c) return c;
   return coll::tc_run(p, j.gated != 0, sms, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
 }

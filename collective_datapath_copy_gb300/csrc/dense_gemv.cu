@@ -1,0 +1,203 @@
+// The products of the dense operators for one to a few tokens.
+//
+// Bound by HBM (the weights, read once) and by latency, so there is no staging, no barrier in the
+// loop and one launch: every warp loads weights straight into the fragments of mma.m16n8k16, 16
+// weight rows by 64 of k a step (gated: eight rows of each matrix, so a lane ends up with g and u
+// of the same output), the tokens are the eight columns. The order of k inside a step is the same
+// for both operands and otherwise free, so a lane takes 16 neighbouring elements of its row, 32
+// bytes, and four lanes a whole 128-byte line. The warps of a CTA take the steps of its rows in
+// turn and join once, in order, through shared memory. Several steps of loads per lane are in
+// flight before the first is used.
+//
+// tcgen05 is the wrong tool here: an instruction of 128 rows by 16 tokens takes about 27 ns to
+// issue whatever the batch, 7 us for k = 4096, and sharing k between CTAs costs a cluster
+// launch and two cluster barriers, 2 to 3 us.
+#include <type_traits>
+
+#include "dense.h"
+#include "dense_epi.cuh"
+#include "dense_tc.h"
+
+namespace coll {
+namespace {
+
+constexpr int kStep = 64;      // elements of k a warp takes at a time
+constexpr int kMaxWarps = 16;
+
+__device__ __forceinline__ void ld_stream32(const void *p, uint32_t (&r)[8]) {
+  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+                 "=r"(r[6]), "=r"(r[7])
+               : "l"(p));
+}
+
+// 16 elements from p (element k of its row of `len`), zeros past the row's end. ALIGN: bytes that
+// every row start and hence p is a multiple of.
+template <int ALIGN>
+__device__ __forceinline__ void load16(const uint16_t *p, int k, int len, uint32_t (&r)[8]) {
+  if (ALIGN == 32) {  // len is a multiple of 16
+    if (k < len) {
+      ld_stream32(p, r);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) r[i] = 0u;
+  } else if (ALIGN == 16) {  // len is a multiple of 8
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (k + 8 * h < len) v = __ldg(reinterpret_cast<const uint4 *>(p) + h);
+      r[4 * h] = v.x, r[4 * h + 1] = v.y, r[4 * h + 2] = v.z, r[4 * h + 3] = v.w;
+    }
+  } else if (ALIGN == 4) {  // len is even
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      r[i] = k + 2 * i < len ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t lo = k + 2 * i < len ? __ldg(p + 2 * i) : 0u;
+      const uint32_t hi = k + 2 * i + 1 < len ? __ldg(p + 2 * i + 1) : 0u;
+      r[i] = lo | hi << 16;
+    }
+  }
+}
+
+template <int TYPE>
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  if (TYPE == COLL_BF16)
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// NT: columns of eight tokens.
+template <bool GATED, int TYPE, int NT, int ALIGN>
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) gemv_kernel(const GemvParams p) {
+  constexpr int FEAT = GATED ? 8 : 16;   // outputs of a CTA
+  constexpr int AHEAD = NT == 1 ? 4 : 2;
+  __shared__ float part[kMaxWarps][8 * NT][16];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  const int64_t f0 = (int64_t)blockIdx.x * FEAT;
+  const int len = (int)p.k;
+  const int64_t fa = f0 + g, fb = GATED ? fa : fa + 8;
+  const int la = fa < p.n ? len : 0, lb = fb < p.n ? len : 0;  // rows that are not there are empty
+  const uint16_t *wa = static_cast<const uint16_t *>(p.w[0]) + (la ? fa : 0) * p.ld[0] + 16 * t;
+  const uint16_t *wb =
+      static_cast<const uint16_t *>(p.w[GATED ? 1 : 0]) + (lb ? fb : 0) * p.ld[GATED ? 1 : 0] +
+      16 * t;
+  const uint16_t *xt[NT];
+  int lx[NT];
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    const int tok = c * 8 + g;
+    lx[c] = tok < (int)p.m ? len : 0;
+    xt[c] = static_cast<const uint16_t *>(p.x) + (lx[c] ? tok : 0) * p.x_ld + 16 * t;
+  }
+  float acc[NT][4] = {};
+  const int steps = (len + kStep - 1) / kStep;
+  for (int s = warp; s < steps; s += AHEAD * warps) {
+    uint32_t a[AHEAD][8], b[AHEAD][8], x[AHEAD][NT][8];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int k = (s + i * warps) * kStep;
+      load16<ALIGN>(wa + k, k + 16 * t, la, a[i]);
+      load16<ALIGN>(wb + k, k + 16 * t, lb, b[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int k = (s + i * warps) * kStep;
+#pragma unroll
+      for (int c = 0; c < NT; ++c) load16<ALIGN>(xt[c] + k, k + 16 * t, lx[c], x[i][c]);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int c = 0; c < NT; ++c)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          mma16816<TYPE>(acc[c], a[i][2 * q], b[i][2 * q], a[i][2 * q + 1], b[i][2 * q + 1],
+                         x[i][c][2 * q], x[i][c][2 * q + 1]);
+  }
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    part[warp][c * 8 + 2 * t][g] = acc[c][0];
+    part[warp][c * 8 + 2 * t + 1][g] = acc[c][1];
+    part[warp][c * 8 + 2 * t][g + 8] = acc[c][2];
+    part[warp][c * 8 + 2 * t + 1][g + 8] = acc[c][3];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < FEAT * (int)p.m; i += blockDim.x) {
+    const int tok = i / FEAT, f = i % FEAT;
+    if (f0 + f >= p.n) continue;
+    float v = part[0][tok][f], u = GATED ? part[0][tok][(f + 8) & 15] : 0.0f;
+    for (int w = 1; w < warps; ++w) {
+      v += part[w][tok][f];
+      if (GATED) u += part[w][tok][(f + 8) & 15];
+    }
+    epilogue_one<GATED>(p.e, 0, tok, f0 + f, v, u, GATED ? 0.0f : bias_at(p.e, f0 + f));
+  }
+}
+
+template <bool GATED, int TYPE, int NT>
+cudaError_t launch(const GemvParams &p, int align, cudaStream_t s) {
+  const unsigned grid = (unsigned)((p.n + (GATED ? 8 : 16) - 1) / (GATED ? 8 : 16));
+  const unsigned threads = p.warps * 32u;
+  switch (align) {
+    case 32: gemv_kernel<GATED, TYPE, NT, 32><<<grid, threads, 0, s>>>(p); break;
+    case 16: gemv_kernel<GATED, TYPE, NT, 16><<<grid, threads, 0, s>>>(p); break;
+    case 4: gemv_kernel<GATED, TYPE, NT, 4><<<grid, threads, 0, s>>>(p); break;
+    default: gemv_kernel<GATED, TYPE, NT, 2><<<grid, threads, 0, s>>>(p);
+  }
+  return cudaGetLastError();
+}
+
+template <bool GATED, int TYPE>
+cudaError_t launch(const GemvParams &p, int align, cudaStream_t s) {
+  return p.m <= 8 ? launch<GATED, TYPE, 1>(p, align, s) : launch<GATED, TYPE, 2>(p, align, s);
+}
+
+// The widest access that every row of the matrix starts on.
+int row_align(const void *p, int64_t rows, int64_t ld, int64_t k) {
+  const uint64_t bits = (uintptr_t)p | (rows > 1 ? (uint64_t)ld * 2 : 0) | (uint64_t)k * 2;
+  return bits % 32 == 0 ? 32 : bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 2;
+}
+
+}  // namespace
+
+cudaError_t gemv_run(const DenseJob &j, uint32_t sms, cudaStream_t s) {
+  GemvParams p = {};
+  p.e = j.e;
+  p.m = j.m;
+  p.n = j.n;
+  p.k = j.k;
+  p.x = j.a[0].p;
+  p.x_ld = j.a[0].rs;
+  int align = row_align(p.x, j.m, p.x_ld, j.k);
+  for (int i = 0; i < (j.gated ? 2 : 1); ++i) {
+    p.w[i] = j.b[i].p;
+    p.ld[i] = j.b[i].rs;
+    const int a = row_align(p.w[i], j.n, p.ld[i], j.k);
+    if (a < align) align = a;
+  }
+  // Warps of a CTA: 16 where there are fewer CTAs than two an SM, so that few rows still keep the
+  // memory busy; no more than there are steps of k.
+  const int64_t ctas = (j.n + 7) / (j.gated ? 8 : 16), steps = (j.k + kStep - 1) / kStep;
+  p.warps = ctas < 2 * (int64_t)sms ? 16 : 8;
+  while (p.warps > 1 && p.warps > steps) p.warps /= 2;
+  if (j.e.type == COLL_BF16)
+    return j.gated ? launch<true, COLL_BF16>(p, align, s) : launch<false, COLL_BF16>(p, align, s);
+  return j.gated ? launch<true, COLL_F16>(p, align, s) : launch<false, COLL_F16>(p, align, s);
+}
+
+}  // namespace coll

@@ -39,4 +39,38 @@ int tc_encode(CUtensorMap *map, const TcOperand &o, int64_t type, uint32_t rows)
 int tc_plan(TcParams &p, const DenseJob &j, const TcOperand *a, const TcOperand *b, uint32_t sms);
 cudaError_t tc_run(const TcParams &p, bool gated, uint32_t sms, cudaStream_t s);
 
+
+// Few rows (dense_skinny.cu): the weights are the 128-row operand, the m tokens its columns.
+constexpr int64_t kSkinnyMost = 128;
+
+struct SkinnyParams {
+  CUtensorMap w[2], x;
+  DenseEpi e;
+  int64_t m, n;
+  int32_t *status;
+  int32_t rows, cols;          // output features of a CTA; tokens, rounded up to 16
+  int32_t w_chunks, x_chunks;  // 64-row chunks of them
+  int32_t kblocks, stages, w_mn, x_mn;
+  uint32_t tiles, split;       // feature tiles; shares of k (the CTAs of a cluster)
+  uint32_t w_bytes, stage_bytes, smem, idesc, tmem_cols;
+};
+
+int skinny_plan(SkinnyParams &p, const DenseJob &j, const TcOperand *w, const TcOperand &x,
+                uint32_t sms);
+cudaError_t skinny_run(const SkinnyParams &p, bool gated, cudaStream_t s);
+
+
+// One to a few tokens (dense_gemv.cu): A and B with unit stride along k, any row strides.
+constexpr int64_t kGemvMost = 16;
+
+struct GemvParams {
+  const void *w[2], *x;
+  int64_t ld[2], x_ld;
+  DenseEpi e;
+  int64_t m, n, k;
+  uint32_t warps;
+};
+
+cudaError_t gemv_run(const DenseJob &j, uint32_t sms, cudaStream_t s);
+
 }  // namespace coll

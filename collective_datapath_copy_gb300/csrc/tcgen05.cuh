@@ -144,29 +144,31 @@ __host__ __device__ inline uint32_t mma_desc(bool bf16, bool a_mn, bool b_mn, ui
          ((b_mn ? 1u : 0u) << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
 
+// Allocate `cols` columns (a power of two from 32) and give up the right to allocate more, which
+// another CTA of this SM would wait for otherwise. A whole warp calls these.
 template <int CG>
 __device__ __forceinline__ void tmem_alloc(uint32_t *saddr, uint32_t cols) {
-  if (CG == 2)
+  if (CG == 2) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(saddr)),
                  "r"(cols)
                  : "memory");
-  else
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  } else {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_u32(saddr)),
                  "r"(cols)
                  : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
 }
 
 template <int CG>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t cols) {
-  if (CG == 2) {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  if (CG == 2)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-  } else {
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  else
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols));
-  }
 }
 
 // D (+)= A B^T over 16 of k, with each descriptor given as two words. One thread issues it.
