@@ -190,10 +190,10 @@ cudaError_t gemv_run(const DenseJob &j, uint32_t sms, cudaStream_t s) {
     const int a = row_align(p.w[i], j.n, p.ld[i], j.k);
     if (a < align) align = a;
   }
-  // Warps of a CTA: 16 where there are fewer CTAs than two an SM, so that few rows still keep the
-  // memory busy; no more than there are steps of k.
-  const int64_t ctas = (j.n + 7) / (j.gated ? 8 : 16), steps = (j.k + kStep - 1) / kStep;
-  p.warps = ctas < 2 * (int64_t)sms ? 16 : 8;
+  // Warps of a CTA: 16, one CTA an SM, where there are no more CTAs than SMs, else 8 and two CTAs
+  // an SM (128 registers a thread); no more than there are steps of k.
+  const int64_t ctas = (j.n + (j.gated ? 7 : 15)) / (j.gated ? 8 : 16), steps = (j.k + kStep - 1) / kStep;
+  p.warps = ctas <= (int64_t)sms ? 16 : 8;
   while (p.warps > 1 && p.warps > steps) p.warps /= 2;
   if (j.e.type == COLL_BF16)
     return j.gated ? launch<true, COLL_BF16>(p, align, s) : launch<false, COLL_BF16>(p, align, s);

@@ -40,6 +40,7 @@ _LINEAR_BWD = struct.Struct("28q")
 _GATED = struct.Struct("26q")
 _GATED_BWD = struct.Struct("36q")
 _NONE = (0, 0, 0)
+_raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream, 2 us cheaper
 
 
 def _weight(name, w):
@@ -110,7 +111,7 @@ class _Dense:
 
     @staticmethod
     def _launch(fn, size_fn, pack, fields, status, device, where):
-        stream = torch.cuda.current_stream(device).cuda_stream
+        stream = _raw_stream(device.index)  # the current stream's handle
         code = fn(pack(*fields, 0, 0, status), stream)
         if code == _EWORKSPACE:
             need = size_fn(pack(*fields, 0, 0, status))
