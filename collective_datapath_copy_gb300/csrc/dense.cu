@@ -128,20 +128,21 @@ bool gated_act(int64_t a) { return a >= COLL_ACT_RELU && a <= COLL_ACT_SIGMOID; 
 DenseMat mat(const coll_mat_t &m) { return DenseMat{m.ptr, m.rs, m.cs}; }
 DenseMat turned(const coll_mat_t &m) { return DenseMat{m.ptr, m.cs, m.rs}; }
 
-bool sectors(const void *p, int64_t rs, int es) {
-  return !p || (((uintptr_t)p & 31u) == 0 && (rs * es) % 32 == 0);
+// Bits of the addresses of a matrix's rows (all rows start on 16 bytes if no bit below 16 is set).
+uint64_t sectors(const void *p, int64_t rs, int es) {
+  return p ? (uintptr_t)p | (uint64_t)(rs * es) : 0;
 }
 
-// Accesses of 32 bytes at columns that are multiples of 32 are aligned in every array.
+// The boundary on which rows start in every array of the epilogue, if all have unit stride.
 void set_vec(DenseJob &j) {
   const coll::DenseEpi &e = j.e;
   const int oe = esize(e.out_type);
-  bool v = true;
-  for (int b = 0; b < j.nbatch; ++b) v = v && sectors(e.out[b], e.out_rs[b], oe);
-  v = v && sectors(e.pre, e.pre_rs, 2) && sectors(e.gate, e.gate_rs, 2) && sectors(e.up, e.up_rs, 2);
-  v = v && sectors(e.bias, 0, 2) && (!e.bias || e.bias_stride == 1);
-  v = v && sectors(e.res, e.res_rs, oe) && (!e.res || e.res_cs == 1);
-  j.e.vec = v;
+  uint64_t v = 0;
+  for (int b = 0; b < j.nbatch; ++b) v |= sectors(e.out[b], e.out_rs[b], oe);
+  v |= sectors(e.pre, e.pre_rs, 2) | sectors(e.gate, e.gate_rs, 2) | sectors(e.up, e.up_rs, 2) |
+       sectors(e.bias, 0, 2) | sectors(e.res, e.res_rs, oe);
+  const bool unit = (!e.bias || e.bias_stride == 1) && (!e.res || e.res_cs == 1);
+  j.e.vec = !unit || v % 16 ? 0 : v % 32 ? 16 : 32;
 }
 
 DenseJob job(int64_t m, int64_t n, int64_t k, int64_t type, int32_t *status) {
@@ -178,21 +179,21 @@ bool in_place(const DenseMat &m, int64_t rows, int64_t k, TcOperand &o) {
   return false;
 }
 
-// Lay the operand out in the workspace along `mn` (0: k, 1: its rows).
-int lay_out(const DenseMat &m, int64_t rows, int64_t k, int mn, Ws &ws, bool dry, cudaStream_t s,
-            TcOperand &o) {
-  const DenseMat src = mn ? DenseMat{m.p, m.cs, m.rs} : m;
-  const int64_t lines = mn ? k : rows, len = mn ? rows : k, ld = round8(len);
-  void *dst = ws.take((uint64_t)lines * ld * 2);
-  o = TcOperand{dst, rows, k, ld, mn};
-  if (dry) return COLL_OK;
-  return coll::dense_pack(src, lines, len, dst, ld, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+// Put the operand on the list of those to lay out in the workspace, along `mn` (0: k, 1: rows).
+void lay_out(const DenseMat &m, int64_t rows, int64_t k, int mn, Ws &ws, coll::DensePack &todo,
+             TcOperand &o) {
+  const int i = todo.count++;
+  todo.src[i] = mn ? DenseMat{m.p, m.cs, m.rs} : m;
+  todo.rows[i] = mn ? k : rows;
+  todo.cols[i] = mn ? rows : k;
+  todo.ld[i] = round8(todo.cols[i]);
+  todo.dst[i] = static_cast<uint16_t *>(ws.take((uint64_t)todo.rows[i] * todo.ld[i] * 2));
+  o = TcOperand{todo.dst[i], rows, k, todo.ld[i], mn};
 }
 
-int operand(const DenseMat &m, int64_t rows, int64_t k, Ws &ws, bool dry, cudaStream_t s,
-            TcOperand &o) {
-  if (in_place(m, rows, k, o)) return COLL_OK;
-  return lay_out(m, rows, k, m.cs != 1 && m.rs == 1, ws, dry, s, o);
+void operand(const DenseMat &m, int64_t rows, int64_t k, Ws &ws, coll::DensePack &todo,
+             TcOperand &o) {
+  if (!in_place(m, rows, k, o)) lay_out(m, rows, k, m.cs != 1 && m.rs == 1, ws, todo, o);
 }
 
 int sm_count(uint32_t &sms) {
@@ -226,26 +227,16 @@ int product(DenseJob &j, Ws &ws, bool dry, cudaStream_t s) {
   }
   TcOperand a[2], b[2];
   const int na = j.nbatch == 2 || j.nseg == 2 ? 2 : 1, nb = j.gated || j.nseg == 2 ? 2 : 1;
-  for (int i = 0; i < na; ++i) {
-    const int c = operand(j.a[i], j.m, j.k, ws, dry, s, a[i]);
-    if (c) return c;
-  }
-  if (j.gated && in_place(j.b[0], j.n, j.k, b[0]) && in_place(j.b[1], j.n, j.k, b[1]) &&
-      b[0].mn != b[1].mn) {
-    // both halves of one instruction's B lie the same way
-    const int c = lay_out(j.b[1], j.n, j.k, b[0].mn, ws, dry, s, b[1]);
-    if (c) return c;
-  } else {
-    for (int i = 0; i < nb; ++i) {
-      int c = operand(j.b[i], j.n, j.k, ws, dry, s, b[i]);
-      if (!c && i == 1 && j.gated && b[1].mn != b[0].mn)
-        c = lay_out(j.b[i], j.n, j.k, b[0].mn, ws, dry, s, b[i]);
-      if (c) return c;
-    }
-  }
+  coll::DensePack todo = {};
+  for (int i = 0; i < na; ++i) operand(j.a[i], j.m, j.k, ws, todo, a[i]);
+  operand(j.b[0], j.n, j.k, ws, todo, b[0]);
+  // both halves of a gated product's instruction lie the same way
+  if (nb == 2 && (!in_place(j.b[1], j.n, j.k, b[1]) || (j.gated && b[1].mn != b[0].mn)))
+    lay_out(j.b[1], j.n, j.k, j.gated ? b[0].mn : j.b[1].cs != 1 && j.b[1].rs == 1, ws, todo, b[1]);
   if (dry) return COLL_OK;
   int c = sm_count(sms);
   if (c) return c;
+  if (todo.count && coll::dense_pack(todo, s) != cudaSuccess) return COLL_ECUDA;
   if (j.m <= coll::kSkinnyMost && j.nseg == 1 && j.nbatch == 1) {
     coll::SkinnyParams q;
     c = coll::skinny_plan(q, j, b, a[0], sms);

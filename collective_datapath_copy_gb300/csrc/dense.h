@@ -30,8 +30,8 @@ struct DenseEpi {
   int32_t type;      // COLL_BF16 / COLL_F16: bias, pre, gate, up
   int32_t out_type;  // type or COLL_F32: out, residual
   int32_t act;
-  int32_t vec;       // 1: every array above has unit column stride, and its rows start on
-                     // 32-byte boundaries
+  int32_t vec;       // 32 or 16: every array above has unit column stride and its rows start on
+                     // that many bytes; 0: not so
 };
 
 // out[b](m, n) = epilogue(sum over s of sum over k of A[b or s](m, k) B[s](n, k)).
@@ -60,12 +60,39 @@ int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n);
 cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s);
 
 
-// dst[i * ld + j] = src(i, j): an operand whose strides or base no tensor map takes, laid out in
-// rows of whole 16-byte runs.
-cudaError_t dense_pack(const DenseMat &src, int64_t rows, int64_t cols, void *dst, int64_t ld,
-                       cudaStream_t s);
+// dst[i * ld + j] = src(i, j): operands whose strides or base no tensor map takes, laid out in
+// rows of whole 16-byte runs, all of a product's in one launch.
+struct DensePack {
+  DenseMat src[4];
+  int64_t rows[4], cols[4], ld[4];
+  uint16_t *dst[4];
+  int count;
+};
+cudaError_t dense_pack(const DensePack &p, cudaStream_t s);
 
 // The job's epilogue over accumulators of zero (nothing to sum over).
 cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s);
+
+// Launch a kernel that may be set up while its predecessor in the stream still runs; every kernel
+// here waits for it (griddep_wait) before it touches memory.
+template <typename... P, typename... A>
+cudaError_t dense_launch(void (*kernel)(P...), dim3 grid, unsigned threads, uint32_t smem,
+                         unsigned cluster, cudaStream_t s, A &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<A &&>(args)...);
+}
 
 }  // namespace coll

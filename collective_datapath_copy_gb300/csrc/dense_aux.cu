@@ -9,6 +9,7 @@
 // order in a second launch, so the result does not depend on timing.
 #include "dense.h"
 #include "dense_epi.cuh"
+#include "tma.cuh"
 
 namespace coll {
 namespace {
@@ -49,6 +50,8 @@ __device__ __forceinline__ void store8(void *base, int64_t off, int type, const 
 template <bool GATED, int ACT, int TYPE, bool VEC>
 __global__ void __launch_bounds__(256, VEC ? 4 : 2) act_bwd_kernel(const DenseActBwd a,
                                                          int64_t rows_per_block) {
+  griddep_launch();
+  griddep_wait();
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * COLS + lane * 8;
   const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
@@ -113,19 +116,20 @@ bool runs16(const DenseMat &m) {
 }
 
 template <bool GATED, int ACT>
-void launch_act_bwd(const DenseActBwd &a, dim3 grid, int64_t per, cudaStream_t s) {
+cudaError_t launch_act_bwd(const DenseActBwd &a, dim3 grid, int64_t per, cudaStream_t s) {
   const bool vec = a.n % 8 == 0 && runs16(a.dy) && runs16(a.pre) && runs16(a.up);
-  if (a.type == COLL_BF16) {
-    if (vec) act_bwd_kernel<GATED, ACT, COLL_BF16, true><<<grid, 256, 0, s>>>(a, per);
-    else act_bwd_kernel<GATED, ACT, COLL_BF16, false><<<grid, 256, 0, s>>>(a, per);
-  } else {
-    if (vec) act_bwd_kernel<GATED, ACT, COLL_F16, true><<<grid, 256, 0, s>>>(a, per);
-    else act_bwd_kernel<GATED, ACT, COLL_F16, false><<<grid, 256, 0, s>>>(a, per);
-  }
+  auto kernel = a.type == COLL_BF16
+                    ? (vec ? act_bwd_kernel<GATED, ACT, COLL_BF16, true>
+                           : act_bwd_kernel<GATED, ACT, COLL_BF16, false>)
+                    : (vec ? act_bwd_kernel<GATED, ACT, COLL_F16, true>
+                           : act_bwd_kernel<GATED, ACT, COLL_F16, false>);
+  return dense_launch(kernel, grid, 256, 0, 1, s, a, per);
 }
 
 __global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t blocks, int64_t n,
                                                    void *db, int type) {
+  griddep_launch();
+  griddep_wait();
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c >= n) return;
   float s = 0.0f;
@@ -135,9 +139,13 @@ __global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t bl
 
 // A thread moves eight neighbouring elements: plain 2-byte loads (the rows start anywhere), one
 // 16-byte store.
-__global__ void __launch_bounds__(256) pack_kernel(const DenseMat src, int64_t rows, int64_t cols,
-                                                   uint16_t *dst, int64_t ld) {
-  const int64_t runs = ld / 8, total = rows * runs;
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ DensePack a) {
+  griddep_launch();
+  griddep_wait();
+  const int o = blockIdx.y;
+  const DenseMat src = a.src[o];
+  const int64_t cols = a.cols[o], ld = a.ld[o], runs = ld / 8, total = a.rows[o] * runs;
+  uint16_t *const dst = a.dst[o];
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / runs, c = (i - r * runs) * 8;
@@ -152,6 +160,8 @@ __global__ void __launch_bounds__(256) pack_kernel(const DenseMat src, int64_t r
 
 template <bool GATED>
 __global__ void __launch_bounds__(256) empty_sum_kernel(const DenseJob j) {
+  griddep_launch();
+  griddep_wait();
   const int64_t total = j.m * j.n;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
@@ -167,18 +177,19 @@ unsigned grid_for(int64_t threads) {
 
 }  // namespace
 
-cudaError_t dense_pack(const DenseMat &src, int64_t rows, int64_t cols, void *dst, int64_t ld,
-                       cudaStream_t s) {
-  pack_kernel<<<grid_for(rows * (ld / 8)), 256, 0, s>>>(src, rows, cols,
-                                                        static_cast<uint16_t *>(dst), ld);
-  return cudaGetLastError();
+cudaError_t dense_pack(const DensePack &p, cudaStream_t s) {
+  int64_t most = 0;
+  for (int i = 0; i < p.count; ++i) {
+    const int64_t runs = p.rows[i] * (p.ld[i] / 8);
+    if (runs > most) most = runs;
+  }
+  return dense_launch(pack_kernel, dim3(grid_for(most), (unsigned)p.count), 256, 0, 1, s, p);
 }
 
 cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s) {
   const dim3 grid(grid_for(j.m * j.n), (unsigned)j.nbatch);
-  if (j.gated) empty_sum_kernel<true><<<grid, 256, 0, s>>>(j);
-  else empty_sum_kernel<false><<<grid, 256, 0, s>>>(j);
-  return cudaGetLastError();
+  return dense_launch(j.gated ? empty_sum_kernel<true> : empty_sum_kernel<false>, grid, 256, 0, 1,
+                      s, j);
 }
 
 // Row blocks: enough CTAs for two waves of eight a multiprocessor, 64 rows a block at least.
@@ -197,24 +208,25 @@ cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s) {
   const int64_t blocks = dense_act_bwd_row_blocks(a.m, a.n);
   const int64_t per = (a.m + blocks - 1) / blocks;
   const dim3 grid((unsigned)((a.n + COLS - 1) / COLS), (unsigned)blocks);
+  cudaError_t err;
   switch (a.act) {
-    case COLL_ACT_NONE: launch_act_bwd<false, COLL_ACT_NONE>(a, grid, per, s); break;
-#define COLL_ACT_CASE(act)                                     \
-  case act:                                                    \
-    if (a.gated) launch_act_bwd<true, act>(a, grid, per, s);   \
-    else launch_act_bwd<false, act>(a, grid, per, s);          \
+    case COLL_ACT_NONE: err = launch_act_bwd<false, COLL_ACT_NONE>(a, grid, per, s); break;
+#define COLL_ACT_CASE(act)                                         \
+  case act:                                                        \
+    err = a.gated ? launch_act_bwd<true, act>(a, grid, per, s)     \
+                  : launch_act_bwd<false, act>(a, grid, per, s);   \
     break;
     COLL_ACT_CASE(COLL_ACT_RELU)
     COLL_ACT_CASE(COLL_ACT_GELU)
     COLL_ACT_CASE(COLL_ACT_GELU_TANH)
     COLL_ACT_CASE(COLL_ACT_SILU)
 #undef COLL_ACT_CASE
-    default: launch_act_bwd<true, COLL_ACT_SIGMOID>(a, grid, per, s);
+    default: err = launch_act_bwd<true, COLL_ACT_SIGMOID>(a, grid, per, s);
   }
-  if (!a.gated && a.db && blocks > 1)
-    join_kernel<<<(unsigned)((a.n + 255) / 256), 256, 0, s>>>(a.part, blocks, a.n, a.db,
-                                                              a.db_type);
-  return cudaGetLastError();
+  if (err == cudaSuccess && !a.gated && a.db && blocks > 1)
+    err = dense_launch(join_kernel, dim3((unsigned)((a.n + 255) / 256)), 256, 0, 1, s, a.part,
+                       blocks, a.n, a.db, a.db_type);
+  return err;
 }
 
 }  // namespace coll

@@ -153,6 +153,35 @@ __device__ __forceinline__ void st_32b(void *p, const uint32_t *r) {
                : "memory");
 }
 
+// A lane's 32 bytes of a row that starts on 32 bytes (`wide`) or 16.
+__device__ __forceinline__ void ld_sector(const void *p, uint32_t *r, bool wide) {
+  if (wide) {
+    ld_32b(p, r);
+  } else {
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "l"(p)
+                 : "memory");
+    asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "l"(static_cast<const char *>(p) + 16)
+                 : "memory");
+  }
+}
+
+__device__ __forceinline__ void st_sector(void *p, const uint32_t *r, bool wide) {
+  if (wide) {
+    st_32b(p, r);
+  } else {
+    asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(p), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3])
+                 : "memory");
+    asm volatile("st.global.v4.b32 [%0], {%1,%2,%3,%4};" ::"l"(static_cast<char *>(p) + 16),
+                 "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+  }
+}
+
 // v[0..32) += 32 neighbouring 16-bit elements held in r[16]
 __device__ __forceinline__ void add_halves(float (&v)[32], const uint32_t *r, int type) {
   if (type == COLL_BF16) {
@@ -172,14 +201,15 @@ __device__ __forceinline__ void add_halves(float (&v)[32], const uint32_t *r, in
   }
 }
 
-__device__ __forceinline__ void ld_halves(const void *p, int64_t i, uint32_t *r) {
+__device__ __forceinline__ void ld_halves(const void *p, int64_t i, uint32_t *r, bool wide) {
   const uint16_t *q = static_cast<const uint16_t *>(p) + i;
-  ld_32b(q, r);
-  ld_32b(q + 16, r + 8);
+  ld_sector(q, r, wide);
+  ld_sector(q + 16, r + 8, wide);
 }
 
-// 32 neighbouring elements from element i on, a multiple of 32 bytes
-__device__ __forceinline__ void st_run32(void *p, int64_t i, int type, const float (&v)[32]) {
+// 32 neighbouring elements from element i on
+__device__ __forceinline__ void st_run32(void *p, int64_t i, int type, bool wide,
+                                         const float (&v)[32]) {
   if (type == COLL_F32) {
     float *o = static_cast<float *>(p) + i;
 #pragma unroll
@@ -187,7 +217,7 @@ __device__ __forceinline__ void st_run32(void *p, int64_t i, int type, const flo
       uint32_t r[8];
 #pragma unroll
       for (int x = 0; x < 8; ++x) r[x] = __float_as_uint(v[8 * q + x]);
-      st_32b(o + 8 * q, r);
+      st_sector(o + 8 * q, r, wide);
     }
     return;
   }
@@ -200,8 +230,8 @@ __device__ __forceinline__ void st_run32(void *p, int64_t i, int type, const flo
     for (int q = 0; q < 16; ++q) r[q] = f2h2(v[2 * q], v[2 * q + 1], COLL_F16);
   }
   uint16_t *o = static_cast<uint16_t *>(p) + i;
-  st_32b(o, r);
-  st_32b(o + 16, r + 8);
+  st_sector(o, r, wide);
+  st_sector(o + 16, r + 8, wide);
 }
 
 // ---- rows that start anywhere: 32 x 32 blocks through shared memory, so that neighbouring lanes

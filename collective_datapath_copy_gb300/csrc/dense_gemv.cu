@@ -17,6 +17,7 @@
 #include "dense.h"
 #include "dense_epi.cuh"
 #include "dense_tc.h"
+#include "tma.cuh"
 
 namespace coll {
 namespace {
@@ -82,7 +83,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 
 // NT: columns of eight tokens.
 template <bool GATED, int TYPE, int NT, int ALIGN>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1) gemv_kernel(const GemvParams p) {
+__global__ void __launch_bounds__(kMaxWarps * 32, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
+  griddep_launch();
   constexpr int FEAT = GATED ? 8 : 16;   // outputs of a CTA
   constexpr int AHEAD = NT == 1 ? 4 : 2;
   __shared__ float part[kMaxWarps][8 * NT][16];
@@ -105,6 +107,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) gemv_kernel(const GemvParam
     xt[c] = static_cast<const uint16_t *>(p.x) + (lx[c] ? tok : 0) * p.x_ld + 16 * t;
   }
   float acc[NT][4] = {};
+  griddep_wait();
   const int steps = (len + kStep - 1) / kStep;
   for (int s = warp; s < steps; s += AHEAD * warps) {
     uint32_t a[AHEAD][8], b[AHEAD][8], x[AHEAD][NT][8];
@@ -153,13 +156,11 @@ template <bool GATED, int TYPE, int NT>
 cudaError_t launch(const GemvParams &p, int align, cudaStream_t s) {
   const unsigned grid = (unsigned)((p.n + (GATED ? 8 : 16) - 1) / (GATED ? 8 : 16));
   const unsigned threads = p.warps * 32u;
-  switch (align) {
-    case 32: gemv_kernel<GATED, TYPE, NT, 32><<<grid, threads, 0, s>>>(p); break;
-    case 16: gemv_kernel<GATED, TYPE, NT, 16><<<grid, threads, 0, s>>>(p); break;
-    case 4: gemv_kernel<GATED, TYPE, NT, 4><<<grid, threads, 0, s>>>(p); break;
-    default: gemv_kernel<GATED, TYPE, NT, 2><<<grid, threads, 0, s>>>(p);
-  }
-  return cudaGetLastError();
+  auto kernel = align == 32   ? gemv_kernel<GATED, TYPE, NT, 32>
+                : align == 16 ? gemv_kernel<GATED, TYPE, NT, 16>
+                : align == 4  ? gemv_kernel<GATED, TYPE, NT, 4>
+                              : gemv_kernel<GATED, TYPE, NT, 2>;
+  return dense_launch(kernel, dim3(grid), threads, 0, 1, s, p);
 }
 
 template <bool GATED, int TYPE>

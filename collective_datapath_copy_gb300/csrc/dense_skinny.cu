@@ -127,6 +127,8 @@ __global__ void __launch_bounds__(kThreads, 2) skinny_kernel(const __grid_consta
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  griddep_launch();
+  griddep_wait();
 
   if (warp == 0) {
     uint32_t s = 0, phase = 0;
@@ -283,19 +285,7 @@ cudaError_t launch(const SkinnyParams &p, cudaStream_t s) {
   static const cudaError_t ready = cudaFuncSetAttribute(
       skinny_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
   if (ready != cudaSuccess) return ready;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.tiles * p.split);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = p.smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = p.split;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, skinny_kernel<GATED>, p);
+  return dense_launch(skinny_kernel<GATED>, dim3(p.tiles * p.split), kThreads, p.smem, p.split, s, p);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -73,7 +73,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   uint32_t *const staged = reinterpret_cast<uint32_t *>(raw + (ring - smem_u32(raw)) +
                                                         (size_t)p.stages * p.stage_bytes);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // the same for all lanes, and known to be
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0u;
   const uint32_t clusters = gridDim.x / CG, cluster = blockIdx.x / CG;
@@ -96,12 +97,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  griddep_launch();
+  griddep_wait();
 
   const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
   const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
 
   if (warp == 0) {
-    const bool one = elect_one();
     const uint32_t arrive0 = map_rank(full0, 0);
     // bytes a stage receives, boxes past the edges counted whole
     const uint32_t kr = p.b_rows * 128, mr = p.b_chunks * kChunk;
@@ -114,10 +116,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
       const uint32_t bytes = CG * (kABytes + (bmn ? mr : kr));
       const int32_t end = p.kblocks * kTileK;
       for (int32_t k = 0; k < end; k += kTileK) {
-        if (!wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status)) return false;
-        if (one) {
-          const uint32_t da = ring + s * stage_bytes, db = da + kABytes, bar = arrive0 + 8 * s;
+        ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
+        if (elect_one() && ok) {
+          const uint32_t bar = arrive0 + 8 * s;
           if (leader) bar_expect(full0 + 8 * s, bytes);
+          const uint32_t da = ring + s * stage_bytes, db = da + kABytes;
           if (amn) {
             tma_box_pair(da, ma, m, k, bar);
             tma_box_pair(da + kChunk, ma, m + 64, k, bar);
@@ -137,26 +140,28 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           phase ^= 1u;
         }
       }
-      return true;
     };
     using Yes = std::integral_constant<bool, true>;
     using No = std::integral_constant<bool, false>;
-    for (uint32_t t = cluster; ok && t < p.tiles; t += clusters) {
+    for (uint32_t t = cluster; t < p.tiles; t += clusters) {
       const Tile tl = tile_at(p, t);
       const int32_t m = (int32_t)tl.m0 + (int32_t)rank * 128;
       const int32_t n = (int32_t)tl.n0 + (GATED ? 0 : (int32_t)rank * p.b_rows);
-      for (int seg = 0; ok && seg < p.nseg; ++seg) {
+      for (int seg = 0; seg < p.nseg; ++seg) {
         const int ia = p.nbatch == 2 ? tl.batch : seg, ib = GATED ? (int)rank : seg;
         const CUtensorMap *ma = &p.a[ia], *mb = &p.b[ib];
-        if (p.a_mn[ia])
-          ok = p.b_mn[ib] ? segment(Yes{}, Yes{}, ma, mb, m, n) : segment(Yes{}, No{}, ma, mb, m, n);
-        else
-          ok = p.b_mn[ib] ? segment(No{}, Yes{}, ma, mb, m, n) : segment(No{}, No{}, ma, mb, m, n);
+        if (p.a_mn[ia]) {
+          if (p.b_mn[ib]) segment(Yes{}, Yes{}, ma, mb, m, n);
+          else segment(Yes{}, No{}, ma, mb, m, n);
+        } else {
+          if (p.b_mn[ib]) segment(No{}, Yes{}, ma, mb, m, n);
+          else segment(No{}, No{}, ma, mb, m, n);
+        }
       }
     }
     // every slot's last products are done before this CTA may go away
-    for (uint32_t i = 0; ok && i < stages; ++i) {
-      ok = wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
+    for (uint32_t i = 0; i < stages; ++i) {
+      ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
       if (++s == stages) {
         s = 0;
         phase ^= 1u;
@@ -164,18 +169,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     }
   } else if (warp == 1) {
     if (leader) {
-      const bool one = elect_one();
       const uint32_t hi = desc_hi(1024), step = stage_bytes >> 4;
       const uint32_t acc_full0 = smem_u32(&sh.acc_full[0]), acc_empty0 = smem_u32(&sh.acc_empty[0]);
       uint32_t s = 0, phase = 0, it = 0, at = 0;  // at: 16-byte units from the ring's start
       bool ok = true;
-      for (uint32_t t = cluster; ok && t < p.tiles; t += clusters, ++it) {
+      for (uint32_t t = cluster; t < p.tiles; t += clusters, ++it) {
         const uint32_t buf = it & 1u, d = tmem + buf * 256u;
-        if (!wait_bar(&sh.abort, acc_empty0 + 8 * buf, ((it >> 1) & 1u) ^ 1u, p.status)) break;
+        ok = ok && wait_bar(&sh.abort, acc_empty0 + 8 * buf, ((it >> 1) & 1u) ^ 1u, p.status);
         tc_fence_after();
         const int batch = p.nbatch == 2 ? tile_at(p, t).batch : 0;
         uint32_t add = 0;
-        for (int seg = 0; ok && seg < p.nseg; ++seg) {
+        for (int seg = 0; seg < p.nseg; ++seg) {
           const int ia = p.nbatch == 2 ? batch : seg;
           const bool amn = p.a_mn[ia], bmn = p.b_mn[seg];
           // an MN-major operand's next 16 of k are 16 rows on, a K-major one's 32 bytes
@@ -184,12 +188,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           const uint32_t b0 = desc_lo(ring + kABytes, bmn ? kChunk : 16u);
           const uint32_t idesc = p.idesc | ((uint32_t)amn << 15) | ((uint32_t)bmn << 16);
           for (int kb = p.kblocks; kb > 0; --kb) {
-            if (!wait_bar(&sh.abort, full0 + 8 * s, phase, p.status)) {
-              ok = false;
-              break;
-            }
+            ok = ok && wait_bar(&sh.abort, full0 + 8 * s, phase, p.status);
             tc_fence_after();
-            if (one) {
+            if (elect_one() && ok) {
               const uint32_t a = a0 + at, b = b0 + at;
               mma_f16<CG>(d, a, hi, b, hi, idesc, add);
               mma_f16<CG>(d, a + as, hi, b + bs, hi, idesc, 1);
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
             }
           }
         }
-        if (ok && one) mma_commit<CG>(acc_full0 + 8 * buf, 3);
+        if (elect_one() && ok) mma_commit<CG>(acc_full0 + 8 * buf, 3);
         __syncwarp();
       }
     }
@@ -216,6 +217,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     uint32_t *const st = staged + (warp - 4) * 32 * kPitch;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
     const DenseEpi &e = p.e;
+    const bool wide = e.vec == 32;
     const bool pre_res = !GATED && e.vec && e.res && e.out_type != COLL_F32;
     uint32_t it = 0;
     for (uint32_t t = cluster; t < p.tiles; t += clusters, ++it) {
@@ -226,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
       const int cols = (int)min((int64_t)p.tile_cols, p.n - tl.n0);
       uint32_t r[16];  // the residual of the next 32 columns, asked for ahead
       auto ask = [&](int c0) {
-        if (pre_res && live && c0 + 32 <= cols) ld_halves(e.res, row * e.res_rs + tl.n0 + c0, r);
+        if (pre_res && live && c0 + 32 <= cols) ld_halves(e.res, row * e.res_rs + tl.n0 + c0, r, wide);
       };
       ask(part * 32);
       if (!__all_sync(~0u, wait_bar(&sh.abort, smem_u32(&sh.acc_full[buf]), (it >> 1) & 1u, p.status))) break;
@@ -241,7 +243,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         const int rows = (int)max((int64_t)0, min((int64_t)32, p.m - row0)), left = min(32, cols - c0);
         auto store = [&](void *base, int64_t rs, int type, const float (&v)[32]) {
           if (vec) {
-            if (live) st_run32(base, row * rs + col, type, v);
+            if (live) st_run32(base, row * rs + col, type, wide, v);
           } else {
             const int64_t at0 = row0 * rs + col;
             staged_store(st, static_cast<char *>(base) + at0 * (type == COLL_F32 ? 4 : 2), rs, type,
@@ -260,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           if (e.bias) {
             if (vec) {
               uint32_t b[16];
-              ld_halves(e.bias, col, b);
+              ld_halves(e.bias, col, b, wide);
               add_halves(g, b, e.type);
             } else {
               add_bias(e, col, left, g);
@@ -281,7 +283,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
               for (int i = 0; i < 32; i += 8) {
                 uint32_t x[8];
-                ld_32b(q + i, x);
+                ld_sector(q + i, x, wide);
 #pragma unroll
                 for (int w = 0; w < 8; ++w) g[i + w] += __uint_as_float(x[w]);
               }
@@ -315,19 +317,7 @@ cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStre
   static const cudaError_t ready = cudaFuncSetAttribute(
       tc_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
   if (ready != cudaSuccess) return ready;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(clusters * CG);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = CG;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tc_kernel<GATED>, p);
+  return dense_launch(tc_kernel<GATED>, dim3(clusters * CG), kThreads, smem, CG, s, p);
 }
 
 uint32_t ceil_div(int64_t a, int64_t b) { return (uint32_t)((a + b - 1) / b); }
@@ -365,15 +355,14 @@ int tc_plan(TcParams &p, const DenseJob &j, const TcOperand *a, const TcOperand 
   p.tile_rows = 128 * CG;
   p.tiles_m = ceil_div(j.m, p.tile_rows);
   // Columns of the accumulator: those with the least rounds of tiles times the time of a tile's k
-  // block. Measured at 4096 x 4096 x 8192: 349 ns for 256 columns, 199 for 128 and 167 for 64,
-  // where issuing a block's copies and products is the limit.
+  // block, 62 ns and 1.08 a column (measured at 4096 x 4096 x 8192: 144 ns for 64 columns, 186 for
+  // 128, 264 for 192, 339 for 256).
   int best = 256;
   int64_t cost = INT64_MAX;
   for (int bn = 256; bn >= 64; bn -= j.gated ? 64 : 32) {
     const int64_t cols = j.gated ? bn / 2 : bn;
     const int64_t tiles = (int64_t)p.tiles_m * ceil_div(j.n, cols) * j.nbatch;
-    const int64_t block = 58 + bn * 73 / 64, c = (tiles + clusters - 1) / clusters *
-                                                (block > 167 ? block : 167);
+    const int64_t c = (tiles + clusters - 1) / clusters * (62 + bn * 69 / 64);
     if (c < cost) {
       cost = c;
       best = bn;

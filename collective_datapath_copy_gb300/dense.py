@@ -40,6 +40,17 @@ _LINEAR_BWD = struct.Struct("28q")
 _GATED = struct.Struct("26q")
 _GATED_BWD = struct.Struct("36q")
 _NONE = (0, 0, 0)
+_entries = {}
+
+
+def _entry(name):
+    e = _entries.get(name)
+    if e is None:
+        h = lib()
+        e = _entries[name] = (getattr(h, name), getattr(h, name + "_workspace"))
+    return e
+
+
 _raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream, 2 us cheaper
 
 
@@ -100,8 +111,9 @@ def _on(stream, tensors):
 
 
 class _Dense:
-    def _init_status(self, device):
+    def _start(self, device):
         self._status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._need = {}
 
     def status(self) -> int:
         """COLL_OK, or COLL_ETIMEDOUT if a bounded device wait of an earlier call expired (its
@@ -109,16 +121,25 @@ class _Dense:
         stream."""
         return int(self._status.item())
 
-    @staticmethod
-    def _launch(fn, size_fn, pack, fields, status, device, where):
+    def _launch(self, where, pack, fields):
+        """Call an entry point on the current stream, with a workspace if it asks for one. The
+        size it last asked for is offered first, so that a loop over one size makes one call."""
+        fn, size = _entry(where)
+        device, status = self._status.device, self._status.data_ptr()
         stream = _raw_stream(device.index)  # the current stream's handle
-        code = fn(pack(*fields, 0, 0, status), stream)
-        if code == _EWORKSPACE:
-            need = size_fn(pack(*fields, 0, 0, status))
+        need = self._need.get(where, 0)
+        while True:
+            if need:
+                ws = torch.empty(need, dtype=torch.uint8, device=device)
+                code = fn(pack(*fields, ws.data_ptr(), need, status), stream)
+            else:
+                code = fn(pack(*fields, 0, 0, status), stream)
+            if code != _EWORKSPACE:
+                break
+            need = int(size(pack(*fields, 0, 0, status)))
             if need < 0:
-                check(int(need), where)
-            ws = torch.empty(need, dtype=torch.uint8, device=device)
-            code = fn(pack(*fields, ws.data_ptr(), need, status), stream)
+                check(need, where)
+            self._need[where] = need
         if code:
             check(code, where)
 
@@ -138,7 +159,7 @@ class Linear(_Dense):
                              f"{weight.device}")
         self.bias = bias
         self.act = act
-        self._init_status(weight.device)
+        self._start(weight.device)
 
     def forward(self, x, residual=None, out=None, out_dtype=None, save=False, pre=None,
                 stream=None):
@@ -177,11 +198,10 @@ class Linear(_Dense):
             if residual.shape != out.shape:
                 residual = residual.expand(out.shape)
             r2 = _rows(residual, n, ot, dev, "residual")
-        self._launch(lib().coll_linear, lib().coll_linear_workspace, _LINEAR.pack,
+        self._launch("coll_linear", _LINEAR.pack,
                      (m, n, k, _TYPE[dt], _TYPE[ot], ACT[self.act], *_mat(x2), *_mat(w),
                       *_mat(r2), *_mat(p2), *_mat(y2), 0 if b is None else b.data_ptr(),
-                      0 if b is None else b.stride(0)), self._status.data_ptr(), dev,
-                     "coll_linear")
+                      0 if b is None else b.stride(0)))
         return (out, pre) if save or p2 is not None else out
 
     __call__ = forward
@@ -230,12 +250,10 @@ class Linear(_Dense):
             db2 = _dest(db, 1, n, (gt,), dev, "db")
             if db.dim() != 1 or (n > 1 and db.stride(0) != 1):
                 raise ValueError("db must be a contiguous vector")
-        self._launch(lib().coll_linear_backward, lib().coll_linear_backward_workspace,
-                     _LINEAR_BWD.pack,
+        self._launch("coll_linear_backward", _LINEAR_BWD.pack,
                      (m, n, k, _TYPE[dt], _TYPE[gt], ACT[self.act], *_mat(dy2), *_mat(p2),
                       *_mat(x2), *_mat(w), *_mat(dx2), *_mat(dw2),
-                      0 if db2 is None else db2.data_ptr()), self._status.data_ptr(), dev,
-                     "coll_linear_backward")
+                      0 if db2 is None else db2.data_ptr()))
         return (dx if need_dx else None, dw if need_dw else None, db if need_db else None)
 
 
@@ -253,7 +271,7 @@ class GatedFFN(_Dense):
         if act not in GATED_ACTS:
             raise ValueError(f"act must be one of {GATED_ACTS}, not {act!r}")
         self.act = act
-        self._init_status(w_gate.device)
+        self._start(w_gate.device)
 
     def forward(self, x, out=None, save=False, gate=None, up=None, stream=None):
         """x [..., K] -> h [..., F]. With `save`, returns (h, gate, up): the two products, which
@@ -279,10 +297,9 @@ class GatedFFN(_Dense):
         if save or gate is not None or up is not None:
             gate, g2 = dest(gate, "gate")
             up, u2 = dest(up, "up")
-        self._launch(lib().coll_gated_ffn, lib().coll_gated_ffn_workspace, _GATED.pack,
+        self._launch("coll_gated_ffn", _GATED.pack,
                      (m, n, k, _TYPE[dt], ACT[self.act], *_mat(x2), *_mat(w), *_mat(self.w_up),
-                      *_mat(g2), *_mat(u2), *_mat(h2)), self._status.data_ptr(), dev,
-                     "coll_gated_ffn")
+                      *_mat(g2), *_mat(u2), *_mat(h2)))
         return out if g2 is None else (out, gate, up)
 
     __call__ = forward
@@ -323,11 +340,9 @@ class GatedFFN(_Dense):
             dw_up = torch.empty(n, k, dtype=gt, device=dev) if dw_up is None else dw_up
             dg2 = _dest(dw_gate, n, k, (gt,), dev, "dw_gate")
             du2 = _dest(dw_up, n, k, (gt,), dev, "dw_up")
-        self._launch(lib().coll_gated_ffn_backward, lib().coll_gated_ffn_backward_workspace,
-                     _GATED_BWD.pack,
+        self._launch("coll_gated_ffn_backward", _GATED_BWD.pack,
                      (m, n, k, _TYPE[dt], _TYPE[gt], ACT[self.act], *_mat(ins[0]),
                       *_mat(ins[1]), *_mat(ins[2]), *_mat(x2), *_mat(w), *_mat(self.w_up),
-                      *_mat(dx2), *_mat(dg2), *_mat(du2)), self._status.data_ptr(), dev,
-                     "coll_gated_ffn_backward")
+                      *_mat(dx2), *_mat(dg2), *_mat(du2)))
         return (dx if need_dx else None, dw_gate if need_dw else None,
                 dw_up if need_dw else None)
