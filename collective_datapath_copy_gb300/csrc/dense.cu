@@ -13,7 +13,7 @@ using coll::DenseJob;
 using coll::DenseMat;
 using coll::TcOperand;
 
-// Bump allocator over the caller's workspace. With base == nullptr it only counts.
+// Bump allocator over the caller's workspace, in steps of 256 bytes from a 128-byte boundary. With base == nullptr it only counts.
 struct Ws {
   char *base;
   uint64_t used;
@@ -25,6 +25,10 @@ struct Ws {
 };
 
 int64_t round8(int64_t v) { return (v + 7) & ~(int64_t)7; }
+
+// Lines of what the workspace holds start on 128 bytes: a tensor copy's 128-byte rows then lie in
+// one line each (512 x 1024 x 5462: 23.4 us with lines of 5464 elements, 15.8 with 5504).
+int64_t round64(int64_t v) { return (v + 63) & ~(int64_t)63; }
 
 bool is_half(int64_t t) { return t == COLL_BF16 || t == COLL_F16; }
 int esize(int64_t t) { return t == COLL_F32 ? 4 : 2; }
@@ -186,7 +190,7 @@ void lay_out(const DenseMat &m, int64_t rows, int64_t k, int mn, Ws &ws, coll::D
   todo.src[i] = mn ? DenseMat{m.p, m.cs, m.rs} : m;
   todo.rows[i] = mn ? k : rows;
   todo.cols[i] = mn ? rows : k;
-  todo.ld[i] = round8(todo.cols[i]);
+  todo.ld[i] = round64(todo.cols[i]);
   todo.dst[i] = static_cast<uint16_t *>(ws.take((uint64_t)todo.rows[i] * todo.ld[i] * 2));
   o = TcOperand{todo.dst[i], rows, k, todo.ld[i], mn};
 }
@@ -231,6 +235,7 @@ int product(DenseJob &j, Ws &ws, bool dry, cudaStream_t s) {
   for (int i = 0; i < na; ++i) operand(j.a[i], j.m, j.k, ws, todo, a[i]);
   operand(j.b[0], j.n, j.k, ws, todo, b[0]);
   // both halves of a gated product's instruction lie the same way
+  // and both batches' first operands always do (they are scratch)
   if (nb == 2 && (!in_place(j.b[1], j.n, j.k, b[1]) || (j.gated && b[1].mn != b[0].mn)))
     lay_out(j.b[1], j.n, j.k, j.gated ? b[0].mn : j.b[1].cs != 1 && j.b[1].rs == 1, ws, todo, b[1]);
   if (dry) return COLL_OK;
@@ -249,9 +254,9 @@ int product(DenseJob &j, Ws &ws, bool dry, cudaStream_t s) {
   return coll::tc_run(p, j.gated != 0, sms, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
 }
 
-// Scratch matrices: rows of whole 16-byte runs.
+// Scratch matrices.
 coll_mat_t scratch(Ws &ws, int64_t rows, int64_t cols) {
-  const int64_t ld = round8(cols);
+  const int64_t ld = round64(cols);
   return coll_mat_t{ws.take((uint64_t)rows * ld * 2), ld, 1};
 }
 
@@ -329,7 +334,7 @@ int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
   }
   if (a.db) {
     b.db = a.db;
-    const int64_t blocks = coll::dense_act_bwd_row_blocks(a.m, a.n);
+    const int64_t blocks = coll::dense_act_bwd_row_blocks(a.m, a.n, true);
     if (blocks > 1) b.part = static_cast<float *>(ws.take((uint64_t)blocks * a.n * 4));
   }
   if ((b.db || (dz.ptr != a.dy.ptr && a.m > 0)) && a.n > 0 && !dry)
@@ -456,7 +461,7 @@ int64_t workspace(const T *a) {
   if (c) return c;
   Ws ws = {};
   const int r = run(*a, ws, true, nullptr);
-  return r ? r : (int64_t)ws.used;
+  return r ? r : ws.used ? (int64_t)ws.used + 128 : 0;  // room to start on 128 bytes
 }
 
 template <typename T>
@@ -467,7 +472,7 @@ int call(const T *a, void *stream) {
   if (need > 0) {
     if (!a->workspace || ((uintptr_t)a->workspace & 15u) || a->workspace_bytes < (uint64_t)need)
       return COLL_EWORKSPACE;
-    ws.base = static_cast<char *>(a->workspace);
+    ws.base = reinterpret_cast<char *>(((uintptr_t)a->workspace + 127) & ~(uintptr_t)127);
   }
   return run(*a, ws, false, static_cast<cudaStream_t>(stream));
 }

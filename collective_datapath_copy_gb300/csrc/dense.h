@@ -56,7 +56,7 @@ struct DenseActBwd {
   float *part;           // column sums of each row block, [row_blocks][n]
   int32_t type, db_type, act, gated;
 };
-int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n);
+int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums);
 cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s);
 
 

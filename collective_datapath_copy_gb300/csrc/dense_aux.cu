@@ -192,11 +192,12 @@ cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s) {
                       s, j);
 }
 
-// Row blocks: enough CTAs for two waves of eight a multiprocessor, 64 rows a block at least.
-int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n) {
-  const int64_t cols = (n + COLS - 1) / COLS;
+// Row blocks: enough CTAs for two waves of eight a multiprocessor; one turn of the rows at least
+// (16), or four where column sums are left for each block.
+int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums) {
+  const int64_t cols = (n + COLS - 1) / COLS, least = sums ? 64 : 16;
   int64_t want = (2432 + cols - 1) / cols;
-  const int64_t most = (m + 63) / 64;
+  const int64_t most = (m + least - 1) / least;
   if (want > most) want = most;
   if (want < 1) want = 1;
   if (want > 65535) want = 65535;
@@ -205,7 +206,7 @@ int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n) {
 }
 
 cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s) {
-  const int64_t blocks = dense_act_bwd_row_blocks(a.m, a.n);
+  const int64_t blocks = dense_act_bwd_row_blocks(a.m, a.n, a.db != nullptr);
   const int64_t per = (a.m + blocks - 1) / blocks;
   const dim3 grid((unsigned)((a.n + COLS - 1) / COLS), (unsigned)blocks);
   cudaError_t err;

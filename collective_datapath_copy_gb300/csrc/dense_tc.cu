@@ -54,15 +54,41 @@ struct Tile {
   int64_t m0, n0;
 };
 
+// t / d and what remains. Up to 2^24 by a reciprocal that is off by one at most: a role of one
+// warp pays for every instruction of its chain.
+__device__ __forceinline__ uint32_t div_rem(uint32_t t, uint32_t d, uint32_t &rest) {
+  uint32_t q;
+  if (t < (1u << 24)) {
+    q = __float2uint_rz(__fdividef((float)t, (float)d));
+    int32_t r = (int32_t)(t - q * d);
+    if (r < 0) {
+      --q;
+      r += (int32_t)d;
+    } else if (r >= (int32_t)d) {
+      ++q;
+      r -= (int32_t)d;
+    }
+    rest = (uint32_t)r;
+  } else {
+    q = t / d;
+    rest = t - q * d;
+  }
+  return q;
+}
+
 __device__ __forceinline__ Tile tile_at(const TcParams &p, uint32_t t) {
   Tile r;
+  uint32_t in = t, row;
+  r.batch = 0;
   const uint32_t per = p.tiles_m * p.tiles_n;
-  r.batch = t / per;
-  t -= r.batch * per;
-  const uint32_t group = 8u * p.tiles_n, g = t / group, first = g * 8u;
-  const uint32_t rows = min(8u, p.tiles_m - first), in = t - g * group;
-  r.m0 = (int64_t)(first + in % rows) * p.tile_rows;
-  r.n0 = (int64_t)(in / rows) * p.tile_cols;
+  if (t >= per) {  // two batches at most
+    r.batch = 1;
+    in -= per;
+  }
+  const uint32_t first = div_rem(in, 8u * p.tiles_n, in) * 8u;
+  const uint32_t col = div_rem(in, min(8u, p.tiles_m - first), row);
+  r.m0 = (int64_t)(first + row) * p.tile_rows;
+  r.n0 = (int64_t)col * p.tile_cols;
   return r;
 }
 
@@ -148,13 +174,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
       const int32_t m = (int32_t)tl.m0 + (int32_t)rank * 128;
       const int32_t n = (int32_t)tl.n0 + (GATED ? 0 : (int32_t)rank * p.b_rows);
       for (int seg = 0; seg < p.nseg; ++seg) {
-        const int ia = p.nbatch == 2 ? tl.batch : seg, ib = GATED ? (int)rank : seg;
-        const CUtensorMap *ma = &p.a[ia], *mb = &p.b[ib];
-        if (p.a_mn[ia]) {
-          if (p.b_mn[ib]) segment(Yes{}, Yes{}, ma, mb, m, n);
+        const CUtensorMap *ma = &p.a[p.nbatch == 2 ? tl.batch : seg];
+        const CUtensorMap *mb = &p.b[GATED ? (int)rank : seg];
+        if (p.a_mn[seg]) {
+          if (p.b_mn[seg]) segment(Yes{}, Yes{}, ma, mb, m, n);
           else segment(Yes{}, No{}, ma, mb, m, n);
         } else {
-          if (p.b_mn[ib]) segment(No{}, Yes{}, ma, mb, m, n);
+          if (p.b_mn[seg]) segment(No{}, Yes{}, ma, mb, m, n);
           else segment(No{}, No{}, ma, mb, m, n);
         }
       }
@@ -177,11 +203,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         const uint32_t buf = it & 1u, d = tmem + buf * 256u;
         ok = ok && wait_bar(&sh.abort, acc_empty0 + 8 * buf, ((it >> 1) & 1u) ^ 1u, p.status);
         tc_fence_after();
-        const int batch = p.nbatch == 2 ? tile_at(p, t).batch : 0;
         uint32_t add = 0;
         for (int seg = 0; seg < p.nseg; ++seg) {
-          const int ia = p.nbatch == 2 ? batch : seg;
-          const bool amn = p.a_mn[ia], bmn = p.b_mn[seg];
+          const bool amn = p.a_mn[seg], bmn = p.b_mn[seg];  // batches lie alike
           // an MN-major operand's next 16 of k are 16 rows on, a K-major one's 32 bytes
           const uint32_t as = amn ? 2048u >> 4 : 32u >> 4, bs = bmn ? 2048u >> 4 : 32u >> 4;
           const uint32_t a0 = desc_lo(ring, amn ? kChunk : 16u);
