@@ -216,42 +216,59 @@ bool few_tokens(const DenseJob &j) {
          along_k(j.b[0]) && (!j.gated || along_k(j.b[1]));
 }
 
-// One product; only counts its workspace where `dry`.
-int product(DenseJob &j, Ws &ws, bool dry, cudaStream_t s) {
-  if (j.m == 0 || j.n == 0) return COLL_OK;
-  set_vec(j);
-  if (j.k == 0)
-    return dry || coll::dense_empty_sum(j, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+// One product, or two independent ones; only counts their workspace where `dry`. `join`: column
+// sums that a launch of tensor-core products takes along.
+int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
+             const coll::DenseJoin *join = nullptr) {
   uint32_t sms = 0;
-  if (few_tokens(j)) {
-    if (dry) return COLL_OK;
+  coll::TcJob todo[2];
+  coll::DensePack pack = {};
+  int n = 0;
+  if (!dry) {
     const int c = sm_count(sms);
     if (c) return c;
-    return coll::gemv_run(j, sms, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
   }
-  TcOperand a[2], b[2];
-  const int na = j.nbatch == 2 || j.nseg == 2 ? 2 : 1, nb = j.gated || j.nseg == 2 ? 2 : 1;
-  coll::DensePack todo = {};
-  for (int i = 0; i < na; ++i) operand(j.a[i], j.m, j.k, ws, todo, a[i]);
-  operand(j.b[0], j.n, j.k, ws, todo, b[0]);
-  // both halves of a gated product's instruction lie the same way
-  // and both batches' first operands always do (they are scratch)
-  if (nb == 2 && (!in_place(j.b[1], j.n, j.k, b[1]) || (j.gated && b[1].mn != b[0].mn)))
-    lay_out(j.b[1], j.n, j.k, j.gated ? b[0].mn : j.b[1].cs != 1 && j.b[1].rs == 1, ws, todo, b[1]);
+  for (int i = 0; i < count; ++i) {
+    DenseJob &j = jobs[i];
+    if (j.m == 0 || j.n == 0) continue;
+    set_vec(j);
+    if (j.k == 0) {
+      if (!dry && coll::dense_empty_sum(j, s) != cudaSuccess) return COLL_ECUDA;
+      continue;
+    }
+    if (few_tokens(j)) {
+      if (!dry && coll::gemv_run(j, sms, s) != cudaSuccess) return COLL_ECUDA;
+      continue;
+    }
+    coll::TcJob &t = todo[n++];
+    t.j = &j;
+    const int na = j.nbatch == 2 || j.nseg == 2 ? 2 : 1, nb = j.gated || j.nseg == 2 ? 2 : 1;
+    for (int x = 0; x < na; ++x) operand(j.a[x], j.m, j.k, ws, pack, t.a[x]);
+    operand(j.b[0], j.n, j.k, ws, pack, t.b[0]);
+    // both halves of a gated product's instruction lie the same way, and so do both batches'
+    // first operands (they are scratch)
+    if (nb == 2 && (!in_place(j.b[1], j.n, j.k, t.b[1]) || (j.gated && t.b[1].mn != t.b[0].mn)))
+      lay_out(j.b[1], j.n, j.k, j.gated ? t.b[0].mn : j.b[1].cs != 1 && j.b[1].rs == 1, ws, pack,
+              t.b[1]);
+  }
   if (dry) return COLL_OK;
-  int c = sm_count(sms);
-  if (c) return c;
-  if (todo.count && coll::dense_pack(todo, s) != cudaSuccess) return COLL_ECUDA;
-  if (j.m <= coll::kSkinnyMost && j.nseg == 1 && j.nbatch == 1) {
+  if (pack.count && coll::dense_pack(pack, s) != cudaSuccess) return COLL_ECUDA;
+  if (n == 1 && !join && todo[0].j->m <= coll::kSkinnyMost && todo[0].j->nseg == 1 &&
+      todo[0].j->nbatch == 1) {
     coll::SkinnyParams q;
-    c = coll::skinny_plan(q, j, b, a[0], sms);
+    const int c = coll::skinny_plan(q, *todo[0].j, todo[0].b, todo[0].a[0], sms);
     if (c) return c;
-    return coll::skinny_run(q, j.gated != 0, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+    return coll::skinny_run(q, todo[0].j->gated != 0, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  }
+  if (n == 0) {
+    if (join) return coll::dense_join(*join, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+    return COLL_OK;
   }
   coll::TcParams p;
-  c = coll::tc_plan(p, j, a, b, sms);
+  const int c = coll::tc_plan(p, todo, n, sms);
   if (c) return c;
-  return coll::tc_run(p, j.gated != 0, sms, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  if (join) p.join = *join;
+  return coll::tc_run(p, todo[0].j->gated != 0, sms, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
 }
 
 // Scratch matrices.
@@ -293,7 +310,7 @@ int run(const coll_linear_t &a, Ws &ws, bool dry, cudaStream_t s) {
   j.e.res = a.residual.ptr;
   j.e.res_rs = a.residual.rs;
   j.e.res_cs = a.residual.cs;
-  return product(j, ws, dry, s);
+  return products(&j, 1, ws, dry, s);
 }
 
 // ---- its gradients
@@ -316,7 +333,7 @@ int check(const coll_linear_bwd_t &a) {
 }
 
 int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
-  const bool products = a.dx.ptr || a.dw.ptr;
+  const bool wanted = a.dx.ptr || a.dw.ptr;
   coll_mat_t dz = a.dy;
   DenseActBwd b = {};
   b.m = a.m;
@@ -327,7 +344,7 @@ int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
   b.act = (int32_t)a.act;
   if (a.act != COLL_ACT_NONE) b.pre = mat(a.pre);
   TcOperand o;
-  if (products && (a.act != COLL_ACT_NONE || !in_place(mat(a.dy), a.m, a.n, o))) {
+  if (wanted && (a.act != COLL_ACT_NONE || !in_place(mat(a.dy), a.m, a.n, o))) {
     dz = scratch(ws, a.m, a.n);  // both products read it
     b.dz = dz.ptr;
     b.ld = dz.rs;
@@ -337,25 +354,27 @@ int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
     const int64_t blocks = coll::dense_act_bwd_row_blocks(a.m, a.n, true);
     if (blocks > 1) b.part = static_cast<float *>(ws.take((uint64_t)blocks * a.n * 4));
   }
+  coll::DenseJoin join = {};
   if ((b.db || (dz.ptr != a.dy.ptr && a.m > 0)) && a.n > 0 && !dry)
-    if (coll::dense_act_bwd(b, s) != cudaSuccess) return COLL_ECUDA;
+    if (coll::dense_act_bwd(b, join, s) != cudaSuccess) return COLL_ECUDA;
+  DenseJob jobs[2];
+  int n = 0;
   if (a.dx.ptr) {  // dx(m, k) = sum over n of dz(m, n) w(n, k)
-    DenseJob j = job(a.m, a.k, a.n, a.dtype, a.status);
+    DenseJob &j = jobs[n++];
+    j = job(a.m, a.k, a.n, a.dtype, a.status);
     j.a[0] = mat(dz);
     j.b[0] = turned(a.w);
     set_out(j, 0, a.dx);
-    const int c = product(j, ws, dry, s);
-    if (c) return c;
   }
   if (a.dw.ptr) {  // dw(n, k) = sum over m of dz(m, n) x(m, k)
-    DenseJob j = job(a.n, a.k, a.m, a.dtype, a.status);
+    DenseJob &j = jobs[n++];
+    j = job(a.n, a.k, a.m, a.dtype, a.status);
     j.a[0] = turned(dz);
     j.b[0] = turned(a.x);
     j.e.out_type = (int32_t)a.grad_dtype;
     set_out(j, 0, a.dw);
-    return product(j, ws, dry, s);
   }
-  return COLL_OK;
+  return products(jobs, n, ws, dry, s, join.db ? &join : nullptr);
 }
 
 // ---- h = act(x w_gate^T) (x w_up^T)
@@ -386,7 +405,7 @@ int run(const coll_gated_t &a, Ws &ws, bool dry, cudaStream_t s) {
   j.e.gate_rs = a.gate.rs;
   j.e.up = a.up.ptr;
   j.e.up_rs = a.up.rs;
-  return product(j, ws, dry, s);
+  return products(&j, 1, ws, dry, s);
 }
 
 // ---- its gradients
@@ -427,21 +446,24 @@ int run(const coll_gated_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
     b.type = (int32_t)a.dtype;
     b.act = (int32_t)a.act;
     b.gated = 1;
-    if (coll::dense_act_bwd(b, s) != cudaSuccess) return COLL_ECUDA;
+    coll::DenseJoin none;
+    if (coll::dense_act_bwd(b, none, s) != cudaSuccess) return COLL_ECUDA;
   }
+  DenseJob jobs[2];
+  int n = 0;
   if (a.dx.ptr) {  // dx = dg w_gate + du w_up: one sum over both
-    DenseJob j = job(a.m, a.k, a.n, a.dtype, a.status);
+    DenseJob &j = jobs[n++];
+    j = job(a.m, a.k, a.n, a.dtype, a.status);
     j.nseg = 2;
     j.a[0] = mat(dg);
     j.a[1] = mat(du);
     j.b[0] = turned(a.w_gate);
     j.b[1] = turned(a.w_up);
     set_out(j, 0, a.dx);
-    const int c = product(j, ws, dry, s);
-    if (c) return c;
   }
-  if (a.dw_gate.ptr) {  // dw_gate = dg^T x, dw_up = du^T x: one launch
-    DenseJob j = job(a.n, a.k, a.m, a.dtype, a.status);
+  if (a.dw_gate.ptr) {  // dw_gate = dg^T x, dw_up = du^T x
+    DenseJob &j = jobs[n++];
+    j = job(a.n, a.k, a.m, a.dtype, a.status);
     j.nbatch = 2;
     j.a[0] = turned(dg);
     j.a[1] = turned(du);
@@ -449,9 +471,8 @@ int run(const coll_gated_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
     j.e.out_type = (int32_t)a.grad_dtype;
     set_out(j, 0, a.dw_gate);
     set_out(j, 1, a.dw_up);
-    return product(j, ws, dry, s);
   }
-  return COLL_OK;
+  return products(jobs, n, ws, dry, s);
 }
 
 template <typename T>

@@ -46,6 +46,14 @@ struct DenseJob {
   int32_t *status;
 };
 
+// Column sums of row blocks still to be added, in order: db[c] = sum over b of part[b][c].
+struct DenseJoin {
+  const float *part;
+  int64_t blocks, n;
+  void *db;  // NULL: nothing to do
+  int32_t type;
+};
+
 // Elementwise parts of the backward calls (dense_aux.cu).
 struct DenseActBwd {
   int64_t m, n;
@@ -57,7 +65,9 @@ struct DenseActBwd {
   int32_t type, db_type, act, gated;
 };
 int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums);
-cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s);
+// With more than one row block, db is only complete after the join that `join` receives.
+cudaError_t dense_act_bwd(const DenseActBwd &a, DenseJoin &join, cudaStream_t s);
+cudaError_t dense_join(const DenseJoin &join, cudaStream_t s);
 
 
 // dst[i * ld + j] = src(i, j): operands whose strides or base no tensor map takes, laid out in
@@ -65,10 +75,11 @@ cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s);
 struct DensePack {
   DenseMat src[4];
   int64_t rows[4], cols[4], ld[4];
+  int64_t parts[4];  // pieces of a row (dense_pack sets them)
   uint16_t *dst[4];
   int count;
 };
-cudaError_t dense_pack(const DensePack &p, cudaStream_t s);
+cudaError_t dense_pack(DensePack &p, cudaStream_t s);
 
 // The job's epilogue over accumulators of zero (nothing to sum over).
 cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s);

@@ -17,12 +17,16 @@ namespace {
 constexpr int COLS = 256;   // columns per CTA: 32 lanes of eight
 constexpr int GROUPS = 8;   // row groups per CTA, a warp each
 
-// eight columns of one row; VEC: all there and 16-byte aligned
-template <bool VEC>
+// Eight columns of one row, zeros past its end. ALIGN 16: rows of whole 16-byte runs; 4: rows of
+// whole pairs; 0: any strides.
+template <int ALIGN>
 __device__ __forceinline__ uint4 load8(const DenseMat &m, int64_t row, int64_t col, int64_t left) {
   const uint16_t *p = static_cast<const uint16_t *>(m.p) + row * m.rs + col * m.cs;
-  if constexpr (VEC) {
+  if constexpr (ALIGN == 16) {
     return __ldcs(reinterpret_cast<const uint4 *>(p));
+  } else if constexpr (ALIGN == 4) {
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(p);
+    return make_uint4(q[0], left > 2 ? q[1] : 0u, left > 4 ? q[2] : 0u, left > 6 ? q[3] : 0u);
   } else {
     uint32_t v[8];
 #pragma unroll
@@ -47,8 +51,8 @@ __device__ __forceinline__ void store8(void *base, int64_t off, int type, const 
 
 // Two rows a turn keep six 16-byte loads of a lane in flight (one row where loads are single
 // elements, which are many already).
-template <bool GATED, int ACT, int TYPE, bool VEC>
-__global__ void __launch_bounds__(256, VEC ? 4 : 2) act_bwd_kernel(const DenseActBwd a,
+template <bool GATED, int ACT, int TYPE, int ALIGN>
+__global__ void __launch_bounds__(256, ALIGN == 16 ? 4 : 2) act_bwd_kernel(const DenseActBwd a,
                                                          int64_t rows_per_block) {
   griddep_launch();
   griddep_wait();
@@ -79,12 +83,12 @@ __global__ void __launch_bounds__(256, VEC ? 4 : 2) act_bwd_kernel(const DenseAc
     if (GATED) store8(a.du, r * a.ld + col, TYPE, z);
   };
   if (left > 0) {
-    constexpr int AHEAD = VEC ? 2 : 1;
+    constexpr int AHEAD = ALIGN ? 2 : 1;
     uint4 y[AHEAD], z[AHEAD] = {}, u[AHEAD] = {};
     auto fetch = [&](int i, int64_t r) {
-      y[i] = load8<VEC>(a.dy, r, col, left);
-      if (ACT != COLL_ACT_NONE) z[i] = load8<VEC>(a.pre, r, col, left);
-      if (GATED) u[i] = load8<VEC>(a.up, r, col, left);
+      y[i] = load8<ALIGN>(a.dy, r, col, left);
+      if (ACT != COLL_ACT_NONE) z[i] = load8<ALIGN>(a.pre, r, col, left);
+      if (GATED) u[i] = load8<ALIGN>(a.up, r, col, left);
     };
     for (int64_t r = r0 + grp; r < r1; r += AHEAD * GROUPS) {
 #pragma unroll
@@ -111,50 +115,56 @@ __global__ void __launch_bounds__(256, VEC ? 4 : 2) act_bwd_kernel(const DenseAc
   }
 }
 
-bool runs16(const DenseMat &m) {
-  return !m.p || (((uintptr_t)m.p & 15u) == 0 && m.cs == 1 && m.rs % 8 == 0);
+// Bits of the rows' addresses; all set where columns are apart.
+uint64_t row_bits(const DenseMat &m) {
+  return !m.p ? 0 : m.cs != 1 ? ~(uint64_t)0 : (uintptr_t)m.p | (uint64_t)(m.rs * 2);
 }
 
 template <bool GATED, int ACT>
 cudaError_t launch_act_bwd(const DenseActBwd &a, dim3 grid, int64_t per, cudaStream_t s) {
-  const bool vec = a.n % 8 == 0 && runs16(a.dy) && runs16(a.pre) && runs16(a.up);
+  const uint64_t bits =
+      (uint64_t)a.n * 2 | row_bits(a.dy) | row_bits(a.pre) | row_bits(a.up);
+  const int align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 0;
   auto kernel = a.type == COLL_BF16
-                    ? (vec ? act_bwd_kernel<GATED, ACT, COLL_BF16, true>
-                           : act_bwd_kernel<GATED, ACT, COLL_BF16, false>)
-                    : (vec ? act_bwd_kernel<GATED, ACT, COLL_F16, true>
-                           : act_bwd_kernel<GATED, ACT, COLL_F16, false>);
+                    ? (align == 16  ? act_bwd_kernel<GATED, ACT, COLL_BF16, 16>
+                       : align == 4 ? act_bwd_kernel<GATED, ACT, COLL_BF16, 4>
+                                    : act_bwd_kernel<GATED, ACT, COLL_BF16, 0>)
+                    : (align == 16  ? act_bwd_kernel<GATED, ACT, COLL_F16, 16>
+                       : align == 4 ? act_bwd_kernel<GATED, ACT, COLL_F16, 4>
+                                    : act_bwd_kernel<GATED, ACT, COLL_F16, 0>);
   return dense_launch(kernel, grid, 256, 0, 1, s, a, per);
 }
 
-__global__ void __launch_bounds__(256) join_kernel(const float *part, int64_t blocks, int64_t n,
-                                                   void *db, int type) {
+__global__ void __launch_bounds__(256) join_kernel(const DenseJoin j) {
   griddep_launch();
   griddep_wait();
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (c >= n) return;
-  float s = 0.0f;
-  for (int64_t b = 0; b < blocks; ++b) s += part[b * n + c];
-  st_elem(db, c, s, type);
+  if (c < j.n) join_column(j, c);
 }
 
-// A thread moves eight neighbouring elements: plain 2-byte loads (the rows start anywhere), one
-// 16-byte store.
+// A warp takes a row, a lane eight neighbouring elements: plain loads of single elements (the rows
+// start anywhere), one 16-byte store.
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ DensePack a) {
   griddep_launch();
   griddep_wait();
-  const int o = blockIdx.y;
+  const int o = blockIdx.y, lane = threadIdx.x & 31;
   const DenseMat src = a.src[o];
-  const int64_t cols = a.cols[o], ld = a.ld[o], runs = ld / 8, total = a.rows[o] * runs;
-  uint16_t *const dst = a.dst[o];
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
-       i += (int64_t)gridDim.x * 256) {
-    const int64_t r = i / runs, c = (i - r * runs) * 8;
-    const uint16_t *p = static_cast<const uint16_t *>(src.p) + r * src.rs + c * src.cs;
-    uint32_t v[8];
+  const int64_t rows = a.rows[o], cols = a.cols[o], ld = a.ld[o];
+  const int64_t warps = (int64_t)gridDim.x * 8;
+  const int64_t parts = a.parts[o], whole = (ld / 8 + parts - 1) / parts;  // runs of a part
+  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < rows * parts; w += warps) {
+    const int64_t r = parts == 1 ? w : w / parts, q0 = (w - r * parts) * whole;
+    const int64_t q1 = q0 + whole < ld / 8 ? q0 + whole : ld / 8;
+    const uint16_t *row = static_cast<const uint16_t *>(src.p) + r * src.rs;
+    for (int64_t q = q0 + lane; q < q1; q += 32) {
+      const int64_t c = q * 8;
+      const uint16_t *p = row + c * src.cs;
+      uint32_t v[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q) v[q] = c + q < cols ? p[q * src.cs] : 0u;
-    *reinterpret_cast<uint4 *>(dst + r * ld + c) =
-        make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+      for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[i * src.cs] : 0u;
+      *reinterpret_cast<uint4 *>(a.dst[o] + r * ld + c) =
+          make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
   }
 }
 
@@ -177,13 +187,15 @@ unsigned grid_for(int64_t threads) {
 
 }  // namespace
 
-cudaError_t dense_pack(const DensePack &p, cudaStream_t s) {
+cudaError_t dense_pack(DensePack &p, cudaStream_t s) {
   int64_t most = 0;
   for (int i = 0; i < p.count; ++i) {
-    const int64_t runs = p.rows[i] * (p.ld[i] / 8);
-    if (runs > most) most = runs;
+    // long rows are cut where there are too few of them for 16 warps on each of 152 SMs
+    p.parts[i] = 1;
+    while (p.rows[i] * p.parts[i] < 2432 && p.ld[i] / 8 / p.parts[i] > 64) p.parts[i] *= 2;
+    if (p.rows[i] * p.parts[i] > most) most = p.rows[i] * p.parts[i];
   }
-  return dense_launch(pack_kernel, dim3(grid_for(most), (unsigned)p.count), 256, 0, 1, s, p);
+  return dense_launch(pack_kernel, dim3(grid_for(most * 32), (unsigned)p.count), 256, 0, 1, s, p);
 }
 
 cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s) {
@@ -205,7 +217,7 @@ int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums) {
   return per ? (m + per - 1) / per : 1;
 }
 
-cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s) {
+cudaError_t dense_act_bwd(const DenseActBwd &a, DenseJoin &join, cudaStream_t s) {
   const int64_t blocks = dense_act_bwd_row_blocks(a.m, a.n, a.db != nullptr);
   const int64_t per = (a.m + blocks - 1) / blocks;
   const dim3 grid((unsigned)((a.n + COLS - 1) / COLS), (unsigned)blocks);
@@ -224,10 +236,12 @@ cudaError_t dense_act_bwd(const DenseActBwd &a, cudaStream_t s) {
 #undef COLL_ACT_CASE
     default: err = launch_act_bwd<true, COLL_ACT_SIGMOID>(a, grid, per, s);
   }
-  if (err == cudaSuccess && !a.gated && a.db && blocks > 1)
-    err = dense_launch(join_kernel, dim3((unsigned)((a.n + 255) / 256)), 256, 0, 1, s, a.part,
-                       blocks, a.n, a.db, a.db_type);
+  join = DenseJoin{a.part, blocks, a.n, !a.gated && blocks > 1 ? a.db : nullptr, a.db_type};
   return err;
+}
+
+cudaError_t dense_join(const DenseJoin &join, cudaStream_t s) {
+  return dense_launch(join_kernel, dim3((unsigned)((join.n + 255) / 256)), 256, 0, 1, s, join);
 }
 
 }  // namespace coll

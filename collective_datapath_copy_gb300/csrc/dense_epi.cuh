@@ -271,14 +271,33 @@ __device__ __forceinline__ void staged_store(uint32_t *st, void *p, int64_t rs, 
     st[lane * kPitch + i] = type == COLL_BF16 ? f2h2(v[2 * i], v[2 * i + 1], COLL_BF16)
                                               : f2h2(v[2 * i], v[2 * i + 1], COLL_F16);
   __syncwarp();
-  uint16_t *const o = static_cast<uint16_t *>(p);
+  uint16_t *o = static_cast<uint16_t *>(p);
   if (in_pairs(p, rs)) {
     const int c = 2 * (lane & 15);
+    if (rows == 32 && cols == 32) {
+      uint32_t w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = st[(2 * i + (lane >> 4)) * kPitch + (lane & 15)];
+      o += (lane >> 4) * rs + c;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        *reinterpret_cast<uint32_t *>(o) = w[i];
+        o += 2 * rs;
+      }
+      return;
+    }
 #pragma unroll 4
     for (int r = lane >> 4; r < rows; r += 2) {
       const uint32_t w = st[r * kPitch + (lane & 15)];
       if (c + 1 < cols) *reinterpret_cast<uint32_t *>(o + r * rs + c) = w;
       else if (c < cols) o[r * rs + c] = (uint16_t)w;
+    }
+  } else if (rows == 32 && cols == 32) {
+    o += lane;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+      *o = reinterpret_cast<const uint16_t *>(st + r * kPitch)[lane];
+      o += rs;
     }
   } else if (lane < cols) {
 #pragma unroll 4
@@ -353,6 +372,20 @@ __device__ __forceinline__ void epilogue_one(const DenseEpi &e, int batch, int64
     if (e.res) g += ld_elem(e.res, row * e.res_rs + col * e.res_cs, e.out_type);
   }
   st_elem(e.out[batch], row * e.out_rs[batch] + col, g, e.out_type);
+}
+
+__device__ __forceinline__ void join_column(const DenseJoin &j, int64_t c) {
+  float s = 0.0f;
+  int64_t b = 0;
+  for (; b + 8 <= j.blocks; b += 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = j.part[(b + i) * j.n + c];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += v[i];
+  }
+  for (; b < j.blocks; ++b) s += j.part[b * j.n + c];
+  st_elem(j.db, c, s, j.type);
 }
 
 __device__ __forceinline__ float bias_at(const DenseEpi &e, int64_t col) {

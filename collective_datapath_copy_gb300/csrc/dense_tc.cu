@@ -36,6 +36,8 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
+constexpr int64_t kTileNs = 600;          // of a tile beside its k blocks
+
 constexpr int CG = 2;                     // CTAs of a tile (cta_group::2)
 constexpr int kTileK = 64;                // elements of k per stage: one 128-byte swizzled row
 constexpr uint32_t kABytes = 128 * 128;   // 128 rows
@@ -50,7 +52,7 @@ struct Shared {
 };
 
 struct Tile {
-  int batch;
+  int prob, batch;
   int64_t m0, n0;
 };
 
@@ -76,21 +78,43 @@ __device__ __forceinline__ uint32_t div_rem(uint32_t t, uint32_t d, uint32_t &re
   return q;
 }
 
-__device__ __forceinline__ Tile tile_at(const TcParams &p, uint32_t t) {
-  Tile r;
-  uint32_t in = t, row;
-  r.batch = 0;
-  const uint32_t per = p.tiles_m * p.tiles_n;
-  if (t >= per) {  // two batches at most
-    r.batch = 1;
-    in -= per;
+// The tiles of one cluster in their order: those of the first product in turn, then the second
+// product's. A cluster that got one tile of the first product less takes `even` tiles of the
+// second before all others join in, so that the clusters end together.
+struct Walk {
+  uint32_t cluster, clusters, first, extra;  // its tiles of product 0; clusters with one more
+  __device__ __forceinline__ Walk(const TcParams &p) {
+    clusters = gridDim.x / CG;
+    cluster = blockIdx.x / CG;
+    const uint32_t t = p.prob[0].tiles;
+    first = t > cluster ? (t - cluster + clusters - 1) / clusters : 0;
+    extra = t % clusters;
   }
-  const uint32_t first = div_rem(in, 8u * p.tiles_n, in) * 8u;
-  const uint32_t col = div_rem(in, min(8u, p.tiles_m - first), row);
-  r.m0 = (int64_t)(first + row) * p.tile_rows;
-  r.n0 = (int64_t)col * p.tile_cols;
-  return r;
-}
+  // the i-th tile; false past the last
+  __device__ __forceinline__ bool at(const TcParams &p, uint32_t i, Tile &r) const {
+    uint32_t t;
+    r.prob = i >= first;
+    if (!r.prob) {
+      t = cluster + i * clusters;
+    } else {
+      i -= first;
+      const uint32_t early = p.even * (clusters - extra);
+      if (cluster >= extra && i < p.even) t = i * (clusters - extra) + cluster - extra;
+      else t = early + (cluster >= extra ? i - p.even : i) * clusters + cluster;
+    }
+    const TcProb &q = p.prob[r.prob];
+    if (t >= q.tiles) return false;
+    const uint32_t per = q.tiles_m * q.tiles_n;
+    r.batch = t >= per;  // two batches at most
+    if (r.batch) t -= per;
+    uint32_t row;
+    const uint32_t top = div_rem(t, 8u * q.tiles_n, t) * 8u;
+    const uint32_t col = div_rem(t, min(8u, q.tiles_m - top), row);
+    r.m0 = (int64_t)(top + row) * (128 * CG);
+    r.n0 = (int64_t)col * q.tile_cols;
+    return true;
+  }
+};
 
 template <bool GATED>
 __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__ TcParams p) {
@@ -103,10 +127,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const bool leader = rank == 0u;
-  const uint32_t clusters = gridDim.x / CG, cluster = blockIdx.x / CG;
+  const Walk walk(p);
+  Tile tl;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
+    for (uint32_t i = 0; i < p.stages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
     }
@@ -131,16 +156,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 
   if (warp == 0) {
     const uint32_t arrive0 = map_rank(full0, 0);
-    // bytes a stage receives, boxes past the edges counted whole
-    const uint32_t kr = p.b_rows * 128, mr = p.b_chunks * kChunk;
     uint32_t s = 0, phase = 0;
     bool ok = true;
     // k blocks of one segment; the operands' major axes are fixed within it
-    auto segment = [&](auto amn_c, auto bmn_c, const CUtensorMap *ma, const CUtensorMap *mb,
-                       int32_t m, int32_t n) {
+    auto segment = [&](auto amn_c, auto bmn_c, const TcProb &q, const CUtensorMap *ma,
+                       const CUtensorMap *mb, int32_t m, int32_t n) {
       constexpr bool amn = decltype(amn_c)::value, bmn = decltype(bmn_c)::value;
-      const uint32_t bytes = CG * (kABytes + (bmn ? mr : kr));
-      const int32_t end = p.kblocks * kTileK;
+      // bytes a stage receives, boxes past the edges counted whole
+      const uint32_t bytes = CG * (kABytes + (bmn ? q.b_chunks * kChunk : q.b_rows * 128u));
+      const int32_t end = q.kblocks * kTileK, chunks = q.b_chunks;
       for (int32_t k = 0; k < end; k += kTileK) {
         ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
         if (elect_one() && ok) {
@@ -155,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           }
           if (bmn) {
             tma_box_pair(db, mb, n, k, bar);
-            if (p.b_chunks > 1) tma_box_pair(db + kChunk, mb, n + 64, k, bar);
+            if (chunks > 1) tma_box_pair(db + kChunk, mb, n + 64, k, bar);
           } else {
             tma_box_pair(db, mb, k, n, bar);
           }
@@ -169,19 +193,19 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     };
     using Yes = std::integral_constant<bool, true>;
     using No = std::integral_constant<bool, false>;
-    for (uint32_t t = cluster; t < p.tiles; t += clusters) {
-      const Tile tl = tile_at(p, t);
+    for (uint32_t i = 0; walk.at(p, i, tl); ++i) {
+      const TcProb &q = p.prob[tl.prob];
       const int32_t m = (int32_t)tl.m0 + (int32_t)rank * 128;
-      const int32_t n = (int32_t)tl.n0 + (GATED ? 0 : (int32_t)rank * p.b_rows);
-      for (int seg = 0; seg < p.nseg; ++seg) {
-        const CUtensorMap *ma = &p.a[p.nbatch == 2 ? tl.batch : seg];
-        const CUtensorMap *mb = &p.b[GATED ? (int)rank : seg];
-        if (p.a_mn[seg]) {
-          if (p.b_mn[seg]) segment(Yes{}, Yes{}, ma, mb, m, n);
-          else segment(Yes{}, No{}, ma, mb, m, n);
+      const int32_t n = (int32_t)tl.n0 + (GATED ? 0 : (int32_t)rank * q.b_rows);
+      for (int seg = 0; seg < q.nseg; ++seg) {
+        const CUtensorMap *ma = &q.a[q.nbatch == 2 ? tl.batch : seg];
+        const CUtensorMap *mb = &q.b[GATED ? (int)rank : seg];
+        if (q.a_mn[seg]) {
+          if (q.b_mn[seg]) segment(Yes{}, Yes{}, q, ma, mb, m, n);
+          else segment(Yes{}, No{}, q, ma, mb, m, n);
         } else {
-          if (p.b_mn[seg]) segment(No{}, Yes{}, ma, mb, m, n);
-          else segment(No{}, No{}, ma, mb, m, n);
+          if (q.b_mn[seg]) segment(No{}, Yes{}, q, ma, mb, m, n);
+          else segment(No{}, No{}, q, ma, mb, m, n);
         }
       }
     }
@@ -197,21 +221,22 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     if (leader) {
       const uint32_t hi = desc_hi(1024), step = stage_bytes >> 4;
       const uint32_t acc_full0 = smem_u32(&sh.acc_full[0]), acc_empty0 = smem_u32(&sh.acc_empty[0]);
-      uint32_t s = 0, phase = 0, it = 0, at = 0;  // at: 16-byte units from the ring's start
+      uint32_t s = 0, phase = 0, at = 0;  // at: 16-byte units from the ring's start
       bool ok = true;
-      for (uint32_t t = cluster; t < p.tiles; t += clusters, ++it) {
+      for (uint32_t it = 0; walk.at(p, it, tl); ++it) {
+        const TcProb &q = p.prob[tl.prob];
         const uint32_t buf = it & 1u, d = tmem + buf * 256u;
         ok = ok && wait_bar(&sh.abort, acc_empty0 + 8 * buf, ((it >> 1) & 1u) ^ 1u, p.status);
         tc_fence_after();
         uint32_t add = 0;
-        for (int seg = 0; seg < p.nseg; ++seg) {
-          const bool amn = p.a_mn[seg], bmn = p.b_mn[seg];  // batches lie alike
+        for (int seg = 0; seg < q.nseg; ++seg) {
+          const bool amn = q.a_mn[seg], bmn = q.b_mn[seg];  // batches lie alike
           // an MN-major operand's next 16 of k are 16 rows on, a K-major one's 32 bytes
           const uint32_t as = amn ? 2048u >> 4 : 32u >> 4, bs = bmn ? 2048u >> 4 : 32u >> 4;
           const uint32_t a0 = desc_lo(ring, amn ? kChunk : 16u);
           const uint32_t b0 = desc_lo(ring + kABytes, bmn ? kChunk : 16u);
-          const uint32_t idesc = p.idesc | ((uint32_t)amn << 15) | ((uint32_t)bmn << 16);
-          for (int kb = p.kblocks; kb > 0; --kb) {
+          const uint32_t idesc = q.idesc | ((uint32_t)amn << 15) | ((uint32_t)bmn << 16);
+          for (int kb = q.kblocks; kb > 0; --kb) {
             ok = ok && wait_bar(&sh.abort, full0 + 8 * s, phase, p.status);
             tc_fence_after();
             if (elect_one() && ok) {
@@ -236,20 +261,23 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         __syncwarp();
       }
     }
+  } else if (warp == 3) {
+    if (!GATED && p.join.db)
+      for (int64_t c = (int64_t)blockIdx.x * 32 + lane; c < p.join.n; c += (int64_t)gridDim.x * 32)
+        join_column(p.join, c);
   } else if (warp >= 4) {
     const int quad = warp & 3, part = (warp - 4) >> 2;
     uint32_t *const st = staged + (warp - 4) * 32 * kPitch;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
-    const DenseEpi &e = p.e;
-    const bool wide = e.vec == 32;
-    const bool pre_res = !GATED && e.vec && e.res && e.out_type != COLL_F32;
-    uint32_t it = 0;
-    for (uint32_t t = cluster; t < p.tiles; t += clusters, ++it) {
-      const Tile tl = tile_at(p, t);
+    for (uint32_t it = 0; walk.at(p, it, tl); ++it) {
+      const TcProb &q = p.prob[tl.prob];
+      const DenseEpi &e = q.e;
+      const bool wide = e.vec == 32;
+      const bool pre_res = !GATED && e.vec && e.res && e.out_type != COLL_F32;
       const uint32_t buf = it & 1u;
       const int64_t row0 = tl.m0 + rank * 128 + quad * 32, row = row0 + lane;
-      const bool live = row < p.m;
-      const int cols = (int)min((int64_t)p.tile_cols, p.n - tl.n0);
+      const bool live = row < q.m;
+      const int cols = (int)min((int64_t)q.tile_cols, q.n - tl.n0);
       uint32_t r[16];  // the residual of the next 32 columns, asked for ahead
       auto ask = [&](int c0) {
         if (pre_res && live && c0 + 32 <= cols) ld_halves(e.res, row * e.res_rs + tl.n0 + c0, r, wide);
@@ -261,10 +289,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         float g[32], u[GATED ? 32 : 1];
         const uint32_t at = lanes + buf * 256u + c0;
         tmem_load32(at, g);
-        if constexpr (GATED) tmem_load32(at + p.tile_cols, u);
+        if constexpr (GATED) tmem_load32(at + q.tile_cols, u);
         const int64_t col = tl.n0 + c0;
         const bool vec = e.vec && c0 + 32 <= cols;
-        const int rows = (int)max((int64_t)0, min((int64_t)32, p.m - row0)), left = min(32, cols - c0);
+        const int rows = (int)max((int64_t)0, min((int64_t)32, q.m - row0));
+        const int left = min(32, cols - c0);
         auto store = [&](void *base, int64_t rs, int type, const float (&v)[32]) {
           if (vec) {
             if (live) st_run32(base, row * rs + col, type, wide, v);
@@ -303,11 +332,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
               add_halves(g, r, e.type);
               ask(c0 + 64);
             } else if (live) {
-              const float *q = static_cast<const float *>(e.res) + row * e.res_rs + col;
+              const float *rp = static_cast<const float *>(e.res) + row * e.res_rs + col;
 #pragma unroll
               for (int i = 0; i < 32; i += 8) {
                 uint32_t x[8];
-                ld_sector(q + i, x, wide);
+                ld_sector(rp + i, x, wide);
 #pragma unroll
                 for (int w = 0; w < 8; ++w) g[i + w] += __uint_as_float(x[w]);
               }
@@ -365,63 +394,86 @@ int tc_encode(CUtensorMap *map, const TcOperand &o, int64_t type, uint32_t rows)
              : COLL_EINVAL;
 }
 
-int tc_plan(TcParams &p, const DenseJob &j, const TcOperand *a, const TcOperand *b,
-            uint32_t sms) {
+int tc_plan(TcParams &p, const TcJob *jobs, int count, uint32_t sms) {
   memset(&p, 0, sizeof(p));
-  p.e = j.e;
-  p.m = j.m;
-  p.n = j.n;
-  p.status = j.status;
-  p.nseg = j.nseg;
-  p.nbatch = j.nbatch;
-  p.kblocks = (int32_t)ceil_div(j.k, kTileK);
-  const uint32_t clusters = sms / CG;
-  p.tile_rows = 128 * CG;
-  p.tiles_m = ceil_div(j.m, p.tile_rows);
-  // Columns of the accumulator: those with the least rounds of tiles times the time of a tile's k
-  // block, 62 ns and 1.08 a column (measured at 4096 x 4096 x 8192: 144 ns for 64 columns, 186 for
-  // 128, 264 for 192, 339 for 256).
-  int best = 256;
-  int64_t cost = INT64_MAX;
-  for (int bn = 256; bn >= 64; bn -= j.gated ? 64 : 32) {
-    const int64_t cols = j.gated ? bn / 2 : bn;
-    const int64_t tiles = (int64_t)p.tiles_m * ceil_div(j.n, cols) * j.nbatch;
-    const int64_t c = (tiles + clusters - 1) / clusters * (62 + bn * 69 / 64);
-    if (c < cost) {
-      cost = c;
-      best = bn;
+  const int64_t clusters = sms / CG;
+  // Columns of each product's accumulator: those that end first. A tile takes its k blocks times
+  // 62 ns and 1.08 a column (measured at 4096 x 4096 x 8192: 144 ns for 64 columns, 186 for 128,
+  // 264 for 192, 339 for 256), and every cluster its tiles one after the other.
+  int64_t tiles[2] = {0, 0}, time[2] = {1, 1}, best = INT64_MAX;
+  int cols[2] = {256, 256};
+  auto measure = [&](int i, int bn) {
+    const DenseJob &j = *jobs[i].j;
+    tiles[i] = (int64_t)ceil_div(j.m, 128 * CG) * ceil_div(j.n, j.gated ? bn / 2 : bn) * j.nbatch;
+    time[i] = (int64_t)ceil_div(j.k, kTileK) * j.nseg * (62 + bn * 69 / 64) + kTileNs;
+  };
+  auto even = [&]() { return (time[0] + time[1] / 2) / time[1]; };
+  for (int b0 = 256; b0 >= 64; b0 -= jobs[0].j->gated ? 64 : 32) {
+    measure(0, b0);
+    for (int b1 = 256; b1 >= (count == 2 ? 64 : 256); b1 -= 32) {
+      if (count == 2) measure(1, b1);
+      // the busiest cluster: of those with one tile of the first product more, or of the others
+      const int64_t whole = tiles[0] / clusters, extra = tiles[0] % clusters;
+      const int64_t early = count == 2 ? even() * (clusters - extra) : 0;
+      int64_t with = 0, without = 0;
+      if (tiles[1] > early) with = without = (tiles[1] - early + clusters - 1) / clusters;
+      if (count == 2)
+        without += tiles[1] > early ? even() : ceil_div(tiles[1], clusters - extra);
+      const int64_t t0 = extra ? (whole + 1) * time[0] + with * time[1] : 0;
+      const int64_t t1 = whole * time[0] + without * time[1], t = t0 > t1 ? t0 : t1;
+      if (t < best) {
+        best = t;
+        cols[0] = b0;
+        cols[1] = b1;
+      }
     }
   }
-  p.b_rows = best / CG;
-  p.tile_cols = j.gated ? best / 2 : best;
-  p.b_chunks = (p.b_rows + 63) / 64;
-  p.tiles_n = ceil_div(j.n, p.tile_cols);
-  const int64_t tiles = (int64_t)p.tiles_m * p.tiles_n * j.nbatch;
-  if (tiles > 0x7FFFFFFF) return COLL_EINVAL;
-  p.tiles = (uint32_t)tiles;
-  const int na = j.nbatch == 2 || j.nseg == 2 ? 2 : 1, nb = j.gated || j.nseg == 2 ? 2 : 1;
-  bool bmn = false;
-  for (int i = 0; i < na; ++i) {
-    p.a_mn[i] = a[i].mn;
-    const int c = tc_encode(&p.a[i], a[i], j.e.type, 128);
-    if (c) return c;
+  p.status = jobs[0].j->status;
+  for (int i = 0; i < count; ++i) {
+    const DenseJob &j = *jobs[i].j;
+    TcProb &q = p.prob[i];
+    measure(i, cols[i]);
+    if (tiles[i] > 0x7FFFFFFF) return COLL_EINVAL;
+    q.e = j.e;
+    q.m = j.m;
+    q.n = j.n;
+    q.nseg = j.nseg;
+    q.nbatch = j.nbatch;
+    q.kblocks = (int32_t)ceil_div(j.k, kTileK);
+    q.tiles_m = ceil_div(j.m, 128 * CG);
+    q.b_rows = cols[i] / CG;
+    q.tile_cols = j.gated ? cols[i] / 2 : cols[i];
+    q.b_chunks = (q.b_rows + 63) / 64;
+    q.tiles_n = ceil_div(j.n, q.tile_cols);
+    q.tiles = (uint32_t)tiles[i];
+    q.idesc = mma_desc(j.e.type == COLL_BF16, false, false, 128 * CG, (uint32_t)cols[i]);
+    const int na = j.nbatch == 2 || j.nseg == 2 ? 2 : 1, nb = j.gated || j.nseg == 2 ? 2 : 1;
+    bool bmn = false;
+    for (int x = 0; x < na; ++x) {
+      q.a_mn[x] = jobs[i].a[x].mn;
+      const int c = tc_encode(&q.a[x], jobs[i].a[x], j.e.type, 128);
+      if (c) return c;
+    }
+    for (int x = 0; x < nb; ++x) {
+      q.b_mn[x] = jobs[i].b[x].mn;
+      bmn = bmn || jobs[i].b[x].mn;
+      const int c = tc_encode(&q.b[x], jobs[i].b[x], j.e.type, (uint32_t)q.b_rows);
+      if (c) return c;
+    }
+    const uint32_t rows = bmn ? (uint32_t)q.b_chunks * 64u : (uint32_t)q.b_rows;
+    const uint32_t bytes = kABytes + ((rows * 128u + 1023u) & ~1023u);
+    if (bytes > p.stage_bytes) p.stage_bytes = bytes;
   }
-  for (int i = 0; i < nb; ++i) {
-    p.b_mn[i] = b[i].mn;
-    bmn = bmn || b[i].mn;
-    const int c = tc_encode(&p.b[i], b[i], j.e.type, (uint32_t)p.b_rows);
-    if (c) return c;
-  }
-  const uint32_t rows = bmn ? (uint32_t)p.b_chunks * 64u : (uint32_t)p.b_rows;
-  p.stage_bytes = kABytes + ((rows * 128u + 1023u) & ~1023u);
-  p.stages = (int32_t)((kTcSmem - 1024 - kStageOut) / p.stage_bytes);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.idesc = mma_desc(j.e.type == COLL_BF16, false, false, 128 * CG, (uint32_t)best);
+  p.even = count == 2 && tiles[0] % clusters ? (uint32_t)even() : 0;
+  p.stages = (kTcSmem - 1024 - kStageOut) / p.stage_bytes;
+  if (p.stages > (uint32_t)kMaxStages) p.stages = kMaxStages;
   return COLL_OK;
 }
 
 cudaError_t tc_run(const TcParams &p, bool gated, uint32_t sms, cudaStream_t s) {
-  const uint32_t most = sms / CG, clusters = p.tiles < most ? p.tiles : most;
+  const uint64_t most = sms / CG, tiles = (uint64_t)p.prob[0].tiles + p.prob[1].tiles;
+  // with two products every cluster takes part: the tiles are dealt for all of them
+  const uint32_t clusters = (uint32_t)(tiles < most && !p.prob[1].tiles ? tiles : most);
   const uint32_t smem = 1024 + (uint32_t)p.stages * p.stage_bytes + kStageOut;
   return gated ? launch<true>(p, clusters, smem, s) : launch<false>(p, clusters, smem, s);
 }

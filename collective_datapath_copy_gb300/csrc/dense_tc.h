@@ -10,17 +10,26 @@ namespace coll {
 
 constexpr uint32_t kTcSmem = 226 * 1024;  // dynamic shared memory a CTA may ask for
 
-struct TcParams {
+// One product of a launch.
+struct TcProb {
   CUtensorMap a[2], b[2];
   DenseEpi e;
   int64_t m, n;
-  int32_t *status;
   uint32_t tiles_m, tiles_n, tiles;
-  int32_t tile_rows, tile_cols;  // of the output
-  int32_t b_rows, b_chunks;      // rows of B per CTA and operand, and 64-row chunks of them
-  int32_t kblocks, nseg, nbatch, stages;
-  uint32_t stage_bytes, idesc;
-  int32_t a_mn[2], b_mn[2];      // 1: the operand's rows (not k) are contiguous
+  int32_t tile_cols;         // of the output
+  int32_t b_rows, b_chunks;  // rows of B per CTA and operand, and 64-row chunks of them
+  int32_t kblocks, nseg, nbatch;
+  uint32_t idesc;
+  int32_t a_mn[2], b_mn[2];  // 1: the operand's rows (not k) are contiguous
+};
+
+struct TcParams {
+  TcProb prob[2];  // the second's tiles may be 0
+  DenseJoin join;
+  int32_t *status;
+  uint32_t even;   // turns of the second product's tiles that only go to the clusters with one
+                   // tile of the first product less
+  uint32_t stages, stage_bytes;
 };
 
 // An operand as the tensor maps take it: rows x k, k contiguous (mn == 0) or rows contiguous.
@@ -35,8 +44,14 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // Map of an operand in boxes of 64 of k by `rows` rows (k contiguous) or 64 rows by 64 of k.
 int tc_encode(CUtensorMap *map, const TcOperand &o, int64_t type, uint32_t rows);
 
-// Fill shapes and maps of `p` for the job; operands a[nseg or nbatch], b[nseg, or 2 when gated].
-int tc_plan(TcParams &p, const DenseJob &j, const TcOperand *a, const TcOperand *b, uint32_t sms);
+// A job with its operands: a[nseg or nbatch], b[nseg, or 2 when gated].
+struct TcJob {
+  const DenseJob *j;
+  TcOperand a[2], b[2];
+};
+
+// Fill shapes and maps of `p` for one or two jobs (two: neither gated).
+int tc_plan(TcParams &p, const TcJob *jobs, int count, uint32_t sms);
 cudaError_t tc_run(const TcParams &p, bool gated, uint32_t sms, cudaStream_t s);
 
 
