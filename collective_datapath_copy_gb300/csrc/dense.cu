@@ -200,15 +200,6 @@ void operand(const DenseMat &m, int64_t rows, int64_t k, Ws &ws, coll::DensePack
   if (!in_place(m, rows, k, o)) lay_out(m, rows, k, m.cs != 1 && m.rs == 1, ws, todo, o);
 }
 
-int sm_count(uint32_t &sms) {
-  int dev = 0, v = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return COLL_ECUDA;
-  sms = (uint32_t)v;
-  return COLL_OK;
-}
-
 // Products that the direct kernel takes: few rows, everything contiguous along k.
 bool few_tokens(const DenseJob &j) {
   auto along_k = [&](const DenseMat &m) { return m.cs == 1 || j.k == 1; };
@@ -220,14 +211,9 @@ bool few_tokens(const DenseJob &j) {
 // sums that a launch of tensor-core products takes along.
 int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
              const coll::DenseJoin *join = nullptr) {
-  uint32_t sms = 0;
   coll::TcJob todo[2];
   coll::DensePack pack = {};
   int n = 0;
-  if (!dry) {
-    const int c = sm_count(sms);
-    if (c) return c;
-  }
   for (int i = 0; i < count; ++i) {
     DenseJob &j = jobs[i];
     if (j.m == 0 || j.n == 0) continue;
@@ -237,7 +223,7 @@ int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
       continue;
     }
     if (few_tokens(j)) {
-      if (!dry && coll::gemv_run(j, sms, s) != cudaSuccess) return COLL_ECUDA;
+      if (!dry && coll::gemv_run(j, s) != cudaSuccess) return COLL_ECUDA;
       continue;
     }
     coll::TcJob &t = todo[n++];
@@ -251,24 +237,30 @@ int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
       lay_out(j.b[1], j.n, j.k, j.gated ? t.b[0].mn : j.b[1].cs != 1 && j.b[1].rs == 1, ws, pack,
               t.b[1]);
   }
+  const bool skinny = n == 1 && !join && todo[0].j->m <= coll::kSkinnyMost &&
+                      todo[0].j->nseg == 1 && todo[0].j->nbatch == 1;
+  coll::TcParams p;
+  if (n && !skinny) {
+    uint64_t bytes[2];
+    const int c = coll::tc_plan(p, todo, n, bytes);
+    if (c) return c;
+    for (int i = 0; i < n; ++i)
+      if (bytes[i]) p.prob[i].part = static_cast<float *>(ws.take(bytes[i]));
+  }
   if (dry) return COLL_OK;
   if (pack.count && coll::dense_pack(pack, s) != cudaSuccess) return COLL_ECUDA;
-  if (n == 1 && !join && todo[0].j->m <= coll::kSkinnyMost && todo[0].j->nseg == 1 &&
-      todo[0].j->nbatch == 1) {
-    coll::SkinnyParams q;
-    const int c = coll::skinny_plan(q, *todo[0].j, todo[0].b, todo[0].a[0], sms);
-    if (c) return c;
-    return coll::skinny_run(q, todo[0].j->gated != 0, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
-  }
   if (n == 0) {
     if (join) return coll::dense_join(*join, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
     return COLL_OK;
   }
-  coll::TcParams p;
-  const int c = coll::tc_plan(p, todo, n, sms);
-  if (c) return c;
+  if (skinny) {
+    coll::SkinnyParams q;
+    const int c = coll::skinny_plan(q, *todo[0].j, todo[0].b, todo[0].a[0]);
+    if (c) return c;
+    return coll::skinny_run(q, todo[0].j->gated != 0, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  }
   if (join) p.join = *join;
-  return coll::tc_run(p, todo[0].j->gated != 0, sms, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  return coll::tc_run(p, todo, n, s);
 }
 
 // Scratch matrices.
@@ -349,10 +341,12 @@ int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
     b.dz = dz.ptr;
     b.ld = dz.rs;
   }
+  bool later = false;  // db's row blocks are joined by the launch of the products
   if (a.db) {
     b.db = a.db;
     const int64_t blocks = coll::dense_act_bwd_row_blocks(a.m, a.n, true);
-    if (blocks > 1) b.part = static_cast<float *>(ws.take((uint64_t)blocks * a.n * 4));
+    later = blocks > 1 && a.n > 0;
+    if (later) b.part = static_cast<float *>(ws.take((uint64_t)blocks * a.n * 4));
   }
   coll::DenseJoin join = {};
   if ((b.db || (dz.ptr != a.dy.ptr && a.m > 0)) && a.n > 0 && !dry)
@@ -374,7 +368,7 @@ int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
     j.e.out_type = (int32_t)a.grad_dtype;
     set_out(j, 0, a.dw);
   }
-  return products(jobs, n, ws, dry, s, join.db ? &join : nullptr);
+  return products(jobs, n, ws, dry, s, later ? &join : nullptr);
 }
 
 // ---- h = act(x w_gate^T) (x w_up^T)

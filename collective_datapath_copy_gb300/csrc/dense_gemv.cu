@@ -176,7 +176,7 @@ int row_align(const void *p, int64_t rows, int64_t ld, int64_t k) {
 
 }  // namespace
 
-cudaError_t gemv_run(const DenseJob &j, uint32_t sms, cudaStream_t s) {
+cudaError_t gemv_run(const DenseJob &j, cudaStream_t s) {
   GemvParams p = {};
   p.e = j.e;
   p.m = j.m;
@@ -194,7 +194,7 @@ cudaError_t gemv_run(const DenseJob &j, uint32_t sms, cudaStream_t s) {
   // Warps of a CTA: 16, one CTA an SM, where there are no more CTAs than SMs, else 8 and two CTAs
   // an SM (128 registers a thread); no more than there are steps of k.
   const int64_t ctas = (j.n + (j.gated ? 7 : 15)) / (j.gated ? 8 : 16), steps = (j.k + kStep - 1) / kStep;
-  p.warps = ctas <= (int64_t)sms ? 16 : 8;
+  p.warps = ctas <= (int64_t)kSms ? 16 : 8;
   while (p.warps > 1 && p.warps > steps) p.warps /= 2;
   if (j.e.type == COLL_BF16)
     return j.gated ? launch<true, COLL_BF16>(p, align, s) : launch<false, COLL_BF16>(p, align, s);

@@ -292,8 +292,7 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-int skinny_plan(SkinnyParams &p, const DenseJob &j, const TcOperand *w, const TcOperand &x,
-                uint32_t sms) {
+int skinny_plan(SkinnyParams &p, const DenseJob &j, const TcOperand *w, const TcOperand &x) {
   memset(&p, 0, sizeof(p));
   p.e = j.e;
   p.m = j.m;
@@ -308,38 +307,49 @@ int skinny_plan(SkinnyParams &p, const DenseJob &j, const TcOperand *w, const Tc
   // accumulators are read 32 columns at a time
   p.tmem_cols = 32;
   while ((int32_t)p.tmem_cols < p.cols * (mats - 1) + (p.cols + 31) / 32 * 32) p.tmem_cols *= 2;
-  // Features per CTA and shares of k: the least time of the busiest SM, in ns. Its bytes arrive
-  // at 45 bytes a ns; a k block takes 250 ns to issue; joining shares costs 3 us.
   const uint32_t x_bytes = (p.x_mn ? p.x_chunks * 64u : (uint32_t)p.cols) * 128u;
+  // A CTA's ring for so many features: four stages or more within what two CTAs of an SM can have,
+  // else one CTA with all of it. A matrix instruction reads 128 rows whatever p.rows is, so the
+  // last stage has slack behind it. Returns the CTAs an SM holds.
+  auto ring = [&](int rows) {
+    p.rows = rows;
+    p.w_chunks = (rows + 63) / 64;
+    p.w_bytes = (uint32_t)rows * 128u;
+    p.stage_bytes = mats * p.w_bytes + ((x_bytes + 1023u) & ~1023u);
+    const uint32_t fixed = 1024 + 16384 - p.w_bytes;
+    const bool two = p.stage_bytes * 4 <= kTwoPerSm - fixed && p.tmem_cols <= 256;
+    p.stages = (int32_t)(((two ? kTwoPerSm : kTcSmem) - fixed) / p.stage_bytes);
+    if (p.stages > kMaxStages) p.stages = kMaxStages;
+    p.smem = fixed + p.stages * p.stage_bytes;
+    if (p.smem < kNoThird) p.smem = kNoThird;
+    return two ? 2 : 1;
+  };
+  // Features per CTA and shares of k: the least time, in ns. An SM takes 45 bytes a ns; a k block
+  // takes 190 ns to issue (gated 300), a wave of CTAs 1.5 us beside its blocks, joining shares
+  // 2.5 us. Clusters fill whole groups of SMs: of 1, 2, 4 and 8 CTAs, 152, 76, 36 and 16 fit at
+  // one CTA an SM.
   int64_t best = INT64_MAX;
+  int best_rows = 128;
   for (int rows = 128; rows >= 32; rows -= p.w_mn ? 64 : 8) {
-    for (int split = 1; split <= 8 && split <= p.kblocks; ++split) {
-      // the partial sums fit what a CTA has at least
-      if (split > 1 && j.m * 128 * 4 * mats > 64 * 1024) break;
-      const int64_t ctas = ceil_div(j.n, rows) * split, blocks = ceil_div(p.kblocks, split);
-      const int64_t per = ceil_div(ctas, sms);
-      const int64_t bytes = per * blocks * (rows * mats * 128 + x_bytes);
-      const int64_t issue = ceil_div(per, 2) * blocks * 250;
-      const int64_t ns = (bytes / 45 > issue ? bytes / 45 : issue) + (split > 1 ? 3000 : 0);
+    const int per_sm = ring(rows);
+    for (int split = 1; split <= 8 && split <= p.kblocks; split *= 2) {
+      if (split > 1 && j.m * 128 * 4 * mats > 64 * 1024) break;  // the shares fit the ring
+      static constexpr int kFit[9] = {0, 152, 76, 0, 36, 0, 0, 0, 16};
+      const int64_t tiles = ceil_div(j.n, rows), blocks = ceil_div(p.kblocks, split);
+      const int64_t waves = ceil_div(tiles, kFit[split] * per_sm);
+      const int64_t beside = tiles * split > kSms ? per_sm : 1;
+      const int64_t arrive = beside * (rows * mats * 128 + x_bytes) / 45;
+      const int64_t issue = j.gated ? 300 : 190;
+      const int64_t ns =
+          waves * (blocks * (arrive > issue ? arrive : issue) + 1500) + (split > 1 ? 2500 : 0);
       if (ns < best) {
         best = ns;
-        p.rows = rows;
+        best_rows = rows;
         p.split = split;
       }
     }
   }
-  p.w_chunks = (p.rows + 63) / 64;
-  p.w_bytes = (uint32_t)p.rows * 128u;
-  p.stage_bytes = mats * p.w_bytes + ((x_bytes + 1023u) & ~1023u);
-  // four stages or more within what two CTAs of an SM can have, else one CTA with all of it; a
-  // matrix instruction reads 128 rows whatever p.rows is, so the last stage has slack behind it
-  const uint32_t slack = 16384 - p.w_bytes, fixed = 1024 + slack;
-  uint32_t room = kTwoPerSm - fixed;
-  if (p.stage_bytes * 4 > room || p.tmem_cols > 256) room = kTcSmem - fixed;
-  p.stages = (int32_t)(room / p.stage_bytes);
-  if (p.stages > kMaxStages) p.stages = kMaxStages;
-  p.smem = fixed + p.stages * p.stage_bytes;
-  if (p.smem < kNoThird) p.smem = kNoThird;
+  ring(best_rows);
   p.tiles = (uint32_t)ceil_div(j.n, p.rows);
   p.idesc = mma_desc(j.e.type == COLL_BF16, p.w_mn != 0, p.x_mn != 0, 128, (uint32_t)p.cols);
   for (int i = 0; i < mats; ++i) {

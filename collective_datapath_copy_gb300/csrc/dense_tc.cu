@@ -37,6 +37,8 @@ namespace {
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
 constexpr int64_t kTileNs = 600;          // of a tile beside its k blocks
+constexpr int64_t kJoinNs = 2500;         // of joining shares, beside their bytes
+constexpr int kMostShares = 16;
 
 constexpr int CG = 2;                     // CTAs of a tile (cta_group::2)
 constexpr int kTileK = 64;                // elements of k per stage: one 128-byte swizzled row
@@ -52,7 +54,7 @@ struct Shared {
 };
 
 struct Tile {
-  int prob, batch;
+  int prob, batch, share;
   int64_t m0, n0;
 };
 
@@ -76,6 +78,14 @@ __device__ __forceinline__ uint32_t div_rem(uint32_t t, uint32_t d, uint32_t &re
     rest = t - q * d;
   }
   return q;
+}
+
+// k blocks [x, y) of a share, counted through the segments.
+__device__ __forceinline__ int2 share_of(const TcProb &q, int share) {
+  const int all = q.nseg * q.kblocks;
+  if (q.split == 1) return make_int2(0, all);
+  return make_int2((int)((int64_t)share * all / q.split),
+                   (int)((int64_t)(share + 1) * all / q.split));
 }
 
 // The tiles of one cluster in their order: those of the first product in turn, then the second
@@ -105,9 +115,13 @@ struct Walk {
     const TcProb &q = p.prob[r.prob];
     if (t >= q.tiles) return false;
     const uint32_t per = q.tiles_m * q.tiles_n;
-    r.batch = t >= per;  // two batches at most
-    if (r.batch) t -= per;
-    uint32_t row;
+    uint32_t row, unit = div_rem(t, per, t);
+    r.batch = 0;
+    if (q.nbatch == 2) {
+      r.batch = unit & 1u;
+      unit >>= 1;
+    }
+    r.share = unit;
     const uint32_t top = div_rem(t, 8u * q.tiles_n, t) * 8u;
     const uint32_t col = div_rem(t, min(8u, q.tiles_m - top), row);
     r.m0 = (int64_t)(top + row) * (128 * CG);
@@ -160,12 +174,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     bool ok = true;
     // k blocks of one segment; the operands' major axes are fixed within it
     auto segment = [&](auto amn_c, auto bmn_c, const TcProb &q, const CUtensorMap *ma,
-                       const CUtensorMap *mb, int32_t m, int32_t n) {
+                       const CUtensorMap *mb, int32_t m, int32_t n, int32_t k, int32_t end) {
       constexpr bool amn = decltype(amn_c)::value, bmn = decltype(bmn_c)::value;
       // bytes a stage receives, boxes past the edges counted whole
       const uint32_t bytes = CG * (kABytes + (bmn ? q.b_chunks * kChunk : q.b_rows * 128u));
-      const int32_t end = q.kblocks * kTileK, chunks = q.b_chunks;
-      for (int32_t k = 0; k < end; k += kTileK) {
+      const int32_t chunks = q.b_chunks;
+      for (; k < end; k += kTileK) {
         ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
         if (elect_one() && ok) {
           const uint32_t bar = arrive0 + 8 * s;
@@ -197,15 +211,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
       const TcProb &q = p.prob[tl.prob];
       const int32_t m = (int32_t)tl.m0 + (int32_t)rank * 128;
       const int32_t n = (int32_t)tl.n0 + (GATED ? 0 : (int32_t)rank * q.b_rows);
+      const int2 range = share_of(q, tl.share);
       for (int seg = 0; seg < q.nseg; ++seg) {
+        const int k0 = max(range.x - seg * q.kblocks, 0) * kTileK;
+        const int k1 = min(range.y - seg * q.kblocks, q.kblocks) * kTileK;
         const CUtensorMap *ma = &q.a[q.nbatch == 2 ? tl.batch : seg];
         const CUtensorMap *mb = &q.b[GATED ? (int)rank : seg];
         if (q.a_mn[seg]) {
-          if (q.b_mn[seg]) segment(Yes{}, Yes{}, q, ma, mb, m, n);
-          else segment(Yes{}, No{}, q, ma, mb, m, n);
+          if (q.b_mn[seg]) segment(Yes{}, Yes{}, q, ma, mb, m, n, k0, k1);
+          else segment(Yes{}, No{}, q, ma, mb, m, n, k0, k1);
         } else {
-          if (q.b_mn[seg]) segment(No{}, Yes{}, q, ma, mb, m, n);
-          else segment(No{}, No{}, q, ma, mb, m, n);
+          if (q.b_mn[seg]) segment(No{}, Yes{}, q, ma, mb, m, n, k0, k1);
+          else segment(No{}, No{}, q, ma, mb, m, n, k0, k1);
         }
       }
     }
@@ -229,6 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         ok = ok && wait_bar(&sh.abort, acc_empty0 + 8 * buf, ((it >> 1) & 1u) ^ 1u, p.status);
         tc_fence_after();
         uint32_t add = 0;
+        const int2 range = share_of(q, tl.share);
         for (int seg = 0; seg < q.nseg; ++seg) {
           const bool amn = q.a_mn[seg], bmn = q.b_mn[seg];  // batches lie alike
           // an MN-major operand's next 16 of k are 16 rows on, a K-major one's 32 bytes
@@ -236,7 +254,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           const uint32_t a0 = desc_lo(ring, amn ? kChunk : 16u);
           const uint32_t b0 = desc_lo(ring + kABytes, bmn ? kChunk : 16u);
           const uint32_t idesc = q.idesc | ((uint32_t)amn << 15) | ((uint32_t)bmn << 16);
-          for (int kb = q.kblocks; kb > 0; --kb) {
+          const int kb0 = max(range.x - seg * q.kblocks, 0);
+          const int kb1 = min(range.y - seg * q.kblocks, q.kblocks);
+          for (int kb = kb0; kb < kb1; ++kb) {
             ok = ok && wait_bar(&sh.abort, full0 + 8 * s, phase, p.status);
             tc_fence_after();
             if (elect_one() && ok) {
@@ -291,6 +311,15 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         tmem_load32(at, g);
         if constexpr (GATED) tmem_load32(at + q.tile_cols, u);
         const int64_t col = tl.n0 + c0;
+        if (q.split > 1) {  // this share's sums; whole runs, the rows are padded for them
+          if (live) {
+            const int64_t plane = (tl.share * q.nbatch + tl.batch) * (GATED ? 2 : 1);
+            st_run32(q.part, (plane * q.m + row) * q.part_ld + col, COLL_F32, true, g);
+            if constexpr (GATED)
+              st_run32(q.part, ((plane + 1) * q.m + row) * q.part_ld + col, COLL_F32, true, u);
+          }
+          continue;
+        }
         const bool vec = e.vec && c0 + 32 <= cols;
         const int rows = (int)max((int64_t)0, min((int64_t)32, q.m - row0));
         const int left = min(32, cols - c0);
@@ -365,6 +394,38 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   }
 }
 
+// The shares of a split product, added in order of k, and its epilogue: a thread takes one output.
+struct ShareJoin {
+  DenseJob j[2];
+  const float *part[2];
+  int64_t part_ld[2];
+  int32_t split[2];
+};
+
+template <bool GATED>
+__global__ void __launch_bounds__(256) share_join_kernel(const __grid_constant__ ShareJoin s) {
+  griddep_launch();
+  griddep_wait();
+  const int w = blockIdx.z;
+  const DenseJob &j = s.j[w];
+  const int64_t ld = s.part_ld[w], plane = j.m * ld, col = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (s.split[w] < 2 || col >= j.n) return;
+  const float bias = GATED ? 0.0f : bias_at(j.e, col);
+  const int64_t rows = j.m * j.nbatch, step = plane * j.nbatch * (GATED ? 2 : 1);
+  for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
+    const int batch = r >= j.m;
+    const int64_t row = r - batch * j.m;
+    const float *p = s.part[w] + batch * plane + row * ld + col;
+    float g = p[0], u = GATED ? p[plane] : 0.0f;
+#pragma unroll 4
+    for (int i = 1; i < s.split[w]; ++i) {
+      g += p[i * step];
+      if (GATED) u += p[i * step + plane];
+    }
+    epilogue_one<GATED>(j.e, batch, row, col, g, u, bias);
+  }
+}
+
 template <bool GATED>
 cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStream_t s) {
   static const cudaError_t ready = cudaFuncSetAttribute(
@@ -372,6 +433,9 @@ cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStre
   if (ready != cudaSuccess) return ready;
   return dense_launch(tc_kernel<GATED>, dim3(clusters * CG), kThreads, smem, CG, s, p);
 }
+
+int operands_a(const DenseJob &j) { return j.nbatch == 2 || j.nseg == 2 ? 2 : 1; }
+int operands_b(const DenseJob &j) { return j.gated || j.nseg == 2 ? 2 : 1; }
 
 uint32_t ceil_div(int64_t a, int64_t b) { return (uint32_t)((a + b - 1) / b); }
 
@@ -394,51 +458,74 @@ int tc_encode(CUtensorMap *map, const TcOperand &o, int64_t type, uint32_t rows)
              : COLL_EINVAL;
 }
 
-int tc_plan(TcParams &p, const TcJob *jobs, int count, uint32_t sms) {
+int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]) {
   memset(&p, 0, sizeof(p));
-  const int64_t clusters = sms / CG;
-  // Columns of each product's accumulator: those that end first. A tile takes its k blocks times
-  // 62 ns and 1.08 a column (measured at 4096 x 4096 x 8192: 144 ns for 64 columns, 186 for 128,
-  // 264 for 192, 339 for 256), and every cluster its tiles one after the other.
-  int64_t tiles[2] = {0, 0}, time[2] = {1, 1}, best = INT64_MAX;
-  int cols[2] = {256, 256};
-  auto measure = [&](int i, int bn) {
+  const int64_t clusters = kSms / CG;
+  // Columns of each product's accumulator and shares of its k: those that end first. A tile takes
+  // its k blocks times 62 ns and 1.08 a column (measured at 4096 x 4096 x 8192: 144 ns for 64
+  // columns, 186 for 128, 264 for 192, 339 for 256), and every cluster its tiles one after the
+  // other. Joining shares costs a launch and their way through L2.
+  int64_t tiles[2] = {0, 0}, time[2] = {1, 1}, joining[2] = {0, 0}, best = INT64_MAX;
+  int cols[2] = {256, 256}, split[2] = {1, 1};
+  auto measure = [&](int i, int bn, int sp) {
     const DenseJob &j = *jobs[i].j;
-    tiles[i] = (int64_t)ceil_div(j.m, 128 * CG) * ceil_div(j.n, j.gated ? bn / 2 : bn) * j.nbatch;
-    time[i] = (int64_t)ceil_div(j.k, kTileK) * j.nseg * (62 + bn * 69 / 64) + kTileNs;
+    tiles[i] =
+        (int64_t)ceil_div(j.m, 128 * CG) * ceil_div(j.n, j.gated ? bn / 2 : bn) * j.nbatch * sp;
+    time[i] = (int64_t)ceil_div((int64_t)ceil_div(j.k, kTileK) * j.nseg, sp) * (62 + bn * 69 / 64) +
+              kTileNs;
+    joining[i] = sp > 1 ? kJoinNs + j.m * j.n * j.nbatch * (j.gated ? 2 : 1) * sp / 500 : 0;
   };
   auto even = [&]() { return (time[0] + time[1] / 2) / time[1]; };
+  // the busiest cluster: of those with one tile of the first product more, or of the others
+  auto makespan = [&]() {
+    const int64_t whole = tiles[0] / clusters, extra = tiles[0] % clusters;
+    const int64_t early = count == 2 ? even() * (clusters - extra) : 0;
+    int64_t with = 0, without = 0;
+    if (tiles[1] > early) with = without = (tiles[1] - early + clusters - 1) / clusters;
+    if (count == 2) without += tiles[1] > early ? even() : ceil_div(tiles[1], clusters - extra);
+    const int64_t t0 = extra ? (whole + 1) * time[0] + with * time[1] : 0;
+    const int64_t t1 = whole * time[0] + without * time[1];
+    return (t0 > t1 ? t0 : t1) + (joining[0] > joining[1] ? joining[0] : joining[1]);
+  };
+  auto keep = [&](int b0, int s0, int b1, int s1) {
+    const int64_t t = makespan();
+    if (t >= best) return;
+    best = t;
+    cols[0] = b0, cols[1] = b1;
+    split[0] = s0, split[1] = s1;
+  };
   for (int b0 = 256; b0 >= 64; b0 -= jobs[0].j->gated ? 64 : 32) {
-    measure(0, b0);
+    measure(0, b0, 1);
     for (int b1 = 256; b1 >= (count == 2 ? 64 : 256); b1 -= 32) {
-      if (count == 2) measure(1, b1);
-      // the busiest cluster: of those with one tile of the first product more, or of the others
-      const int64_t whole = tiles[0] / clusters, extra = tiles[0] % clusters;
-      const int64_t early = count == 2 ? even() * (clusters - extra) : 0;
-      int64_t with = 0, without = 0;
-      if (tiles[1] > early) with = without = (tiles[1] - early + clusters - 1) / clusters;
-      if (count == 2)
-        without += tiles[1] > early ? even() : ceil_div(tiles[1], clusters - extra);
-      const int64_t t0 = extra ? (whole + 1) * time[0] + with * time[1] : 0;
-      const int64_t t1 = whole * time[0] + without * time[1], t = t0 > t1 ? t0 : t1;
-      if (t < best) {
-        best = t;
-        cols[0] = b0;
-        cols[1] = b1;
-      }
+      if (count == 2) measure(1, b1, 1);
+      keep(b0, 1, b1, 1);
     }
+  }
+  // shares of k, where a tile takes longer than a fair part of everything
+  for (int i = 0; i < count; ++i) {
+    const int other = 1 - i, other_cols = cols[other], other_split = split[other];
+    if (count == 2) measure(other, other_cols, other_split);
+    const int64_t blocks = (int64_t)ceil_div(jobs[i].j->k, kTileK) * jobs[i].j->nseg;
+    for (int bn = 256; bn >= 64; bn -= 64)
+      for (int sp = 2; sp <= kMostShares && blocks >= 4 * sp; sp += sp < 4 ? 1 : sp < 8 ? 2 : 4) {
+        measure(i, bn, sp);
+        if (tiles[i] > 4 * clusters) break;
+        if (i == 0) keep(bn, sp, other_cols, other_split);
+        else keep(other_cols, other_split, bn, sp);
+      }
   }
   p.status = jobs[0].j->status;
   for (int i = 0; i < count; ++i) {
     const DenseJob &j = *jobs[i].j;
     TcProb &q = p.prob[i];
-    measure(i, cols[i]);
+    measure(i, cols[i], split[i]);
     if (tiles[i] > 0x7FFFFFFF) return COLL_EINVAL;
     q.e = j.e;
     q.m = j.m;
     q.n = j.n;
     q.nseg = j.nseg;
     q.nbatch = j.nbatch;
+    q.split = split[i];
     q.kblocks = (int32_t)ceil_div(j.k, kTileK);
     q.tiles_m = ceil_div(j.m, 128 * CG);
     q.b_rows = cols[i] / CG;
@@ -447,35 +534,63 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint32_t sms) {
     q.tiles_n = ceil_div(j.n, q.tile_cols);
     q.tiles = (uint32_t)tiles[i];
     q.idesc = mma_desc(j.e.type == COLL_BF16, false, false, 128 * CG, (uint32_t)cols[i]);
-    const int na = j.nbatch == 2 || j.nseg == 2 ? 2 : 1, nb = j.gated || j.nseg == 2 ? 2 : 1;
+    q.part_ld = (j.n + 31) / 32 * 32;
+    part_bytes[i] = split[i] > 1 ? (uint64_t)split[i] * j.nbatch * (j.gated ? 2 : 1) * j.m *
+                                       q.part_ld * 4
+                                 : 0;
     bool bmn = false;
-    for (int x = 0; x < na; ++x) {
+    for (int x = 0; x < 2; ++x) {
       q.a_mn[x] = jobs[i].a[x].mn;
-      const int c = tc_encode(&q.a[x], jobs[i].a[x], j.e.type, 128);
-      if (c) return c;
-    }
-    for (int x = 0; x < nb; ++x) {
       q.b_mn[x] = jobs[i].b[x].mn;
-      bmn = bmn || jobs[i].b[x].mn;
-      const int c = tc_encode(&q.b[x], jobs[i].b[x], j.e.type, (uint32_t)q.b_rows);
-      if (c) return c;
     }
+    for (int x = 0; x < operands_b(j); ++x) bmn = bmn || q.b_mn[x];
     const uint32_t rows = bmn ? (uint32_t)q.b_chunks * 64u : (uint32_t)q.b_rows;
     const uint32_t bytes = kABytes + ((rows * 128u + 1023u) & ~1023u);
     if (bytes > p.stage_bytes) p.stage_bytes = bytes;
   }
+  for (int i = count; i < 2; ++i) part_bytes[i] = 0;
   p.even = count == 2 && tiles[0] % clusters ? (uint32_t)even() : 0;
   p.stages = (kTcSmem - 1024 - kStageOut) / p.stage_bytes;
   if (p.stages > (uint32_t)kMaxStages) p.stages = kMaxStages;
   return COLL_OK;
 }
 
-cudaError_t tc_run(const TcParams &p, bool gated, uint32_t sms, cudaStream_t s) {
-  const uint64_t most = sms / CG, tiles = (uint64_t)p.prob[0].tiles + p.prob[1].tiles;
+int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s) {
+  ShareJoin join = {};
+  int64_t cols = 0, rows = 0;
+  for (int i = 0; i < count; ++i) {
+    const DenseJob &j = *jobs[i].j;
+    TcProb &q = p.prob[i];
+    for (int x = 0; x < operands_a(j); ++x) {
+      const int c = tc_encode(&q.a[x], jobs[i].a[x], j.e.type, 128);
+      if (c) return c;
+    }
+    for (int x = 0; x < operands_b(j); ++x) {
+      const int c = tc_encode(&q.b[x], jobs[i].b[x], j.e.type, (uint32_t)q.b_rows);
+      if (c) return c;
+    }
+    join.split[i] = q.split;
+    if (q.split > 1) {
+      join.j[i] = j;
+      join.part[i] = q.part;
+      join.part_ld[i] = q.part_ld;
+      if (j.n > cols) cols = j.n;
+      if (j.m * j.nbatch > rows) rows = j.m * j.nbatch;
+    }
+  }
+  const bool gated = jobs[0].j->gated != 0;
+  const uint64_t most = kSms / CG, tiles = (uint64_t)p.prob[0].tiles + p.prob[1].tiles;
   // with two products every cluster takes part: the tiles are dealt for all of them
-  const uint32_t clusters = (uint32_t)(tiles < most && !p.prob[1].tiles ? tiles : most);
-  const uint32_t smem = 1024 + (uint32_t)p.stages * p.stage_bytes + kStageOut;
-  return gated ? launch<true>(p, clusters, smem, s) : launch<false>(p, clusters, smem, s);
+  const uint32_t clusters = (uint32_t)(tiles < most && count == 1 ? tiles : most);
+  const uint32_t smem = 1024 + p.stages * p.stage_bytes + kStageOut;
+  cudaError_t e = gated ? launch<true>(p, clusters, smem, s) : launch<false>(p, clusters, smem, s);
+  if (e == cudaSuccess && cols) {
+    const dim3 grid((unsigned)((cols + 255) / 256), (unsigned)(rows < 1024 ? rows : 1024),
+                    (unsigned)count);
+    e = dense_launch(gated ? share_join_kernel<true> : share_join_kernel<false>, grid, 256, 0, 1, s,
+                     join);
+  }
+  return e == cudaSuccess ? COLL_OK : COLL_ECUDA;
 }
 
 }  // namespace coll

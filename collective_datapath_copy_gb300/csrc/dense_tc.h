@@ -8,6 +8,7 @@
 
 namespace coll {
 
+constexpr uint32_t kSms = 152;            // multiprocessors of a GB300: what shapes are chosen for
 constexpr uint32_t kTcSmem = 226 * 1024;  // dynamic shared memory a CTA may ask for
 
 // One product of a launch.
@@ -19,6 +20,9 @@ struct TcProb {
   int32_t tile_cols;         // of the output
   int32_t b_rows, b_chunks;  // rows of B per CTA and operand, and 64-row chunks of them
   int32_t kblocks, nseg, nbatch;
+  int32_t split;             // shares of k, each with its own tiles
+  float *part;               // split > 1: their sums, [share][batch][gate, up][m][part_ld]
+  int64_t part_ld;
   uint32_t idesc;
   int32_t a_mn[2], b_mn[2];  // 1: the operand's rows (not k) are contiguous
 };
@@ -50,13 +54,16 @@ struct TcJob {
   TcOperand a[2], b[2];
 };
 
-// Fill shapes and maps of `p` for one or two jobs (two: neither gated).
-int tc_plan(TcParams &p, const TcJob *jobs, int count, uint32_t sms);
-cudaError_t tc_run(const TcParams &p, bool gated, uint32_t sms, cudaStream_t s);
+// The shapes of `p` for one or two jobs (two: neither gated); part_bytes: room for each job's
+// shares, 0 where k is not split. Makes no device call.
+int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]);
+// Tensor maps (p.prob[i].part is set by now), then the launch; the shares of split jobs join in a
+// second one.
+int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s);
 
 
 // Few rows (dense_skinny.cu): the weights are the 128-row operand, the m tokens its columns.
-constexpr int64_t kSkinnyMost = 128;
+constexpr int64_t kSkinnyMost = 64;
 
 struct SkinnyParams {
   CUtensorMap w[2], x;
@@ -70,8 +77,7 @@ struct SkinnyParams {
   uint32_t w_bytes, stage_bytes, smem, idesc, tmem_cols;
 };
 
-int skinny_plan(SkinnyParams &p, const DenseJob &j, const TcOperand *w, const TcOperand &x,
-                uint32_t sms);
+int skinny_plan(SkinnyParams &p, const DenseJob &j, const TcOperand *w, const TcOperand &x);
 cudaError_t skinny_run(const SkinnyParams &p, bool gated, cudaStream_t s);
 
 
@@ -86,6 +92,6 @@ struct GemvParams {
   uint32_t warps;
 };
 
-cudaError_t gemv_run(const DenseJob &j, uint32_t sms, cudaStream_t s);
+cudaError_t gemv_run(const DenseJob &j, cudaStream_t s);
 
 }  // namespace coll

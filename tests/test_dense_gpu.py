@@ -285,6 +285,60 @@ def test_gated_backward_layouts(layouts):
     assert none is None and torch.equal(dx, got[0])
 
 
+# few output tiles and a long sum: k is shared between the tiles of several clusters
+LONG = [(20, 40, 9000), (130, 72, 4100), (200, 130, 16384), (257, 520, 5000), (150, 33, 20001),
+        (600, 300, 3000)]
+
+
+@pytest.mark.parametrize("i,size", list(enumerate(LONG)))
+def test_long_sums(i, size):
+    m, n, k = size
+    dtype = (BF, HF)[i % 2]
+    g = gen(500 + i)
+    x, w, w2 = rnd(g, m, k, dtype), rnd(g, n, k, dtype, k ** -0.5), rnd(g, n, k, dtype, k ** -0.5)
+    b, r = rnd(g, 1, n, dtype)[0], rnd(g, m, n, dtype)
+    y, p = Out(m, n, dtype, 3, 1), Out(m, n, dtype, aligned(n), 0)
+    cdc.Linear(w, b, ACTS[i % 5]).forward(x, residual=r, out=y.v, pre=p.v)
+    want, pre = ref.linear(x, w, b, r, ACTS[i % 5], dtype, dtype)
+    ref.assert_close(y.v, want, "y")
+    ref.assert_close(p.v, pre, "pre")
+    ref.assert_rms(p.v, pre, dtype, "pre")
+    f = cdc.Linear(w, b, ACTS[i % 5]).forward(x, residual=r.float(), out_dtype=F32)
+    ref.assert_close(f, ref.linear(x, w, b, r, ACTS[i % 5], F32, dtype)[0], "f32")
+    h, gate, up = (Out(m, n, dtype, 1, 1) for _ in range(3))
+    cdc.GatedFFN(w, w2, GACTS[i % 5]).forward(x, out=h.v, gate=gate.v, up=up.v)
+    for o, q, what in zip((h, gate, up), ref.gated(x, w, w2, GACTS[i % 5], dtype),
+                          ("h", "gate", "up")):
+        ref.assert_close(o.v, q, what)
+        assert o.untouched()
+    assert y.untouched() and p.untouched()
+
+
+@pytest.mark.parametrize("i,size", list(enumerate(LONG)))
+def test_long_sums_backward(i, size):
+    """dx sums over n, dW over m: each axis in turn is the long one."""
+    a, b, c = size
+    dtype = (HF, BF)[i % 2]
+    g = gen(600 + i)
+    for m, n, k in ((a, c, b), (c, a, b)):
+        x, w, w2 = rnd(g, m, k, dtype), rnd(g, n, k, dtype, .05), rnd(g, n, k, dtype, .05)
+        dy, z, u = (rnd(g, m, n, dtype) for _ in range(3))
+        act = ACTS[i % 5]
+        dx, dw, db = Out(m, k, dtype, 3, 1), Out(n, k, dtype, 3, 1), Out(1, n, dtype, 1, 1)
+        cdc.Linear(w, None, act).backward(dy, x, pre=z, dx=dx.v, dw=dw.v, db=db.v[0])
+        for o, q, what in zip((dx.v, dw.v, db.v[0]),
+                              ref.linear_bwd(dy, z, x, w, act, dtype, dtype), ("dx", "dw", "db")):
+            ref.assert_close(o, q, what)
+        assert dx.untouched() and dw.untouched() and db.untouched()
+        alone = cdc.Linear(w, None, act)
+        ref.assert_close(alone.backward(dy, x, pre=z, need_dw=False, need_db=True)[0],
+                         ref.linear_bwd(dy, z, x, w, act, dtype, dtype)[0])
+        got = cdc.GatedFFN(w, w2, GACTS[i % 5]).backward(dy, x, z, u, grad_dtype=F32)
+        for o, q, what in zip(got, ref.gated_bwd(dy, z, u, x, w, w2, GACTS[i % 5], dtype, F32),
+                              ("dx", "dw_gate", "dw_up")):
+            ref.assert_close(o, q, what)
+
+
 @pytest.mark.parametrize("m,n,k", [(0, 40, 64), (5, 0, 64), (5, 40, 0), (0, 0, 0), (200, 300, 0)])
 def test_empty_axes(m, n, k):
     """No tokens, no outputs, nothing to sum over: zeros, the bias and the residual remain."""
