@@ -200,11 +200,23 @@ void operand(const DenseMat &m, int64_t rows, int64_t k, Ws &ws, coll::DensePack
   if (!in_place(m, rows, k, o)) lay_out(m, rows, k, m.cs != 1 && m.rs == 1, ws, todo, o);
 }
 
-// Products that the direct kernel takes: few rows, everything contiguous along k.
+// Products that the direct kernel takes: few tokens, everything contiguous along k. It reads the
+// tokens again for every 16 outputs, so the more tokens, the sooner that traffic outweighs what it
+// saves (no staging, no tensor maps). Up to 16 tokens always (14336 x 4096: 23 us, the next best
+// 23). Up to 32 for weights of 32 MiB or less (4096 x 1792 for 32 tokens: 6.7 us against 8.7;
+// 6144 x 4096: 20 us against 15) or operands that would have to be laid out first; up to 64 for
+// 4 MiB or less (1024 x 1024 for 48: 4.0 us against 4.9; 1792 x 4096: 11.5 against 8.1).
 bool few_tokens(const DenseJob &j) {
   auto along_k = [&](const DenseMat &m) { return m.cs == 1 || j.k == 1; };
-  return j.m <= coll::kGemvMost && j.k <= (int64_t)1 << 30 && j.nseg == 1 && j.nbatch == 1 && along_k(j.a[0]) &&
-         along_k(j.b[0]) && (!j.gated || along_k(j.b[1]));
+  if (j.m > coll::kGemvMost || j.k > (int64_t)1 << 30 || j.nseg != 1 || j.nbatch != 1 ||
+      !along_k(j.a[0]) || !along_k(j.b[0]) || (j.gated && !along_k(j.b[1])))
+    return false;
+  const int64_t bytes = j.n * j.k * (j.gated ? 4 : 2);
+  TcOperand o;
+  const bool as_it_lies = in_place(j.a[0], j.m, j.k, o) && in_place(j.b[0], j.n, j.k, o) &&
+                          (!j.gated || in_place(j.b[1], j.n, j.k, o));
+  return j.m <= 16 || (j.m <= 32 && (!as_it_lies || bytes <= (int64_t)32 << 20)) ||
+         bytes <= (int64_t)4 << 20;
 }
 
 // One product, or two independent ones; only counts their workspace where `dry`. `join`: column
@@ -238,7 +250,8 @@ int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
               t.b[1]);
   }
   const bool skinny = n == 1 && !join && todo[0].j->m <= coll::kSkinnyMost &&
-                      todo[0].j->nseg == 1 && todo[0].j->nbatch == 1;
+                      todo[0].j->n >= coll::kSkinnyLeast && todo[0].j->nseg == 1 &&
+                      todo[0].j->nbatch == 1;
   coll::TcParams p;
   if (n && !skinny) {
     uint64_t bytes[2];

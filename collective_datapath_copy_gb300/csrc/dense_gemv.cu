@@ -23,7 +23,9 @@ namespace coll {
 namespace {
 
 constexpr int kStep = 64;      // elements of k a warp takes at a time
-constexpr int kMaxWarps = 16;
+// warps of a CTA: shared memory for their sums is 32 KiB at most
+template <int NT>
+constexpr int kMostWarps = NT == 8 ? 8 : 16;
 
 __device__ __forceinline__ void ld_stream32(const void *p, uint32_t (&r)[8]) {
   asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
@@ -83,11 +85,11 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 
 // NT: columns of eight tokens.
 template <bool GATED, int TYPE, int NT, int ALIGN>
-__global__ void __launch_bounds__(kMaxWarps * 32, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
+__global__ void __launch_bounds__(kMostWarps<NT> * 32, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
   griddep_launch();
   constexpr int FEAT = GATED ? 8 : 16;   // outputs of a CTA
-  constexpr int AHEAD = NT == 1 ? 4 : 2;
-  __shared__ float part[kMaxWarps][8 * NT][16];
+  constexpr int AHEAD = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+  __shared__ float part[kMostWarps<NT>][8 * NT][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int64_t f0 = (int64_t)blockIdx.x * FEAT;
@@ -155,7 +157,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32, 1) gemv_kernel(const __grid_co
 template <bool GATED, int TYPE, int NT>
 cudaError_t launch(const GemvParams &p, int align, cudaStream_t s) {
   const unsigned grid = (unsigned)((p.n + (GATED ? 8 : 16) - 1) / (GATED ? 8 : 16));
-  const unsigned threads = p.warps * 32u;
+  const unsigned threads = 32u * (p.warps < kMostWarps<NT> ? p.warps : kMostWarps<NT>);
   auto kernel = align == 32   ? gemv_kernel<GATED, TYPE, NT, 32>
                 : align == 16 ? gemv_kernel<GATED, TYPE, NT, 16>
                 : align == 4  ? gemv_kernel<GATED, TYPE, NT, 4>
@@ -165,7 +167,10 @@ cudaError_t launch(const GemvParams &p, int align, cudaStream_t s) {
 
 template <bool GATED, int TYPE>
 cudaError_t launch(const GemvParams &p, int align, cudaStream_t s) {
-  return p.m <= 8 ? launch<GATED, TYPE, 1>(p, align, s) : launch<GATED, TYPE, 2>(p, align, s);
+  return p.m <= 8    ? launch<GATED, TYPE, 1>(p, align, s)
+         : p.m <= 16 ? launch<GATED, TYPE, 2>(p, align, s)
+         : p.m <= 32 ? launch<GATED, TYPE, 4>(p, align, s)
+                     : launch<GATED, TYPE, 8>(p, align, s);
 }
 
 // The widest access that every row of the matrix starts on.

@@ -1,20 +1,17 @@
-// The products of the dense operators for few rows (serving: from one token to a small batch),
-// on the tensor cores with the operands' roles turned: the weights are the 128-row operand, the
+// The products of the dense operators for a small batch of tokens against many output features, on
+// the tensor cores with the operands' roles turned: the weights are the 128-row operand, the
 // tokens its columns, so no byte that is streamed is padding.
 //
 // Bound by HBM: every weight is read once (2 n k bytes, gated 4 n k) and each SM has to keep
 // about 45 bytes a nanosecond arriving. A CTA takes up to 128 output features (gated: of both
-// matrices, two accumulators in the same lanes) and a share of k; the CTAs of a cluster take the
-// other shares of the same features, so that narrow outputs still occupy every SM. Features per
-// CTA and shares are chosen together for the least bytes on the busiest SM (skinny_plan). The
-// shares join through distributed shared memory in order of k: every CTA leaves its binary32
-// partial sums in its own shared memory and, after a cluster barrier, adds all shares of its part
-// of the outputs. No atomics, no second launch, the same result every time.
+// matrices, two accumulators in the same lanes) over the whole of k; how many is chosen for the
+// least time of the busiest SM (skinny_plan), and dense.cu sends only products here whose features
+// occupy every SM that way. Against the kernel of CTA pairs, which takes the tokens as rows:
+// 14336 x 4096 for 17 to 64 tokens 23 us against 25, gated 40 us (5.8 TB/s) against 45.
 //
-// Two CTAs fit an SM where the batch is small, so that one's start and end run beside the
-// other's stream. Tensor memory is never oversubscribed: the shared memory a CTA asks for keeps
-// a third one off the SM and a CTA takes at most 256 of the 512 columns, so no CTA of a cluster
-// waits for columns while another of its cluster waits for it.
+// Two CTAs fit an SM, so that one's start and end run beside the other's stream. Tensor memory is
+// never oversubscribed: the shared memory a CTA asks for keeps a third one off the SM and a CTA
+// takes at most 256 of the 512 columns.
 #include <cuda.h>
 #include <string.h>
 
@@ -40,12 +37,6 @@ struct Shared {
   uint32_t tmem;
   uint32_t abort;
 };
-
-__device__ __forceinline__ float ld_remote(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-  return v;
-}
 
 // Up to 32 tokens of one feature (lane): values g (and u) are finished and stored; a warp's lanes
 // are neighbouring features, so every access is to neighbouring elements.
@@ -104,10 +95,7 @@ __global__ void __launch_bounds__(kThreads, 2) skinny_kernel(const __grid_consta
   __shared__ Shared sh;
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t split = p.split, tile = blockIdx.x / split, rank = blockIdx.x - tile * split;
-  const int64_t n0 = (int64_t)tile * p.rows;
-  const int kb0 = (int)(rank * (uint32_t)p.kblocks / split);
-  const int kb1 = (int)((rank + 1) * (uint32_t)p.kblocks / split);
+  const int64_t n0 = (int64_t)blockIdx.x * p.rows;
   const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
   const uint32_t done = smem_u32(&sh.done);
   const uint32_t stages = p.stages, stage_bytes = p.stage_bytes, w_bytes = p.w_bytes;
@@ -137,8 +125,8 @@ __global__ void __launch_bounds__(kThreads, 2) skinny_kernel(const __grid_consta
                            (p.x_mn ? p.x_chunks * kChunk : p.cols * 128u);
     // Tiles start at different k blocks and wrap around: all reading the same tokens' lines, and
     // the same columns of every weight row, at once would queue on a few slices of L2.
-    int kb = kb0 + (int)(tile % (uint32_t)(kb1 - kb0));
-    for (int left = kb1 - kb0; left > 0; --left, kb = kb + 1 < kb1 ? kb + 1 : kb0) {
+    int kb = (int)(blockIdx.x % (uint32_t)p.kblocks);
+    for (int left = p.kblocks; left > 0; --left, kb = kb + 1 < p.kblocks ? kb + 1 : 0) {
       ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
       if (elect_one() && ok) {
         const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes;
@@ -175,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 2) skinny_kernel(const __grid_consta
     const uint32_t second = w_bytes >> 4, d2 = tmem + p.cols;
     uint32_t s = 0, phase = 0, add = 0;
     bool ok = true;
-    for (int kb = kb0; kb < kb1; ++kb) {
+    for (int kb = 0; kb < p.kblocks; ++kb) {
       ok = ok && wait_bar(&sh.abort, full0 + 8 * s, phase, p.status);
       tc_fence_after();
       if (elect_one() && ok) {
@@ -212,26 +200,15 @@ __global__ void __launch_bounds__(kThreads, 2) skinny_kernel(const __grid_consta
         float g[32], u[GATED ? 32 : 1];
         tmem_load32(lanes + t0, g);
         if constexpr (GATED) tmem_load32(lanes + p.cols + t0, u);
-        if (split > 1) {  // leave the partial sums, [w][token][128 features]
-          float *const part = reinterpret_cast<float *>(raw + (ring - smem_u32(raw)));
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            if (t0 + i < m) {
-              part[(t0 + i) * 128 + row] = g[i];
-              if (GATED) part[(m + t0 + i) * 128 + row] = u[GATED ? i : 0];
-            }
-          }
+        const int64_t f = n0 + row;
+        if (p.e.type == COLL_BF16) {
+          if (p.e.out_type == COLL_F32)
+            finish32<GATED, COLL_BF16, !GATED>(p.e, t0, f, m - t0, live, g, u);
+          else finish32<GATED, COLL_BF16, false>(p.e, t0, f, m - t0, live, g, u);
         } else {
-          const int64_t f = n0 + row;
-          if (p.e.type == COLL_BF16) {
-            if (p.e.out_type == COLL_F32)
-              finish32<GATED, COLL_BF16, !GATED>(p.e, t0, f, m - t0, live, g, u);
-            else finish32<GATED, COLL_BF16, false>(p.e, t0, f, m - t0, live, g, u);
-          } else {
-            if (p.e.out_type == COLL_F32)
-              finish32<GATED, COLL_F16, !GATED>(p.e, t0, f, m - t0, live, g, u);
-            else finish32<GATED, COLL_F16, false>(p.e, t0, f, m - t0, live, g, u);
-          }
+          if (p.e.out_type == COLL_F32)
+            finish32<GATED, COLL_F16, !GATED>(p.e, t0, f, m - t0, live, g, u);
+          else finish32<GATED, COLL_F16, false>(p.e, t0, f, m - t0, live, g, u);
         }
       }
     }
@@ -241,39 +218,6 @@ __global__ void __launch_bounds__(kThreads, 2) skinny_kernel(const __grid_consta
   tc_fence_before();
   __syncthreads();
   if (sh.abort) drain();
-  if (split > 1) {
-    cluster_sync();
-    if (!sh.abort) {
-      // this CTA's part of the tile's tokens x 128 features, every share added in order of k
-      const int total = (int)p.m * 128;
-      const int per = ((total + (int)split - 1) / (int)split + 31) & ~31;
-      const int end = min(total, (int)(rank + 1) * per);
-      for (int i = (int)rank * per + threadIdx.x; i < end; i += kThreads) {
-        const int t = i >> 7, row = i & 127;
-        if (row >= p.rows || n0 + row >= p.n) continue;
-        float v[8], v2[GATED ? 8 : 1];
-#pragma unroll
-        for (uint32_t q = 0; q < 8; ++q) {
-          if (q < split) {
-            const uint32_t at = map_rank(ring + i * 4, q);
-            v[q] = ld_remote(at);
-            if (GATED) v2[GATED ? q : 0] = ld_remote(at + total * 4);
-          }
-        }
-        float g = v[0], u = v2[0];
-#pragma unroll
-        for (uint32_t q = 1; q < 8; ++q) {
-          if (q < split) {
-            g += v[q];
-            if (GATED) u += v2[GATED ? q : 0];
-          }
-        }
-        const int64_t f = n0 + row;
-        epilogue_one<GATED>(p.e, 0, t, f, g, u, GATED ? 0.0f : bias_at(p.e, f));
-      }
-    }
-    cluster_sync();  // no share goes away while it is read
-  }
   if (warp == 1) {
     tc_fence_after();
     tmem_free<1>(tmem, p.tmem_cols);
@@ -285,7 +229,7 @@ cudaError_t launch(const SkinnyParams &p, cudaStream_t s) {
   static const cudaError_t ready = cudaFuncSetAttribute(
       skinny_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
   if (ready != cudaSuccess) return ready;
-  return dense_launch(skinny_kernel<GATED>, dim3(p.tiles * p.split), kThreads, p.smem, p.split, s, p);
+  return dense_launch(skinny_kernel<GATED>, dim3(p.tiles), kThreads, p.smem, 1, s, p);
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
@@ -324,29 +268,20 @@ int skinny_plan(SkinnyParams &p, const DenseJob &j, const TcOperand *w, const Tc
     if (p.smem < kNoThird) p.smem = kNoThird;
     return two ? 2 : 1;
   };
-  // Features per CTA and shares of k: the least time, in ns. An SM takes 45 bytes a ns; a k block
-  // takes 190 ns to issue (gated 300), a wave of CTAs 1.5 us beside its blocks, joining shares
-  // 2.5 us. Clusters fill whole groups of SMs: of 1, 2, 4 and 8 CTAs, 152, 76, 36 and 16 fit at
-  // one CTA an SM.
+  // Features per CTA: the least time, in ns. An SM takes 45 bytes a ns; a k block takes 190 ns to
+  // issue (gated 300), a wave of CTAs 1.5 us beside its blocks.
   int64_t best = INT64_MAX;
   int best_rows = 128;
   for (int rows = 128; rows >= 32; rows -= p.w_mn ? 64 : 8) {
     const int per_sm = ring(rows);
-    for (int split = 1; split <= 8 && split <= p.kblocks; split *= 2) {
-      if (split > 1 && j.m * 128 * 4 * mats > 64 * 1024) break;  // the shares fit the ring
-      static constexpr int kFit[9] = {0, 152, 76, 0, 36, 0, 0, 0, 16};
-      const int64_t tiles = ceil_div(j.n, rows), blocks = ceil_div(p.kblocks, split);
-      const int64_t waves = ceil_div(tiles, kFit[split] * per_sm);
-      const int64_t beside = tiles * split > kSms ? per_sm : 1;
-      const int64_t arrive = beside * (rows * mats * 128 + x_bytes) / 45;
-      const int64_t issue = j.gated ? 300 : 190;
-      const int64_t ns =
-          waves * (blocks * (arrive > issue ? arrive : issue) + 1500) + (split > 1 ? 2500 : 0);
-      if (ns < best) {
-        best = ns;
-        best_rows = rows;
-        p.split = split;
-      }
+    const int64_t tiles = ceil_div(j.n, rows), waves = ceil_div(tiles, (int64_t)kSms * per_sm);
+    const int64_t beside = tiles > kSms ? per_sm : 1;
+    const int64_t arrive = beside * (rows * mats * 128 + x_bytes) / 45;
+    const int64_t issue = j.gated ? 300 : 190;
+    const int64_t ns = waves * (p.kblocks * (arrive > issue ? arrive : issue) + 1500);
+    if (ns < best) {
+      best = ns;
+      best_rows = rows;
     }
   }
   ring(best_rows);

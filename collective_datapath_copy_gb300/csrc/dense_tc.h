@@ -62,8 +62,10 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
 int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s);
 
 
-// Few rows (dense_skinny.cu): the weights are the 128-row operand, the m tokens its columns.
-constexpr int64_t kSkinnyMost = 64;
+// A small batch against many output features (dense_skinny.cu): the weights are the 128-row
+// operand, the m tokens its columns.
+constexpr int64_t kSkinnyMost = 64;           // tokens
+constexpr int64_t kSkinnyLeast = 64 * kSms;   // output features: 64 for every SM
 
 struct SkinnyParams {
   CUtensorMap w[2], x;
@@ -73,7 +75,7 @@ struct SkinnyParams {
   int32_t rows, cols;          // output features of a CTA; tokens, rounded up to 16
   int32_t w_chunks, x_chunks;  // 64-row chunks of them
   int32_t kblocks, stages, w_mn, x_mn;
-  uint32_t tiles, split;       // feature tiles; shares of k (the CTAs of a cluster)
+  uint32_t tiles;
   uint32_t w_bytes, stage_bytes, smem, idesc, tmem_cols;
 };
 
@@ -82,7 +84,7 @@ cudaError_t skinny_run(const SkinnyParams &p, bool gated, cudaStream_t s);
 
 
 // One to a few tokens (dense_gemv.cu): A and B with unit stride along k, any row strides.
-constexpr int64_t kGemvMost = 16;
+constexpr int64_t kGemvMost = 64;
 
 struct GemvParams {
   const void *w[2], *x;
