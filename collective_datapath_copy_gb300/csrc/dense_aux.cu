@@ -142,8 +142,27 @@ __global__ void __launch_bounds__(256) join_kernel(const DenseJoin j) {
   if (c < j.n) join_column(j, c);
 }
 
-// A warp takes a row, a lane eight neighbouring elements: plain loads of single elements (the rows
-// start anywhere), one 16-byte store.
+// Eight elements that start at p, on any 2-byte boundary: the two aligned 16-byte words that hold
+// them, shifted.
+__device__ __forceinline__ uint4 shifted8(const uint16_t *p) {
+  const uint32_t off = (uint32_t)((uintptr_t)p & 15u), word = off >> 2, bits = (off & 2u) * 8u;
+  const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - off);
+  const uint4 a = q[0], b = q[1];
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (word & 2) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (word & 1) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// A warp takes a row, a lane eight neighbouring elements. Inside a row that is contiguous the
+// loads are 16-byte words (all of whose bytes are the row's); elsewhere single elements.
 __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ DensePack a) {
   griddep_launch();
   griddep_wait();
@@ -159,11 +178,17 @@ __global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ Dense
     for (int64_t q = q0 + lane; q < q1; q += 32) {
       const int64_t c = q * 8;
       const uint16_t *p = row + c * src.cs;
-      uint32_t v[8];
+      uint4 out;
+      if (src.cs == 1 && c >= 8 && c + 16 <= cols) {
+        out = shifted8(p);
+      } else {
+        uint32_t v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[i * src.cs] : 0u;
-      *reinterpret_cast<uint4 *>(a.dst[o] + r * ld + c) =
-          make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[i * src.cs] : 0u;
+        out = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
+                         v[6] | v[7] << 16);
+      }
+      *reinterpret_cast<uint4 *>(a.dst[o] + r * ld + c) = out;
     }
   }
 }

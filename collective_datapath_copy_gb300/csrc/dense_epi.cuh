@@ -314,29 +314,41 @@ __device__ __forceinline__ void staged_add(uint32_t *st, const void *p, int64_t 
     const float *q = static_cast<const float *>(p);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      const int c = lane & 15, r0 = lane >> 4;
+      const float *o = q + r0 * rs + (16 * h + c) * cs;
+      float w[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i, o += 2 * rs)
+        w[i] = r0 + 2 * i < rows && 16 * h + c < cols ? *o : 0.0f;
       __syncwarp();
-      const int c = lane & 15;
-      if (16 * h + c < cols)
-#pragma unroll 8
-        for (int r = lane >> 4; r < rows; r += 2)
-          st[r * kPitch + c] = __float_as_uint(q[r * rs + (16 * h + c) * cs]);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) st[(r0 + 2 * i) * kPitch + c] = __float_as_uint(w[i]);
       __syncwarp();
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[16 * h + i] += __uint_as_float(st[lane * kPitch + i]);
     }
     return;
   }
+  // all loads in flight before the first is used
   const uint16_t *q = static_cast<const uint16_t *>(p);
-  __syncwarp();
   if (cs == 1 && in_pairs(p, rs) && cols == 32) {
-#pragma unroll 8
-    for (int r = lane >> 4; r < rows; r += 2)
-      st[r * kPitch + (lane & 15)] =
-          *reinterpret_cast<const uint32_t *>(q + r * rs + 2 * (lane & 15));
-  } else if (lane < cols) {
-#pragma unroll 8
-    for (int r = 0; r < rows; ++r)
-      reinterpret_cast<uint16_t *>(st + r * kPitch)[lane] = q[r * rs + lane * cs];
+    uint32_t w[16];
+    const int r0 = lane >> 4;
+    const uint16_t *o = q + r0 * rs + 2 * (lane & 15);
+#pragma unroll
+    for (int i = 0; i < 16; ++i, o += 2 * rs)
+      w[i] = r0 + 2 * i < rows ? *reinterpret_cast<const uint32_t *>(o) : 0u;
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) st[(r0 + 2 * i) * kPitch + (lane & 15)] = w[i];
+  } else {
+    uint16_t w[32];
+    const uint16_t *o = q + lane * cs;
+#pragma unroll
+    for (int r = 0; r < 32; ++r, o += rs) w[r] = r < rows && lane < cols ? *o : (uint16_t)0;
+    __syncwarp();
+#pragma unroll
+    for (int r = 0; r < 32; ++r) reinterpret_cast<uint16_t *>(st + r * kPitch)[lane] = w[r];
   }
   __syncwarp();
   uint32_t w[16];

@@ -123,7 +123,10 @@ __global__ void __launch_bounds__(kMostWarps<NT> * 32, 1) gemv_kernel(const __gr
     for (int i = 0; i < AHEAD; ++i) {
       const int k = (s + i * warps) * kStep;
 #pragma unroll
-      for (int c = 0; c < NT; ++c) load16<ALIGN>(xt[c] + k, k + 16 * t, lx[c], x[i][c]);
+      for (int c = 0; c < NT; ++c) {
+        if (p.x_align >= ALIGN) load16<ALIGN>(xt[c] + k, k + 16 * t, lx[c], x[i][c]);
+        else load16<2>(xt[c] + k, k + 16 * t, lx[c], x[i][c]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
@@ -189,7 +192,8 @@ cudaError_t gemv_run(const DenseJob &j, cudaStream_t s) {
   p.k = j.k;
   p.x = j.a[0].p;
   p.x_ld = j.a[0].rs;
-  int align = row_align(p.x, j.m, p.x_ld, j.k);
+  p.x_align = row_align(p.x, j.m, p.x_ld, j.k);
+  int align = 32;
   for (int i = 0; i < (j.gated ? 2 : 1); ++i) {
     p.w[i] = j.b[i].p;
     p.ld[i] = j.b[i].rs;

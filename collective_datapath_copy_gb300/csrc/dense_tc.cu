@@ -434,6 +434,14 @@ cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStre
   return dense_launch(tc_kernel<GATED>, dim3(clusters * CG), kThreads, smem, CG, s, p);
 }
 
+// ns an output column of a tile (256 rows, two CTAs) takes in the epilogue
+int64_t epilogue_ns(const DenseJob &j, int split) {
+  if (split > 1) return j.gated ? 40 : 20;
+  const DenseEpi &e = j.e;
+  return 14 + (e.out_type == COLL_F32 ? 8 : 0) + (e.res ? 10 : 0) + (e.pre ? 8 : 0) +
+         (e.gate ? 16 : 0) + (e.act != COLL_ACT_NONE ? 18 : 0) + (e.vec ? 0 : 8);
+}
+
 int operands_a(const DenseJob &j) { return j.nbatch == 2 || j.nseg == 2 ? 2 : 1; }
 int operands_b(const DenseJob &j) { return j.gated || j.nseg == 2 ? 2 : 1; }
 
@@ -463,16 +471,22 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
   const int64_t clusters = kSms / CG;
   // Columns of each product's accumulator and shares of its k: those that end first. A tile takes
   // its k blocks times 62 ns and 1.08 a column (measured at 4096 x 4096 x 8192: 144 ns for 64
-  // columns, 186 for 128, 264 for 192, 339 for 256), and every cluster its tiles one after the
-  // other. Joining shares costs a launch and their way through L2.
-  int64_t tiles[2] = {0, 0}, time[2] = {1, 1}, joining[2] = {0, 0}, best = INT64_MAX;
+  // columns, 186 for 128, 264 for 192, 339 for 256) or the time of its epilogue beside the next
+  // tile's products, and every cluster its tiles one after the other; the last epilogue comes on
+  // top. An epilogue takes 14 ns a column, 10 more for a residual, 8 for each thing kept and 18 for
+  // an activation (8192 x 8192 x 64: 49 us plain, 85 with a residual, 160 with everything).
+  // Joining shares costs a launch and their way through L2.
+  int64_t tiles[2] = {0, 0}, time[2] = {1, 1}, joining[2] = {0, 0}, last[2] = {0, 0};
+  int64_t best = INT64_MAX;
   int cols[2] = {256, 256}, split[2] = {1, 1};
   auto measure = [&](int i, int bn, int sp) {
     const DenseJob &j = *jobs[i].j;
     tiles[i] =
         (int64_t)ceil_div(j.m, 128 * CG) * ceil_div(j.n, j.gated ? bn / 2 : bn) * j.nbatch * sp;
-    time[i] = (int64_t)ceil_div((int64_t)ceil_div(j.k, kTileK) * j.nseg, sp) * (62 + bn * 69 / 64) +
-              kTileNs;
+    const int64_t main = (int64_t)ceil_div((int64_t)ceil_div(j.k, kTileK) * j.nseg, sp) *
+                         (62 + bn * 69 / 64);
+    last[i] = bn * epilogue_ns(j, sp) / (j.gated ? 2 : 1);
+    time[i] = (main > last[i] ? main : last[i]) + kTileNs;
     joining[i] = sp > 1 ? kJoinNs + j.m * j.n * j.nbatch * (j.gated ? 2 : 1) * sp / 500 : 0;
   };
   auto even = [&]() { return (time[0] + time[1] / 2) / time[1]; };
@@ -485,7 +499,8 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
     if (count == 2) without += tiles[1] > early ? even() : ceil_div(tiles[1], clusters - extra);
     const int64_t t0 = extra ? (whole + 1) * time[0] + with * time[1] : 0;
     const int64_t t1 = whole * time[0] + without * time[1];
-    return (t0 > t1 ? t0 : t1) + (joining[0] > joining[1] ? joining[0] : joining[1]);
+    return (t0 > t1 ? t0 : t1) + last[count - 1] +
+           (joining[0] > joining[1] ? joining[0] : joining[1]);
   };
   auto keep = [&](int b0, int s0, int b1, int s1) {
     const int64_t t = makespan();

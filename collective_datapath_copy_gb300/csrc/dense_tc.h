@@ -92,6 +92,7 @@ struct GemvParams {
   DenseEpi e;
   int64_t m, n, k;
   uint32_t warps;
+  int32_t x_align;  // what the rows of x start on; the weights' is the kernel's
 };
 
 cudaError_t gemv_run(const DenseJob &j, cudaStream_t s);
