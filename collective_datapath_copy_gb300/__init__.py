@@ -20,4 +20,7 @@ def __getattr__(name):  # the dense operators need torch, which nothing above im
     if name in ("GatedFFN", "Linear"):
         from . import dense
         return getattr(dense, name)
+    if name == "TensorParallelMLP":
+        from . import mlp
+        return mlp.TensorParallelMLP
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
