@@ -40,7 +40,8 @@ struct DenseEpi {
 //   gated: g = A[0] B[0], u = A[0] B[1], one output
 struct DenseJob {
   int64_t m, n, k;
-  int32_t nseg, nbatch, gated, pad;
+  int32_t nseg, nbatch, gated;
+  int32_t forward;  // 0: a gradient, kept to one kernel whichever others are asked for
   DenseMat a[2], b[2];
   DenseEpi e;
   int32_t *status;

@@ -176,6 +176,105 @@ cudaError_t launch(const GemvParams &p, int align, cudaStream_t s) {
                      : launch<GATED, TYPE, 8>(p, align, s);
 }
 
+// ---- weights that lie the other way: stored as k rows of n
+//
+// The tokens are the 16 rows, the outputs the columns. A lane reads four neighbouring outputs of
+// four neighbouring rows of k and pairs the rows up with byte permutes; which output is which
+// column of which fragment is free, so those four serve four fragments, and the eight lanes of a
+// row of k read 64 neighbouring bytes. Rows of k in turn go to the warps, which join as above.
+
+constexpr int kFeat = 32;  // outputs of a CTA
+
+// Four elements from p, `left` of them there. ALIGN 8: all or none are, on 8 bytes.
+template <int ALIGN>
+__device__ __forceinline__ uint2 load4(const uint16_t *p, int left) {
+  if (ALIGN == 8) {
+    uint2 v = make_uint2(0u, 0u);
+    if (left > 0) v = __ldg(reinterpret_cast<const uint2 *>(p));
+    return v;
+  }
+  uint32_t v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = i < left ? __ldg(p + i) : 0u;
+  return make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
+}
+
+template <bool GATED, int TYPE, int ALIGN>
+__global__ void __launch_bounds__(GATED ? 256 : 512, 1) gemv_t_kernel(
+    const __grid_constant__ GemvTParams p) {
+  griddep_launch();
+  constexpr int W = GATED ? 2 : 1, WARPS = GATED ? 8 : 16, AHEAD = GATED ? 2 : 4;
+  __shared__ float part[WARPS][W][16][kFeat + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3, m = (int)p.m, len = (int)p.k;
+  const int64_t f0 = (int64_t)blockIdx.x * kFeat, fl = f0 + 4 * g;
+  const int left = (int)(p.n - fl < 4 ? p.n - fl : 4);  // outputs of this lane, may be negative
+  float acc[W][4][4] = {};
+  griddep_wait();
+  const int steps = (len + 15) / 16;
+  for (int s0 = warp; s0 < steps; s0 += AHEAD * warps) {
+    uint2 w[AHEAD][W][4], x[AHEAD][2];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int k = (s0 + i * warps) * 16 + 4 * t;
+#pragma unroll
+      for (int q = 0; q < W; ++q) {
+        const uint16_t *row = static_cast<const uint16_t *>(p.w[q]) + (int64_t)k * p.ld[q] + fl;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          w[i][q][r] = k + r < len && left > 0 ? load4<ALIGN>(row + r * p.ld[q], left)
+                                               : make_uint2(0u, 0u);
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int tok = g + 8 * h;
+        const uint16_t *row = static_cast<const uint16_t *>(p.x) + tok * p.x_ld + k;
+        x[i][h] = make_uint2(0u, 0u);
+        if (tok < m && k < len) {
+          if (p.x_align == 8) x[i][h] = __ldg(reinterpret_cast<const uint2 *>(row));
+          else x[i][h] = load4<2>(row, len - k < 4 ? len - k : 4);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int q = 0; q < W; ++q)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          // output j of the lane's four: rows k, k + 1 and k + 2, k + 3
+          const uint32_t sel = j & 1 ? 0x7632u : 0x5410u;
+          const uint2 *r = w[i][q];
+          const uint32_t b0 = j < 2 ? __byte_perm(r[0].x, r[1].x, sel)
+                                    : __byte_perm(r[0].y, r[1].y, sel);
+          const uint32_t b1 = j < 2 ? __byte_perm(r[2].x, r[3].x, sel)
+                                    : __byte_perm(r[2].y, r[3].y, sel);
+          mma16816<TYPE>(acc[q][j], x[i][0].x, x[i][1].x, x[i][0].y, x[i][1].y, b0, b1);
+        }
+  }
+#pragma unroll
+  for (int q = 0; q < W; ++q)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      // column c of fragment j is output 4 c + j
+      part[warp][q][g][8 * t + j] = acc[q][j][0];
+      part[warp][q][g][8 * t + 4 + j] = acc[q][j][1];
+      part[warp][q][g + 8][8 * t + j] = acc[q][j][2];
+      part[warp][q][g + 8][8 * t + 4 + j] = acc[q][j][3];
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < kFeat * m; i += blockDim.x) {
+    const int tok = i / kFeat, f = i % kFeat;
+    if (f0 + f >= p.n) continue;
+    float v = part[0][0][tok][f], u = GATED ? part[0][W - 1][tok][f] : 0.0f;
+    for (int c = 1; c < warps; ++c) {
+      v += part[c][0][tok][f];
+      if (GATED) u += part[c][W - 1][tok][f];
+    }
+    epilogue_one<GATED>(p.e, 0, tok, f0 + f, v, u, GATED ? 0.0f : bias_at(p.e, f0 + f));
+  }
+}
+
 // The widest access that every row of the matrix starts on.
 int row_align(const void *p, int64_t rows, int64_t ld, int64_t k) {
   const uint64_t bits = (uintptr_t)p | (rows > 1 ? (uint64_t)ld * 2 : 0) | (uint64_t)k * 2;
@@ -208,6 +307,40 @@ cudaError_t gemv_run(const DenseJob &j, cudaStream_t s) {
   if (j.e.type == COLL_BF16)
     return j.gated ? launch<true, COLL_BF16>(p, align, s) : launch<false, COLL_BF16>(p, align, s);
   return j.gated ? launch<true, COLL_F16>(p, align, s) : launch<false, COLL_F16>(p, align, s);
+}
+
+cudaError_t gemv_t_run(const DenseJob &j, cudaStream_t s) {
+  GemvTParams p = {};
+  p.e = j.e;
+  p.m = j.m;
+  p.n = j.n;
+  p.k = j.k;
+  p.x = j.a[0].p;
+  p.x_ld = j.a[0].rs;
+  // bits of what the four-element accesses start on
+  const uint64_t xb =
+      (uint64_t)j.k * 2 | (uintptr_t)p.x | (j.m > 1 ? (uint64_t)p.x_ld * 2 : 0);
+  uint64_t wb = (uint64_t)j.n * 2;
+  for (int i = 0; i < (j.gated ? 2 : 1); ++i) {
+    p.w[i] = j.b[i].p;
+    p.ld[i] = j.b[i].cs;
+    wb |= (uintptr_t)p.w[i] | (j.k > 1 ? (uint64_t)p.ld[i] * 2 : 0);
+  }
+  p.x_align = xb % 8 ? 2 : 8;
+  const int64_t steps = (j.k + 15) / 16;
+  // all the warps the sums have room for, no more than there are steps
+  unsigned warps = j.gated ? 8 : 16;
+  while (warps > 1 && warps > steps) warps /= 2;
+  const dim3 grid((unsigned)((j.n + kFeat - 1) / kFeat));
+  const bool bf = j.e.type == COLL_BF16, wide = wb % 8 == 0;
+  auto kernel =
+      j.gated ? (bf ? (wide ? gemv_t_kernel<true, COLL_BF16, 8> : gemv_t_kernel<true, COLL_BF16, 2>)
+                    : (wide ? gemv_t_kernel<true, COLL_F16, 8> : gemv_t_kernel<true, COLL_F16, 2>))
+              : (bf ? (wide ? gemv_t_kernel<false, COLL_BF16, 8>
+                            : gemv_t_kernel<false, COLL_BF16, 2>)
+                    : (wide ? gemv_t_kernel<false, COLL_F16, 8>
+                            : gemv_t_kernel<false, COLL_F16, 2>));
+  return dense_launch(kernel, grid, 32 * warps, 0, 1, s, p);
 }
 
 }  // namespace coll

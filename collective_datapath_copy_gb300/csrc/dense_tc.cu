@@ -176,8 +176,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     auto segment = [&](auto amn_c, auto bmn_c, const TcProb &q, const CUtensorMap *ma,
                        const CUtensorMap *mb, int32_t m, int32_t n, int32_t k, int32_t end) {
       constexpr bool amn = decltype(amn_c)::value, bmn = decltype(bmn_c)::value;
-      // bytes a stage receives, boxes past the edges counted whole
-      const uint32_t bytes = CG * (kABytes + (bmn ? q.b_chunks * kChunk : q.b_rows * 128u));
+      // bytes a stage receives, boxes past the edges counted whole; the second CTA's rows may be
+      // past the last
+      const uint32_t rows = amn ? kABytes : q.a_rows * 128u;
+      const bool second = tl.m0 + 128 < q.m, mine = leader || second;
+      const uint32_t bytes =
+          rows + (second ? rows : 0u) + CG * (bmn ? q.b_chunks * kChunk : q.b_rows * 128u);
       const int32_t chunks = q.b_chunks;
       for (; k < end; k += kTileK) {
         ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
@@ -185,10 +189,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           const uint32_t bar = arrive0 + 8 * s;
           if (leader) bar_expect(full0 + 8 * s, bytes);
           const uint32_t da = ring + s * stage_bytes, db = da + kABytes;
-          if (amn) {
+          if (amn && mine) {
             tma_box_pair(da, ma, m, k, bar);
             tma_box_pair(da + kChunk, ma, m + 64, k, bar);
-          } else {
+          } else if (mine) {
             tma_box_pair(da, ma, k, m, bar);
           }
           if (bmn) {
@@ -543,6 +547,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
     q.split = split[i];
     q.kblocks = (int32_t)ceil_div(j.k, kTileK);
     q.tiles_m = ceil_div(j.m, 128 * CG);
+    q.a_rows = j.m < 128 ? (int32_t)((j.m + 7) / 8 * 8) : 128;
     q.b_rows = cols[i] / CG;
     q.tile_cols = j.gated ? cols[i] / 2 : cols[i];
     q.b_chunks = (q.b_rows + 63) / 64;
@@ -577,7 +582,7 @@ int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s) {
     const DenseJob &j = *jobs[i].j;
     TcProb &q = p.prob[i];
     for (int x = 0; x < operands_a(j); ++x) {
-      const int c = tc_encode(&q.a[x], jobs[i].a[x], j.e.type, 128);
+      const int c = tc_encode(&q.a[x], jobs[i].a[x], j.e.type, (uint32_t)q.a_rows);
       if (c) return c;
     }
     for (int x = 0; x < operands_b(j); ++x) {

@@ -18,6 +18,7 @@ struct TcProb {
   int64_t m, n;
   uint32_t tiles_m, tiles_n, tiles;
   int32_t tile_cols;         // of the output
+  int32_t a_rows;            // rows of A a CTA loads: 128, or all there are
   int32_t b_rows, b_chunks;  // rows of B per CTA and operand, and 64-row chunks of them
   int32_t kblocks, nseg, nbatch;
   int32_t split;             // shares of k, each with its own tiles
@@ -96,5 +97,18 @@ struct GemvParams {
 };
 
 cudaError_t gemv_run(const DenseJob &j, cudaStream_t s);
+
+// The same with B's rows contiguous instead, up to 16 tokens.
+constexpr int64_t kGemvTMost = 16;
+
+struct GemvTParams {
+  const void *w[2], *x;
+  int64_t ld[2], x_ld;
+  DenseEpi e;
+  int64_t m, n, k;
+  int32_t x_align;
+};
+
+cudaError_t gemv_t_run(const DenseJob &j, cudaStream_t s);
 
 }  // namespace coll

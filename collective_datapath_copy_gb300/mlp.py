@@ -73,7 +73,8 @@ class TensorParallelMLP:
         return [t.view(torch.int16) if t.dtype is torch.bfloat16 else t for t in ts]
 
     def forward(self, x, residual=None, keep=False):
-        """x [tokens, K] -> y, one tensor per rank, all equal. residual is added once, by rank 0's
+        """x [tokens, K] -> y, one tensor per rank, all equal (the object's buffers, overwritten by
+        the next call). residual is added once, by rank 0's
         epilogue; its gradient is dy. keep: what backward needs."""
         kept = []
         for r in range(self.R):
@@ -91,7 +92,7 @@ class TensorParallelMLP:
         return self._y
 
     def backward(self, dy):
-        """dx, one tensor per rank, and (dw_gate_r, dw_up_r, dw_down_r) of every rank's shards, for
+        """dx, one tensor per rank (the object's buffers), and (dw_gate_r, dw_up_r, dw_down_r) of every rank's shards, for
         the last forward(keep=True)."""
         if self._kept is None:
             raise RuntimeError("backward needs forward(keep=True) before it")
