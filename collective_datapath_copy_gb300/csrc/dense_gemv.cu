@@ -27,11 +27,35 @@ constexpr int kStep = 64;      // elements of k a warp takes at a time
 template <int NT>
 constexpr int kMostWarps = NT == 8 ? 8 : 16;
 
+// Plain loads that stay behind the wait for the predecessor; not the read-only path, whose data
+// may not change while the kernel runs, and this one starts before its predecessor has finished.
 __device__ __forceinline__ void ld_stream32(const void *p, uint32_t (&r)[8]) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+  asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
                  "=r"(r[6]), "=r"(r[7])
                : "l"(p));
+}
+__device__ __forceinline__ uint4 ld_word16(const void *p) {
+  uint4 v;
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint2 ld_word8(const void *p) {
+  uint2 v;
+  asm volatile("ld.global.v2.b32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_word4(const void *p) {
+  uint32_t v;
+  asm volatile("ld.global.b32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint32_t ld_word2(const void *p) {
+  uint16_t v;
+  asm volatile("ld.global.b16 %0, [%1];" : "=h"(v) : "l"(p));
+  return v;
 }
 
 // 16 elements from p (element k of its row of `len`), zeros past the row's end. ALIGN: bytes that
@@ -49,18 +73,18 @@ __device__ __forceinline__ void load16(const uint16_t *p, int k, int len, uint32
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint4 v = make_uint4(0u, 0u, 0u, 0u);
-      if (k + 8 * h < len) v = __ldg(reinterpret_cast<const uint4 *>(p) + h);
+      if (k + 8 * h < len) v = ld_word16(p + 8 * h);
       r[4 * h] = v.x, r[4 * h + 1] = v.y, r[4 * h + 2] = v.z, r[4 * h + 3] = v.w;
     }
   } else if (ALIGN == 4) {  // len is even
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      r[i] = k + 2 * i < len ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
+      r[i] = k + 2 * i < len ? ld_word4(p + 2 * i) : 0u;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint32_t lo = k + 2 * i < len ? __ldg(p + 2 * i) : 0u;
-      const uint32_t hi = k + 2 * i + 1 < len ? __ldg(p + 2 * i + 1) : 0u;
+      const uint32_t lo = k + 2 * i < len ? ld_word2(p + 2 * i) : 0u;
+      const uint32_t hi = k + 2 * i + 1 < len ? ld_word2(p + 2 * i + 1) : 0u;
       r[i] = lo | hi << 16;
     }
   }
@@ -190,12 +214,12 @@ template <int ALIGN>
 __device__ __forceinline__ uint2 load4(const uint16_t *p, int left) {
   if (ALIGN == 8) {
     uint2 v = make_uint2(0u, 0u);
-    if (left > 0) v = __ldg(reinterpret_cast<const uint2 *>(p));
+    if (left > 0) v = ld_word8(p);
     return v;
   }
   uint32_t v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = i < left ? __ldg(p + i) : 0u;
+  for (int i = 0; i < 4; ++i) v[i] = i < left ? ld_word2(p + i) : 0u;
   return make_uint2(v[0] | v[1] << 16, v[2] | v[3] << 16);
 }
 
@@ -231,7 +255,7 @@ __global__ void __launch_bounds__(GATED ? 256 : 512, 1) gemv_t_kernel(
         const uint16_t *row = static_cast<const uint16_t *>(p.x) + tok * p.x_ld + k;
         x[i][h] = make_uint2(0u, 0u);
         if (tok < m && k < len) {
-          if (p.x_align == 8) x[i][h] = __ldg(reinterpret_cast<const uint2 *>(row));
+          if (p.x_align == 8) x[i][h] = ld_word8(row);
           else x[i][h] = load4<2>(row, len - k < 4 ? len - k : 4);
         }
       }

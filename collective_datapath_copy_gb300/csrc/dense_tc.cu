@@ -176,12 +176,12 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     auto segment = [&](auto amn_c, auto bmn_c, const TcProb &q, const CUtensorMap *ma,
                        const CUtensorMap *mb, int32_t m, int32_t n, int32_t k, int32_t end) {
       constexpr bool amn = decltype(amn_c)::value, bmn = decltype(bmn_c)::value;
-      // bytes a stage receives, boxes past the edges counted whole; the second CTA's rows may be
-      // past the last
+      // bytes a stage receives, boxes past the edges counted whole; the second CTA's rows of
+      // A may all be past the last
       const uint32_t rows = amn ? kABytes : q.a_rows * 128u;
       const bool second = tl.m0 + 128 < q.m, mine = leader || second;
-      const uint32_t bytes =
-          rows + (second ? rows : 0u) + CG * (bmn ? q.b_chunks * kChunk : q.b_rows * 128u);
+      const uint32_t cols = bmn ? q.b_chunks * kChunk : q.b_box * 128u;
+      const uint32_t bytes = rows + (second ? rows : 0u) + CG * cols;
       const int32_t chunks = q.b_chunks;
       for (; k < end; k += kTileK) {
         ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
@@ -189,11 +189,13 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           const uint32_t bar = arrive0 + 8 * s;
           if (leader) bar_expect(full0 + 8 * s, bytes);
           const uint32_t da = ring + s * stage_bytes, db = da + kABytes;
-          if (amn && mine) {
-            tma_box_pair(da, ma, m, k, bar);
-            tma_box_pair(da + kChunk, ma, m + 64, k, bar);
-          } else if (mine) {
-            tma_box_pair(da, ma, k, m, bar);
+          if (mine) {
+            if (amn) {
+              tma_box_pair(da, ma, m, k, bar);
+              tma_box_pair(da + kChunk, ma, m + 64, k, bar);
+            } else {
+              tma_box_pair(da, ma, k, m, bar);
+            }
           }
           if (bmn) {
             tma_box_pair(db, mb, n, k, bar);
@@ -481,6 +483,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
   // an activation (8192 x 8192 x 64: 49 us plain, 85 with a residual, 160 with everything).
   // Joining shares costs a launch and their way through L2.
   int64_t tiles[2] = {0, 0}, time[2] = {1, 1}, joining[2] = {0, 0}, last[2] = {0, 0};
+  int64_t first = 0;  // what the first tile's products do not wait for: an epilogue before them
   int64_t best = INT64_MAX;
   int cols[2] = {256, 256}, split[2] = {1, 1};
   auto measure = [&](int i, int bn, int sp) {
@@ -491,6 +494,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
                          (62 + bn * 69 / 64);
     last[i] = bn * epilogue_ns(j, sp) / (j.gated ? 2 : 1);
     time[i] = (main > last[i] ? main : last[i]) + kTileNs;
+    if (i == 0) first = main > last[0] ? 0 : last[0] - main;
     joining[i] = sp > 1 ? kJoinNs + j.m * j.n * j.nbatch * (j.gated ? 2 : 1) * sp / 500 : 0;
   };
   auto even = [&]() { return (time[0] + time[1] / 2) / time[1]; };
@@ -503,7 +507,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
     if (count == 2) without += tiles[1] > early ? even() : ceil_div(tiles[1], clusters - extra);
     const int64_t t0 = extra ? (whole + 1) * time[0] + with * time[1] : 0;
     const int64_t t1 = whole * time[0] + without * time[1];
-    return (t0 > t1 ? t0 : t1) + last[count - 1] +
+    return (t0 > t1 ? t0 : t1) - first + last[count - 1] +
            (joining[0] > joining[1] ? joining[0] : joining[1]);
   };
   auto keep = [&](int b0, int s0, int b1, int s1) {
@@ -550,6 +554,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
     q.a_rows = j.m < 128 ? (int32_t)((j.m + 7) / 8 * 8) : 128;
     q.b_rows = cols[i] / CG;
     q.tile_cols = j.gated ? cols[i] / 2 : cols[i];
+    q.b_box = j.n < q.b_rows ? (int32_t)((j.n + 7) / 8 * 8) : q.b_rows;
     q.b_chunks = (q.b_rows + 63) / 64;
     q.tiles_n = ceil_div(j.n, q.tile_cols);
     q.tiles = (uint32_t)tiles[i];
@@ -586,7 +591,7 @@ int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s) {
       if (c) return c;
     }
     for (int x = 0; x < operands_b(j); ++x) {
-      const int c = tc_encode(&q.b[x], jobs[i].b[x], j.e.type, (uint32_t)q.b_rows);
+      const int c = tc_encode(&q.b[x], jobs[i].b[x], j.e.type, (uint32_t)q.b_box);
       if (c) return c;
     }
     join.split[i] = q.split;

@@ -20,6 +20,7 @@ struct TcProb {
   int32_t tile_cols;         // of the output
   int32_t a_rows;            // rows of A a CTA loads: 128, or all there are
   int32_t b_rows, b_chunks;  // rows of B per CTA and operand, and 64-row chunks of them
+  int32_t b_box;             // rows of B a CTA loads (k contiguous): b_rows, or all there are
   int32_t kblocks, nseg, nbatch;
   int32_t split;             // shares of k, each with its own tiles
   float *part;               // split > 1: their sums, [share][batch][gate, up][m][part_ld]

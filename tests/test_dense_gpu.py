@@ -339,6 +339,73 @@ def test_long_sums_backward(i, size):
             ref.assert_close(o, q, what)
 
 
+# a small batch against many outputs: the weights' rows are the wide side
+@pytest.mark.parametrize("m,n,k", [(17, 9728, 72), (33, 9800, 200), (48, 10003, 136),
+                                   (64, 12296, 328), (50, 9984, 1000)])
+@pytest.mark.parametrize("layouts", [("rows", "rows"), ("slice3", "cols"), ("cols", "slice8")])
+def test_wide_outputs_for_a_small_batch(m, n, k, layouts):
+    for dtype, act, i in ((BF, "gelu", 0), (HF, "silu", 1)):
+        g = gen(m + i)
+        x = rnd(g, m, k, dtype, 1.0, layouts[0])
+        w, w2 = (rnd(g, n, k, dtype, k ** -0.5, layouts[1]) for _ in range(2))
+        b, r = rnd(g, 1, n, dtype)[0], rnd(g, m, n, dtype)
+        y, p = Out(m, n, dtype, 3, 1), Out(m, n, dtype, aligned(n), 0)
+        lin = cdc.Linear(w, b, act)
+        lin.forward(x, residual=r, out=y.v, pre=p.v)
+        want, pre = ref.linear(x, w, b, r, act, dtype, dtype)
+        ref.assert_close(y.v, want, "y")
+        ref.assert_close(p.v, pre, "pre")
+        ref.assert_rms(p.v, pre, dtype, "pre")
+        f = lin.forward(x, residual=r.float(), out_dtype=F32)
+        ref.assert_close(f, ref.linear(x, w, b, r, act, F32, dtype)[0], "f32")
+        h, gate, up = (Out(m, n, dtype, 1, 1) for _ in range(3))
+        ffn = cdc.GatedFFN(w, w2, act)
+        ffn.forward(x, out=h.v, gate=gate.v, up=up.v)
+        for o, q, what in zip((h, gate, up), ref.gated(x, w, w2, act, dtype), ("h", "gate", "up")):
+            ref.assert_close(o.v, q, what)
+            assert o.untouched()
+        assert y.untouched() and p.untouched()
+        assert lin.status() == _lib.OK and ffn.status() == _lib.OK
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 96, 128), (3, 100, 1024), (9, 264, 300), (16, 33, 77)])
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_few_tokens_over_transposed_weights(m, n, k, dtype):
+    g = gen(m)
+    for layout in ("cols", "cols3"):
+        x = rnd(g, m, k, dtype, 1.0, "rows" if layout == "cols" else "slice3")
+        w, w2 = (rnd(g, n, k, dtype, k ** -0.5, layout) for _ in range(2))
+        r = rnd(g, m, n, dtype)
+        y, h = Out(m, n, dtype, 1, 1), Out(m, n, dtype, 1, 1)
+        cdc.Linear(w, None, "relu").forward(x, residual=r, out=y.v)
+        ref.assert_close(y.v, ref.linear(x, w, None, r, "relu", dtype, dtype)[0])
+        cdc.GatedFFN(w, w2, "sigmoid").forward(x, out=h.v)
+        ref.assert_close(h.v, ref.gated(x, w, w2, "sigmoid", dtype)[0])
+        assert y.untouched() and h.untouched()
+
+
+def test_offsets_beyond_32_bits():
+    """More than 2^32 bytes and 2^31 elements in the output and in the gradient's scratch."""
+    m, n, k = 66000, 33000, 40
+    g = gen(2)
+    x, w = rnd(g, m, k, BF), rnd(g, n, k, BF, k ** -0.5)
+    lin = cdc.Linear(w, None, "relu")
+    y, z = lin.forward(x, save=True)
+    rows = torch.tensor([0, 1, 32537, 32538, 65000, m - 1], device="cuda")
+    want, pre = ref.linear(x[rows], w, None, None, "relu", BF, BF)
+    ref.assert_close(y[rows], want)
+    ref.assert_close(z[rows], pre)
+    del y
+    dy = rnd(g, 1, n, BF).expand(m, n)
+    dx, dw, _ = lin.backward(dy, x, pre=z)
+    rdx = ref.linear_bwd(dy[rows], z[rows], x[rows], w, "relu", BF, BF)[0]
+    ref.assert_close(dx[rows], rdx)
+    cols = torch.tensor([0, 7, n - 1], device="cuda")
+    rdw = ref.linear_bwd(dy[:, cols], z[:, cols], x, w[cols], "relu", BF, BF)[1]
+    ref.assert_close(dw[cols], rdw)
+    torch.cuda.empty_cache()
+
+
 @pytest.mark.parametrize("m,n,k", [(0, 40, 64), (5, 0, 64), (5, 40, 0), (0, 0, 0), (200, 300, 0)])
 def test_empty_axes(m, n, k):
     """No tokens, no outputs, nothing to sum over: zeros, the bias and the residual remain."""
