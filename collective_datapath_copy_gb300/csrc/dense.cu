@@ -17,6 +17,10 @@ using coll::TcOperand;
 struct Ws {
   char *base;
   uint64_t used;
+  // shapes of the tensor-core launch: the counting pass leaves them for the launching one
+  coll::TcParams *plan;
+  bool planned;
+  uint64_t part[2];
   void *take(uint64_t bytes) {
     const uint64_t at = used;
     used += (bytes + 255) & ~(uint64_t)255;
@@ -264,13 +268,15 @@ int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
   }
   const bool skinny = n == 1 && todo[0].j->forward && todo[0].j->m <= coll::kSkinnyMost &&
                       todo[0].j->n >= coll::kSkinnyLeast;
-  coll::TcParams p;
+  coll::TcParams &p = *ws.plan;
   if (n && !skinny) {
-    uint64_t bytes[2];
-    const int c = coll::tc_plan(p, todo, n, bytes);
-    if (c) return c;
+    if (!ws.planned) {
+      const int c = coll::tc_plan(p, todo, n, ws.part);
+      if (c) return c;
+      ws.planned = true;
+    }
     for (int i = 0; i < n; ++i)
-      if (bytes[i]) p.prob[i].part = static_cast<float *>(ws.take(bytes[i]));
+      if (ws.part[i]) p.prob[i].part = static_cast<float *>(ws.take(ws.part[i]));
   }
   if (dry) return COLL_OK;
   if (pack.count && coll::dense_pack(pack, s) != cudaSuccess) return COLL_ECUDA;
@@ -495,26 +501,37 @@ int run(const coll_gated_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
   return products(jobs, n, ws, dry, s);
 }
 
+// Checks, then the counting pass: workspace bytes, or a code.
 template <typename T>
-int64_t workspace(const T *a) {
+int64_t count(const T *a, Ws &ws) {
   if (!a) return COLL_EINVAL;
   const int c = check(*a);
   if (c) return c;
-  Ws ws = {};
   const int r = run(*a, ws, true, nullptr);
   return r ? r : ws.used ? (int64_t)ws.used + 128 : 0;  // room to start on 128 bytes
 }
 
 template <typename T>
-int call(const T *a, void *stream) {
-  const int64_t need = workspace(a);
-  if (need < 0) return (int)need;
+int64_t workspace(const T *a) {
+  coll::TcParams plan;
   Ws ws = {};
+  ws.plan = &plan;
+  return count(a, ws);
+}
+
+template <typename T>
+int call(const T *a, void *stream) {
+  coll::TcParams plan;
+  Ws ws = {};
+  ws.plan = &plan;
+  const int64_t need = count(a, ws);
+  if (need < 0) return (int)need;
   if (need > 0) {
     if (!a->workspace || ((uintptr_t)a->workspace & 15u) || a->workspace_bytes < (uint64_t)need)
       return COLL_EWORKSPACE;
     ws.base = reinterpret_cast<char *>(((uintptr_t)a->workspace + 127) & ~(uintptr_t)127);
   }
+  ws.used = 0;
   return run(*a, ws, false, static_cast<cudaStream_t>(stream));
 }
 

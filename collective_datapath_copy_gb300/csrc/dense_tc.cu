@@ -36,8 +36,8 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
-constexpr int64_t kTileNs = 600;          // of a tile beside its k blocks
-constexpr int64_t kJoinNs = 2500;         // of joining shares, beside their bytes
+constexpr float kTileNs = 600.0f;          // of a tile beside its k blocks
+constexpr float kJoinNs = 2500.0f;         // of joining shares, beside their bytes
 constexpr int kMostShares = 16;
 
 constexpr int CG = 2;                     // CTAs of a tile (cta_group::2)
@@ -474,95 +474,114 @@ int tc_encode(CUtensorMap *map, const TcOperand &o, int64_t type, uint32_t rows)
 
 int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]) {
   memset(&p, 0, sizeof(p));
-  const int64_t clusters = kSms / CG;
+  constexpr uint32_t clusters = kSms / CG;
   // Columns of each product's accumulator and shares of its k: those that end first. A tile takes
   // its k blocks times 62 ns and 1.08 a column (measured at 4096 x 4096 x 8192: 144 ns for 64
   // columns, 186 for 128, 264 for 192, 339 for 256) or the time of its epilogue beside the next
   // tile's products, and every cluster its tiles one after the other; the last epilogue comes on
   // top. An epilogue takes 14 ns a column, 10 more for a residual, 8 for each thing kept and 18 for
   // an activation (8192 x 8192 x 64: 49 us plain, 85 with a residual, 160 with everything).
-  // Joining shares costs a launch and their way through L2.
-  int64_t tiles[2] = {0, 0}, time[2] = {1, 1}, joining[2] = {0, 0}, last[2] = {0, 0};
-  int64_t first = 0;  // what the first tile's products do not wait for: an epilogue before them
-  int64_t best = INT64_MAX;
-  int cols[2] = {256, 256}, split[2] = {1, 1};
-  auto measure = [&](int i, int bn, int sp) {
+  // Joining shares costs a launch and their way through L2. Calls of a few us wait for this, so it
+  // tries no more than it has to.
+  struct Option {
+    int cols, split;
+    uint32_t tiles;
+    float main, last, join;  // ns: a tile's products, its epilogue; joining shares
+    float time() const { return (main > last ? main : last) + kTileNs; }
+  };
+  auto option = [&](int i, int bn, int sp) {
     const DenseJob &j = *jobs[i].j;
-    tiles[i] =
+    Option o = {bn, sp, 0, 0.0f, 0.0f, 0.0f};
+    const int64_t tiles =
         (int64_t)ceil_div(j.m, 128 * CG) * ceil_div(j.n, j.gated ? bn / 2 : bn) * j.nbatch * sp;
-    const int64_t main = (int64_t)ceil_div((int64_t)ceil_div(j.k, kTileK) * j.nseg, sp) *
-                         (62 + bn * 69 / 64);
-    last[i] = bn * epilogue_ns(j, sp) / (j.gated ? 2 : 1);
-    time[i] = (main > last[i] ? main : last[i]) + kTileNs;
-    if (i == 0) first = main > last[0] ? 0 : last[0] - main;
-    joining[i] = sp > 1 ? kJoinNs + j.m * j.n * j.nbatch * (j.gated ? 2 : 1) * sp / 500 : 0;
+    o.tiles = tiles > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)tiles;
+    o.main = (float)ceil_div((int64_t)ceil_div(j.k, kTileK) * j.nseg, sp) * (62.0f + 1.08f * bn);
+    o.last = (float)(bn * epilogue_ns(j, sp) / (j.gated ? 2 : 1));
+    if (sp > 1)
+      o.join = kJoinNs + (float)j.m * (float)j.n * (float)(j.nbatch * (j.gated ? 2 : 1) * sp) / 500.0f;
+    return o;
   };
-  auto even = [&]() { return (time[0] + time[1] / 2) / time[1]; };
+  auto even = [&](const Option &o, const Option &q) {
+    return (uint32_t)(o.time() / q.time() + 0.5f);
+  };
   // the busiest cluster: of those with one tile of the first product more, or of the others
-  auto makespan = [&]() {
-    const int64_t whole = tiles[0] / clusters, extra = tiles[0] % clusters;
-    const int64_t early = count == 2 ? even() * (clusters - extra) : 0;
-    int64_t with = 0, without = 0;
-    if (tiles[1] > early) with = without = (tiles[1] - early + clusters - 1) / clusters;
-    if (count == 2) without += tiles[1] > early ? even() : ceil_div(tiles[1], clusters - extra);
-    const int64_t t0 = extra ? (whole + 1) * time[0] + with * time[1] : 0;
-    const int64_t t1 = whole * time[0] + without * time[1];
-    return (t0 > t1 ? t0 : t1) - first + last[count - 1] +
-           (joining[0] > joining[1] ? joining[0] : joining[1]);
-  };
-  auto keep = [&](int b0, int s0, int b1, int s1) {
-    const int64_t t = makespan();
-    if (t >= best) return;
-    best = t;
-    cols[0] = b0, cols[1] = b1;
-    split[0] = s0, split[1] = s1;
-  };
-  for (int b0 = 256; b0 >= 64; b0 -= jobs[0].j->gated ? 64 : 32) {
-    measure(0, b0, 1);
-    for (int b1 = 256; b1 >= (count == 2 ? 64 : 256); b1 -= 32) {
-      if (count == 2) measure(1, b1, 1);
-      keep(b0, 1, b1, 1);
+  auto makespan = [&](const Option &o, const Option *q) {
+    const uint32_t whole = o.tiles / clusters, extra = o.tiles % clusters;
+    float with = (float)(whole + 1), t = o.time(), end = o.last, join = o.join;
+    float without = (float)whole * t;
+    with *= t;
+    if (q) {
+      const uint32_t e = even(o, *q), early = e * (clusters - extra);
+      if (q->tiles > early) {
+        const float more = (float)((q->tiles - early + clusters - 1) / clusters);
+        with += more * q->time();
+        without += (more + (float)e) * q->time();
+      } else {
+        without += (float)((q->tiles + clusters - extra - 1) / (clusters - extra)) * q->time();
+      }
+      end = q->last;
+      join = join > q->join ? join : q->join;
     }
+    const float busy = extra && with > without ? with : without;
+    // nothing waits for an epilogue before the first tile's products
+    return busy - (o.last > o.main ? o.last - o.main : 0.0f) + end + join;
+  };
+  Option best[2];
+  float least = 3.0e38f;
+  auto keep = [&](const Option &o, const Option *q) {
+    const float t = makespan(o, q);
+    if (t >= least) return;
+    least = t;
+    best[0] = o;
+    if (q) best[1] = *q;
+  };
+  Option second[7];
+  if (count == 2)
+    for (int x = 0; x < 7; ++x) second[x] = option(1, 256 - 32 * x, 1);
+  for (int bn = 256; bn >= 64; bn -= jobs[0].j->gated ? 64 : 32) {
+    const Option o = option(0, bn, 1);
+    if (count == 1) keep(o, nullptr);
+    else
+      for (const Option &q : second) keep(o, &q);
   }
-  // shares of k, where a tile takes longer than a fair part of everything
+  // shares of k, where a tile takes a good part of the whole time
   for (int i = 0; i < count; ++i) {
-    const int other = 1 - i, other_cols = cols[other], other_split = split[other];
-    if (count == 2) measure(other, other_cols, other_split);
+    if (best[i].main * 2 < least) continue;
+    const Option other = best[1 - i < count ? 1 - i : i];
     const int64_t blocks = (int64_t)ceil_div(jobs[i].j->k, kTileK) * jobs[i].j->nseg;
     for (int bn = 256; bn >= 64; bn -= 64)
       for (int sp = 2; sp <= kMostShares && blocks >= 4 * sp; sp += sp < 4 ? 1 : sp < 8 ? 2 : 4) {
-        measure(i, bn, sp);
-        if (tiles[i] > 4 * clusters) break;
-        if (i == 0) keep(bn, sp, other_cols, other_split);
-        else keep(other_cols, other_split, bn, sp);
+        const Option o = option(i, bn, sp);
+        if (o.tiles > 4 * clusters) break;
+        if (count == 1) keep(o, nullptr);
+        else if (i == 0) keep(o, &other);
+        else keep(other, &o);
       }
   }
   p.status = jobs[0].j->status;
   for (int i = 0; i < count; ++i) {
     const DenseJob &j = *jobs[i].j;
     TcProb &q = p.prob[i];
-    measure(i, cols[i], split[i]);
-    if (tiles[i] > 0x7FFFFFFF) return COLL_EINVAL;
-    q.e = j.e;
+    const int cols = best[i].cols, split = best[i].split;
+    if (best[i].tiles == 0x7FFFFFFFu) return COLL_EINVAL;
     q.m = j.m;
     q.n = j.n;
     q.nseg = j.nseg;
     q.nbatch = j.nbatch;
-    q.split = split[i];
+    q.split = split;
     q.kblocks = (int32_t)ceil_div(j.k, kTileK);
     q.tiles_m = ceil_div(j.m, 128 * CG);
     q.a_rows = j.m < 128 ? (int32_t)((j.m + 7) / 8 * 8) : 128;
-    q.b_rows = cols[i] / CG;
-    q.tile_cols = j.gated ? cols[i] / 2 : cols[i];
+    q.b_rows = cols / CG;
+    q.tile_cols = j.gated ? cols / 2 : cols;
     q.b_box = j.n < q.b_rows ? (int32_t)((j.n + 7) / 8 * 8) : q.b_rows;
     q.b_chunks = (q.b_rows + 63) / 64;
     q.tiles_n = ceil_div(j.n, q.tile_cols);
-    q.tiles = (uint32_t)tiles[i];
-    q.idesc = mma_desc(j.e.type == COLL_BF16, false, false, 128 * CG, (uint32_t)cols[i]);
+    q.tiles = best[i].tiles;
+    q.idesc = mma_desc(j.e.type == COLL_BF16, false, false, 128 * CG, (uint32_t)cols);
     q.part_ld = (j.n + 31) / 32 * 32;
-    part_bytes[i] = split[i] > 1 ? (uint64_t)split[i] * j.nbatch * (j.gated ? 2 : 1) * j.m *
-                                       q.part_ld * 4
-                                 : 0;
+    part_bytes[i] =
+        split > 1 ? (uint64_t)split * j.nbatch * (j.gated ? 2 : 1) * j.m * q.part_ld * 4 : 0;
     bool bmn = false;
     for (int x = 0; x < 2; ++x) {
       q.a_mn[x] = jobs[i].a[x].mn;
@@ -574,7 +593,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
     if (bytes > p.stage_bytes) p.stage_bytes = bytes;
   }
   for (int i = count; i < 2; ++i) part_bytes[i] = 0;
-  p.even = count == 2 && tiles[0] % clusters ? (uint32_t)even() : 0;
+  p.even = count == 2 && best[0].tiles % clusters ? even(best[0], best[1]) : 0;
   p.stages = (kTcSmem - 1024 - kStageOut) / p.stage_bytes;
   if (p.stages > (uint32_t)kMaxStages) p.stages = kMaxStages;
   return COLL_OK;
@@ -586,6 +605,7 @@ int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s) {
   for (int i = 0; i < count; ++i) {
     const DenseJob &j = *jobs[i].j;
     TcProb &q = p.prob[i];
+    q.e = j.e;
     for (int x = 0; x < operands_a(j); ++x) {
       const int c = tc_encode(&q.a[x], jobs[i].a[x], j.e.type, (uint32_t)q.a_rows);
       if (c) return c;
