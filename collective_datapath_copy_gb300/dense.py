@@ -18,6 +18,7 @@ stride. The operators record nothing for autograd: the backward calls are explic
 from __future__ import annotations
 
 import contextlib
+import math
 import struct
 
 import torch
@@ -64,39 +65,49 @@ def _weight(name, w):
     return w
 
 
-def _rows(t, cols, dtype, device, what):
-    """An input as a matrix of `cols` columns (leading dimensions flattened)."""
+def _read(t, m, cols, dtype, dev, what, keep):
+    """An input's address and strides as a matrix of `cols` columns (leading dimensions flattened)
+    and m rows (any where m is None). What has to be copied for that lives in `keep`."""
+    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 2 and t.size(1) == cols
+            and (m is None or t.size(0) == m)):
+        return (t.data_ptr(), *t.stride())
     if t.dtype is not dtype:
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the weights are on {device}")
-    s = t.shape
-    if len(s) == 0 or s[-1] != cols:
-        raise ValueError(f"{what} has shape {tuple(s)}, expected {cols} columns")
-    if len(s) == 2:
-        return t
-    m = 1
-    for d in s[:-1]:
-        m *= d
-    return t.reshape(m, cols)
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the weights are on cuda:{dev}")
+    if t.dim() == 0 or t.shape[-1] != cols:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {cols} columns")
+    rows = math.prod(t.shape[:-1])
+    if m is not None and rows != m:
+        raise ValueError(f"{what} has {rows} rows, x has {m}")
+    t = t.reshape(rows, cols)
+    keep.append(t)
+    return (t.data_ptr(), *t.stride())
 
 
-def _dest(t, m, cols, dtypes, device, what):
-    """An output the caller passed, as a matrix; never a copy."""
-    if t.dtype not in dtypes:
-        raise ValueError(f"{what} is {t.dtype}, expected {' or '.join(map(str, dtypes))}")
-    if t.device != device:
-        raise ValueError(f"{what} is on {t.device}, the weights are on {device}")
+def _write(t, m, cols, dtype, dev, what):
+    """An output's address and strides as a matrix; never a copy."""
+    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 2 and t.size(1) == cols
+            and t.size(0) == m):
+        return (t.data_ptr(), *t.stride())
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, the weights are on cuda:{dev}")
     if t.dim() == 0 or t.shape[-1] != cols or t.numel() != m * cols:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {m} rows of {cols}")
-    return t if t.dim() == 2 else t.view(m, cols)
+    t = t.view(m, cols)
+    return (t.data_ptr(), *t.stride())
 
 
-def _mat(t):
-    if t is None:
-        return _NONE
-    a, b = t.stride()
-    return t.data_ptr(), a, b
+def _row_count(x):
+    return x.size(0) if x.dim() == 2 else math.prod(x.shape[:-1])
+
+
+def _new(m, cols, dtype, weight, like):
+    """An output on the current stream, with the leading dimensions of `like`."""
+    t = torch.empty(m, cols, dtype=dtype, device=weight.device)
+    return t if like.dim() == 2 else t.view(*like.shape[:-1], cols)
 
 
 @contextlib.contextmanager
@@ -114,6 +125,7 @@ class _Dense:
     def _start(self, device):
         self._status = torch.zeros(1, dtype=torch.int32, device=device)
         self._need = {}
+        self._dev = self._status.get_device()
 
     def status(self) -> int:
         """COLL_OK, or COLL_ETIMEDOUT if a bounded device wait of an earlier call expired (its
@@ -125,12 +137,12 @@ class _Dense:
         """Call an entry point on the current stream, with a workspace if it asks for one. The
         size it last asked for is offered first, so that a loop over one size makes one call."""
         fn, size = _entry(where)
-        device, status = self._status.device, self._status.data_ptr()
-        stream = _raw_stream(device.index)  # the current stream's handle
+        status = self._status.data_ptr()
+        stream = _raw_stream(self._dev)  # the current stream's handle
         need = self._need.get(where, 0)
         while True:
             if need:
-                ws = torch.empty(need, dtype=torch.uint8, device=device)
+                ws = torch.empty(need, dtype=torch.uint8, device=self._status.device)
                 code = fn(pack(*fields, ws.data_ptr(), need, status), stream)
             else:
                 code = fn(pack(*fields, 0, 0, status), stream)
@@ -170,39 +182,36 @@ class Linear(_Dense):
         if stream is not None:
             with _on(stream, (x, residual, out, pre, self.weight, self.bias)):
                 return self.forward(x, residual, out, out_dtype, save, pre)
-        w, b = self.weight, self.bias
+        w, b, dev, keep = self.weight, self.bias, self._dev, []
         n, k = w.shape
-        dt, dev = w.dtype, w.device
-        x2 = _rows(x, k, dt, dev, "x")
-        m = x2.shape[0]
-        if out is not None:
+        dt = w.dtype
+        xm = _read(x, None, k, dt, dev, "x", keep)
+        m = _row_count(x)
+        if out is None:
+            ot = out_dtype or dt
+            if ot is not dt and ot is not torch.float32:
+                raise ValueError(f"out_dtype must be {dt} or torch.float32, not {ot}")
+            out = _new(m, n, ot, w, x)
+        else:
             ot = out.dtype
             if out_dtype is not None and out_dtype is not ot:
                 raise ValueError(f"out is {ot}, out_dtype is {out_dtype}")
-            y2 = _dest(out, m, n, (dt, torch.float32), dev, "out")
-        else:
-            ot = out_dtype or dt
-            if ot not in (dt, torch.float32):
-                raise ValueError(f"out_dtype must be {dt} or torch.float32, not {ot}")
-            y2 = torch.empty(m, n, dtype=ot, device=dev)
-            out = y2 if x.dim() == 2 else y2.view(*x.shape[:-1], n)
-        if pre is not None:
-            p2 = _dest(pre, m, n, (dt,), dev, "pre")
-        elif save:
-            p2 = torch.empty(m, n, dtype=dt, device=dev)
-            pre = p2 if x.dim() == 2 else p2.view(*x.shape[:-1], n)
-        else:
-            p2 = None
-        r2 = None
+            if ot is not dt and ot is not torch.float32:
+                raise ValueError(f"out is {ot}, expected {dt} or torch.float32")
+        ym = _write(out, m, n, ot, dev, "out")
+        if pre is None and save:
+            pre = _new(m, n, dt, w, x)
+        pm = _NONE if pre is None else _write(pre, m, n, dt, dev, "pre")
+        rm = _NONE
         if residual is not None:
             if residual.shape != out.shape:
                 residual = residual.expand(out.shape)
-            r2 = _rows(residual, n, ot, dev, "residual")
+            rm = _read(residual, m, n, ot, dev, "residual", keep)
         self._launch("coll_linear", _LINEAR.pack,
-                     (m, n, k, _TYPE[dt], _TYPE[ot], ACT[self.act], *_mat(x2), *_mat(w),
-                      *_mat(r2), *_mat(p2), *_mat(y2), 0 if b is None else b.data_ptr(),
+                     (m, n, k, _TYPE[dt], _TYPE[ot], ACT[self.act], *xm, w.data_ptr(),
+                      *w.stride(), *rm, *pm, *ym, 0 if b is None else b.data_ptr(),
                       0 if b is None else b.stride(0)))
-        return (out, pre) if save or p2 is not None else out
+        return out if pre is None else (out, pre)
 
     __call__ = forward
 
@@ -215,45 +224,39 @@ class Linear(_Dense):
             with _on(stream, (dy, x, pre, dx, dw, db, self.weight)):
                 return self.backward(dy, x, pre, need_dx, need_dw, need_db, dx, dw, db,
                                      grad_dtype)
-        w = self.weight
+        w, dev, keep = self.weight, self._dev, []
         n, k = w.shape
-        dt, dev = w.dtype, w.device
-        x2 = _rows(x, k, dt, dev, "x")
-        m = x2.shape[0]
-        dy2 = _rows(dy, n, dt, dev, "dy")
-        if dy2.shape[0] != m:
-            raise ValueError(f"dy has {dy2.shape[0]} rows, x has {m}")
-        p2 = None
+        dt = w.dtype
+        xm = _read(x, None, k, dt, dev, "x", keep)
+        m = _row_count(x)
+        dym = _read(dy, m, n, dt, dev, "dy", keep)
+        pm = _NONE
         if self.act != "none":
             if pre is None:
                 raise ValueError(f"backward of act={self.act!r} needs pre")
-            p2 = _rows(pre, n, dt, dev, "pre")
-            if p2.shape[0] != m:
-                raise ValueError(f"pre has {p2.shape[0]} rows, x has {m}")
+            pm = _read(pre, m, n, dt, dev, "pre", keep)
         if need_db is None:
             need_db = self.bias is not None or db is not None
         gt = grad_dtype or (dw.dtype if dw is not None else db.dtype if db is not None else dt)
-        if gt not in (dt, torch.float32):
+        if gt is not dt and gt is not torch.float32:
             raise ValueError(f"grad_dtype must be {dt} or torch.float32, not {gt}")
-        dx2 = dw2 = db2 = None
+        dxm = dwm = _NONE
+        dbp = 0
         if need_dx:
-            if dx is None:
-                dx2 = torch.empty(m, k, dtype=dt, device=dev)
-                dx = dx2 if x.dim() == 2 else dx2.view(x.shape)
-            else:
-                dx2 = _dest(dx, m, k, (dt,), dev, "dx")
+            dx = _new(m, k, dt, w, x) if dx is None else dx
+            dxm = _write(dx, m, k, dt, dev, "dx")
         if need_dw:
-            dw = torch.empty(n, k, dtype=gt, device=dev) if dw is None else dw
-            dw2 = _dest(dw, n, k, (gt,), dev, "dw")
+            dw = torch.empty(n, k, dtype=gt, device=w.device) if dw is None else dw
+            dwm = _write(dw, n, k, gt, dev, "dw")
         if need_db:
-            db = torch.empty(n, dtype=gt, device=dev) if db is None else db
-            db2 = _dest(db, 1, n, (gt,), dev, "db")
-            if db.dim() != 1 or (n > 1 and db.stride(0) != 1):
-                raise ValueError("db must be a contiguous vector")
+            db = torch.empty(n, dtype=gt, device=w.device) if db is None else db
+            if (db.dtype is not gt or db.get_device() != dev or db.dim() != 1 or db.size(0) != n
+                    or (n > 1 and db.stride(0) != 1)):
+                raise ValueError(f"db must be a contiguous vector of {n} {gt} on cuda:{dev}")
+            dbp = db.data_ptr()
         self._launch("coll_linear_backward", _LINEAR_BWD.pack,
-                     (m, n, k, _TYPE[dt], _TYPE[gt], ACT[self.act], *_mat(dy2), *_mat(p2),
-                      *_mat(x2), *_mat(w), *_mat(dx2), *_mat(dw2),
-                      0 if db2 is None else db2.data_ptr()))
+                     (m, n, k, _TYPE[dt], _TYPE[gt], ACT[self.act], *dym, *pm, *xm, w.data_ptr(),
+                      *w.stride(), *dxm, *dwm, dbp))
         return (dx if need_dx else None, dw if need_dw else None, db if need_db else None)
 
 
@@ -279,28 +282,23 @@ class GatedFFN(_Dense):
         if stream is not None:
             with _on(stream, (x, out, gate, up, self.w_gate, self.w_up)):
                 return self.forward(x, out, save, gate, up)
-        w = self.w_gate
+        w, wu, dev, keep = self.w_gate, self.w_up, self._dev, []
         n, k = w.shape
-        dt, dev = w.dtype, w.device
-        x2 = _rows(x, k, dt, dev, "x")
-        m = x2.shape[0]
-        lead = x.shape[:-1]
-
-        def dest(t, what):
-            if t is None:
-                t2 = torch.empty(m, n, dtype=dt, device=dev)
-                return (t2 if len(lead) == 1 else t2.view(*lead, n)), t2
-            return t, _dest(t, m, n, (dt,), dev, what)
-
-        out, h2 = dest(out, "out")
-        g2 = u2 = None
-        if save or gate is not None or up is not None:
-            gate, g2 = dest(gate, "gate")
-            up, u2 = dest(up, "up")
+        dt = w.dtype
+        xm = _read(x, None, k, dt, dev, "x", keep)
+        m = _row_count(x)
+        out = _new(m, n, dt, w, x) if out is None else out
+        hm = _write(out, m, n, dt, dev, "out")
+        gm = um = _NONE
+        kept = save or gate is not None or up is not None
+        if kept:
+            gate = _new(m, n, dt, w, x) if gate is None else gate
+            up = _new(m, n, dt, w, x) if up is None else up
+            gm, um = _write(gate, m, n, dt, dev, "gate"), _write(up, m, n, dt, dev, "up")
         self._launch("coll_gated_ffn", _GATED.pack,
-                     (m, n, k, _TYPE[dt], ACT[self.act], *_mat(x2), *_mat(w), *_mat(self.w_up),
-                      *_mat(g2), *_mat(u2), *_mat(h2)))
-        return out if g2 is None else (out, gate, up)
+                     (m, n, k, _TYPE[dt], ACT[self.act], *xm, w.data_ptr(), *w.stride(),
+                      wu.data_ptr(), *wu.stride(), *gm, *um, *hm))
+        return (out, gate, up) if kept else out
 
     __call__ = forward
 
@@ -313,36 +311,29 @@ class GatedFFN(_Dense):
             with _on(stream, (dh, x, gate, up, dx, dw_gate, dw_up, self.w_gate, self.w_up)):
                 return self.backward(dh, x, gate, up, need_dx, need_dw, dx, dw_gate, dw_up,
                                      grad_dtype)
-        w = self.w_gate
+        w, wu, dev, keep = self.w_gate, self.w_up, self._dev, []
         n, k = w.shape
-        dt, dev = w.dtype, w.device
-        x2 = _rows(x, k, dt, dev, "x")
-        m = x2.shape[0]
-        ins = []
-        for t, what in ((dh, "dh"), (gate, "gate"), (up, "up")):
-            t2 = _rows(t, n, dt, dev, what)
-            if t2.shape[0] != m:
-                raise ValueError(f"{what} has {t2.shape[0]} rows, x has {m}")
-            ins.append(t2)
+        dt = w.dtype
+        xm = _read(x, None, k, dt, dev, "x", keep)
+        m = _row_count(x)
+        dhm = _read(dh, m, n, dt, dev, "dh", keep)
+        gm = _read(gate, m, n, dt, dev, "gate", keep)
+        um = _read(up, m, n, dt, dev, "up", keep)
         gt = grad_dtype or (dw_gate.dtype if dw_gate is not None else
                             dw_up.dtype if dw_up is not None else dt)
-        if gt not in (dt, torch.float32):
+        if gt is not dt and gt is not torch.float32:
             raise ValueError(f"grad_dtype must be {dt} or torch.float32, not {gt}")
-        dx2 = dg2 = du2 = None
+        dxm = dgm = dum = _NONE
         if need_dx:
-            if dx is None:
-                dx2 = torch.empty(m, k, dtype=dt, device=dev)
-                dx = dx2 if x.dim() == 2 else dx2.view(x.shape)
-            else:
-                dx2 = _dest(dx, m, k, (dt,), dev, "dx")
+            dx = _new(m, k, dt, w, x) if dx is None else dx
+            dxm = _write(dx, m, k, dt, dev, "dx")
         if need_dw:
-            dw_gate = torch.empty(n, k, dtype=gt, device=dev) if dw_gate is None else dw_gate
-            dw_up = torch.empty(n, k, dtype=gt, device=dev) if dw_up is None else dw_up
-            dg2 = _dest(dw_gate, n, k, (gt,), dev, "dw_gate")
-            du2 = _dest(dw_up, n, k, (gt,), dev, "dw_up")
+            dw_gate = torch.empty(n, k, dtype=gt, device=w.device) if dw_gate is None else dw_gate
+            dw_up = torch.empty(n, k, dtype=gt, device=w.device) if dw_up is None else dw_up
+            dgm = _write(dw_gate, n, k, gt, dev, "dw_gate")
+            dum = _write(dw_up, n, k, gt, dev, "dw_up")
         self._launch("coll_gated_ffn_backward", _GATED_BWD.pack,
-                     (m, n, k, _TYPE[dt], _TYPE[gt], ACT[self.act], *_mat(ins[0]),
-                      *_mat(ins[1]), *_mat(ins[2]), *_mat(x2), *_mat(w), *_mat(self.w_up),
-                      *_mat(dx2), *_mat(dg2), *_mat(du2)))
+                     (m, n, k, _TYPE[dt], _TYPE[gt], ACT[self.act], *dhm, *gm, *um, *xm,
+                      w.data_ptr(), *w.stride(), wu.data_ptr(), *wu.stride(), *dxm, *dgm, *dum))
         return (dx if need_dx else None, dw_gate if need_dw else None,
                 dw_up if need_dw else None)
