@@ -146,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 
   if (threadIdx.x == 0) {
     for (uint32_t i = 0; i < p.stages; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], 2);  // A's and B's loads
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -168,70 +168,64 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
   const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
   const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
 
-  if (warp == 0) {
-    const uint32_t arrive0 = map_rank(full0, 0);
+  if (warp == 0 || warp == 3) {
+    const bool first = warp == 0;  // loads A; the other B
+    const uint32_t arrive0 = map_rank(full0, 0), offset = first ? 0u : kABytes;
     uint32_t s = 0, phase = 0;
     bool ok = true;
-    // k blocks of one segment; the operands' major axes are fixed within it
-    auto segment = [&](auto amn_c, auto bmn_c, const TcProb &q, const CUtensorMap *ma,
-                       const CUtensorMap *mb, int32_t m, int32_t n, int32_t k, int32_t end) {
-      constexpr bool amn = decltype(amn_c)::value, bmn = decltype(bmn_c)::value;
-      // bytes a stage receives, boxes past the edges counted whole; the second CTA's rows of
-      // A may all be past the last
-      const uint32_t rows = amn ? kABytes : q.a_rows * 128u;
-      const bool second = tl.m0 + 128 < q.m, mine = leader || second;
-      const uint32_t cols = bmn ? q.b_chunks * kChunk : q.b_box * 128u;
-      const uint32_t bytes = rows + (second ? rows : 0u) + CG * cols;
-      const int32_t chunks = q.b_chunks;
+    // k blocks [k, end) of one segment of this warp's operand from row r on, `bytes` of both CTAs
+    // a block (boxes past the edges counted whole); `mine`: this CTA has rows of it
+    auto segment = [&](auto mn, const CUtensorMap *map, int32_t r, int32_t chunks, uint32_t bytes,
+                       bool mine, int32_t k, int32_t end) {
+      bool ready = bar_test(empty0 + 8 * s, phase ^ 1u);
       for (; k < end; k += kTileK) {
-        ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
-        if (elect_one() && ok) {
-          const uint32_t bar = arrive0 + 8 * s;
-          if (leader) bar_expect(full0 + 8 * s, bytes);
-          const uint32_t da = ring + s * stage_bytes, db = da + kABytes;
-          if (mine) {
-            if (amn) {
-              tma_box_pair(da, ma, m, k, bar);
-              tma_box_pair(da + kChunk, ma, m + 64, k, bar);
-            } else {
-              tma_box_pair(da, ma, k, m, bar);
-            }
-          }
-          if (bmn) {
-            tma_box_pair(db, mb, n, k, bar);
-            if (chunks > 1) tma_box_pair(db + kChunk, mb, n + 64, k, bar);
-          } else {
-            tma_box_pair(db, mb, k, n, bar);
-          }
-        }
-        __syncwarp();
+        if (!ready) ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
+        const uint32_t bar = arrive0 + 8 * s, full = full0 + 8 * s;
+        const uint32_t d = ring + s * stage_bytes + offset;
         if (++s == stages) {
           s = 0;
           phase ^= 1u;
         }
+        ready = bar_test(empty0 + 8 * s, phase ^ 1u);  // the next slot, while this one is filled
+        if (elect_one() && ok) {
+          if (leader) bar_expect(full, bytes);
+          if (mine) {
+            if (decltype(mn)::value) {
+              tma_box_pair(d, map, r, k, bar);
+              if (chunks > 1) tma_box_pair(d + kChunk, map, r + 64, k, bar);
+            } else {
+              tma_box_pair(d, map, k, r, bar);
+            }
+          }
+        }
+        __syncwarp();
       }
     };
     using Yes = std::integral_constant<bool, true>;
     using No = std::integral_constant<bool, false>;
     for (uint32_t i = 0; walk.at(p, i, tl); ++i) {
       const TcProb &q = p.prob[tl.prob];
-      const int32_t m = (int32_t)tl.m0 + (int32_t)rank * 128;
-      const int32_t n = (int32_t)tl.n0 + (GATED ? 0 : (int32_t)rank * q.b_rows);
       const int2 range = share_of(q, tl.share);
+      const bool second = tl.m0 + 128 < q.m;  // the second CTA's rows of A may all be past the last
+      const int32_t r = first ? (int32_t)tl.m0 + (int32_t)rank * 128
+                              : (int32_t)tl.n0 + (GATED ? 0 : (int32_t)rank * q.b_rows);
       for (int seg = 0; seg < q.nseg; ++seg) {
         const int k0 = max(range.x - seg * q.kblocks, 0) * kTileK;
         const int k1 = min(range.y - seg * q.kblocks, q.kblocks) * kTileK;
-        const CUtensorMap *ma = &q.a[q.nbatch == 2 ? tl.batch : seg];
-        const CUtensorMap *mb = &q.b[GATED ? (int)rank : seg];
-        if (q.a_mn[seg]) {
-          if (q.b_mn[seg]) segment(Yes{}, Yes{}, q, ma, mb, m, n, k0, k1);
-          else segment(Yes{}, No{}, q, ma, mb, m, n, k0, k1);
-        } else {
-          if (q.b_mn[seg]) segment(No{}, Yes{}, q, ma, mb, m, n, k0, k1);
-          else segment(No{}, No{}, q, ma, mb, m, n, k0, k1);
-        }
+        const CUtensorMap *map = first ? &q.a[q.nbatch == 2 ? tl.batch : seg]
+                                       : &q.b[GATED ? (int)rank : seg];
+        const bool mn = first ? q.a_mn[seg] : q.b_mn[seg];
+        const int32_t chunks = first ? 2 : q.b_chunks;
+        const uint32_t one = mn ? chunks * kChunk : (first ? q.a_rows : q.b_box) * 128u;
+        const uint32_t bytes = first && !second ? one : CG * one;
+        const bool mine = !first || leader || second;
+        if (mn) segment(Yes{}, map, r, chunks, bytes, mine, k0, k1);
+        else segment(No{}, map, r, chunks, bytes, mine, k0, k1);
       }
     }
+    if (!GATED && !first && p.join.db)
+      for (int64_t c = (int64_t)blockIdx.x * 32 + lane; c < p.join.n; c += (int64_t)gridDim.x * 32)
+        join_column(p.join, c);
     // every slot's last products are done before this CTA may go away
     for (uint32_t i = 0; i < stages; ++i) {
       ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
@@ -287,10 +281,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         __syncwarp();
       }
     }
-  } else if (warp == 3) {
-    if (!GATED && p.join.db)
-      for (int64_t c = (int64_t)blockIdx.x * 32 + lane; c < p.join.n; c += (int64_t)gridDim.x * 32)
-        join_column(p.join, c);
   } else if (warp >= 4) {
     const int quad = warp & 3, part = (warp - 4) >> 2;
     uint32_t *const st = staged + (warp - 4) * 32 * kPitch;

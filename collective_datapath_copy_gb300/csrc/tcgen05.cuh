@@ -60,6 +60,19 @@ __device__ __forceinline__ bool bar_try_wait(uint32_t bar, uint32_t parity) {
   return ok != 0;
 }
 
+// The same without the hardware's suspended wait (up to some 4 us where the phase never ends).
+__device__ __forceinline__ bool bar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // Every wait is bounded. The slow part of one: false once it has run out of time or another role
 // of the CTA has given up; then the roles leave their loops, the CTA drains and `status` says so.
 constexpr uint64_t kWaitNs = 2000000000ull;
