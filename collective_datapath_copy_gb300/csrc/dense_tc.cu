@@ -19,6 +19,12 @@
 // let the epilogue of one tile run beside the products of the next. The grid is persistent; tiles are walked eight rows of tiles at a time,
 // which keeps the operands of the tiles in flight in L2.
 //
+// Measured: 4096 x 4096 x 4096 75 us (1830 TFLOP/s); gated 8192 x 14336 x 4096 with everything kept
+// 1.01 ms alone (1900 TFLOP/s, tensor pipe 96 % busy) and 1.14 ms back to back, where the card's
+// power cap sets the clock. Wide tiles are bound by the tensor pipe, tiles of up to 128 columns by
+// issuing (about 27 ns an instruction), sums of a few k blocks by the epilogue's way to HBM
+// (8192 x 8192 x 64: 49 us, 2.7 TB/s of writes, where filling the same memory reaches 3.4).
+//
 // Every wait is bounded: a wait that runs out sets an abort flag, the CTA's roles leave their
 // loops, in-flight copies and products get time to land, TMEM is freed, and status says so.
 #include <cuda.h>
@@ -470,7 +476,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
   // columns, 186 for 128, 264 for 192, 339 for 256) or the time of its epilogue beside the next
   // tile's products, and every cluster its tiles one after the other; the last epilogue comes on
   // top. An epilogue takes 14 ns a column, 10 more for a residual, 8 for each thing kept and 18 for
-  // an activation (8192 x 8192 x 64: 49 us plain, 85 with a residual, 160 with everything).
+  // an activation (8192 x 8192 x 64: 49 us plain, 85 with a residual, 175 with everything).
   // Joining shares costs a launch and their way through L2. Calls of a few us wait for this, so it
   // tries no more than it has to.
   struct Option {
