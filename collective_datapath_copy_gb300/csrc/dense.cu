@@ -141,7 +141,7 @@ uint64_t sectors(const void *p, int64_t rs, int es) {
   return p ? (uintptr_t)p | (uint64_t)(rs * es) : 0;
 }
 
-// The boundary on which rows start in every array of the epilogue, if all have unit stride.
+// Do rows start on 16 bytes in every array of the epilogue?
 void set_vec(DenseJob &j) {
   const coll::DenseEpi &e = j.e;
   const int oe = esize(e.out_type);
@@ -150,7 +150,7 @@ void set_vec(DenseJob &j) {
   v |= sectors(e.pre, e.pre_rs, 2) | sectors(e.gate, e.gate_rs, 2) | sectors(e.up, e.up_rs, 2) |
        sectors(e.bias, 0, 2) | sectors(e.res, e.res_rs, oe);
   const bool unit = (!e.bias || e.bias_stride == 1) && (!e.res || e.res_cs == 1);
-  j.e.vec = !unit || v % 16 ? 0 : v % 32 ? 16 : 32;
+  j.e.vec = unit && v % 16 == 0;
 }
 
 DenseJob job(int64_t m, int64_t n, int64_t k, int64_t type, int32_t *status) {

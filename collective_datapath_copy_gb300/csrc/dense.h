@@ -30,8 +30,7 @@ struct DenseEpi {
   int32_t type;      // COLL_BF16 / COLL_F16: bias, pre, gate, up
   int32_t out_type;  // type or COLL_F32: out, residual
   int32_t act;
-  int32_t vec;       // 32 or 16: every array above has unit column stride and its rows start on
-                     // that many bytes; 0: not so
+  int32_t vec;       // 1: every array above has unit column stride, its rows start on 16 bytes
 };
 
 // out[b](m, n) = epilogue(sum over s of sum over k of A[b or s](m, k) B[s](n, k)).

@@ -23,7 +23,7 @@
 // 1.01 ms alone (1900 TFLOP/s, tensor pipe 96 % busy) and 1.14 ms back to back, where the card's
 // power cap sets the clock. Wide tiles are bound by the tensor pipe, tiles of up to 128 columns by
 // issuing (about 27 ns an instruction), sums of a few k blocks by the epilogue's way to HBM
-// (8192 x 8192 x 64: 49 us, 2.7 TB/s of writes, where filling the same memory reaches 3.4).
+// (8192 x 8192 x 64: 52 us, 2.6 TB/s of writes, where filling the same memory reaches 3.4).
 //
 // Every wait is bounded: a wait that runs out sets an abort flag, the CTA's roles leave their
 // loops, in-flight copies and products get time to land, TMEM is freed, and status says so.
@@ -294,7 +294,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     for (uint32_t it = 0; walk.at(p, it, tl); ++it) {
       const TcProb &q = p.prob[tl.prob];
       const DenseEpi &e = q.e;
-      const bool wide = e.vec == 32;
       const bool pre_res = !GATED && e.vec && e.res && e.out_type != COLL_F32;
       const uint32_t buf = it & 1u;
       const int64_t row0 = tl.m0 + rank * 128 + quad * 32, row = row0 + lane;
@@ -302,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
       const int cols = (int)min((int64_t)q.tile_cols, q.n - tl.n0);
       uint32_t r[16];  // the residual of the next 32 columns, asked for ahead
       auto ask = [&](int c0) {
-        if (pre_res && live && c0 + 32 <= cols) ld_halves(e.res, row * e.res_rs + tl.n0 + c0, r, wide);
+        if (pre_res && live && c0 + 32 <= cols) ld_halves(e.res, row * e.res_rs + tl.n0 + c0, r);
       };
       ask(part * 32);
       if (!__all_sync(~0u, wait_bar(&sh.abort, smem_u32(&sh.acc_full[buf]), (it >> 1) & 1u, p.status))) break;
@@ -316,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         if (q.split > 1) {  // this share's sums; whole runs, the rows are padded for them
           if (live) {
             const int64_t plane = (tl.share * q.nbatch + tl.batch) * (GATED ? 2 : 1);
-            st_run32(q.part, (plane * q.m + row) * q.part_ld + col, COLL_F32, true, g);
+            st_run32(q.part, (plane * q.m + row) * q.part_ld + col, COLL_F32, g);
             if constexpr (GATED)
-              st_run32(q.part, ((plane + 1) * q.m + row) * q.part_ld + col, COLL_F32, true, u);
+              st_run32(q.part, ((plane + 1) * q.m + row) * q.part_ld + col, COLL_F32, u);
           }
           continue;
         }
@@ -327,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         const int left = min(32, cols - c0);
         auto store = [&](void *base, int64_t rs, int type, const float (&v)[32]) {
           if (vec) {
-            if (live) st_run32(base, row * rs + col, type, wide, v);
+            if (live) st_run32(base, row * rs + col, type, v);
           } else {
             const int64_t at0 = row0 * rs + col;
             staged_store(st, static_cast<char *>(base) + at0 * (type == COLL_F32 ? 4 : 2), rs, type,
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           if (e.bias) {
             if (vec) {
               uint32_t b[16];
-              ld_halves(e.bias, col, b, wide);
+              ld_halves(e.bias, col, b);
               add_halves(g, b, e.type);
             } else {
               add_bias(e, col, left, g);
@@ -364,13 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
               ask(c0 + 64);
             } else if (live) {
               const float *rp = static_cast<const float *>(e.res) + row * e.res_rs + col;
+              uint32_t x[32];
+              ld_row<32>(rp, x);
 #pragma unroll
-              for (int i = 0; i < 32; i += 8) {
-                uint32_t x[8];
-                ld_sector(rp + i, x, wide);
-#pragma unroll
-                for (int w = 0; w < 8; ++w) g[i + w] += __uint_as_float(x[w]);
-              }
+              for (int i = 0; i < 32; ++i) g[i] += __uint_as_float(x[i]);
             }
           }
         }
@@ -476,7 +472,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
   // columns, 186 for 128, 264 for 192, 339 for 256) or the time of its epilogue beside the next
   // tile's products, and every cluster its tiles one after the other; the last epilogue comes on
   // top. An epilogue takes 14 ns a column, 10 more for a residual, 8 for each thing kept and 18 for
-  // an activation (8192 x 8192 x 64: 49 us plain, 85 with a residual, 175 with everything).
+  // an activation (8192 x 8192 x 64: 52 us plain, 86 with a residual, 160 with everything).
   // Joining shares costs a launch and their way through L2. Calls of a few us wait for this, so it
   // tries no more than it has to.
   struct Option {
@@ -553,6 +549,15 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
         else if (i == 0) keep(o, &other);
         else keep(other, &o);
       }
+  }
+  // with one product's shares settled the other's columns may be better off elsewhere
+  if (count == 2 && best[0].split + best[1].split > 2) {
+    const Option o = best[0], q = best[1];
+    for (int bn = 256; bn >= 64; bn -= 32) {
+      const Option a = option(0, bn, o.split), b = option(1, bn, q.split);
+      keep(a, &q);
+      keep(o, &b);
+    }
   }
   p.status = jobs[0].j->status;
   for (int i = 0; i < count; ++i) {
