@@ -42,7 +42,6 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
-constexpr float kTileNs = 600.0f;          // of a tile beside its k blocks
 constexpr float kJoinNs = 2500.0f;         // of joining shares, beside their bytes
 constexpr int kMostShares = 16;
 
@@ -432,12 +431,13 @@ cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStre
   return dense_launch(tc_kernel<GATED>, dim3(clusters * CG), kThreads, smem, CG, s, p);
 }
 
-// ns an output column of a tile (256 rows, two CTAs) takes in the epilogue
-int64_t epilogue_ns(const DenseJob &j, int split) {
-  if (split > 1) return j.gated ? 40 : 20;
+// ns a tile's epilogue takes for each column of its accumulator (256 rows, two CTAs)
+float epilogue_ns(const DenseJob &j, int split) {
+  if (split > 1) return 14.0f;
   const DenseEpi &e = j.e;
-  return 14 + (e.out_type == COLL_F32 ? 8 : 0) + (e.res ? 10 : 0) + (e.pre ? 8 : 0) +
-         (e.gate ? 16 : 0) + (e.act != COLL_ACT_NONE ? 18 : 0) + (e.vec ? 0 : 8);
+  const float act = j.gated || e.act == COLL_ACT_NONE || e.act == COLL_ACT_RELU ? 0.0f : 18.0f;
+  return 7.0f + (e.out_type == COLL_F32 ? 7.0f : 0.0f) + (e.res ? 9.5f : 0.0f) +
+         (e.pre ? 5.0f : 0.0f) + (e.gate ? 8.0f : 0.0f) + act + (e.vec ? 0.0f : 4.0f);
 }
 
 int operands_a(const DenseJob &j) { return j.nbatch == 2 || j.nseg == 2 ? 2 : 1; }
@@ -471,15 +471,20 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
   // its k blocks times 62 ns and 1.08 a column (measured at 4096 x 4096 x 8192: 144 ns for 64
   // columns, 186 for 128, 264 for 192, 339 for 256) or the time of its epilogue beside the next
   // tile's products, and every cluster its tiles one after the other; the last epilogue comes on
-  // top. An epilogue takes 14 ns a column, 10 more for a residual, 8 for each thing kept and 18 for
-  // an activation (8192 x 8192 x 64: 52 us plain, 86 with a residual, 160 with everything).
+  // top. An epilogue takes 1.35 us and 7 ns a column, 9.5 more for a residual and 18 for an
+  // activation (8192 x 8192 x 64: 52 us plain, 86 with a residual, 160 with everything); where
+  // both take long, not all of the shorter one is hidden (4864 rows, k = 512, 256 columns: 4.05 us
+  // a round of 2.7 and 3.2).
   // Joining shares costs a launch and their way through L2. Calls of a few us wait for this, so it
   // tries no more than it has to.
   struct Option {
     int cols, split;
     uint32_t tiles;
     float main, last, join;  // ns: a tile's products, its epilogue; joining shares
-    float time() const { return (main > last ? main : last) + kTileNs; }
+    float time() const {
+      const float less = main < last ? main : last, more = main < last ? last : main;
+      return more + (less < 2700.0f ? 0.3f * less : 800.0f);
+    }
   };
   auto option = [&](int i, int bn, int sp) {
     const DenseJob &j = *jobs[i].j;
@@ -488,7 +493,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
         (int64_t)ceil_div(j.m, 128 * CG) * ceil_div(j.n, j.gated ? bn / 2 : bn) * j.nbatch * sp;
     o.tiles = tiles > 0x7FFFFFFF ? 0x7FFFFFFFu : (uint32_t)tiles;
     o.main = (float)ceil_div((int64_t)ceil_div(j.k, kTileK) * j.nseg, sp) * (62.0f + 1.08f * bn);
-    o.last = (float)(bn * epilogue_ns(j, sp) / (j.gated ? 2 : 1));
+    o.last = 1350.0f + bn * epilogue_ns(j, sp);
     if (sp > 1)
       o.join = kJoinNs + (float)j.m * (float)j.n * (float)(j.nbatch * (j.gated ? 2 : 1) * sp) / 500.0f;
     return o;
