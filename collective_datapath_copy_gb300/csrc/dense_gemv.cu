@@ -92,6 +92,46 @@ __device__ __forceinline__ void load16(const uint16_t *p, int k, int len, uint32
   }
 }
 
+// The same from anywhere, in two halves so that the loads of several calls are in flight together:
+// the three aligned 16-byte words around the elements, if all their bytes are the row's, ...
+struct Around {
+  uint32_t w[12];
+  bool whole;
+};
+
+__device__ __forceinline__ void ask16(const uint16_t *p, int k, int len, Around &a) {
+  const int off = (int)((uintptr_t)p & 15u);
+  a.whole = 2 * k >= off && k + (48 - off) / 2 <= len;
+  const char *q = reinterpret_cast<const char *>(p) - off;
+#pragma unroll
+  for (int h = 0; h < 3; ++h) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (a.whole) v = ld_word16(q + 16 * h);
+    a.w[4 * h] = v.x, a.w[4 * h + 1] = v.y, a.w[4 * h + 2] = v.z, a.w[4 * h + 3] = v.w;
+  }
+}
+
+// ... then the elements out of them; single ones at the row's ends.
+__device__ __forceinline__ void take16(const uint16_t *p, int k, int len, Around &a,
+                                       uint32_t (&r)[8]) {
+  const int off = (int)((uintptr_t)p & 15u);
+  if (!a.whole) {
+    load16<2>(p, k, len, r);
+    return;
+  }
+  uint32_t *w = a.w;
+  if (off & 8) {
+#pragma unroll
+    for (int i = 0; i < 10; ++i) w[i] = w[i + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int i = 0; i < 9; ++i) w[i] = w[i + 1];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = __funnelshift_r(w[i], w[i + 1], (off & 2) * 8);
+}
+
 template <int TYPE>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -114,7 +154,7 @@ template <bool GATED, int TYPE, int NT, int ALIGN>
 __global__ void __launch_bounds__(kMostWarps<NT> * 32, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
   griddep_launch();
   constexpr int FEAT = GATED ? 8 : 16;   // outputs of a CTA
-  constexpr int AHEAD = NT == 1 ? 4 : NT == 2 ? 2 : 1;
+  constexpr int AHEAD = NT == 1 && ALIGN > 2 ? 4 : NT <= 2 ? 2 : 1;
   __shared__ float part[kMostWarps<NT>][8 * NT][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -139,11 +179,27 @@ __global__ void __launch_bounds__(kMostWarps<NT> * 32, 1) gemv_kernel(const __gr
   const int steps = (len + kStep - 1) / kStep;
   for (int s = warp; s < steps; s += AHEAD * warps) {
     uint32_t a[AHEAD][8], b[AHEAD][8], x[AHEAD][NT][8];
+    if constexpr (ALIGN == 2) {
+      Around ra[AHEAD], rb[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int k = (s + i * warps) * kStep;
-      load16<ALIGN>(wa + k, k + 16 * t, la, a[i]);
-      load16<ALIGN>(wb + k, k + 16 * t, lb, b[i]);
+      for (int i = 0; i < AHEAD; ++i) {
+        const int k = (s + i * warps) * kStep;
+        ask16(wa + k, k + 16 * t, la, ra[i]);
+        ask16(wb + k, k + 16 * t, lb, rb[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int k = (s + i * warps) * kStep;
+        take16(wa + k, k + 16 * t, la, ra[i], a[i]);
+        take16(wb + k, k + 16 * t, lb, rb[i], b[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int k = (s + i * warps) * kStep;
+        load16<ALIGN>(wa + k, k + 16 * t, la, a[i]);
+        load16<ALIGN>(wb + k, k + 16 * t, lb, b[i]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
