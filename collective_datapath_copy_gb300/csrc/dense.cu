@@ -13,7 +13,8 @@ using coll::DenseJob;
 using coll::DenseMat;
 using coll::TcOperand;
 
-// Bump allocator over the caller's workspace, in steps of 256 bytes from a 128-byte boundary. With base == nullptr it only counts.
+// Bump allocator over the caller's workspace, in steps of 256 bytes from a 128-byte boundary. With
+// base == nullptr it only counts.
 struct Ws {
   char *base;
   uint64_t used;
@@ -85,8 +86,11 @@ bool same(const View &a, const View &b) {
 int check_mat(const View &v, bool needed, bool output) {
   if (!v.p) return needed && v.rows > 0 && v.cols > 0 ? COLL_EINVAL : COLL_OK;
   if ((uintptr_t)v.p % (unsigned)v.es) return COLL_EALIGN;
+  // what a device can address, so that no offset below leaves 64 bits
   const int64_t lim = (int64_t)1 << 40;
-  if (v.rs > lim || v.rs < -lim || v.cs > lim || v.cs < -lim) return COLL_EINVAL;
+  const int64_t rs = v.rows > 1 ? lim / (v.rows - 1) : lim;
+  const int64_t cs = v.cols > 1 ? lim / (v.cols - 1) : lim;
+  if (v.rs > rs || v.rs < -rs || v.cs > cs || v.cs < -cs) return COLL_EINVAL;
   if (output && v.rows > 0 && v.cols > 0) {
     if (v.cols > 1 && v.cs != 1) return COLL_EINVAL;
     if (v.rows > 1 && v.rs < v.cols) return COLL_EINVAL;

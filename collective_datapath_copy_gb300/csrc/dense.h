@@ -69,7 +69,6 @@ int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums);
 cudaError_t dense_act_bwd(const DenseActBwd &a, DenseJoin &join, cudaStream_t s);
 cudaError_t dense_join(const DenseJoin &join, cudaStream_t s);
 
-
 // dst[i * ld + j] = src(i, j): operands whose strides or base no tensor map takes, laid out in
 // rows of whole 16-byte runs, all of a product's in one launch.
 struct DensePack {

@@ -151,7 +151,8 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
 
 // NT: columns of eight tokens.
 template <bool GATED, int TYPE, int NT, int ALIGN>
-__global__ void __launch_bounds__(kMostWarps<NT> * 32, 1) gemv_kernel(const __grid_constant__ GemvParams p) {
+__global__ void __launch_bounds__(kMostWarps<NT> * 32, 1)
+    gemv_kernel(const __grid_constant__ GemvParams p) {
   griddep_launch();
   constexpr int FEAT = GATED ? 8 : 16;   // outputs of a CTA
   constexpr int AHEAD = NT == 1 && ALIGN > 2 ? 4 : NT <= 2 ? 2 : 1;
@@ -383,7 +384,8 @@ cudaError_t gemv_run(const DenseJob &j, cudaStream_t s) {
   }
   // Warps of a CTA: 16, one CTA an SM, where there are no more CTAs than SMs, else 8 and two CTAs
   // an SM (128 registers a thread); no more than there are steps of k.
-  const int64_t ctas = (j.n + (j.gated ? 7 : 15)) / (j.gated ? 8 : 16), steps = (j.k + kStep - 1) / kStep;
+  const int64_t ctas = (j.n + (j.gated ? 7 : 15)) / (j.gated ? 8 : 16);
+  const int64_t steps = (j.k + kStep - 1) / kStep;
   p.warps = ctas <= (int64_t)kSms ? 16 : 8;
   while (p.warps > 1 && p.warps > steps) p.warps /= 2;
   if (j.e.type == COLL_BF16)

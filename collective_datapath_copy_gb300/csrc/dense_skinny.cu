@@ -90,7 +90,8 @@ __device__ __forceinline__ void finish32(const DenseEpi &e, int64_t t0, int64_t 
 }
 
 template <bool GATED>
-__global__ void __launch_bounds__(kThreads, 2) skinny_kernel(const __grid_constant__ SkinnyParams p) {
+__global__ void __launch_bounds__(kThreads, 2)
+    skinny_kernel(const __grid_constant__ SkinnyParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ Shared sh;
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;

@@ -11,13 +11,14 @@
 // 64 multiply-adds. Gated: CTA 0 holds rows of the gate's weights and CTA 1 the same rows of the
 // up weights, and the accumulator's halves are g and u of the same columns.
 //
-// Warps: 0 loads, 1 issues the matrix instructions (the pair's first CTA only), 2
-// owns TMEM, 4-11 run the epilogue, two warps for each 32 rows, 32 columns at a time: a lane holds
-// 32 columns of its row and reads and writes whole 32-byte sectors. Where an array's rows do not
-// start on 32 bytes, or the row ends inside the 32 columns, 16 columns at a time pass through
-// shared memory and neighbouring lanes take neighbouring columns. Two accumulators of 256 columns
-// let the epilogue of one tile run beside the products of the next. The grid is persistent; tiles are walked eight rows of tiles at a time,
-// which keeps the operands of the tiles in flight in L2.
+// Warps: 0 loads A, 3 loads B (and adds up column sums that came along), 1 issues the matrix
+// instructions (the pair's first CTA only), 2 owns TMEM, 4-11 run the epilogue, two warps for each
+// 32 rows, 32 columns at a time: a lane holds 32 columns of its row and accesses whole 32-byte
+// sectors. Where an array's rows do not start on 16 bytes, or the row ends inside the 32 columns,
+// the block passes through shared memory and neighbouring lanes take neighbouring columns. Two
+// accumulators of 256 columns let the epilogue of one tile run beside the products of the next.
+// The grid is persistent; tiles are walked eight rows of tiles at a time, which keeps the operands
+// of the tiles in flight in L2.
 //
 // Measured: 4096 x 4096 x 4096 75 us (1830 TFLOP/s); gated 8192 x 14336 x 4096 with everything kept
 // 1.01 ms alone (1900 TFLOP/s, tensor pipe 96 % busy) and 1.14 ms back to back, where the card's
@@ -42,15 +43,14 @@ namespace {
 
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
-constexpr float kJoinNs = 2500.0f;         // of joining shares, beside their bytes
-constexpr int kMostShares = 16;
-
 constexpr int CG = 2;                     // CTAs of a tile (cta_group::2)
+constexpr float kJoinNs = 2500.0f;        // of joining shares, beside their bytes
+constexpr int kMostShares = 16;
 constexpr int kTileK = 64;                // elements of k per stage: one 128-byte swizzled row
 constexpr uint32_t kABytes = 128 * 128;   // 128 rows
 constexpr uint32_t kChunk = 64 * 128;     // MN-major: 64 k rows of 64 elements
 constexpr int kMaxStages = 12;
-constexpr uint32_t kStageOut = kEpiWarps * 32 * kPitch * 4;
+constexpr uint32_t kStageOut = kEpiWarps * 32 * kPitch * 4;  // the epilogue's blocks
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], acc_full[2], acc_empty[2];
@@ -63,11 +63,11 @@ struct Tile {
   int64_t m0, n0;
 };
 
-// t / d and what remains. Up to 2^24 by a reciprocal that is off by one at most: a role of one
+// t / d and what remains. Up to 2^22 by a quotient in binary32, off by one at most: a role of one
 // warp pays for every instruction of its chain.
 __device__ __forceinline__ uint32_t div_rem(uint32_t t, uint32_t d, uint32_t &rest) {
   uint32_t q;
-  if (t < (1u << 24)) {
+  if (t < (1u << 22)) {
     q = __float2uint_rz(__fdividef((float)t, (float)d));
     int32_t r = (int32_t)(t - q * d);
     if (r < 0) {
@@ -303,7 +303,9 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
         if (pre_res && live && c0 + 32 <= cols) ld_halves(e.res, row * e.res_rs + tl.n0 + c0, r);
       };
       ask(part * 32);
-      if (!__all_sync(~0u, wait_bar(&sh.abort, smem_u32(&sh.acc_full[buf]), (it >> 1) & 1u, p.status))) break;
+      if (!__all_sync(~0u, wait_bar(&sh.abort, smem_u32(&sh.acc_full[buf]), (it >> 1) & 1u,
+                                    p.status)))
+        break;
       tc_fence_after();
       for (int c0 = part * 32; c0 < cols; c0 += 64) {
         float g[32], u[GATED ? 32 : 1];
@@ -355,7 +357,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
           if (e.res) {
             if (!vec) {
               const int64_t at0 = row0 * e.res_rs + col * e.res_cs;
-              staged_add(st, static_cast<const char *>(e.res) + at0 * (e.out_type == COLL_F32 ? 4 : 2),
+              staged_add(st,
+                         static_cast<const char *>(e.res) + at0 * (e.out_type == COLL_F32 ? 4 : 2),
                          e.res_rs, e.res_cs, e.out_type, rows, left, g);
             } else if (pre_res) {
               add_halves(g, r, e.type);
@@ -495,7 +498,8 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
     o.main = (float)ceil_div((int64_t)ceil_div(j.k, kTileK) * j.nseg, sp) * (62.0f + 1.08f * bn);
     o.last = 1350.0f + bn * epilogue_ns(j, sp);
     if (sp > 1)
-      o.join = kJoinNs + (float)j.m * (float)j.n * (float)(j.nbatch * (j.gated ? 2 : 1) * sp) / 500.0f;
+      o.join = kJoinNs +
+               (float)j.m * (float)j.n * (float)(j.nbatch * (j.gated ? 2 : 1) * sp) / 500.0f;
     return o;
   };
   auto even = [&](const Option &o, const Option &q) {

@@ -92,8 +92,8 @@ class TensorParallelMLP:
         return self._y
 
     def backward(self, dy):
-        """dx, one tensor per rank (the object's buffers), and (dw_gate_r, dw_up_r, dw_down_r) of every rank's shards, for
-        the last forward(keep=True)."""
+        """dx, one tensor per rank (the object's buffers), and (dw_gate_r, dw_up_r, dw_down_r) of
+        every rank's shards, for the last forward(keep=True)."""
         if self._kept is None:
             raise RuntimeError("backward needs forward(keep=True) before it")
         x, kept = self._kept
