@@ -214,6 +214,10 @@ void operand(const DenseMat &m, int64_t rows, int64_t k, Ws &ws, coll::DensePack
 // 23). Up to 32 for weights of 32 MiB or less (4096 x 1792 for 32 tokens: 6.7 us against 8.7;
 // 6144 x 4096: 20 us against 15) or operands that would have to be laid out first; up to 64 for
 // 4 MiB or less (1024 x 1024 for 48: 4.0 us against 4.9; 1792 x 4096: 11.5 against 8.1).
+// Whatever the batch, not where the sums are long and the outputs few: a warp's turns through k, at
+// the time a turn was measured to take, against the tensor-core launch, its bytes and laying out
+// (512 x 12288 for 32 tokens: 13.8 us against 10.0; 76 x 12289: 24 against 11, for one token 16
+// against 11).
 bool few_tokens(const DenseJob &j) {
   auto along_k = [&](const DenseMat &m) { return m.cs == 1 || j.k == 1; };
   if (!j.forward || j.m > coll::kGemvMost || j.k > (int64_t)1 << 30 || !along_k(j.a[0]) ||
@@ -223,6 +227,10 @@ bool few_tokens(const DenseJob &j) {
   TcOperand o;
   const bool as_it_lies = in_place(j.a[0], j.m, j.k, o) && in_place(j.b[0], j.n, j.k, o) &&
                           (!j.gated || in_place(j.b[1], j.n, j.k, o));
+  const int64_t columns = j.m <= 8 ? 1 : j.m <= 16 ? 2 : 4;  // of eight tokens, at most four
+  const int64_t turn = as_it_lies ? 100 + 150 * columns : 900 + 300 * columns;  // ns
+  const int64_t ns = j.k * turn / (j.m <= 32 ? 1024 : 512);
+  if (ns > (as_it_lies ? 4500 + bytes / 5500 : 8000 + bytes / 1850)) return false;
   return j.m <= 16 || (j.m <= 32 && (!as_it_lies || bytes <= (int64_t)32 << 20)) ||
          bytes <= (int64_t)4 << 20;
 }

@@ -111,11 +111,11 @@ __device__ __forceinline__ void ask16(const uint16_t *p, int k, int len, Around 
   }
 }
 
-// ... then the elements out of them; single ones at the row's ends.
+// ... then the elements out of them; single ones at the row's ends, zeros past them.
 __device__ __forceinline__ void take16(const uint16_t *p, int k, int len, Around &a,
                                        uint32_t (&r)[8]) {
   const int off = (int)((uintptr_t)p & 15u);
-  if (!a.whole) {
+  if (!a.whole && k < len) {
     load16<2>(p, k, len, r);
     return;
   }
@@ -205,10 +205,18 @@ __global__ void __launch_bounds__(kMostWarps<NT> * 32, 1)
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const int k = (s + i * warps) * kStep;
+      if constexpr (ALIGN == 2) {
+        Around rx[NT];
 #pragma unroll
-      for (int c = 0; c < NT; ++c) {
-        if (p.x_align >= ALIGN) load16<ALIGN>(xt[c] + k, k + 16 * t, lx[c], x[i][c]);
-        else load16<2>(xt[c] + k, k + 16 * t, lx[c], x[i][c]);
+        for (int c = 0; c < NT; ++c) ask16(xt[c] + k, k + 16 * t, lx[c], rx[c]);
+#pragma unroll
+        for (int c = 0; c < NT; ++c) take16(xt[c] + k, k + 16 * t, lx[c], rx[c], x[i][c]);
+      } else {
+#pragma unroll
+        for (int c = 0; c < NT; ++c) {
+          if (p.x_align >= ALIGN) load16<ALIGN>(xt[c] + k, k + 16 * t, lx[c], x[i][c]);
+          else load16<2>(xt[c] + k, k + 16 * t, lx[c], x[i][c]);
+        }
       }
     }
 #pragma unroll

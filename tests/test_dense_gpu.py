@@ -601,3 +601,39 @@ def test_refusals():
     with pytest.raises(cdc.CollError) as e:   # rows of an output that overlap
         lin.forward(x, out=torch.zeros(64, dtype=BF, device="cuda").as_strided((8, 32), (4, 1)))
     assert e.value.code == _lib.D["COLL_EINVAL"]
+
+
+FEW = [(1, 76, 12289), (4, 40, 9000), (16, 76, 13679), (32, 76, 13679), (32, 64, 12288),
+       (64, 76, 4099), (64, 40, 4096), (24, 33, 4001), (12, 50, 1027), (48, 90, 611)]
+
+
+@pytest.mark.parametrize("m,n,k", FEW)
+@pytest.mark.parametrize("dtype", [BF, HF])
+def test_few_tokens_over_long_sums(m, n, k, dtype):
+    g = gen(k + m)
+    x, w = rnd(g, m, k, dtype), rnd(g, n, k, dtype, k ** -0.5)
+    wu, b = rnd(g, n, k, dtype, k ** -0.5), rnd(g, 1, n, dtype)[0]
+    y = Out(m, n, dtype, 1, 1)
+    cdc.Linear(w, b, "gelu").forward(x, out=y.v)
+    ref.assert_close(y.v, ref.linear(x, w, b, None, "gelu", dtype, dtype)[0])
+    assert y.untouched()
+    h = Out(m, n, dtype)
+    cdc.GatedFFN(w, wu, "silu").forward(x, out=h.v)
+    ref.assert_close(h.v, ref.gated(x, w, wu, "silu", dtype)[0])
+    assert h.untouched()
+
+
+@pytest.mark.parametrize("shift", range(8))
+@pytest.mark.parametrize("m", [1, 12, 30, 60])
+def test_few_tokens_at_any_offset(m, shift):
+    """Rows that start on every even byte, with infinities around them that must not be read in."""
+    g = gen(shift)
+    n, k = 35, 301
+    def inside(rows):
+        buf = torch.full((rows, k + 16), float("inf"), dtype=BF, device="cuda")
+        v = buf[:, shift:shift + k]
+        v.copy_(rnd(g, rows, k, BF, k ** -0.5))
+        return v
+    x, w = inside(m), inside(n)
+    y = cdc.Linear(w).forward(x)
+    ref.assert_close(y, ref.linear(x, w, None, None, "none", BF, BF)[0])
