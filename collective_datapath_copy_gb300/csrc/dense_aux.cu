@@ -4,9 +4,10 @@
 //   gated:        dg = dh u act'(g), du = dh act(g)
 // Bound by HBM (gated, 4096 x 14336: 92 us for 587 MB, 6.4 TB/s): each input is read once, dz (dg,
 // du) written once, rounded to the operands' type for the tensor-core products that follow (their
-// sums over rows or columns average the rounding, which is that of any stored activation). db sums the unrounded binary32 dz: a thread
-// adds its rows in order, row groups of a CTA join in order in shared memory, and row blocks in
-// order in a second launch, so the result does not depend on timing.
+// sums over rows or columns average the rounding, which is that of any stored activation). db sums
+// the unrounded binary32 dz: a thread adds its rows in order, row groups of a CTA join in order in
+// shared memory, and row blocks in order in a second launch, so the result does not depend on
+// timing.
 #include "dense.h"
 #include "dense_epi.cuh"
 #include "tma.cuh"

@@ -33,26 +33,49 @@ __device__ __forceinline__ void h2f2(uint32_t w, int type, float &lo, float &hi)
   hi = h2f((uint16_t)(w >> 16), type);
 }
 
-__device__ __forceinline__ float logistic(float z) { return __fdividef(1.0f, 1.0f + __expf(-z)); }
+// The hardware's approximations of 1 / x and 2^x, an instruction each: results too small for a
+// normal number are zero, which takes the steps that would save them out of every element (gelu
+// over 8192 x 8192 outputs: 75 us, with __fdividef and __expf 99).
+__device__ __forceinline__ float recip(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 
+constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kRsqrt2 = 0.70710678118654752f;
 constexpr float kRsqrt2Pi = 0.39894228040143268f;
 constexpr float kTanhScale = 0.79788456080286536f;  // sqrt(2 / pi)
 constexpr float kTanhCubic = 0.044715f;
+
+__device__ __forceinline__ float logistic(float z) {
+  return recip(1.0f + exp2_fast(-kLog2e * z));
+}
+
+// (1 + tanh(a)) / 2 = logistic(2 a) for a = sqrt(2 / pi) (z + kTanhCubic z^3)
+__device__ __forceinline__ float tanh_gate(float z) {
+  const float c = fmaf(-2.0f * kTanhScale * kTanhCubic * kLog2e, z * z,
+                       -2.0f * kTanhScale * kLog2e);
+  return recip(1.0f + exp2_fast(z * c));
+}
 
 // Phi(z), the standard normal distribution function, and exp(-z^2 / 2), by the polynomial
 // 7.1.26 of Abramowitz and Stegun for erfc(|z| / sqrt 2): absolute error below 1e-7, and the
 // factor exp(-z^2 / 2) keeps it small against the far negative values too. A reciprocal, an
 // exponential and eight multiply-adds.
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
-  const float x = fabsf(z) * kRsqrt2;
-  const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
-  e = __expf(-x * x);
-  float p = fmaf(1.061405429f, t, -1.453152027f);
-  p = fmaf(p, t, 1.421413741f);
-  p = fmaf(p, t, -0.284496736f);
-  p = fmaf(p, t, 0.254829592f);
-  const float half = 0.5f * p * t * e;
+  const float t = recip(fmaf(0.3275911f * kRsqrt2, fabsf(z), 1.0f));
+  e = exp2_fast(z * z * (-0.5f * kLog2e));
+  float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+  p = fmaf(p, t, 0.5f * 1.421413741f);
+  p = fmaf(p, t, 0.5f * -0.284496736f);
+  p = fmaf(p, t, 0.5f * 0.254829592f);
+  const float half = p * t * e;
   return z < 0.0f ? half : 1.0f - half;
 }
 
@@ -63,9 +86,7 @@ __device__ __forceinline__ float act_value(float z, int act) {
       float e;
       return z * normal_cdf(z, e);
     }
-    case COLL_ACT_GELU_TANH:
-      // (1 + tanh(a)) / 2 = logistic(2 a)
-      return z * logistic(2.0f * kTanhScale * fmaf(kTanhCubic * z * z, z, z));
+    case COLL_ACT_GELU_TANH: return z * tanh_gate(z);
     case COLL_ACT_SILU: return z * logistic(z);
     case COLL_ACT_SIGMOID: return logistic(z);
     default: return z;
@@ -87,7 +108,7 @@ __device__ __forceinline__ void act_value_slope(float z, int act, float &v, floa
       return;
     }
     case COLL_ACT_GELU_TANH: {
-      const float s = logistic(2.0f * kTanhScale * fmaf(kTanhCubic * z * z, z, z));
+      const float s = tanh_gate(z);
       v = z * s;
       d = fmaf(v * (1.0f - s), 2.0f * kTanhScale * fmaf(3.0f * kTanhCubic * z, z, 1.0f), s);
       return;
@@ -166,17 +187,17 @@ __device__ __forceinline__ void st_16b(void *p, const uint32_t *r) {
                : "memory");
 }
 
-// WORDS 32-bit words of a row from a 16-byte boundary on, in as many whole sectors as there are:
-// where every other row starts in the middle of a sector, its first and last 16 bytes go alone
-// (8192 x 8200 written in 16-byte accesses: 69 us).
+// WORDS 32-bit words of a row from a 16-byte boundary on, whole sectors at a time where the row
+// starts on one. Where every other row starts in the middle of a sector, stores write the first
+// and last 16 bytes alone (8192 x 8200 written in 16-byte accesses: 69 us, so: 62); loads are 16
+// bytes each, whose registers lie the same way in both forms, so that what was asked for ahead
+// need not be moved, and waited for, before its use.
 template <int WORDS>
 __device__ __forceinline__ void ld_row(const void *p, uint32_t *r) {
   const char *q = static_cast<const char *>(p);
   if ((uintptr_t)p & 16u) {
-    ld_16b(q, r);
 #pragma unroll
-    for (int i = 4; i < WORDS - 4; i += 8) ld_32b(q + 4 * i, r + i);
-    ld_16b(q + 4 * (WORDS - 4), r + WORDS - 4);
+    for (int i = 0; i < WORDS; i += 4) ld_16b(q + 4 * i, r + i);
   } else {
 #pragma unroll
     for (int i = 0; i < WORDS; i += 8) ld_32b(q + 4 * i, r + i);
@@ -363,14 +384,16 @@ __device__ __forceinline__ void staged_add(uint32_t *st, const void *p, int64_t 
   add_halves(v, w, type);
 }
 
-// v[i] += bias of column i, for every row
-__device__ __forceinline__ void add_bias(const DenseEpi &e, int64_t col, int cols,
-                                         float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-  const float b =
-      lane < cols ? ld_elem(e.bias, (col + lane) * e.bias_stride, e.type) : 0.0f;
+// v[i] += b of lane i, through the warp's block
+__device__ __forceinline__ void add_lanes(uint32_t *st, float b, float (&v)[32]) {
+  __syncwarp();
+  st[threadIdx.x & 31] = __float_as_uint(b);
+  __syncwarp();
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] += __shfl_sync(~0u, b, i);
+  for (int i = 0; i < 32; i += 4) {
+    const float4 w = *reinterpret_cast<const float4 *>(st + i);
+    v[i] += w.x, v[i + 1] += w.y, v[i + 2] += w.z, v[i + 3] += w.w;
+  }
 }
 
 // One element: g holds the product (gated: the gate's), u the up product; b the bias.

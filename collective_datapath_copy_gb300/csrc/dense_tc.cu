@@ -290,6 +290,19 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
     const int quad = warp & 3, part = (warp - 4) >> 2;
     uint32_t *const st = staged + (warp - 4) * 32 * kPitch;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    // The residual's lines of a tile into L2 while its products run, a lane for its row, every
+    // other line each of the two warps of a row: a block then waits for L2, not for HBM (8192 x
+    // 8192 with bias, gelu and residual: 124 -> 109 us).
+    auto fetch = [&](const Tile &tl) {
+      const TcProb &q = p.prob[tl.prob];
+      const int64_t row = tl.m0 + rank * 128 + quad * 32 + lane;
+      if (GATED || !q.e.res || q.e.res_cs != 1 || row >= q.m) return;
+      const int cols = (int)min((int64_t)q.tile_cols, q.n - tl.n0);
+      const int es = q.e.out_type == COLL_F32 ? 4 : 2, line = 128 / es;
+      const char *at = static_cast<const char *>(q.e.res) + (row * q.e.res_rs + tl.n0) * es;
+      for (int c = part * line; c < cols; c += 2 * line)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + c * es));
+    };
     for (uint32_t it = 0; walk.at(p, it, tl); ++it) {
       const TcProb &q = p.prob[tl.prob];
       const DenseEpi &e = q.e;
@@ -298,11 +311,17 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
       const int64_t row0 = tl.m0 + rank * 128 + quad * 32, row = row0 + lane;
       const bool live = row < q.m;
       const int cols = (int)min((int64_t)q.tile_cols, q.n - tl.n0);
-      uint32_t r[16];  // the residual of the next 32 columns, asked for ahead
+      // The bias (a lane's column) and the residual of the next 32 columns, asked for ahead: the
+      // bias loaded at its use cost 20 to 40 us of 8192 x 8192 outputs.
+      uint32_t r[16];
+      uint16_t bias = 0;
       auto ask = [&](int c0) {
+        if (!GATED && e.bias && c0 + lane < cols)
+          bias = static_cast<const uint16_t *>(e.bias)[(tl.n0 + c0 + lane) * e.bias_stride];
         if (pre_res && live && c0 + 32 <= cols) ld_halves(e.res, row * e.res_rs + tl.n0 + c0, r);
       };
       ask(part * 32);
+      fetch(tl);
       if (!__all_sync(~0u, wait_bar(&sh.abort, smem_u32(&sh.acc_full[buf]), (it >> 1) & 1u,
                                     p.status)))
         break;
@@ -343,15 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
 #pragma unroll
           for (int i = 0; i < 32; ++i) g[i] *= u[i];
         } else {
-          if (e.bias) {
-            if (vec) {
-              uint32_t b[16];
-              ld_halves(e.bias, col, b);
-              add_halves(g, b, e.type);
-            } else {
-              add_bias(e, col, left, g);
-            }
-          }
+          if (e.bias) add_lanes(st, h2f(bias, e.type), g);
           if (e.pre) store(e.pre, e.pre_rs, e.type, g);
           act_run(g, e.act);
           if (e.res) {
@@ -362,7 +373,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
                          e.res_rs, e.res_cs, e.out_type, rows, left, g);
             } else if (pre_res) {
               add_halves(g, r, e.type);
-              ask(c0 + 64);
             } else if (live) {
               const float *rp = static_cast<const float *>(e.res) + row * e.res_rs + col;
               uint32_t x[32];
@@ -371,6 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kernel(const __grid_constant__
               for (int i = 0; i < 32; ++i) g[i] += __uint_as_float(x[i]);
             }
           }
+          ask(c0 + 64);
         }
         store(e.out[tl.batch], e.out_rs[tl.batch], e.out_type, g);
       }
@@ -438,9 +449,10 @@ cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStre
 float epilogue_ns(const DenseJob &j, int split) {
   if (split > 1) return 14.0f;
   const DenseEpi &e = j.e;
-  const float act = j.gated || e.act == COLL_ACT_NONE || e.act == COLL_ACT_RELU ? 0.0f : 18.0f;
-  return 7.0f + (e.out_type == COLL_F32 ? 7.0f : 0.0f) + (e.res ? 9.5f : 0.0f) +
-         (e.pre ? 5.0f : 0.0f) + (e.gate ? 8.0f : 0.0f) + act + (e.vec ? 0.0f : 4.0f);
+  const float act = j.gated || e.act == COLL_ACT_NONE || e.act == COLL_ACT_RELU ? 0.0f : 6.0f;
+  return 7.0f + (e.out_type == COLL_F32 ? 7.0f : 0.0f) + (e.res ? 8.5f : 0.0f) +
+         (e.bias ? 2.0f : 0.0f) + (e.pre ? 5.0f : 0.0f) + (e.gate ? 8.0f : 0.0f) + act +
+         (e.vec ? 0.0f : 4.0f);
 }
 
 int operands_a(const DenseJob &j) { return j.nbatch == 2 || j.nseg == 2 ? 2 : 1; }
@@ -474,10 +486,10 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
   // its k blocks times 62 ns and 1.08 a column (measured at 4096 x 4096 x 8192: 144 ns for 64
   // columns, 186 for 128, 264 for 192, 339 for 256) or the time of its epilogue beside the next
   // tile's products, and every cluster its tiles one after the other; the last epilogue comes on
-  // top. An epilogue takes 1.35 us and 7 ns a column, 9.5 more for a residual and 18 for an
-  // activation (8192 x 8192 x 64: 52 us plain, 86 with a residual, 160 with everything); where
-  // both take long, not all of the shorter one is hidden (4864 rows, k = 512, 256 columns: 4.05 us
-  // a round of 2.7 and 3.2).
+  // top. An epilogue takes 1.35 us and 7 ns a column, 8.5 more for a residual, 6 for an activation
+  // and 2 for a bias (8192 x 8192 x 64: 53 us plain, 84 with a residual, 75 with gelu, 109 with
+  // everything); where both take long, not all of the shorter one is hidden (4864 rows, k = 512,
+  // 256 columns: 4.05 us a round of 2.7 and 3.2).
   // Joining shares costs a launch and their way through L2. Calls of a few us wait for this, so it
   // tries no more than it has to.
   struct Option {
