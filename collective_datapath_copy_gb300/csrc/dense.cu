@@ -244,10 +244,11 @@ bool few_tokens_turned(const DenseJob &j) {
   return (j.a[0].cs == 1 || j.k == 1) && along_n(j.b[0]) && (!j.gated || along_n(j.b[1]));
 }
 
-// One product, or two independent ones; only counts their workspace where `dry`. `join`: column
-// sums that a launch of tensor-core products takes along.
+// One product, or two independent ones, after the elementwise step `act`, if there is one; only
+// counts their workspace where `dry`. Column sums that the step leaves to be added are taken along
+// by the launch of the products.
 int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
-             const coll::DenseJoin *join = nullptr) {
+             const DenseActBwd *act = nullptr) {
   coll::TcJob todo[2];
   coll::DensePack pack = {};
   int n = 0;
@@ -291,9 +292,14 @@ int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
       if (ws.part[i]) p.prob[i].part = static_cast<float *>(ws.take(ws.part[i]));
   }
   if (dry) return COLL_OK;
-  if (pack.count && coll::dense_pack(pack, s) != cudaSuccess) return COLL_ECUDA;
+  coll::DenseJoin join = {};
+  if (act) {
+    if (coll::dense_act_bwd(*act, pack, join, s) != cudaSuccess) return COLL_ECUDA;
+  } else if (pack.count && coll::dense_pack(pack, s) != cudaSuccess) {
+    return COLL_ECUDA;
+  }
   if (n == 0) {
-    if (join) return coll::dense_join(*join, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+    if (join.db) return coll::dense_join(join, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
     return COLL_OK;
   }
   if (skinny) {
@@ -302,7 +308,7 @@ int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
     if (c) return c;
     return coll::skinny_run(q, todo[0].j->gated != 0, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
   }
-  if (join) p.join = *join;
+  p.join = join;
   return coll::tc_run(p, todo, n, s);
 }
 
@@ -385,16 +391,12 @@ int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
     b.dz = dz.ptr;
     b.ld = dz.rs;
   }
-  bool later = false;  // db's row blocks are joined by the launch of the products
   if (a.db) {
     b.db = a.db;
     const int64_t blocks = coll::dense_act_bwd_row_blocks(a.m, a.n, true);
-    later = blocks > 1 && a.n > 0;
-    if (later) b.part = static_cast<float *>(ws.take((uint64_t)blocks * a.n * 4));
+    if (blocks > 1) b.part = static_cast<float *>(ws.take((uint64_t)blocks * a.n * 4));
   }
-  coll::DenseJoin join = {};
-  if ((b.db || (dz.ptr != a.dy.ptr && a.m > 0)) && a.n > 0 && !dry)
-    if (coll::dense_act_bwd(b, join, s) != cudaSuccess) return COLL_ECUDA;
+  const bool step = (a.db || (b.dz && a.m > 0)) && a.n > 0;
   DenseJob jobs[2];
   int n = 0;
   if (a.dx.ptr) {  // dx(m, k) = sum over n of dz(m, n) w(n, k)
@@ -412,7 +414,7 @@ int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
     j.e.out_type = (int32_t)a.grad_dtype;
     set_out(j, 0, a.dw);
   }
-  return products(jobs, n, ws, dry, s, later ? &join : nullptr);
+  return products(jobs, n, ws, dry, s, step ? &b : nullptr);
 }
 
 // ---- h = act(x w_gate^T) (x w_up^T)
@@ -471,22 +473,18 @@ int check(const coll_gated_bwd_t &a) {
 int run(const coll_gated_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
   if (!a.dx.ptr && !a.dw_gate.ptr) return COLL_OK;
   const coll_mat_t dg = scratch(ws, a.m, a.n), du = scratch(ws, a.m, a.n);
-  if (a.m > 0 && a.n > 0 && !dry) {
-    DenseActBwd b = {};
-    b.m = a.m;
-    b.n = a.n;
-    b.dy = mat(a.dh);
-    b.pre = mat(a.gate);
-    b.up = mat(a.up);
-    b.dz = dg.ptr;
-    b.du = du.ptr;
-    b.ld = dg.rs;
-    b.type = (int32_t)a.dtype;
-    b.act = (int32_t)a.act;
-    b.gated = 1;
-    coll::DenseJoin none;
-    if (coll::dense_act_bwd(b, none, s) != cudaSuccess) return COLL_ECUDA;
-  }
+  DenseActBwd b = {};
+  b.m = a.m;
+  b.n = a.n;
+  b.dy = mat(a.dh);
+  b.pre = mat(a.gate);
+  b.up = mat(a.up);
+  b.dz = dg.ptr;
+  b.du = du.ptr;
+  b.ld = dg.rs;
+  b.type = (int32_t)a.dtype;
+  b.act = (int32_t)a.act;
+  b.gated = 1;
   DenseJob jobs[2];
   int n = 0;
   if (a.dx.ptr) {  // dx = dg w_gate + du w_up: one sum over both
@@ -510,7 +508,7 @@ int run(const coll_gated_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
     set_out(j, 0, a.dw_gate);
     set_out(j, 1, a.dw_up);
   }
-  return products(jobs, n, ws, dry, s);
+  return products(jobs, n, ws, dry, s, a.m > 0 && a.n > 0 ? &b : nullptr);
 }
 
 // Checks, then the counting pass: workspace bytes, or a code.

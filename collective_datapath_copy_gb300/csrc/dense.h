@@ -64,20 +64,21 @@ struct DenseActBwd {
   float *part;           // column sums of each row block, [row_blocks][n]
   int32_t type, db_type, act, gated;
 };
-int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums);
-// With more than one row block, db is only complete after the join that `join` receives.
-cudaError_t dense_act_bwd(const DenseActBwd &a, DenseJoin &join, cudaStream_t s);
-cudaError_t dense_join(const DenseJoin &join, cudaStream_t s);
-
 // dst[i * ld + j] = src(i, j): operands whose strides or base no tensor map takes, laid out in
-// rows of whole 16-byte runs, all of a product's in one launch.
+// rows of whole 16-byte runs, all of a call's in one launch.
 struct DensePack {
   DenseMat src[4];
   int64_t rows[4], cols[4], ld[4];
-  int64_t parts[4];  // pieces of a row (dense_pack sets them)
+  int64_t parts[4];  // pieces of a row, and below the CTAs for an operand (set at the launch)
+  unsigned ctas;
   uint16_t *dst[4];
   int count;
 };
+int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums);
+// Lays out `pack` too, in the same launch if that is not much. With more than one row block, db is only complete after the
+// join that `join` receives.
+cudaError_t dense_act_bwd(const DenseActBwd &a, DensePack &pack, DenseJoin &join, cudaStream_t s);
+cudaError_t dense_join(const DenseJoin &join, cudaStream_t s);
 cudaError_t dense_pack(DensePack &p, cudaStream_t s);
 
 // The job's epilogue over accumulators of zero (nothing to sum over).

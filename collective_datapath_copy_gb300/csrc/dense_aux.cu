@@ -50,13 +50,75 @@ __device__ __forceinline__ void store8(void *base, int64_t off, int type, const 
                  f2h2(v[6], v[7], type));
 }
 
-// Two rows a turn keep six 16-byte loads of a lane in flight (one row where loads are single
-// elements, which are many already).
-template <bool GATED, int ACT, int TYPE, int ALIGN>
-__global__ void __launch_bounds__(256, ALIGN == 16 ? 4 : 2) act_bwd_kernel(const DenseActBwd a,
-                                                         int64_t rows_per_block) {
+// Eight elements that start at p, on any 2-byte boundary: the two aligned 16-byte words that hold
+// them, shifted.
+__device__ __forceinline__ uint4 shifted8(const uint16_t *p) {
+  const uint32_t off = (uint32_t)((uintptr_t)p & 15u), word = off >> 2, bits = (off & 2u) * 8u;
+  const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - off);
+  const uint4 a = q[0], b = q[1];
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (word & 2) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (word & 1) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+// One of `ctas` CTAs that lay out operand o. A warp takes a row, a lane eight neighbouring
+// elements. Inside a row that is contiguous the loads are 16-byte words (all of whose bytes are
+// the row's); elsewhere single elements. 8183 x 10167: 68 us for 333 MB, 4.9 TB/s.
+__device__ __forceinline__ void pack_rows(const DensePack &a, int o, int64_t cta, int64_t ctas) {
+  const int lane = threadIdx.x & 31;
+  const DenseMat src = a.src[o];
+  const int64_t rows = a.rows[o], cols = a.cols[o], ld = a.ld[o];
+  const int64_t parts = a.parts[o], whole = (ld / 8 + parts - 1) / parts;  // runs of a part
+  for (int64_t w = cta * 8 + (threadIdx.x >> 5); w < rows * parts; w += ctas * 8) {
+    const int64_t r = parts == 1 ? w : w / parts, q0 = (w - r * parts) * whole;
+    const int64_t q1 = q0 + whole < ld / 8 ? q0 + whole : ld / 8;
+    const uint16_t *row = static_cast<const uint16_t *>(src.p) + r * src.rs;
+    for (int64_t q = q0 + lane; q < q1; q += 32) {
+      const int64_t c = q * 8;
+      const uint16_t *p = row + c * src.cs;
+      uint4 out;
+      if (src.cs == 1 && c >= 8 && c + 16 <= cols) {
+        out = shifted8(p);
+      } else {
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[i * src.cs] : 0u;
+        out = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
+                         v[6] | v[7] << 16);
+      }
+      *reinterpret_cast<uint4 *>(a.dst[o] + r * ld + c) = out;
+    }
+  }
+}
+
+__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ DensePack a) {
   griddep_launch();
   griddep_wait();
+  pack_rows(a, blockIdx.y, blockIdx.x, gridDim.x);
+}
+
+// Two rows a turn keep six 16-byte loads of a lane in flight (one row where loads are single
+// elements, which are many already). CTAs past the row blocks lay out the products' operands: a
+// launch of its own for that costs 2 to 4 us (777 x 1530 x 1016: 21 us, so: 17).
+template <bool GATED, int ACT, int TYPE, int ALIGN>
+__global__ void __launch_bounds__(256, ALIGN == 16 ? 4 : 2)
+    act_bwd_kernel(const DenseActBwd a, int64_t rows_per_block, unsigned row_blocks,
+                   const __grid_constant__ DensePack pack) {
+  griddep_launch();
+  griddep_wait();
+  if (blockIdx.y >= row_blocks) {
+    const unsigned i = (blockIdx.y - row_blocks) * gridDim.x + blockIdx.x, o = i / pack.ctas;
+    if (o < (unsigned)pack.count) pack_rows(pack, (int)o, i - o * pack.ctas, pack.ctas);
+    return;
+  }
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * COLS + lane * 8;
   const int64_t r0 = (int64_t)blockIdx.y * rows_per_block;
@@ -111,7 +173,7 @@ __global__ void __launch_bounds__(256, ALIGN == 16 ? 4 : 2) act_bwd_kernel(const
     float s = part[0][threadIdx.x];
 #pragma unroll
     for (int g = 1; g < GROUPS; ++g) s += part[g][threadIdx.x];
-    if (gridDim.y == 1) st_elem(a.db, c, s, a.db_type);
+    if (row_blocks == 1) st_elem(a.db, c, s, a.db_type);
     else a.part[(int64_t)blockIdx.y * a.n + c] = s;
   }
 }
@@ -122,7 +184,8 @@ uint64_t row_bits(const DenseMat &m) {
 }
 
 template <bool GATED, int ACT>
-cudaError_t launch_act_bwd(const DenseActBwd &a, dim3 grid, int64_t per, cudaStream_t s) {
+cudaError_t launch_act_bwd(const DenseActBwd &a, const DensePack &pack, dim3 grid, int64_t per,
+                           cudaStream_t s) {
   const uint64_t bits =
       (uint64_t)a.n * 2 | row_bits(a.dy) | row_bits(a.pre) | row_bits(a.up);
   const int align = bits % 16 == 0 ? 16 : bits % 4 == 0 ? 4 : 0;
@@ -133,7 +196,9 @@ cudaError_t launch_act_bwd(const DenseActBwd &a, dim3 grid, int64_t per, cudaStr
                     : (align == 16  ? act_bwd_kernel<GATED, ACT, COLL_F16, 16>
                        : align == 4 ? act_bwd_kernel<GATED, ACT, COLL_F16, 4>
                                     : act_bwd_kernel<GATED, ACT, COLL_F16, 0>);
-  return dense_launch(kernel, grid, 256, 0, 1, s, a, per);
+  const unsigned row_blocks = grid.y;
+  if (pack.count) grid.y += (pack.ctas * (unsigned)pack.count + grid.x - 1) / grid.x;
+  return dense_launch(kernel, grid, 256, 0, 1, s, a, per, row_blocks, pack);
 }
 
 __global__ void __launch_bounds__(256) join_kernel(const DenseJoin j) {
@@ -141,58 +206,6 @@ __global__ void __launch_bounds__(256) join_kernel(const DenseJoin j) {
   griddep_wait();
   const int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x;
   if (c < j.n) join_column(j, c);
-}
-
-// Eight elements that start at p, on any 2-byte boundary: the two aligned 16-byte words that hold
-// them, shifted.
-__device__ __forceinline__ uint4 shifted8(const uint16_t *p) {
-  const uint32_t off = (uint32_t)((uintptr_t)p & 15u), word = off >> 2, bits = (off & 2u) * 8u;
-  const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - off);
-  const uint4 a = q[0], b = q[1];
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  if (word & 2) {
-#pragma unroll
-    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
-  }
-  if (word & 1) {
-#pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
-  }
-  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
-                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
-}
-
-// A warp takes a row, a lane eight neighbouring elements. Inside a row that is contiguous the
-// loads are 16-byte words (all of whose bytes are the row's); elsewhere single elements. 8183 x
-// 10167: 68 us for 333 MB, 4.9 TB/s.
-__global__ void __launch_bounds__(256) pack_kernel(const __grid_constant__ DensePack a) {
-  griddep_launch();
-  griddep_wait();
-  const int o = blockIdx.y, lane = threadIdx.x & 31;
-  const DenseMat src = a.src[o];
-  const int64_t rows = a.rows[o], cols = a.cols[o], ld = a.ld[o];
-  const int64_t warps = (int64_t)gridDim.x * 8;
-  const int64_t parts = a.parts[o], whole = (ld / 8 + parts - 1) / parts;  // runs of a part
-  for (int64_t w = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); w < rows * parts; w += warps) {
-    const int64_t r = parts == 1 ? w : w / parts, q0 = (w - r * parts) * whole;
-    const int64_t q1 = q0 + whole < ld / 8 ? q0 + whole : ld / 8;
-    const uint16_t *row = static_cast<const uint16_t *>(src.p) + r * src.rs;
-    for (int64_t q = q0 + lane; q < q1; q += 32) {
-      const int64_t c = q * 8;
-      const uint16_t *p = row + c * src.cs;
-      uint4 out;
-      if (src.cs == 1 && c >= 8 && c + 16 <= cols) {
-        out = shifted8(p);
-      } else {
-        uint32_t v[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[i * src.cs] : 0u;
-        out = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
-                         v[6] | v[7] << 16);
-      }
-      *reinterpret_cast<uint4 *>(a.dst[o] + r * ld + c) = out;
-    }
-  }
 }
 
 template <bool GATED>
@@ -203,7 +216,7 @@ __global__ void __launch_bounds__(256) empty_sum_kernel(const DenseJob j) {
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
        i += (int64_t)gridDim.x * 256) {
     const int64_t r = i / j.n, c = i - r * j.n;
-    epilogue_one<GATED>(j.e, blockIdx.y, r, c, 0.0f, 0.0f, GATED ? 0.0f : bias_at(j.e, c));
+    epilogue_one<GATED>(j.e, blockIdx.y, r, c, 0.0f, 0.0f, ask_addends<GATED>(j.e, r, c));
   }
 }
 
@@ -212,9 +225,8 @@ unsigned grid_for(int64_t threads) {
   return (unsigned)(b < 4864 ? b : 4864);  // four CTAs of eight warps on each of 152 SMs, 8 deep
 }
 
-}  // namespace
-
-cudaError_t dense_pack(DensePack &p, cudaStream_t s) {
+// Pieces of each operand's rows and CTAs for each operand.
+void cut(DensePack &p) {
   int64_t most = 0;
   for (int i = 0; i < p.count; ++i) {
     // long rows are cut where there are too few of them for 16 warps on each of 152 SMs
@@ -222,7 +234,14 @@ cudaError_t dense_pack(DensePack &p, cudaStream_t s) {
     while (p.rows[i] * p.parts[i] < 2432 && p.ld[i] / 8 / p.parts[i] > 64) p.parts[i] *= 2;
     if (p.rows[i] * p.parts[i] > most) most = p.rows[i] * p.parts[i];
   }
-  return dense_launch(pack_kernel, dim3(grid_for(most * 32), (unsigned)p.count), 256, 0, 1, s, p);
+  p.ctas = grid_for(most * 32);
+}
+
+}  // namespace
+
+cudaError_t dense_pack(DensePack &p, cudaStream_t s) {
+  cut(p);
+  return dense_launch(pack_kernel, dim3(p.ctas, (unsigned)p.count), 256, 0, 1, s, p);
 }
 
 cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s) {
@@ -244,24 +263,35 @@ int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums) {
   return per ? (m + per - 1) / per : 1;
 }
 
-cudaError_t dense_act_bwd(const DenseActBwd &a, DenseJoin &join, cudaStream_t s) {
+cudaError_t dense_act_bwd(const DenseActBwd &a, DensePack &pack, DenseJoin &join,
+                          cudaStream_t s) {
+  // In this launch where the copies are small: they have fewer warps an SM here (176 MB: 60 us, in
+  // this launch 95), which is what a launch of their own costs at about 12 MB.
+  int64_t bytes = 0;
+  for (int i = 0; i < pack.count; ++i) bytes += pack.rows[i] * pack.ld[i] * 2;
+  if (bytes > (int64_t)12 << 20) {
+    const cudaError_t e = dense_pack(pack, s);
+    if (e != cudaSuccess) return e;
+    pack.count = 0;
+  }
+  cut(pack);
   const int64_t blocks = dense_act_bwd_row_blocks(a.m, a.n, a.db != nullptr);
   const int64_t per = (a.m + blocks - 1) / blocks;
   const dim3 grid((unsigned)((a.n + COLS - 1) / COLS), (unsigned)blocks);
   cudaError_t err;
   switch (a.act) {
-    case COLL_ACT_NONE: err = launch_act_bwd<false, COLL_ACT_NONE>(a, grid, per, s); break;
-#define COLL_ACT_CASE(act)                                         \
-  case act:                                                        \
-    err = a.gated ? launch_act_bwd<true, act>(a, grid, per, s)     \
-                  : launch_act_bwd<false, act>(a, grid, per, s);   \
+    case COLL_ACT_NONE: err = launch_act_bwd<false, COLL_ACT_NONE>(a, pack, grid, per, s); break;
+#define COLL_ACT_CASE(act)                                             \
+  case act:                                                            \
+    err = a.gated ? launch_act_bwd<true, act>(a, pack, grid, per, s)   \
+                  : launch_act_bwd<false, act>(a, pack, grid, per, s); \
     break;
     COLL_ACT_CASE(COLL_ACT_RELU)
     COLL_ACT_CASE(COLL_ACT_GELU)
     COLL_ACT_CASE(COLL_ACT_GELU_TANH)
     COLL_ACT_CASE(COLL_ACT_SILU)
 #undef COLL_ACT_CASE
-    default: err = launch_act_bwd<true, COLL_ACT_SIGMOID>(a, grid, per, s);
+    default: err = launch_act_bwd<true, COLL_ACT_SIGMOID>(a, pack, grid, per, s);
   }
   join = DenseJoin{a.part, blocks, a.n, !a.gated && blocks > 1 ? a.db : nullptr, a.db_type};
   return err;

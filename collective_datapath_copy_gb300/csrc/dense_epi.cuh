@@ -396,10 +396,29 @@ __device__ __forceinline__ void add_lanes(uint32_t *st, float b, float (&v)[32])
   }
 }
 
-// One element: g holds the product (gated: the gate's), u the up product; b the bias.
+// What the epilogue of one element adds, as it lies in memory: asked for before the sums it is
+// added to are there (one token, 4096 x 1792 with bias and residual: 4.6 us, asked for after: 5.4).
+struct Addends {
+  uint32_t bias, res;
+};
+
+template <bool GATED>
+__device__ __forceinline__ Addends ask_addends(const DenseEpi &e, int64_t row, int64_t col) {
+  Addends a = {0u, 0u};
+  if (GATED) return a;
+  if (e.bias) a.bias = static_cast<const uint16_t *>(e.bias)[col * e.bias_stride];
+  if (e.res) {
+    const int64_t at = row * e.res_rs + col * e.res_cs;
+    if (e.out_type == COLL_F32) a.res = static_cast<const uint32_t *>(e.res)[at];
+    else a.res = static_cast<const uint16_t *>(e.res)[at];
+  }
+  return a;
+}
+
+// One element: g holds the product (gated: the gate's), u the up product.
 template <bool GATED>
 __device__ __forceinline__ void epilogue_one(const DenseEpi &e, int batch, int64_t row, int64_t col,
-                                             float g, float u, float b) {
+                                             float g, float u, Addends a) {
   if (GATED) {
     if (e.gate) {
       st_elem(e.gate, row * e.gate_rs + col, g, e.type);
@@ -407,10 +426,11 @@ __device__ __forceinline__ void epilogue_one(const DenseEpi &e, int batch, int64
     }
     g = act_value(g, e.act) * u;
   } else {
-    g += b;
+    if (e.bias) g += h2f((uint16_t)a.bias, e.type);
     if (e.pre) st_elem(e.pre, row * e.pre_rs + col, g, e.type);
     g = act_value(g, e.act);
-    if (e.res) g += ld_elem(e.res, row * e.res_rs + col * e.res_cs, e.out_type);
+    if (e.res)
+      g += e.out_type == COLL_F32 ? __uint_as_float(a.res) : h2f((uint16_t)a.res, e.out_type);
   }
   st_elem(e.out[batch], row * e.out_rs[batch] + col, g, e.out_type);
 }

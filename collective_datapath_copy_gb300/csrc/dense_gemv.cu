@@ -177,6 +177,10 @@ __global__ void __launch_bounds__(kMostWarps<NT> * 32, 1)
   }
   float acc[NT][4] = {};
   griddep_wait();
+  // the first of the outputs that this thread finishes
+  Addends ahead = {0u, 0u};
+  if ((int)threadIdx.x < FEAT * (int)p.m && f0 + threadIdx.x % FEAT < p.n)
+    ahead = ask_addends<GATED>(p.e, threadIdx.x / FEAT, f0 + threadIdx.x % FEAT);
   const int steps = (len + kStep - 1) / kStep;
   for (int s = warp; s < steps; s += AHEAD * warps) {
     uint32_t a[AHEAD][8], b[AHEAD][8], x[AHEAD][NT][8];
@@ -244,7 +248,8 @@ __global__ void __launch_bounds__(kMostWarps<NT> * 32, 1)
       v += part[w][tok][f];
       if (GATED) u += part[w][tok][(f + 8) & 15];
     }
-    epilogue_one<GATED>(p.e, 0, tok, f0 + f, v, u, GATED ? 0.0f : bias_at(p.e, f0 + f));
+    if (i != (int)threadIdx.x) ahead = ask_addends<GATED>(p.e, tok, f0 + f);
+    epilogue_one<GATED>(p.e, 0, tok, f0 + f, v, u, ahead);
   }
 }
 
@@ -302,6 +307,9 @@ __global__ void __launch_bounds__(GATED ? 256 : 512, 1) gemv_t_kernel(
   const int left = (int)(p.n - fl < 4 ? p.n - fl : 4);  // outputs of this lane, may be negative
   float acc[W][4][4] = {};
   griddep_wait();
+  Addends ahead = {0u, 0u};  // the first of the outputs that this thread finishes
+  if ((int)threadIdx.x < kFeat * m && f0 + threadIdx.x % kFeat < p.n)
+    ahead = ask_addends<GATED>(p.e, threadIdx.x / kFeat, f0 + threadIdx.x % kFeat);
   const int steps = (len + 15) / 16;
   for (int s0 = warp; s0 < steps; s0 += AHEAD * warps) {
     uint2 w[AHEAD][W][4], x[AHEAD][2];
@@ -362,7 +370,8 @@ __global__ void __launch_bounds__(GATED ? 256 : 512, 1) gemv_t_kernel(
       v += part[c][0][tok][f];
       if (GATED) u += part[c][W - 1][tok][f];
     }
-    epilogue_one<GATED>(p.e, 0, tok, f0 + f, v, u, GATED ? 0.0f : bias_at(p.e, f0 + f));
+    if (i != (int)threadIdx.x) ahead = ask_addends<GATED>(p.e, tok, f0 + f);
+    epilogue_one<GATED>(p.e, 0, tok, f0 + f, v, u, ahead);
   }
 }
 

@@ -420,20 +420,28 @@ __global__ void __launch_bounds__(256) share_join_kernel(const __grid_constant__
   const int w = blockIdx.z;
   const DenseJob &j = s.j[w];
   const int64_t ld = s.part_ld[w], plane = j.m * ld, col = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (s.split[w] < 2 || col >= j.n) return;
-  const float bias = GATED ? 0.0f : bias_at(j.e, col);
+  const int split = s.split[w];
+  if (split < 2 || col >= j.n) return;
   const int64_t rows = j.m * j.nbatch, step = plane * j.nbatch * (GATED ? 2 : 1);
   for (int64_t r = blockIdx.y; r < rows; r += gridDim.y) {
     const int batch = r >= j.m;
     const int64_t row = r - batch * j.m;
     const float *p = s.part[w] + batch * plane + row * ld + col;
-    float g = p[0], u = GATED ? p[plane] : 0.0f;
-#pragma unroll 4
-    for (int i = 1; i < s.split[w]; ++i) {
-      g += p[i * step];
-      if (GATED) u += p[i * step + plane];
+    // everything in flight before the first is added
+    float a[kMostShares], b[GATED ? kMostShares : 1];
+#pragma unroll
+    for (int i = 0; i < kMostShares; ++i) {
+      a[i] = i < split ? p[i * step] : 0.0f;
+      if constexpr (GATED) b[i] = i < split ? p[i * step + plane] : 0.0f;
     }
-    epilogue_one<GATED>(j.e, batch, row, col, g, u, bias);
+    const Addends more = ask_addends<GATED>(j.e, row, col);
+    float g = a[0], u = GATED ? b[0] : 0.0f;
+#pragma unroll
+    for (int i = 1; i < kMostShares; ++i) {
+      g += a[i];
+      if constexpr (GATED) u += b[i];
+    }
+    epilogue_one<GATED>(j.e, batch, row, col, g, u, more);
   }
 }
 
