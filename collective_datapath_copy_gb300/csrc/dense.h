@@ -69,13 +69,12 @@ struct DenseActBwd {
 struct DensePack {
   DenseMat src[4];
   int64_t rows[4], cols[4], ld[4];
-  int64_t parts[4];  // pieces of a row, and below the CTAs for an operand (set at the launch)
-  unsigned ctas;
+  unsigned ctas;  // for an operand (set at the launch)
   uint16_t *dst[4];
   int count;
 };
 int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums);
-// Lays out `pack` too, in the same launch if that is not much. With more than one row block, db is only complete after the
+// Lays out `pack` in the same launch. With more than one row block, db is only complete after the
 // join that `join` receives.
 cudaError_t dense_act_bwd(const DenseActBwd &a, DensePack &pack, DenseJoin &join, cudaStream_t s);
 cudaError_t dense_join(const DenseJoin &join, cudaStream_t s);

@@ -50,12 +50,10 @@ __device__ __forceinline__ void store8(void *base, int64_t off, int type, const 
                  f2h2(v[6], v[7], type));
 }
 
-// Eight elements that start at p, on any 2-byte boundary: the two aligned 16-byte words that hold
-// them, shifted.
-__device__ __forceinline__ uint4 shifted8(const uint16_t *p) {
+// Eight elements that start at p, on any 2-byte boundary, out of the two aligned 16-byte words
+// that hold them.
+__device__ __forceinline__ uint4 shifted8(const uint16_t *p, const uint4 &a, const uint4 &b) {
   const uint32_t off = (uint32_t)((uintptr_t)p & 15u), word = off >> 2, bits = (off & 2u) * 8u;
-  const uint4 *q = reinterpret_cast<const uint4 *>(reinterpret_cast<uintptr_t>(p) - off);
-  const uint4 a = q[0], b = q[1];
   uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   if (word & 2) {
 #pragma unroll
@@ -69,32 +67,51 @@ __device__ __forceinline__ uint4 shifted8(const uint16_t *p) {
                     __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
 }
 
-// One of `ctas` CTAs that lay out operand o. A warp takes a row, a lane eight neighbouring
-// elements. Inside a row that is contiguous the loads are 16-byte words (all of whose bytes are
-// the row's); elsewhere single elements. 8183 x 10167: 68 us for 333 MB, 4.9 TB/s.
+// One of `ctas` CTAs that lay out operand o. A thread takes kRuns runs of eight elements, counted
+// through the rows, all in flight together. Inside a row that is contiguous the loads are 16-byte
+// words (all of whose bytes are the row's); elsewhere single elements. 8183 x 10167: 48 us for
+// 333 MB, 7.0 TB/s (two runs in flight 54, a warp for each row 68).
+constexpr int kRuns = 4;
+
 __device__ __forceinline__ void pack_rows(const DensePack &a, int o, int64_t cta, int64_t ctas) {
-  const int lane = threadIdx.x & 31;
   const DenseMat src = a.src[o];
-  const int64_t rows = a.rows[o], cols = a.cols[o], ld = a.ld[o];
-  const int64_t parts = a.parts[o], whole = (ld / 8 + parts - 1) / parts;  // runs of a part
-  for (int64_t w = cta * 8 + (threadIdx.x >> 5); w < rows * parts; w += ctas * 8) {
-    const int64_t r = parts == 1 ? w : w / parts, q0 = (w - r * parts) * whole;
-    const int64_t q1 = q0 + whole < ld / 8 ? q0 + whole : ld / 8;
-    const uint16_t *row = static_cast<const uint16_t *>(src.p) + r * src.rs;
-    for (int64_t q = q0 + lane; q < q1; q += 32) {
-      const int64_t c = q * 8;
-      const uint16_t *p = row + c * src.cs;
+  const uint32_t runs = (uint32_t)(a.ld[o] / 8), cols = (uint32_t)a.cols[o];
+  const int64_t total = a.rows[o] * runs;
+  for (int64_t at = cta * (256 * kRuns); at < total; at += ctas * (256 * kRuns)) {
+    const int64_t row0 = at / runs;
+    const uint32_t q0 = (uint32_t)(at - row0 * runs);
+    uint4 w[kRuns][2];
+    const uint16_t *p[kRuns];
+    uint32_t c[kRuns];
+    bool whole[kRuns], there[kRuns];
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      const uint32_t l = q0 + i * 256 + threadIdx.x, r = l / runs;
+      c[i] = (l - r * runs) * 8;
+      there[i] = at + i * 256 + threadIdx.x < total;
+      p[i] = static_cast<const uint16_t *>(src.p) + (row0 + r) * src.rs + c[i] * src.cs;
+      whole[i] = there[i] && src.cs == 1 && c[i] >= 8 && c[i] + 16 <= cols;
+      if (whole[i]) {
+        const uint4 *q = reinterpret_cast<const uint4 *>((uintptr_t)p[i] & ~(uintptr_t)15u);
+        w[i][0] = q[0];
+        w[i][1] = q[1];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kRuns; ++i) {
+      if (!there[i]) continue;
       uint4 out;
-      if (src.cs == 1 && c >= 8 && c + 16 <= cols) {
-        out = shifted8(p);
+      if (whole[i]) {
+        out = shifted8(p[i], w[i][0], w[i][1]);
       } else {
         uint32_t v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = c + i < cols ? p[i * src.cs] : 0u;
+        for (int k = 0; k < 8; ++k) v[k] = c[i] + k < cols ? p[i][k * src.cs] : 0u;
         out = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16,
                          v[6] | v[7] << 16);
       }
-      *reinterpret_cast<uint4 *>(a.dst[o] + r * ld + c) = out;
+      // rows of the copy follow one another
+      reinterpret_cast<uint4 *>(a.dst[o])[at + i * 256 + threadIdx.x] = out;
     }
   }
 }
@@ -225,16 +242,13 @@ unsigned grid_for(int64_t threads) {
   return (unsigned)(b < 4864 ? b : 4864);  // four CTAs of eight warps on each of 152 SMs, 8 deep
 }
 
-// Pieces of each operand's rows and CTAs for each operand.
+// CTAs for each operand: of the longest, no more than eight an SM.
 void cut(DensePack &p) {
   int64_t most = 0;
-  for (int i = 0; i < p.count; ++i) {
-    // long rows are cut where there are too few of them for 16 warps on each of 152 SMs
-    p.parts[i] = 1;
-    while (p.rows[i] * p.parts[i] < 2432 && p.ld[i] / 8 / p.parts[i] > 64) p.parts[i] *= 2;
-    if (p.rows[i] * p.parts[i] > most) most = p.rows[i] * p.parts[i];
-  }
-  p.ctas = grid_for(most * 32);
+  for (int i = 0; i < p.count; ++i)
+    if (p.rows[i] * (p.ld[i] / 8) > most) most = p.rows[i] * (p.ld[i] / 8);
+  const int64_t ctas = (most + 256 * kRuns - 1) / (256 * kRuns);
+  p.ctas = (unsigned)(ctas < 1216 ? ctas : 1216);
 }
 
 }  // namespace
@@ -265,15 +279,6 @@ int64_t dense_act_bwd_row_blocks(int64_t m, int64_t n, bool sums) {
 
 cudaError_t dense_act_bwd(const DenseActBwd &a, DensePack &pack, DenseJoin &join,
                           cudaStream_t s) {
-  // In this launch where the copies are small: they have fewer warps an SM here (176 MB: 60 us, in
-  // this launch 95), which is what a launch of their own costs at about 12 MB.
-  int64_t bytes = 0;
-  for (int i = 0; i < pack.count; ++i) bytes += pack.rows[i] * pack.ld[i] * 2;
-  if (bytes > (int64_t)12 << 20) {
-    const cudaError_t e = dense_pack(pack, s);
-    if (e != cudaSuccess) return e;
-    pack.count = 0;
-  }
   cut(pack);
   const int64_t blocks = dense_act_bwd_row_blocks(a.m, a.n, a.db != nullptr);
   const int64_t per = (a.m + blocks - 1) / blocks;

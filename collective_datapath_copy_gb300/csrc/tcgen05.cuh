@@ -227,8 +227,7 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// 32 columns of this warp's 32 lanes: v[c] of lane l is column c of row l. Call tmem_wait()
-// before using v.
+// 32 columns of this warp's 32 lanes: v[c] of lane l is column c of row l.
 __device__ __forceinline__ void tmem_load32(uint32_t addr, float (&v)[32]) {
   uint32_t r[32];
   asm volatile(
