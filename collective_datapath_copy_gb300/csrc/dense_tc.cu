@@ -21,10 +21,10 @@
 // of the tiles in flight in L2.
 //
 // Measured: 4096 x 4096 x 4096 75 us (1830 TFLOP/s); gated 8192 x 14336 x 4096 with everything kept
-// 1.01 ms alone (1900 TFLOP/s, tensor pipe 96 % busy) and 1.14 ms back to back, where the card's
+// 0.98 ms alone (1960 TFLOP/s, tensor pipe 96 % busy) and 1.12 ms back to back, where the card's
 // power cap sets the clock. Wide tiles are bound by the tensor pipe, tiles of up to 128 columns by
 // issuing (about 27 ns an instruction), sums of a few k blocks by the epilogue's way to HBM
-// (8192 x 8192 x 64: 52 us, 2.6 TB/s of writes, where filling the same memory reaches 3.4).
+// (8192 x 8192 x 64: 53 us, 2.5 TB/s of writes, where filling the same memory reaches 3.4).
 //
 // Every wait is bounded: a wait that runs out sets an abort flag, the CTA's roles leave their
 // loops, in-flight copies and products get time to land, TMEM is freed, and status says so.
