@@ -102,23 +102,23 @@ struct Check {
   int code = COLL_OK;
   View in[8], out[4];
   int n_in = 0, n_out = 0;
-  void input(const View &v, bool needed = true) {
+  int input(const View &v, bool needed = true) {  // returns its place
     if (!code) code = check_mat(v, needed, false);
-    in[n_in++] = v;
+    in[n_in] = v;
+    return n_in++;
   }
   void output(const View &v, bool needed = true) {
     if (!code) code = check_mat(v, needed, true);
     out[n_out++] = v;
   }
-  // overlaps after every check above; `in_place`: an input that out[0] may equal
-  int finish(const View *in_place) {
+  // Overlaps after every check above. `in_place`: the place of the one input that out[0] may
+  // equal; another input of the same memory would be read after out[0] was written over it.
+  int finish(int in_place = -1) {
     if (code) return code;
     for (int o = 0; o < n_out; ++o) {
       for (int i = 0; i < n_in; ++i) {
         if (!shares(out[o], in[i])) continue;
-        if (o == 0 && in_place && in[i].p == in_place->p && same(out[o], in[i]) &&
-            same(*in_place, in[i]))
-          continue;
+        if (o == 0 && i == in_place && same(out[o], in[i])) continue;
         return COLL_EOVERLAP;
       }
       for (int q = 0; q < o; ++q)
@@ -327,14 +327,13 @@ int check(const coll_linear_t &a) {
     return COLL_EINVAL;
   const int oe = esize(a.out_dtype);
   Check k;
-  const View res = view(a.residual, a.m, a.n, oe);
   k.output(view(a.y, a.m, a.n, oe));
   k.output(view(a.pre, a.m, a.n, 2), false);
   k.input(view(a.x, a.m, a.k, 2));
   k.input(view(a.w, a.n, a.k, 2));
-  k.input(res, false);
+  const int res = k.input(view(a.residual, a.m, a.n, oe), false);
   k.input(View{a.bias, 1, a.n, 0, a.bias_stride, 2}, false);
-  return k.finish(a.residual.ptr ? &res : nullptr);
+  return k.finish(res);
 }
 
 int run(const coll_linear_t &a, Ws &ws, bool dry, cudaStream_t s) {
@@ -371,7 +370,7 @@ int check(const coll_linear_bwd_t &a) {
   k.input(view(a.pre, a.m, a.n, 2), a.act != COLL_ACT_NONE);
   k.input(view(a.x, a.m, a.k, 2), a.dw.ptr != nullptr);
   k.input(view(a.w, a.n, a.k, 2), a.dx.ptr != nullptr);
-  return k.finish(nullptr);
+  return k.finish();
 }
 
 int run(const coll_linear_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
@@ -430,7 +429,7 @@ int check(const coll_gated_t &a) {
   k.input(view(a.x, a.m, a.k, 2));
   k.input(view(a.w_gate, a.n, a.k, 2));
   k.input(view(a.w_up, a.n, a.k, 2));
-  return k.finish(nullptr);
+  return k.finish();
 }
 
 int run(const coll_gated_t &a, Ws &ws, bool dry, cudaStream_t s) {
@@ -467,7 +466,7 @@ int check(const coll_gated_bwd_t &a) {
   k.input(view(a.x, a.m, a.k, 2), a.dw_gate.ptr != nullptr);
   k.input(view(a.w_gate, a.n, a.k, 2), a.dx.ptr != nullptr);
   k.input(view(a.w_up, a.n, a.k, 2), a.dx.ptr != nullptr);
-  return k.finish(nullptr);
+  return k.finish();
 }
 
 int run(const coll_gated_bwd_t &a, Ws &ws, bool dry, cudaStream_t s) {
