@@ -53,6 +53,7 @@ def _entry(name):
 
 
 _raw_stream = torch._C._cuda_getCurrentRawStream  # torch.cuda.current_stream, 2 us cheaper
+_current_device = torch._C._cuda_getDevice
 
 
 def _weight(name, w):
@@ -135,7 +136,11 @@ class _Dense:
 
     def _launch(self, where, pack, fields):
         """Call an entry point on the current stream, with a workspace if it asks for one. The
-        size it last asked for is offered first, so that a loop over one size makes one call."""
+        size it last asked for is offered first, so that a loop over one size makes one call.
+        The library launches on the current device, which the weights' is made for the call."""
+        if _current_device() != self._dev:
+            with torch.cuda.device(self._dev):
+                return self._launch(where, pack, fields)
         fn, size = _entry(where)
         status = self._status.data_ptr()
         stream = _raw_stream(self._dev)  # the current stream's handle

@@ -349,8 +349,9 @@ const char *coll_strerror(int code);
  * calls round dz (dg, du) to the operands' type once before the products that read them.
  * Results do not depend on timing: every sum has a fixed order for given sizes and layouts.
  *
- * Calls enqueue on `stream` and return; they hold no state between calls and allocate nothing,
- * so calls on different streams may overlap when their workspaces differ, and calls may be
+ * Calls enqueue on `stream` and return. `stream` and every buffer belong to the current device:
+ * a call does not look for another, as stream 0 names each device's. They hold no state between
+ * calls and allocate nothing, so calls on different streams may overlap when their workspaces differ, and calls may be
  * captured into a CUDA graph. Buffers must stay live and unmodified until the stream has
  * passed the call. `status`: optional device int32 that receives COLL_ETIMEDOUT if a bounded
  * device wait expires (never cleared by a call). The workspace must be 16-byte aligned and
