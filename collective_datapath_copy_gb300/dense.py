@@ -112,9 +112,11 @@ def _new(m, cols, dtype, weight, like):
 
 
 @contextlib.contextmanager
-def _on(stream, tensors):
+def _on(stream, dev, tensors):
     """Run a call on another stream than the current one: allocations belong to that stream, and
     the caller's tensors are not handed out again before it has passed the call."""
+    if stream.device_index != dev:
+        raise ValueError(f"stream is of cuda:{stream.device_index}, the weights are on cuda:{dev}")
     with torch.cuda.stream(stream):
         yield
     for t in tensors:
@@ -185,7 +187,8 @@ class Linear(_Dense):
         torch.float32 (a partial for a binary32 sum; its residual is float32 too). residual may be
         `out` itself."""
         if stream is not None:
-            with _on(stream, (x, residual, out, pre, self.weight, self.bias, self._status)):
+            with _on(stream, self._dev, (x, residual, out, pre, self.weight, self.bias,
+                                         self._status)):
                 return self.forward(x, residual, out, out_dtype, save, pre)
         w, b, dev, keep = self.weight, self.bias, self._dev, []
         n, k = w.shape
@@ -226,7 +229,7 @@ class Linear(_Dense):
         needed (db follows the bias unless need_db says otherwise). The residual's gradient is dy
         itself. grad_dtype: the type of dw and db, the operands' or torch.float32."""
         if stream is not None:
-            with _on(stream, (dy, x, pre, dx, dw, db, self.weight, self._status)):
+            with _on(stream, self._dev, (dy, x, pre, dx, dw, db, self.weight, self._status)):
                 return self.backward(dy, x, pre, need_dx, need_dw, need_db, dx, dw, db,
                                      grad_dtype)
         w, dev, keep = self.weight, self._dev, []
@@ -285,7 +288,7 @@ class GatedFFN(_Dense):
         """x [..., K] -> h [..., F]. With `save`, returns (h, gate, up): the two products, which
         backward needs."""
         if stream is not None:
-            with _on(stream, (x, out, gate, up, self.w_gate, self.w_up, self._status)):
+            with _on(stream, self._dev, (x, out, gate, up, self.w_gate, self.w_up, self._status)):
                 return self.forward(x, out, save, gate, up)
         w, wu, dev, keep = self.w_gate, self.w_up, self._dev, []
         n, k = w.shape
@@ -313,8 +316,8 @@ class GatedFFN(_Dense):
         is not needed. gate and up: what forward kept. grad_dtype: the type of dw_gate and dw_up,
         the operands' or torch.float32."""
         if stream is not None:
-            with _on(stream, (dh, x, gate, up, dx, dw_gate, dw_up, self.w_gate, self.w_up,
-                              self._status)):
+            with _on(stream, self._dev, (dh, x, gate, up, dx, dw_gate, dw_up, self.w_gate,
+                                         self.w_up, self._status)):
                 return self.backward(dh, x, gate, up, need_dx, need_dw, dx, dw_gate, dw_up,
                                      grad_dtype)
         w, wu, dev, keep = self.w_gate, self.w_up, self._dev, []

@@ -46,3 +46,32 @@ def test_a_call_is_launched_on_the_device_of_the_weights(monkeypatch, current, d
     operator(dev)._launch("coll_linear", lambda *fields: fields, (8, 32, 64))
     assert m.launches == [(dev, 100 + dev)]
     assert m.current == current
+
+
+class Stream:
+    def __init__(self, dev):
+        self.device_index = dev
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Its handle would be ignored: the call looks up the current stream of the weights' device."""
+    m = Machine(monkeypatch, 0)
+    monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
+    w = torch.zeros(8, 16, dtype=torch.bfloat16)
+    lin, ffn = operator(-1), object.__new__(dense.GatedFFN)   # -1: where torch's CPU tensors are
+    m.current = -1
+    lin.weight, lin.bias, lin.act = w, None, "none"
+    ffn.w_gate, ffn.w_up, ffn.act = w, w, "silu"
+    ffn._start(torch.device("cpu"))
+    x, y = torch.zeros(4, 16, dtype=w.dtype), torch.zeros(4, 8, dtype=w.dtype)
+    calls = [lambda s: lin.forward(x, out=y, stream=s), lambda s: lin.backward(y, x, stream=s),
+             lambda s: ffn.forward(x, out=y, stream=s),
+             lambda s: ffn.backward(y, x, y, y, stream=s)]
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: None)
+    for call in calls:
+        with pytest.raises(ValueError, match="stream"):
+            call(Stream(1))
+    assert m.launches == []
+    for call in calls:
+        call(Stream(-1))
+    assert len(m.launches) == len(calls)
