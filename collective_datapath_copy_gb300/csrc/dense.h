@@ -4,6 +4,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "coll.h"
 
 namespace coll {
@@ -104,5 +106,27 @@ cudaError_t dense_launch(void (*kernel)(P...), dim3 grid, unsigned threads, uint
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<A &&>(args)...);
 }
+
+// Shared memory past 48 KiB that a kernel may ask for: the runtime keeps the limit for each device,
+// so it is set by the first launch on each (a stream capture then records the launch alone). One
+// object for each kernel.
+class DenseSmemLimit {
+ public:
+  cudaError_t operator()(const void *kernel, uint32_t bytes) {
+    int dev = 0;
+    const cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const bool kept = dev >= 0 && dev < kDevices;
+    if (kept && set_[dev].load(std::memory_order_acquire)) return cudaSuccess;
+    const cudaError_t r =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    if (r == cudaSuccess && kept) set_[dev].store(true, std::memory_order_release);
+    return r;
+  }
+
+ private:
+  static constexpr int kDevices = 64;
+  std::atomic<bool> set_[kDevices] = {};
+};
 
 }  // namespace coll

@@ -227,9 +227,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 template <bool GATED>
 cudaError_t launch(const SkinnyParams &p, cudaStream_t s) {
-  static const cudaError_t ready = cudaFuncSetAttribute(
-      skinny_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-  if (ready != cudaSuccess) return ready;
+  static DenseSmemLimit limit;
+  const cudaError_t e = limit((const void *)skinny_kernel<GATED>, kTcSmem);
+  if (e != cudaSuccess) return e;
   return dense_launch(skinny_kernel<GATED>, dim3(p.tiles), kThreads, p.smem, 1, s, p);
 }
 

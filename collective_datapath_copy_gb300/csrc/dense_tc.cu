@@ -447,9 +447,9 @@ __global__ void __launch_bounds__(256) share_join_kernel(const __grid_constant__
 
 template <bool GATED>
 cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStream_t s) {
-  static const cudaError_t ready = cudaFuncSetAttribute(
-      tc_kernel<GATED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem);
-  if (ready != cudaSuccess) return ready;
+  static DenseSmemLimit limit;
+  const cudaError_t e = limit((const void *)tc_kernel<GATED>, kTcSmem);
+  if (e != cudaSuccess) return e;
   return dense_launch(tc_kernel<GATED>, dim3(clusters * CG), kThreads, smem, CG, s, p);
 }
 
