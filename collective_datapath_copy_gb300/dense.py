@@ -44,6 +44,19 @@ _NONE = (0, 0, 0)
 _entries = {}
 
 
+def _mask(kinds):
+    """Over a packed structure as one number: whole fields (.), of an address (a) its place within
+    16 bytes, nothing of the workspace and status at the end. Two calls alike in this, and in which
+    optional arrays are there, need the same workspace."""
+    return sum((15 if kind == "a" else 2 ** 64 - 1) << 64 * i for i, kind in enumerate(kinds))
+
+
+_MASK = {"coll_linear": _mask("......" + "a.." * 5 + "a."),
+         "coll_linear_backward": _mask("......" + "a.." * 6 + "a"),
+         "coll_gated_ffn": _mask("....." + "a.." * 6),
+         "coll_gated_ffn_backward": _mask("......" + "a.." * 9)}
+
+
 def _entry(name):
     e = _entries.get(name)
     if e is None:
@@ -136,29 +149,41 @@ class _Dense:
         stream."""
         return int(self._status.item())
 
-    def _launch(self, where, pack, fields):
-        """Call an entry point on the current stream, with a workspace if it asks for one. The
-        size it last asked for is offered first, so that a loop over one size makes one call.
-        The library launches on the current device, which the weights' is made for the call."""
+    def _launch(self, where, pack, fields, given=False):
+        """Call an entry point on the current stream, with the workspace it needs. The size of the
+        last call is kept with what decided it, so that a loop over one size asks once and a
+        smaller call is not given a larger one's workspace; a call after one that needed none is
+        first made without. `given`: whether the one optional array is there whose strides do not
+        tell. The library launches on the current device, which the weights' is made for the call.
+        """
         if _current_device() != self._dev:
             with torch.cuda.device(self._dev):
-                return self._launch(where, pack, fields)
+                return self._launch(where, pack, fields, given)
         fn, size = _entry(where)
         status = self._status.data_ptr()
         stream = _raw_stream(self._dev)  # the current stream's handle
-        need = self._need.get(where, 0)
-        while True:
-            if need:
-                ws = torch.empty(need, dtype=torch.uint8, device=self._status.device)
-                code = fn(pack(*fields, ws.data_ptr(), need, status), stream)
-            else:
-                code = fn(pack(*fields, 0, 0, status), stream)
-            if code != _EWORKSPACE:
-                break
-            need = int(size(pack(*fields, 0, 0, status)))
+
+        def fit():
+            plain = pack(*fields, 0, 0, status)
+            key = (int.from_bytes(plain, "little") & _MASK[where], given)
+            kept = self._need.get(where)
+            if kept is not None and kept[1] == key:
+                return kept[0]
+            need = int(size(plain))
             if need < 0:
                 check(need, where)
-            self._need[where] = need
+            self._need[where] = (need, key)
+            return need
+
+        kept = self._need.get(where)
+        need = fit() if kept is not None and kept[0] else 0
+        if not need:
+            code = fn(pack(*fields, 0, 0, status), stream)
+            if code == _EWORKSPACE:
+                need = fit()
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=self._status.device)
+            code = fn(pack(*fields, ws.data_ptr(), need, status), stream)
         if code:
             check(code, where)
 
@@ -218,7 +243,7 @@ class Linear(_Dense):
         self._launch("coll_linear", _LINEAR.pack,
                      (m, n, k, _TYPE[dt], _TYPE[ot], ACT[self.act], *xm, w.data_ptr(),
                       *w.stride(), *rm, *pm, *ym, 0 if b is None else b.data_ptr(),
-                      0 if b is None else b.stride(0)))
+                      0 if b is None else b.stride(0)), residual is not None)
         return out if pre is None else (out, pre)
 
     __call__ = forward
@@ -264,7 +289,7 @@ class Linear(_Dense):
             dbp = db.data_ptr()
         self._launch("coll_linear_backward", _LINEAR_BWD.pack,
                      (m, n, k, _TYPE[dt], _TYPE[gt], ACT[self.act], *dym, *pm, *xm, w.data_ptr(),
-                      *w.stride(), *dxm, *dwm, dbp))
+                      *w.stride(), *dxm, *dwm, dbp), need_db)
         return (dx if need_dx else None, dw if need_dw else None, db if need_db else None)
 
 
