@@ -244,30 +244,34 @@ bool few_tokens_turned(const DenseJob &j) {
   return (j.a[0].cs == 1 || j.k == 1) && along_n(j.b[0]) && (!j.gated || along_n(j.b[1]));
 }
 
+// The job through a kernel that takes its operands as they lie.
+enum Direct { kNotDirect, kEmptySum, kGemv, kGemvTurned };
+
+cudaError_t run_direct(const DenseJob &j, Direct how, cudaStream_t s) {
+  return how == kEmptySum ? coll::dense_empty_sum(j, s)
+         : how == kGemv   ? coll::gemv_run(j, s)
+                          : coll::gemv_t_run(j, s);
+}
+
 // One product, or two independent ones, after the elementwise step `act`, if there is one; only
 // counts their workspace where `dry`. Column sums that the step leaves to be added are taken along
-// by the launch of the products.
+// by the launch of the products. Nothing is launched before all that may be refused has been asked
+// for: shapes, tensor maps, shared memory.
 int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
              const DenseActBwd *act = nullptr) {
   coll::TcJob todo[2];
+  Direct direct[2] = {};
   coll::DensePack pack = {};
   int n = 0;
   for (int i = 0; i < count; ++i) {
     DenseJob &j = jobs[i];
     if (j.m == 0 || j.n == 0) continue;
     set_vec(j);
-    if (j.k == 0) {
-      if (!dry && coll::dense_empty_sum(j, s) != cudaSuccess) return COLL_ECUDA;
-      continue;
-    }
-    if (few_tokens(j)) {
-      if (!dry && coll::gemv_run(j, s) != cudaSuccess) return COLL_ECUDA;
-      continue;
-    }
-    if (few_tokens_turned(j)) {
-      if (!dry && coll::gemv_t_run(j, s) != cudaSuccess) return COLL_ECUDA;
-      continue;
-    }
+    direct[i] = j.k == 0               ? kEmptySum
+                : few_tokens(j)        ? kGemv
+                : few_tokens_turned(j) ? kGemvTurned
+                                       : kNotDirect;
+    if (direct[i]) continue;
     coll::TcJob &t = todo[n++];
     t.j = &j;
     const int na = j.nbatch == 2 || j.nseg == 2 ? 2 : 1, nb = j.gated || j.nseg == 2 ? 2 : 1;
@@ -292,24 +296,25 @@ int products(DenseJob *jobs, int count, Ws &ws, bool dry, cudaStream_t s,
       if (ws.part[i]) p.prob[i].part = static_cast<float *>(ws.take(ws.part[i]));
   }
   if (dry) return COLL_OK;
-  coll::DenseJoin join = {};
-  if (act) {
-    if (coll::dense_act_bwd(*act, pack, join, s) != cudaSuccess) return COLL_ECUDA;
-  } else if (pack.count && coll::dense_pack(pack, s) != cudaSuccess) {
-    return COLL_ECUDA;
-  }
-  if (n == 0) {
-    if (join.db) return coll::dense_join(join, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
-    return COLL_OK;
-  }
-  if (skinny) {
-    coll::SkinnyParams q;
-    const int c = coll::skinny_plan(q, *todo[0].j, todo[0].b, todo[0].a[0]);
+  coll::SkinnyParams q;
+  if (n) {
+    const int c = skinny ? coll::skinny_plan(q, *todo[0].j, todo[0].b, todo[0].a[0])
+                         : coll::tc_prepare(p, todo, n);
     if (c) return c;
-    return coll::skinny_run(q, todo[0].j->gated != 0, s) == cudaSuccess ? COLL_OK : COLL_ECUDA;
   }
-  p.join = join;
-  return coll::tc_run(p, todo, n, s);
+  cudaError_t e = cudaSuccess;
+  for (int i = 0; i < count && e == cudaSuccess; ++i)
+    if (direct[i]) e = run_direct(jobs[i], direct[i], s);
+  coll::DenseJoin join = {};
+  if (e == cudaSuccess && act) e = coll::dense_act_bwd(*act, pack, join, s);
+  else if (e == cudaSuccess && pack.count) e = coll::dense_pack(pack, s);
+  if (e == cudaSuccess) {
+    p.join = join;
+    if (skinny) e = coll::skinny_run(q, todo[0].j->gated != 0, s);
+    else if (n) e = coll::tc_run(p, todo, n, s);
+    else if (join.db) e = coll::dense_join(join, s);
+  }
+  return e == cudaSuccess ? COLL_OK : COLL_ECUDA;
 }
 
 // Scratch matrices.

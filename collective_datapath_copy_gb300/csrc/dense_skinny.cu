@@ -226,10 +226,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 }
 
 template <bool GATED>
-cudaError_t launch(const SkinnyParams &p, cudaStream_t s) {
+cudaError_t set_up() {
   static DenseSmemLimit limit;
-  const cudaError_t e = limit((const void *)skinny_kernel<GATED>, kTcSmem);
-  if (e != cudaSuccess) return e;
+  return limit((const void *)skinny_kernel<GATED>, kTcSmem);
+}
+
+template <bool GATED>
+cudaError_t launch(const SkinnyParams &p, cudaStream_t s) {
   return dense_launch(skinny_kernel<GATED>, dim3(p.tiles), kThreads, p.smem, 1, s, p);
 }
 
@@ -292,7 +295,9 @@ int skinny_plan(SkinnyParams &p, const DenseJob &j, const TcOperand *w, const Tc
     const int c = tc_encode(&p.w[i], w[i], j.e.type, (uint32_t)p.rows);
     if (c) return c;
   }
-  return tc_encode(&p.x, x, j.e.type, (uint32_t)p.cols);
+  const int c = tc_encode(&p.x, x, j.e.type, (uint32_t)p.cols);
+  if (c) return c;
+  return (j.gated ? set_up<true>() : set_up<false>()) == cudaSuccess ? COLL_OK : COLL_ECUDA;
 }
 
 cudaError_t skinny_run(const SkinnyParams &p, bool gated, cudaStream_t s) {

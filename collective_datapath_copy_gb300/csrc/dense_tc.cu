@@ -446,10 +446,13 @@ __global__ void __launch_bounds__(256) share_join_kernel(const __grid_constant__
 }
 
 template <bool GATED>
-cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStream_t s) {
+cudaError_t set_up() {
   static DenseSmemLimit limit;
-  const cudaError_t e = limit((const void *)tc_kernel<GATED>, kTcSmem);
-  if (e != cudaSuccess) return e;
+  return limit((const void *)tc_kernel<GATED>, kTcSmem);
+}
+
+template <bool GATED>
+cudaError_t launch(const TcParams &p, uint32_t clusters, uint32_t smem, cudaStream_t s) {
   return dense_launch(tc_kernel<GATED>, dim3(clusters * CG), kThreads, smem, CG, s, p);
 }
 
@@ -629,9 +632,7 @@ int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]
   return COLL_OK;
 }
 
-int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s) {
-  ShareJoin join = {};
-  int64_t cols = 0, rows = 0;
+int tc_prepare(TcParams &p, const TcJob *jobs, int count) {
   for (int i = 0; i < count; ++i) {
     const DenseJob &j = *jobs[i].j;
     TcProb &q = p.prob[i];
@@ -644,6 +645,17 @@ int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s) {
       const int c = tc_encode(&q.b[x], jobs[i].b[x], j.e.type, (uint32_t)q.b_box);
       if (c) return c;
     }
+  }
+  return (jobs[0].j->gated ? set_up<true>() : set_up<false>()) == cudaSuccess ? COLL_OK
+                                                                              : COLL_ECUDA;
+}
+
+cudaError_t tc_run(const TcParams &p, const TcJob *jobs, int count, cudaStream_t s) {
+  ShareJoin join = {};
+  int64_t cols = 0, rows = 0;
+  for (int i = 0; i < count; ++i) {
+    const DenseJob &j = *jobs[i].j;
+    const TcProb &q = p.prob[i];
     join.split[i] = q.split;
     if (q.split > 1) {
       join.j[i] = j;
@@ -665,7 +677,7 @@ int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s) {
     e = dense_launch(gated ? share_join_kernel<true> : share_join_kernel<false>, grid, 256, 0, 1, s,
                      join);
   }
-  return e == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  return e;
 }
 
 }  // namespace coll

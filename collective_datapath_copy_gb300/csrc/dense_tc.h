@@ -59,9 +59,12 @@ struct TcJob {
 // The shapes of `p` for one or two jobs (two: neither gated); part_bytes: room for each job's
 // shares, 0 where k is not split. Makes no device call.
 int tc_plan(TcParams &p, const TcJob *jobs, int count, uint64_t (&part_bytes)[2]);
-// Tensor maps (p.prob[i].part is set by now), then the launch; the shares of split jobs join in a
-// second one.
-int tc_run(TcParams &p, const TcJob *jobs, int count, cudaStream_t s);
+// Tensor maps and the kernel's shared memory: what may be refused, before anything of the call is
+// launched.
+int tc_prepare(TcParams &p, const TcJob *jobs, int count);
+// The launch (p.prob[i].part and p.join are set by now); the shares of split jobs join in a second
+// one.
+cudaError_t tc_run(const TcParams &p, const TcJob *jobs, int count, cudaStream_t s);
 
 
 // A small batch against many output features (dense_skinny.cu): the weights are the 128-row
@@ -81,6 +84,7 @@ struct SkinnyParams {
   uint32_t w_bytes, stage_bytes, smem, idesc, tmem_cols;
 };
 
+// Shapes, tensor maps and shared memory: nothing is refused after it.
 int skinny_plan(SkinnyParams &p, const DenseJob &j, const TcOperand *w, const TcOperand &x);
 cudaError_t skinny_run(const SkinnyParams &p, bool gated, cudaStream_t s);
 

@@ -359,7 +359,8 @@ const char *coll_strerror(int code);
  * Errors (synchronous, nothing enqueued): COLL_EINVAL (sizes, types, activation, a NULL that is
  * not optional, outputs whose rows overlap), COLL_EALIGN (a base that is not a multiple of its
  * element), COLL_EOVERLAP (an output that shares memory with an input or another output; only
- * y == residual, the same view, is allowed), COLL_EWORKSPACE, COLL_ECUDA. */
+ * y == residual, the same view, is allowed), COLL_EWORKSPACE, COLL_ECUDA. A launch that CUDA itself
+ * refuses is COLL_ECUDA too; those of the call before it, if any, are enqueued then. */
 #define COLL_ACT_NONE 0
 #define COLL_ACT_RELU 1
 #define COLL_ACT_GELU 2      /* z/2 (1 + erf(z / sqrt 2))                                       */
