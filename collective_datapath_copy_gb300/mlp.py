@@ -50,6 +50,10 @@ class TensorParallelMLP:
                    for r in range(R)]
         self.down = [Linear(w_down[:, r * f:(r + 1) * f]) for r in range(R)]
         dev, dt = w_gate.device, w_gate.dtype
+        # the operators' status words, side by side
+        self._words = torch.zeros(2 * R, dtype=torch.int32, device=dev)
+        for i, op in enumerate(self.up + self.down):
+            op._status = self._words[i:i + 1]
         self._ptype = torch.float32 if partials == "f32" else torch.bfloat16
         self._p = [torch.empty(tokens, K, dtype=self._ptype, device=dev) for _ in range(R)]
         self._y = [torch.empty(tokens, K, dtype=self._ptype, device=dev) for _ in range(R)]
@@ -66,6 +70,16 @@ class TensorParallelMLP:
         if n * (2 if dtype == "bf16" else 4) <= STAGED_BYTES:
             return Plan(allreduce(self.R, n, dtype), protocol="spec")
         return Plan(allreduce(self.R, n, dtype), zero_copy=1, datapath="twoshot")
+
+    def status(self) -> int:
+        """COLL_OK, or the code of an operator whose bounded device wait expired in any call so far
+        or of a sum whose last run failed: results are then incomplete. Calls enqueue their sums
+        behind their products without looking, so a caller asks before it relies on them.
+        Synchronises with the object's calls."""
+        code = int(self._words.min())  # codes are negative
+        for plan in (self._sum, self._gsum):
+            code = code or plan.status()["code"]
+        return code
 
     @staticmethod
     def _carrier(ts):
