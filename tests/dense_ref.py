@@ -115,8 +115,8 @@ def gated_bwd(dh, g, u, x, wg, wu, name, dtype, grad_dtype):
 
 
 def assert_close(got, ref, what=""):
-    """Every element within its bound, and the whole within the output type's rounding (twice it
-    for what was rounded once on the way): the bound above grows with K, the error does not."""
+    """Every element within its bound. The bound grows with K and the error does not: over a long
+    sum a lost block of k passes it, and assert_rms has to look at the whole."""
     want, bound = ref
     got = got.double()
     assert got.shape == want.shape, (what, got.shape, want.shape)
@@ -129,6 +129,8 @@ def assert_close(got, ref, what=""):
 
 
 def assert_rms(got, ref, dtype, what="", times=1.0):
+    """The root mean square of the error within `times` the rounding of `dtype` (2 for an output
+    whose dz was rounded on the way)."""
     want = ref[0]
     err = (got.double() - want).square().mean().sqrt()
     size = want.square().mean().sqrt()
