@@ -110,7 +110,9 @@ __device__ __forceinline__ void act_value_slope(float z, int act, float &v, floa
     case COLL_ACT_GELU_TANH: {
       const float s = tanh_gate(z);
       v = z * s;
-      d = fmaf(v * (1.0f - s), 2.0f * kTanhScale * fmaf(3.0f * kTanhCubic * z, z, 1.0f), s);
+      // far out s is 0 or 1 and the first factor 0: the square is kept from overflowing beside it
+      const float zz = fminf(z * z, 4096.0f);
+      d = fmaf(v * (1.0f - s), 2.0f * kTanhScale * fmaf(3.0f * kTanhCubic, zz, 1.0f), s);
       return;
     }
     case COLL_ACT_SILU: {
