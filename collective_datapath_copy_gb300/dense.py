@@ -40,6 +40,7 @@ _LINEAR = struct.Struct("26q")
 _LINEAR_BWD = struct.Struct("28q")
 _GATED = struct.Struct("26q")
 _GATED_BWD = struct.Struct("36q")
+_WORKSPACE = struct.Struct("3q")  # their last fields: the workspace, its bytes, the status word
 _NONE = (0, 0, 0)
 _entries = {}
 
@@ -162,28 +163,19 @@ class _Dense:
         fn, size = _entry(where)
         status = self._status.data_ptr()
         stream = _raw_stream(self._dev)  # the current stream's handle
-
-        def fit():
-            plain = pack(*fields, 0, 0, status)
-            key = (int.from_bytes(plain, "little") & _MASK[where], given)
-            kept = self._need.get(where)
-            if kept is not None and kept[1] == key:
-                return kept[0]
-            need = int(size(plain))
-            if need < 0:
-                check(need, where)
-            self._need[where] = (need, key)
-            return need
-
-        kept = self._need.get(where)
-        need = fit() if kept is not None and kept[0] else 0
-        if not need:
-            code = fn(pack(*fields, 0, 0, status), stream)
-            if code == _EWORKSPACE:
-                need = fit()
-        if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=self._status.device)
-            code = fn(pack(*fields, ws.data_ptr(), need, status), stream)
+        args = pack(*fields, 0, 0, status)
+        kept = self._need.get(where)  # (workspace, what decided it)
+        code = fn(args, stream) if kept is None or not kept[0] else _EWORKSPACE
+        if code == _EWORKSPACE:
+            key = (int.from_bytes(args, "little") & _MASK[where], given)
+            if kept is None or kept[1] != key:
+                kept = int(size(args)), key
+                if kept[0] < 0:
+                    check(kept[0], where)
+                self._need[where] = kept
+            ws = torch.empty(kept[0], dtype=torch.uint8, device=self._status.device)
+            code = fn(args[:-_WORKSPACE.size] + _WORKSPACE.pack(ws.data_ptr(), kept[0], status),
+                      stream)
         if code:
             check(code, where)
 
