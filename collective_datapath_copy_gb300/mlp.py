@@ -65,11 +65,17 @@ class TensorParallelMLP:
             "bf16" if self._gtype is torch.bfloat16 else "f32")
         self._kept = None
 
+    def _here(self):
+        """The weights' device as the current one: a plan belongs to the device it was made on,
+        and runs only while that is current."""
+        return torch.cuda.device(self.up[0]._dev)
+
     def _plan(self, dtype):
         n = self.tokens * self.K
-        if n * (2 if dtype == "bf16" else 4) <= STAGED_BYTES:
-            return Plan(allreduce(self.R, n, dtype), protocol="spec")
-        return Plan(allreduce(self.R, n, dtype), zero_copy=1, datapath="twoshot")
+        with self._here():
+            if n * (2 if dtype == "bf16" else 4) <= STAGED_BYTES:
+                return Plan(allreduce(self.R, n, dtype), protocol="spec")
+            return Plan(allreduce(self.R, n, dtype), zero_copy=1, datapath="twoshot")
 
     def status(self) -> int:
         """COLL_OK, or the code of an operator whose bounded device wait expired in any call so far
@@ -77,8 +83,9 @@ class TensorParallelMLP:
         behind their products without looking, so a caller asks before it relies on them.
         Synchronises with the object's calls."""
         code = int(self._words.min())  # codes are negative
-        for plan in (self._sum, self._gsum):
-            code = code or plan.status()["code"]
+        with self._here():
+            for plan in (self._sum, self._gsum):
+                code = code or plan.status()["code"]
         return code
 
     @staticmethod
@@ -102,7 +109,8 @@ class TensorParallelMLP:
                 res = res.float()
             self.down[r].forward(h, residual=res, out=self._p[r])
         self._kept = (x, kept) if keep else None
-        self._sum.run(self._carrier(self._p), self._carrier(self._y))
+        with self._here():
+            self._sum.run(self._carrier(self._p), self._carrier(self._y))
         return self._y
 
     def backward(self, dy):
@@ -125,7 +133,8 @@ class TensorParallelMLP:
             if not direct:
                 self._g[r].copy_(dx)
             grads.append((dw_gate, dw_up, dw_down))
-        self._gsum.run(self._carrier(self._g), self._carrier(self._dx))
+        with self._here():
+            self._gsum.run(self._carrier(self._g), self._carrier(self._dx))
         return self._dx, grads
 
 
