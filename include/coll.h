@@ -346,7 +346,8 @@ const char *coll_strerror(int code);
  *
  * Operands are COLL_BF16 or COLL_F16 (one type per call); products accumulate in binary32 and
  * every output is rounded once, to nearest even, from the binary32 epilogue. The backward
- * calls round dz (dg, du) to the operands' type once before the products that read them.
+ * calls round dz (dg, du) to the operands' type once before the products that read them: in
+ * COLL_F16 one past 65504 is infinite there, and with it what it enters of dx, dw, dw_gate, dw_up.
  * Results do not depend on timing: every sum has a fixed order for given sizes and layouts.
  *
  * Calls enqueue on `stream` and return. `stream` and every buffer belong to the current device:
