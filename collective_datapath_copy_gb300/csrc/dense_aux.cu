@@ -6,12 +6,11 @@
 // du) written once, rounded to the operands' type for the tensor-core products that follow (their
 // sums over rows or columns average the rounding, which is that of any stored activation; the
 // gradients' error against 64 bits is 1.4 times that of rounding them alone, 0.0023 for 0.0017 in
-// bf16). In f16 that also bounds dz: past 65504 it is infinite, and with it the rows of dx and of dW
+// bf16). In f16 that also bounds dz: past 65504 it is infinite, and with it the rows of dx and dW
 // that it enters, where a binary32 dz would have stayed finite; below 2^-25 it is zero. A caller
-// scales its loss for that, as for its stored activations. db sums
-// the unrounded binary32 dz: a thread adds its rows in order, row groups of a CTA join in order in
-// shared memory, and row blocks in order in a second launch, so the result does not depend on
-// timing.
+// scales its loss for that, as for its stored activations. db sums the unrounded binary32 dz: a
+// thread adds its rows in order, row groups of a CTA join in order in shared memory, and row blocks
+// in order in a second launch, so the result does not depend on timing.
 #include "dense.h"
 #include "dense_epi.cuh"
 #include "tma.cuh"

@@ -67,9 +67,9 @@ __device__ __forceinline__ float tanh_gate(float z) {
 // Phi(z), the standard normal distribution function, and exp(-z^2 / 2), by the polynomial
 // 7.1.26 of Abramowitz and Stegun for erfc(|z| / sqrt 2): a reciprocal, an exponential and eight
 // multiply-adds. Its absolute error is below 1e-7, 2e-7 as evaluated here, which is what an output
-// that adds up with others sees. Against Phi itself it grows for negative z: 3e-6 at -2, 5e-5 at -3,
-// 5e-4 at -4, 1.6e-3 at -5, 1e-2 at -8. (The sum 1 + erf in binary32 is off by 4e-4 at -4, by a
-// twentieth at -5, and zero from -5.6 on.)
+// that adds up with others sees. Against Phi itself it grows for negative z: 3e-6 at -2, 5e-5 at
+// -3, 5e-4 at -4, 1.6e-3 at -5, 1e-2 at -8. (The sum 1 + erf in binary32 is off by 4e-4 at -4, by
+// a twentieth at -5, and zero from -5.6 on.)
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
   const float t = recip(fmaf(0.3275911f * kRsqrt2, fabsf(z), 1.0f));
   e = exp2_fast(z * z * (-0.5f * kLog2e));

@@ -9,7 +9,8 @@
 // turn and join once, in order, through shared memory. Several steps of loads per lane are in
 // flight before the first is used.
 //
-// Measured for one token: 4096 x 1792 4.5 us, gated 14336 x 4096 36 us (6.5 TB/s).
+// Measured for one token, weights from HBM: 4096 x 1792 4.6 us, gated 14336 x 4096 37 us (6.3
+// TB/s).
 //
 // tcgen05 is the wrong tool here: an instruction of 128 rows by 16 tokens takes about 27 ns to
 // issue whatever the batch, 7 us for k = 4096, and sharing k between CTAs costs a cluster

@@ -7,7 +7,7 @@
 // matrices, two accumulators in the same lanes) over the whole of k; how many is chosen for the
 // least time of the busiest SM (skinny_plan), and dense.cu sends only products here whose features
 // occupy every SM that way. Against the kernel of CTA pairs, which takes the tokens as rows:
-// 14336 x 4096 for 17 to 64 tokens 23 us against 25, gated 40 us (5.8 TB/s) against 45.
+// 14336 x 4096 for 17 to 64 tokens 23 us against 25, gated 41 us (5.7 TB/s) against 45.
 //
 // Two CTAs fit an SM, so that one's start and end run beside the other's stream. Tensor memory is
 // never oversubscribed: the shared memory a CTA asks for keeps a third one off the SM and a CTA

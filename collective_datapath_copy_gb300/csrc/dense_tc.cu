@@ -20,8 +20,8 @@
 // The grid is persistent; tiles are walked eight rows of tiles at a time, which keeps the operands
 // of the tiles in flight in L2.
 //
-// Measured: 4096 x 4096 x 4096 75 us (1830 TFLOP/s); gated 8192 x 14336 x 4096 with everything kept
-// 0.98 ms alone (1960 TFLOP/s, tensor pipe 96 % busy) and 1.12 ms back to back, where the card's
+// Measured: 4096 x 4096 x 4096 76 us (1820 TFLOP/s); gated 8192 x 14336 x 4096 with everything kept
+// 1.02 ms alone (1890 TFLOP/s, tensor pipe 96 % busy) and 1.13 ms back to back, where the card's
 // power cap sets the clock. Wide tiles are bound by the tensor pipe, tiles of up to 128 columns by
 // issuing (about 27 ns an instruction), sums of a few k blocks by the epilogue's way to HBM
 // (8192 x 8192 x 64: 53 us, 2.5 TB/s of writes, where filling the same memory reaches 3.4).

@@ -13,8 +13,8 @@ unless given.
 
 Inputs may have any strides and leading dimensions; outputs that a caller passes have unit column
 stride. The operators record nothing for autograd: the backward calls are explicit, and an input
-that requires a gradient gets none from them. Gradients of the products (dz, dg, du) pass to the next
-ones in the operands' type: in float16 one past 65504 is infinite, so scale the loss.
+that requires a gradient gets none from them. Gradients of the products (dz, dg, du) pass to the
+next ones in the operands' type: in float16 one past 65504 is infinite, so scale the loss.
 """
 
 from __future__ import annotations
