@@ -13,6 +13,8 @@ using coll::DenseJob;
 using coll::DenseMat;
 using coll::TcOperand;
 
+constexpr uint64_t kAddressable = (uint64_t)1 << 40;
+
 // Bump allocator over the caller's workspace, in steps of 256 bytes from a 128-byte boundary. With
 // base == nullptr it only counts.
 struct Ws {
@@ -22,7 +24,12 @@ struct Ws {
   coll::TcParams *plan;
   bool planned;
   uint64_t part[2];
+  bool over;  // more was asked for than a device can address; the counting pass ends the call then
   void *take(uint64_t bytes) {
+    if (bytes > kAddressable - used) {
+      over = true;
+      return nullptr;
+    }
     const uint64_t at = used;
     used += (bytes + 255) & ~(uint64_t)255;
     return base ? base + at : nullptr;
@@ -87,7 +94,7 @@ int check_mat(const View &v, bool needed, bool output) {
   if (!v.p) return needed && v.rows > 0 && v.cols > 0 ? COLL_EINVAL : COLL_OK;
   if ((uintptr_t)v.p % (unsigned)v.es) return COLL_EALIGN;
   // what a device can address, so that no offset below leaves 64 bits
-  const int64_t lim = (int64_t)1 << 40;
+  const int64_t lim = (int64_t)kAddressable;
   const int64_t rs = v.rows > 1 ? lim / (v.rows - 1) : lim;
   const int64_t cs = v.cols > 1 ? lim / (v.cols - 1) : lim;
   if (v.rs > rs || v.rs < -rs || v.cs > cs || v.cs < -cs) return COLL_EINVAL;
@@ -522,7 +529,7 @@ int64_t count(const T *a, Ws &ws) {
   const int c = check(*a);
   if (c) return c;
   const int r = run(*a, ws, true, nullptr);
-  return r ? r : ws.used ? (int64_t)ws.used + 128 : 0;  // room to start on 128 bytes
+  return r ? r : ws.over ? COLL_EINVAL : ws.used ? (int64_t)ws.used + 128 : 0;  // room to start on 128 bytes
 }
 
 template <typename T>

@@ -357,8 +357,8 @@ const char *coll_strerror(int code);
  * passed the call. `status`: optional device int32 that receives COLL_ETIMEDOUT if a bounded
  * device wait expires (never cleared by a call). The workspace must be 16-byte aligned and
  * hold what the call's *_workspace function returns for the same arguments.
- * Errors (synchronous, nothing enqueued): COLL_EINVAL (sizes, types, activation, a NULL that is
- * not optional, outputs whose rows overlap), COLL_EALIGN (a base that is not a multiple of its
+ * Errors (synchronous, nothing enqueued): COLL_EINVAL (sizes, a workspace past 2^40 bytes, types,
+ * activation, a NULL that is not optional, outputs whose rows overlap), COLL_EALIGN (a base that is not a multiple of its
  * element), COLL_EOVERLAP (an output that shares memory with an input or another output; only
  * y == residual, the same view, is allowed), COLL_EWORKSPACE, COLL_ECUDA. A launch that CUDA itself
  * refuses is COLL_ECUDA too; those of the call before it, if any, are enqueued then. */
