@@ -528,6 +528,7 @@ int64_t count(const T *a, Ws &ws) {
   if (!a) return COLL_EINVAL;
   const int c = check(*a);
   if (c) return c;
+  if ((uintptr_t)a->status % sizeof(int32_t)) return COLL_EALIGN;
   const int r = run(*a, ws, true, nullptr);
   return r ? r : ws.over ? COLL_EINVAL : ws.used ? (int64_t)ws.used + 128 : 0;  // room to start on 128 bytes
 }

@@ -3,9 +3,11 @@ argument check (no GPU: the addresses are made up)."""
 
 import pytest
 
+from collective_datapath_copy_gb300 import _lib, dense
 from collective_datapath_copy_gb300.build import build
-from test_dense_host import A, EINVAL, F32, gated, gated_bwd, linear, linear_bwd
+from test_dense_host import A, EALIGN, EINVAL, F32, gated, gated_bwd, linear, linear_bwd
 
+NO = (0, 0, 0)
 MOST = 0x7FFFFFFF - 4096
 
 
@@ -43,3 +45,11 @@ def test_large_scratch_that_a_device_might_hold():
     assert need >= 2 * (1 << 35)
     assert linear_bwd(m=1 << 17, n=1 << 17, k=8, act=1, dy=zero(1), pre=zero(2),
                       dx=(1000 * A, 8, 1), dw=(2000 * A, 8, 1)) >= 1 << 35
+
+
+def test_a_status_word_is_four_bytes_on_four():
+    """It is only written when a wait expires, where an odd address would fault."""
+    vals = (8, 32, 64, 0, 0, 0, A, 64, 1, 2 * A, 64, 1, *NO, *NO, 3 * A, 32, 1, 0, 0)
+    for off in (0, 4, 2, 1):
+        got = _lib.lib().coll_linear_workspace(dense._LINEAR.pack(*vals, 0, 0, 4 * A + off))
+        assert got == (EALIGN if off % 4 else 0)
