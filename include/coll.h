@@ -355,13 +355,15 @@ const char *coll_strerror(int code);
  * calls and allocate nothing, so calls on different streams may overlap when their workspaces differ, and calls may be
  * captured into a CUDA graph. Buffers must stay live and unmodified until the stream has
  * passed the call. `status`: optional device int32 that receives COLL_ETIMEDOUT if a bounded
- * device wait expires (never cleared by a call). The workspace must be 16-byte aligned and
- * hold what the call's *_workspace function returns for the same arguments.
+ * device wait expires (never cleared by a call). The workspace must be 16-byte aligned, hold
+ * what the call's *_workspace function returns for the same arguments and share no memory with
+ * the call's buffers.
  * Errors (synchronous, nothing enqueued): COLL_EINVAL (sizes, a workspace past 2^40 bytes, types,
- * activation, a NULL that is not optional, outputs whose rows overlap), COLL_EALIGN (a base that is not a multiple of its
- * element), COLL_EOVERLAP (an output that shares memory with an input or another output; only
- * y == residual, the same view, is allowed), COLL_EWORKSPACE, COLL_ECUDA. A launch that CUDA itself
- * refuses is COLL_ECUDA too; those of the call before it, if any, are enqueued then. */
+ * activation, a NULL that is not optional, outputs whose rows overlap), COLL_EALIGN (a base that
+ * is not a multiple of its element, a status word off four bytes), COLL_EOVERLAP (an output that
+ * shares memory with an input or another output; only y == residual, the same view, is allowed),
+ * COLL_EWORKSPACE, COLL_ECUDA. A launch that CUDA itself refuses is COLL_ECUDA too; those of the
+ * call before it, if any, are enqueued then. */
 #define COLL_ACT_NONE 0
 #define COLL_ACT_RELU 1
 #define COLL_ACT_GELU 2      /* z/2 (1 + erf(z / sqrt 2))                                       */
