@@ -42,7 +42,6 @@ _LINEAR = struct.Struct("26q")
 _LINEAR_BWD = struct.Struct("28q")
 _GATED = struct.Struct("26q")
 _GATED_BWD = struct.Struct("36q")
-_WORKSPACE = struct.Struct("3q")  # their last fields: the workspace, its bytes, the status word
 _NONE = (0, 0, 0)
 _entries = {}
 
@@ -61,10 +60,8 @@ _MASK = {"coll_linear": _mask("......" + "a.." * 5 + "a."),
 
 
 def _entry(name):
-    e = _entries.get(name)
-    if e is None:
-        h = lib()
-        e = _entries[name] = (getattr(h, name), getattr(h, name + "_workspace"))
+    h = lib()
+    e = _entries[name] = (getattr(h, name), getattr(h, name + "_workspace"))
     return e
 
 
@@ -142,9 +139,14 @@ def _on(stream, dev, tensors):
 
 class _Dense:
     def _start(self, device):
-        self._status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._report_to(torch.zeros(1, dtype=torch.int32, device=device))
         self._need = {}
-        self._dev = self._status.get_device()
+
+    def _report_to(self, word):
+        """`word` is what an expired wait is written to from now on."""
+        self._status = word
+        self._word = word.data_ptr()
+        self._dev = word.get_device()
 
     def status(self) -> int:
         """COLL_OK, or COLL_ETIMEDOUT if a bounded device wait of an earlier call expired (its
@@ -162,24 +164,31 @@ class _Dense:
         if _current_device() != self._dev:
             with torch.cuda.device(self._dev):
                 return self._launch(where, pack, fields, given)
-        fn, size = _entry(where)
-        status = self._status.data_ptr()
+        fn, size = _entries.get(where) or _entry(where)
         stream = _raw_stream(self._dev)  # the current stream's handle
-        args = pack(*fields, 0, 0, status)
-        kept = self._need.get(where)  # (workspace, what decided it)
-        code = fn(args, stream) if kept is None or not kept[0] else _EWORKSPACE
-        if code == _EWORKSPACE:
-            key = (int.from_bytes(args, "little") & _MASK[where], given)
-            if kept is None or kept[1] != key:
-                kept = int(size(args)), key
-                if kept[0] < 0:
-                    check(kept[0], where)
-                self._need[where] = kept
-            ws = torch.empty(kept[0], dtype=torch.uint8, device=self._status.device)
-            code = fn(args[:-_WORKSPACE.size] + _WORKSPACE.pack(ws.data_ptr(), kept[0], status),
-                      stream)
+        need, kept = 0, self._need.get(where)
+        if kept is not None and kept[0]:
+            need = kept[0] if kept[1] == fields else self._fit(where, pack, size, fields, given)
+        if not need:
+            code = fn(pack(*fields, 0, 0, self._word), stream)
+            if code == _EWORKSPACE:
+                need = self._fit(where, pack, size, fields, given)
+        if need:
+            ws = torch.empty(need, dtype=torch.uint8, device=self._status.device)
+            code = fn(pack(*fields, ws.data_ptr(), need, self._word), stream)
         if code:
             check(code, where)
+
+    def _fit(self, where, pack, size, fields, given):
+        """The workspace of a call, asked for unless the last one was alike."""
+        args = pack(*fields, 0, 0, self._word)
+        key = (int.from_bytes(args, "little") & _MASK[where], given)
+        kept = self._need.get(where)  # (workspace, of which call, what decided it)
+        need = kept[0] if kept is not None and kept[2] == key else int(size(args))
+        if need < 0:
+            check(need, where)
+        self._need[where] = (need, fields, key)
+        return need
 
 
 class Linear(_Dense):

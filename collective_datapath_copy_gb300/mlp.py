@@ -53,7 +53,7 @@ class TensorParallelMLP:
         # the operators' status words, side by side
         self._words = torch.zeros(2 * R, dtype=torch.int32, device=dev)
         for i, op in enumerate(self.up + self.down):
-            op._status = self._words[i:i + 1]
+            op._report_to(self._words[i:i + 1])
         self._ptype = torch.float32 if partials == "f32" else torch.bfloat16
         self._p = [torch.empty(tokens, K, dtype=self._ptype, device=dev) for _ in range(R)]
         self._y = [torch.empty(tokens, K, dtype=self._ptype, device=dev) for _ in range(R)]

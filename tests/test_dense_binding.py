@@ -28,6 +28,7 @@ class Machine:
         monkeypatch.setattr(torch.cuda, "device", device)
         monkeypatch.setattr(dense, "_current_device", lambda: self.current, raising=False)
         monkeypatch.setattr(dense, "_raw_stream", lambda d: 100 + d)
+        monkeypatch.setattr(dense, "_entries", {})
         monkeypatch.setattr(dense, "_entry", lambda name: (call, lambda packed: 0))
 
 

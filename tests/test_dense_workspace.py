@@ -47,6 +47,7 @@ class Calls:
         self.op._start(torch.device("cpu"))
         monkeypatch.setattr(dense, "_current_device", lambda: self.op._dev, raising=False)
         monkeypatch.setattr(dense, "_raw_stream", lambda d: 0)
+        monkeypatch.setattr(dense, "_entries", {})
         monkeypatch.setattr(dense, "_entry", self.entry)
 
     def entry(self, name):
