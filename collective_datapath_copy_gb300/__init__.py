@@ -4,8 +4,9 @@ A collective is a naming of per-rank input and output segments plus copy or sum
 (``namings``); ``Plan`` compiles it through the C ABI of libcoll.so (include/coll.h) and
 runs it with the staged Stage/Notify/Consume engine (barrier, dual-buffer or speculative
 protocol) or the zero-copy datapath. ``Linear`` and ``GatedFFN`` are the dense operators on
-either side of a tensor-parallel layer's collective, with their gradients. The library is
-required: there is no fallback.
+either side of a tensor-parallel layer's collective, with their gradients; ``Router`` and
+``GatedExperts`` are a mixture of experts' choice and its experts for a few tokens. The library
+is required: there is no fallback.
 """
 
 from . import namings  # noqa: F401
@@ -16,10 +17,16 @@ from .namings import (Naming, allgather, allreduce, alltoall, alltoallv_from_rou
 from .plan import Plan, allreduce_static, probe_flag_rtt, validate, validate_code  # noqa: F401
 
 
-def __getattr__(name):  # the dense operators need torch, which nothing above imports
+def __getattr__(name):  # the operators need torch, which nothing above imports
     if name in ("GatedFFN", "Linear"):
         from . import dense
         return getattr(dense, name)
+    if name in ("GatedExperts", "Router"):
+        from . import experts
+        return getattr(experts, name)
+    if name == "ExpertParallelMoE":
+        from . import moe
+        return moe.ExpertParallelMoE
     if name == "TensorParallelMLP":
         from . import mlp
         return mlp.TensorParallelMLP

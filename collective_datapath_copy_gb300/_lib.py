@@ -43,6 +43,7 @@ DATAPATH = {"oneshot": D["COLL_DP_ONESHOT"], "twoshot": D["COLL_DP_TWOSHOT"],
             "twoshot_pull": D["COLL_DP_TWOSHOT_PULL"]}
 SPEC_CHECK = {"tagged": D["COLL_SPEC_TAGGED"], "literal": D["COLL_SPEC_LITERAL"],
               "relaxed": D["COLL_SPEC_TAGGED_RELAXED"]}
+SCORE = {"softmax": D["COLL_SCORE_SOFTMAX"], "sigmoid": D["COLL_SCORE_SIGMOID"]}
 ORDER = {"rank": D["COLL_ORDER_RANK"], "tree": D["COLL_ORDER_TREE"]}
 INJECT = {"skip_notify": D["COLL_INJECT_SKIP_NOTIFY"], "stagger": D["COLL_INJECT_STAGGER"],
           "spec_pause": D["COLL_INJECT_SPEC_PAUSE"]}
@@ -103,6 +104,10 @@ _SIGS = {
        ("coll_linear", "coll_linear_backward", "coll_gated_ffn", "coll_gated_ffn_backward")},
     **{name + "_workspace": (C.c_int64, [C.c_char_p]) for name in
        ("coll_linear", "coll_linear_backward", "coll_gated_ffn", "coll_gated_ffn_backward")},
+    # mixture of experts, in the same form
+    **{name: (C.c_int, [C.c_char_p, _P]) for name in
+       ("coll_route", "coll_route_backward", "coll_gated_experts")},
+    "coll_gated_experts_workspace": (C.c_int64, [C.c_char_p]),
 }
 
 _lib = None

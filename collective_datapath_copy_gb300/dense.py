@@ -125,11 +125,11 @@ def _new(m, cols, dtype, weight, like):
 
 
 @contextlib.contextmanager
-def _on(stream, dev, tensors):
+def _on(stream, dev, tensors, what="weights are"):
     """Run a call on another stream than the current one: allocations belong to that stream, and
     the caller's tensors are not handed out again before it has passed the call."""
     if stream.device_index != dev:
-        raise ValueError(f"stream is of cuda:{stream.device_index}, the weights are on cuda:{dev}")
+        raise ValueError(f"stream is of cuda:{stream.device_index}, the {what} on cuda:{dev}")
     with torch.cuda.stream(stream):
         yield
     for t in tensors:

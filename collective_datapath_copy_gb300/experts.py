@@ -1,0 +1,207 @@
+"""Python face of the mixture-of-experts operators: Router and GatedExperts.
+
+A router's choice of experts from its logits, with its gradient, and a few tokens through their
+chosen gated experts, as a decode step runs them. Calls marshal the C entry points
+(include/coll.h), enqueue on a stream and return; outputs and workspaces come from PyTorch's
+allocator on that stream unless given.
+
+    logits = cdc.Linear(w_router).forward(x, out_dtype=torch.float32)
+    ids, weights = cdc.Router(8).forward(logits)          # int32 and binary32, [tokens, 8]
+    experts = cdc.GatedExperts(w_gate, w_up, w_down)      # [E, F, K], [E, F, K], [E, N, F]
+    y = experts.forward(x, ids, weights, residual=x)
+
+A rank that holds experts [first, first + E) passes over the others' ids; the ranks' outputs add up
+(ExpertParallelMoE). `ids` is also the routing table that moe_dispatch takes. The operators record
+nothing for autograd: Router.backward is explicit, and GatedExperts is for serving.
+"""
+
+from __future__ import annotations
+
+import math
+import struct
+
+import torch
+
+from . import _lib, dense
+from ._lib import check, lib
+from .dense import ACT, GATED_ACTS, _NONE, _TYPE, _Dense, _mask, _new, _on, _read, _row_count
+
+_ROUTE = struct.Struct("6qd9q")
+_ROUTE_BWD = struct.Struct("6qd12q")
+_EXPERTS = struct.Struct("37q")
+_LOGITS = (torch.float32, torch.bfloat16, torch.float16)
+
+dense._MASK["coll_gated_experts"] = _mask("." * 10 + "a.." * 8)
+
+
+def _out(t, m, cols, dtype, dev, what):
+    """An output's address and strides as a matrix; never a copy."""
+    if t.dtype is not dtype:
+        raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} is on {t.device}, expected cuda:{dev}")
+    if t.dim() == 0 or t.shape[-1] != cols or t.numel() != m * cols:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {m} rows of {cols}")
+    if t.dim() != 2:
+        t = t.view(m, cols)
+    return (t.data_ptr(), *t.stride())
+
+
+def _stack(name, w, like=None):
+    if not isinstance(w, torch.Tensor) or w.dim() != 3:
+        raise ValueError(f"{name} must have three dimensions")
+    if w.dtype not in (torch.bfloat16, torch.float16):
+        raise ValueError(f"{name} must be bfloat16 or float16, not {w.dtype}")
+    if not w.is_cuda:
+        raise ValueError(f"{name} is not a CUDA tensor")
+    if like is not None and (w.dtype != like.dtype or w.device != like.device):
+        raise ValueError(f"{name} must be {like.dtype} on {like.device}")
+    if w.stride(2) != 1 and w.shape[2] > 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return w
+
+
+class Router:
+    """Each token's choice of `top_k` experts, by its largest logits, and their weights.
+
+    score: "softmax" (over all experts) or "sigmoid"; normalize: a token's weights add up to `scale`,
+    else each is `scale` times its score."""
+
+    def __init__(self, top_k, score="softmax", normalize=True, scale=1.0):
+        if not 1 <= top_k <= 32:
+            raise ValueError(f"top_k must be 1 to 32, not {top_k}")
+        if score not in _lib.SCORE:
+            raise ValueError(f"score must be one of {tuple(_lib.SCORE)}, not {score!r}")
+        if not math.isfinite(scale):
+            raise ValueError(f"scale must be finite, not {scale}")
+        self.top_k, self.score = int(top_k), score
+        self.normalize, self.scale = bool(normalize), float(scale)
+
+    def _head(self, t, e, dtype):
+        return (t, e, self.top_k, _TYPE[dtype], _lib.SCORE[self.score], int(self.normalize),
+                self.scale)
+
+    @staticmethod
+    def _logits(logits):
+        if logits.dtype not in _LOGITS:
+            raise ValueError(f"logits must be one of {_LOGITS}, not {logits.dtype}")
+        if not logits.is_cuda:
+            raise ValueError("logits is not a CUDA tensor")
+        if logits.dim() == 0:
+            raise ValueError("logits must have a dimension of experts")
+        return logits.get_device()
+
+    @staticmethod
+    def _launch(where, packed, dev):
+        if dense._current_device() != dev:
+            with torch.cuda.device(dev):
+                return Router._launch(where, packed, dev)
+        code = getattr(lib(), where)(packed, dense._raw_stream(dev))
+        if code:
+            check(code, where)
+
+    def forward(self, logits, ids=None, weights=None, stream=None):
+        """logits [..., E] (binary32, bfloat16 or float16) -> ids [..., top_k] (int32) and weights
+        [..., top_k] (binary32), the largest logit first, equal ones by ascending index. A logit of
+        -inf is not chosen: where too few are left, ids ends in -1 with weight 0."""
+        dev = self._logits(logits)
+        if stream is not None:
+            with _on(stream, dev, (logits, ids, weights), "logits are"):
+                return self.forward(logits, ids, weights)
+        keep, e, top = [], logits.shape[-1], self.top_k
+        lm = _read(logits, None, e, logits.dtype, dev, "logits", keep)
+        t = _row_count(logits)
+        if ids is None:
+            ids = torch.empty(*logits.shape[:-1], top, dtype=torch.int32, device=logits.device)
+        if weights is None:
+            weights = torch.empty(*logits.shape[:-1], top, dtype=torch.float32,
+                                  device=logits.device)
+        self._launch("coll_route", _ROUTE.pack(
+            *self._head(t, e, logits.dtype), *lm, *_out(ids, t, top, torch.int32, dev, "ids"),
+            *_out(weights, t, top, torch.float32, dev, "weights")), dev)
+        return ids, weights
+
+    __call__ = forward
+
+    def backward(self, dweights, logits, ids, dlogits=None, stream=None):
+        """dlogits [..., E], of the logits' type, for the gradient dweights [..., top_k] (binary32)
+        of forward's weights and the ids it returned. The choice itself has no gradient."""
+        dev = self._logits(logits)
+        if stream is not None:
+            with _on(stream, dev, (dweights, logits, ids, dlogits), "logits are"):
+                return self.backward(dweights, logits, ids, dlogits)
+        keep, e, top = [], logits.shape[-1], self.top_k
+        lm = _read(logits, None, e, logits.dtype, dev, "logits", keep)
+        t = _row_count(logits)
+        gm = _read(dweights, t, top, torch.float32, dev, "dweights", keep)
+        im = _read(ids, t, top, torch.int32, dev, "ids", keep)
+        if dlogits is None:
+            dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
+        self._launch("coll_route_backward", _ROUTE_BWD.pack(
+            *self._head(t, e, logits.dtype), *gm, *lm, *im,
+            *_out(dlogits, t, e, logits.dtype, dev, "dlogits")), dev)
+        return dlogits
+
+
+class GatedExperts(_Dense):
+    """y = residual + sum over a token's choices of weight * (act(x w_gate^T) * (x w_up^T)) w_down^T:
+    a few tokens through the experts they chose.  w_gate, w_up [E, F, K], w_down [E, N, F],
+    bfloat16 or float16, each one's last dimension contiguous. Updates in place are seen by the next
+    call.
+
+    act: "silu", "gelu", "gelu_tanh", "relu" or "sigmoid". first: the id of w_gate[0]; a token's ids
+    outside [first, first + E) are passed over."""
+
+    def __init__(self, w_gate, w_up, w_down, act="silu", first=0):
+        self.w_gate = _stack("w_gate", w_gate)
+        self.w_up = _stack("w_up", w_up, w_gate)
+        self.w_down = _stack("w_down", w_down, w_gate)
+        E, F, K = w_gate.shape
+        if w_up.shape != w_gate.shape or w_down.shape[0] != E or w_down.shape[2] != F:
+            raise ValueError(f"w_up must be {(E, F, K)} and w_down {(E, 'N', F)}, not "
+                             f"{tuple(w_up.shape)} and {tuple(w_down.shape)}")
+        if act not in GATED_ACTS:
+            raise ValueError(f"act must be one of {GATED_ACTS}, not {act!r}")
+        if not 0 <= first < 2 ** 31 - 4096:
+            raise ValueError(f"first must be the id of an expert, not {first}")
+        self.act, self.first = act, int(first)
+        self._start(w_gate.device)
+
+    def forward(self, x, ids, weights, residual=None, out=None, out_dtype=None, stream=None):
+        """x [..., K], ids [..., top] (int32) and weights [..., top] (binary32) -> y [..., N].
+        out_dtype: the operands' type or torch.float32 (a partial for a binary32 sum; its residual
+        is float32 too). residual may be `out` itself. The chosen experts' weights are read once for
+        every 128 tokens."""
+        wg, wu, wd, dev, keep = self.w_gate, self.w_up, self.w_down, self._dev, []
+        if stream is not None:
+            with _on(stream, dev, (x, ids, weights, residual, out, wg, wu, wd, self._status)):
+                return self.forward(x, ids, weights, residual, out, out_dtype)
+        E, F, K = wg.shape
+        n, dt = wd.shape[1], wg.dtype
+        xm = _read(x, None, K, dt, dev, "x", keep)
+        m = _row_count(x)
+        if ids.dim() == 0:
+            raise ValueError("ids must have a dimension of choices")
+        top = ids.shape[-1]
+        im = _read(ids, m, top, torch.int32, dev, "ids", keep)
+        sm = _read(weights, m, top, torch.float32, dev, "weights", keep)
+        ot = out.dtype if out is not None else out_dtype or dt
+        if (ot is not dt and ot is not torch.float32) or out_dtype not in (None, ot):
+            raise ValueError(f"the output must be {dt} or torch.float32, not "
+                             f"{ot if out_dtype in (None, ot) else out_dtype}")
+        if out is None:
+            out = _new(m, n, ot, wg, x)
+        ym = _out(out, m, n, ot, dev, "out")
+        rm = _NONE
+        if residual is not None:
+            if residual.shape != out.shape:
+                residual = residual.expand(out.shape)
+            rm = _read(residual, m, n, ot, dev, "residual", keep)
+        self._launch("coll_gated_experts", _EXPERTS.pack,
+                     (m, n, K, F, E, self.first, top, _TYPE[dt], _TYPE[ot], ACT[self.act],
+                      wg.data_ptr(), wg.stride(0), wg.stride(1),
+                      wu.data_ptr(), wu.stride(0), wu.stride(1),
+                      wd.data_ptr(), wd.stride(0), wd.stride(1), *xm, *im, *sm, *rm, *ym))
+        return out
+
+    __call__ = forward

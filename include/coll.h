@@ -441,6 +441,74 @@ int64_t coll_linear_backward_workspace(const coll_linear_bwd_t *a);
 int64_t coll_gated_ffn_workspace(const coll_gated_t *a);
 int64_t coll_gated_ffn_backward_workspace(const coll_gated_bwd_t *a);
 
+/* ------------------------------------------------------- mixture of experts
+ * A router's choice of experts from its logits, the gradient of that choice, and a few tokens
+ * through their chosen gated experts. The logits are a coll_linear with a COLL_F32 output; with one
+ * coll_gated_experts for each rank's experts and the all-reduce of their outputs it is a mixture
+ * of experts over the ranks (the routing table of the dispatch and combine namings is `ids`). No
+ * counterpart on the pages.
+ *
+ * Streams, buffers, overlaps and errors are the dense operators'. coll_route and
+ * coll_route_backward need no workspace and wait for nothing. Results do not depend on timing. */
+#define COLL_SCORE_SOFTMAX 0 /* exp(l - max) / sum over all experts */
+#define COLL_SCORE_SIGMOID 1 /* 1 / (1 + exp(-l))                   */
+
+/* For each of t tokens: the `top` largest of its e logits, largest first, equal ones by ascending
+ * index (-0 equals 0; a NaN is the largest), and a weight for each: scale times its score, or with
+ * normalize == 1 scale times its score over the chosen scores' sum. A logit of -inf is not chosen:
+ * where fewer than `top` others are left, ids ends in -1 with weight 0. 1 <= top <= 32, top <= e
+ * <= 1024. logits [t][e] of dtype (COLL_F32, COLL_BF16 or COLL_F16), any strides; ids [t][top]
+ * int32; weights [t][top] binary32, as are the sums. */
+typedef struct {
+  int64_t t, e, top;
+  int64_t dtype, score, normalize;
+  double scale;
+  coll_mat_t logits, ids, weights;
+} coll_route_t;
+
+/* dlogits [t][e] of dtype, for the gradient dweights [t][top] (binary32) of the weights and the ids
+ * that were chosen (any strides; an id outside 0..e-1 has no part in it). The choice itself has no
+ * gradient: with normalize or sigmoid scores, logits that were not chosen get 0. */
+typedef struct {
+  int64_t t, e, top;
+  int64_t dtype, score, normalize;
+  double scale;
+  coll_mat_t dweights, logits, ids, dlogits;
+} coll_route_bwd_t;
+
+int coll_route(const coll_route_t *a, void *stream);
+int coll_route_backward(const coll_route_bwd_t *a, void *stream);
+
+/* A stack of matrices: element (e, i, j) at ptr + e * es + i * rs + j elements. */
+typedef struct {
+  const void *ptr;
+  int64_t es, rs;
+} coll_stack_t;
+
+/* y[i] = residual[i] + sum over j of weights[i][j] down_e(act(gate_e x[i]) (up_e x[i])), where
+ * e = ids[i][j] - first is one of this call's experts; other ids (another rank's experts, -1) are
+ * passed over, their weights and experts unread. x [m][k], w_gate and w_up [experts][f][k],
+ * w_down [experts][n][f], residual and y [m][n] (y of out_dtype: dtype or COLL_F32, the residual
+ * alike), ids [m][top] int32, weights [m][top] binary32; x, ids, weights and residual may have any
+ * strides. The inner act(g) u is rounded to dtype once, as coll_gated_ffn rounds its h (in COLL_F16
+ * one past 65504 is infinite); everything else is kept in binary32 until y is rounded. An expert
+ * chosen twice by a token counts twice.
+ * For a few tokens: the weights of every expert that some token chose are read once for every 128
+ * tokens. 1 <= experts <= 1024, 1 <= top <= 32. */
+typedef struct {
+  int64_t m, n, k, f;
+  int64_t experts, first, top;
+  int64_t dtype, out_dtype, act;
+  coll_stack_t w_gate, w_up, w_down;
+  coll_mat_t x, ids, weights, residual, y;
+  void *workspace;
+  uint64_t workspace_bytes;
+  int32_t *status;
+} coll_experts_t;
+
+int coll_gated_experts(const coll_experts_t *a, void *stream);
+int64_t coll_gated_experts_workspace(const coll_experts_t *a);
+
 #ifdef __cplusplus
 }
 #endif
