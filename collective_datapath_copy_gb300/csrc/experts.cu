@@ -2,13 +2,24 @@
 //
 //   h_ij = act(gate_e x_i) (up_e x_i),  y_i = residual_i + sum over j of weights_ij down_e h_ij,
 //   e = ids_ij - first
+//
+// Bound by HBM: the weights of every chosen expert are read once, 6 n f bytes each (n = k), and a
+// token or two an expert multiply them. Three launches: plan_kernel sorts the choices by expert;
+// product_kernel<true> computes the inner values, product_kernel<false> the sums. Both are
+// persistent, a CTA an SM, and share their work to the k block: the list of (expert, tile of 128
+// features) is one line of k blocks that is cut into 152 equal lengths, because whole tiles would
+// leave SMs idle (8 experts of 2048 inner features are 128 tiles). A tile that is cut joins in the
+// last of its CTAs to arrive, in the order of k: nothing waits, and results do not depend on timing.
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+#include <string.h>
 
 #include "dense.h"
 #include "dense_check.h"
 #include "dense_epi.cuh"
-#include "tma.cuh"
+#include "dense_tc.h"
+#include "tcgen05.cuh"
 
 namespace coll {
 namespace {
@@ -91,6 +102,527 @@ __global__ void __launch_bounds__(kWarps * 32) outer_kernel(const ExpertsParams 
   }
 }
 
+// ---------------------------------------------------------------- choices sorted by expert
+
+constexpr int kGroup = 128;    // tokens that a launch takes
+constexpr int kTileK = 64;
+constexpr int kPlanThreads = 1024;
+
+// What plan_kernel leaves for the products: chunks of at most `cols` choices of one expert, each
+// choice's token and weight in the order of the chunks. A chunk's choices start on a multiple of
+// four, so that four of their tokens are one load.
+struct PlanOut {
+  int32_t *chunks;   // their number
+  int4 *chunk;       // {expert, first place, choices, 0}
+  int32_t *token;
+  float *weight;
+  uint32_t *counters;  // of cut tiles, all set to 0
+};
+
+struct PlanParams {
+  DenseMat ids, weights;  // of this group's tokens
+  PlanOut out;
+  DenseMat x;             // rows to lay out; p NULL: none
+  uint16_t *packed;
+  int64_t k, packed_ld;
+  uint32_t counters;
+  int32_t tokens, top, experts, first, cols;
+};
+
+// CTA 0 plans; the others lay out x in rows of whole 16-byte runs where no tensor copy takes it as
+// it lies.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+  __shared__ int16_t expert[kGroup * kMostChosen];
+  __shared__ uint32_t base[kMostExperts];  // chunks before it << 16 | places before it
+  __shared__ uint16_t count[kMostExperts];
+  __shared__ uint32_t sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+  griddep_launch();
+  griddep_wait();
+  if (blockIdx.x > 0) {
+    const int64_t runs = p.packed_ld / 8, all = runs * p.tokens;
+    for (int64_t r = (int64_t)(blockIdx.x - 1) * blockDim.x + tid; r < all;
+         r += (int64_t)(gridDim.x - 1) * blockDim.x) {
+      const int64_t i = r / runs, k = r % runs * 8;
+      const uint16_t *q = static_cast<const uint16_t *>(p.x.p) + i * p.x.rs + k * p.x.cs;
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = k + j < p.k ? q[j * p.x.cs] : 0u;
+      *reinterpret_cast<uint4 *>(p.packed + i * p.packed_ld + k) =
+          make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+    return;
+  }
+  const int n = p.tokens * p.top;
+  for (int s = tid; s < n; s += blockDim.x) {
+    const int i = s / p.top, j = s - i * p.top;
+    const int id = static_cast<const int32_t *>(p.ids.p)[i * p.ids.rs + j * p.ids.cs];
+    const int64_t e = (int64_t)id - p.first;
+    expert[s] = id >= 0 && e >= 0 && e < p.experts ? (int16_t)e : (int16_t)-1;
+  }
+  for (uint32_t i = tid; i < p.counters; i += blockDim.x) p.out.counters[i] = 0u;
+  __syncthreads();
+  for (int e = warp; e < p.experts; e += warps) {
+    int c = 0;
+    for (int s = lane; s - lane < n; s += 32)
+      c += __popc(__ballot_sync(~0u, s < n && expert[s] == e));
+    if (lane == 0) count[e] = (uint16_t)c;
+  }
+  __syncthreads();
+  // exclusive sums over the experts, one a thread
+  uint32_t mine = 0u;
+  if (tid < p.experts) {
+    const uint32_t c = count[tid];
+    mine = ((c + p.cols - 1) / p.cols) << 16 | ((c + 3u) & ~3u);
+  }
+  uint32_t run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(~0u, run, o);
+    if (lane >= o) run += v;
+  }
+  if (lane == 31) sums[warp] = run;
+  __syncthreads();
+  uint32_t before = 0u, all = 0u;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += sums[w];
+    all += sums[w];
+  }
+  if (tid < p.experts) base[tid] = before + run - mine;
+  if (tid == 0) *p.out.chunks = (int32_t)(all >> 16);
+  __syncthreads();
+  for (int e = warp; e < p.experts; e += warps) {
+    const int c = count[e];
+    if (c == 0) continue;
+    const int first = (int)(base[e] >> 16), at = (int)(base[e] & 0xFFFFu);
+    for (int q = lane; q * p.cols < c; q += 32)
+      p.out.chunk[first + q] = make_int4(e, at + q * p.cols, min(p.cols, c - q * p.cols), 0);
+    int done = 0;
+    for (int s = lane; s - lane < n; s += 32) {
+      const bool hit = s < n && expert[s] == e;
+      const uint32_t mask = __ballot_sync(~0u, hit);
+      if (hit) {
+        const int place = at + done + __popc(mask & ((1u << lane) - 1u));
+        const int i = s / p.top, j = s - i * p.top;
+        p.out.token[place] = i;
+        p.out.weight[place] =
+            static_cast<const float *>(p.weights.p)[i * p.weights.rs + j * p.weights.cs];
+      }
+      done += __popc(mask);
+    }
+    if (lane < ((c + 3) & ~3) - c) {  // up to the next chunk: any token, its product is not used
+      p.out.token[at + c + lane] = 0;
+      p.out.weight[at + c + lane] = 0.0f;
+    }
+  }
+}
+
+// ---------------------------------------------------------------- products
+
+constexpr int kThreads = 192;  // warp 0 loads, 1 matrix instructions and TMEM, 2-5 epilogue
+constexpr int kMaxStages = 12;
+constexpr uint32_t kTile = 128 * 128;  // bytes of 128 rows of one k block
+
+struct ProductParams {
+  CUtensorMap w[2], b;  // weights {k, rows, experts}; tokens {k, rows}, by four rows or by 16
+  PlanOut plan;
+  DenseMat res;         // sums only
+  void *out;            // inner values [place][out_rs], or y
+  int64_t out_rs;
+  float *part;          // of cut tiles
+  int32_t *status;
+  int32_t rows;         // output features of a tile: at most 128
+  int32_t features;     // of the product
+  int32_t tiles, kblocks, cols, tokens;
+  int32_t stages;
+  uint32_t stage_bytes, ring;
+  int32_t type, out_type, act;
+  int32_t nothing;      // sums of nothing: y = residual
+};
+
+struct Shared {
+  uint64_t full[kMaxStages], empty[kMaxStages], ready[2], free[2];
+  uint32_t tmem, abort, last;
+};
+
+__device__ __forceinline__ void tma_box3(uint32_t sdst, const void *map, int32_t x, int32_t y,
+                                         int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(sdst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+// Rows r of a two-dimensional map of boxes one row high, from column x on.
+__device__ __forceinline__ void tma_gather4(uint32_t sdst, const void *map, int32_t x, int4 r,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4"
+      ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(sdst),
+      "l"(map), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
+      : "memory");
+}
+
+// 16 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// This CTA's length of the line of k blocks, cut into `ctas` lengths of `all` in total.
+struct Line {
+  uint32_t all, ctas;
+  __device__ uint32_t begin(uint32_t c) const {
+    return (uint32_t)((uint64_t)all * c / ctas);
+  }
+  // whose length block u is in
+  __device__ uint32_t owner(uint32_t u) const {
+    return (uint32_t)((((uint64_t)u + 1) * ctas - 1) / all);
+  }
+};
+
+// Part of a tile: k blocks [k0, k1) of tile `tile` of chunk `chunk`.
+struct Piece {
+  int chunk, tile, k0, k1;
+};
+
+// INNER walks chunk by chunk, tile after tile: all of an expert's rows. The sums walk tile by tile,
+// chunk after chunk, so that one tile's sums over the experts stay in the CTA.
+template <bool INNER>
+__device__ __forceinline__ Piece piece_at(const ProductParams &p, int chunks, uint32_t u,
+                                          uint32_t end) {
+  const uint32_t item = u / (uint32_t)p.kblocks;
+  Piece q;
+  q.k0 = (int)(u - item * (uint32_t)p.kblocks);
+  q.k1 = (int)min((uint32_t)p.kblocks, q.k0 + (end - u));
+  if (INNER) {
+    q.chunk = (int)(item / (uint32_t)p.tiles);
+    q.tile = (int)(item - (uint32_t)q.chunk * p.tiles);
+  } else {
+    q.tile = (int)(item / (uint32_t)chunks);
+    q.chunk = (int)(item - (uint32_t)q.tile * chunks);
+  }
+  return q;
+}
+
+__device__ __forceinline__ void epilogue_sync() {
+  asm volatile("bar.sync 1, 128;" ::: "memory");
+}
+
+// Have all of the epilogue's threads got this far without giving up? Every cut tile asks, so that no
+// thread waits at a barrier that another has passed by.
+__device__ __forceinline__ bool epilogue_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0u;
+}
+
+// After this CTA's share of `job` is in memory: is it the last of `shares`? The others' are visible
+// to the epilogue's threads then.
+__device__ __forceinline__ bool arrive_last(const ProductParams &p, Shared &sh, int job,
+                                            uint32_t shares, int tid) {
+  __threadfence();
+  epilogue_sync();
+  if (tid == 0) sh.last = atomicAdd(&p.plan.counters[job], 1u) == shares - 1u;
+  epilogue_sync();
+  const bool last = sh.last != 0u;
+  if (last) __threadfence();
+  return last;
+}
+
+__device__ __forceinline__ void inner_out(const ProductParams &p, int64_t place, int f, int rows,
+                                          float (&g)[16], const float (&u)[16]) {
+  act_run(g, p.act);
+  uint16_t *o = static_cast<uint16_t *>(p.out) + place * p.out_rs + f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    if (i < rows) o[i * p.out_rs] = f2h(g[i] * u[i], p.type);
+}
+
+template <bool INNER>
+__global__ void __launch_bounds__(kThreads, 1)
+    product_kernel(const __grid_constant__ ProductParams p) {
+  extern __shared__ uint8_t raw[];
+  __shared__ Shared sh;
+  const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
+  const uint32_t ready0 = smem_u32(&sh.ready[0]), free0 = smem_u32(&sh.free[0]);
+  constexpr int W = INNER ? 2 : 1;
+  const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
+  uint32_t tmem_cols = 32;
+  while (tmem_cols < 2u * W * p.cols) tmem_cols *= 2;
+
+  if (threadIdx.x == 0) {
+    for (uint32_t i = 0; i < stages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.ready[i], 1);
+      mbar_init(&sh.free[i], 4);
+    }
+    sh.abort = 0u;
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc<1>(&sh.tmem, tmem_cols);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  griddep_launch();
+  griddep_wait();
+
+  const int chunks = p.nothing ? 0 : *p.plan.chunks;
+  Line line;
+  line.all = (uint32_t)chunks * (uint32_t)p.tiles * (uint32_t)p.kblocks;
+  line.ctas = min(gridDim.x, line.all);
+  const uint32_t cta = blockIdx.x;
+  uint32_t u = 0, end = 0;
+  if (cta < line.ctas) {
+    u = line.begin(cta);
+    end = line.begin(cta + 1);
+  }
+
+  if (warp == 0) {
+    uint32_t s = 0, phase = 0;
+    bool ok = true;
+    while (u < end) {
+      const Piece q = piece_at<INNER>(p, chunks, u, end);
+      const int4 c = p.plan.chunk[q.chunk];
+      const int fours = (c.z + 3) / 4, sixteens = (c.z + 15) / 16;
+      int4 tok = make_int4(0, 0, 0, 0);
+      if (INNER && lane < fours)
+        tok = *reinterpret_cast<const int4 *>(p.plan.token + c.y + 4 * lane);
+      const uint32_t bytes =
+          W * (uint32_t)p.rows * 128u + (INNER ? (uint32_t)fours * 512u : (uint32_t)sixteens * 2048u);
+      for (int kb = q.k0; kb < q.k1; ++kb) {
+        ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
+        const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes;
+        const int32_t k = kb * kTileK;
+        if (elect_one() && ok) {
+          bar_expect(bar, bytes);
+#pragma unroll
+          for (int w = 0; w < W; ++w)
+            tma_box3(at + w * kTile, &p.w[w], k, q.tile * p.rows, c.x, bar);
+          if (!INNER)
+            for (int i = 0; i < sixteens; ++i)
+              tma_box(at + W * kTile + i * 2048u, &p.b, k, c.y + 16 * i, bar);
+        }
+        __syncwarp();
+        if (INNER && ok && lane < fours) tma_gather4(at + W * kTile + lane * 512u, &p.b, k, tok, bar);
+        __syncwarp();
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1u;
+        }
+      }
+      u += q.k1 - q.k0;
+    }
+  } else if (warp == 1) {
+    const uint32_t hi = desc_hi(1024), step = stage_bytes >> 4;
+    uint32_t a = desc_lo(ring, 16u), b = desc_lo(ring + W * kTile, 16u);
+    uint32_t s = 0, phase = 0, d = 0, dphase = 0;
+    bool ok = true;
+    while (u < end) {
+      const Piece q = piece_at<INNER>(p, chunks, u, end);
+      const uint32_t n = (uint32_t)(p.plan.chunk[q.chunk].z + 15) & ~15u;
+      const uint32_t idesc = mma_desc(p.type == COLL_BF16, false, false, 128, n);
+      const uint32_t d0 = tmem + d * W * p.cols, d1 = d0 + p.cols;
+      ok = ok && wait_bar(&sh.abort, free0 + 8 * d, dphase ^ 1u, p.status);
+      tc_fence_after();
+      uint32_t add = 0;
+      for (int kb = q.k0; kb < q.k1; ++kb) {
+        ok = ok && wait_bar(&sh.abort, full0 + 8 * s, phase, p.status);
+        tc_fence_after();
+        if (elect_one() && ok) {
+#pragma unroll
+          for (uint32_t i = 0; i < 4; ++i) {
+            mma_f16<1>(d0, a + 2 * i, hi, b + 2 * i, hi, idesc, i ? 1u : add);
+            if (INNER)
+              mma_f16<1>(d1, a + (kTile >> 4) + 2 * i, hi, b + 2 * i, hi, idesc, i ? 1u : add);
+          }
+          mma_commit<1>(empty0 + 8 * s, 0);
+        }
+        __syncwarp();
+        add = 1;
+        a += step;
+        b += step;
+        if (++s == stages) {
+          s = 0;
+          phase ^= 1u;
+          a -= stages * step;
+          b -= stages * step;
+        }
+      }
+      if (elect_one() && ok) mma_commit<1>(ready0 + 8 * d, 0);
+      __syncwarp();
+      dphase ^= d;
+      d ^= 1u;
+      u += q.k1 - q.k0;
+    }
+  } else {
+    const int quad = warp & 3, row = quad * 32 + lane;
+    const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t step = INNER ? (uint32_t)p.kblocks : (uint32_t)p.kblocks * (uint32_t)chunks;
+    float *sums = reinterpret_cast<float *>(raw + (ring - smem_u32(raw)) + p.ring) + row;
+    uint32_t d = 0, dphase = 0;
+    bool ok = true;
+    if (!INNER && chunks == 0) {
+      for (int t = (int)cta; t < p.tiles; t += (int)gridDim.x) {
+        const int f = t * p.rows + row;
+        if (row >= p.rows || f >= p.features) continue;
+        for (int i = 0; i < p.tokens; ++i)
+          st_elem(p.out, i * p.out_rs + f,
+                  p.res.p ? ld_elem(p.res.p, i * p.res.rs + f * p.res.cs, p.out_type) : 0.0f,
+                  p.out_type);
+      }
+    }
+    while (u < end) {
+      // a cut tile (sums: all of a tile's chunks) belongs to CTAs [c0, c1]
+      const uint32_t job = u / step;
+      const uint32_t c0 = line.owner(job * step), c1 = line.owner(job * step + step - 1);
+      const uint32_t job_end = min(end, job * step + step);
+      // its share in memory: that of a tile begun by an earlier CTA, or of one ended by a later
+      const int64_t share = (int64_t)INNER ? (int64_t)2 * p.cols * 128 : (int64_t)p.tokens * 128;
+      float *part = p.part + (2 * (int64_t)cta + (cta == c0)) * share + row;
+      if (!INNER)
+        for (int i = 0; i < p.tokens; ++i) sums[i * 128] = 0.0f;
+      while (u < job_end) {
+        const Piece q = piece_at<INNER>(p, chunks, u, job_end);
+        const int4 c = p.plan.chunk[q.chunk];
+        const int f = q.tile * p.rows + row;
+        const bool live = row < p.rows && f < p.features;
+        ok = ok && __all_sync(~0u, wait_bar(&sh.abort, ready0 + 8 * d, dphase, p.status));
+        tc_fence_after();
+        const uint32_t from = lanes + d * W * p.cols;
+        for (int i0 = 0; ok && i0 < c.z; i0 += 16) {
+          const int rows = min(16, c.z - i0);
+          float v[16];
+          tmem_load16(from + i0, v);
+          if constexpr (INNER) {
+            float up[16];
+            tmem_load16(from + p.cols + i0, up);
+            if (c0 == c1) {
+              if (live) inner_out(p, c.y + i0, f, rows, v, up);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (i < rows) {
+                  __stcg(part + (i0 + i) * 128, v[i]);
+                  __stcg(part + (p.cols + i0 + i) * 128, up[i]);
+                }
+            }
+          } else {
+            int tok = 0;
+            float wt = 0.0f;
+            if (lane < rows) {
+              tok = p.plan.token[c.y + i0 + lane];
+              wt = p.plan.weight[c.y + i0 + lane];
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const int t = __shfl_sync(~0u, tok, i);
+              const float w = __shfl_sync(~0u, wt, i);
+              if (i < rows) sums[t * 128] = fmaf(w, v[i], sums[t * 128]);
+            }
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (elect_one())
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(free0 + 8 * d) : "memory");
+        dphase ^= d;
+        d ^= 1u;
+        u += q.k1 - q.k0;
+      }
+      if (c0 != c1) ok = epilogue_all(ok);
+      if (!ok) continue;
+      if (INNER) {
+        if (c0 != c1 && arrive_last(p, sh, (int)job, c1 - c0 + 1, (int)threadIdx.x - 64)) {
+          const Piece q = piece_at<INNER>(p, chunks, job * step, line.all);
+          const int4 c = p.plan.chunk[q.chunk];
+          const int f = q.tile * p.rows + row;
+          const bool live = row < p.rows && f < p.features;
+          for (int i0 = 0; i0 < c.z; i0 += 16) {
+            const int rows = min(16, c.z - i0);
+            float g[16], up[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) g[i] = up[i] = 0.0f;
+            for (uint32_t w = c0; w <= c1; ++w) {
+              const float *o = p.part + (2 * (int64_t)w + (w == c0)) * share + row;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (i < rows) {
+                  g[i] += __ldcg(o + (i0 + i) * 128);
+                  up[i] += __ldcg(o + (p.cols + i0 + i) * 128);
+                }
+            }
+            if (live) inner_out(p, c.y + i0, f, rows, g, up);
+          }
+        }
+      } else {
+        const int f = (int)job * p.rows + row;
+        const bool live = row < p.rows && f < p.features;
+        bool write = c0 == c1;
+        if (!write) {
+          for (int i = 0; i < p.tokens; ++i) __stcg(part + i * 128, sums[i * 128]);
+          write = arrive_last(p, sh, (int)job, c1 - c0 + 1, (int)threadIdx.x - 64);
+          if (write) {
+            for (int i0 = 0; i0 < p.tokens; i0 += 16) {
+              float v[16];
+#pragma unroll
+              for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+              for (uint32_t w = c0; w <= c1; ++w) {
+                const float *o = p.part + (2 * (int64_t)w + (w == c0)) * share + row;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (i0 + i < p.tokens) v[i] += __ldcg(o + (i0 + i) * 128);
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (i0 + i < p.tokens) sums[(i0 + i) * 128] = v[i];
+            }
+          }
+        }
+        if (write && live) {
+          for (int i = 0; i < p.tokens; ++i) {
+            float v = sums[i * 128];
+            if (p.res.p) v += ld_elem(p.res.p, i * p.res.rs + f * p.res.cs, p.out_type);
+            st_elem(p.out, i * p.out_rs + f, v, p.out_type);
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (sh.abort) drain();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_free<1>(tmem, tmem_cols);
+  }
+}
+
+// ---------------------------------------------------------------- host
+
 int check_stack(const coll_stack_t &w, int64_t e, int64_t rows, int64_t cols, View &v) {
   const int64_t lim = (int64_t)kAddressable;
   v = View{w.ptr, 0, 0, 0, 1, 2};
@@ -132,14 +664,167 @@ int check(const coll_experts_t &a) {
   return k.finish(res);
 }
 
-int64_t need(const coll_experts_t &a) {
-  if (a.m == 0 || a.n == 0) return 0;
-  const uint64_t slots = (uint64_t)(a.m * a.top);
-  if (a.f && slots > kAddressable / 2 / (uint64_t)a.f) return COLL_EINVAL;
-  return (int64_t)(slots * a.f * 2 + 128);
+int64_t round_up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// A stack that a tensor copy takes as it lies: its base and strides on 16 bytes.
+bool copied(const coll_stack_t &w, int64_t e, int64_t rows) {
+  return (uintptr_t)w.ptr % 16 == 0 && (e == 1 || (w.es > 0 && w.es % 8 == 0)) &&
+         (rows == 1 || (w.rs > 0 && w.rs % 8 == 0));
 }
 
-int run(const coll_experts_t &a, cudaStream_t s) {
+// Rows of tokens the same.
+bool copied(const coll_mat_t &x, int64_t rows, int64_t k) {
+  return (uintptr_t)x.ptr % 16 == 0 && (x.cs == 1 || k == 1) &&
+         (rows == 1 || (x.rs > 0 && x.rs % 8 == 0));
+}
+
+int encode(CUtensorMap *map, int64_t type, int rank, const void *base, const cuuint64_t *dims,
+           const cuuint64_t *strides, uint32_t rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
+  if (!fn) return COLL_ECUDA;
+  const cuuint32_t box[3] = {kTileK, rows, 1}, step[3] = {1, 1, 1};
+  return fn(map,
+            type == COLL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+            (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? COLL_OK
+             : COLL_EINVAL;
+}
+
+int encode_stack(CUtensorMap *map, int64_t type, const coll_stack_t &w, int64_t e, int64_t rows,
+                 int64_t k, int box) {
+  // the stride of a dimension of one is not used, but has to be one that a map may have
+  const int64_t line = round_up(k, 8);
+  const cuuint64_t dims[3] = {(cuuint64_t)k, (cuuint64_t)rows, (cuuint64_t)e};
+  const cuuint64_t strides[2] = {(cuuint64_t)(rows == 1 ? line : w.rs) * 2,
+                                 (cuuint64_t)(e == 1 ? line : w.es) * 2};
+  return encode(map, type, 3, w.ptr, dims, strides, (uint32_t)box);
+}
+
+int encode_rows(CUtensorMap *map, int64_t type, const void *base, int64_t rows, int64_t k,
+                int64_t ld, int box) {
+  const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
+  return encode(map, type, 2, base, dims, strides, (uint32_t)box);
+}
+
+// The workspace of a group of tokens, and the shapes of its launches.
+struct Layout {
+  int64_t tokens, places, chunks, ld, packed_ld;
+  int32_t cols;
+  bool simple, pack;
+  ProductParams inner, outer;
+  PlanParams plan;
+  uint64_t bytes;
+};
+
+int lay_out(const coll_experts_t &a, Layout &l, char *base) {
+  memset(&l, 0, sizeof(l));
+  l.tokens = a.m < kGroup ? a.m : kGroup;
+  l.simple = a.k > 0 && a.f > 0 &&
+             !(copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f) &&
+               copied(a.w_down, a.experts, a.n));
+  uint64_t used = 0;
+  bool over = false;
+  auto take = [&](uint64_t bytes) -> char * {
+    if (bytes > kAddressable - used) {
+      over = true;
+      return nullptr;
+    }
+    const uint64_t at = used;
+    used += (bytes + 255) & ~(uint64_t)255;
+    return base ? base + at : nullptr;
+  };
+  if (l.simple) {
+    const uint64_t slots = (uint64_t)(a.m * a.top);
+    if (slots > kAddressable / 2 / (uint64_t)a.f) return COLL_EINVAL;
+    take(slots * a.f * 2);
+    l.bytes = used;
+    return COLL_OK;
+  }
+  l.cols = (int32_t)round_up(l.tokens, 16);
+  const int64_t choices = l.tokens * a.top;
+  l.chunks = (a.experts < choices ? a.experts : choices) + choices / l.cols;
+  l.places = choices + 3 * l.chunks;
+  l.ld = round_up(a.f, 64);
+  l.pack = !copied(a.x, a.m, a.k) && a.k > 0;
+  ProductParams &p = l.inner, &q = l.outer;
+  p.tiles = (int32_t)ceil_div(a.f, 128);
+  q.tiles = (int32_t)ceil_div(a.n, 128);
+  p.rows = (int32_t)round_up(ceil_div(a.f, p.tiles ? p.tiles : 1), 8);
+  q.rows = (int32_t)round_up(ceil_div(a.n, q.tiles), 8);
+  p.features = (int32_t)a.f;
+  q.features = (int32_t)a.n;
+  p.kblocks = (int32_t)ceil_div(a.k, kTileK);
+  q.kblocks = (int32_t)ceil_div(a.f, kTileK);
+  // the line of k blocks is counted in 32 bits
+  if ((uint64_t)l.chunks * p.tiles * p.kblocks >> 32 || (uint64_t)l.chunks * q.tiles * q.kblocks >> 32)
+    return COLL_EINVAL;
+  q.nothing = a.k == 0 || a.f == 0;
+  p.cols = q.cols = l.cols;
+  p.type = q.type = (int32_t)a.dtype;
+  p.out_type = (int32_t)a.dtype;
+  q.out_type = (int32_t)a.out_dtype;
+  p.act = (int32_t)a.act;
+  p.status = q.status = a.status;
+  auto ring = [&](ProductParams &r, int w, uint32_t fixed) {
+    r.stage_bytes = w * kTile + (uint32_t)l.cols * 128u;
+    r.stages = (int32_t)((kTcSmem - 1024 - fixed) / r.stage_bytes);
+    if (r.stages > kMaxStages) r.stages = kMaxStages;
+    r.ring = r.stages * r.stage_bytes;
+  };
+  ring(p, 2, 0);
+  ring(q, 1, (uint32_t)l.tokens * 512u);
+  PlanParams &s = l.plan;
+  s.top = (int32_t)a.top;
+  s.experts = (int32_t)a.experts;
+  s.first = (int32_t)a.first;
+  s.cols = l.cols;
+  s.k = a.k;
+  const int64_t jobs = l.chunks * p.tiles;
+  s.counters = (uint32_t)(jobs + q.tiles);
+  PlanOut &o = s.out;
+  o.chunks = reinterpret_cast<int32_t *>(take(4));
+  o.chunk = reinterpret_cast<int4 *>(take((uint64_t)l.chunks * 16));
+  o.token = reinterpret_cast<int32_t *>(take((uint64_t)l.places * 4));
+  o.weight = reinterpret_cast<float *>(take((uint64_t)l.places * 4));
+  o.counters = reinterpret_cast<uint32_t *>(take((uint64_t)s.counters * 4));
+  p.plan = q.plan = o;
+  if (base) q.plan.counters = o.counters + jobs;
+  p.out = take((uint64_t)l.places * l.ld * 2);
+  p.out_rs = l.ld;
+  const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
+  p.part = q.part = reinterpret_cast<float *>(take(2 * kSms * (inner > outer ? inner : outer)));
+  if (l.pack) {
+    l.packed_ld = round_up(a.k, 64);
+    s.packed = reinterpret_cast<uint16_t *>(take((uint64_t)l.tokens * l.packed_ld * 2));
+    s.packed_ld = l.packed_ld;
+  }
+  l.bytes = used;
+  return over ? COLL_EINVAL : COLL_OK;
+}
+
+int64_t need(const coll_experts_t &a) {
+  if (a.m == 0 || a.n == 0) return 0;
+  Layout l;
+  const int c = lay_out(a, l, nullptr);
+  return c ? c : (int64_t)l.bytes + 128;  // room to start on 128 bytes
+}
+
+template <bool INNER>
+int set_up() {
+  static DenseSmemLimit limit;
+  return limit((const void *)product_kernel<INNER>, kTcSmem) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+}
+
+template <bool INNER>
+cudaError_t launch(const ProductParams &p, cudaStream_t s) {
+  return dense_launch(product_kernel<INNER>, dim3(kSms), kThreads, kTcSmem, 1, s, p);
+}
+
+int run_simple(const coll_experts_t &a, uint16_t *h, cudaStream_t s) {
   ExpertsParams p = {};
   p.gate = static_cast<const uint16_t *>(a.w_gate.ptr);
   p.up = static_cast<const uint16_t *>(a.w_up.ptr);
@@ -153,7 +838,7 @@ int run(const coll_experts_t &a, cudaStream_t s) {
   p.res = DenseMat{a.residual.ptr, a.residual.rs, a.residual.cs};
   p.y = a.y.ptr;
   p.y_rs = a.y.rs;
-  p.h = reinterpret_cast<uint16_t *>(((uintptr_t)a.workspace + 127) & ~(uintptr_t)127);
+  p.h = h;
   p.m = a.m, p.n = a.n, p.k = a.k, p.f = a.f;
   p.experts = (int32_t)a.experts;
   p.first = (int32_t)a.first;
@@ -161,11 +846,57 @@ int run(const coll_experts_t &a, cudaStream_t s) {
   p.type = (int32_t)a.dtype;
   p.out_type = (int32_t)a.out_dtype;
   p.act = (int32_t)a.act;
-  const dim3 grid(152 * 8);
-  cudaError_t e = cudaSuccess;
-  if (a.f > 0) e = dense_launch(inner_kernel, grid, kWarps * 32, 0, 1, s, p);
+  const dim3 grid(kSms * 8);
+  cudaError_t e = dense_launch(inner_kernel, grid, kWarps * 32, 0, 1, s, p);
   if (e == cudaSuccess) e = dense_launch(outer_kernel, grid, kWarps * 32, 0, 1, s, p);
   return e == cudaSuccess ? COLL_OK : COLL_ECUDA;
+}
+
+int run(const coll_experts_t &a, char *base, cudaStream_t s) {
+  Layout l;
+  int c = lay_out(a, l, base);
+  if (c) return c;
+  if (l.simple) return run_simple(a, reinterpret_cast<uint16_t *>(base), s);
+  ProductParams &p = l.inner, &q = l.outer;
+  c = set_up<true>();
+  if (!c) c = set_up<false>();
+  if (!c && !q.nothing) {
+    c = encode_stack(&p.w[0], a.dtype, a.w_gate, a.experts, a.f, a.k, p.rows);
+    if (!c) c = encode_stack(&p.w[1], a.dtype, a.w_up, a.experts, a.f, a.k, p.rows);
+    if (!c) c = encode_stack(&q.w[0], a.dtype, a.w_down, a.experts, a.n, a.f, q.rows);
+    if (!c) c = encode_rows(&q.b, a.dtype, p.out, l.places, a.f, l.ld, 16);
+    // the first group's rows as a trial of them all
+    if (!c)
+      c = l.pack ? encode_rows(&p.b, a.dtype, l.plan.packed, l.tokens, a.k, l.packed_ld, 1)
+                 : encode_rows(&p.b, a.dtype, a.x.ptr, l.tokens, a.k,
+                               a.m == 1 ? round_up(a.k, 8) : a.x.rs, 1);
+  }
+  if (c) return c;
+  const int oe = esize(a.out_dtype);
+  for (int64_t t = 0; t < a.m; t += l.tokens) {
+    const int64_t tokens = a.m - t < l.tokens ? a.m - t : l.tokens;
+    PlanParams &o = l.plan;
+    o.ids = DenseMat{static_cast<const int32_t *>(a.ids.ptr) + t * a.ids.rs, a.ids.rs, a.ids.cs};
+    o.weights = DenseMat{static_cast<const float *>(a.weights.ptr) + t * a.weights.rs,
+                         a.weights.rs, a.weights.cs};
+    o.tokens = p.tokens = q.tokens = (int32_t)tokens;
+    const uint16_t *x = static_cast<const uint16_t *>(a.x.ptr) + t * a.x.rs;
+    if (l.pack) o.x = DenseMat{x, a.x.rs, a.x.cs};
+    else if (t && !q.nothing)
+      c = encode_rows(&p.b, a.dtype, x, tokens, a.k, a.x.rs, 1);
+    if (c) return c;
+    q.out = static_cast<char *>(a.y.ptr) + t * a.y.rs * oe;
+    q.out_rs = a.y.rs;
+    if (a.residual.ptr)
+      q.res = DenseMat{static_cast<const char *>(a.residual.ptr) + t * a.residual.rs * oe,
+                       a.residual.rs, a.residual.cs};
+    const unsigned more = l.pack ? (unsigned)ceil_div(tokens * l.packed_ld / 8, kPlanThreads) : 0;
+    cudaError_t e = dense_launch(plan_kernel, dim3(1 + more), kPlanThreads, 0, 1, s, o);
+    if (e == cudaSuccess && !q.nothing) e = launch<true>(p, s);
+    if (e == cudaSuccess) e = launch<false>(q, s);
+    if (e != cudaSuccess) return COLL_ECUDA;
+  }
+  return COLL_OK;
 }
 
 }  // namespace
@@ -184,5 +915,6 @@ extern "C" int coll_gated_experts(const coll_experts_t *a, void *stream) {
   if (n && (!a->workspace || ((uintptr_t)a->workspace & 15u) ||
             a->workspace_bytes < (uint64_t)n))
     return COLL_EWORKSPACE;
-  return coll::run(*a, static_cast<cudaStream_t>(stream));
+  char *base = reinterpret_cast<char *>(((uintptr_t)a->workspace + 127) & ~(uintptr_t)127);
+  return coll::run(*a, base, static_cast<cudaStream_t>(stream));
 }
