@@ -27,7 +27,8 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompil
 CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", f"-I{INCLUDE}", f"-I{CSRC}"]
 
 CU_SOURCES = ["engine.cu", "bulk.cu", "api.cu", "noalloc.cu", "dense.cu", "dense_tc.cu",
-              "dense_skinny.cu", "dense_gemv.cu", "dense_aux.cu", "route.cu", "experts.cu"]
+              "dense_skinny.cu", "dense_gemv.cu", "dense_aux.cu", "route.cu", "experts.cu",
+              "experts_direct.cu"]
 CXX_SOURCES = ["plan.cpp"]
 
 

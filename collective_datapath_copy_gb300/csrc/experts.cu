@@ -19,122 +19,34 @@
 #include "dense_check.h"
 #include "dense_epi.cuh"
 #include "dense_tc.h"
+#include "experts.h"
 #include "tcgen05.cuh"
 
 namespace coll {
 namespace {
 
-constexpr int kMostExperts = 1024;
-constexpr int kMostChosen = 32;
-constexpr int kWarps = 8;
-
-struct ExpertsParams {
-  const uint16_t *gate, *up, *down;
-  int64_t gate_es, gate_rs, up_es, up_rs, down_es, down_rs;
-  DenseMat x, ids, weights, res;
-  void *y;
-  int64_t y_rs;
-  uint16_t *h;  // [m * top][f]
-  int64_t m, n, k, f;
-  int32_t experts, first, top, type, out_type, act;
-};
-
-__device__ __forceinline__ int local_id(const ExpertsParams &p, int64_t i, int j) {
-  const int id = static_cast<const int32_t *>(p.ids.p)[i * p.ids.rs + j * p.ids.cs];
-  const int64_t e = (int64_t)id - p.first;
-  return id >= 0 && e >= 0 && e < p.experts ? (int)e : -1;
-}
-
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-  return v;
-}
-
-// A warp for each inner feature of each (token, choice).
-__global__ void __launch_bounds__(kWarps * 32) inner_kernel(const ExpertsParams p) {
-  griddep_launch();
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t all = p.m * p.top * p.f;
-  for (int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); w < all;
-       w += (int64_t)gridDim.x * kWarps) {
-    const int64_t slot = w / p.f, f = w % p.f, i = slot / p.top;
-    const int e = local_id(p, i, (int)(slot % p.top));
-    if (e < 0) continue;
-    const uint16_t *x = static_cast<const uint16_t *>(p.x.p) + i * p.x.rs;
-    const uint16_t *a = p.gate + e * p.gate_es + f * p.gate_rs;
-    const uint16_t *b = p.up + e * p.up_es + f * p.up_rs;
-    float g = 0.0f, u = 0.0f;
-    for (int64_t k = lane; k < p.k; k += 32) {
-      const float v = h2f(x[k * p.x.cs], p.type);
-      g = fmaf(v, h2f(a[k], p.type), g);
-      u = fmaf(v, h2f(b[k], p.type), u);
-    }
-    g = warp_sum(g);
-    u = warp_sum(u);
-    if (lane == 0) p.h[slot * p.f + f] = f2h(act_value(g, p.act) * u, p.type);
-  }
-}
-
-// A warp for each output.
-__global__ void __launch_bounds__(kWarps * 32) outer_kernel(const ExpertsParams p) {
-  griddep_launch();
-  griddep_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t all = p.m * p.n;
-  for (int64_t w = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); w < all;
-       w += (int64_t)gridDim.x * kWarps) {
-    const int64_t i = w / p.n, n = w % p.n;
-    float y = p.res.p ? ld_elem(p.res.p, i * p.res.rs + n * p.res.cs, p.out_type) : 0.0f;
-    for (int j = 0; j < p.top; ++j) {
-      const int e = local_id(p, i, j);
-      if (e < 0) continue;
-      const uint16_t *h = p.h + (i * p.top + j) * p.f;
-      const uint16_t *a = p.down + e * p.down_es + n * p.down_rs;
-      float d = 0.0f;
-      for (int64_t f = lane; f < p.f; f += 32)
-        d = fmaf(h2f(h[f], p.type), h2f(a[f], p.type), d);
-      d = warp_sum(d);
-      y = fmaf(static_cast<const float *>(p.weights.p)[i * p.weights.rs + j * p.weights.cs], d, y);
-    }
-    if (lane == 0) st_elem(p.y, i * p.y_rs + n, y, p.out_type);
-  }
-}
-
 // ---------------------------------------------------------------- choices sorted by expert
 
-constexpr int kGroup = 128;    // tokens that a launch takes
 constexpr int kTileK = 64;
 constexpr int kPlanThreads = 1024;
 
-// What plan_kernel leaves for the products: chunks of at most `cols` choices of one expert, each
-// choice's token and weight in the order of the chunks. A chunk's choices start on a multiple of
-// four, so that four of their tokens are one load.
-struct PlanOut {
-  int32_t *chunks;   // their number
-  int4 *chunk;       // {expert, first place, choices, 0}
-  int32_t *token;
-  float *weight;
-  uint32_t *counters;  // of cut tiles, all set to 0
-};
-
 struct PlanParams {
   DenseMat ids, weights;  // of this group's tokens
-  PlanOut out;
+  ExpertsPlan out;
+  uint32_t *counters;     // of cut tiles, all set to 0
   DenseMat x;             // rows to lay out; p NULL: none
   uint16_t *packed;
   int64_t k, packed_ld;
-  uint32_t counters;
+  uint32_t n_counters;
   int32_t tokens, top, experts, first, cols;
 };
 
 // CTA 0 plans; the others lay out x in rows of whole 16-byte runs where no tensor copy takes it as
 // it lies.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
-  __shared__ int16_t expert[kGroup * kMostChosen];
-  __shared__ uint32_t base[kMostExperts];  // chunks before it << 16 | places before it
-  __shared__ uint16_t count[kMostExperts];
+  __shared__ int16_t expert[kExpertsGroup * kChosenMost];
+  __shared__ uint32_t base[kExpertsMost];  // chunks before it << 16 | places before it
+  __shared__ uint16_t count[kExpertsMost];
   __shared__ uint32_t sums[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
   griddep_launch();
@@ -160,7 +72,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     const int64_t e = (int64_t)id - p.first;
     expert[s] = id >= 0 && e >= 0 && e < p.experts ? (int16_t)e : (int16_t)-1;
   }
-  for (uint32_t i = tid; i < p.counters; i += blockDim.x) p.out.counters[i] = 0u;
+  for (uint32_t i = tid; i < p.n_counters; i += blockDim.x) p.counters[i] = 0u;
   __syncthreads();
   for (int e = warp; e < p.experts; e += warps) {
     int c = 0;
@@ -225,7 +137,8 @@ constexpr uint32_t kTile = 128 * 128;  // bytes of 128 rows of one k block
 
 struct ProductParams {
   CUtensorMap w[2], b;  // weights {k, rows, experts}; tokens {k, rows}, by four rows or by 16
-  PlanOut plan;
+  ExpertsPlan plan;
+  uint32_t *counters;
   DenseMat res;         // sums only
   void *out;            // inner values [place][out_rs], or y
   int64_t out_rs;
@@ -338,7 +251,7 @@ __device__ __forceinline__ bool arrive_last(const ProductParams &p, Shared &sh, 
                                             uint32_t shares, int tid) {
   __threadfence();
   epilogue_sync();
-  if (tid == 0) sh.last = atomicAdd(&p.plan.counters[job], 1u) == shares - 1u;
+  if (tid == 0) sh.last = atomicAdd(&p.counters[job], 1u) == shares - 1u;
   epilogue_sync();
   const bool last = sh.last != 0u;
   if (last) __threadfence();
@@ -643,7 +556,7 @@ int check(const coll_experts_t &a) {
     if (v < 0 || v > most) return COLL_EINVAL;
   if (!is_half(a.dtype) || (a.out_dtype != a.dtype && a.out_dtype != COLL_F32)) return COLL_EINVAL;
   if (a.act < COLL_ACT_RELU || a.act > COLL_ACT_SIGMOID) return COLL_EINVAL;
-  if (a.experts < 1 || a.experts > kMostExperts || a.top < 1 || a.top > kMostChosen ||
+  if (a.experts < 1 || a.experts > kExpertsMost || a.top < 1 || a.top > kChosenMost ||
       a.first < 0 || a.first > most)
     return COLL_EINVAL;
   const int oe = esize(a.out_dtype);
@@ -710,22 +623,48 @@ int encode_rows(CUtensorMap *map, int64_t type, const void *base, int64_t rows, 
   return encode(map, type, 2, base, dims, strides, (uint32_t)box);
 }
 
+// The bytes that every row of a stack starts on and is a multiple of: 32, 16, 4 or 2.
+int alignment(const void *base, int64_t es, int64_t e, int64_t rs, int64_t rows, int64_t len) {
+  uint64_t v = (uintptr_t)base | (uint64_t)len * 2;
+  if (e > 1) v |= (uint64_t)es * 2;
+  if (rows > 1) v |= (uint64_t)rs * 2;
+  return v % 32 == 0 ? 32 : v % 16 == 0 ? 16 : v % 4 == 0 ? 4 : 2;
+}
+
+// Tokens up to which the kernels without staging are used whatever the weights' layout.
+constexpr int64_t kDirectTokens = 8;
+
 // The workspace of a group of tokens, and the shapes of its launches.
 struct Layout {
   int64_t tokens, places, chunks, ld, packed_ld;
   int32_t cols;
-  bool simple, pack;
+  bool nothing, direct, planned, pack;
   ProductParams inner, outer;
+  DirectParams few, few_sums;
+  int inner_align, outer_align;
   PlanParams plan;
   uint64_t bytes;
 };
 
 int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   memset(&l, 0, sizeof(l));
-  l.tokens = a.m < kGroup ? a.m : kGroup;
-  l.simple = a.k > 0 && a.f > 0 &&
-             !(copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f) &&
-               copied(a.w_down, a.experts, a.n));
+  l.tokens = a.m < kExpertsGroup ? a.m : kExpertsGroup;
+  l.nothing = a.k == 0 || a.f == 0;
+  const int64_t choices = l.tokens * a.top;
+  l.direct = !l.nothing &&
+             (l.tokens <= kDirectTokens ||
+              !(copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f) &&
+                copied(a.w_down, a.experts, a.n)));
+  l.cols = !l.direct ? (int32_t)round_up(l.tokens, 16)
+           : l.tokens <= 8 ? 8 : l.tokens <= 16 ? 16 : 32;
+  const bool rows = a.x.cs == 1 || a.k == 1;
+  const int x_align = alignment(a.x.ptr, 0, 1, a.x.rs, a.m, a.k);
+  l.planned = !l.direct || choices > kDirectUnplanned || l.tokens > 8 || !rows;
+  l.pack = !l.nothing && (l.direct ? l.planned && (!rows || x_align < 16) : !copied(a.x, a.m, a.k));
+  l.chunks = (a.experts < choices ? a.experts : choices) + choices / l.cols;
+  l.places = l.planned ? choices + 3 * l.chunks : 8 * l.chunks;
+  l.ld = round_up(a.f, 64);
+  l.packed_ld = round_up(a.k, 64);
   uint64_t used = 0;
   bool over = false;
   auto take = [&](uint64_t bytes) -> char * {
@@ -737,71 +676,102 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     used += (bytes + 255) & ~(uint64_t)255;
     return base ? base + at : nullptr;
   };
-  if (l.simple) {
-    const uint64_t slots = (uint64_t)(a.m * a.top);
-    if (slots > kAddressable / 2 / (uint64_t)a.f) return COLL_EINVAL;
-    take(slots * a.f * 2);
-    l.bytes = used;
-    return COLL_OK;
-  }
-  l.cols = (int32_t)round_up(l.tokens, 16);
-  const int64_t choices = l.tokens * a.top;
-  l.chunks = (a.experts < choices ? a.experts : choices) + choices / l.cols;
-  l.places = choices + 3 * l.chunks;
-  l.ld = round_up(a.f, 64);
-  l.pack = !copied(a.x, a.m, a.k) && a.k > 0;
   ProductParams &p = l.inner, &q = l.outer;
-  p.tiles = (int32_t)ceil_div(a.f, 128);
-  q.tiles = (int32_t)ceil_div(a.n, 128);
-  p.rows = (int32_t)round_up(ceil_div(a.f, p.tiles ? p.tiles : 1), 8);
-  q.rows = (int32_t)round_up(ceil_div(a.n, q.tiles), 8);
-  p.features = (int32_t)a.f;
-  q.features = (int32_t)a.n;
-  p.kblocks = (int32_t)ceil_div(a.k, kTileK);
-  q.kblocks = (int32_t)ceil_div(a.f, kTileK);
-  // the line of k blocks is counted in 32 bits
-  if ((uint64_t)l.chunks * p.tiles * p.kblocks >> 32 || (uint64_t)l.chunks * q.tiles * q.kblocks >> 32)
-    return COLL_EINVAL;
-  q.nothing = a.k == 0 || a.f == 0;
-  p.cols = q.cols = l.cols;
-  p.type = q.type = (int32_t)a.dtype;
-  p.out_type = (int32_t)a.dtype;
-  q.out_type = (int32_t)a.out_dtype;
-  p.act = (int32_t)a.act;
-  p.status = q.status = a.status;
-  auto ring = [&](ProductParams &r, int w, uint32_t fixed) {
-    r.stage_bytes = w * kTile + (uint32_t)l.cols * 128u;
-    r.stages = (int32_t)((kTcSmem - 1024 - fixed) / r.stage_bytes);
-    if (r.stages > kMaxStages) r.stages = kMaxStages;
-    r.ring = r.stages * r.stage_bytes;
-  };
-  ring(p, 2, 0);
-  ring(q, 1, (uint32_t)l.tokens * 512u);
+  DirectParams &d = l.few, &e = l.few_sums;
   PlanParams &s = l.plan;
+  ExpertsPlan o = {};
+  uint64_t part = 0, jobs = 0, sums = 0;
+  if (!l.direct) {
+    p.tiles = (int32_t)ceil_div(a.f, 128);
+    q.tiles = (int32_t)ceil_div(a.n, 128);
+    p.rows = (int32_t)round_up(ceil_div(a.f, p.tiles ? p.tiles : 1), 8);
+    q.rows = (int32_t)round_up(ceil_div(a.n, q.tiles), 8);
+    p.features = (int32_t)a.f;
+    q.features = (int32_t)a.n;
+    p.kblocks = (int32_t)ceil_div(a.k, kTileK);
+    q.kblocks = (int32_t)ceil_div(a.f, kTileK);
+    // the line of k blocks is counted in 32 bits
+    if ((uint64_t)l.chunks * p.tiles * p.kblocks >> 32 ||
+        (uint64_t)l.chunks * q.tiles * q.kblocks >> 32)
+      return COLL_EINVAL;
+    q.nothing = l.nothing;
+    p.cols = q.cols = l.cols;
+    p.type = q.type = (int32_t)a.dtype;
+    p.out_type = (int32_t)a.dtype;
+    q.out_type = (int32_t)a.out_dtype;
+    p.act = (int32_t)a.act;
+    p.status = q.status = a.status;
+    auto ring = [&](ProductParams &r, int w, uint32_t fixed) {
+      r.stage_bytes = w * kTile + (uint32_t)l.cols * 128u;
+      r.stages = (int32_t)((kTcSmem - 1024 - fixed) / r.stage_bytes);
+      if (r.stages > kMaxStages) r.stages = kMaxStages;
+      r.ring = r.stages * r.stage_bytes;
+    };
+    ring(p, 2, 0);
+    ring(q, 1, (uint32_t)l.tokens * 512u);
+    jobs = (uint64_t)l.chunks * p.tiles;
+    sums = q.tiles;
+    const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
+    part = 2 * kSms * (inner > outer ? inner : outer);
+  } else {
+    l.inner_align = alignment(a.w_gate.ptr, a.w_gate.es, a.experts, a.w_gate.rs, a.f, a.k);
+    const int up = alignment(a.w_up.ptr, a.w_up.es, a.experts, a.w_up.rs, a.f, a.k);
+    if (up < l.inner_align) l.inner_align = up;
+    l.outer_align = alignment(a.w_down.ptr, a.w_down.es, a.experts, a.w_down.rs, a.n, a.f);
+    d.w[0] = static_cast<const uint16_t *>(a.w_gate.ptr), d.es[0] = a.w_gate.es;
+    d.w[1] = static_cast<const uint16_t *>(a.w_up.ptr), d.es[1] = a.w_up.es;
+    e.w[0] = static_cast<const uint16_t *>(a.w_down.ptr), e.es[0] = a.w_down.es;
+    d.rs[0] = a.w_gate.rs, d.rs[1] = a.w_up.rs, e.rs[0] = a.w_down.rs;
+    d.len = (int32_t)a.k, e.len = (int32_t)a.f;
+    d.features = (int32_t)a.f, e.features = (int32_t)a.n;
+    d.x_align = l.pack ? 32 : x_align;
+    e.x_align = 32;
+    for (DirectParams *r : {&d, &e}) {
+      r->first = (int32_t)a.first, r->experts = (int32_t)a.experts, r->top = (int32_t)a.top;
+      r->type = (int32_t)a.dtype, r->out_type = (int32_t)a.out_dtype, r->act = (int32_t)a.act;
+      r->most_chunks = (uint32_t)l.chunks;
+      const int64_t steps = ceil_div(r->len, 64) * (r == &e ? l.chunks : 1);
+      r->warps = steps < 8 ? (uint32_t)steps : 8;
+      r->tiles = (int32_t)ceil_div(a.n, kDirectOuter);
+      r->splits = 1;
+    }
+    // two CTAs for every SM, but two turns or more for each warp
+    int64_t splits = ceil_div(2 * kSms, e.tiles);
+    const int64_t most = l.chunks * ceil_div(a.f, 64) / (2 * e.warps);
+    if (splits > most) splits = most;
+    if (splits > 32) splits = 32;
+    if (splits > 1) {
+      d.splits = e.splits = (int32_t)splits;
+      sums = (uint64_t)e.tiles;
+      part = (uint64_t)splits * e.tiles * l.tokens * 64;
+    }
+  }
+  if (l.planned) {
+    o.chunks = reinterpret_cast<int32_t *>(take(4));
+    o.chunk = reinterpret_cast<int4 *>(take((uint64_t)l.chunks * 16));
+    o.token = reinterpret_cast<int32_t *>(take((uint64_t)l.places * 4));
+    o.weight = reinterpret_cast<float *>(take((uint64_t)l.places * 4));
+  }
+  uint32_t *counters = reinterpret_cast<uint32_t *>(take((jobs + sums) * 4));
+  char *h = take((uint64_t)l.places * l.ld * 2);
+  p.part = q.part = e.part = reinterpret_cast<float *>(take(part));
+  if (l.pack)
+    s.packed = reinterpret_cast<uint16_t *>(take((uint64_t)l.tokens * l.packed_ld * 2));
+  s.packed_ld = l.packed_ld;
   s.top = (int32_t)a.top;
   s.experts = (int32_t)a.experts;
   s.first = (int32_t)a.first;
   s.cols = l.cols;
   s.k = a.k;
-  const int64_t jobs = l.chunks * p.tiles;
-  s.counters = (uint32_t)(jobs + q.tiles);
-  PlanOut &o = s.out;
-  o.chunks = reinterpret_cast<int32_t *>(take(4));
-  o.chunk = reinterpret_cast<int4 *>(take((uint64_t)l.chunks * 16));
-  o.token = reinterpret_cast<int32_t *>(take((uint64_t)l.places * 4));
-  o.weight = reinterpret_cast<float *>(take((uint64_t)l.places * 4));
-  o.counters = reinterpret_cast<uint32_t *>(take((uint64_t)s.counters * 4));
-  p.plan = q.plan = o;
-  if (base) q.plan.counters = o.counters + jobs;
-  p.out = take((uint64_t)l.places * l.ld * 2);
+  s.out = p.plan = q.plan = d.plan = e.plan = o;
+  s.counters = p.counters = d.counters = e.counters = counters;
+  s.n_counters = (uint32_t)(jobs + sums);
+  if (base) q.counters = counters + jobs;
+  p.out = h;
   p.out_rs = l.ld;
-  const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
-  p.part = q.part = reinterpret_cast<float *>(take(2 * kSms * (inner > outer ? inner : outer)));
-  if (l.pack) {
-    l.packed_ld = round_up(a.k, 64);
-    s.packed = reinterpret_cast<uint16_t *>(take((uint64_t)l.tokens * l.packed_ld * 2));
-    s.packed_ld = l.packed_ld;
-  }
+  d.h = reinterpret_cast<uint16_t *>(h);
+  d.h_ld = e.x_ld = l.ld;
+  e.x = d.h;
   l.bytes = used;
   return over ? COLL_EINVAL : COLL_OK;
 }
@@ -824,54 +794,30 @@ cudaError_t launch(const ProductParams &p, cudaStream_t s) {
   return dense_launch(product_kernel<INNER>, dim3(kSms), kThreads, kTcSmem, 1, s, p);
 }
 
-int run_simple(const coll_experts_t &a, uint16_t *h, cudaStream_t s) {
-  ExpertsParams p = {};
-  p.gate = static_cast<const uint16_t *>(a.w_gate.ptr);
-  p.up = static_cast<const uint16_t *>(a.w_up.ptr);
-  p.down = static_cast<const uint16_t *>(a.w_down.ptr);
-  p.gate_es = a.w_gate.es, p.gate_rs = a.w_gate.rs;
-  p.up_es = a.w_up.es, p.up_rs = a.w_up.rs;
-  p.down_es = a.w_down.es, p.down_rs = a.w_down.rs;
-  p.x = DenseMat{a.x.ptr, a.x.rs, a.x.cs};
-  p.ids = DenseMat{a.ids.ptr, a.ids.rs, a.ids.cs};
-  p.weights = DenseMat{a.weights.ptr, a.weights.rs, a.weights.cs};
-  p.res = DenseMat{a.residual.ptr, a.residual.rs, a.residual.cs};
-  p.y = a.y.ptr;
-  p.y_rs = a.y.rs;
-  p.h = h;
-  p.m = a.m, p.n = a.n, p.k = a.k, p.f = a.f;
-  p.experts = (int32_t)a.experts;
-  p.first = (int32_t)a.first;
-  p.top = (int32_t)a.top;
-  p.type = (int32_t)a.dtype;
-  p.out_type = (int32_t)a.out_dtype;
-  p.act = (int32_t)a.act;
-  const dim3 grid(kSms * 8);
-  cudaError_t e = dense_launch(inner_kernel, grid, kWarps * 32, 0, 1, s, p);
-  if (e == cudaSuccess) e = dense_launch(outer_kernel, grid, kWarps * 32, 0, 1, s, p);
-  return e == cudaSuccess ? COLL_OK : COLL_ECUDA;
-}
-
 int run(const coll_experts_t &a, char *base, cudaStream_t s) {
   Layout l;
   int c = lay_out(a, l, base);
   if (c) return c;
-  if (l.simple) return run_simple(a, reinterpret_cast<uint16_t *>(base), s);
   ProductParams &p = l.inner, &q = l.outer;
-  c = set_up<true>();
-  if (!c) c = set_up<false>();
-  if (!c && !q.nothing) {
-    c = encode_stack(&p.w[0], a.dtype, a.w_gate, a.experts, a.f, a.k, p.rows);
-    if (!c) c = encode_stack(&p.w[1], a.dtype, a.w_up, a.experts, a.f, a.k, p.rows);
-    if (!c) c = encode_stack(&q.w[0], a.dtype, a.w_down, a.experts, a.n, a.f, q.rows);
-    if (!c) c = encode_rows(&q.b, a.dtype, p.out, l.places, a.f, l.ld, 16);
-    // the first group's rows as a trial of them all
-    if (!c)
-      c = l.pack ? encode_rows(&p.b, a.dtype, l.plan.packed, l.tokens, a.k, l.packed_ld, 1)
-                 : encode_rows(&p.b, a.dtype, a.x.ptr, l.tokens, a.k,
-                               a.m == 1 ? round_up(a.k, 8) : a.x.rs, 1);
+  DirectParams &d = l.few, &e = l.few_sums;
+  if (l.direct) {
+    if (experts_direct_set_up(l.cols, l.outer_align, a.dtype) != cudaSuccess) return COLL_ECUDA;
+  } else {
+    c = set_up<true>();
+    if (!c) c = set_up<false>();
+    if (!c && !l.nothing) {
+      c = encode_stack(&p.w[0], a.dtype, a.w_gate, a.experts, a.f, a.k, p.rows);
+      if (!c) c = encode_stack(&p.w[1], a.dtype, a.w_up, a.experts, a.f, a.k, p.rows);
+      if (!c) c = encode_stack(&q.w[0], a.dtype, a.w_down, a.experts, a.n, a.f, q.rows);
+      if (!c) c = encode_rows(&q.b, a.dtype, p.out, l.places, a.f, l.ld, 16);
+      // the first group's rows as a trial of them all
+      if (!c)
+        c = l.pack ? encode_rows(&p.b, a.dtype, l.plan.packed, l.tokens, a.k, l.packed_ld, 1)
+                   : encode_rows(&p.b, a.dtype, a.x.ptr, l.tokens, a.k,
+                                 a.m == 1 ? round_up(a.k, 8) : a.x.rs, 1);
+    }
+    if (c) return c;
   }
-  if (c) return c;
   const int oe = esize(a.out_dtype);
   for (int64_t t = 0; t < a.m; t += l.tokens) {
     const int64_t tokens = a.m - t < l.tokens ? a.m - t : l.tokens;
@@ -879,22 +825,40 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
     o.ids = DenseMat{static_cast<const int32_t *>(a.ids.ptr) + t * a.ids.rs, a.ids.rs, a.ids.cs};
     o.weights = DenseMat{static_cast<const float *>(a.weights.ptr) + t * a.weights.rs,
                          a.weights.rs, a.weights.cs};
-    o.tokens = p.tokens = q.tokens = (int32_t)tokens;
+    o.tokens = p.tokens = q.tokens = d.tokens = e.tokens = (int32_t)tokens;
     const uint16_t *x = static_cast<const uint16_t *>(a.x.ptr) + t * a.x.rs;
     if (l.pack) o.x = DenseMat{x, a.x.rs, a.x.cs};
-    else if (t && !q.nothing)
+    else if (!l.direct && t && !l.nothing)
       c = encode_rows(&p.b, a.dtype, x, tokens, a.k, a.x.rs, 1);
     if (c) return c;
-    q.out = static_cast<char *>(a.y.ptr) + t * a.y.rs * oe;
-    q.out_rs = a.y.rs;
+    void *y = static_cast<char *>(a.y.ptr) + t * a.y.rs * oe;
+    DenseMat res = {};
     if (a.residual.ptr)
-      q.res = DenseMat{static_cast<const char *>(a.residual.ptr) + t * a.residual.rs * oe,
-                       a.residual.rs, a.residual.cs};
-    const unsigned more = l.pack ? (unsigned)ceil_div(tokens * l.packed_ld / 8, kPlanThreads) : 0;
-    cudaError_t e = dense_launch(plan_kernel, dim3(1 + more), kPlanThreads, 0, 1, s, o);
-    if (e == cudaSuccess && !q.nothing) e = launch<true>(p, s);
-    if (e == cudaSuccess) e = launch<false>(q, s);
-    if (e != cudaSuccess) return COLL_ECUDA;
+      res = DenseMat{static_cast<const char *>(a.residual.ptr) + t * a.residual.rs * oe,
+                     a.residual.rs, a.residual.cs};
+    cudaError_t err = cudaSuccess;
+    if (l.planned) {
+      const unsigned more = l.pack ? (unsigned)ceil_div(tokens * l.packed_ld / 8, kPlanThreads) : 0;
+      err = dense_launch(plan_kernel, dim3(1 + more), kPlanThreads, 0, 1, s, o);
+    }
+    if (l.direct) {
+      d.ids = e.ids = o.ids;
+      d.weights = e.weights = o.weights;
+      d.x = l.pack ? o.packed : x;
+      d.x_ld = l.pack ? l.packed_ld : a.x.rs;
+      e.y = y;
+      e.y_rs = a.y.rs;
+      e.res = res;
+      if (err == cudaSuccess) err = experts_direct_inner(d, l.cols, l.inner_align, s);
+      if (err == cudaSuccess) err = experts_direct_outer(e, l.cols, l.outer_align, s);
+    } else {
+      q.out = y;
+      q.out_rs = a.y.rs;
+      q.res = res;
+      if (err == cudaSuccess && !l.nothing) err = launch<true>(p, s);
+      if (err == cudaSuccess) err = launch<false>(q, s);
+    }
+    if (err != cudaSuccess) return COLL_ECUDA;
   }
   return COLL_OK;
 }

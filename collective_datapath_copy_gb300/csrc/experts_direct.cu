@@ -1,0 +1,417 @@
+// A few tokens through their chosen experts without staging: every warp loads weights straight into
+// the fragments of mma.m16n8k16, as dense_gemv.cu does for one matrix. A chunk of choices of one
+// expert is the columns of a fragment, 16 rows of weights its rows (inner: eight of gate and eight of
+// up, so a lane ends up with g and u of the same feature).
+//
+// Bound by HBM and, for a token or two, by latency: one launch for the inner values and one for the
+// sums. Up to 32 choices the chunks are made by a warp of every CTA, from the ids alone (a launch
+// that sorts them first would cost as much as either kernel); beyond that plan_kernel makes them.
+#include "dense_direct.cuh"
+#include "dense_epi.cuh"
+#include "dense_tc.h"
+#include "experts.h"
+#include "tma.cuh"
+
+namespace coll {
+namespace {
+
+constexpr int kStep = 64;  // elements of a row that a warp takes at a time
+constexpr int kWarps = 8;
+
+template <int NT, int ALIGN>
+constexpr int kAhead = NT == 1 && ALIGN > 2 ? 4 : NT <= 2 ? 2 : 1;
+
+// Chunks of eight made here, for plans of few choices.
+struct Few {
+  int32_t token[8 * kDirectUnplanned];
+  float weight[8 * kDirectUnplanned];
+};
+
+// One warp: the chunks of at most 32 choices, by first choice; their places are eight apart.
+__device__ __forceinline__ int make_chunks(const DirectParams &p, int4 *chunk, Few &few) {
+  const int s = threadIdx.x & 31, n = p.tokens * p.top;
+  int e = -1;
+  float w = 0.0f;
+  if (s < n) {
+    const int i = s / p.top, j = s - i * p.top;
+    const int id = static_cast<const int32_t *>(p.ids.p)[i * p.ids.rs + j * p.ids.cs];
+    w = static_cast<const float *>(p.weights.p)[i * p.weights.rs + j * p.weights.cs];
+    const int64_t d = (int64_t)id - p.first;
+    if (id >= 0 && d >= 0 && d < p.experts) e = (int)d;
+  }
+  const uint32_t same = __match_any_sync(~0u, e);
+  const int lead = __ffs(same) - 1, count = __popc(same);
+  const int mine = e >= 0 && lead == s ? (count + 7) / 8 : 0;
+  int run = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(~0u, run, o);
+    if (s >= o) run += v;
+  }
+  const int first = __shfl_sync(~0u, run - mine, lead), all = __shfl_sync(~0u, run, 31);
+  if (e >= 0) {
+    const int place = 8 * first + __popc(same & ((1u << s) - 1u));
+    few.token[place] = s / p.top;
+    few.weight[place] = w;
+  }
+  for (int q = 0; q < mine; ++q)
+    chunk[first + q] = make_int4(e, 8 * (first + q), min(8, count - 8 * q), 0);
+  return all;
+}
+
+// Row pointers and lengths of the tokens of a fragment's columns.
+template <int NT>
+struct Columns {
+  const uint16_t *x[NT];
+  int len[NT];
+};
+
+template <int NT, int ALIGN>
+__device__ __forceinline__ void load_x(const DirectParams &p, const Columns<NT> &c, int k, int at,
+                                       uint32_t (&x)[NT][8]) {
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    if (p.x_align >= 32) load16<32>(c.x[i] + k, at, c.len[i], x[i]);
+    else if (p.x_align >= 16) load16<16>(c.x[i] + k, at, c.len[i], x[i]);
+    else load16<2>(c.x[i] + k, at, c.len[i], x[i]);
+  }
+}
+
+// 16 elements of one row of each matrix, AHEAD of them asked for before the first is used.
+template <int ALIGN, int AHEAD>
+struct Rows {
+  uint32_t a[AHEAD][8], b[AHEAD][8];
+};
+
+template <int ALIGN, int AHEAD>
+__device__ __forceinline__ void load_rows(const uint16_t *const (&pa)[AHEAD],
+                                          const uint16_t *const (&pb)[AHEAD],
+                                          const int (&at)[AHEAD], const int (&la)[AHEAD],
+                                          const int (&lb)[AHEAD], Rows<ALIGN, AHEAD> &r) {
+  if constexpr (ALIGN == 2) {
+    Around ra[AHEAD], rb[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      ask16(pa[i], at[i], la[i], ra[i]);
+      ask16(pb[i], at[i], lb[i], rb[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      take16(pa[i], at[i], la[i], ra[i], r.a[i]);
+      take16(pb[i], at[i], lb[i], rb[i], r.b[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      load16<ALIGN>(pa[i], at[i], la[i], r.a[i]);
+      load16<ALIGN>(pb[i], at[i], lb[i], r.b[i]);
+    }
+  }
+}
+
+// Eight inner features of one chunk's choices: gate's rows are the fragment's first eight, up's the
+// others. The warps take the steps of k in turn and join in order.
+template <int TYPE, int NT, int ALIGN>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    direct_inner_kernel(const __grid_constant__ DirectParams p) {
+  constexpr int AHEAD = kAhead<NT, ALIGN>;
+  __shared__ float part[kWarps][8 * NT][16];
+  __shared__ int4 few_chunk[kDirectUnplanned];
+  __shared__ Few few;
+  __shared__ int chunks;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  griddep_launch();
+  griddep_wait();
+  int4 c;
+  const int32_t *token;
+  if (p.plan.chunks) {
+    if ((int)blockIdx.y >= *p.plan.chunks) return;
+    c = p.plan.chunk[blockIdx.y];
+    token = p.plan.token + c.y;
+  } else {
+    if (warp == 0) {
+      const int n = make_chunks(p, few_chunk, few);
+      if (lane == 0) chunks = n;
+    }
+    if (blockIdx.x == 0 && blockIdx.y == 0 && p.splits > 1)
+      for (int i = threadIdx.x; i < p.tiles; i += blockDim.x) p.counters[i] = 0u;
+    __syncthreads();
+    if ((int)blockIdx.y >= chunks) return;
+    c = few_chunk[blockIdx.y];
+    token = few.token + c.y;
+  }
+  const int f0 = (int)blockIdx.x * kDirectInner, f = f0 + g;
+  const int len = f < p.features ? p.len : 0;  // rows that are not there are empty
+  const int64_t row = len ? f : 0;
+  const uint16_t *wa = p.w[0] + c.x * p.es[0] + row * p.rs[0] + 16 * t;
+  const uint16_t *wb = p.w[1] + c.x * p.es[1] + row * p.rs[1] + 16 * t;
+  Columns<NT> col;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    const bool there = i * 8 + g < c.z;
+    col.len[i] = there ? p.len : 0;
+    col.x[i] = p.x + (there ? token[i * 8 + g] : 0) * p.x_ld + 16 * t;
+  }
+  float acc[NT][4] = {};
+  const int steps = (p.len + kStep - 1) / kStep;
+  for (int s = warp; s < steps; s += AHEAD * warps) {
+    const uint16_t *pa[AHEAD], *pb[AHEAD];
+    int at[AHEAD], la[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int k = (s + i * warps) * kStep;
+      pa[i] = wa + k, pb[i] = wb + k, at[i] = k + 16 * t, la[i] = len;
+    }
+    Rows<ALIGN, AHEAD> r;
+    load_rows<ALIGN, AHEAD>(pa, pb, at, la, la, r);
+    uint32_t x[AHEAD][NT][8];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      load_x<NT, ALIGN>(p, col, (s + i * warps) * kStep, at[i], x[i]);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          mma16816<TYPE>(acc[n], r.a[i][2 * q], r.b[i][2 * q], r.a[i][2 * q + 1],
+                         r.b[i][2 * q + 1], x[i][n][2 * q], x[i][n][2 * q + 1]);
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    part[warp][n * 8 + 2 * t][g] = acc[n][0];
+    part[warp][n * 8 + 2 * t + 1][g] = acc[n][1];
+    part[warp][n * 8 + 2 * t][g + 8] = acc[n][2];
+    part[warp][n * 8 + 2 * t + 1][g + 8] = acc[n][3];
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < 8 * c.z; i += blockDim.x) {
+    const int n = i / 8, j = i % 8;
+    if (f0 + j >= p.features) continue;
+    float v = 0.0f, u = 0.0f;
+    for (int w = 0; w < warps; ++w) {
+      v += part[w][n][j];
+      u += part[w][n][j + 8];
+    }
+    p.h[(int64_t)(c.y + n) * p.h_ld + f0 + j] = f2h(act_value(v, p.act) * u, TYPE);
+  }
+  // the sums read rows in whole runs of 16
+  if (blockIdx.x == gridDim.x - 1)
+    for (int i = threadIdx.x; i < 16 * c.z; i += blockDim.x) {
+      const int j = p.features + i % 16;
+      if (j < ((p.features + 15) & ~15)) p.h[(int64_t)(c.y + i / 16) * p.h_ld + j] = 0;
+    }
+}
+
+// 16 outputs of all tokens. The steps of all chunks are one list, the splits' shares of it
+// neighbouring, and inside a share the warps take steps in turn; each adds its finished products,
+// times their weights, to its own sums in shared memory. The warps join in order, and so do the
+// splits, in the last of their CTAs to arrive.
+template <int TYPE, int NT, int ALIGN>
+__global__ void __launch_bounds__(kWarps * 32, 1)
+    direct_outer_kernel(const __grid_constant__ DirectParams p) {
+  constexpr int AHEAD = kAhead<NT, ALIGN>;
+  extern __shared__ float sums[];  // [warps][tokens][16], then the plan's chunks
+  __shared__ int4 few_chunk[kDirectUnplanned];
+  __shared__ Few few;
+  __shared__ int chunks;
+  __shared__ uint32_t last;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int g = lane >> 2, t = lane & 3, size = p.tokens * 16;
+  griddep_launch();
+  for (int i = threadIdx.x; i < warps * size; i += blockDim.x) sums[i] = 0.0f;
+  griddep_wait();
+  const int4 *chunk = few_chunk;
+  const int32_t *token = few.token;
+  const float *weight = few.weight;
+  int n_chunks;
+  if (p.plan.chunks) {
+    int4 *copy = reinterpret_cast<int4 *>(sums + warps * size);
+    n_chunks = *p.plan.chunks;
+    for (int i = threadIdx.x; i < n_chunks; i += blockDim.x) copy[i] = p.plan.chunk[i];
+    chunk = copy;
+    token = p.plan.token;
+    weight = p.plan.weight;
+    __syncthreads();
+  } else {
+    if (warp == 0) {
+      const int n = make_chunks(p, few_chunk, few);
+      if (lane == 0) chunks = n;
+    }
+    __syncthreads();
+    n_chunks = chunks;
+  }
+  const int n0 = (int)blockIdx.x * kDirectOuter;
+  const int la = n0 + g < p.features ? p.len : 0, lb = n0 + g + 8 < p.features ? p.len : 0;
+  const uint16_t *wa = p.w[0] + (int64_t)(la ? n0 + g : 0) * p.rs[0] + 16 * t;
+  const uint16_t *wb = p.w[0] + (int64_t)(lb ? n0 + g + 8 : 0) * p.rs[0] + 16 * t;
+  const uint16_t *h = p.x + 16 * t;
+  float *mine = sums + warp * size;
+  const int steps = (p.len + kStep - 1) / kStep;
+  const int64_t all = (int64_t)n_chunks * steps;
+  const int64_t lo = all * blockIdx.y / p.splits, hi = all * (blockIdx.y + 1) / p.splits;
+  float acc[NT][4] = {};
+  int now = -1;
+  // what the accumulators hold of chunk `now` goes to its tokens; of two columns of one token, one
+  // after the other
+  auto flush = [&]() {
+    const int4 c = chunk[now];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      int tok[2];
+      float w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int at = n * 8 + 2 * t + j;
+        tok[j] = at < c.z ? token[c.y + at] : -1;
+        w[j] = at < c.z ? weight[c.y + at] : 0.0f;
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (t == q) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (tok[j] >= 0) {
+              float *y = mine + tok[j] * 16 + g;
+              y[0] = fmaf(w[j], acc[n][j], y[0]);
+              y[8] = fmaf(w[j], acc[n][j + 2], y[8]);
+            }
+        }
+        __syncwarp();
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+    }
+  };
+  int64_t s = lo + warp;
+  int at_chunk = (int)(s / steps), at_step = (int)(s - (int64_t)at_chunk * steps);
+  while (s < hi) {
+    const uint16_t *pa[AHEAD], *pb[AHEAD];
+    int at[AHEAD], ka[AHEAD], kb[AHEAD], which[AHEAD], from[AHEAD];
+    Columns<NT> col[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const bool there = s < hi;
+      which[i] = there ? at_chunk : -1;
+      const int4 c = there ? chunk[at_chunk] : make_int4(0, 0, 0, 0);
+      const int k = at_step * kStep;
+      from[i] = k;
+      pa[i] = wa + c.x * p.es[0] + k;
+      pb[i] = wb + c.x * p.es[0] + k;
+      at[i] = k + 16 * t;
+      ka[i] = there ? la : 0;
+      kb[i] = there ? lb : 0;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const bool row = n * 8 + g < c.z;
+        col[i].len[n] = row ? p.len : 0;
+        col[i].x[n] = h + (int64_t)(row ? c.y + n * 8 + g : 0) * p.x_ld;
+      }
+      s += warps;
+      at_step += warps;
+      while (at_step >= steps) {
+        at_step -= steps;
+        ++at_chunk;
+      }
+    }
+    Rows<ALIGN, AHEAD> r;
+    load_rows<ALIGN, AHEAD>(pa, pb, at, ka, kb, r);
+    uint32_t x[AHEAD][NT][8];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) load_x<NT, ALIGN>(p, col[i], from[i], at[i], x[i]);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (which[i] < 0) break;
+      if (which[i] != now) {
+        if (now >= 0) flush();
+        now = which[i];
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          mma16816<TYPE>(acc[n], r.a[i][2 * q], r.b[i][2 * q], r.a[i][2 * q + 1],
+                         r.b[i][2 * q + 1], x[i][n][2 * q], x[i][n][2 * q + 1]);
+    }
+  }
+  if (now >= 0) flush();
+  __syncthreads();
+  auto finish = [&](int i, float v) {
+    const int tok = i / 16, f = n0 + i % 16;
+    if (f >= p.features) return;
+    if (p.res.p) v += ld_elem(p.res.p, tok * p.res.rs + f * p.res.cs, p.out_type);
+    st_elem(p.y, tok * p.y_rs + f, v, p.out_type);
+  };
+  const int64_t share = (int64_t)gridDim.x * size;
+  float *part = p.part + (int64_t)blockIdx.x * size;
+  for (int i = threadIdx.x; i < size; i += blockDim.x) {
+    float v = 0.0f;
+    for (int w = 0; w < warps; ++w) v += sums[w * size + i];
+    if (p.splits == 1) finish(i, v);
+    else __stcg(part + blockIdx.y * share + i, v);
+  }
+  if (p.splits == 1) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0)
+    last = atomicAdd(&p.counters[blockIdx.x], 1u) == (uint32_t)p.splits - 1u;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  for (int i = threadIdx.x; i < size; i += blockDim.x) {
+    float v = 0.0f;
+#pragma unroll 8
+    for (int w = 0; w < p.splits; ++w) v += __ldcg(part + w * share + i);
+    finish(i, v);
+  }
+}
+
+uint32_t outer_smem(const DirectParams &p) {
+  return p.warps * (uint32_t)p.tokens * 64u + (p.plan.chunks ? p.most_chunks * 16u : 0u);
+}
+
+// The kernels of a type, a chunk's columns and an alignment.
+using Kernel = void (*)(const DirectParams);
+template <int TYPE, int NT>
+Kernel pick(bool inner, int align) {
+#define COLL_DIRECT(A) \
+  return inner ? (Kernel)direct_inner_kernel<TYPE, NT, A> : (Kernel)direct_outer_kernel<TYPE, NT, A>
+  if (align >= 32) COLL_DIRECT(32);
+  if (align >= 16) COLL_DIRECT(16);
+  if (align >= 4) COLL_DIRECT(4);
+  COLL_DIRECT(2);
+#undef COLL_DIRECT
+}
+template <int TYPE>
+Kernel pick(bool inner, int columns, int align) {
+  return columns == 8 ? pick<TYPE, 1>(inner, align)
+         : columns == 16 ? pick<TYPE, 2>(inner, align)
+                         : pick<TYPE, 4>(inner, align);
+}
+Kernel pick(int64_t type, bool inner, int columns, int align) {
+  return type == COLL_BF16 ? pick<COLL_BF16>(inner, columns, align)
+                           : pick<COLL_F16>(inner, columns, align);
+}
+
+}  // namespace
+
+cudaError_t experts_direct_set_up(int columns, int align, int64_t type) {
+  static DenseSmemLimit limit[2][3][4];
+  const int c = columns == 8 ? 0 : columns == 16 ? 1 : 2;
+  const int a = align >= 32 ? 0 : align >= 16 ? 1 : align >= 4 ? 2 : 3;
+  return limit[type == COLL_BF16][c][a]((const void *)pick(type, false, columns, align),
+                                        200 * 1024);
+}
+
+cudaError_t experts_direct_inner(const DirectParams &p, int columns, int align, cudaStream_t s) {
+  const dim3 grid((unsigned)((p.features + kDirectInner - 1) / kDirectInner), p.most_chunks);
+  return dense_launch(pick(p.type, true, columns, align), grid, 32 * p.warps, 0, 1, s, p);
+}
+
+cudaError_t experts_direct_outer(const DirectParams &p, int columns, int align, cudaStream_t s) {
+  return dense_launch(pick(p.type, false, columns, align), dim3(p.tiles, p.splits), 32 * p.warps,
+                      outer_smem(p), 1, s, p);
+}
+
+}  // namespace coll
