@@ -42,15 +42,14 @@ struct PlanParams {
 };
 
 // CTA 0 plans; the others lay out x in rows of whole 16-byte runs where no tensor copy takes it as
-// it lies.
+// it lies. The choices go through the CTA 32 at a time, a warp after the other, each adding to its
+// experts' counts: so they stay in order, and the plan does not depend on timing.
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
-  __shared__ int16_t expert[kExpertsGroup * kChosenMost];
-  __shared__ uint32_t base[kExpertsMost];  // chunks before it << 16 | places before it
-  __shared__ uint16_t count[kExpertsMost];
+  __shared__ uint32_t base[kExpertsMost];  // count; then chunks before it << 16 | places before it
   __shared__ uint32_t sums[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  griddep_launch();
   griddep_wait();
+  griddep_launch();
   if (blockIdx.x > 0) {
     const int64_t runs = p.packed_ld / 8, all = runs * p.tokens;
     for (int64_t r = (int64_t)(blockIdx.x - 1) * blockDim.x + tid; r < all;
@@ -66,67 +65,82 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     return;
   }
   const int n = p.tokens * p.top;
-  for (int s = tid; s < n; s += blockDim.x) {
-    const int i = s / p.top, j = s - i * p.top;
-    const int id = static_cast<const int32_t *>(p.ids.p)[i * p.ids.rs + j * p.ids.cs];
-    const int64_t e = (int64_t)id - p.first;
-    expert[s] = id >= 0 && e >= 0 && e < p.experts ? (int16_t)e : (int16_t)-1;
+  constexpr int kTurns = kExpertsGroup * kChosenMost / kPlanThreads;
+  int expert[kTurns], token[kTurns], place[kTurns];
+  float weight[kTurns];
+#pragma unroll
+  for (int r = 0; r < kTurns; ++r) {
+    const int s = r * (int)blockDim.x + tid;
+    expert[r] = -1;
+    if (s < n) {
+      const int i = s / p.top, j = s - i * p.top;
+      const int id = static_cast<const int32_t *>(p.ids.p)[i * p.ids.rs + j * p.ids.cs];
+      weight[r] = static_cast<const float *>(p.weights.p)[i * p.weights.rs + j * p.weights.cs];
+      const int64_t e = (int64_t)id - p.first;
+      token[r] = i;
+      if (id >= 0 && e >= 0 && e < p.experts) expert[r] = (int)e;
+    }
   }
+  for (int i = tid; i < p.experts; i += blockDim.x) base[i] = 0u;
   for (uint32_t i = tid; i < p.n_counters; i += blockDim.x) p.counters[i] = 0u;
   __syncthreads();
-  for (int e = warp; e < p.experts; e += warps) {
-    int c = 0;
-    for (int s = lane; s - lane < n; s += 32)
-      c += __popc(__ballot_sync(~0u, s < n && expert[s] == e));
-    if (lane == 0) count[e] = (uint16_t)c;
-  }
-  __syncthreads();
-  // exclusive sums over the experts, one a thread
-  uint32_t mine = 0u;
-  if (tid < p.experts) {
-    const uint32_t c = count[tid];
-    mine = ((c + p.cols - 1) / p.cols) << 16 | ((c + 3u) & ~3u);
-  }
-  uint32_t run = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t v = __shfl_up_sync(~0u, run, o);
-    if (lane >= o) run += v;
-  }
-  if (lane == 31) sums[warp] = run;
-  __syncthreads();
-  uint32_t before = 0u, all = 0u;
-  for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += sums[w];
-    all += sums[w];
-  }
-  if (tid < p.experts) base[tid] = before + run - mine;
-  if (tid == 0) *p.out.chunks = (int32_t)(all >> 16);
-  __syncthreads();
-  for (int e = warp; e < p.experts; e += warps) {
-    const int c = count[e];
-    if (c == 0) continue;
-    const int first = (int)(base[e] >> 16), at = (int)(base[e] & 0xFFFFu);
-    for (int q = lane; q * p.cols < c; q += 32)
-      p.out.chunk[first + q] = make_int4(e, at + q * p.cols, min(p.cols, c - q * p.cols), 0);
-    int done = 0;
-    for (int s = lane; s - lane < n; s += 32) {
-      const bool hit = s < n && expert[s] == e;
-      const uint32_t mask = __ballot_sync(~0u, hit);
-      if (hit) {
-        const int place = at + done + __popc(mask & ((1u << lane) - 1u));
-        const int i = s / p.top, j = s - i * p.top;
-        p.out.token[place] = i;
-        p.out.weight[place] =
-            static_cast<const float *>(p.weights.p)[i * p.weights.rs + j * p.weights.cs];
+  for (int r = 0; r < kTurns; ++r) {
+    if (r * (int)blockDim.x >= n) break;
+    const int e = expert[r];
+    const uint32_t same = __match_any_sync(~0u, e);
+    const int lead = __ffs(same) - 1, rank = __popc(same & ((1u << lane) - 1u));
+    const int turns = min(warps, (n - r * (int)blockDim.x + 31) / 32);
+    int before = 0;
+    for (int w = 0; w < turns; ++w) {
+      if (w == warp && e >= 0 && lane == lead) {
+        before = (int)base[e];
+        base[e] = (uint32_t)(before + __popc(same));
       }
-      done += __popc(mask);
+      __syncthreads();
     }
-    if (lane < ((c + 3) & ~3) - c) {  // up to the next chunk: any token, its product is not used
-      p.out.token[at + c + lane] = 0;
-      p.out.weight[at + c + lane] = 0.0f;
+    place[r] = __shfl_sync(~0u, before, lead) + rank;
+  }
+  // exclusive sums over the experts
+  uint32_t at = 0u;
+  for (int e0 = 0; e0 < p.experts; e0 += (int)blockDim.x) {
+    const int e = e0 + tid;
+    const int c = e < p.experts ? (int)base[e] : 0;
+    const int chunks = (c + p.cols - 1) / p.cols;
+    const uint32_t mine = (uint32_t)chunks << 16 | (uint32_t)((c + 3) & ~3);
+    uint32_t run = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(~0u, run, o);
+      if (lane >= o) run += v;
+    }
+    __syncthreads();
+    if (lane == 31) sums[warp] = run;
+    __syncthreads();
+    uint32_t first = at + run - mine;
+    for (int w = 0; w < warps; ++w) {
+      const uint32_t v = sums[w];
+      if (w < warp) first += v;
+      at += v;
+    }
+    if (e < p.experts) base[e] = first;
+    const int q0 = (int)(first >> 16), s0 = (int)(first & 0xFFFFu);
+    for (int q = 0; q < chunks; ++q)
+      p.out.chunk[q0 + q] = make_int4(e, s0 + q * p.cols, min(p.cols, c - q * p.cols), 0);
+    for (int i = c; i < ((c + 3) & ~3); ++i) {  // any token: its product is not used
+      p.out.token[s0 + i] = 0;
+      p.out.weight[s0 + i] = 0.0f;
     }
   }
+  if (tid == 0) *p.out.chunks = (int32_t)(at >> 16);
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kTurns; ++r)
+    if (expert[r] >= 0) {
+      const int s = (int)(base[expert[r]] & 0xFFFFu) + place[r];
+      p.out.token[s] = token[r];
+      p.out.weight[s] = weight[r];
+    }
 }
 
 // ---------------------------------------------------------------- products
@@ -134,6 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 constexpr int kThreads = 192;  // warp 0 loads, 1 matrix instructions and TMEM, 2-5 epilogue
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTile = 128 * 128;  // bytes of 128 rows of one k block
+constexpr uint32_t kShort = 8;
 
 struct ProductParams {
   CUtensorMap w[2], b;  // weights {k, rows, experts}; tokens {k, rows}, by four rows or by 16
@@ -148,7 +163,7 @@ struct ProductParams {
   int32_t features;     // of the product
   int32_t tiles, kblocks, cols, tokens;
   int32_t stages;
-  uint32_t stage_bytes, ring;
+  uint32_t stage_bytes, ring, smem;
   int32_t type, out_type, act;
   int32_t nothing;      // sums of nothing: y = residual
 };
@@ -192,7 +207,7 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// This CTA's length of the line of k blocks, cut into `ctas` lengths of `all` in total.
+// The line of k blocks, cut into `ctas` equal lengths.
 struct Line {
   uint32_t all, ctas;
   __device__ uint32_t begin(uint32_t c) const {
@@ -203,6 +218,15 @@ struct Line {
     return (uint32_t)((((uint64_t)u + 1) * ctas - 1) / all);
   }
 };
+
+// A length is kShort blocks at least where there is too little for every CTA: shorter ones would
+// come sooner, but a tile's shares take longer to join.
+__device__ __forceinline__ Line line_of(const ProductParams &p, int chunks) {
+  Line l;
+  l.all = (uint32_t)chunks * (uint32_t)p.tiles * (uint32_t)p.kblocks;
+  l.ctas = min(kSms, max(l.all / kShort, min(l.all, 1u)));
+  return l;
+}
 
 // Part of a tile: k blocks [k0, k1) of tile `tile` of chunk `chunk`.
 struct Piece {
@@ -298,13 +322,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  // The sums may start beside the inner values where shared memory has room for both, and bring
+  // weights for their whole ring then: the plan they go by is done, because the inner kernel lets
+  // them start only after its own wait for it.
+  if (INNER || warp != 0) griddep_wait();
   griddep_launch();
-  griddep_wait();
 
   const int chunks = p.nothing ? 0 : *p.plan.chunks;
-  Line line;
-  line.all = (uint32_t)chunks * (uint32_t)p.tiles * (uint32_t)p.kblocks;
-  line.ctas = min(gridDim.x, line.all);
+  const Line line = line_of(p, chunks);
   const uint32_t cta = blockIdx.x;
   uint32_t u = 0, end = 0;
   if (cta < line.ctas) {
@@ -313,8 +338,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   if (warp == 0) {
-    uint32_t s = 0, phase = 0;
+    uint32_t s = 0, phase = 0, early = 0;
     bool ok = true;
+    auto weights = [&](const Piece &q, const int4 &c, int kb) {
+      const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes;
+      bar_expect(bar, W * (uint32_t)p.rows * 128u +
+                          (INNER ? (uint32_t)((c.z + 3) / 4) * 512u
+                                 : (uint32_t)((c.z + 15) / 16) * 2048u));
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        tma_box3(at + w * kTile, &p.w[w], kb * kTileK, q.tile * p.rows, c.x, bar);
+    };
+    if (!INNER) {
+      for (uint32_t v = u; v < end && early < stages;) {
+        const Piece q = piece_at<INNER>(p, chunks, v, end);
+        const int4 c = p.plan.chunk[q.chunk];
+        for (int kb = q.k0; kb < q.k1 && early < stages; ++kb) {
+          if (elect_one()) weights(q, c, kb);
+          __syncwarp();
+          ++early;
+          ++s;
+        }
+        v += q.k1 - q.k0;
+      }
+      s = 0;
+      griddep_wait();
+    }
     while (u < end) {
       const Piece q = piece_at<INNER>(p, chunks, u, end);
       const int4 c = p.plan.chunk[q.chunk];
@@ -322,23 +371,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       int4 tok = make_int4(0, 0, 0, 0);
       if (INNER && lane < fours)
         tok = *reinterpret_cast<const int4 *>(p.plan.token + c.y + 4 * lane);
-      const uint32_t bytes =
-          W * (uint32_t)p.rows * 128u + (INNER ? (uint32_t)fours * 512u : (uint32_t)sixteens * 2048u);
       for (int kb = q.k0; kb < q.k1; ++kb) {
-        ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
-        const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes;
-        const int32_t k = kb * kTileK;
-        if (elect_one() && ok) {
-          bar_expect(bar, bytes);
-#pragma unroll
-          for (int w = 0; w < W; ++w)
-            tma_box3(at + w * kTile, &p.w[w], k, q.tile * p.rows, c.x, bar);
-          if (!INNER)
-            for (int i = 0; i < sixteens; ++i)
-              tma_box(at + W * kTile + i * 2048u, &p.b, k, c.y + 16 * i, bar);
+        const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes + W * kTile;
+        if (INNER || early == 0) {
+          ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
+          if (elect_one() && ok) weights(q, c, kb);
+        } else {
+          --early;
         }
         __syncwarp();
-        if (INNER && ok && lane < fours) tma_gather4(at + W * kTile + lane * 512u, &p.b, k, tok, bar);
+        if (INNER) {
+          if (ok && lane < fours) tma_gather4(at + lane * 512u, &p.b, kb * kTileK, tok, bar);
+        } else if (elect_one() && ok) {
+          for (int i = 0; i < sixteens; ++i)
+            tma_box(at + i * 2048u, &p.b, kb * kTileK, c.y + 16 * i, bar);
+        }
         __syncwarp();
         if (++s == stages) {
           s = 0;
@@ -464,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         d ^= 1u;
         u += q.k1 - q.k0;
       }
-      if (c0 != c1) ok = epilogue_all(ok);
+      if (INNER && c0 != c1) ok = epilogue_all(ok);
       if (!ok) continue;
       if (INNER) {
         if (c0 != c1 && arrive_last(p, sh, (int)job, c1 - c0 + 1, (int)threadIdx.x - 64)) {
@@ -477,14 +524,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             float g[16], up[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) g[i] = up[i] = 0.0f;
+#pragma unroll 2
             for (uint32_t w = c0; w <= c1; ++w) {
               const float *o = p.part + (2 * (int64_t)w + (w == c0)) * share + row;
+              float a[16], b[16];
 #pragma unroll
               for (int i = 0; i < 16; ++i)
                 if (i < rows) {
-                  g[i] += __ldcg(o + (i0 + i) * 128);
-                  up[i] += __ldcg(o + (p.cols + i0 + i) * 128);
+                  a[i] = __ldcg(o + (i0 + i) * 128);
+                  b[i] = __ldcg(o + (p.cols + i0 + i) * 128);
                 }
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (i < rows) g[i] += a[i], up[i] += b[i];
             }
             if (live) inner_out(p, c.y + i0, f, rows, g, up);
           }
@@ -492,28 +544,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else {
         const int f = (int)job * p.rows + row;
         const bool live = row < p.rows && f < p.features;
-        bool write = c0 == c1;
-        if (!write) {
+        if (c0 != c1) {
           for (int i = 0; i < p.tokens; ++i) __stcg(part + i * 128, sums[i * 128]);
-          write = arrive_last(p, sh, (int)job, c1 - c0 + 1, (int)threadIdx.x - 64);
-          if (write) {
-            for (int i0 = 0; i0 < p.tokens; i0 += 16) {
-              float v[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-              for (uint32_t w = c0; w <= c1; ++w) {
-                const float *o = p.part + (2 * (int64_t)w + (w == c0)) * share + row;
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                  if (i0 + i < p.tokens) v[i] += __ldcg(o + (i0 + i) * 128);
-              }
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (i0 + i < p.tokens) sums[(i0 + i) * 128] = v[i];
-            }
-          }
+          continue;
         }
-        if (write && live) {
+        if (live) {
+#pragma unroll 8
           for (int i = 0; i < p.tokens; ++i) {
             float v = sums[i * 128];
             if (p.res.p) v += ld_elem(p.res.p, i * p.res.rs + f * p.res.cs, p.out_type);
@@ -532,6 +568,46 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_after();
     tmem_free<1>(tmem, tmem_cols);
   }
+}
+
+// The shares of the sums' cut tiles, in order of the line, and the residual: a launch of its own,
+// because one CTA would be long over up to 128 tokens of a tile (1024 x 512, 128 tokens, eight
+// experts, 19 shares a tile: 100 us).
+constexpr int kJoinTokens = 8;
+
+__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ ProductParams p) {
+  griddep_launch();
+  griddep_wait();
+  const int chunks = *p.plan.chunks;
+  if (chunks == 0) return;
+  const Line line = line_of(p, chunks);
+  const uint32_t step = (uint32_t)p.kblocks * (uint32_t)chunks, job = blockIdx.x;
+  const uint32_t c0 = line.owner(job * step), c1 = line.owner(job * step + step - 1);
+  const int row = threadIdx.x, f = (int)job * p.rows + row, t0 = (int)blockIdx.y * kJoinTokens;
+  if (c0 == c1 || row >= p.rows || f >= p.features) return;
+  const int tokens = min(kJoinTokens, p.tokens - t0);
+  const int64_t share = (int64_t)p.tokens * 128;
+  float v[kJoinTokens];
+#pragma unroll
+  for (int i = 0; i < kJoinTokens; ++i) v[i] = 0.0f;
+#pragma unroll 4
+  for (uint32_t w = c0; w <= c1; ++w) {
+    const float *o = p.part + (2 * (int64_t)w + (w == c0)) * share + t0 * 128 + row;
+    float a[kJoinTokens];
+#pragma unroll
+    for (int i = 0; i < kJoinTokens; ++i)
+      if (i < tokens) a[i] = __ldcg(o + i * 128);
+#pragma unroll
+    for (int i = 0; i < kJoinTokens; ++i)
+      if (i < tokens) v[i] += a[i];
+  }
+#pragma unroll
+  for (int i = 0; i < kJoinTokens; ++i)
+    if (i < tokens) {
+      const int64_t t = t0 + i;
+      if (p.res.p) v[i] += ld_elem(p.res.p, t * p.res.rs + f * p.res.cs, p.out_type);
+      st_elem(p.out, t * p.out_rs + f, v[i], p.out_type);
+    }
 }
 
 // ---------------------------------------------------------------- host
@@ -634,6 +710,14 @@ int alignment(const void *base, int64_t es, int64_t e, int64_t rs, int64_t rows,
 // Tokens up to which the kernels without staging are used whatever the weights' layout.
 constexpr int64_t kDirectTokens = 8;
 
+// Shared memory for the products. Up to 64 tokens the sums' CTAs fit beside those of the inner values
+// (all an SM has is 228 KB, of which a CTA takes 1 KB and its static arrays beside what it asks for):
+// three stages of the inner ring, two where a stage has room for 64 tokens.
+constexpr int64_t kBesideTokens = 64;
+constexpr uint32_t kBesideAll = 228 * 1024 - 2 * 1536;
+constexpr uint32_t kBesideInner = 1024 + 3 * (2 * kTile + 32 * 128);
+constexpr uint32_t kBesideInner64 = 1024 + 2 * (2 * kTile + 64 * 128);
+
 // The workspace of a group of tokens, and the shapes of its launches.
 struct Layout {
   int64_t tokens, places, chunks, ld, packed_ld;
@@ -655,7 +739,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
              (l.tokens <= kDirectTokens ||
               !(copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f) &&
                 copied(a.w_down, a.experts, a.n)));
-  l.cols = !l.direct ? (int32_t)round_up(l.tokens, 16)
+  l.cols = !l.direct ? (l.tokens <= 32 ? (int32_t)round_up(l.tokens, 16) : l.tokens <= 64 ? 64 : 128)
            : l.tokens <= 8 ? 8 : l.tokens <= 16 ? 16 : 32;
   const bool rows = a.x.cs == 1 || a.k == 1;
   const int x_align = alignment(a.x.ptr, 0, 1, a.x.rs, a.m, a.k);
@@ -701,16 +785,21 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     q.out_type = (int32_t)a.out_dtype;
     p.act = (int32_t)a.act;
     p.status = q.status = a.status;
-    auto ring = [&](ProductParams &r, int w, uint32_t fixed) {
+    auto ring = [&](ProductParams &r, int w, uint32_t fixed, uint32_t room) {
       r.stage_bytes = w * kTile + (uint32_t)l.cols * 128u;
-      r.stages = (int32_t)((kTcSmem - 1024 - fixed) / r.stage_bytes);
+      r.stages = (int32_t)((room - 1024 - fixed) / r.stage_bytes);
       if (r.stages > kMaxStages) r.stages = kMaxStages;
       r.ring = r.stages * r.stage_bytes;
+      r.smem = 1024 + r.ring + fixed;
     };
-    ring(p, 2, 0);
-    ring(q, 1, (uint32_t)l.tokens * 512u);
+    if (l.tokens <= kBesideTokens) {
+      ring(p, 2, 0, l.cols <= 32 ? kBesideInner : kBesideInner64);
+      ring(q, 1, (uint32_t)l.tokens * 512u, kBesideAll - p.smem);
+    } else {
+      ring(p, 2, 0, kTcSmem);
+      ring(q, 1, (uint32_t)l.tokens * 512u, kTcSmem);
+    }
     jobs = (uint64_t)l.chunks * p.tiles;
-    sums = q.tiles;
     const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
     part = 2 * kSms * (inner > outer ? inner : outer);
   } else {
@@ -766,7 +855,6 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   s.out = p.plan = q.plan = d.plan = e.plan = o;
   s.counters = p.counters = d.counters = e.counters = counters;
   s.n_counters = (uint32_t)(jobs + sums);
-  if (base) q.counters = counters + jobs;
   p.out = h;
   p.out_rs = l.ld;
   d.h = reinterpret_cast<uint16_t *>(h);
@@ -791,7 +879,7 @@ int set_up() {
 
 template <bool INNER>
 cudaError_t launch(const ProductParams &p, cudaStream_t s) {
-  return dense_launch(product_kernel<INNER>, dim3(kSms), kThreads, kTcSmem, 1, s, p);
+  return dense_launch(product_kernel<INNER>, dim3(kSms), kThreads, p.smem, 1, s, p);
 }
 
 int run(const coll_experts_t &a, char *base, cudaStream_t s) {
@@ -838,8 +926,10 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
                      a.residual.rs, a.residual.cs};
     cudaError_t err = cudaSuccess;
     if (l.planned) {
-      const unsigned more = l.pack ? (unsigned)ceil_div(tokens * l.packed_ld / 8, kPlanThreads) : 0;
-      err = dense_launch(plan_kernel, dim3(1 + more), kPlanThreads, 0, 1, s, o);
+      const int64_t most = tokens * a.top > a.experts ? tokens * a.top : a.experts;
+      const unsigned threads = most >= kPlanThreads ? kPlanThreads : (unsigned)round_up(most, 32);
+      const unsigned more = l.pack ? (unsigned)ceil_div(tokens * l.packed_ld / 8, threads) : 0;
+      err = dense_launch(plan_kernel, dim3(1 + more), threads, 0, 1, s, o);
     }
     if (l.direct) {
       d.ids = e.ids = o.ids;
@@ -857,6 +947,9 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
       q.res = res;
       if (err == cudaSuccess && !l.nothing) err = launch<true>(p, s);
       if (err == cudaSuccess) err = launch<false>(q, s);
+      if (err == cudaSuccess && !l.nothing)
+        err = dense_launch(join_kernel,
+                           dim3(q.tiles, (unsigned)ceil_div(tokens, kJoinTokens)), 128, 0, 1, s, q);
     }
     if (err != cudaSuccess) return COLL_ECUDA;
   }

@@ -112,7 +112,7 @@ __device__ __forceinline__ void load_rows(const uint16_t *const (&pa)[AHEAD],
 // Eight inner features of one chunk's choices: gate's rows are the fragment's first eight, up's the
 // others. The warps take the steps of k in turn and join in order.
 template <int TYPE, int NT, int ALIGN>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(kWarps * 32, 2)
     direct_inner_kernel(const __grid_constant__ DirectParams p) {
   constexpr int AHEAD = kAhead<NT, ALIGN>;
   __shared__ float part[kWarps][8 * NT][16];
@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   __shared__ int chunks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
-  griddep_launch();
   griddep_wait();
+  griddep_launch();
   int4 c;
   const int32_t *token;
   if (p.plan.chunks) {
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
 // times their weights, to its own sums in shared memory. The warps join in order, and so do the
 // splits, in the last of their CTAs to arrive.
 template <int TYPE, int NT, int ALIGN>
-__global__ void __launch_bounds__(kWarps * 32, 1)
+__global__ void __launch_bounds__(kWarps * 32, 2)
     direct_outer_kernel(const __grid_constant__ DirectParams p) {
   constexpr int AHEAD = kAhead<NT, ALIGN>;
   extern __shared__ float sums[];  // [warps][tokens][16], then the plan's chunks
@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
   const int g = lane >> 2, t = lane & 3, size = p.tokens * 16;
   griddep_launch();
   for (int i = threadIdx.x; i < warps * size; i += blockDim.x) sums[i] = 0.0f;
-  griddep_wait();
+  // The inner kernel lets this one start after its own wait, so what that waited for (the choices,
+  // the plan, the weights) is there; its inner values are not before the wait below.
   const int4 *chunk = few_chunk;
   const int32_t *token = few.token;
   const float *weight = few.weight;
@@ -317,6 +318,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
     Rows<ALIGN, AHEAD> r;
     load_rows<ALIGN, AHEAD>(pa, pb, at, ka, kb, r);
+    griddep_wait();
     uint32_t x[AHEAD][NT][8];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) load_x<NT, ALIGN>(p, col[i], from[i], at[i], x[i]);
@@ -336,6 +338,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1)
     }
   }
   if (now >= 0) flush();
+  griddep_wait();  // also where nothing was to be done
   __syncthreads();
   auto finish = [&](int i, float v) {
     const int tok = i / 16, f = n0 + i % 16;
