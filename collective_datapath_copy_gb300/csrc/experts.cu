@@ -33,7 +33,7 @@ constexpr int kPlanThreads = 1024;
 struct PlanParams {
   DenseMat ids, weights;  // of this group's tokens
   ExpertsPlan out;
-  uint32_t *counters;     // of cut tiles, all set to 0
+  uint32_t *counters;     // that the launches after it want set to 0
   DenseMat x;             // rows to lay out; p NULL: none
   uint16_t *packed;
   int64_t k, packed_ld;
@@ -153,7 +153,6 @@ constexpr uint32_t kShort = 8;
 struct ProductParams {
   CUtensorMap w[2], b;  // weights {k, rows, experts}; tokens {k, rows}, by four rows or by 16
   ExpertsPlan plan;
-  uint32_t *counters;
   DenseMat res;         // sums only
   void *out;            // inner values [place][out_rs], or y
   int64_t out_rs;
@@ -170,7 +169,7 @@ struct ProductParams {
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], ready[2], free[2];
-  uint32_t tmem, abort, last;
+  uint32_t tmem, abort;
 };
 
 __device__ __forceinline__ void tma_box3(uint32_t sdst, const void *map, int32_t x, int32_t y,
@@ -190,6 +189,11 @@ __device__ __forceinline__ void tma_gather4(uint32_t sdst, const void *map, int3
       ".mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(sdst),
       "l"(map), "r"(x), "r"(r.x), "r"(r.y), "r"(r.z), "r"(r.w), "r"(bar)
       : "memory");
+}
+
+// Bring a tensor map, whose first use would wait for it.
+__device__ __forceinline__ void map_ahead(const void *map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // 16 columns of this warp's 32 lanes.
@@ -228,6 +232,13 @@ __device__ __forceinline__ Line line_of(const ProductParams &p, int chunks) {
   return l;
 }
 
+// A CTA's share of a cut tile that CTA c0 begins: of one begun by an earlier CTA, or of one ended by a
+// later one. Inner: [g, u][choice][128]; sums: [token][128].
+template <bool INNER>
+__device__ __forceinline__ float *share_of(const ProductParams &p, uint32_t cta, uint32_t c0) {
+  return p.part + (2 * (int64_t)cta + (cta == c0)) * (INNER ? 2 * p.cols : p.tokens) * 128;
+}
+
 // Part of a tile: k blocks [k0, k1) of tile `tile` of chunk `chunk`.
 struct Piece {
   int chunk, tile, k0, k1;
@@ -250,36 +261,6 @@ __device__ __forceinline__ Piece piece_at(const ProductParams &p, int chunks, ui
     q.chunk = (int)(item - (uint32_t)q.tile * chunks);
   }
   return q;
-}
-
-__device__ __forceinline__ void epilogue_sync() {
-  asm volatile("bar.sync 1, 128;" ::: "memory");
-}
-
-// Have all of the epilogue's threads got this far without giving up? Every cut tile asks, so that no
-// thread waits at a barrier that another has passed by.
-__device__ __forceinline__ bool epilogue_all(bool ok) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
-      "barrier.red.and.pred q, 1, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-      : "=r"(r)
-      : "r"((uint32_t)ok)
-      : "memory");
-  return r != 0u;
-}
-
-// After this CTA's share of `job` is in memory: is it the last of `shares`? The others' are visible
-// to the epilogue's threads then.
-__device__ __forceinline__ bool arrive_last(const ProductParams &p, Shared &sh, int job,
-                                            uint32_t shares, int tid) {
-  __threadfence();
-  epilogue_sync();
-  if (tid == 0) sh.last = atomicAdd(&p.counters[job], 1u) == shares - 1u;
-  epilogue_sync();
-  const bool last = sh.last != 0u;
-  if (last) __threadfence();
-  return last;
 }
 
 __device__ __forceinline__ void inner_out(const ProductParams &p, int64_t place, int f, int rows,
@@ -306,6 +287,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   while (tmem_cols < 2u * W * p.cols) tmem_cols *= 2;
 
   if (threadIdx.x == 0) {
+    map_ahead(&p.w[0]);
+    if (INNER) map_ahead(&p.w[1]);
+    map_ahead(&p.b);
     for (uint32_t i = 0; i < stages; ++i) {
       mbar_init(&sh.full[i], 1);
       mbar_init(&sh.empty[i], 1);
@@ -349,21 +333,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int w = 0; w < W; ++w)
         tma_box3(at + w * kTile, &p.w[w], kb * kTileK, q.tile * p.rows, c.x, bar);
     };
-    if (!INNER) {
-      for (uint32_t v = u; v < end && early < stages;) {
-        const Piece q = piece_at<INNER>(p, chunks, v, end);
-        const int4 c = p.plan.chunk[q.chunk];
-        for (int kb = q.k0; kb < q.k1 && early < stages; ++kb) {
-          if (elect_one()) weights(q, c, kb);
-          __syncwarp();
-          ++early;
-          ++s;
-        }
-        v += q.k1 - q.k0;
+    for (uint32_t v = u; v < end && early < stages;) {
+      const Piece q = piece_at<INNER>(p, chunks, v, end);
+      const int4 c = p.plan.chunk[q.chunk];
+      for (int kb = q.k0; kb < q.k1 && early < stages; ++kb) {
+        if (elect_one()) weights(q, c, kb);
+        __syncwarp();
+        ++early;
+        ++s;
       }
-      s = 0;
-      griddep_wait();
+      v += q.k1 - q.k0;
     }
+    s = 0;
+    if (!INNER) griddep_wait();
     while (u < end) {
       const Piece q = piece_at<INNER>(p, chunks, u, end);
       const int4 c = p.plan.chunk[q.chunk];
@@ -373,7 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tok = *reinterpret_cast<const int4 *>(p.plan.token + c.y + 4 * lane);
       for (int kb = q.k0; kb < q.k1; ++kb) {
         const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes + W * kTile;
-        if (INNER || early == 0) {
+        if (early == 0) {
           ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
           if (elect_one() && ok) weights(q, c, kb);
         } else {
@@ -458,9 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t job = u / step;
       const uint32_t c0 = line.owner(job * step), c1 = line.owner(job * step + step - 1);
       const uint32_t job_end = min(end, job * step + step);
-      // its share in memory: that of a tile begun by an earlier CTA, or of one ended by a later
-      const int64_t share = (int64_t)INNER ? (int64_t)2 * p.cols * 128 : (int64_t)p.tokens * 128;
-      float *part = p.part + (2 * (int64_t)cta + (cta == c0)) * share + row;
+      float *part = share_of<INNER>(p, cta, c0) + row;
       if (!INNER)
         for (int i = 0; i < p.tokens; ++i) sums[i * 128] = 0.0f;
       while (u < job_end) {
@@ -511,44 +491,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         d ^= 1u;
         u += q.k1 - q.k0;
       }
-      if (INNER && c0 != c1) ok = epilogue_all(ok);
-      if (!ok) continue;
-      if (INNER) {
-        if (c0 != c1 && arrive_last(p, sh, (int)job, c1 - c0 + 1, (int)threadIdx.x - 64)) {
-          const Piece q = piece_at<INNER>(p, chunks, job * step, line.all);
-          const int4 c = p.plan.chunk[q.chunk];
-          const int f = q.tile * p.rows + row;
-          const bool live = row < p.rows && f < p.features;
-          for (int i0 = 0; i0 < c.z; i0 += 16) {
-            const int rows = min(16, c.z - i0);
-            float g[16], up[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) g[i] = up[i] = 0.0f;
-#pragma unroll 2
-            for (uint32_t w = c0; w <= c1; ++w) {
-              const float *o = p.part + (2 * (int64_t)w + (w == c0)) * share + row;
-              float a[16], b[16];
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (i < rows) {
-                  a[i] = __ldcg(o + (i0 + i) * 128);
-                  b[i] = __ldcg(o + (p.cols + i0 + i) * 128);
-                }
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (i < rows) g[i] += a[i], up[i] += b[i];
-            }
-            if (live) inner_out(p, c.y + i0, f, rows, g, up);
-          }
-        }
-      } else {
+      if (!INNER && ok) {
         const int f = (int)job * p.rows + row;
-        const bool live = row < p.rows && f < p.features;
         if (c0 != c1) {
+#pragma unroll 8
           for (int i = 0; i < p.tokens; ++i) __stcg(part + i * 128, sums[i * 128]);
-          continue;
-        }
-        if (live) {
+        } else if (row < p.rows && f < p.features) {
 #pragma unroll 8
           for (int i = 0; i < p.tokens; ++i) {
             float v = sums[i * 128];
@@ -570,44 +518,67 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-// The shares of the sums' cut tiles, in order of the line, and the residual: a launch of its own,
-// because one CTA would be long over up to 128 tokens of a tile (1024 x 512, 128 tokens, eight
-// experts, 19 shares a tile: 100 us).
-constexpr int kJoinTokens = 8;
+// The shares of cut tiles, in order of the line: inner values are finished, sums get the residual. A
+// launch of its own (about 2.5 us), because the last CTA to arrive would do it with one SM's loads in
+// flight, and after a fence and an atomic: 5 us a tile, and a CTA can have two.
+constexpr int kJoinRows = 16;
 
-__global__ void __launch_bounds__(128) join_kernel(const __grid_constant__ ProductParams p) {
+template <bool INNER>
+__global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ ProductParams p) {
   griddep_launch();
-  griddep_wait();
+  // the plan is done: the kernel before lets this one start after its own wait
   const int chunks = *p.plan.chunks;
-  if (chunks == 0) return;
   const Line line = line_of(p, chunks);
-  const uint32_t step = (uint32_t)p.kblocks * (uint32_t)chunks, job = blockIdx.x;
-  const uint32_t c0 = line.owner(job * step), c1 = line.owner(job * step + step - 1);
-  const int row = threadIdx.x, f = (int)job * p.rows + row, t0 = (int)blockIdx.y * kJoinTokens;
-  if (c0 == c1 || row >= p.rows || f >= p.features) return;
-  const int tokens = min(kJoinTokens, p.tokens - t0);
-  const int64_t share = (int64_t)p.tokens * 128;
-  float v[kJoinTokens];
-#pragma unroll
-  for (int i = 0; i < kJoinTokens; ++i) v[i] = 0.0f;
-#pragma unroll 4
-  for (uint32_t w = c0; w <= c1; ++w) {
-    const float *o = p.part + (2 * (int64_t)w + (w == c0)) * share + t0 * 128 + row;
-    float a[kJoinTokens];
-#pragma unroll
-    for (int i = 0; i < kJoinTokens; ++i)
-      if (i < tokens) a[i] = __ldcg(o + i * 128);
-#pragma unroll
-    for (int i = 0; i < kJoinTokens; ++i)
-      if (i < tokens) v[i] += a[i];
+  const uint32_t cta = blockIdx.x;
+  const uint32_t step = INNER ? (uint32_t)p.kblocks : (uint32_t)p.kblocks * (uint32_t)chunks;
+  uint32_t job = 0, c1 = 0;
+  bool cut = false;
+  if (cta < line.ctas) {  // the tile that this CTA of the line began last
+    job = (line.begin(cta + 1) - 1) / step;
+    c1 = line.owner(job * step + step - 1);
+    cut = line.owner(job * step) == cta && c1 > cta;
   }
+  const int row = threadIdx.x & 127, group = threadIdx.x >> 7;
+  Piece q = {};
+  int4 c = make_int4(0, 0, 0, 0);
+  if (cut) {
+    q = piece_at<INNER>(p, chunks, job * step, line.all);
+    if (INNER) c = p.plan.chunk[q.chunk];
+  }
+  griddep_wait();
+  if (!cut) return;
+  const int f = q.tile * p.rows + row;
+  if (row >= p.rows || f >= p.features) return;
+  const int all = INNER ? c.z : p.tokens;
+  for (int i0 = (int)blockIdx.y * kJoinRows + group; i0 < all;
+       i0 += (int)gridDim.y * kJoinRows) {
+    constexpr int R = kJoinRows / 4;
+    float v[R], u[R];
 #pragma unroll
-  for (int i = 0; i < kJoinTokens; ++i)
-    if (i < tokens) {
-      const int64_t t = t0 + i;
-      if (p.res.p) v[i] += ld_elem(p.res.p, t * p.res.rs + f * p.res.cs, p.out_type);
-      st_elem(p.out, t * p.out_rs + f, v[i], p.out_type);
+    for (int i = 0; i < R; ++i) v[i] = u[i] = 0.0f;
+#pragma unroll 4
+    for (uint32_t w = cta; w <= c1; ++w) {
+      const float *o = share_of<INNER>(p, w, cta) + i0 * 128 + row;
+#pragma unroll
+      for (int i = 0; i < R; ++i)
+        if (i0 + 4 * i < all) {
+          v[i] += __ldcg(o + 4 * i * 128);
+          if (INNER) u[i] += __ldcg(o + (p.cols + 4 * i) * 128);
+        }
     }
+    if constexpr (INNER) act_run(v, p.act);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const int64_t t = i0 + 4 * i;
+      if (t >= all) break;
+      if constexpr (INNER) {
+        static_cast<uint16_t *>(p.out)[(c.y + t) * p.out_rs + f] = f2h(v[i] * u[i], p.type);
+      } else {
+        if (p.res.p) v[i] += ld_elem(p.res.p, t * p.res.rs + f * p.res.cs, p.out_type);
+        st_elem(p.out, t * p.out_rs + f, v[i], p.out_type);
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- host
@@ -764,7 +735,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   DirectParams &d = l.few, &e = l.few_sums;
   PlanParams &s = l.plan;
   ExpertsPlan o = {};
-  uint64_t part = 0, jobs = 0, sums = 0;
+  uint64_t part = 0, counters = 0;
   if (!l.direct) {
     p.tiles = (int32_t)ceil_div(a.f, 128);
     q.tiles = (int32_t)ceil_div(a.n, 128);
@@ -799,7 +770,6 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
       ring(p, 2, 0, kTcSmem);
       ring(q, 1, (uint32_t)l.tokens * 512u, kTcSmem);
     }
-    jobs = (uint64_t)l.chunks * p.tiles;
     const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
     part = 2 * kSms * (inner > outer ? inner : outer);
   } else {
@@ -831,7 +801,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     if (splits > 32) splits = 32;
     if (splits > 1) {
       d.splits = e.splits = (int32_t)splits;
-      sums = (uint64_t)e.tiles;
+      counters = (uint64_t)e.tiles;
       part = (uint64_t)splits * e.tiles * l.tokens * 64;
     }
   }
@@ -841,7 +811,8 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     o.token = reinterpret_cast<int32_t *>(take((uint64_t)l.places * 4));
     o.weight = reinterpret_cast<float *>(take((uint64_t)l.places * 4));
   }
-  uint32_t *counters = reinterpret_cast<uint32_t *>(take((jobs + sums) * 4));
+  s.counters = d.counters = e.counters = reinterpret_cast<uint32_t *>(take(counters * 4));
+  s.n_counters = (uint32_t)counters;
   char *h = take((uint64_t)l.places * l.ld * 2);
   p.part = q.part = e.part = reinterpret_cast<float *>(take(part));
   if (l.pack)
@@ -853,8 +824,6 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   s.cols = l.cols;
   s.k = a.k;
   s.out = p.plan = q.plan = d.plan = e.plan = o;
-  s.counters = p.counters = d.counters = e.counters = counters;
-  s.n_counters = (uint32_t)(jobs + sums);
   p.out = h;
   p.out_rs = l.ld;
   d.h = reinterpret_cast<uint16_t *>(h);
@@ -879,7 +848,12 @@ int set_up() {
 
 template <bool INNER>
 cudaError_t launch(const ProductParams &p, cudaStream_t s) {
-  return dense_launch(product_kernel<INNER>, dim3(kSms), kThreads, p.smem, 1, s, p);
+  const cudaError_t e =
+      dense_launch(product_kernel<INNER>, dim3(kSms), kThreads, p.smem, 1, s, p);
+  if (e != cudaSuccess || p.nothing) return e;
+  // beside each other on an SM: these wait there while the products run
+  const int64_t turns = ceil_div(INNER ? p.cols : p.tokens, kJoinRows);
+  return dense_launch(join_kernel<INNER>, dim3(kSms, turns < 2 ? 1 : 2), 512, 0, 1, s, p);
 }
 
 int run(const coll_experts_t &a, char *base, cudaStream_t s) {
@@ -947,9 +921,6 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
       q.res = res;
       if (err == cudaSuccess && !l.nothing) err = launch<true>(p, s);
       if (err == cudaSuccess) err = launch<false>(q, s);
-      if (err == cudaSuccess && !l.nothing)
-        err = dense_launch(join_kernel,
-                           dim3(q.tiles, (unsigned)ceil_div(tokens, kJoinTokens)), 128, 0, 1, s, q);
     }
     if (err != cudaSuccess) return COLL_ECUDA;
   }
