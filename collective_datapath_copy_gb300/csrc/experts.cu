@@ -30,46 +30,24 @@ namespace {
 constexpr int kTileK = 64;
 constexpr int kPlanThreads = 1024;
 
-struct PlanParams {
-  DenseMat ids, weights;  // of this group's tokens
-  ExpertsPlan out;
-  uint32_t *counters;     // that the launches after it want set to 0
-  DenseMat x;             // rows to lay out; p NULL: none
-  uint16_t *packed;
-  int64_t k, packed_ld;
-  uint32_t n_counters;
+// Where the choices come from.
+struct Choices {
+  DenseMat ids, weights;
   int32_t tokens, top, experts, first, cols;
 };
 
-// CTA 0 plans; the others lay out x in rows of whole 16-byte runs where no tensor copy takes it as
-// it lies. The choices go through the CTA 32 at a time, a warp after the other, each adding to its
-// experts' counts: so they stay in order, and the plan does not depend on timing.
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
-  __shared__ uint32_t base[kExpertsMost];  // count; then chunks before it << 16 | places before it
-  __shared__ uint32_t sums[32];
+// The plan of up to TURNS choices a thread, by all threads of the CTA; the number of chunks. The
+// choices go through the CTA 32 at a time, a warp after the other, each adding to its experts'
+// counts: so they stay in order, and the plan does not depend on timing. base: a word an expert.
+template <int TURNS>
+__device__ __forceinline__ int make_plan(const Choices &p, int4 *chunk, int32_t *tokens,
+                                         float *weights, uint32_t *base, uint32_t *sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-  griddep_wait();
-  griddep_launch();
-  if (blockIdx.x > 0) {
-    const int64_t runs = p.packed_ld / 8, all = runs * p.tokens;
-    for (int64_t r = (int64_t)(blockIdx.x - 1) * blockDim.x + tid; r < all;
-         r += (int64_t)(gridDim.x - 1) * blockDim.x) {
-      const int64_t i = r / runs, k = r % runs * 8;
-      const uint16_t *q = static_cast<const uint16_t *>(p.x.p) + i * p.x.rs + k * p.x.cs;
-      uint32_t v[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = k + j < p.k ? q[j * p.x.cs] : 0u;
-      *reinterpret_cast<uint4 *>(p.packed + i * p.packed_ld + k) =
-          make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-    }
-    return;
-  }
   const int n = p.tokens * p.top;
-  constexpr int kTurns = kExpertsGroup * kChosenMost / kPlanThreads;
-  int expert[kTurns], token[kTurns], place[kTurns];
-  float weight[kTurns];
+  int expert[TURNS], token[TURNS], place[TURNS];
+  float weight[TURNS];
 #pragma unroll
-  for (int r = 0; r < kTurns; ++r) {
+  for (int r = 0; r < TURNS; ++r) {
     const int s = r * (int)blockDim.x + tid;
     expert[r] = -1;
     if (s < n) {
@@ -82,10 +60,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     }
   }
   for (int i = tid; i < p.experts; i += blockDim.x) base[i] = 0u;
-  for (uint32_t i = tid; i < p.n_counters; i += blockDim.x) p.counters[i] = 0u;
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kTurns; ++r) {
+  for (int r = 0; r < TURNS; ++r) {
     if (r * (int)blockDim.x >= n) break;
     const int e = expert[r];
     const uint32_t same = __match_any_sync(~0u, e);
@@ -101,13 +78,13 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     }
     place[r] = __shfl_sync(~0u, before, lead) + rank;
   }
-  // exclusive sums over the experts
+  // from counts to chunks before an expert << 16 | places before it
   uint32_t at = 0u;
   for (int e0 = 0; e0 < p.experts; e0 += (int)blockDim.x) {
     const int e = e0 + tid;
     const int c = e < p.experts ? (int)base[e] : 0;
     const int chunks = (c + p.cols - 1) / p.cols;
-    const uint32_t mine = (uint32_t)chunks << 16 | (uint32_t)((c + 3) & ~3);
+    const uint32_t mine = (uint32_t)chunks << 16 | (uint32_t)c;
     uint32_t run = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -126,21 +103,54 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     if (e < p.experts) base[e] = first;
     const int q0 = (int)(first >> 16), s0 = (int)(first & 0xFFFFu);
     for (int q = 0; q < chunks; ++q)
-      p.out.chunk[q0 + q] = make_int4(e, s0 + q * p.cols, min(p.cols, c - q * p.cols), 0);
-    for (int i = c; i < ((c + 3) & ~3); ++i) {  // any token: its product is not used
-      p.out.token[s0 + i] = 0;
-      p.out.weight[s0 + i] = 0.0f;
-    }
+      chunk[q0 + q] = make_int4(e, s0 + q * p.cols, min(p.cols, c - q * p.cols), 0);
   }
-  if (tid == 0) *p.out.chunks = (int32_t)(at >> 16);
   __syncthreads();
 #pragma unroll
-  for (int r = 0; r < kTurns; ++r)
+  for (int r = 0; r < TURNS; ++r)
     if (expert[r] >= 0) {
       const int s = (int)(base[expert[r]] & 0xFFFFu) + place[r];
-      p.out.token[s] = token[r];
-      p.out.weight[s] = weight[r];
+      tokens[s] = token[r];
+      weights[s] = weight[r];
     }
+  return (int)(at >> 16);
+}
+
+struct PlanParams {
+  Choices choices;        // of this group's tokens
+  ExpertsPlan out;
+  uint32_t *counters;     // that the launches after it want set to 0
+  DenseMat x;             // rows to lay out; p NULL: none
+  uint16_t *packed;
+  int64_t k, packed_ld;
+  uint32_t n_counters;
+};
+
+// CTA 0 plans; the others lay out x in rows of whole 16-byte runs where no tensor copy takes it as
+// it lies.
+__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
+  __shared__ uint32_t base[kExpertsMost], sums[32];
+  const int tid = threadIdx.x;
+  griddep_wait();
+  griddep_launch();
+  if (blockIdx.x > 0) {
+    const int64_t runs = p.packed_ld / 8, all = runs * p.choices.tokens;
+    for (int64_t r = (int64_t)(blockIdx.x - 1) * blockDim.x + tid; r < all;
+         r += (int64_t)(gridDim.x - 1) * blockDim.x) {
+      const int64_t i = r / runs, k = r % runs * 8;
+      const uint16_t *q = static_cast<const uint16_t *>(p.x.p) + i * p.x.rs + k * p.x.cs;
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = k + j < p.k ? q[j * p.x.cs] : 0u;
+      *reinterpret_cast<uint4 *>(p.packed + i * p.packed_ld + k) =
+          make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+    return;
+  }
+  for (uint32_t i = tid; i < p.n_counters; i += blockDim.x) p.counters[i] = 0u;
+  const int chunks = make_plan<kExpertsGroup * kChosenMost / kPlanThreads>(
+      p.choices, p.out.chunk, p.out.token, p.out.weight, base, sums);
+  if (tid == 0) *p.out.chunks = chunks;
 }
 
 // ---------------------------------------------------------------- products
@@ -152,7 +162,8 @@ constexpr uint32_t kShort = 8;
 
 struct ProductParams {
   CUtensorMap w[2], b;  // weights {k, rows, experts}; tokens {k, rows}, by four rows or by 16
-  ExpertsPlan plan;
+  Choices choices;
+  ExpertsPlan plan;     // plan.chunks NULL: every CTA makes its own
   DenseMat res;         // sums only
   void *out;            // inner values [place][out_rs], or y
   int64_t out_rs;
@@ -166,6 +177,35 @@ struct ProductParams {
   int32_t type, out_type, act;
   int32_t nothing;      // sums of nothing: y = residual
 };
+
+// A plan of few choices, made by every CTA that goes by it: no launch and no way through memory
+// before the first weights are asked for (16 tokens of two, eight experts of 4096 x 1792: 71 us with
+// plan_kernel, 67 so).
+constexpr int kOwnChoices = 256;
+
+struct OwnPlan {
+  int4 chunk[kOwnChoices];
+  int32_t token[kOwnChoices];
+  float weight[kOwnChoices];
+  uint32_t base[kExpertsMost], sums[32];
+};
+
+struct PlanView {
+  const int4 *chunk;
+  const int32_t *token;
+  const float *weight;
+  int chunks;
+};
+
+// By all threads of the CTA. What the plan depends on is there: the caller has waited for it, or the
+// kernel before it had before it let this one start.
+template <int TURNS>
+__device__ __forceinline__ PlanView view_plan(const ProductParams &p, OwnPlan &own) {
+  if (p.plan.chunks) return PlanView{p.plan.chunk, p.plan.token, p.plan.weight, *p.plan.chunks};
+  const int n = make_plan<TURNS>(p.choices, own.chunk, own.token, own.weight, own.base, own.sums);
+  __syncthreads();
+  return PlanView{own.chunk, own.token, own.weight, n};
+}
 
 struct Shared {
   uint64_t full[kMaxStages], empty[kMaxStages], ready[2], free[2];
@@ -277,6 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     product_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ Shared sh;
+  __shared__ OwnPlan own;
   const uint32_t ring = (smem_u32(raw) + 1023u) & ~1023u;
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t full0 = smem_u32(&sh.full[0]), empty0 = smem_u32(&sh.empty[0]);
@@ -309,10 +350,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The sums may start beside the inner values where shared memory has room for both, and bring
   // weights for their whole ring then: the plan they go by is done, because the inner kernel lets
   // them start only after its own wait for it.
-  if (INNER || warp != 0) griddep_wait();
+  if (INNER || p.nothing) griddep_wait();
   griddep_launch();
-
-  const int chunks = p.nothing ? 0 : *p.plan.chunks;
+  PlanView plan = {};
+  if (!p.nothing) plan = view_plan<(kOwnChoices + kThreads - 1) / kThreads>(p, own);
+  if (!INNER && warp != 0) griddep_wait();
+  const int chunks = plan.chunks;
   const Line line = line_of(p, chunks);
   const uint32_t cta = blockIdx.x;
   uint32_t u = 0, end = 0;
@@ -335,7 +378,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     for (uint32_t v = u; v < end && early < stages;) {
       const Piece q = piece_at<INNER>(p, chunks, v, end);
-      const int4 c = p.plan.chunk[q.chunk];
+      const int4 c = plan.chunk[q.chunk];
       for (int kb = q.k0; kb < q.k1 && early < stages; ++kb) {
         if (elect_one()) weights(q, c, kb);
         __syncwarp();
@@ -348,11 +391,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (!INNER) griddep_wait();
     while (u < end) {
       const Piece q = piece_at<INNER>(p, chunks, u, end);
-      const int4 c = p.plan.chunk[q.chunk];
+      const int4 c = plan.chunk[q.chunk];
       const int fours = (c.z + 3) / 4, sixteens = (c.z + 15) / 16;
       int4 tok = make_int4(0, 0, 0, 0);
-      if (INNER && lane < fours)
-        tok = *reinterpret_cast<const int4 *>(p.plan.token + c.y + 4 * lane);
+      if (INNER && lane < fours) {  // behind the last choice the first again: its product is not used
+        const int32_t *q4 = plan.token + c.y;
+        const int i = 4 * lane;
+        tok = make_int4(q4[i], q4[i + 1 < c.z ? i + 1 : 0], q4[i + 2 < c.z ? i + 2 : 0],
+                        q4[i + 3 < c.z ? i + 3 : 0]);
+      }
       for (int kb = q.k0; kb < q.k1; ++kb) {
         const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes + W * kTile;
         if (early == 0) {
@@ -383,7 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     while (u < end) {
       const Piece q = piece_at<INNER>(p, chunks, u, end);
-      const uint32_t n = (uint32_t)(p.plan.chunk[q.chunk].z + 15) & ~15u;
+      const uint32_t n = (uint32_t)(plan.chunk[q.chunk].z + 15) & ~15u;
       const uint32_t idesc = mma_desc(p.type == COLL_BF16, false, false, 128, n);
       const uint32_t d0 = tmem + d * W * p.cols, d1 = d0 + p.cols;
       ok = ok && wait_bar(&sh.abort, free0 + 8 * d, dphase ^ 1u, p.status);
@@ -445,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < p.tokens; ++i) sums[i * 128] = 0.0f;
       while (u < job_end) {
         const Piece q = piece_at<INNER>(p, chunks, u, job_end);
-        const int4 c = p.plan.chunk[q.chunk];
+        const int4 c = plan.chunk[q.chunk];
         const int f = q.tile * p.rows + row;
         const bool live = row < p.rows && f < p.features;
         ok = ok && __all_sync(~0u, wait_bar(&sh.abort, ready0 + 8 * d, dphase, p.status));
@@ -472,8 +519,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             int tok = 0;
             float wt = 0.0f;
             if (lane < rows) {
-              tok = p.plan.token[c.y + i0 + lane];
-              wt = p.plan.weight[c.y + i0 + lane];
+              tok = plan.token[c.y + i0 + lane];
+              wt = plan.weight[c.y + i0 + lane];
             }
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
@@ -525,9 +572,10 @@ constexpr int kJoinRows = 16;
 
 template <bool INNER>
 __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ ProductParams p) {
+  __shared__ OwnPlan own;
   griddep_launch();
-  // the plan is done: the kernel before lets this one start after its own wait
-  const int chunks = *p.plan.chunks;
+  const PlanView plan = view_plan<1>(p, own);
+  const int chunks = plan.chunks;
   const Line line = line_of(p, chunks);
   const uint32_t cta = blockIdx.x;
   const uint32_t step = INNER ? (uint32_t)p.kblocks : (uint32_t)p.kblocks * (uint32_t)chunks;
@@ -543,7 +591,7 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Produ
   int4 c = make_int4(0, 0, 0, 0);
   if (cut) {
     q = piece_at<INNER>(p, chunks, job * step, line.all);
-    if (INNER) c = p.plan.chunk[q.chunk];
+    if (INNER) c = plan.chunk[q.chunk];
   }
   griddep_wait();
   if (!cut) return;
@@ -685,7 +733,8 @@ constexpr int64_t kDirectTokens = 8;
 // (all an SM has is 228 KB, of which a CTA takes 1 KB and its static arrays beside what it asks for):
 // three stages of the inner ring, two where a stage has room for 64 tokens.
 constexpr int64_t kBesideTokens = 64;
-constexpr uint32_t kBesideAll = 228 * 1024 - 2 * 1536;
+constexpr uint32_t kBesideAll = 228 * 1024 - 2 * (1024 + sizeof(OwnPlan) + sizeof(Shared) + 64);
+constexpr uint32_t kAloneSmem = 227 * 1024 - sizeof(OwnPlan) - sizeof(Shared) - 64;
 constexpr uint32_t kBesideInner = 1024 + 3 * (2 * kTile + 32 * 128);
 constexpr uint32_t kBesideInner64 = 1024 + 2 * (2 * kTile + 64 * 128);
 
@@ -714,10 +763,11 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
            : l.tokens <= 8 ? 8 : l.tokens <= 16 ? 16 : 32;
   const bool rows = a.x.cs == 1 || a.k == 1;
   const int x_align = alignment(a.x.ptr, 0, 1, a.x.rs, a.m, a.k);
-  l.planned = !l.direct || choices > kDirectUnplanned || l.tokens > 8 || !rows;
+  l.planned = l.direct ? choices > kDirectUnplanned || l.tokens > 8 || !rows
+                       : choices > kOwnChoices || !copied(a.x, a.m, a.k);
   l.pack = !l.nothing && (l.direct ? l.planned && (!rows || x_align < 16) : !copied(a.x, a.m, a.k));
   l.chunks = (a.experts < choices ? a.experts : choices) + choices / l.cols;
-  l.places = l.planned ? choices + 3 * l.chunks : 8 * l.chunks;
+  l.places = l.direct && !l.planned ? 8 * l.chunks : choices;
   l.ld = round_up(a.f, 64);
   l.packed_ld = round_up(a.k, 64);
   uint64_t used = 0;
@@ -767,8 +817,8 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
       ring(p, 2, 0, l.cols <= 32 ? kBesideInner : kBesideInner64);
       ring(q, 1, (uint32_t)l.tokens * 512u, kBesideAll - p.smem);
     } else {
-      ring(p, 2, 0, kTcSmem);
-      ring(q, 1, (uint32_t)l.tokens * 512u, kTcSmem);
+      ring(p, 2, 0, kAloneSmem);
+      ring(q, 1, (uint32_t)l.tokens * 512u, kAloneSmem);
     }
     const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
     part = 2 * kSms * (inner > outer ? inner : outer);
@@ -818,10 +868,10 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   if (l.pack)
     s.packed = reinterpret_cast<uint16_t *>(take((uint64_t)l.tokens * l.packed_ld * 2));
   s.packed_ld = l.packed_ld;
-  s.top = (int32_t)a.top;
-  s.experts = (int32_t)a.experts;
-  s.first = (int32_t)a.first;
-  s.cols = l.cols;
+  s.choices.top = (int32_t)a.top;
+  s.choices.experts = (int32_t)a.experts;
+  s.choices.first = (int32_t)a.first;
+  s.choices.cols = l.cols;
   s.k = a.k;
   s.out = p.plan = q.plan = d.plan = e.plan = o;
   p.out = h;
@@ -843,7 +893,7 @@ int64_t need(const coll_experts_t &a) {
 template <bool INNER>
 int set_up() {
   static DenseSmemLimit limit;
-  return limit((const void *)product_kernel<INNER>, kTcSmem) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  return limit((const void *)product_kernel<INNER>, kAloneSmem) == cudaSuccess ? COLL_OK : COLL_ECUDA;
 }
 
 template <bool INNER>
@@ -884,10 +934,12 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
   for (int64_t t = 0; t < a.m; t += l.tokens) {
     const int64_t tokens = a.m - t < l.tokens ? a.m - t : l.tokens;
     PlanParams &o = l.plan;
-    o.ids = DenseMat{static_cast<const int32_t *>(a.ids.ptr) + t * a.ids.rs, a.ids.rs, a.ids.cs};
-    o.weights = DenseMat{static_cast<const float *>(a.weights.ptr) + t * a.weights.rs,
-                         a.weights.rs, a.weights.cs};
-    o.tokens = p.tokens = q.tokens = d.tokens = e.tokens = (int32_t)tokens;
+    Choices &ch = o.choices;
+    ch.ids = DenseMat{static_cast<const int32_t *>(a.ids.ptr) + t * a.ids.rs, a.ids.rs, a.ids.cs};
+    ch.weights = DenseMat{static_cast<const float *>(a.weights.ptr) + t * a.weights.rs,
+                          a.weights.rs, a.weights.cs};
+    ch.tokens = p.tokens = q.tokens = d.tokens = e.tokens = (int32_t)tokens;
+    p.choices = q.choices = ch;
     const uint16_t *x = static_cast<const uint16_t *>(a.x.ptr) + t * a.x.rs;
     if (l.pack) o.x = DenseMat{x, a.x.rs, a.x.cs};
     else if (!l.direct && t && !l.nothing)
@@ -906,8 +958,8 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
       err = dense_launch(plan_kernel, dim3(1 + more), threads, 0, 1, s, o);
     }
     if (l.direct) {
-      d.ids = e.ids = o.ids;
-      d.weights = e.weights = o.weights;
+      d.ids = e.ids = ch.ids;
+      d.weights = e.weights = ch.weights;
       d.x = l.pack ? o.packed : x;
       d.x_ld = l.pack ? l.packed_ld : a.x.rs;
       e.y = y;

@@ -10,8 +10,7 @@ constexpr int kChosenMost = 32;     // choices of a token
 constexpr int kExpertsGroup = 128;  // tokens that a launch takes
 
 // The choices sorted by expert, in chunks of at most so many of one expert; each choice's token and
-// weight in the order of the chunks. A chunk's choices start on a multiple of four, so that four of
-// their tokens are one load.
+// weight in the order of the chunks.
 struct ExpertsPlan {
   int32_t *chunks;   // their number
   int4 *chunk;       // {expert, first place, choices, 0}
