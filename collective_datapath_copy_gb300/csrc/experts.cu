@@ -103,7 +103,8 @@ __device__ __forceinline__ int make_plan(const Choices &p, int4 *chunk, int32_t 
     if (e < p.experts) base[e] = first;
     const int q0 = (int)(first >> 16), s0 = (int)(first & 0xFFFFu);
     for (int q = 0; q < chunks; ++q)
-      chunk[q0 + q] = make_int4(e, s0 + q * p.cols, min(p.cols, c - q * p.cols), 0);
+      chunk[q0 + q] =
+          make_int4(e, s0 + q * p.cols, min(p.cols, c - q * p.cols), q0 | chunks << 16);
   }
   __syncthreads();
 #pragma unroll
@@ -284,21 +285,24 @@ struct Piece {
   int chunk, tile, k0, k1;
 };
 
-// INNER walks chunk by chunk, tile after tile: all of an expert's rows. The sums walk tile by tile,
-// chunk after chunk, so that one tile's sums over the experts stay in the CTA.
+// INNER walks expert by expert, tile after tile, and in a tile the expert's chunks. The sums walk tile
+// by tile, chunk after chunk, so that one tile's sums over the experts stay in the CTA. Either way an
+// expert's chunks read the same weights one right after the other.
 template <bool INNER>
-__device__ __forceinline__ Piece piece_at(const ProductParams &p, int chunks, uint32_t u,
+__device__ __forceinline__ Piece piece_at(const ProductParams &p, const PlanView &plan, uint32_t u,
                                           uint32_t end) {
   const uint32_t item = u / (uint32_t)p.kblocks;
   Piece q;
   q.k0 = (int)(u - item * (uint32_t)p.kblocks);
   q.k1 = (int)min((uint32_t)p.kblocks, q.k0 + (end - u));
   if (INNER) {
-    q.chunk = (int)(item / (uint32_t)p.tiles);
-    q.tile = (int)(item - (uint32_t)q.chunk * p.tiles);
+    const uint32_t c = item / (uint32_t)p.tiles, w = (uint32_t)plan.chunk[c].w;
+    const uint32_t first = w & 0xFFFFu, count = w >> 16, r = item - first * p.tiles;
+    q.tile = (int)(r / count);
+    q.chunk = (int)(first + r - (uint32_t)q.tile * count);
   } else {
-    q.tile = (int)(item / (uint32_t)chunks);
-    q.chunk = (int)(item - (uint32_t)q.tile * chunks);
+    q.tile = (int)(item / (uint32_t)plan.chunks);
+    q.chunk = (int)(item - (uint32_t)q.tile * plan.chunks);
   }
   return q;
 }
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_box3(at + w * kTile, &p.w[w], kb * kTileK, q.tile * p.rows, c.x, bar);
     };
     for (uint32_t v = u; v < end && early < stages;) {
-      const Piece q = piece_at<INNER>(p, chunks, v, end);
+      const Piece q = piece_at<INNER>(p, plan, v, end);
       const int4 c = plan.chunk[q.chunk];
       for (int kb = q.k0; kb < q.k1 && early < stages; ++kb) {
         if (elect_one()) weights(q, c, kb);
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     s = 0;
     if (!INNER) griddep_wait();
     while (u < end) {
-      const Piece q = piece_at<INNER>(p, chunks, u, end);
+      const Piece q = piece_at<INNER>(p, plan, u, end);
       const int4 c = plan.chunk[q.chunk];
       const int fours = (c.z + 3) / 4, sixteens = (c.z + 15) / 16;
       int4 tok = make_int4(0, 0, 0, 0);
@@ -429,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t s = 0, phase = 0, d = 0, dphase = 0;
     bool ok = true;
     while (u < end) {
-      const Piece q = piece_at<INNER>(p, chunks, u, end);
+      const Piece q = piece_at<INNER>(p, plan, u, end);
       const uint32_t n = (uint32_t)(plan.chunk[q.chunk].z + 15) & ~15u;
       const uint32_t idesc = mma_desc(p.type == COLL_BF16, false, false, 128, n);
       const uint32_t d0 = tmem + d * W * p.cols, d1 = d0 + p.cols;
@@ -491,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!INNER)
         for (int i = 0; i < p.tokens; ++i) sums[i * 128] = 0.0f;
       while (u < job_end) {
-        const Piece q = piece_at<INNER>(p, chunks, u, job_end);
+        const Piece q = piece_at<INNER>(p, plan, u, job_end);
         const int4 c = plan.chunk[q.chunk];
         const int f = q.tile * p.rows + row;
         const bool live = row < p.rows && f < p.features;
@@ -567,58 +571,58 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The shares of cut tiles, in order of the line: inner values are finished, sums get the residual. A
 // launch of its own (about 2.5 us), because the last CTA to arrive would do it with one SM's loads in
-// flight, and after a fence and an atomic: 5 us a tile, and a CTA can have two.
-constexpr int kJoinRows = 16;
+// flight, and after a fence and an atomic: 5 us a tile, and a CTA can have two. Inner values: a CTA for
+// every CTA of the line, which takes the tile that one began last. Sums: a CTA for every tile and
+// eight tokens.
+constexpr int kJoinTokens = 8;
 
 template <bool INNER>
 __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ ProductParams p) {
   __shared__ OwnPlan own;
   griddep_launch();
-  const PlanView plan = view_plan<1>(p, own);
+  const PlanView plan = view_plan<kOwnChoices / 256>(p, own);
   const int chunks = plan.chunks;
   const Line line = line_of(p, chunks);
-  const uint32_t cta = blockIdx.x;
   const uint32_t step = INNER ? (uint32_t)p.kblocks : (uint32_t)p.kblocks * (uint32_t)chunks;
-  uint32_t job = 0, c1 = 0;
-  bool cut = false;
-  if (cta < line.ctas) {  // the tile that this CTA of the line began last
-    job = (line.begin(cta + 1) - 1) / step;
+  uint32_t job = 0, c0 = 0, c1 = 0;
+  if (INNER ? blockIdx.x < line.ctas : chunks > 0) {
+    job = INNER ? (line.begin(blockIdx.x + 1) - 1) / step : blockIdx.x;
+    c0 = line.owner(job * step);
     c1 = line.owner(job * step + step - 1);
-    cut = line.owner(job * step) == cta && c1 > cta;
   }
-  const int row = threadIdx.x & 127, group = threadIdx.x >> 7;
+  const bool cut = c1 > c0 && (!INNER || c0 == blockIdx.x);
   Piece q = {};
   int4 c = make_int4(0, 0, 0, 0);
   if (cut) {
-    q = piece_at<INNER>(p, chunks, job * step, line.all);
+    q = piece_at<INNER>(p, plan, job * step, line.all);
     if (INNER) c = plan.chunk[q.chunk];
   }
   griddep_wait();
-  if (!cut) return;
+  const int row = threadIdx.x & 127, groups = blockDim.x >> 7;
   const int f = q.tile * p.rows + row;
-  if (row >= p.rows || f >= p.features) return;
-  const int all = INNER ? c.z : p.tokens;
-  for (int i0 = (int)blockIdx.y * kJoinRows + group; i0 < all;
-       i0 += (int)gridDim.y * kJoinRows) {
-    constexpr int R = kJoinRows / 4;
+  if (!cut || row >= p.rows || f >= p.features) return;
+  constexpr int R = 4;
+  const int end = INNER ? c.z : min(p.tokens, ((int)blockIdx.y + 1) * kJoinTokens);
+  for (int i0 = (INNER ? 0 : (int)blockIdx.y * kJoinTokens) + (threadIdx.x >> 7); i0 < end;
+       i0 += R * groups) {
     float v[R], u[R];
 #pragma unroll
     for (int i = 0; i < R; ++i) v[i] = u[i] = 0.0f;
 #pragma unroll 4
-    for (uint32_t w = cta; w <= c1; ++w) {
-      const float *o = share_of<INNER>(p, w, cta) + i0 * 128 + row;
+    for (uint32_t w = c0; w <= c1; ++w) {
+      const float *o = share_of<INNER>(p, w, c0) + i0 * 128 + row;
 #pragma unroll
       for (int i = 0; i < R; ++i)
-        if (i0 + 4 * i < all) {
-          v[i] += __ldcg(o + 4 * i * 128);
-          if (INNER) u[i] += __ldcg(o + (p.cols + 4 * i) * 128);
+        if (i0 + groups * i < end) {
+          v[i] += __ldcg(o + groups * i * 128);
+          if (INNER) u[i] += __ldcg(o + (p.cols + groups * i) * 128);
         }
     }
     if constexpr (INNER) act_run(v, p.act);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
-      const int64_t t = i0 + 4 * i;
-      if (t >= all) break;
+      const int64_t t = i0 + groups * i;
+      if (t >= end) break;
       if constexpr (INNER) {
         static_cast<uint16_t *>(p.out)[(c.y + t) * p.out_rs + f] = f2h(v[i] * u[i], p.type);
       } else {
@@ -759,7 +763,9 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
              (l.tokens <= kDirectTokens ||
               !(copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f) &&
                 copied(a.w_down, a.experts, a.n)));
-  l.cols = !l.direct ? (l.tokens <= 32 ? (int32_t)round_up(l.tokens, 16) : l.tokens <= 64 ? 64 : 128)
+  // columns of a chunk: all tokens, or 32 where the experts have fewer than half as many each
+  const bool spread = choices <= 16 * a.experts;
+  l.cols = !l.direct ? (l.tokens <= 16 ? 16 : l.tokens <= 32 || spread ? 32 : l.tokens <= 64 ? 64 : 128)
            : l.tokens <= 8 ? 8 : l.tokens <= 16 ? 16 : 32;
   const bool rows = a.x.cs == 1 || a.k == 1;
   const int x_align = alignment(a.x.ptr, 0, 1, a.x.rs, a.m, a.k);
@@ -901,9 +907,8 @@ cudaError_t launch(const ProductParams &p, cudaStream_t s) {
   const cudaError_t e =
       dense_launch(product_kernel<INNER>, dim3(kSms), kThreads, p.smem, 1, s, p);
   if (e != cudaSuccess || p.nothing) return e;
-  // beside each other on an SM: these wait there while the products run
-  const int64_t turns = ceil_div(INNER ? p.cols : p.tokens, kJoinRows);
-  return dense_launch(join_kernel<INNER>, dim3(kSms, turns < 2 ? 1 : 2), 512, 0, 1, s, p);
+  const dim3 grid = INNER ? dim3(kSms) : dim3(p.tiles, (unsigned)ceil_div(p.tokens, kJoinTokens));
+  return dense_launch(join_kernel<INNER>, grid, INNER ? 512 : 256, 0, 1, s, p);
 }
 
 int run(const coll_experts_t &a, char *base, cudaStream_t s) {
