@@ -7,7 +7,10 @@
 //               a = l (softmax) or log s (sigmoid), so that no sum of tiny scores vanishes
 //
 // A warp takes a token. Its logits stay in registers, as keys whose unsigned order is that of the
-// numbers; choosing is by the keys alone, so it depends on no computed score.
+// numbers; choosing is by the keys alone, so it depends on no computed score. Bound by the warps'
+// instructions as much as by HBM, so for many experts the chosen are not taken one by one: the k-th
+// largest of the lanes' largest keys is passed by at least k keys and by few more, which a lane each
+// then ranks.
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -79,49 +82,173 @@ __device__ __forceinline__ float normalised(float l, bool there, int score) {
   return there ? x / warp_sum(x) : (warp_sum(x), 0.0f);
 }
 
-// Expert i * 32 + lane in v[i].
-template <int V>
-__device__ __forceinline__ void load_row(const RouteParams &p, int64_t row, int lane,
-                                         float (&v)[V]) {
-  const int64_t at = row * p.logits.rs + (int64_t)lane * p.logits.cs;
+// How a row lies over a warp: lane l holds runs of L neighbouring logits, V / L of them. VEC: the runs
+// are one load each, up to 16 bytes; else L is 1.
+template <int V, int TYPE, bool VEC>
+struct Row {
+  static constexpr int kSize = TYPE == COLL_F32 ? 4 : 2;
+  static constexpr int L = !VEC ? 1 : V < 16 / kSize ? V : 16 / kSize;
+  static __device__ __forceinline__ int index(int i, int lane) {
+    return (i / L * 32 + lane) * L + i % L;
+  }
+  // -inf past the end
+  static __device__ __forceinline__ void load(const RouteParams &p, int64_t row, int lane,
+                                              float (&v)[V]) {
+    const char *base = static_cast<const char *>(p.logits.p) + row * p.logits.rs * kSize;
+    constexpr int kWords = L * kSize >= 4 ? L * kSize / 4 : 1;
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    v[i] = i * 32 + lane < p.e ? ld_elem(p.logits.p, at + (int64_t)(i * 32) * p.logits.cs, p.type)
-                               : -INFINITY;
-}
+    for (int i = 0; i < V; i += L) {
+      const int e = index(i, lane);
+      if constexpr (L * kSize < 4 || !VEC) {
+        v[i] = e < p.e ? ld_elem(base, (int64_t)e * p.logits.cs, TYPE) : -INFINITY;
+      } else {
+        uint32_t w[kWords];
+        const char *q = base + e * kSize;
+        if (e < p.e) {
+          if constexpr (kWords == 4) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(q);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+          } else if constexpr (kWords == 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(q);
+            w[0] = x.x, w[1] = x.y;
+          } else {
+            w[0] = *reinterpret_cast<const uint32_t *>(q);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < L; ++j) {
+          const float x = TYPE == COLL_F32 ? __uint_as_float(w[j])
+                                           : h2f((uint16_t)(w[j / 2] >> (16 * (j & 1))), TYPE);
+          v[i + j] = e < p.e ? x : -INFINITY;
+        }
+      }
+    }
+  }
+  static __device__ __forceinline__ void store(const RouteParams &p, int64_t row, int lane,
+                                               const float (&v)[V]) {
+    char *base = static_cast<char *>(p.dlogits) + row * p.dl_rs * kSize;
+    constexpr int kWords = L * kSize >= 4 ? L * kSize / 4 : 1;
+#pragma unroll
+    for (int i = 0; i < V; i += L) {
+      const int e = index(i, lane);
+      if (e >= p.e) continue;
+      if constexpr (L * kSize < 4 || !VEC) {
+        st_elem(base, e, v[i], TYPE);
+      } else {
+        uint32_t w[kWords];
+#pragma unroll
+        for (int j = 0; j < kWords; ++j)
+          w[j] = TYPE == COLL_F32 ? __float_as_uint(v[i + j])
+                                  : f2h2(v[i + 2 * j], v[i + (2 * j + 1) % V], TYPE);
+        char *q = base + e * kSize;
+        if constexpr (kWords == 4)
+          *reinterpret_cast<uint4 *>(q) = make_uint4(w[0], w[1], w[2], w[3]);
+        else if constexpr (kWords == 2) *reinterpret_cast<uint2 *>(q) = make_uint2(w[0], w[1]);
+        else *reinterpret_cast<uint32_t *>(q) = w[0];
+      }
+    }
+  }
+};
 
-template <int V>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  griddep_launch();
-  griddep_wait();
-  if (row >= p.t) return;
-  float v[V];
-  load_row<V>(p, row, lane, v);
-  uint32_t key[V];
-#pragma unroll
-  for (int i = 0; i < V; ++i) key[i] = order_key(v[i]);
-  float chosen = -INFINITY;
-  int id = -1;
-  for (int j = 0; j < p.top; ++j) {
+// One round for each choice: the largest key, of equal ones that of the lowest index. Lane j gets the
+// j-th.
+template <typename R, int V>
+__device__ __forceinline__ void choose_in_turn(int top, int lane, uint32_t (&key)[V], int &id,
+                                               float &chosen) {
+  for (int j = 0; j < top; ++j) {
     uint32_t best = 0u;
     int at = 0;
 #pragma unroll
     for (int i = V - 1; i >= 0; --i)
-      if (key[i] >= best) best = key[i], at = i;
+      if (key[i] >= best) best = key[i], at = R::index(i, lane);
     const uint32_t most = __reduce_max_sync(~0u, best);
     if (most == 0u) break;
-    const uint32_t first =
-        __reduce_min_sync(~0u, best == most ? (uint32_t)(at * 32 + lane) : ~0u);
+    const uint32_t first = __reduce_min_sync(~0u, best == most ? (uint32_t)at : ~0u);
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if ((uint32_t)(i * 32 + lane) == first) key[i] = 0u;
+      if ((uint32_t)R::index(i, lane) == first) key[i] = 0u;
     if (lane == j) {
       id = (int)first;
       chosen = key_value(most);
     }
   }
+}
+
+// The same by rank among the keys that reach the top-th largest of the lanes' own largest: all that
+// are chosen, and few more. `mine`: 32 places of this warp. False where there are more than 32.
+template <typename R, int V>
+__device__ __forceinline__ bool choose_by_rank(int top, int lane, const uint32_t (&key)[V],
+                                               uint2 *mine, int &id, float &chosen) {
+  uint32_t best = key[0];
+#pragma unroll
+  for (int i = 1; i < V; ++i) best = max(best, key[i]);
+  uint32_t least = 1u;
+  for (int n = 0; n < top;) {
+    const uint32_t most = __reduce_max_sync(~0u, best);
+    if (most == 0u) {  // fewer lanes than choices have any left: every key is wanted
+      least = 1u;
+      break;
+    }
+    least = most;
+    n += __popc(__ballot_sync(~0u, best == most));
+    if (best == most) best = 0u;
+  }
+  int n = 0;
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const bool in = key[i] >= least;
+    const uint32_t who = __ballot_sync(~0u, in);
+    const int at = n + __popc(who & below);
+    if (in && at < 32) mine[at] = make_uint2(key[i], (uint32_t)R::index(i, lane));
+    n += __popc(who);
+  }
+  if (n > 32) return false;
+  __syncwarp();
+  const uint2 own = lane < n ? mine[lane] : make_uint2(0u, 0u);
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const uint2 o = mine[j];
+    rank += o.x > own.x || (o.x == own.x && o.y < own.y);
+  }
+  __syncwarp();
+  if (lane < n && rank < top) mine[rank] = own;
+  __syncwarp();
+  if (lane < top && lane < n) {
+    id = (int)mine[lane].y;
+    chosen = key_value(mine[lane].x);
+  }
+  return true;
+}
+
+template <int V, int TYPE, bool VEC>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p) {
+  using R = Row<V, TYPE, VEC>;
+  __shared__ uint2 places[kWarps][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
+  griddep_launch();
+  griddep_wait();
+  if (row >= p.t) return;
+  float v[V];
+  R::load(p, row, lane, v);
+  uint32_t key[V];
+  bool odd = false;  // NaN or an infinity among the logits
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t u = __float_as_uint(v[i] + 0.0f);
+    const bool there = R::index(i, lane) < p.e;
+    key[i] = there ? u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u) : 0u;
+    odd = odd || (there && !(fabsf(v[i]) < INFINITY));
+  }
+  if (__any_sync(~0u, odd)) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = order_key(v[i]);
+  }
+  float chosen = -INFINITY;
+  int id = -1;
+  if (V <= 2 || !choose_by_rank<R, V>(p.top, lane, key, places[warp], id, chosen))
+    choose_in_turn<R, V>(p.top, lane, key, id, chosen);
   const bool there = id >= 0;
   float w;
   if (p.norm) {
@@ -145,9 +272,11 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p)
 //   normalised softmax  dl_j = w_j (g_j - sum g w);      sigmoid, normalised  the same times 1 - s_j
 //   softmax             dl_e = p_e ([e chosen] g_e - sum g p);        sigmoid  dl_j = g_j s_j (1 - s_j)
 // 1 - s is the sigmoid of -l. Logits not chosen get 0 but for the plain softmax. Chosen twice, an
-// expert gets both gradients (and a normalised weight for each).
-template <int V>
+// expert gets both gradients (and a normalised weight for each). The row is written whole as if
+// nothing were chosen, then the chosen logits' lanes write theirs over it.
+template <int V, int TYPE, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParams p) {
+  using R = Row<V, TYPE, VEC>;
   const int lane = threadIdx.x & 31;
   const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
   griddep_launch();
@@ -155,13 +284,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
   if (row >= p.t) return;
   int id = -1;
   float g = 0.0f, l = -INFINITY;
+  const bool plain = !p.norm && p.score == COLL_SCORE_SOFTMAX;
   if (lane < p.top) {
     id = p.ids[row * p.ids_rs + lane * p.ids_cs];
     g = p.weights[row * p.w_rs + lane * p.w_cs] * p.scale;
   }
+  float v[V], d, rest = 0.0f;  // rest: what an expert gets beside its own gradients
+  if (plain) R::load(p, row, lane, v);
   const bool there = (uint32_t)id < (uint32_t)p.e;
-  if (there) l = ld_elem(p.logits.p, row * p.logits.rs + id * p.logits.cs, p.type);
-  float v[V], d;
+  if (there) l = ld_elem(p.logits.p, row * p.logits.rs + id * p.logits.cs, TYPE);
   if (p.norm) {
     const float w = normalised(l, there, p.score);
     const float sum = warp_sum(there ? g * w : 0.0f);
@@ -170,7 +301,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
   } else if (p.score == COLL_SCORE_SIGMOID) {
     d = g * sigmoid(l) * sigmoid(-l);
   } else {
-    load_row<V>(p, row, lane, v);
     float most = v[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) most = v[i] > most || v[i] != v[i] ? v[i] : most;
@@ -183,40 +313,70 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
     }
     sum = warp_sum(sum);
     const float r = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    d = there && most != -INFINITY ? expf(l - most) * r * g : 0.0f;
+    const float own = there && most != -INFINITY ? expf(l - most) * r : 0.0f;
+    d = own * g;
     const float all = warp_sum(d);
+    rest = -all * own;
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] *= -all * r;
   }
-  if (p.norm || p.score == COLL_SCORE_SIGMOID) {
+  if (!plain) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = 0.0f;
   }
-  if (!there) d = 0.0f;
-  for (int j = 0; j < p.top; ++j) {
-    const int e = __shfl_sync(~0u, id, j);
-    const float x = __shfl_sync(~0u, d, j);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (i * 32 + lane == e) v[i] += x;
+  R::store(p, row, lane, v);
+  if (!there) {
+    d = 0.0f;
+    id = -1;
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (i * 32 + lane < p.e) st_elem(p.dlogits, row * p.dl_rs + i * 32 + lane, v[i], p.type);
+  // an expert that was chosen more than once: its first lane adds the others' up, in order
+  const uint32_t same = __match_any_sync(~0u, id);
+  const bool first = there && __ffs(same) - 1 == lane;
+  float sum = d;
+  if (__any_sync(~0u, first && __popc(same) > 1)) {
+    for (int j = 0; j < p.top; ++j) {
+      const float x = __shfl_sync(~0u, d, j);
+      if (first && j > lane && (same >> j & 1u)) sum += x;
+    }
+  }
+  __syncwarp();
+  if (first) st_elem(p.dlogits, row * p.dl_rs + id, sum + rest, TYPE);
 }
 
-template <bool BWD>
+template <bool BWD, int TYPE, bool VEC>
 cudaError_t launch(const RouteParams &p, cudaStream_t s) {
   const dim3 grid((unsigned)((p.t + kWarps - 1) / kWarps));
-#define COLL_ROUTE(V)                                                                        \
-  return BWD ? dense_launch(route_bwd_kernel<V>, grid, kWarps * 32, 0, 1, s, p) \
-             : dense_launch(route_kernel<V>, grid, kWarps * 32, 0, 1, s, p)
+#define COLL_ROUTE(V)                                                                           \
+  return BWD ? dense_launch(route_bwd_kernel<V, TYPE, VEC>, grid, kWarps * 32, 0, 1, s, p)      \
+             : dense_launch(route_kernel<V, TYPE, VEC>, grid, kWarps * 32, 0, 1, s, p)
   if (p.e <= 32) COLL_ROUTE(1);
   if (p.e <= 64) COLL_ROUTE(2);
   if (p.e <= 128) COLL_ROUTE(4);
   if (p.e <= 256) COLL_ROUTE(8);
   if (p.e <= 512) COLL_ROUTE(16);
   COLL_ROUTE(32);
+#undef COLL_ROUTE
+}
+
+// Do rows lie so that every lane's runs are whole loads (and stores)? Runs are of at most 16 bytes
+// and V elements.
+bool whole_runs(const RouteParams &p, bool bwd) {
+  const int size = esize(p.type), v = p.e <= 32 ? 1 : p.e <= 64 ? 2 : p.e <= 128 ? 4 : 8;
+  const int run = v * size < 16 ? v * size : 16;
+  auto fits = [&](const void *q, int64_t rs) {
+    return ((uintptr_t)q | (p.t > 1 ? (uint64_t)(rs * size) : 0)) % run == 0;
+  };
+  return run >= 4 && p.e * size % run == 0 && p.logits.cs == 1 && fits(p.logits.p, p.logits.rs) &&
+         (!bwd || fits(p.dlogits, p.dl_rs));
+}
+
+template <bool BWD>
+cudaError_t launch(const RouteParams &p, cudaStream_t s) {
+  const bool vec = whole_runs(p, BWD);
+#define COLL_ROUTE(TYPE) return vec ? launch<BWD, TYPE, true>(p, s) : launch<BWD, TYPE, false>(p, s)
+  if (p.type == COLL_F32) COLL_ROUTE(COLL_F32);
+  if (p.type == COLL_BF16) COLL_ROUTE(COLL_BF16);
+  COLL_ROUTE(COLL_F16);
 #undef COLL_ROUTE
 }
 
