@@ -59,27 +59,42 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   return v;
 }
+// NaN only where every lane's is.
 __device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    const float w = __shfl_xor_sync(~0u, v, o);
-    v = w > v || w != w ? w : v;
-  }
-  return v;
+  float r;
+  asm("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
+
+// exp(d) for d <= 0, off by 2^-22 and d's rounding times log2 e, 2^-23 |d|: for sums and products over
+// all experts, a third of expf's instructions.
+__device__ __forceinline__ float exp_below(float d) { return exp2_fast(d * kLog2e); }
 
 __device__ __forceinline__ float log_sigmoid(float l) {
   return fminf(l, 0.0f) - log1pf(expf(-fabsf(l)));
 }
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
+// The sum over the first `top` lanes, which the others have to leave at 0, in those lanes.
+__device__ __forceinline__ float chosen_sum(float v, int top) {
+  if (top > 8) {
+    v += __shfl_xor_sync(~0u, v, 16);
+    v += __shfl_xor_sync(~0u, v, 8);
+  }
+#pragma unroll
+  for (int o = 4; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
+  return v;
+}
+
 // Normalised weights over the chosen logits, one in each of the first `top` lanes; `there`: a choice
-// was left for this lane.
-__device__ __forceinline__ float normalised(float l, bool there, int score) {
+// was left for this lane. SORTED: the largest is lane 0's.
+template <bool SORTED>
+__device__ __forceinline__ float normalised(float l, bool there, int top, int score) {
   const float a = score == COLL_SCORE_SIGMOID ? log_sigmoid(l) : l;
-  const float most = warp_max(there ? a : -INFINITY);
+  const float most = SORTED ? __shfl_sync(~0u, a, 0) : warp_max(there ? a : -INFINITY);
   const float x = there ? expf(a - most) : 0.0f;
-  return there ? x / warp_sum(x) : (warp_sum(x), 0.0f);
+  const float sum = chosen_sum(x, top);
+  return there ? x / sum : 0.0f;
 }
 
 // How a row lies over a warp: lane l holds runs of L neighbouring logits, V / L of them. VEC: the runs
@@ -182,89 +197,99 @@ __device__ __forceinline__ bool choose_by_rank(int top, int lane, const uint32_t
   uint32_t best = key[0];
 #pragma unroll
   for (int i = 1; i < V; ++i) best = max(best, key[i]);
-  uint32_t least = 1u;
-  for (int n = 0; n < top;) {
-    const uint32_t most = __reduce_max_sync(~0u, best);
-    if (most == 0u) {  // fewer lanes than choices have any left: every key is wanted
-      least = 1u;
-      break;
-    }
-    least = most;
-    n += __popc(__ballot_sync(~0u, best == most));
-    if (best == most) best = 0u;
+  // equal lanes go together, which only lowers what is left
+  uint32_t least = 0u;
+  for (int j = 0; j < top; ++j) {
+    least = __reduce_max_sync(~0u, best);
+    if (best == least) best = 0u;
   }
-  int n = 0;
-  const uint32_t below = (1u << lane) - 1u;
+  least = max(least, 1u);  // lanes ran out: every key is wanted
+  int count = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const bool in = key[i] >= least;
-    const uint32_t who = __ballot_sync(~0u, in);
-    const int at = n + __popc(who & below);
-    if (in && at < 32) mine[at] = make_uint2(key[i], (uint32_t)R::index(i, lane));
-    n += __popc(who);
+  for (int i = 0; i < V; ++i) count += key[i] >= least;
+  int at = count;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int c = __shfl_up_sync(~0u, at, o);
+    if (lane >= o) at += c;
   }
+  const int n = __shfl_sync(~0u, at, 31);
   if (n > 32) return false;
+  at -= count;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (key[i] >= least) mine[at++] = make_uint2(~(uint32_t)R::index(i, lane), key[i]);
+  if (lane >= n) mine[lane] = make_uint2(0u, 0u);
   __syncwarp();
-  const uint2 own = lane < n ? mine[lane] : make_uint2(0u, 0u);
+  // as one number: the key, then the lower index
+  const uint64_t *all = reinterpret_cast<const uint64_t *>(mine);
+  const uint64_t own = all[lane];
   int rank = 0;
-  for (int j = 0; j < n; ++j) {
-    const uint2 o = mine[j];
-    rank += o.x > own.x || (o.x == own.x && o.y < own.y);
+#pragma unroll 4
+  for (int j = 0; j < n; j += 2) {
+    const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(all + j);
+    rank += o.x > own;
+    rank += o.y > own;
   }
   __syncwarp();
-  if (lane < n && rank < top) mine[rank] = own;
+  if (lane < n && rank < top) reinterpret_cast<uint64_t *>(mine)[rank] = own;
   __syncwarp();
   if (lane < top && lane < n) {
-    id = (int)mine[lane].y;
-    chosen = key_value(mine[lane].x);
+    id = (int)~mine[lane].x;
+    chosen = key_value(mine[lane].y);
   }
+  __syncwarp();
   return true;
 }
 
 template <int V, int TYPE, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p) {
   using R = Row<V, TYPE, VEC>;
-  __shared__ uint2 places[kWarps][32];
+  __shared__ __align__(16) uint2 places[kWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
+  const int64_t step = (int64_t)gridDim.x * kWarps;
+  int64_t row = (int64_t)blockIdx.x * kWarps + warp;
   griddep_launch();
   griddep_wait();
-  if (row >= p.t) return;
-  float v[V];
-  R::load(p, row, lane, v);
-  uint32_t key[V];
-  bool odd = false;  // NaN or an infinity among the logits
+  float v[V], next[V];
+  if (row < p.t) R::load(p, row, lane, next);
+  for (; row < p.t; row += step) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const uint32_t u = __float_as_uint(v[i] + 0.0f);
-    const bool there = R::index(i, lane) < p.e;
-    key[i] = there ? u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u) : 0u;
-    odd = odd || (there && !(fabsf(v[i]) < INFINITY));
-  }
-  if (__any_sync(~0u, odd)) {
+    for (int i = 0; i < V; ++i) v[i] = next[i];
+    if (row + step < p.t) R::load(p, row + step, lane, next);
+    uint32_t key[V];
+    bool odd = false;  // NaN or an infinity among the logits
 #pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = order_key(v[i]);
-  }
-  float chosen = -INFINITY;
-  int id = -1;
-  if (V <= 2 || !choose_by_rank<R, V>(p.top, lane, key, places[warp], id, chosen))
-    choose_in_turn<R, V>(p.top, lane, key, id, chosen);
-  const bool there = id >= 0;
-  float w;
-  if (p.norm) {
-    w = normalised(chosen, there, p.score);
-  } else if (p.score == COLL_SCORE_SIGMOID) {
-    w = sigmoid(chosen);
-  } else {
-    const float most = __shfl_sync(~0u, chosen, 0);
-    float sum = 0.0f;
+    for (int i = 0; i < V; ++i) {
+      const uint32_t u = __float_as_uint(v[i] + 0.0f);
+      key[i] = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+      odd = odd || !(fabsf(v[i]) < INFINITY);
+    }
+    if (__any_sync(~0u, odd)) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += expf(v[i] - most);
-    w = expf(chosen - most) / warp_sum(sum);
-  }
-  if (lane < p.top) {
-    p.ids[row * p.ids_rs + lane * p.ids_cs] = id;
-    p.weights[row * p.w_rs + lane * p.w_cs] = there ? w * p.scale : 0.0f;
+      for (int i = 0; i < V; ++i) key[i] = order_key(v[i]);
+    }
+    float chosen = -INFINITY;
+    int id = -1;
+    if (V <= 2 || !choose_by_rank<R, V>(p.top, lane, key, places[warp], id, chosen))
+      choose_in_turn<R, V>(p.top, lane, key, id, chosen);
+    const bool there = id >= 0;
+    float w;
+    if (p.norm) {
+      w = normalised<true>(chosen, there, p.top, p.score);
+    } else if (p.score == COLL_SCORE_SIGMOID) {
+      w = sigmoid(chosen);
+    } else {
+      const float most = __shfl_sync(~0u, chosen, 0);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) sum += exp_below(v[i] - most);
+      w = expf(chosen - most) / warp_sum(sum);
+    }
+    if (lane < p.top) {
+      p.ids[row * p.ids_rs + lane * p.ids_cs] = id;
+      p.weights[row * p.w_rs + lane * p.w_cs] = there ? w * p.scale : 0.0f;
+    }
   }
 }
 
@@ -294,8 +319,8 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
   const bool there = (uint32_t)id < (uint32_t)p.e;
   if (there) l = ld_elem(p.logits.p, row * p.logits.rs + id * p.logits.cs, TYPE);
   if (p.norm) {
-    const float w = normalised(l, there, p.score);
-    const float sum = warp_sum(there ? g * w : 0.0f);
+    const float w = normalised<false>(l, there, p.top, p.score);
+    const float sum = chosen_sum(there ? g * w : 0.0f, p.top);
     d = w * (g - sum);
     if (p.score == COLL_SCORE_SIGMOID) d *= sigmoid(-l);
   } else if (p.score == COLL_SCORE_SIGMOID) {
@@ -303,22 +328,23 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
   } else {
     float most = v[0];
 #pragma unroll
-    for (int i = 1; i < V; ++i) most = v[i] > most || v[i] != v[i] ? v[i] : most;
+    for (int i = 1; i < V; ++i) most = fmaxf(most, v[i]);
     most = warp_max(most);
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      v[i] = most == -INFINITY ? 0.0f : expf(v[i] - most);
+      v[i] = exp_below(v[i] - most);
       sum += v[i];
     }
     sum = warp_sum(sum);
-    const float r = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-    const float own = there && most != -INFINITY ? expf(l - most) * r : 0.0f;
+    // a row of -inf has no probabilities, and no gradient
+    const float r = most == -INFINITY ? 0.0f : 1.0f / sum;
+    const float own = there ? (most == -INFINITY ? 0.0f : expf(l - most) * r) : 0.0f;
     d = own * g;
-    const float all = warp_sum(d);
+    const float all = __shfl_sync(~0u, chosen_sum(d, p.top), 0);
     rest = -all * own;
 #pragma unroll
-    for (int i = 0; i < V; ++i) v[i] *= -all * r;
+    for (int i = 0; i < V; ++i) v[i] = most == -INFINITY ? 0.0f : v[i] * (-all * r);
   }
   if (!plain) {
 #pragma unroll
@@ -345,7 +371,9 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
 
 template <bool BWD, int TYPE, bool VEC>
 cudaError_t launch(const RouteParams &p, cudaStream_t s) {
-  const dim3 grid((unsigned)((p.t + kWarps - 1) / kWarps));
+  // warps that stay, four rows each or more, ask for their next row ahead
+  const int64_t rows = (p.t + kWarps - 1) / kWarps;
+  const dim3 grid((unsigned)(BWD || rows <= 152 * 4 ? rows : rows <= 152 * 16 ? 152 * 4 : rows / 4));
 #define COLL_ROUTE(V)                                                                           \
   return BWD ? dense_launch(route_bwd_kernel<V, TYPE, VEC>, grid, kWarps * 32, 0, 1, s, p)      \
              : dense_launch(route_kernel<V, TYPE, VEC>, grid, kWarps * 32, 0, 1, s, p)
