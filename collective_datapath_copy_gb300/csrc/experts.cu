@@ -17,6 +17,7 @@
 
 #include "dense.h"
 #include "dense_check.h"
+#include "dense_direct.cuh"
 #include "dense_epi.cuh"
 #include "dense_tc.h"
 #include "experts.h"
@@ -157,6 +158,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
 // ---------------------------------------------------------------- products
 
 constexpr int kThreads = 192;  // warp 0 loads, 1 matrix instructions and TMEM, 2-5 epilogue
+constexpr int kLoaders = 16;   // more warps, where no tensor copy takes the weights as they lie
+template <bool COPY>
+constexpr int kAllThreads = kThreads + (COPY ? 0 : 32 * kLoaders);
 constexpr int kMaxStages = 12;
 constexpr uint32_t kTile = 128 * 128;  // bytes of 128 rows of one k block
 constexpr uint32_t kShort = 8;
@@ -174,9 +178,13 @@ struct ProductParams {
   int32_t features;     // of the product
   int32_t tiles, kblocks, cols, tokens;
   int32_t stages;
-  uint32_t stage_bytes, ring, smem;
+  uint32_t stage_bytes, ring, raw, smem;  // raw: where the loader warps' rings start
   int32_t type, out_type, act;
   int32_t nothing;      // sums of nothing: y = residual
+  const uint16_t *stack[2];  // weights that loader warps bring, with their extent
+  int64_t es[2], rs[2];
+  uintptr_t stack_end[2];
+  int32_t len;               // elements of a row of them
 };
 
 // A plan of few choices, made by every CTA that goes by it: no launch and no way through memory
@@ -307,6 +315,170 @@ __device__ __forceinline__ Piece piece_at(const ProductParams &p, const PlanView
   return q;
 }
 
+// Loader warps: the weights of this CTA's k blocks from rows that start anywhere, into the layout that a
+// tensor copy with a 128-byte swizzle gives. The nine aligned 16-byte words around a row's 128 bytes are
+// copied asynchronously into a ring of the warp's own, kRaw k blocks ahead (loads into registers kept
+// too little on its way: 2.1 TB/s), and from there a lane shifts two into the 16 bytes it stores.
+template <bool INNER>
+constexpr int kRaw = INNER ? 2 : 3;
+template <bool INNER>
+constexpr int kLoaderRows = (INNER ? 2 : 1) * 128 / kLoaders;
+constexpr int kRawRow = 144;  // bytes
+template <bool INNER>
+constexpr uint32_t kRawBytes = kLoaders * kLoaderRows<INNER> * kRawRow * kRaw<INNER>;
+
+// The aligned 16-byte word at `from` to shared memory: those of its bytes that are [lo, hi), and zeros.
+__device__ __forceinline__ void copy_word(uint32_t to, uintptr_t from, uintptr_t lo, uintptr_t hi) {
+  if (from >= lo) {
+    const uint32_t bytes = from + 16 <= hi ? 16u : from < hi ? (uint32_t)(hi - from) : 0u;
+    if (bytes)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(bytes)
+                   : "memory");
+    return;
+  }
+#pragma unroll 1
+  for (uint32_t j = 0; j < 16; j += 2) {
+    const uint16_t x = from + j >= lo && from + j < hi ? (uint16_t)ld_word2((const void *)(from + j))
+                                                       : (uint16_t)0;
+    asm volatile("st.shared.b16 [%0], %1;" ::"r"(to + j), "h"(x) : "memory");
+  }
+}
+
+template <bool INNER>
+__device__ __forceinline__ void load_weights(const ProductParams &p, const PlanView &plan,
+                                             uint32_t u, uint32_t end, uint32_t ring,
+                                             uint32_t raw, uint32_t full0, uint32_t empty0,
+                                             Shared &sh, int loader, int lane) {
+  constexpr int ROWS = kLoaderRows<INNER>, STEPS = ROWS / 4, DEPTH = kRaw<INNER>;
+  constexpr int WORDS = (ROWS * 9 + 31) / 32;
+  const int w = INNER ? loader / (kLoaders / 2) : 0;
+  const int first = loader * ROWS & 127;  // of this warp's rows in a tile
+  const int sub = lane >> 3, chunk = lane & 7;
+  const uintptr_t lo = (uintptr_t)p.stack[w], hi = p.stack_end[w];
+  const int64_t pitch = p.rs[w] * 2;
+  raw += loader * ROWS * kRawRow * DEPTH;
+  // Two places on this CTA's length, `ahead` DEPTH k blocks before `now`. All that does not change
+  // from one k block of a tile to the next is made once.
+  struct Place {
+    uint32_t v;
+    int kb, kb1, rows;
+    uintptr_t tile;
+  } ahead = {u, 0, 0, 0, 0}, now = {u, 0, 0, 0, 0};
+  auto begin = [&](Place &c) {
+    const Piece q = piece_at<INNER>(p, plan, c.v, end);
+    c.kb = q.k0, c.kb1 = q.k1;
+    c.v += q.k1 - q.k0;
+    const int f = q.tile * p.rows;
+    c.rows = min(p.rows, p.features - f) - first;  // of this warp's that are the tile's
+    c.tile = lo + (uintptr_t)(plan.chunk[q.chunk].x * p.es[w] + (int64_t)(f + first) * p.rs[w]) * 2;
+  };
+  uintptr_t word[WORDS];  // this lane's words of the k block ahead
+  bool inside = false;    // all of the warp's words of these k blocks are the stack's
+  auto begin_ahead = [&]() {
+    if (ahead.v >= end) return;
+    begin(ahead);
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      const int row = (i * 32 + lane) / 9;
+      word[i] = ((ahead.tile + row * pitch) & ~(uintptr_t)15) + ahead.kb * (2 * kTileK) +
+                (i * 32 + lane - 9 * row) * 16;
+    }
+    const uintptr_t last = ahead.tile + (min(ROWS, max(ahead.rows, 1)) - 1) * pitch;
+    inside = (ahead.tile & ~(uintptr_t)15) >= lo &&
+             (last & ~(uintptr_t)15) + ahead.kb1 * (2 * kTileK) + 16 <= hi;
+  };
+  auto ask = [&](uint32_t slot) {
+    const uint32_t to = raw + slot * (ROWS * kRawRow);
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) {
+      const int at = i * 32 + lane, row = at / 9;  // rows of nine words, one behind the other
+      if (row < min(ROWS, ahead.rows)) {
+        if (inside)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + at * 16),
+                       "l"(word[i])
+                       : "memory");
+        else
+          copy_word(to + at * 16, word[i], lo, hi);
+      }
+      word[i] += 2 * kTileK;
+    }
+    if (++ahead.kb == ahead.kb1) begin_ahead();
+  };
+  uint32_t shift[STEPS];  // bytes, of this lane's rows
+  auto begin_now = [&]() {
+    if (now.v >= end) return;
+    begin(now);
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j)
+      shift[j] = ((uint32_t)now.tile + (uint32_t)(4 * j + sub) * (uint32_t)pitch) & 15u;
+  };
+  const uint32_t n = end - u;
+  begin_ahead();
+  begin_now();
+#pragma unroll
+  for (int d = 0; d < DEPTH; ++d) {
+    if (d < n) ask(d);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  const uint32_t from = raw + sub * kRawRow + chunk * 16;
+  const uint32_t to = ring + w * kTile + (first + sub) * 128 + ((chunk ^ sub) << 4);
+  uint32_t s = 0, phase = 0, slot = 0;
+  bool ok = true;
+  for (uint32_t i = 0; i < n; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    __syncwarp();
+    ok = ok && __all_sync(~0u, wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status));
+    if (ok) {
+      const int left = p.len - now.kb * kTileK - chunk * 8;
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        uint32_t e[8];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(e[4 * h]), "=r"(e[4 * h + 1]), "=r"(e[4 * h + 2]), "=r"(e[4 * h + 3])
+                       : "r"(from + (slot * ROWS + 4 * j) * kRawRow + 16 * h));
+        const uint32_t o = shift[j];
+        if (o & 8) {
+#pragma unroll
+          for (int x = 0; x < 6; ++x) e[x] = e[x + 2];
+        }
+        if (o & 4) {
+#pragma unroll
+          for (int x = 0; x < 5; ++x) e[x] = e[x + 1];
+        }
+        uint32_t r[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) r[x] = __funnelshift_r(e[x], e[x + 1], (o & 2) * 8);
+        if (left < 8) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            r[x] = 2 * x + 1 < left ? r[x] : 2 * x < left ? r[x] & 0xFFFFu : 0u;
+        }
+        if (4 * j + sub < now.rows)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           (to + s * p.stage_bytes + j * 512) ^ ((j & 1) << 6)),
+                       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                       : "memory");
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (elect_one())
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(full0 + 8 * s) : "memory");
+    }
+    __syncwarp();
+    if (i + DEPTH < n) ask(slot);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if (++now.kb == now.kb1) begin_now();
+    if (++slot == DEPTH) slot = 0;
+    if (++s == (uint32_t)p.stages) {
+      s = 0;
+      phase ^= 1u;
+    }
+  }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+
 __device__ __forceinline__ void inner_out(const ProductParams &p, int64_t place, int f, int rows,
                                           float (&g)[16], const float (&u)[16]) {
   act_run(g, p.act);
@@ -316,8 +488,8 @@ __device__ __forceinline__ void inner_out(const ProductParams &p, int64_t place,
     if (i < rows) o[i * p.out_rs] = f2h(g[i] * u[i], p.type);
 }
 
-template <bool INNER>
-__global__ void __launch_bounds__(kThreads, 1)
+template <bool INNER, bool COPY>
+__global__ void __launch_bounds__(kAllThreads<COPY>, 1)
     product_kernel(const __grid_constant__ ProductParams p) {
   extern __shared__ uint8_t raw[];
   __shared__ Shared sh;
@@ -332,11 +504,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   while (tmem_cols < 2u * W * p.cols) tmem_cols *= 2;
 
   if (threadIdx.x == 0) {
-    map_ahead(&p.w[0]);
-    if (INNER) map_ahead(&p.w[1]);
-    map_ahead(&p.b);
+    if (!p.nothing) {
+      if (COPY) {
+        map_ahead(&p.w[0]);
+        if (INNER) map_ahead(&p.w[1]);
+      }
+      map_ahead(&p.b);
+    }
     for (uint32_t i = 0; i < stages; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], COPY ? 1 : 1 + kLoaders);
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -358,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   griddep_launch();
   PlanView plan = {};
   if (!p.nothing) plan = view_plan<(kOwnChoices + kThreads - 1) / kThreads>(p, own);
-  if (!INNER && warp != 0) griddep_wait();
+  if (!INNER && warp != 0 && warp < kThreads / 32) griddep_wait();
   const int chunks = plan.chunks;
   const Line line = line_of(p, chunks);
   const uint32_t cta = blockIdx.x;
@@ -373,14 +549,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     auto weights = [&](const Piece &q, const int4 &c, int kb) {
       const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes;
-      bar_expect(bar, W * (uint32_t)p.rows * 128u +
+      bar_expect(bar, (COPY ? W * (uint32_t)p.rows * 128u : 0u) +
                           (INNER ? (uint32_t)((c.z + 3) / 4) * 512u
                                  : (uint32_t)((c.z + 15) / 16) * 2048u));
+      if (!COPY) return;
 #pragma unroll
       for (int w = 0; w < W; ++w)
         tma_box3(at + w * kTile, &p.w[w], kb * kTileK, q.tile * p.rows, c.x, bar);
     };
-    for (uint32_t v = u; v < end && early < stages;) {
+    for (uint32_t v = u; COPY && v < end && early < stages;) {
       const Piece q = piece_at<INNER>(p, plan, v, end);
       const int4 c = plan.chunk[q.chunk];
       for (int kb = q.k0; kb < q.k1 && early < stages; ++kb) {
@@ -469,6 +646,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       d ^= 1u;
       u += q.k1 - q.k0;
     }
+  } else if (warp >= kThreads / 32) {
+    if constexpr (!COPY)
+      load_weights<INNER>(p, plan, u, end, ring, ring + p.raw, full0, empty0, sh,
+                          warp - kThreads / 32, lane);
   } else {
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -747,6 +928,7 @@ struct Layout {
   int64_t tokens, places, chunks, ld, packed_ld;
   int32_t cols;
   bool nothing, direct, planned, pack;
+  bool inner_copied, outer_copied;  // the weights by tensor copies
   ProductParams inner, outer;
   DirectParams few, few_sums;
   int inner_align, outer_align;
@@ -759,10 +941,9 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   l.tokens = a.m < kExpertsGroup ? a.m : kExpertsGroup;
   l.nothing = a.k == 0 || a.f == 0;
   const int64_t choices = l.tokens * a.top;
-  l.direct = !l.nothing &&
-             (l.tokens <= kDirectTokens ||
-              !(copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f) &&
-                copied(a.w_down, a.experts, a.n)));
+  l.direct = !l.nothing && l.tokens <= kDirectTokens;
+  l.inner_copied = copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f);
+  l.outer_copied = copied(a.w_down, a.experts, a.n);
   // columns of a chunk: all tokens, or 32 where the experts have fewer than half as many each
   const bool spread = choices <= 16 * a.experts;
   l.cols = !l.direct ? (l.tokens <= 16 ? 16 : l.tokens <= 32 || spread ? 32 : l.tokens <= 64 ? 64 : 128)
@@ -812,19 +993,31 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     q.out_type = (int32_t)a.out_dtype;
     p.act = (int32_t)a.act;
     p.status = q.status = a.status;
-    auto ring = [&](ProductParams &r, int w, uint32_t fixed, uint32_t room) {
+    auto ring = [&](ProductParams &r, int w, uint32_t fixed, uint32_t raw, uint32_t room) {
       r.stage_bytes = w * kTile + (uint32_t)l.cols * 128u;
-      r.stages = (int32_t)((room - 1024 - fixed) / r.stage_bytes);
+      r.stages = (int32_t)((room - 1024 - fixed - raw) / r.stage_bytes);
       if (r.stages > kMaxStages) r.stages = kMaxStages;
+      if (raw && r.stages > 3) r.stages = 3;
       r.ring = r.stages * r.stage_bytes;
-      r.smem = 1024 + r.ring + fixed;
+      r.raw = r.ring + fixed;
+      r.smem = 1024 + r.ring + fixed + raw;
     };
-    if (l.tokens <= kBesideTokens) {
-      ring(p, 2, 0, l.cols <= 32 ? kBesideInner : kBesideInner64);
-      ring(q, 1, (uint32_t)l.tokens * 512u, kBesideAll - p.smem);
+    auto by_hand = [&](ProductParams &r, int w, const coll_stack_t &m, int64_t rows, int64_t len) {
+      r.stack[w] = static_cast<const uint16_t *>(m.ptr);
+      r.es[w] = m.es, r.rs[w] = m.rs;
+      r.stack_end[w] =
+          (uintptr_t)m.ptr + 2 * (uintptr_t)((a.experts - 1) * m.es + (rows - 1) * m.rs + len);
+      r.len = (int32_t)len;
+    };
+    by_hand(p, 0, a.w_gate, a.f, a.k);
+    by_hand(p, 1, a.w_up, a.f, a.k);
+    by_hand(q, 0, a.w_down, a.n, a.f);
+    if (l.tokens <= kBesideTokens && l.inner_copied && l.outer_copied) {
+      ring(p, 2, 0, 0, l.cols <= 32 ? kBesideInner : kBesideInner64);
+      ring(q, 1, (uint32_t)l.tokens * 512u, 0, kBesideAll - p.smem);
     } else {
-      ring(p, 2, 0, kAloneSmem);
-      ring(q, 1, (uint32_t)l.tokens * 512u, kAloneSmem);
+      ring(p, 2, 0, l.inner_copied ? 0 : kRawBytes<true>, kAloneSmem);
+      ring(q, 1, (uint32_t)l.tokens * 512u, l.outer_copied ? 0 : kRawBytes<false>, kAloneSmem);
     }
     const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
     part = 2 * kSms * (inner > outer ? inner : outer);
@@ -845,16 +1038,18 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
       r->first = (int32_t)a.first, r->experts = (int32_t)a.experts, r->top = (int32_t)a.top;
       r->type = (int32_t)a.dtype, r->out_type = (int32_t)a.out_dtype, r->act = (int32_t)a.act;
       r->most_chunks = (uint32_t)l.chunks;
-      const int64_t steps = ceil_div(r->len, 64) * (r == &e ? l.chunks : 1);
-      r->warps = steps < 8 ? (uint32_t)steps : 8;
       r->tiles = (int32_t)ceil_div(a.n, kDirectOuter);
       r->splits = 1;
     }
-    // two CTAs for every SM, but two turns or more for each warp
+    // two CTAs for every SM; warps that have four steps each, all in flight at once
+    auto warps = [](int64_t steps) { return (uint32_t)(steps > 28 ? 8 : (steps + 3) / 4); };
+    d.warps = warps(ceil_div(a.k, 64));
+    const int64_t steps = l.chunks * ceil_div(a.f, 64);
     int64_t splits = ceil_div(2 * kSms, e.tiles);
-    const int64_t most = l.chunks * ceil_div(a.f, 64) / (2 * e.warps);
-    if (splits > most) splits = most;
+    if (splits > steps / 16) splits = steps / 16;
     if (splits > 32) splits = 32;
+    if (splits < 1) splits = 1;
+    e.warps = warps(ceil_div(steps, splits));
     if (splits > 1) {
       d.splits = e.splits = (int32_t)splits;
       counters = (uint64_t)e.tiles;
@@ -896,16 +1091,17 @@ int64_t need(const coll_experts_t &a) {
   return c ? c : (int64_t)l.bytes + 128;  // room to start on 128 bytes
 }
 
-template <bool INNER>
+template <bool INNER, bool COPY>
 int set_up() {
   static DenseSmemLimit limit;
-  return limit((const void *)product_kernel<INNER>, kAloneSmem) == cudaSuccess ? COLL_OK : COLL_ECUDA;
+  return limit((const void *)product_kernel<INNER, COPY>, kAloneSmem) == cudaSuccess ? COLL_OK
+                                                                                   : COLL_ECUDA;
 }
 
-template <bool INNER>
+template <bool INNER, bool COPY>
 cudaError_t launch(const ProductParams &p, cudaStream_t s) {
-  const cudaError_t e =
-      dense_launch(product_kernel<INNER>, dim3(kSms), kThreads, p.smem, 1, s, p);
+  const cudaError_t e = dense_launch(product_kernel<INNER, COPY>, dim3(kSms), kAllThreads<COPY>,
+                                     p.smem, 1, s, p);
   if (e != cudaSuccess || p.nothing) return e;
   const dim3 grid = INNER ? dim3(kSms) : dim3(p.tiles, (unsigned)ceil_div(p.tokens, kJoinTokens));
   return dense_launch(join_kernel<INNER>, grid, INNER ? 512 : 256, 0, 1, s, p);
@@ -920,12 +1116,15 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
   if (l.direct) {
     if (experts_direct_set_up(l.cols, l.outer_align, a.dtype) != cudaSuccess) return COLL_ECUDA;
   } else {
-    c = set_up<true>();
-    if (!c) c = set_up<false>();
+    c = l.inner_copied ? set_up<true, true>() : set_up<true, false>();
+    if (!c) c = l.outer_copied ? set_up<false, true>() : set_up<false, false>();
     if (!c && !l.nothing) {
-      c = encode_stack(&p.w[0], a.dtype, a.w_gate, a.experts, a.f, a.k, p.rows);
-      if (!c) c = encode_stack(&p.w[1], a.dtype, a.w_up, a.experts, a.f, a.k, p.rows);
-      if (!c) c = encode_stack(&q.w[0], a.dtype, a.w_down, a.experts, a.n, a.f, q.rows);
+      if (l.inner_copied) {
+        c = encode_stack(&p.w[0], a.dtype, a.w_gate, a.experts, a.f, a.k, p.rows);
+        if (!c) c = encode_stack(&p.w[1], a.dtype, a.w_up, a.experts, a.f, a.k, p.rows);
+      }
+      if (!c && l.outer_copied)
+        c = encode_stack(&q.w[0], a.dtype, a.w_down, a.experts, a.n, a.f, q.rows);
       if (!c) c = encode_rows(&q.b, a.dtype, p.out, l.places, a.f, l.ld, 16);
       // the first group's rows as a trial of them all
       if (!c)
@@ -976,8 +1175,10 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
       q.out = y;
       q.out_rs = a.y.rs;
       q.res = res;
-      if (err == cudaSuccess && !l.nothing) err = launch<true>(p, s);
-      if (err == cudaSuccess) err = launch<false>(q, s);
+      if (err == cudaSuccess && !l.nothing)
+        err = l.inner_copied ? launch<true, true>(p, s) : launch<true, false>(p, s);
+      if (err == cudaSuccess)
+        err = l.outer_copied ? launch<false, true>(q, s) : launch<false, false>(q, s);
     }
     if (err != cudaSuccess) return COLL_ECUDA;
   }
