@@ -121,11 +121,9 @@ __device__ __forceinline__ int make_plan(const Choices &p, int4 *chunk, int32_t 
 struct PlanParams {
   Choices choices;        // of this group's tokens
   ExpertsPlan out;
-  uint32_t *counters;     // that the launches after it want set to 0
   DenseMat x;             // rows to lay out; p NULL: none
   uint16_t *packed;
   int64_t k, packed_ld;
-  uint32_t n_counters;
 };
 
 // CTA 0 plans; the others lay out x in rows of whole 16-byte runs where no tensor copy takes it as
@@ -149,7 +147,6 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     }
     return;
   }
-  for (uint32_t i = tid; i < p.n_counters; i += blockDim.x) p.counters[i] = 0u;
   const int chunks = make_plan<kExpertsGroup * kChosenMost / kPlanThreads>(
       p.choices, p.out.chunk, p.out.token, p.out.weight, base, sums);
   if (tid == 0) *p.out.chunks = chunks;
@@ -911,8 +908,9 @@ int alignment(const void *base, int64_t es, int64_t e, int64_t rs, int64_t rows,
   return v % 32 == 0 ? 32 : v % 16 == 0 ? 16 : v % 4 == 0 ? 4 : 2;
 }
 
-// Tokens up to which the kernels without staging are used whatever the weights' layout.
-constexpr int64_t kDirectTokens = 8;
+// Bytes of the weights that a call may read up to which the kernels without staging are faster (their
+// comment has both sides).
+constexpr double kDirectBytes = 100 << 20;
 
 // Shared memory for the products. Up to 64 tokens the sums' CTAs fit beside those of the inner values
 // (all an SM has is 228 KB, of which a CTA takes 1 KB and its static arrays beside what it asks for):
@@ -941,20 +939,22 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   l.tokens = a.m < kExpertsGroup ? a.m : kExpertsGroup;
   l.nothing = a.k == 0 || a.f == 0;
   const int64_t choices = l.tokens * a.top;
-  l.direct = !l.nothing && l.tokens <= kDirectTokens;
+  const bool rows = a.x.cs == 1 || a.k == 1;
+  const int64_t chosen = a.experts < choices ? a.experts : choices;
+  l.direct = !l.nothing && l.tokens <= kDirectTokens && choices <= kDirectChoices && rows &&
+             2.0 * chosen * a.f * (2.0 * a.k + a.n) <= kDirectBytes;
   l.inner_copied = copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f);
   l.outer_copied = copied(a.w_down, a.experts, a.n);
   // columns of a chunk: all tokens, or 32 where the experts have fewer than half as many each
   const bool spread = choices <= 16 * a.experts;
-  l.cols = !l.direct ? (l.tokens <= 16 ? 16 : l.tokens <= 32 || spread ? 32 : l.tokens <= 64 ? 64 : 128)
-           : l.tokens <= 8 ? 8 : l.tokens <= 16 ? 16 : 32;
-  const bool rows = a.x.cs == 1 || a.k == 1;
-  const int x_align = alignment(a.x.ptr, 0, 1, a.x.rs, a.m, a.k);
-  l.planned = l.direct ? choices > kDirectUnplanned || l.tokens > 8 || !rows
-                       : choices > kOwnChoices || !copied(a.x, a.m, a.k);
-  l.pack = !l.nothing && (l.direct ? l.planned && (!rows || x_align < 16) : !copied(a.x, a.m, a.k));
-  l.chunks = (a.experts < choices ? a.experts : choices) + choices / l.cols;
-  l.places = l.direct && !l.planned ? 8 * l.chunks : choices;
+  l.cols = l.direct ? 8
+           : l.tokens <= 16 ? 16
+           : l.tokens <= 32 || spread ? 32
+           : l.tokens <= 64 ? 64 : 128;
+  l.planned = !l.direct && (choices > kOwnChoices || !copied(a.x, a.m, a.k));
+  l.pack = !l.nothing && !l.direct && !copied(a.x, a.m, a.k);
+  l.chunks = chosen + choices / l.cols;
+  l.places = l.direct ? 8 * l.chunks : choices;
   l.ld = round_up(a.f, 64);
   l.packed_ld = round_up(a.k, 64);
   uint64_t used = 0;
@@ -1032,7 +1032,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     d.rs[0] = a.w_gate.rs, d.rs[1] = a.w_up.rs, e.rs[0] = a.w_down.rs;
     d.len = (int32_t)a.k, e.len = (int32_t)a.f;
     d.features = (int32_t)a.f, e.features = (int32_t)a.n;
-    d.x_align = l.pack ? 32 : x_align;
+    d.x_align = alignment(a.x.ptr, 0, 1, a.x.rs, a.m, a.k);
     e.x_align = 32;
     for (DirectParams *r : {&d, &e}) {
       r->first = (int32_t)a.first, r->experts = (int32_t)a.experts, r->top = (int32_t)a.top;
@@ -1062,8 +1062,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     o.token = reinterpret_cast<int32_t *>(take((uint64_t)l.places * 4));
     o.weight = reinterpret_cast<float *>(take((uint64_t)l.places * 4));
   }
-  s.counters = d.counters = e.counters = reinterpret_cast<uint32_t *>(take(counters * 4));
-  s.n_counters = (uint32_t)counters;
+  d.counters = e.counters = reinterpret_cast<uint32_t *>(take(counters * 4));
   char *h = take((uint64_t)l.places * l.ld * 2);
   p.part = q.part = e.part = reinterpret_cast<float *>(take(part));
   if (l.pack)
@@ -1074,7 +1073,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   s.choices.first = (int32_t)a.first;
   s.choices.cols = l.cols;
   s.k = a.k;
-  s.out = p.plan = q.plan = d.plan = e.plan = o;
+  s.out = p.plan = q.plan = o;
   p.out = h;
   p.out_rs = l.ld;
   d.h = reinterpret_cast<uint16_t *>(h);
@@ -1113,9 +1112,7 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
   if (c) return c;
   ProductParams &p = l.inner, &q = l.outer;
   DirectParams &d = l.few, &e = l.few_sums;
-  if (l.direct) {
-    if (experts_direct_set_up(l.cols, l.outer_align, a.dtype) != cudaSuccess) return COLL_ECUDA;
-  } else {
+  if (!l.direct) {
     c = l.inner_copied ? set_up<true, true>() : set_up<true, false>();
     if (!c) c = l.outer_copied ? set_up<false, true>() : set_up<false, false>();
     if (!c && !l.nothing) {
@@ -1164,13 +1161,13 @@ int run(const coll_experts_t &a, char *base, cudaStream_t s) {
     if (l.direct) {
       d.ids = e.ids = ch.ids;
       d.weights = e.weights = ch.weights;
-      d.x = l.pack ? o.packed : x;
-      d.x_ld = l.pack ? l.packed_ld : a.x.rs;
+      d.x = x;
+      d.x_ld = a.x.rs;
       e.y = y;
       e.y_rs = a.y.rs;
       e.res = res;
-      if (err == cudaSuccess) err = experts_direct_inner(d, l.cols, l.inner_align, s);
-      if (err == cudaSuccess) err = experts_direct_outer(e, l.cols, l.outer_align, s);
+      if (err == cudaSuccess) err = experts_direct_inner(d, l.inner_align, s);
+      if (err == cudaSuccess) err = experts_direct_outer(e, l.outer_align, s);
     } else {
       q.out = y;
       q.out_rs = a.y.rs;

@@ -18,16 +18,15 @@ struct ExpertsPlan {
   float *weight;
 };
 
-// Few choices an expert, or weights that no tensor copy takes (experts_direct.cu).
-constexpr int kDirectUnplanned = 32;  // choices that a warp sorts by itself
-constexpr int kDirectChunks = kExpertsMost + kExpertsGroup * kChosenMost / 8;
+// One to a few tokens of few choices (experts_direct.cu).
+constexpr int kDirectChoices = 32;  // that a warp sorts by itself
+constexpr int kDirectTokens = 8;
 
 struct DirectParams {
   const uint16_t *w[2];  // gate and up, or down
   int64_t es[2], rs[2];
   const uint16_t *x;     // tokens, or the inner values in the order of the chunks
   int64_t x_ld;
-  ExpertsPlan plan;      // plan.chunks NULL: chunks of eight from ids, which are few enough
   DenseMat ids, weights;
   int32_t first, experts, top, tokens;
   int32_t type, out_type, act;
@@ -36,7 +35,7 @@ struct DirectParams {
   int32_t x_align;       // bytes that rows of x start on and are a multiple of
   uint16_t *h;           // inner: the output
   int64_t h_ld;
-  uint32_t *counters;    // of the sums' tiles; the inner kernel sets them to 0 where no plan does
+  uint32_t *counters;    // of the sums' tiles; the inner kernel sets them to 0
   int32_t tiles;
   void *y;               // sums: the output
   int64_t y_rs;
@@ -49,10 +48,8 @@ struct DirectParams {
 constexpr int kDirectInner = 8;   // inner features of a CTA
 constexpr int kDirectOuter = 16;  // outputs of a CTA
 
-// align: of the weights' rows, as x_align; columns: of a chunk, 8, 16 or 32.
-// Of the sums alone: the inner kernels need no more shared memory than a kernel has anyway.
-cudaError_t experts_direct_set_up(int columns, int align, int64_t type);
-cudaError_t experts_direct_inner(const DirectParams &p, int columns, int align, cudaStream_t s);
-cudaError_t experts_direct_outer(const DirectParams &p, int columns, int align, cudaStream_t s);
+// align: of the weights' rows, as x_align.
+cudaError_t experts_direct_inner(const DirectParams &p, int align, cudaStream_t s);
+cudaError_t experts_direct_outer(const DirectParams &p, int align, cudaStream_t s);
 
 }  // namespace coll

@@ -1,11 +1,13 @@
-// A few tokens through their chosen experts without staging: every warp loads weights straight into
-// the fragments of mma.m16n8k16, as dense_gemv.cu does for one matrix. A chunk of choices of one
-// expert is the columns of a fragment, 16 rows of weights its rows (inner: eight of gate and eight of
-// up, so a lane ends up with g and u of the same feature).
+// A token or a few through their chosen experts without staging: every warp loads weights straight into
+// the fragments of mma.m16n8k16, as dense_gemv.cu does for one matrix. A chunk of up to eight choices of
+// one expert is the columns of a fragment, 16 rows of weights its rows (inner: eight of gate and eight
+// of up, so a lane ends up with g and u of the same feature).
 //
-// Bound by HBM and, for a token or two, by latency: one launch for the inner values and one for the
-// sums. Up to 32 choices the chunks are made by a warp of every CTA, from the ids alone (a launch
-// that sorts them first would cost as much as either kernel); beyond that plan_kernel makes them.
+// Bound by latency and HBM: two launches, the chunks made by a warp of every CTA from the ids alone,
+// the sums' first weights asked for while the inner values are still being made. One token, six of 64
+// experts of 2048 x 176 (13 MB): 8 us, where the tensor-core kernels' cut tiles and joins take 18; 16
+// choices of 16 experts of 1024 x 512 18 against 20; from some 100 MB on those are as fast or faster
+// (eight experts of 7168 x 2048: 115 us against 120).
 #include "dense_direct.cuh"
 #include "dense_epi.cuh"
 #include "dense_tc.h"
@@ -18,17 +20,19 @@ namespace {
 constexpr int kStep = 64;  // elements of a row that a warp takes at a time
 constexpr int kWarps = 8;
 
-template <int NT, int ALIGN>
-constexpr int kAhead = NT == 1 && ALIGN > 2 ? 4 : NT <= 2 ? 2 : 1;
+template <int ALIGN>
+constexpr int kAhead = ALIGN > 2 ? 4 : 2;
 
-// Chunks of eight made here, for plans of few choices.
+// The chunks and, by place, their choices' tokens and weights.
 struct Few {
-  int32_t token[8 * kDirectUnplanned];
-  float weight[8 * kDirectUnplanned];
+  int4 chunk[kDirectChoices];  // {expert, first place, choices, 0}
+  int32_t token[8 * kDirectChoices];
+  float weight[8 * kDirectChoices];
+  int chunks;
 };
 
 // One warp: the chunks of at most 32 choices, by first choice; their places are eight apart.
-__device__ __forceinline__ int make_chunks(const DirectParams &p, int4 *chunk, Few &few) {
+__device__ __forceinline__ void make_chunks(const DirectParams &p, Few &few) {
   const int s = threadIdx.x & 31, n = p.tokens * p.top;
   int e = -1;
   float w = 0.0f;
@@ -55,26 +59,15 @@ __device__ __forceinline__ int make_chunks(const DirectParams &p, int4 *chunk, F
     few.weight[place] = w;
   }
   for (int q = 0; q < mine; ++q)
-    chunk[first + q] = make_int4(e, 8 * (first + q), min(8, count - 8 * q), 0);
-  return all;
+    few.chunk[first + q] = make_int4(e, 8 * (first + q), min(8, count - 8 * q), 0);
+  if (s == 0) few.chunks = all;
 }
 
-// Row pointers and lengths of the tokens of a fragment's columns.
-template <int NT>
-struct Columns {
-  const uint16_t *x[NT];
-  int len[NT];
-};
-
-template <int NT, int ALIGN>
-__device__ __forceinline__ void load_x(const DirectParams &p, const Columns<NT> &c, int k, int at,
-                                       uint32_t (&x)[NT][8]) {
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    if (p.x_align >= 32) load16<32>(c.x[i] + k, at, c.len[i], x[i]);
-    else if (p.x_align >= 16) load16<16>(c.x[i] + k, at, c.len[i], x[i]);
-    else load16<2>(c.x[i] + k, at, c.len[i], x[i]);
-  }
+__device__ __forceinline__ void load_x(const DirectParams &p, const uint16_t *x, int at, int len,
+                                       uint32_t (&r)[8]) {
+  if (p.x_align >= 32) load16<32>(x, at, len, r);
+  else if (p.x_align >= 16) load16<16>(x, at, len, r);
+  else load16<2>(x, at, len, r);
 }
 
 // 16 elements of one row of each matrix, AHEAD of them asked for before the first is used.
@@ -109,206 +102,150 @@ __device__ __forceinline__ void load_rows(const uint16_t *const (&pa)[AHEAD],
   }
 }
 
-// Eight inner features of one chunk's choices: gate's rows are the fragment's first eight, up's the
-// others. The warps take the steps of k in turn and join in order.
-template <int TYPE, int NT, int ALIGN>
+// Eight inner features of one chunk's choices at a time: gate's rows are the fragment's first eight,
+// up's the others. The warps take the steps of k in turn and join in order.
+template <int TYPE, int ALIGN>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     direct_inner_kernel(const __grid_constant__ DirectParams p) {
-  constexpr int AHEAD = kAhead<NT, ALIGN>;
-  __shared__ float part[kWarps][8 * NT][16];
-  __shared__ int4 few_chunk[kDirectUnplanned];
+  constexpr int AHEAD = kAhead<ALIGN>;
+  __shared__ float part[2][kWarps][8][16];
   __shared__ Few few;
-  __shared__ int chunks;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   griddep_wait();
   griddep_launch();
-  int4 c;
-  const int32_t *token;
-  if (p.plan.chunks) {
-    if ((int)blockIdx.y >= *p.plan.chunks) return;
-    c = p.plan.chunk[blockIdx.y];
-    token = p.plan.token + c.y;
-  } else {
-    if (warp == 0) {
-      const int n = make_chunks(p, few_chunk, few);
-      if (lane == 0) chunks = n;
-    }
-    if (blockIdx.x == 0 && blockIdx.y == 0 && p.splits > 1)
-      for (int i = threadIdx.x; i < p.tiles; i += blockDim.x) p.counters[i] = 0u;
-    __syncthreads();
-    if ((int)blockIdx.y >= chunks) return;
-    c = few_chunk[blockIdx.y];
-    token = few.token + c.y;
-  }
-  const int f0 = (int)blockIdx.x * kDirectInner, f = f0 + g;
-  const int len = f < p.features ? p.len : 0;  // rows that are not there are empty
-  const int64_t row = len ? f : 0;
-  const uint16_t *wa = p.w[0] + c.x * p.es[0] + row * p.rs[0] + 16 * t;
-  const uint16_t *wb = p.w[1] + c.x * p.es[1] + row * p.rs[1] + 16 * t;
-  Columns<NT> col;
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    const bool there = i * 8 + g < c.z;
-    col.len[i] = there ? p.len : 0;
-    col.x[i] = p.x + (there ? token[i * 8 + g] : 0) * p.x_ld + 16 * t;
-  }
-  float acc[NT][4] = {};
+  if (warp == 0) make_chunks(p, few);
+  if (blockIdx.x == 0 && p.splits > 1)
+    for (int i = threadIdx.x; i < p.tiles; i += blockDim.x) p.counters[i] = 0u;
+  __syncthreads();
+  const int tiles = (p.features + kDirectInner - 1) / kDirectInner, items = few.chunks * tiles;
   const int steps = (p.len + kStep - 1) / kStep;
-  for (int s = warp; s < steps; s += AHEAD * warps) {
-    const uint16_t *pa[AHEAD], *pb[AHEAD];
-    int at[AHEAD], la[AHEAD];
+  int turn = 0;
+  for (int item = blockIdx.x; item < items; item += gridDim.x, turn ^= 1) {
+    const int which = item / tiles, tile = item - which * tiles;
+    const int4 c = few.chunk[which];
+    const int f0 = tile * kDirectInner, f = f0 + g;
+    const int len = f < p.features ? p.len : 0;  // rows that are not there are empty
+    const int64_t row = len ? f : 0;
+    const uint16_t *wa = p.w[0] + c.x * p.es[0] + row * p.rs[0] + 16 * t;
+    const uint16_t *wb = p.w[1] + c.x * p.es[1] + row * p.rs[1] + 16 * t;
+    const int x_len = g < c.z ? p.len : 0;
+    const uint16_t *x = p.x + (x_len ? few.token[c.y + g] : 0) * p.x_ld + 16 * t;
+    float acc[4] = {};
+    for (int s = warp; s < steps; s += AHEAD * warps) {
+      const uint16_t *pa[AHEAD], *pb[AHEAD];
+      int at[AHEAD], la[AHEAD];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int k = (s + i * warps) * kStep;
-      pa[i] = wa + k, pb[i] = wb + k, at[i] = k + 16 * t, la[i] = len;
-    }
-    Rows<ALIGN, AHEAD> r;
-    load_rows<ALIGN, AHEAD>(pa, pb, at, la, la, r);
-    uint32_t x[AHEAD][NT][8];
+      for (int i = 0; i < AHEAD; ++i) {
+        const int k = (s + i * warps) * kStep;
+        pa[i] = wa + k, pb[i] = wb + k, at[i] = k + 16 * t, la[i] = len;
+      }
+      Rows<ALIGN, AHEAD> r;
+      load_rows<ALIGN, AHEAD>(pa, pb, at, la, la, r);
+      uint32_t xs[AHEAD][8];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-      load_x<NT, ALIGN>(p, col, (s + i * warps) * kStep, at[i], x[i]);
+      for (int i = 0; i < AHEAD; ++i) load_x(p, x + (s + i * warps) * kStep, at[i], x_len, xs[i]);
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int i = 0; i < AHEAD; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          mma16816<TYPE>(acc[n], r.a[i][2 * q], r.b[i][2 * q], r.a[i][2 * q + 1],
-                         r.b[i][2 * q + 1], x[i][n][2 * q], x[i][n][2 * q + 1]);
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    part[warp][n * 8 + 2 * t][g] = acc[n][0];
-    part[warp][n * 8 + 2 * t + 1][g] = acc[n][1];
-    part[warp][n * 8 + 2 * t][g + 8] = acc[n][2];
-    part[warp][n * 8 + 2 * t + 1][g + 8] = acc[n][3];
-  }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 8 * c.z; i += blockDim.x) {
-    const int n = i / 8, j = i % 8;
-    if (f0 + j >= p.features) continue;
-    float v = 0.0f, u = 0.0f;
-    for (int w = 0; w < warps; ++w) {
-      v += part[w][n][j];
-      u += part[w][n][j + 8];
+          mma16816<TYPE>(acc, r.a[i][2 * q], r.b[i][2 * q], r.a[i][2 * q + 1], r.b[i][2 * q + 1],
+                         xs[i][2 * q], xs[i][2 * q + 1]);
     }
-    p.h[(int64_t)(c.y + n) * p.h_ld + f0 + j] = f2h(act_value(v, p.act) * u, TYPE);
-  }
-  // the sums read rows in whole runs of 16
-  if (blockIdx.x == gridDim.x - 1)
-    for (int i = threadIdx.x; i < 16 * c.z; i += blockDim.x) {
-      const int j = p.features + i % 16;
-      if (j < ((p.features + 15) & ~15)) p.h[(int64_t)(c.y + i / 16) * p.h_ld + j] = 0;
+    float(*mine)[16] = part[turn][warp];  // the other half may still be read
+    mine[2 * t][g] = acc[0];
+    mine[2 * t + 1][g] = acc[1];
+    mine[2 * t][g + 8] = acc[2];
+    mine[2 * t + 1][g + 8] = acc[3];
+    __syncthreads();
+    for (int i = threadIdx.x; i < 8 * c.z; i += blockDim.x) {
+      const int n = i / 8, j = i % 8;
+      if (f0 + j >= p.features) continue;
+      float v = 0.0f, u = 0.0f;
+      for (int w = 0; w < warps; ++w) {
+        v += part[turn][w][n][j];
+        u += part[turn][w][n][j + 8];
+      }
+      p.h[(int64_t)(c.y + n) * p.h_ld + f0 + j] = f2h(act_value(v, p.act) * u, TYPE);
     }
+    // the sums read rows in whole runs of 16
+    if (tile == tiles - 1)
+      for (int i = threadIdx.x; i < 16 * c.z; i += blockDim.x) {
+        const int j = p.features + i % 16;
+        if (j < ((p.features + 15) & ~15)) p.h[(int64_t)(c.y + i / 16) * p.h_ld + j] = 0;
+      }
+  }
 }
 
 // 16 outputs of all tokens. The steps of all chunks are one list, the splits' shares of it
 // neighbouring, and inside a share the warps take steps in turn; each adds its finished products,
 // times their weights, to its own sums in shared memory. The warps join in order, and so do the
 // splits, in the last of their CTAs to arrive.
-template <int TYPE, int NT, int ALIGN>
+template <int TYPE, int ALIGN>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     direct_outer_kernel(const __grid_constant__ DirectParams p) {
-  constexpr int AHEAD = kAhead<NT, ALIGN>;
-  extern __shared__ float sums[];  // [warps][tokens][16], then the plan's chunks
-  __shared__ int4 few_chunk[kDirectUnplanned];
+  constexpr int AHEAD = kAhead<ALIGN>;
+  __shared__ float sums[kWarps][kDirectTokens * 16];
   __shared__ Few few;
-  __shared__ int chunks;
   __shared__ uint32_t last;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3, size = p.tokens * 16;
   griddep_launch();
-  for (int i = threadIdx.x; i < warps * size; i += blockDim.x) sums[i] = 0.0f;
+  float *mine = sums[warp];
+  for (int i = lane; i < size; i += 32) mine[i] = 0.0f;
   // The inner kernel lets this one start after its own wait, so what that waited for (the choices,
-  // the plan, the weights) is there; its inner values are not before the wait below.
-  const int4 *chunk = few_chunk;
-  const int32_t *token = few.token;
-  const float *weight = few.weight;
-  int n_chunks;
-  if (p.plan.chunks) {
-    int4 *copy = reinterpret_cast<int4 *>(sums + warps * size);
-    n_chunks = *p.plan.chunks;
-    for (int i = threadIdx.x; i < n_chunks; i += blockDim.x) copy[i] = p.plan.chunk[i];
-    chunk = copy;
-    token = p.plan.token;
-    weight = p.plan.weight;
-    __syncthreads();
-  } else {
-    if (warp == 0) {
-      const int n = make_chunks(p, few_chunk, few);
-      if (lane == 0) chunks = n;
-    }
-    __syncthreads();
-    n_chunks = chunks;
-  }
+  // the weights) is there; its inner values are not before the wait below.
+  if (warp == 0) make_chunks(p, few);
+  __syncthreads();
   const int n0 = (int)blockIdx.x * kDirectOuter;
   const int la = n0 + g < p.features ? p.len : 0, lb = n0 + g + 8 < p.features ? p.len : 0;
   const uint16_t *wa = p.w[0] + (int64_t)(la ? n0 + g : 0) * p.rs[0] + 16 * t;
   const uint16_t *wb = p.w[0] + (int64_t)(lb ? n0 + g + 8 : 0) * p.rs[0] + 16 * t;
   const uint16_t *h = p.x + 16 * t;
-  float *mine = sums + warp * size;
   const int steps = (p.len + kStep - 1) / kStep;
-  const int64_t all = (int64_t)n_chunks * steps;
+  const int64_t all = (int64_t)few.chunks * steps;
   const int64_t lo = all * blockIdx.y / p.splits, hi = all * (blockIdx.y + 1) / p.splits;
-  float acc[NT][4] = {};
+  float acc[4] = {};
   int now = -1;
   // what the accumulators hold of chunk `now` goes to its tokens; of two columns of one token, one
   // after the other
   auto flush = [&]() {
-    const int4 c = chunk[now];
+    const int4 c = few.chunk[now];
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      int tok[2];
-      float w[2];
+    for (int q = 0; q < 4; ++q) {
+      if (t == q) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int at = n * 8 + 2 * t + j;
-        tok[j] = at < c.z ? token[c.y + at] : -1;
-        w[j] = at < c.z ? weight[c.y + at] : 0.0f;
+        for (int j = 0; j < 2; ++j)
+          if (2 * t + j < c.z) {
+            float *y = mine + few.token[c.y + 2 * t + j] * 16 + g;
+            const float w = few.weight[c.y + 2 * t + j];
+            y[0] = fmaf(w, acc[j], y[0]);
+            y[8] = fmaf(w, acc[j + 2], y[8]);
+          }
       }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (t == q) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (tok[j] >= 0) {
-              float *y = mine + tok[j] * 16 + g;
-              y[0] = fmaf(w[j], acc[n][j], y[0]);
-              y[8] = fmaf(w[j], acc[n][j + 2], y[8]);
-            }
-        }
-        __syncwarp();
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[n][j] = 0.0f;
+      __syncwarp();
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = 0.0f;
   };
   int64_t s = lo + warp;
   int at_chunk = (int)(s / steps), at_step = (int)(s - (int64_t)at_chunk * steps);
   while (s < hi) {
-    const uint16_t *pa[AHEAD], *pb[AHEAD];
-    int at[AHEAD], ka[AHEAD], kb[AHEAD], which[AHEAD], from[AHEAD];
-    Columns<NT> col[AHEAD];
+    const uint16_t *pa[AHEAD], *pb[AHEAD], *x[AHEAD];
+    int at[AHEAD], ka[AHEAD], kb[AHEAD], which[AHEAD], x_len[AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const bool there = s < hi;
       which[i] = there ? at_chunk : -1;
-      const int4 c = there ? chunk[at_chunk] : make_int4(0, 0, 0, 0);
+      const int4 c = there ? few.chunk[at_chunk] : make_int4(0, 0, 0, 0);
       const int k = at_step * kStep;
-      from[i] = k;
       pa[i] = wa + c.x * p.es[0] + k;
       pb[i] = wb + c.x * p.es[0] + k;
       at[i] = k + 16 * t;
       ka[i] = there ? la : 0;
       kb[i] = there ? lb : 0;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        const bool row = n * 8 + g < c.z;
-        col[i].len[n] = row ? p.len : 0;
-        col[i].x[n] = h + (int64_t)(row ? c.y + n * 8 + g : 0) * p.x_ld;
-      }
+      x_len[i] = g < c.z ? p.len : 0;
+      x[i] = h + (int64_t)(g < c.z ? c.y + g : 0) * p.x_ld + k;
       s += warps;
       at_step += warps;
       while (at_step >= steps) {
@@ -319,9 +256,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     Rows<ALIGN, AHEAD> r;
     load_rows<ALIGN, AHEAD>(pa, pb, at, ka, kb, r);
     griddep_wait();
-    uint32_t x[AHEAD][NT][8];
+    uint32_t xs[AHEAD][8];
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) load_x<NT, ALIGN>(p, col[i], from[i], at[i], x[i]);
+    for (int i = 0; i < AHEAD; ++i) load_x(p, x[i], at[i], x_len[i], xs[i]);
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       if (which[i] < 0) break;
@@ -330,11 +267,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         now = which[i];
       }
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          mma16816<TYPE>(acc[n], r.a[i][2 * q], r.b[i][2 * q], r.a[i][2 * q + 1],
-                         r.b[i][2 * q + 1], x[i][n][2 * q], x[i][n][2 * q + 1]);
+      for (int q = 0; q < 4; ++q)
+        mma16816<TYPE>(acc, r.a[i][2 * q], r.b[i][2 * q], r.a[i][2 * q + 1], r.b[i][2 * q + 1],
+                       xs[i][2 * q], xs[i][2 * q + 1]);
     }
   }
   if (now >= 0) flush();
@@ -350,7 +285,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   float *part = p.part + (int64_t)blockIdx.x * size;
   for (int i = threadIdx.x; i < size; i += blockDim.x) {
     float v = 0.0f;
-    for (int w = 0; w < warps; ++w) v += sums[w * size + i];
+    for (int w = 0; w < warps; ++w) v += sums[w][i];
     if (p.splits == 1) finish(i, v);
     else __stcg(part + blockIdx.y * share + i, v);
   }
@@ -370,51 +305,32 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   }
 }
 
-uint32_t outer_smem(const DirectParams &p) {
-  return p.warps * (uint32_t)p.tokens * 64u + (p.plan.chunks ? p.most_chunks * 16u : 0u);
-}
-
-// The kernels of a type, a chunk's columns and an alignment.
 using Kernel = void (*)(const DirectParams);
-template <int TYPE, int NT>
-Kernel pick(bool inner, int align) {
+template <bool INNER, int TYPE>
+Kernel pick(int align) {
 #define COLL_DIRECT(A) \
-  return inner ? (Kernel)direct_inner_kernel<TYPE, NT, A> : (Kernel)direct_outer_kernel<TYPE, NT, A>
+  return INNER ? (Kernel)direct_inner_kernel<TYPE, A> : (Kernel)direct_outer_kernel<TYPE, A>
   if (align >= 32) COLL_DIRECT(32);
   if (align >= 16) COLL_DIRECT(16);
   if (align >= 4) COLL_DIRECT(4);
   COLL_DIRECT(2);
 #undef COLL_DIRECT
 }
-template <int TYPE>
-Kernel pick(bool inner, int columns, int align) {
-  return columns == 8 ? pick<TYPE, 1>(inner, align)
-         : columns == 16 ? pick<TYPE, 2>(inner, align)
-                         : pick<TYPE, 4>(inner, align);
-}
-Kernel pick(int64_t type, bool inner, int columns, int align) {
-  return type == COLL_BF16 ? pick<COLL_BF16>(inner, columns, align)
-                           : pick<COLL_F16>(inner, columns, align);
-}
 
 }  // namespace
 
-cudaError_t experts_direct_set_up(int columns, int align, int64_t type) {
-  static DenseSmemLimit limit[2][3][4];
-  const int c = columns == 8 ? 0 : columns == 16 ? 1 : 2;
-  const int a = align >= 32 ? 0 : align >= 16 ? 1 : align >= 4 ? 2 : 3;
-  return limit[type == COLL_BF16][c][a]((const void *)pick(type, false, columns, align),
-                                        200 * 1024);
+cudaError_t experts_direct_inner(const DirectParams &p, int align, cudaStream_t s) {
+  const Kernel k = p.type == COLL_BF16 ? pick<true, COLL_BF16>(align) : pick<true, COLL_F16>(align);
+  const int64_t items =
+      (int64_t)((p.features + kDirectInner - 1) / kDirectInner) * p.most_chunks;
+  const int64_t most = kSms * (16 / p.warps);  // as many as are on the SMs at once
+  return dense_launch(k, dim3((unsigned)(items < most ? items : most)), 32 * p.warps, 0, 1, s, p);
 }
 
-cudaError_t experts_direct_inner(const DirectParams &p, int columns, int align, cudaStream_t s) {
-  const dim3 grid((unsigned)((p.features + kDirectInner - 1) / kDirectInner), p.most_chunks);
-  return dense_launch(pick(p.type, true, columns, align), grid, 32 * p.warps, 0, 1, s, p);
-}
-
-cudaError_t experts_direct_outer(const DirectParams &p, int columns, int align, cudaStream_t s) {
-  return dense_launch(pick(p.type, false, columns, align), dim3(p.tiles, p.splits), 32 * p.warps,
-                      outer_smem(p), 1, s, p);
+cudaError_t experts_direct_outer(const DirectParams &p, int align, cudaStream_t s) {
+  const Kernel k =
+      p.type == COLL_BF16 ? pick<false, COLL_BF16>(align) : pick<false, COLL_F16>(align);
+  return dense_launch(k, dim3(p.tiles, p.splits), 32 * p.warps, 0, 1, s, p);
 }
 
 }  // namespace coll
