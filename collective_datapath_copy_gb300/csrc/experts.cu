@@ -12,6 +12,7 @@
 // last of its CTAs to arrive, in the order of k: nothing waits, and results do not depend on timing.
 #include <cuda.h>
 #include <cuda_runtime.h>
+#include <math.h>
 #include <stdint.h>
 #include <string.h>
 
@@ -178,6 +179,7 @@ struct ProductParams {
   uint32_t stage_bytes, ring, raw, smem;  // raw: where the loader warps' rings start
   int32_t type, out_type, act;
   int32_t nothing;      // sums of nothing: y = residual
+  int32_t whole;        // inner: no tile is cut
   const uint16_t *stack[2];  // weights that loader warps bring, with their extent
   int64_t es[2], rs[2];
   uintptr_t stack_end[2];
@@ -257,24 +259,28 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// The line of k blocks, cut into `ctas` equal lengths.
+// The line of k blocks, cut into `ctas` equal lengths of whole units.
 struct Line {
-  uint32_t all, ctas;
+  uint32_t units, unit, ctas;  // unit: k blocks
   __device__ uint32_t begin(uint32_t c) const {
-    return (uint32_t)((uint64_t)all * c / ctas);
+    return (uint32_t)((uint64_t)units * c / ctas) * unit;
   }
   // whose length block u is in
   __device__ uint32_t owner(uint32_t u) const {
-    return (uint32_t)((((uint64_t)u + 1) * ctas - 1) / all);
+    return (uint32_t)((((uint64_t)(u / unit) + 1) * ctas - 1) / units);
   }
+  __device__ uint32_t end() const { return units * unit; }
 };
 
 // A length is kShort blocks at least where there is too little for every CTA: shorter ones would
 // come sooner, but a tile's shares take longer to join.
+template <bool INNER>
 __device__ __forceinline__ Line line_of(const ProductParams &p, int chunks) {
   Line l;
-  l.all = (uint32_t)chunks * (uint32_t)p.tiles * (uint32_t)p.kblocks;
-  l.ctas = min(kSms, max(l.all / kShort, min(l.all, 1u)));
+  l.unit = INNER && p.whole ? (uint32_t)p.kblocks : 1u;
+  l.units = (uint32_t)chunks * (uint32_t)p.tiles * ((uint32_t)p.kblocks / l.unit);
+  const uint32_t least = INNER && p.whole ? 1u : kShort;
+  l.ctas = min(kSms, max(l.units / least, min(l.units, 1u)));
   return l;
 }
 
@@ -533,7 +539,7 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
   if (!p.nothing) plan = view_plan<(kOwnChoices + kThreads - 1) / kThreads>(p, own);
   if (!INNER && warp != 0 && warp < kThreads / 32) griddep_wait();
   const int chunks = plan.chunks;
-  const Line line = line_of(p, chunks);
+  const Line line = line_of<INNER>(p, chunks);
   const uint32_t cta = blockIdx.x;
   uint32_t u = 0, end = 0;
   if (cta < line.ctas) {
@@ -760,7 +766,7 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Produ
   griddep_launch();
   const PlanView plan = view_plan<kOwnChoices / 256>(p, own);
   const int chunks = plan.chunks;
-  const Line line = line_of(p, chunks);
+  const Line line = line_of<INNER>(p, chunks);
   const uint32_t step = INNER ? (uint32_t)p.kblocks : (uint32_t)p.kblocks * (uint32_t)chunks;
   uint32_t job = 0, c0 = 0, c1 = 0;
   if (INNER ? blockIdx.x < line.ctas : chunks > 0) {
@@ -772,7 +778,7 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Produ
   Piece q = {};
   int4 c = make_int4(0, 0, 0, 0);
   if (cut) {
-    q = piece_at<INNER>(p, plan, job * step, line.all);
+    q = piece_at<INNER>(p, plan, job * step, line.end());
     if (INNER) c = plan.chunk[q.chunk];
   }
   griddep_wait();
@@ -934,6 +940,47 @@ struct Layout {
   uint64_t bytes;
 };
 
+// Rows of the inner tiles. 128 and cut where a CTA's length ends, or fewer and whole, which saves the
+// launch that joins them (16 tokens of two, eight experts of 4096 x 1792: 66 us against 68.5; 32
+// tokens, 64 of 2048 x 176: 36.7 against 39.4): whole if that takes less time for as many experts as
+// uniform choices come to, one more and all of them (four tokens, of eight experts, six of which were
+// chosen where 5.3 were expected: 61 us whole, 50 cut). A k block takes its bytes at 45 a ns or 250 ns
+// to issue; what cutting costs, 4 us.
+void inner_tiles(const coll_experts_t &a, Layout &l) {
+  ProductParams &p = l.inner;
+  const double choices = (double)l.tokens * a.top, e = (double)a.experts;
+  const double likely = e * (1.0 - pow(1.0 - 1.0 / e, choices));
+  const double most = e < choices ? e : choices;
+  const double chunks[3] = {likely, likely + 1.0 < most ? likely + 1.0 : most, most};
+  const double kblocks = (double)ceil_div(a.k, kTileK);
+  auto set = [&](int64_t rows) {  // the time of a k block
+    p.tiles = (int32_t)ceil_div(a.f, rows);
+    p.rows = (int32_t)round_up(ceil_div(a.f, p.tiles), 8);
+    const double ns = (p.rows * 256.0 + l.cols * 128.0) / 45.0;
+    return ns > 250.0 ? ns : 250.0;
+  };
+  double cut[3], best = 1.0;
+  for (int i = 0; i < 3; ++i) {
+    const double block = set(128), blocks = chunks[i] * p.tiles * kblocks / kSms;
+    cut[i] = (blocks > kShort ? blocks : kShort) * block + 4000.0;
+  }
+  int64_t rows = 128;
+  for (int64_t r = 16; r <= 128; r += 8) {
+    const double block = set(r);
+    double worst = 0.0;  // of the times whole in those cut
+    for (int i = 0; i < 3; ++i) {
+      const double part = ceil(chunks[i] * p.tiles / kSms - 1e-9) * kblocks * block / cut[i];
+      if (part > worst) worst = part;
+    }
+    if (worst < best) {
+      best = worst;
+      rows = r;
+      p.whole = 1;
+    }
+  }
+  set(rows);
+}
+
 int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   memset(&l, 0, sizeof(l));
   l.tokens = a.m < kExpertsGroup ? a.m : kExpertsGroup;
@@ -974,9 +1021,8 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   ExpertsPlan o = {};
   uint64_t part = 0, counters = 0;
   if (!l.direct) {
-    p.tiles = (int32_t)ceil_div(a.f, 128);
+    if (!l.nothing) inner_tiles(a, l);
     q.tiles = (int32_t)ceil_div(a.n, 128);
-    p.rows = (int32_t)round_up(ceil_div(a.f, p.tiles ? p.tiles : 1), 8);
     q.rows = (int32_t)round_up(ceil_div(a.n, q.tiles), 8);
     p.features = (int32_t)a.f;
     q.features = (int32_t)a.n;
@@ -1101,7 +1147,7 @@ template <bool INNER, bool COPY>
 cudaError_t launch(const ProductParams &p, cudaStream_t s) {
   const cudaError_t e = dense_launch(product_kernel<INNER, COPY>, dim3(kSms), kAllThreads<COPY>,
                                      p.smem, 1, s, p);
-  if (e != cudaSuccess || p.nothing) return e;
+  if (e != cudaSuccess || p.nothing || p.whole) return e;
   const dim3 grid = INNER ? dim3(kSms) : dim3(p.tiles, (unsigned)ceil_div(p.tokens, kJoinTokens));
   return dense_launch(join_kernel<INNER>, grid, INNER ? 512 : 256, 0, 1, s, p);
 }
