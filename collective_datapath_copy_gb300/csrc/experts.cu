@@ -959,7 +959,7 @@ void inner_tiles(const coll_experts_t &a, Layout &l) {
     const double ns = (p.rows * 256.0 + l.cols * 128.0) / 45.0;
     return ns > 250.0 ? ns : 250.0;
   };
-  double cut[3], best = 1.0;
+  double cut[3], best = 0.97;  // nearly as long is not sure to save
   for (int i = 0; i < 3; ++i) {
     const double block = set(128), blocks = chunks[i] * p.tiles * kblocks / kSms;
     cut[i] = (blocks > kShort ? blocks : kShort) * block + 4000.0;
@@ -998,7 +998,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
            : l.tokens <= 16 ? 16
            : l.tokens <= 32 || spread ? 32
            : l.tokens <= 64 ? 64 : 128;
-  l.planned = !l.direct && (choices > kOwnChoices || !copied(a.x, a.m, a.k));
+  l.planned = !l.nothing && !l.direct && (choices > kOwnChoices || !copied(a.x, a.m, a.k));
   l.pack = !l.nothing && !l.direct && !copied(a.x, a.m, a.k);
   l.chunks = chosen + choices / l.cols;
   l.places = l.direct ? 8 * l.chunks : choices;
@@ -1066,7 +1066,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
       ring(q, 1, (uint32_t)l.tokens * 512u, l.outer_copied ? 0 : kRawBytes<false>, kAloneSmem);
     }
     const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
-    part = 2 * kSms * (inner > outer ? inner : outer);
+    part = l.nothing ? 0 : 2 * kSms * (inner > outer ? inner : outer);
   } else {
     l.inner_align = alignment(a.w_gate.ptr, a.w_gate.es, a.experts, a.w_gate.rs, a.f, a.k);
     const int up = alignment(a.w_up.ptr, a.w_up.es, a.experts, a.w_up.rs, a.f, a.k);
@@ -1152,10 +1152,8 @@ cudaError_t launch(const ProductParams &p, cudaStream_t s) {
   return dense_launch(join_kernel<INNER>, grid, INNER ? 512 : 256, 0, 1, s, p);
 }
 
-int run(const coll_experts_t &a, char *base, cudaStream_t s) {
-  Layout l;
-  int c = lay_out(a, l, base);
-  if (c) return c;
+int run(const coll_experts_t &a, Layout &l, cudaStream_t s) {
+  int c = COLL_OK;
   ProductParams &p = l.inner, &q = l.outer;
   DirectParams &d = l.few, &e = l.few_sums;
   if (!l.direct) {
@@ -1238,12 +1236,15 @@ extern "C" int64_t coll_gated_experts_workspace(const coll_experts_t *a) {
 }
 
 extern "C" int coll_gated_experts(const coll_experts_t *a, void *stream) {
-  const int64_t n = coll_gated_experts_workspace(a);
-  if (n < 0) return (int)n;
-  if (a->m == 0 || a->n == 0) return COLL_OK;
-  if (n && (!a->workspace || ((uintptr_t)a->workspace & 15u) ||
-            a->workspace_bytes < (uint64_t)n))
-    return COLL_EWORKSPACE;
+  if (!a) return COLL_EINVAL;
+  int c = coll::check(*a);
+  if (c || a->m == 0 || a->n == 0) return c;
+  // laid out from where the workspace starts, whether or not it is there or large enough
   char *base = reinterpret_cast<char *>(((uintptr_t)a->workspace + 127) & ~(uintptr_t)127);
-  return coll::run(*a, base, static_cast<cudaStream_t>(stream));
+  coll::Layout l;
+  c = coll::lay_out(*a, l, base);
+  if (c) return c;
+  if (!a->workspace || ((uintptr_t)a->workspace & 15u) || a->workspace_bytes < l.bytes + 128)
+    return COLL_EWORKSPACE;
+  return coll::run(*a, l, static_cast<cudaStream_t>(stream));
 }

@@ -165,6 +165,8 @@ class GatedExperts(_Dense):
         if not 0 <= first < 2 ** 31 - 4096:
             raise ValueError(f"first must be the id of an expert, not {first}")
         self.act, self.first = act, int(first)
+        self._sizes = (w_down.shape[1], K, F, E)
+        self._strides = tuple(w.stride()[:2] for w in (w_gate, w_up, w_down))
         self._start(w_gate.device)
 
     def forward(self, x, ids, weights, residual=None, out=None, out_dtype=None, stream=None):
@@ -176,8 +178,8 @@ class GatedExperts(_Dense):
         if stream is not None:
             with _on(stream, dev, (x, ids, weights, residual, out, wg, wu, wd, self._status)):
                 return self.forward(x, ids, weights, residual, out, out_dtype)
-        E, F, K = wg.shape
-        n, dt = wd.shape[1], wg.dtype
+        n, K, F, E = self._sizes
+        dt = wg.dtype
         xm = _read(x, None, K, dt, dev, "x", keep)
         m = _row_count(x)
         if ids.dim() == 0:
@@ -197,11 +199,11 @@ class GatedExperts(_Dense):
             if residual.shape != out.shape:
                 residual = residual.expand(out.shape)
             rm = _read(residual, m, n, ot, dev, "residual", keep)
+        gs, us, ds = self._strides
         self._launch("coll_gated_experts", _EXPERTS.pack,
                      (m, n, K, F, E, self.first, top, _TYPE[dt], _TYPE[ot], ACT[self.act],
-                      wg.data_ptr(), wg.stride(0), wg.stride(1),
-                      wu.data_ptr(), wu.stride(0), wu.stride(1),
-                      wd.data_ptr(), wd.stride(0), wd.stride(1), *xm, *im, *sm, *rm, *ym))
+                      wg.data_ptr(), *gs, wu.data_ptr(), *us, wd.data_ptr(), *ds, *xm, *im, *sm,
+                      *rm, *ym))
         return out
 
     __call__ = forward

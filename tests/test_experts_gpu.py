@@ -200,6 +200,28 @@ def test_all_choose_the_same(m, top):
     check(op, x, ids, w)
 
 
+@pytest.mark.parametrize("k,f", [(128, 72), (131, 75)])
+@pytest.mark.parametrize("m", [40, 100, 128])
+def test_a_hot_expert_among_many(m, k, f):
+    """More tokens on one expert than a chunk has columns, where the others have one or none."""
+    g = gen(m + k)
+    op = cdc.GatedExperts(*stacks(g, 64, 136, k, f, BF))
+    ids, w = routing(g, m, 64, 3)
+    ids[:, 1] = 7
+    ids[::3, 2] = 63
+    check(op, normal(g, m, k, dtype=BF), ids, w)
+
+
+@pytest.mark.parametrize("m,E,top,k,f", [(128, 40, 32, 64, 72), (128, 1024, 32, 64, 8),
+                                         (97, 1000, 7, 72, 40), (33, 300, 20, 67, 9),
+                                         (8, 1024, 4, 64, 16), (3, 1024, 32, 64, 16)])
+def test_many_experts_and_choices(m, E, top, k, f):
+    g = gen(E + top)
+    op = cdc.GatedExperts(*stacks(g, E, 72, k, f, BF))
+    ids, w = routing(g, m, E, top)
+    check(op, normal(g, m, k, dtype=BF), ids, w)
+
+
 def test_nan_stays_where_it_is():
     g = gen(6)
     wg, wu, wd = stacks(g, 8, 136, 128, 72, BF)
