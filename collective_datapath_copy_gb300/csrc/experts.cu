@@ -159,7 +159,7 @@ constexpr int kThreads = 192;  // warp 0 loads, 1 matrix instructions and TMEM, 
 constexpr int kLoaders = 16;   // more warps, where no tensor copy takes the weights as they lie
 template <bool COPY>
 constexpr int kAllThreads = kThreads + (COPY ? 0 : 32 * kLoaders);
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 16;
 constexpr uint32_t kTile = 128 * 128;  // bytes of 128 rows of one k block
 constexpr uint32_t kShort = 8;
 
@@ -176,7 +176,7 @@ struct ProductParams {
   int32_t features;     // of the product
   int32_t tiles, kblocks, cols, tokens;
   int32_t stages;
-  uint32_t stage_bytes, ring, raw, smem;  // raw: where the loader warps' rings start
+  uint32_t w_bytes, stage_bytes, ring, raw, smem;  // raw: where the loader warps' rings start
   int32_t type, out_type, act;
   int32_t nothing;      // sums of nothing: y = residual
   int32_t whole;        // inner: no tile is cut
@@ -424,7 +424,7 @@ __device__ __forceinline__ void load_weights(const ProductParams &p, const PlanV
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   const uint32_t from = raw + sub * kRawRow + chunk * 16;
-  const uint32_t to = ring + w * kTile + (first + sub) * 128 + ((chunk ^ sub) << 4);
+  const uint32_t to = ring + w * p.w_bytes + (first + sub) * 128 + ((chunk ^ sub) << 4);
   uint32_t s = 0, phase = 0, slot = 0;
   bool ok = true;
   for (uint32_t i = 0; i < n; ++i) {
@@ -558,7 +558,7 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
       if (!COPY) return;
 #pragma unroll
       for (int w = 0; w < W; ++w)
-        tma_box3(at + w * kTile, &p.w[w], kb * kTileK, q.tile * p.rows, c.x, bar);
+        tma_box3(at + w * p.w_bytes, &p.w[w], kb * kTileK, q.tile * p.rows, c.x, bar);
     };
     for (uint32_t v = u; COPY && v < end && early < stages;) {
       const Piece q = piece_at<INNER>(p, plan, v, end);
@@ -585,7 +585,7 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
                         q4[i + 3 < c.z ? i + 3 : 0]);
       }
       for (int kb = q.k0; kb < q.k1; ++kb) {
-        const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes + W * kTile;
+        const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes + W * p.w_bytes;
         if (early == 0) {
           ok = ok && wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status);
           if (elect_one() && ok) weights(q, c, kb);
@@ -609,7 +609,8 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
     }
   } else if (warp == 1) {
     const uint32_t hi = desc_hi(1024), step = stage_bytes >> 4;
-    uint32_t a = desc_lo(ring, 16u), b = desc_lo(ring + W * kTile, 16u);
+    uint32_t a = desc_lo(ring, 16u), b = desc_lo(ring + W * p.w_bytes, 16u);
+    const uint32_t second = p.w_bytes >> 4;
     uint32_t s = 0, phase = 0, d = 0, dphase = 0;
     bool ok = true;
     while (u < end) {
@@ -628,7 +629,7 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
           for (uint32_t i = 0; i < 4; ++i) {
             mma_f16<1>(d0, a + 2 * i, hi, b + 2 * i, hi, idesc, i ? 1u : add);
             if (INNER)
-              mma_f16<1>(d1, a + (kTile >> 4) + 2 * i, hi, b + 2 * i, hi, idesc, i ? 1u : add);
+              mma_f16<1>(d1, a + second + 2 * i, hi, b + 2 * i, hi, idesc, i ? 1u : add);
           }
           mma_commit<1>(empty0 + 8 * s, 0);
         }
@@ -944,8 +945,8 @@ struct Layout {
 // launch that joins them (16 tokens of two, eight experts of 4096 x 1792: 66 us against 68.5; 32
 // tokens, 64 of 2048 x 176: 36.7 against 39.4): whole if that takes less time for as many experts as
 // uniform choices come to, one more and all of them (four tokens, of eight experts, six of which were
-// chosen where 5.3 were expected: 61 us whole, 50 cut). A k block takes its bytes at 45 a ns or 250 ns
-// to issue; what cutting costs, 4 us.
+// chosen where 5.3 were expected: 61 us whole, 50 cut). A k block takes its bytes at 45 a ns or 300 ns
+// to issue; what cutting costs, 6 us.
 void inner_tiles(const coll_experts_t &a, Layout &l) {
   ProductParams &p = l.inner;
   const double choices = (double)l.tokens * a.top, e = (double)a.experts;
@@ -957,12 +958,12 @@ void inner_tiles(const coll_experts_t &a, Layout &l) {
     p.tiles = (int32_t)ceil_div(a.f, rows);
     p.rows = (int32_t)round_up(ceil_div(a.f, p.tiles), 8);
     const double ns = (p.rows * 256.0 + l.cols * 128.0) / 45.0;
-    return ns > 250.0 ? ns : 250.0;
+    return ns > 300.0 ? ns : 300.0;
   };
   double cut[3], best = 0.97;  // nearly as long is not sure to save
   for (int i = 0; i < 3; ++i) {
     const double block = set(128), blocks = chunks[i] * p.tiles * kblocks / kSms;
-    cut[i] = (blocks > kShort ? blocks : kShort) * block + 4000.0;
+    cut[i] = (blocks > kShort ? blocks : kShort) * block + 6000.0;
   }
   int64_t rows = 128;
   for (int64_t r = 16; r <= 128; r += 8) {
@@ -1040,13 +1041,15 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     p.act = (int32_t)a.act;
     p.status = q.status = a.status;
     auto ring = [&](ProductParams &r, int w, uint32_t fixed, uint32_t raw, uint32_t room) {
-      r.stage_bytes = w * kTile + (uint32_t)l.cols * 128u;
-      r.stages = (int32_t)((room - 1024 - fixed - raw) / r.stage_bytes);
+      r.w_bytes = (uint32_t)r.rows * 128u;
+      r.stage_bytes = w * r.w_bytes + (uint32_t)l.cols * 128u;
+      // a matrix instruction reads 128 rows whatever a tile has: slack behind the last stage's
+      const uint32_t other = 1024 + kTile - r.w_bytes + fixed + raw;
+      r.stages = (int32_t)((room - other) / r.stage_bytes);
       if (r.stages > kMaxStages) r.stages = kMaxStages;
-      if (raw && r.stages > 3) r.stages = 3;
       r.ring = r.stages * r.stage_bytes;
       r.raw = r.ring + fixed;
-      r.smem = 1024 + r.ring + fixed + raw;
+      r.smem = r.ring + other;
     };
     auto by_hand = [&](ProductParams &r, int w, const coll_stack_t &m, int64_t rows, int64_t len) {
       r.stack[w] = static_cast<const uint16_t *>(m.ptr);

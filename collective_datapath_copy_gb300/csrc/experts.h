@@ -20,7 +20,7 @@ struct ExpertsPlan {
 
 // One to a few tokens of few choices (experts_direct.cu).
 constexpr int kDirectChoices = 32;  // that a warp sorts by itself
-constexpr int kDirectTokens = 8;
+constexpr int kDirectTokens = 32;
 
 struct DirectParams {
   const uint16_t *w[2];  // gate and up, or down
