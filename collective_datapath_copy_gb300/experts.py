@@ -30,6 +30,7 @@ _ROUTE = struct.Struct("6qd9q")
 _ROUTE_BWD = struct.Struct("6qd12q")
 _EXPERTS = struct.Struct("37q")
 _LOGITS = (torch.float32, torch.bfloat16, torch.float16)
+_entries = {}
 
 dense._MASK["coll_gated_experts"] = _mask("." * 10 + "a.." * 8)
 
@@ -76,10 +77,10 @@ class Router:
             raise ValueError(f"scale must be finite, not {scale}")
         self.top_k, self.score = int(top_k), score
         self.normalize, self.scale = bool(normalize), float(scale)
+        self._how = (_lib.SCORE[score], int(self.normalize), self.scale)
 
     def _head(self, t, e, dtype):
-        return (t, e, self.top_k, _TYPE[dtype], _lib.SCORE[self.score], int(self.normalize),
-                self.scale)
+        return (t, e, self.top_k, _TYPE[dtype], *self._how)
 
     @staticmethod
     def _logits(logits):
@@ -96,7 +97,10 @@ class Router:
         if dense._current_device() != dev:
             with torch.cuda.device(dev):
                 return Router._launch(where, packed, dev)
-        code = getattr(lib(), where)(packed, dense._raw_stream(dev))
+        fn = _entries.get(where)
+        if fn is None:
+            fn = _entries[where] = getattr(lib(), where)
+        code = fn(packed, dense._raw_stream(dev))
         if code:
             check(code, where)
 

@@ -224,6 +224,7 @@ class Machine:
         monkeypatch.setattr(dense, "_current_device", lambda: self.current)
         monkeypatch.setattr(dense, "_raw_stream", lambda d: 100 + d)
         monkeypatch.setattr(experts, "lib", Library)
+        monkeypatch.setattr(experts, "_entries", {})
 
 
 @pytest.mark.parametrize("current", [0, 1])
