@@ -1094,7 +1094,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     auto warps = [](int64_t steps) { return (uint32_t)(steps > 28 ? 8 : (steps + 3) / 4); };
     d.warps = warps(ceil_div(a.k, 64));
     const int64_t steps = l.chunks * ceil_div(a.f, 64);
-    int64_t splits = ceil_div(2 * kSms, e.tiles);
+    int64_t splits = 2 * kSms / e.tiles;
     if (splits > steps / 16) splits = steps / 16;
     if (splits > 32) splits = 32;
     if (splits < 1) splits = 1;

@@ -75,9 +75,12 @@ class Router:
             raise ValueError(f"score must be one of {tuple(_lib.SCORE)}, not {score!r}")
         if not math.isfinite(scale):
             raise ValueError(f"scale must be finite, not {scale}")
-        self.top_k, self.score = int(top_k), score
-        self.normalize, self.scale = bool(normalize), float(scale)
-        self._how = (_lib.SCORE[score], int(self.normalize), self.scale)
+        self.top_k, self._score = int(top_k), score
+        self._how = (_lib.SCORE[score], int(bool(normalize)), float(scale))
+
+    score = property(lambda self: self._score)
+    normalize = property(lambda self: bool(self._how[1]))
+    scale = property(lambda self: self._how[2])
 
     def _head(self, t, e, dtype):
         return (t, e, self.top_k, _TYPE[dtype], *self._how)
@@ -157,9 +160,8 @@ class GatedExperts(_Dense):
     outside [first, first + E) are passed over."""
 
     def __init__(self, w_gate, w_up, w_down, act="silu", first=0):
-        self.w_gate = _stack("w_gate", w_gate)
-        self.w_up = _stack("w_up", w_up, w_gate)
-        self.w_down = _stack("w_down", w_down, w_gate)
+        self._w = (_stack("w_gate", w_gate), _stack("w_up", w_up, w_gate),
+                   _stack("w_down", w_down, w_gate))
         E, F, K = w_gate.shape
         if w_up.shape != w_gate.shape or w_down.shape[0] != E or w_down.shape[2] != F:
             raise ValueError(f"w_up must be {(E, F, K)} and w_down {(E, 'N', F)}, not "
@@ -173,12 +175,18 @@ class GatedExperts(_Dense):
         self._strides = tuple(w.stride()[:2] for w in (w_gate, w_up, w_down))
         self._start(w_gate.device)
 
+    # one object, one set of stacks: their sizes and strides are taken once
+    w_gate = property(lambda self: self._w[0])
+    w_up = property(lambda self: self._w[1])
+    w_down = property(lambda self: self._w[2])
+
     def forward(self, x, ids, weights, residual=None, out=None, out_dtype=None, stream=None):
         """x [..., K], ids [..., top] (int32) and weights [..., top] (binary32) -> y [..., N].
         out_dtype: the operands' type or torch.float32 (a partial for a binary32 sum; its residual
         is float32 too). residual may be `out` itself. The chosen experts' weights are read once for
         every 128 tokens."""
-        wg, wu, wd, dev, keep = self.w_gate, self.w_up, self.w_down, self._dev, []
+        wg, wu, wd = self._w
+        dev, keep = self._dev, []
         if stream is not None:
             with _on(stream, dev, (x, ids, weights, residual, out, wg, wu, wd, self._status)):
                 return self.forward(x, ids, weights, residual, out, out_dtype)
