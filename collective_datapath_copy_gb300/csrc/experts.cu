@@ -915,10 +915,6 @@ int alignment(const void *base, int64_t es, int64_t e, int64_t rs, int64_t rows,
   return v % 32 == 0 ? 32 : v % 16 == 0 ? 16 : v % 4 == 0 ? 4 : 2;
 }
 
-// Bytes of the weights that a call may read up to which the kernels without staging are faster (their
-// comment has both sides).
-constexpr double kDirectBytes = 100 << 20;
-
 // Shared memory for the products. Up to 64 tokens the sums' CTAs fit beside those of the inner values
 // (all an SM has is 228 KB, of which a CTA takes 1 KB and its static arrays beside what it asks for):
 // three stages of the inner ring, two where a stage has room for 64 tokens.
@@ -989,8 +985,8 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   const int64_t choices = l.tokens * a.top;
   const bool rows = a.x.cs == 1 || a.k == 1;
   const int64_t chosen = a.experts < choices ? a.experts : choices;
-  l.direct = !l.nothing && l.tokens <= kDirectTokens && choices <= kDirectChoices && rows &&
-             2.0 * chosen * a.f * (2.0 * a.k + a.n) <= kDirectBytes;
+  l.direct = !l.nothing && rows && l.tokens <= kDirectTokens && choices <= kDirectChoices &&
+             ceil_div(a.f, kDirectInner) * (chosen + choices / 8) < 0x7FFFFFFF;
   l.inner_copied = copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f);
   l.outer_copied = copied(a.w_down, a.experts, a.n);
   // columns of a chunk: all tokens, or 32 where the experts have fewer than half as many each

@@ -3,11 +3,14 @@
 // one expert is the columns of a fragment, 16 rows of weights its rows (inner: eight of gate and eight
 // of up, so a lane ends up with g and u of the same feature).
 //
-// Bound by latency and HBM: two launches, the chunks made by a warp of every CTA from the ids alone,
-// the sums' first weights asked for while the inner values are still being made. One token, six of 64
-// experts of 2048 x 176 (13 MB): 8 us, where the tensor-core kernels' cut tiles and joins take 18; 16
-// choices of 16 experts of 1024 x 512 18 against 20; from some 100 MB on those are as fast or faster
-// (eight experts of 7168 x 2048: 115 us against 120).
+// Bound by HBM, and for small experts by latency: two launches, the chunks made by a warp of every CTA
+// from the ids alone, the sums' first weights asked for while the inner values are still being made, the
+// sums' CTAs all on the SMs at once (two waves of them: 24 us where one takes 19, two experts of 4096 x
+// 1792). One token, six of 64 experts of 2048 x 176 (13 MB): 8.3 us, where the tensor-core kernels' cut
+// tiles and joins take 18; two tokens, four of eight experts of 4096 x 14336: 177 us (7 TB/s) against
+// 192; 16 tokens of two, eight of 4096 x 1792: 57 against 63. With more choices a CTA's plan takes
+// longer and an expert's choices fill more chunks: 48 choices within 3 % either way, 96 of 16 experts of
+// 7168 x 2048 224 against 219.
 #include "dense_direct.cuh"
 #include "dense_epi.cuh"
 #include "dense_tc.h"

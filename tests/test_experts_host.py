@@ -117,7 +117,9 @@ def test_what_a_call_launches(rt):
     for v, want in ((call(1, 2048, 2048, 176, 64, 6), DIRECT),
                     (call(5, 1001, 1001, 517, 20, 4), DIRECT),
                     (call(5, 64, 64, 64, 3, 2, off=2), DIRECT),
-                    (call(1, 7168, 7168, 2048, 32, 8), CUT),            # past the direct kernels' bytes
+                    (call(1, 7168, 7168, 2048, 32, 8), DIRECT), (call(16, 4096, 4096, 1792, 8, 2), DIRECT),
+                    (call(17, 4096, 4096, 14336, 8, 2), CUT),        # 34 choices
+                    (call(5, 64, 64, 14336, 3, 2, x=(4 * A, 200, 3)), ["plan_kernel", CUT[0]] + CUT[2:]),
                     (call(9, 64, 64, 64, 3, 2), None),
                     (call(128, 4096, 4096, 14336, 8, 2), CUT),
                     (call(128, 4096, 4096, 14336, 8, 3), ["plan_kernel"] + CUT),  # 384 choices
