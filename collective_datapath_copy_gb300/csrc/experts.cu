@@ -3,13 +3,17 @@
 //   h_ij = act(gate_e x_i) (up_e x_i),  y_i = residual_i + sum over j of weights_ij down_e h_ij,
 //   e = ids_ij - first
 //
-// Bound by HBM: the weights of every chosen expert are read once, 6 n f bytes each (n = k), and a
-// token or two an expert multiply them. Three launches: plan_kernel sorts the choices by expert;
-// product_kernel<true> computes the inner values, product_kernel<false> the sums. Both are
-// persistent, a CTA an SM, and share their work to the k block: the list of (expert, tile of 128
-// features) is one line of k blocks that is cut into 152 equal lengths, because whole tiles would
-// leave SMs idle (8 experts of 2048 inner features are 128 tiles). A tile that is cut joins in the
-// last of its CTAs to arrive, in the order of k: nothing waits, and results do not depend on timing.
+// Bound by HBM: the weights of every chosen expert are read once, 4 f k + 2 n f bytes each, and a token
+// or a few an expert multiply them. Up to 32 choices go to experts_direct.cu. Here the weights are the
+// 128-row operand of tcgen05 and an expert's tokens its columns: product_kernel<true> computes the
+// inner values, product_kernel<false> the sums. Both are persistent, a CTA an SM, and share their work
+// to the k block: the list of (expert, tile of 128 features) is one line of k blocks that is cut into
+// 152 equal lengths, because whole tiles would leave SMs idle (8 experts of 2048 inner features are
+// 128 tiles). The shares of a tile that was cut join in a launch behind, in the order of k: nothing
+// waits, and results do not depend on timing. Measured: 128 tokens of two, eight experts of 4096 x 14336
+// (2.8 GB) 447 us, 6.3 TB/s; a chunk of 32 choices of 256, of which this call has 32 experts of 7168 x
+// 2048 284 us, 6.3 TB/s; 16 to 128 tokens over weights of some MB 18 to 25 us, which is the chain of the
+// launches: plan 2 us, first weights 3, inner values, join 4, sums, join 4.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -187,8 +191,8 @@ struct ProductParams {
 };
 
 // A plan of few choices, made by every CTA that goes by it: no launch and no way through memory
-// before the first weights are asked for (16 tokens of two, eight experts of 4096 x 1792: 71 us with
-// plan_kernel, 67 so).
+// before the first weights are asked for (32 choices of eight experts of 4096 x 1792: 71 us with
+// plan_kernel, 67 so, when those came here).
 constexpr int kOwnChoices = 256;
 
 struct OwnPlan {
@@ -938,9 +942,9 @@ struct Layout {
 };
 
 // Rows of the inner tiles. 128 and cut where a CTA's length ends, or fewer and whole, which saves the
-// launch that joins them (16 tokens of two, eight experts of 4096 x 1792: 66 us against 68.5; 32
-// tokens, 64 of 2048 x 176: 36.7 against 39.4): whole if that takes less time for as many experts as
-// uniform choices come to, one more and all of them (four tokens, of eight experts, six of which were
+// launch that joins them (32 choices of eight experts of 4096 x 1792: 66 us against 68.5; 32 tokens of
+// six, 64 of 2048 x 176: 36.7 against 39.4): whole if that takes less time for as many experts as
+// uniform choices come to, one more and all of them (eight choices of eight experts, six of which were
 // chosen where 5.3 were expected: 61 us whole, 50 cut). A k block takes its bytes at 45 a ns or 300 ns
 // to issue; what cutting costs, 6 us.
 void inner_tiles(const coll_experts_t &a, Layout &l) {

@@ -93,7 +93,8 @@ def moe_dispatch(routing: np.ndarray, experts_per_rank: int, hidden: int,
     """All-to-all with uneven splits from a routing table [R, T, k] of expert ids.
 
     Token (s, t) is name s*T+t (its row of `hidden` elements on rank s). It is copied once
-    to every rank hosting one of its experts (expert e lives on rank e // experts_per_rank);
+    to every rank hosting one of its experts (expert e lives on rank e // experts_per_rank; an id
+    of -1, a choice that was not made, is no expert);
     at a destination, rows are ordered by (source rank, source token). meta["counts"] holds
     the rows each rank receives.
     """
@@ -102,7 +103,9 @@ def moe_dispatch(routing: np.ndarray, experts_per_rank: int, hidden: int,
     tok = np.arange(T)
     for s in range(R):
         for j in range(k):
-            dest[s, tok, routing[s, :, j] // experts_per_rank] = True
+            e = routing[s, :, j]
+            there = e >= 0
+            dest[s, tok[there], e[there] // experts_per_rank] = True
     names = np.arange(R * T)
     i = _segs_cols(np.repeat(np.arange(R), T), np.tile(tok, R) * hidden, np.full(R * T, hidden),
                    names)

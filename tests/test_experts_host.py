@@ -3,11 +3,12 @@ call launches over a fake CUDA runtime, workspaces, and which device a Python ca
 
 import contextlib
 
+import numpy as np
 import pytest
 import torch
 
 import fake_cuda
-from collective_datapath_copy_gb300 import _lib, dense, experts
+from collective_datapath_copy_gb300 import _lib, dense, experts, namings
 
 D = _lib.D
 BF, HF, F32 = D["COLL_BF16"], D["COLL_F16"], D["COLL_F32"]
@@ -271,6 +272,14 @@ def test_arguments_before_any_device_is_asked():
         experts.Router(0)
     with pytest.raises(ValueError, match="score"):
         experts.Router(2, "max")
+
+
+def test_choices_that_were_not_made_go_to_no_rank():
+    """The router's table as moe_dispatch takes it: -1 ends the choices of a token with few experts."""
+    routing = np.array([[[3, 0], [1, -1]], [[-1, -1], [2, 3]]], dtype=np.int32)
+    nm = namings.moe_dispatch(routing, 2, 4)
+    assert nm.meta["counts"] == [2, 2]
+    assert nm.rows("out") == [(0, 0, 4, 0), (0, 4, 4, 1), (1, 0, 4, 0), (1, 4, 4, 3)]
 
 
 def test_the_structures_are_as_long_as_the_header_says():
