@@ -188,6 +188,7 @@ struct ProductParams {
   int64_t es[2], rs[2];
   uintptr_t stack_end[2];
   int32_t len;               // elements of a row of them
+  int32_t lines;             // places of the loader warps' rings
 };
 
 // A plan of few choices, made by every CTA that goes by it: no launch and no way through memory
@@ -323,16 +324,16 @@ __device__ __forceinline__ Piece piece_at(const ProductParams &p, const PlanView
 }
 
 // Loader warps: the weights of this CTA's k blocks from rows that start anywhere, into the layout that a
-// tensor copy with a 128-byte swizzle gives. The nine aligned 16-byte words around a row's 128 bytes are
-// copied asynchronously into a ring of the warp's own, kRaw k blocks ahead (loads into registers kept
-// too little on its way: 2.1 TB/s), and from there a lane shifts two into the 16 bytes it stores.
-template <bool INNER>
-constexpr int kRaw = INNER ? 2 : 3;
+// tensor copy with a 128-byte swizzle gives. A row's 128-byte lines are copied asynchronously into a ring
+// of the warp's own, each once: a k block's 128 bytes are the end of one and the start of the next. (Nine
+// words around each k block instead straddle two lines, 13 shared-memory wavefronts a copy instruction
+// where whole lines take four; loads into registers kept too little on its way, 2.1 TB/s.) From there a
+// lane shifts two words into the 16 bytes it stores. A warp takes every eighth row, so that all of its
+// rows start alike within 16 bytes and the shift is the warp's.
 template <bool INNER>
 constexpr int kLoaderRows = (INNER ? 2 : 1) * 128 / kLoaders;
-constexpr int kRawRow = 144;  // bytes
 template <bool INNER>
-constexpr uint32_t kRawBytes = kLoaders * kLoaderRows<INNER> * kRawRow * kRaw<INNER>;
+constexpr uint32_t kLineBytes = kLoaders * kLoaderRows<INNER> * 128;  // of one line of all rows
 
 // The aligned 16-byte word at `from` to shared memory: those of its bytes that are [lo, hi), and zeros.
 __device__ __forceinline__ void copy_word(uint32_t to, uintptr_t from, uintptr_t lo, uintptr_t hi) {
@@ -351,133 +352,158 @@ __device__ __forceinline__ void copy_word(uint32_t to, uintptr_t from, uintptr_t
   }
 }
 
-template <bool INNER>
+// 16 bytes that start 4 S bytes and `bits` bits into the first of two words, from shared memory to `to`,
+// for `rows` rows of this lane, of which `left` elements each are there.
+template <int S, int STEPS>
+__device__ __forceinline__ void shift_words(uint32_t raw, const uint32_t (&at)[STEPS],
+                                            const uint32_t (&next)[STEPS], uint32_t to, int rows,
+                                            int left, uint32_t bits) {
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    uint32_t e[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(e[4 * h]), "=r"(e[4 * h + 1]), "=r"(e[4 * h + 2]), "=r"(e[4 * h + 3])
+                   : "r"(raw + (h ? next[j] : at[j])));
+    uint32_t r[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) r[x] = __funnelshift_r(e[x + S], e[x + S + 1], bits);
+    if (left < 8) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        r[x] = 2 * x + 1 < left ? r[x] : 2 * x < left ? r[x] & 0xFFFFu : 0u;
+    }
+    if (j < rows)
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + j * 4096), "r"(r[0]),
+                   "r"(r[1]), "r"(r[2]), "r"(r[3])
+                   : "memory");
+  }
+}
+
+// LINES: places of a warp's ring, a power of two. The k block that is next needs two lines in a row, and
+// all that the ring has room for are asked for.
+template <bool INNER, int LINES>
 __device__ __forceinline__ void load_weights(const ProductParams &p, const PlanView &plan,
                                              uint32_t u, uint32_t end, uint32_t ring,
                                              uint32_t raw, uint32_t full0, uint32_t empty0,
                                              Shared &sh, int loader, int lane) {
-  constexpr int ROWS = kLoaderRows<INNER>, STEPS = ROWS / 4, DEPTH = kRaw<INNER>;
-  constexpr int WORDS = (ROWS * 9 + 31) / 32;
-  const int w = INNER ? loader / (kLoaders / 2) : 0;
-  const int first = loader * ROWS & 127;  // of this warp's rows in a tile
+  constexpr int ROWS = kLoaderRows<INNER>, STEPS = ROWS / 4;
+  constexpr uint32_t LINE = ROWS * 128, ALL = LINES * LINE;
+  const int w = INNER ? loader >> 3 : 0;
+  // this warp's rows of a tile: first, first + 8, ...
+  const int first = (loader & 7) + (INNER ? 0 : (loader >> 3) * 8 * ROWS);
   const int sub = lane >> 3, chunk = lane & 7;
   const uintptr_t lo = (uintptr_t)p.stack[w], hi = p.stack_end[w];
-  const int64_t pitch = p.rs[w] * 2;
-  raw += loader * ROWS * kRawRow * DEPTH;
-  // Two places on this CTA's length, `ahead` DEPTH k blocks before `now`. All that does not change
-  // from one k block of a tile to the next is made once.
+  const int64_t pitch = p.rs[w] * 16;  // bytes from one of them to the next
+  raw += loader * ALL;
+  // Two places on this CTA's length, `ahead` by lines and `now` by k blocks. All that does not change
+  // from one to the next of a tile is made once.
   struct Place {
     uint32_t v;
     int kb, kb1, rows;
-    uintptr_t tile;
+    uintptr_t row;
   } ahead = {u, 0, 0, 0, 0}, now = {u, 0, 0, 0, 0};
   auto begin = [&](Place &c) {
     const Piece q = piece_at<INNER>(p, plan, c.v, end);
     c.kb = q.k0, c.kb1 = q.k1;
     c.v += q.k1 - q.k0;
     const int f = q.tile * p.rows;
-    c.rows = min(p.rows, p.features - f) - first;  // of this warp's that are the tile's
-    c.tile = lo + (uintptr_t)(plan.chunk[q.chunk].x * p.es[w] + (int64_t)(f + first) * p.rs[w]) * 2;
+    c.rows = min(ROWS, (min(p.rows, p.features - f) - first + 7) >> 3);  // this warp's
+    c.row = lo + (uintptr_t)(plan.chunk[q.chunk].x * p.es[w] + (int64_t)(f + first) * p.rs[w]) * 2;
   };
-  uintptr_t word[WORDS];  // this lane's words of the k block ahead
-  bool inside = false;    // all of the warp's words of these k blocks are the stack's
+  uintptr_t word[STEPS];  // this lane's of the line ahead; of rows that are not there, the last one's
+  bool inside = false;    // all of the warp's lines of this tile are the stack's
+  int lines = 0;          // of it that are still to be asked for
   auto begin_ahead = [&]() {
     if (ahead.v >= end) return;
     begin(ahead);
+    lines = ahead.kb1 - ahead.kb + 1;
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      const int row = (i * 32 + lane) / 9;
-      word[i] = ((ahead.tile + row * pitch) & ~(uintptr_t)15) + ahead.kb * (2 * kTileK) +
-                (i * 32 + lane - 9 * row) * 16;
+    for (int j = 0; j < STEPS; ++j) {
+      const int row = min(4 * j + sub, max(ahead.rows, 1) - 1);
+      word[j] = ((ahead.row + row * pitch) & ~(uintptr_t)127) + ahead.kb * 128 + chunk * 16;
     }
-    const uintptr_t last = ahead.tile + (min(ROWS, max(ahead.rows, 1)) - 1) * pitch;
-    inside = (ahead.tile & ~(uintptr_t)15) >= lo &&
-             (last & ~(uintptr_t)15) + ahead.kb1 * (2 * kTileK) + 16 <= hi;
+    const uintptr_t last = ahead.row + (max(ahead.rows, 1) - 1) * pitch;
+    inside = (ahead.row & ~(uintptr_t)127) >= lo &&
+             (last & ~(uintptr_t)127) + (ahead.kb1 + 1) * 128 <= hi;
   };
-  auto ask = [&](uint32_t slot) {
-    const uint32_t to = raw + slot * (ROWS * kRawRow);
+  auto ask = [&](uint32_t place) {
+    if (lines > 0) {
+      const uint32_t to = raw + place + sub * 128 + chunk * 16;
+      if (ahead.rows > 0) {
+        if (inside) {
 #pragma unroll
-    for (int i = 0; i < WORDS; ++i) {
-      const int at = i * 32 + lane, row = at / 9;  // rows of nine words, one behind the other
-      if (row < min(ROWS, ahead.rows)) {
-        if (inside)
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + at * 16),
-                       "l"(word[i])
-                       : "memory");
-        else
-          copy_word(to + at * 16, word[i], lo, hi);
+          for (int j = 0; j < STEPS; ++j)
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + j * 512),
+                         "l"(word[j])
+                         : "memory");
+        } else {
+#pragma unroll
+          for (int j = 0; j < STEPS; ++j) copy_word(to + j * 512, word[j], lo, hi);
+        }
       }
-      word[i] += 2 * kTileK;
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) word[j] += 128;
+      if (--lines == 0) begin_ahead();
     }
-    if (++ahead.kb == ahead.kb1) begin_ahead();
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  uint32_t shift[STEPS];  // bytes, of this lane's rows
+  int shift = 0, rows = 0;           // elements; rows of this lane
+  uint32_t at[STEPS], next[STEPS];   // its words of this k block in the ring
+  uint32_t place = 0;                // of the k block's first line
   auto begin_now = [&]() {
     if (now.v >= end) return;
     begin(now);
+    shift = (int)(now.row >> 1 & 7);
+    rows = (now.rows - sub + 3) >> 2;
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j)
-      shift[j] = ((uint32_t)now.tile + (uint32_t)(4 * j + sub) * (uint32_t)pitch) & 15u;
+    for (int j = 0; j < STEPS; ++j) {
+      const int64_t row = 4 * j + sub;
+      const uint32_t off = (uint32_t)((now.row + row * pitch) & 112u) + chunk * 16;
+      auto in_ring = [&](uint32_t o) {
+        return (place + (o >> 7) * LINE) % ALL + (uint32_t)row * 128 + (o & 127u);
+      };
+      at[j] = in_ring(off);
+      next[j] = in_ring(off + 16);
+    }
   };
   const uint32_t n = end - u;
   begin_ahead();
   begin_now();
 #pragma unroll
-  for (int d = 0; d < DEPTH; ++d) {
-    if (d < n) ask(d);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-  }
-  const uint32_t from = raw + sub * kRawRow + chunk * 16;
-  const uint32_t to = ring + w * p.w_bytes + (first + sub) * 128 + ((chunk ^ sub) << 4);
-  uint32_t s = 0, phase = 0, slot = 0;
+  for (int d = 0; d < LINES; ++d) ask(d * LINE);
+  const uint32_t to0 = ring + w * p.w_bytes + (first + 8 * sub) * 128 + ((chunk ^ (loader & 7)) << 4);
+  uint32_t s = 0, phase = 0;
   bool ok = true;
   for (uint32_t i = 0; i < n; ++i) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
+    asm volatile("cp.async.wait_group %0;" ::"n"(LINES - 2) : "memory");
     __syncwarp();
     ok = ok && __all_sync(~0u, wait_bar(&sh.abort, empty0 + 8 * s, phase ^ 1u, p.status));
     if (ok) {
       const int left = p.len - now.kb * kTileK - chunk * 8;
-#pragma unroll
-      for (int j = 0; j < STEPS; ++j) {
-        uint32_t e[8];
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(e[4 * h]), "=r"(e[4 * h + 1]), "=r"(e[4 * h + 2]), "=r"(e[4 * h + 3])
-                       : "r"(from + (slot * ROWS + 4 * j) * kRawRow + 16 * h));
-        const uint32_t o = shift[j];
-        if (o & 8) {
-#pragma unroll
-          for (int x = 0; x < 6; ++x) e[x] = e[x + 2];
-        }
-        if (o & 4) {
-#pragma unroll
-          for (int x = 0; x < 5; ++x) e[x] = e[x + 1];
-        }
-        uint32_t r[4];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) r[x] = __funnelshift_r(e[x], e[x + 1], (o & 2) * 8);
-        if (left < 8) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-            r[x] = 2 * x + 1 < left ? r[x] : 2 * x < left ? r[x] & 0xFFFFu : 0u;
-        }
-        if (4 * j + sub < now.rows)
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           (to + s * p.stage_bytes + j * 512) ^ ((j & 1) << 6)),
-                       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
-                       : "memory");
-      }
+      const uint32_t to = to0 + s * p.stage_bytes, bits = (uint32_t)(shift & 1) * 16;
+      if (shift < 2) shift_words<0, STEPS>(raw, at, next, to, rows, left, bits);
+      else if (shift < 4) shift_words<1, STEPS>(raw, at, next, to, rows, left, bits);
+      else if (shift < 6) shift_words<2, STEPS>(raw, at, next, to, rows, left, bits);
+      else shift_words<3, STEPS>(raw, at, next, to, rows, left, bits);
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (elect_one())
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(full0 + 8 * s) : "memory");
     }
     __syncwarp();
-    if (i + DEPTH < n) ask(slot);
-    asm volatile("cp.async.commit_group;" ::: "memory");
-    if (++now.kb == now.kb1) begin_now();
-    if (++slot == DEPTH) slot = 0;
+    // the first line is done with, behind a tile's last k block the second too
+    ask(place);
+    place = (place + LINE) % ALL;
+    if (++now.kb == now.kb1) {
+      ask(place);
+      place = (place + LINE) % ALL;
+      begin_now();
+    } else {
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) at[j] = (at[j] + LINE) % ALL, next[j] = (next[j] + LINE) % ALL;
+    }
     if (++s == (uint32_t)p.stages) {
       s = 0;
       phase ^= 1u;
@@ -655,9 +681,13 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
       u += q.k1 - q.k0;
     }
   } else if (warp >= kThreads / 32) {
-    if constexpr (!COPY)
-      load_weights<INNER>(p, plan, u, end, ring, ring + p.raw, full0, empty0, sh,
-                          warp - kThreads / 32, lane);
+    if constexpr (!COPY) {
+      const int loader = warp - kThreads / 32;
+      if (!INNER && p.lines == 8)
+        load_weights<INNER, 8>(p, plan, u, end, ring, ring + p.raw, full0, empty0, sh, loader, lane);
+      else
+        load_weights<INNER, 4>(p, plan, u, end, ring, ring + p.raw, full0, empty0, sh, loader, lane);
+    }
   } else {
     const int quad = warp & 3, row = quad * 32 + lane;
     const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16);
@@ -960,13 +990,15 @@ void inner_tiles(const coll_experts_t &a, Layout &l) {
     const double ns = (p.rows * 256.0 + l.cols * 128.0) / 45.0;
     return ns > 300.0 ? ns : 300.0;
   };
+  // two stages have to fit beside the loader warps' rings
+  const int64_t full = l.inner_copied || l.cols < 128 ? 128 : 88;
   double cut[3], best = 0.97;  // nearly as long is not sure to save
   for (int i = 0; i < 3; ++i) {
-    const double block = set(128), blocks = chunks[i] * p.tiles * kblocks / kSms;
+    const double block = set(full), blocks = chunks[i] * p.tiles * kblocks / kSms;
     cut[i] = (blocks > kShort ? blocks : kShort) * block + 6000.0;
   }
-  int64_t rows = 128;
-  for (int64_t r = 16; r <= 128; r += 8) {
+  int64_t rows = full;
+  for (int64_t r = 16; r <= full; r += 8) {
     const double block = set(r);
     double worst = 0.0;  // of the times whole in those cut
     for (int i = 0; i < 3; ++i) {
@@ -1045,7 +1077,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
       r.stage_bytes = w * r.w_bytes + (uint32_t)l.cols * 128u;
       // a matrix instruction reads 128 rows whatever a tile has: slack behind the last stage's
       const uint32_t other = 1024 + kTile - r.w_bytes + fixed + raw;
-      r.stages = (int32_t)((room - other) / r.stage_bytes);
+      r.stages = room > other ? (int32_t)((room - other) / r.stage_bytes) : 0;
       if (r.stages > kMaxStages) r.stages = kMaxStages;
       r.ring = r.stages * r.stage_bytes;
       r.raw = r.ring + fixed;
@@ -1065,8 +1097,13 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
       ring(p, 2, 0, 0, l.cols <= 32 ? kBesideInner : kBesideInner64);
       ring(q, 1, (uint32_t)l.tokens * 512u, 0, kBesideAll - p.smem);
     } else {
-      ring(p, 2, 0, l.inner_copied ? 0 : kRawBytes<true>, kAloneSmem);
-      ring(q, 1, (uint32_t)l.tokens * 512u, l.outer_copied ? 0 : kRawBytes<false>, kAloneSmem);
+      const uint32_t sums = (uint32_t)l.tokens * 512u;
+      p.lines = 4;
+      ring(p, 2, 0, l.inner_copied ? 0 : 4 * kLineBytes<true>, kAloneSmem);
+      for (q.lines = 8; q.lines >= 4; q.lines /= 2) {  // as long as two stages fit beside it
+        ring(q, 1, sums, l.outer_copied ? 0 : q.lines * kLineBytes<false>, kAloneSmem);
+        if (q.stages >= 2) break;
+      }
     }
     const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
     part = l.nothing ? 0 : 2 * kSms * (inner > outer ? inner : outer);
