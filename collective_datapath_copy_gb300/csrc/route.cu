@@ -24,6 +24,7 @@ namespace coll {
 namespace {
 
 constexpr int kWarps = 8;
+constexpr int kSmCount = 152;         // of a GB300
 constexpr int kMostExperts = 1024;  // 32 a lane
 constexpr int kMostChosen = 32;     // one a lane
 
@@ -109,6 +110,12 @@ struct Row {
   // -inf past the end
   static __device__ __forceinline__ void load(const RouteParams &p, int64_t row, int lane,
                                               float (&v)[V]) {
+    if (VEC && p.e == 32 * V) load_run<true>(p, row, lane, v);
+    else load_run<false>(p, row, lane, v);
+  }
+  template <bool FULL>
+  static __device__ __forceinline__ void load_run(const RouteParams &p, int64_t row, int lane,
+                                                  float (&v)[V]) {
     const char *base = static_cast<const char *>(p.logits.p) + row * p.logits.rs * kSize;
     constexpr int kWords = L * kSize >= 4 ? L * kSize / 4 : 1;
 #pragma unroll
@@ -119,7 +126,7 @@ struct Row {
       } else {
         uint32_t w[kWords];
         const char *q = base + e * kSize;
-        if (e < p.e) {
+        if (FULL || e < p.e) {
           if constexpr (kWords == 4) {
             const uint4 x = *reinterpret_cast<const uint4 *>(q);
             w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
@@ -134,7 +141,7 @@ struct Row {
         for (int j = 0; j < L; ++j) {
           const float x = TYPE == COLL_F32 ? __uint_as_float(w[j])
                                            : h2f((uint16_t)(w[j / 2] >> (16 * (j & 1))), TYPE);
-          v[i + j] = e < p.e ? x : -INFINITY;
+          v[i + j] = FULL || e < p.e ? x : -INFINITY;
         }
       }
     }
@@ -199,9 +206,10 @@ __device__ __forceinline__ bool choose_by_rank(int top, int lane, const uint32_t
   for (int i = 1; i < V; ++i) best = max(best, key[i]);
   // equal lanes go together, which only lowers what is left
   uint32_t least = 0u;
+#pragma unroll 4
   for (int j = 0; j < top; ++j) {
     least = __reduce_max_sync(~0u, best);
-    if (best == least) best = 0u;
+    best = best == least ? 0u : best;
   }
   least = max(least, 1u);  // lanes ran out: every key is wanted
   int count = 0;
@@ -215,10 +223,15 @@ __device__ __forceinline__ bool choose_by_rank(int top, int lane, const uint32_t
   }
   const int n = __shfl_sync(~0u, at, 31);
   if (n > 32) return false;
-  at -= count;
+  uint32_t to = smem_u32(mine + at - count);
 #pragma unroll
   for (int i = 0; i < V; ++i)
-    if (key[i] >= least) mine[at++] = make_uint2(~(uint32_t)R::index(i, lane), key[i]);
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\t"
+        "@p st.shared.v2.u32 [%0], {%3, %1};\n\t@p add.u32 %0, %0, 8;\n\t}"
+        : "+r"(to)
+        : "r"(key[i]), "r"(least), "r"(~(uint32_t)R::index(i, lane))
+        : "memory");
   if (lane >= n) mine[lane] = make_uint2(0u, 0u);
   __syncwarp();
   // as one number: the key, then the lower index
@@ -242,8 +255,12 @@ __device__ __forceinline__ bool choose_by_rank(int top, int lane, const uint32_t
   return true;
 }
 
+// CTAs that an SM holds: what the registers of V logits, asked for ahead, leave.
+template <int V>
+constexpr int kPerSm = V <= 2 ? 8 : V <= 4 ? 6 : V <= 8 ? 4 : V <= 16 ? 3 : 1;
+
 template <int V, int TYPE, bool VEC>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(kWarps * 32, kPerSm<V>) route_kernel(const RouteParams p) {
   using R = Row<V, TYPE, VEC>;
   __shared__ __align__(16) uint2 places[kWarps][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -371,12 +388,15 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
 
 template <bool BWD, int TYPE, bool VEC>
 cudaError_t launch(const RouteParams &p, cudaStream_t s) {
-  // warps that stay, four rows each or more, ask for their next row ahead
+  // as many CTAs as the SMs hold, whose warps ask for their next row ahead (a second wave of a few: 18
+  // us for 32768 x 256)
   const int64_t rows = (p.t + kWarps - 1) / kWarps;
-  const dim3 grid((unsigned)(BWD || rows <= 152 * 4 ? rows : rows <= 152 * 16 ? 152 * 4 : rows / 4));
-#define COLL_ROUTE(V)                                                                           \
-  return BWD ? dense_launch(route_bwd_kernel<V, TYPE, VEC>, grid, kWarps * 32, 0, 1, s, p)      \
-             : dense_launch(route_kernel<V, TYPE, VEC>, grid, kWarps * 32, 0, 1, s, p)
+  auto grid = [&](int per_sm) {
+    return dim3((unsigned)(BWD || rows <= kSmCount * per_sm ? rows : kSmCount * per_sm));
+  };
+#define COLL_ROUTE(V)                                                                               \
+  return BWD ? dense_launch(route_bwd_kernel<V, TYPE, VEC>, grid(0), kWarps * 32, 0, 1, s, p)       \
+             : dense_launch(route_kernel<V, TYPE, VEC>, grid(kPerSm<V>), kWarps * 32, 0, 1, s, p)
   if (p.e <= 32) COLL_ROUTE(1);
   if (p.e <= 64) COLL_ROUTE(2);
   if (p.e <= 128) COLL_ROUTE(4);
