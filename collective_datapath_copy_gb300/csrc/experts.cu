@@ -11,8 +11,8 @@
 // 152 equal lengths, because whole tiles would leave SMs idle (8 experts of 2048 inner features are
 // 128 tiles). The shares of a tile that was cut join in a launch behind, in the order of k: nothing
 // waits, and results do not depend on timing. Measured: 128 tokens of two, eight experts of 4096 x 14336
-// (2.8 GB) 447 us, 6.3 TB/s; a chunk of 32 choices of 256, of which this call has 32 experts of 7168 x
-// 2048 284 us, 6.3 TB/s; 16 to 128 tokens over weights of some MB 18 to 25 us, which is the chain of the
+// (2.8 GB) 451 us, 6.3 TB/s; 32 tokens of eight out of 256, 32 of these experts here, of 7168 x 2048,
+// 280 us, 6.4 TB/s; 16 to 128 tokens over weights of some MB 20 to 25 us, which is the chain of the
 // launches: plan 2 us, first weights 3, inner values, join 4, sums, join 4.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -560,9 +560,8 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  // The sums may start beside the inner values where shared memory has room for both, and bring
-  // weights for their whole ring then: the plan they go by is done, because the inner kernel lets
-  // them start only after its own wait for it.
+  // The sums start as the inner values' CTAs leave, and bring weights for their whole ring then: the
+  // plan they go by is done, because the inner kernel lets them start only after its own wait for it.
   if (INNER || p.nothing) griddep_wait();
   griddep_launch();
   PlanView plan = {};
@@ -949,14 +948,13 @@ int alignment(const void *base, int64_t es, int64_t e, int64_t rs, int64_t rows,
   return v % 32 == 0 ? 32 : v % 16 == 0 ? 16 : v % 4 == 0 ? 4 : 2;
 }
 
-// Shared memory for the products. Up to 64 tokens the sums' CTAs fit beside those of the inner values
-// (all an SM has is 228 KB, of which a CTA takes 1 KB and its static arrays beside what it asks for):
-// three stages of the inner ring, two where a stage has room for 64 tokens.
-constexpr int64_t kBesideTokens = 64;
-constexpr uint32_t kBesideAll = 228 * 1024 - 2 * (1024 + sizeof(OwnPlan) + sizeof(Shared) + 64);
-constexpr uint32_t kAloneSmem = 227 * 1024 - sizeof(OwnPlan) - sizeof(Shared) - 64;
-constexpr uint32_t kBesideInner = 1024 + 3 * (2 * kTile + 32 * 128);
-constexpr uint32_t kBesideInner64 = 1024 + 2 * (2 * kTile + 64 * 128);
+// Shared memory for a product's CTA: an SM's. (Half of it, so that the sums' CTAs fit beside the inner
+// values' and bring their weights early, left too few stages: 16 experts of 4096 x 4096, 60 tokens, 265 us
+// against 252; a call of 20 us gained one.) Tensor copies leave room for a CTA of the join, which then makes
+// its plan beside the products (64 experts of 2048 x 704, 16 tokens of six: 86.7 us without, 82.9 with);
+// loader warps need the room themselves (eight of 2001 x 5001, 128 tokens: 137 us, 147 without it).
+constexpr uint32_t kSmem = 227 * 1024 - sizeof(OwnPlan) - sizeof(Shared) - 64;
+constexpr uint32_t kJoinSmem = 1024 + sizeof(OwnPlan) + 512;
 
 // The workspace of a group of tokens, and the shapes of its launches.
 struct Layout {
@@ -1025,12 +1023,13 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
              ceil_div(a.f, kDirectInner) * (chosen + choices / 8) < 0x7FFFFFFF;
   l.inner_copied = copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f);
   l.outer_copied = copied(a.w_down, a.experts, a.n);
-  // columns of a chunk: all tokens, or 32 where the experts have fewer than half as many each
+  // columns of a chunk: all tokens, or 64 or 32 where the experts have half as many each at most (100
+  // tokens of two, eight experts of 4096 x 1792: 80 us with 128, 72 with 64, whose ring is deeper)
   const bool spread = choices <= 16 * a.experts;
   l.cols = l.direct ? 8
            : l.tokens <= 16 ? 16
            : l.tokens <= 32 || spread ? 32
-           : l.tokens <= 64 ? 64 : 128;
+           : l.tokens <= 64 || choices <= 32 * a.experts ? 64 : 128;
   l.planned = !l.nothing && !l.direct && (choices > kOwnChoices || !copied(a.x, a.m, a.k));
   l.pack = !l.nothing && !l.direct && !copied(a.x, a.m, a.k);
   l.chunks = chosen + choices / l.cols;
@@ -1072,11 +1071,12 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     q.out_type = (int32_t)a.out_dtype;
     p.act = (int32_t)a.act;
     p.status = q.status = a.status;
-    auto ring = [&](ProductParams &r, int w, uint32_t fixed, uint32_t raw, uint32_t room) {
+    auto ring = [&](ProductParams &r, int w, uint32_t fixed, uint32_t raw) {
       r.w_bytes = (uint32_t)r.rows * 128u;
       r.stage_bytes = w * r.w_bytes + (uint32_t)l.cols * 128u;
       // a matrix instruction reads 128 rows whatever a tile has: slack behind the last stage's
       const uint32_t other = 1024 + kTile - r.w_bytes + fixed + raw;
+      const uint32_t room = raw ? kSmem : kSmem - kJoinSmem;
       r.stages = room > other ? (int32_t)((room - other) / r.stage_bytes) : 0;
       if (r.stages > kMaxStages) r.stages = kMaxStages;
       r.ring = r.stages * r.stage_bytes;
@@ -1093,17 +1093,12 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     by_hand(p, 0, a.w_gate, a.f, a.k);
     by_hand(p, 1, a.w_up, a.f, a.k);
     by_hand(q, 0, a.w_down, a.n, a.f);
-    if (l.tokens <= kBesideTokens && l.inner_copied && l.outer_copied) {
-      ring(p, 2, 0, 0, l.cols <= 32 ? kBesideInner : kBesideInner64);
-      ring(q, 1, (uint32_t)l.tokens * 512u, 0, kBesideAll - p.smem);
-    } else {
-      const uint32_t sums = (uint32_t)l.tokens * 512u;
-      p.lines = 4;
-      ring(p, 2, 0, l.inner_copied ? 0 : 4 * kLineBytes<true>, kAloneSmem);
-      for (q.lines = 8; q.lines >= 4; q.lines /= 2) {  // as long as two stages fit beside it
-        ring(q, 1, sums, l.outer_copied ? 0 : q.lines * kLineBytes<false>, kAloneSmem);
-        if (q.stages >= 2) break;
-      }
+    const uint32_t sums = (uint32_t)l.tokens * 512u;
+    p.lines = 4;
+    ring(p, 2, 0, l.inner_copied ? 0 : 4 * kLineBytes<true>);
+    for (q.lines = 8; q.lines >= 4; q.lines /= 2) {  // as long as two stages fit beside it
+      ring(q, 1, sums, l.outer_copied ? 0 : q.lines * kLineBytes<false>);
+      if (q.stages >= 2) break;
     }
     const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
     part = l.nothing ? 0 : 2 * kSms * (inner > outer ? inner : outer);
@@ -1179,7 +1174,7 @@ int64_t need(const coll_experts_t &a) {
 template <bool INNER, bool COPY>
 int set_up() {
   static DenseSmemLimit limit;
-  return limit((const void *)product_kernel<INNER, COPY>, kAloneSmem) == cudaSuccess ? COLL_OK
+  return limit((const void *)product_kernel<INNER, COPY>, kSmem) == cudaSuccess ? COLL_OK
                                                                                    : COLL_ECUDA;
 }
 
