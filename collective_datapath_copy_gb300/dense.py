@@ -82,8 +82,9 @@ def _weight(name, w):
 def _read(t, m, cols, dtype, dev, what, keep):
     """An input's address and strides as a matrix of `cols` columns (leading dimensions flattened)
     and m rows (any where m is None). What has to be copied for that lives in `keep`."""
-    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 2 and t.size(1) == cols
-            and (m is None or t.size(0) == m)):
+    shape = t.shape
+    if (len(shape) == 2 and shape[1] == cols and (m is None or shape[0] == m)
+            and t.dtype is dtype and t.get_device() == dev):
         return (t.data_ptr(), *t.stride())
     if t.dtype is not dtype:
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
@@ -101,8 +102,7 @@ def _read(t, m, cols, dtype, dev, what, keep):
 
 def _write(t, m, cols, dtype, dev, what):
     """An output's address and strides as a matrix; never a copy."""
-    if (t.dtype is dtype and t.get_device() == dev and t.dim() == 2 and t.size(1) == cols
-            and t.size(0) == m):
+    if t.shape == (m, cols) and t.dtype is dtype and t.get_device() == dev:
         return (t.data_ptr(), *t.stride())
     if t.dtype is not dtype:
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
@@ -115,7 +115,8 @@ def _write(t, m, cols, dtype, dev, what):
 
 
 def _row_count(x):
-    return x.size(0) if x.dim() == 2 else math.prod(x.shape[:-1])
+    shape = x.shape
+    return shape[0] if len(shape) == 2 else math.prod(shape[:-1])
 
 
 def _new(m, cols, dtype, weight, like):
@@ -174,10 +175,14 @@ class _Dense:
             if code == _EWORKSPACE:
                 need = self._fit(where, pack, size, fields, given)
         if need:
-            ws = torch.empty(need, dtype=torch.uint8, device=self._status.device)
-            code = fn(pack(*fields, ws.data_ptr(), need, self._word), stream)
+            code = self._lend(fn, pack, fields, need, stream)
         if code:
             check(code, where)
+
+    def _lend(self, fn, pack, fields, need, stream):
+        """The call with a workspace of `need` bytes, which is free again behind it in the stream."""
+        ws = torch.empty(need, dtype=torch.uint8, device=self._status.device)
+        return fn(pack(*fields, ws.data_ptr(), need, self._word), stream)
 
     def _fit(self, where, pack, size, fields, given):
         """The workspace of a call, asked for unless the last one was alike."""

@@ -29,7 +29,10 @@ from .dense import ACT, GATED_ACTS, _NONE, _TYPE, _Dense, _mask, _new, _on, _rea
 _ROUTE = struct.Struct("6qd9q")
 _ROUTE_BWD = struct.Struct("6qd12q")
 _EXPERTS = struct.Struct("37q")
-_LOGITS = (torch.float32, torch.bfloat16, torch.float16)
+# What lies behind torch.cuda.caching_allocator_alloc and _delete: blocks of the caching allocator, as
+# torch.empty has them (of a graph's pool under capture, reused in the stream's order).
+_alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
+_free = torch._C._cuda_cudaCachingAllocator_raw_delete
 _entries = {}
 
 dense._MASK["coll_gated_experts"] = _mask("." * 10 + "a.." * 8)
@@ -37,14 +40,15 @@ dense._MASK["coll_gated_experts"] = _mask("." * 10 + "a.." * 8)
 
 def _out(t, m, cols, dtype, dev, what):
     """An output's address and strides as a matrix; never a copy."""
+    if t.shape == (m, cols) and t.dtype is dtype and t.get_device() == dev:
+        return (t.data_ptr(), *t.stride())
     if t.dtype is not dtype:
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
     if t.get_device() != dev:
         raise ValueError(f"{what} is on {t.device}, expected cuda:{dev}")
     if t.dim() == 0 or t.shape[-1] != cols or t.numel() != m * cols:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {m} rows of {cols}")
-    if t.dim() != 2:
-        t = t.view(m, cols)
+    t = t.view(m, cols)
     return (t.data_ptr(), *t.stride())
 
 
@@ -82,18 +86,29 @@ class Router:
     normalize = property(lambda self: bool(self._how[1]))
     scale = property(lambda self: self._how[2])
 
-    def _head(self, t, e, dtype):
-        return (t, e, self.top_k, _TYPE[dtype], *self._how)
-
     @staticmethod
     def _logits(logits):
-        if logits.dtype not in _LOGITS:
-            raise ValueError(f"logits must be one of {_LOGITS}, not {logits.dtype}")
-        if not logits.is_cuda:
+        if logits.dtype not in _TYPE:
+            raise ValueError(f"logits must be one of {tuple(_TYPE)}, not {logits.dtype}")
+        dev = logits.get_device()
+        if dev < 0:
             raise ValueError("logits is not a CUDA tensor")
         if logits.dim() == 0:
             raise ValueError("logits must have a dimension of experts")
-        return logits.get_device()
+        return dev
+
+    def _head(self, logits, keep):
+        """Sizes and how to choose, the first fields of a call, and the logits as a matrix."""
+        shape = logits.shape
+        e = shape[-1]
+        if len(shape) == 2:
+            t, rows = shape[0], logits
+        else:
+            t = math.prod(shape[:-1])
+            rows = logits.reshape(t, e)
+            keep.append(rows)
+        return ((t, e, self.top_k, _TYPE[logits.dtype], *self._how),
+                (rows.data_ptr(), *rows.stride()))
 
     @staticmethod
     def _launch(where, packed, dev):
@@ -115,16 +130,16 @@ class Router:
         if stream is not None:
             with _on(stream, dev, (logits, ids, weights), "logits are"):
                 return self.forward(logits, ids, weights)
-        keep, e, top = [], logits.shape[-1], self.top_k
-        lm = _read(logits, None, e, logits.dtype, dev, "logits", keep)
-        t = _row_count(logits)
+        keep, top = [], self.top_k
+        head, lm = self._head(logits, keep)
+        t = head[0]
         if ids is None:
             ids = torch.empty(*logits.shape[:-1], top, dtype=torch.int32, device=logits.device)
         if weights is None:
             weights = torch.empty(*logits.shape[:-1], top, dtype=torch.float32,
                                   device=logits.device)
         self._launch("coll_route", _ROUTE.pack(
-            *self._head(t, e, logits.dtype), *lm, *_out(ids, t, top, torch.int32, dev, "ids"),
+            *head, *lm, *_out(ids, t, top, torch.int32, dev, "ids"),
             *_out(weights, t, top, torch.float32, dev, "weights")), dev)
         return ids, weights
 
@@ -137,15 +152,15 @@ class Router:
         if stream is not None:
             with _on(stream, dev, (dweights, logits, ids, dlogits), "logits are"):
                 return self.backward(dweights, logits, ids, dlogits)
-        keep, e, top = [], logits.shape[-1], self.top_k
-        lm = _read(logits, None, e, logits.dtype, dev, "logits", keep)
-        t = _row_count(logits)
+        keep, top = [], self.top_k
+        head, lm = self._head(logits, keep)
+        t, e = head[:2]
         gm = _read(dweights, t, top, torch.float32, dev, "dweights", keep)
         im = _read(ids, t, top, torch.int32, dev, "ids", keep)
         if dlogits is None:
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         self._launch("coll_route_backward", _ROUTE_BWD.pack(
-            *self._head(t, e, logits.dtype), *gm, *lm, *im,
+            *head, *gm, *lm, *im,
             *_out(dlogits, t, e, logits.dtype, dev, "dlogits")), dev)
         return dlogits
 
@@ -179,6 +194,14 @@ class GatedExperts(_Dense):
     w_gate = property(lambda self: self._w[0])
     w_up = property(lambda self: self._w[1])
     w_down = property(lambda self: self._w[2])
+
+    def _lend(self, fn, pack, fields, need, stream):
+        # no tensor around it: making one costs as much as the launches (one token: 14.6 us a call, 10.7 so)
+        ws = _alloc(need, stream)
+        try:
+            return fn(pack(*fields, ws, need, self._word), stream)
+        finally:
+            _free(ws)
 
     def forward(self, x, ids, weights, residual=None, out=None, out_dtype=None, stream=None):
         """x [..., K], ids [..., top] (int32) and weights [..., top] (binary32) -> y [..., N].

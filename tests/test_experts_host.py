@@ -260,6 +260,35 @@ def test_a_stream_of_another_device_is_refused(monkeypatch):
     assert [n for n, _, _ in m.calls] == ["coll_route", "coll_route_backward"]
 
 
+@pytest.mark.parametrize("code", [0, D["COLL_ECUDA"]])
+@pytest.mark.parametrize("current", [0, 1])
+def test_a_workspace_is_of_the_calls_device_and_stream_and_freed(monkeypatch, current, code):
+    m, op = Machine(monkeypatch, current), object.__new__(experts.GatedExperts)
+    op._start(torch.device("cpu"))
+    op._dev = 1
+    seen = []
+    monkeypatch.setattr(experts, "_alloc", lambda n, s: seen.append((n, m.current, s)) or 5 * A)
+    monkeypatch.setattr(experts, "_free", lambda p: seen.append(("free", p)))
+    fields = (8, 256, 256, 128, 4, 0, 2, BF, BF, D["COLL_ACT_SILU"], A, 128 * 256, 256, 2 * A,
+              128 * 256, 256, 3 * A, 256 * 128, 128, 4 * A, 256, 1, 5 * A, 2, 1, 6 * A, 2, 1, *NO,
+              7 * A, 256, 1)
+
+    def call(packed, stream):
+        given = packed[-24:]
+        if given[:16] == bytes(16):
+            return D["COLL_EWORKSPACE"]
+        seen.append((given, m.current, stream))
+        return code
+
+    monkeypatch.setattr(dense, "_entries", {"coll_gated_experts": (call, lambda packed: 4096)})
+    for _ in range(2):
+        seen.clear()
+        with contextlib.nullcontext() if code == 0 else pytest.raises(_lib.CollError):
+            op._launch("coll_gated_experts", experts._EXPERTS.pack, fields)
+        given = np.array([5 * A, 4096, op._word], np.int64).tobytes()
+        assert seen == [(4096, 1, 101), (given, 1, 101), ("free", 5 * A)]
+
+
 def test_arguments_before_any_device_is_asked():
     w = torch.zeros(4, 8, 16, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
