@@ -7,11 +7,12 @@
 //               a = l (softmax) or log s (sigmoid), so that no sum of tiny scores vanishes
 //
 // A warp takes a token. Its logits stay in registers, as keys whose unsigned order is that of the
-// numbers; choosing is by the keys alone, so it depends on no computed score. Bound by the warps'
-// instructions as much as by HBM, so for many experts the chosen are not taken one by one: the k-th
-// largest of the lanes' largest keys is passed by at least k keys and by few more, which a lane each
-// then ranks.
+// numbers, or as they are; choosing is by them alone, so it depends on no computed score. Bound by the
+// warps' instructions as much as by HBM (32768 x 256, eight chosen: 12.8 us, of which reading takes 5), so
+// for many experts the chosen are not taken one by one: the k-th largest of the lanes' largest is reached
+// by at least k logits and by few more, which a lane each then ranks.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <math.h>
 #include <stdint.h>
 
@@ -91,6 +92,13 @@ __device__ __forceinline__ float chosen_sum(float v, int top) {
 // was left for this lane. SORTED: the largest is lane 0's.
 template <bool SORTED>
 __device__ __forceinline__ float normalised(float l, bool there, int top, int score) {
+  // sigmoids that are far from underflow as they are, without their logarithms (32768 x 128, six chosen:
+  // 13.7 us with them, 13.3 without)
+  if (score == COLL_SCORE_SIGMOID && __all_sync(~0u, !there || l > -60.0f)) {
+    const float s = there ? sigmoid(l) : 0.0f;
+    const float sum = chosen_sum(s, top);
+    return there ? s / sum : 0.0f;
+  }
   const float a = score == COLL_SCORE_SIGMOID ? log_sigmoid(l) : l;
   const float most = SORTED ? __shfl_sync(~0u, a, 0) : warp_max(there ? a : -INFINITY);
   const float x = there ? expf(a - most) : 0.0f;
@@ -107,16 +115,18 @@ struct Row {
   static __device__ __forceinline__ int index(int i, int lane) {
     return (i / L * 32 + lane) * L + i % L;
   }
+  static __device__ __forceinline__ const char *row(const RouteParams &p, int64_t row) {
+    return static_cast<const char *>(p.logits.p) + row * p.logits.rs * kSize;
+  }
   // -inf past the end
-  static __device__ __forceinline__ void load(const RouteParams &p, int64_t row, int lane,
+  static __device__ __forceinline__ void load(const RouteParams &p, const char *base, int lane,
                                               float (&v)[V]) {
-    if (VEC && p.e == 32 * V) load_run<true>(p, row, lane, v);
-    else load_run<false>(p, row, lane, v);
+    if (VEC && p.e == 32 * V) load_run<true>(p, base, lane, v);
+    else load_run<false>(p, base, lane, v);
   }
   template <bool FULL>
-  static __device__ __forceinline__ void load_run(const RouteParams &p, int64_t row, int lane,
+  static __device__ __forceinline__ void load_run(const RouteParams &p, const char *base, int lane,
                                                   float (&v)[V]) {
-    const char *base = static_cast<const char *>(p.logits.p) + row * p.logits.rs * kSize;
     constexpr int kWords = L * kSize >= 4 ? L * kSize / 4 : 1;
 #pragma unroll
     for (int i = 0; i < V; i += L) {
@@ -175,8 +185,20 @@ struct Row {
 // One round for each choice: the largest key, of equal ones that of the lowest index. Lane j gets the
 // j-th.
 template <typename R, int V>
-__device__ __forceinline__ void choose_in_turn(int top, int lane, uint32_t (&key)[V], int &id,
+__device__ __forceinline__ void choose_in_turn(int top, int lane, const float (&v)[V], int &id,
                                                float &chosen) {
+  uint32_t key[V];
+  bool odd = false;  // NaN or an infinity among the logits
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const uint32_t u = __float_as_uint(v[i] + 0.0f);
+    key[i] = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    odd = odd || !(fabsf(v[i]) < INFINITY);
+  }
+  if (__any_sync(~0u, odd)) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = order_key(v[i]);
+  }
   for (int j = 0; j < top; ++j) {
     uint32_t best = 0u;
     int at = 0;
@@ -196,25 +218,40 @@ __device__ __forceinline__ void choose_in_turn(int top, int lane, uint32_t (&key
   }
 }
 
-// The same by rank among the keys that reach the top-th largest of the lanes' own largest: all that
-// are chosen, and few more. `mine`: 32 places of this warp. False where there are more than 32.
+// NaN where one is.
+__device__ __forceinline__ float max_of_three(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+struct Places {
+  uint2 of[32];  // value, index
+  float value[32];
+};
+
+// The same by rank among the logits that reach the top-th largest of the lanes' own largest: all that
+// are chosen, and few more, a lane each. On the numbers themselves: only rows with a NaN need keys.
+// False for those, and where more than 32 reach it.
 template <typename R, int V>
-__device__ __forceinline__ bool choose_by_rank(int top, int lane, const uint32_t (&key)[V],
-                                               uint2 *mine, int &id, float &chosen) {
-  uint32_t best = key[0];
+__device__ __forceinline__ bool choose_by_rank(int top, int lane, const float (&v)[V], Places &mine,
+                                               int &id, float &chosen) {
+  static_assert(V % 2 == 0, "logits in pairs");
+  float best = v[0];
 #pragma unroll
-  for (int i = 1; i < V; ++i) best = max(best, key[i]);
+  for (int i = 0; i < V; i += 2) best = max_of_three(best, v[i], v[i + 1]);
+  if (__any_sync(~0u, best != best)) return false;
   // equal lanes go together, which only lowers what is left
-  uint32_t least = 0u;
+  float least = 0.0f;
 #pragma unroll 4
   for (int j = 0; j < top; ++j) {
-    least = __reduce_max_sync(~0u, best);
-    best = best == least ? 0u : best;
+    least = warp_max(best);
+    best = best == least ? -INFINITY : best;
   }
-  least = max(least, 1u);  // lanes ran out: every key is wanted
+  least = fmaxf(least, -FLT_MAX);  // lanes ran out: all but -inf are wanted
   int count = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) count += key[i] >= least;
+  for (int i = 0; i < V; ++i) count += v[i] >= least;
   int at = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -223,74 +260,79 @@ __device__ __forceinline__ bool choose_by_rank(int top, int lane, const uint32_t
   }
   const int n = __shfl_sync(~0u, at, 31);
   if (n > 32) return false;
-  uint32_t to = smem_u32(mine + at - count);
+  uint32_t to = smem_u32(mine.of + at - count);
 #pragma unroll
   for (int i = 0; i < V; ++i)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ge.u32 p, %1, %2;\n\t"
-        "@p st.shared.v2.u32 [%0], {%3, %1};\n\t@p add.u32 %0, %0, 8;\n\t}"
+        "{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, %2;\n\t"
+        "@p st.shared.v2.b32 [%0], {%1, %3};\n\t@p add.u32 %0, %0, 8;\n\t}"
         : "+r"(to)
-        : "r"(key[i]), "r"(least), "r"(~(uint32_t)R::index(i, lane))
+        : "f"(v[i]), "f"(least), "r"(R::index(i, lane))
         : "memory");
-  if (lane >= n) mine[lane] = make_uint2(0u, 0u);
   __syncwarp();
-  // as one number: the key, then the lower index
-  const uint64_t *all = reinterpret_cast<const uint64_t *>(mine);
-  const uint64_t own = all[lane];
-  int rank = 0;
-#pragma unroll 4
-  for (int j = 0; j < n; j += 2) {
-    const ulonglong2 o = *reinterpret_cast<const ulonglong2 *>(all + j);
-    rank += o.x > own;
-    rank += o.y > own;
+  const bool one = lane < n;
+  const uint2 own = mine.of[lane];
+  const float value = one ? __uint_as_float(own.x) : -INFINITY;
+  mine.value[lane] = value;
+  __syncwarp();
+  uint32_t rank = 0;
+#pragma unroll 2
+  for (int j = 0; j < n; j += 4) {
+    const float4 o = *reinterpret_cast<const float4 *>(mine.value + j);
+    rank += o.x > value;
+    rank += o.y > value;
+    rank += o.z > value;
+    rank += o.w > value;
   }
+  // different numbers have the ranks 0 to n - 1; of equal ones the lower index comes first
+  if (__reduce_add_sync(~0u, one ? rank : 0u) != (uint32_t)(n * (n - 1) / 2)) {
+    for (int j = 0; j < n; ++j) rank += mine.value[j] == value && mine.of[j].y < own.y;
+    __syncwarp();
+  }
+  if (one && rank < (uint32_t)top) mine.of[rank] = own;
   __syncwarp();
-  if (lane < n && rank < top) reinterpret_cast<uint64_t *>(mine)[rank] = own;
-  __syncwarp();
-  if (lane < top && lane < n) {
-    id = (int)~mine[lane].x;
-    chosen = key_value(mine[lane].y);
+  if (one && lane < top) {
+    const uint2 o = mine.of[lane];
+    chosen = __uint_as_float(o.x);
+    id = (int)o.y;
   }
   __syncwarp();
   return true;
 }
 
-// CTAs that an SM is sure to hold: what the registers of V logits, asked for ahead, leave. With V <= 2 the
-// compiler needs fewer and eight fit: held to eight it was slower (5003 tokens of 60: 3.9 us against 3.5).
+// CTAs that an SM is sure to hold, which bounds the registers: those of V logits, asked for ahead, and what
+// lets a row's instructions overlap. 8000 tokens of 1000: 12.8 us with one, 10.6 with two; 8192 of 512: 8.9
+// with two, 7.5 with three; 32768 of 256: 12.8 with four, 13.9 with five; of 128: 16.2 with four, 13.3 with
+// six; 5003 of 60: 3.0 with four, 3.4 with six, 4.0 with eight (more fit, and the grid has eight an SM).
 template <int V>
-constexpr int kPerSm = V <= 4 ? 6 : V <= 8 ? 4 : V <= 16 ? 3 : 1;
+constexpr int kPerSm = V <= 2 ? 4 : V <= 4 ? 6 : V <= 8 ? 4 : V <= 16 ? 3 : 2;
 
 template <int V, int TYPE, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32, kPerSm<V>) route_kernel(const RouteParams p) {
   using R = Row<V, TYPE, VEC>;
-  __shared__ __align__(16) uint2 places[kWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  __shared__ __align__(16) Places places[kWarps];
+  // by a shuffle, from which the compiler knows that it is the same for all lanes: the row's branches and
+  // addresses are then the warp's (32768 x 256: 14.3 us without, 12.8 with)
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * kWarps;
   int64_t row = (int64_t)blockIdx.x * kWarps + warp;
+  const char *from = R::row(p, row);
+  int32_t *ids = p.ids + row * p.ids_rs + lane * p.ids_cs;
+  float *weights = p.weights + row * p.w_rs + lane * p.w_cs;
   griddep_launch();
   griddep_wait();
   float v[V], next[V];
-  if (row < p.t) R::load(p, row, lane, next);
+  if (row < p.t) R::load(p, from, lane, next);
   for (; row < p.t; row += step) {
 #pragma unroll
     for (int i = 0; i < V; ++i) v[i] = next[i];
-    if (row + step < p.t) R::load(p, row + step, lane, next);
-    uint32_t key[V];
-    bool odd = false;  // NaN or an infinity among the logits
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const uint32_t u = __float_as_uint(v[i] + 0.0f);
-      key[i] = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
-      odd = odd || !(fabsf(v[i]) < INFINITY);
-    }
-    if (__any_sync(~0u, odd)) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = order_key(v[i]);
-    }
+    from += step * p.logits.rs * R::kSize;
+    if (row + step < p.t) R::load(p, from, lane, next);
     float chosen = -INFINITY;
     int id = -1;
-    if (V <= 2 || !choose_by_rank<R, V>(p.top, lane, key, places[warp], id, chosen))
-      choose_in_turn<R, V>(p.top, lane, key, id, chosen);
+    bool done = false;
+    if constexpr (V > 2) done = choose_by_rank<R, V>(p.top, lane, v, places[warp], id, chosen);
+    if (!done) choose_in_turn<R, V>(p.top, lane, v, id, chosen);
     const bool there = id >= 0;
     float w;
     if (p.norm) {
@@ -305,9 +347,11 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<V>) route_kernel(const Rou
       w = expf(chosen - most) / warp_sum(sum);
     }
     if (lane < p.top) {
-      p.ids[row * p.ids_rs + lane * p.ids_cs] = id;
-      p.weights[row * p.w_rs + lane * p.w_cs] = there ? w * p.scale : 0.0f;
+      *ids = id;
+      *weights = there ? w * p.scale : 0.0f;
     }
+    ids += step * p.ids_rs;
+    weights += step * p.w_rs;
   }
 }
 
@@ -320,8 +364,8 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<V>) route_kernel(const Rou
 template <int V, int TYPE, bool VEC>
 __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParams p) {
   using R = Row<V, TYPE, VEC>;
-  const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * kWarps + warp;
   griddep_launch();
   griddep_wait();
   if (row >= p.t) return;
@@ -333,7 +377,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
     g = p.weights[row * p.w_rs + lane * p.w_cs] * p.scale;
   }
   float v[V], d, rest = 0.0f;  // rest: what an expert gets beside its own gradients
-  if (plain) R::load(p, row, lane, v);
+  if (plain) R::load(p, R::row(p, row), lane, v);
   const bool there = (uint32_t)id < (uint32_t)p.e;
   if (there) l = ld_elem(p.logits.p, row * p.logits.rs + id * p.logits.cs, TYPE);
   if (p.norm) {

@@ -164,6 +164,43 @@ def test_nan_and_infinity(kind):
     assert bool(dl[clean].isfinite().all())
 
 
+@pytest.mark.parametrize("e", [100, 256, 500, 1000])
+@pytest.mark.parametrize("kind", KINDS)
+def test_odd_rows_among_many_experts(kind, e):
+    """NaN, infinities, equal leaders and zeros of both signs between ordinary rows."""
+    logits = draw(8, 3000, e, F32)
+    places = torch.randperm(e, generator=torch.Generator().manual_seed(e))[:12].cuda()
+    ties = torch.arange(0, 3000, 7, device="cuda")
+    logits[ties[:, None], places] = torch.tensor([9.0, 8.0, 9.0, 7.0, 9.0, 8.0] * 2, device="cuda")
+    zeros = ties[:-1] + 1
+    logits[zeros] = -logits[zeros].abs() - 1
+    logits[zeros[:, None], places] = torch.tensor([0.0, -0.0] * 6, device="cuda")
+    high = ties[:-1] + 2
+    logits[high] = -INF
+    logits[high[:, None], places[:5]] = torch.arange(5.0, device="cuda")
+    check_forward(logits, 8, *kind)
+    nan = ties[:-1] + 3
+    logits[nan, places[0]] = -float("nan")
+    logits[nan[::2], places[1]] = INF
+    logits[nan[1::2], places[2]] = float("nan")
+    logits[ties[:-1] + 4, places[3]] = INF
+    r = cdc.Router(8, *kind)
+    ids, w = r.forward(logits)
+    assert torch.equal(ids.long(), er.choose(logits, 8))
+    assert bool(w[nan, 0].isnan().all())
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+def test_sigmoids_around_where_their_logarithms_are_taken(normalize):
+    rows = [[-58.0, -59.5, -60.0, -60.5], [-59.9, -59.99, -59.0, -59.5], [0.0, -59.9, 3.0, -60.1],
+            [-61.0, -88.0, -104.0, -120.0], [20.0, -100.0, -1.0, -59.0], [90.0, 100.0, -59.0, 0.5]]
+    logits = torch.tensor(rows, device="cuda").repeat(1, 20) - torch.arange(80, device="cuda") * 1e-3
+    ids, _ = check_forward(logits, 6, "sigmoid", normalize, 1.0)
+    check_backward(logits, ids, "sigmoid", normalize, 1.0)
+    ids, _ = check_forward(logits, 32, "sigmoid", normalize, 1.0)
+    check_backward(logits, ids, "sigmoid", normalize, 1.0)
+
+
 def test_backward_takes_any_ids():
     """Out of order, outside the experts, the same one twice."""
     logits = draw(7, 50, 33, F32)
