@@ -6,11 +6,12 @@
 // Bound by HBM, and for small experts by latency: two launches, the chunks made by a warp of every CTA
 // from the ids alone, the sums' first weights asked for while the inner values are still being made, the
 // sums' CTAs all on the SMs at once (two waves of them: 24 us where one takes 19, two experts of 4096 x
-// 1792). One token, six of 64 experts of 2048 x 176 (13 MB): 8.3 us, where the tensor-core kernels' cut
+// 1792). One token, six of 64 experts of 2048 x 176 (13 MB): 8.0 us, where the tensor-core kernels' cut
 // tiles and joins take 18; two tokens, four of eight experts of 4096 x 14336: 177 us (7 TB/s) against
 // 192; 16 tokens of two, eight of 4096 x 1792: 57 against 63. With more choices a CTA's plan takes
 // longer and an expert's choices fill more chunks: 48 choices within 3 % either way, 96 of 16 experts of
-// 7168 x 2048 224 against 219.
+// 7168 x 2048 224 against 219. The warp's number comes by a shuffle, so that the compiler knows it to be
+// the same for all lanes (one token: 8.3 us without).
 #include "dense_direct.cuh"
 #include "dense_epi.cuh"
 #include "dense_tc.h"
@@ -113,7 +114,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   constexpr int AHEAD = kAhead<ALIGN>;
   __shared__ float part[2][kWarps][8][16];
   __shared__ Few few;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3;
   griddep_wait();
   griddep_launch();
@@ -191,7 +193,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   __shared__ float sums[kWarps][kDirectTokens * 16];
   __shared__ Few few;
   __shared__ uint32_t last;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0);
+  const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int g = lane >> 2, t = lane & 3, size = p.tokens * 16;
   griddep_launch();
   float *mine = sums[warp];
