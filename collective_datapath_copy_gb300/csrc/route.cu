@@ -8,7 +8,7 @@
 //
 // A warp takes a token. Its logits stay in registers, as keys whose unsigned order is that of the
 // numbers, or as they are; choosing is by them alone, so it depends on no computed score. Bound by the
-// warps' instructions as much as by HBM (32768 x 256, eight chosen: 12.8 us, of which reading takes 5), so
+// warps' instructions as much as by HBM (32768 x 256, eight chosen: 11.8 us, of which reading takes 5), so
 // for many experts the chosen are not taken one by one: the k-th largest of the lanes' largest is reached
 // by at least k logits and by few more, which a lane each then ranks.
 #include <cuda_runtime.h>
@@ -72,10 +72,14 @@ __device__ __forceinline__ float warp_max(float v) {
 // all experts, a third of expf's instructions.
 __device__ __forceinline__ float exp_below(float d) { return exp2_fast(d * kLog2e); }
 
+// a / b, off by two steps at most; 0 for b past 2^126. With exact divisions 32768 x 256 took 12.9 us in
+// place of 11.8, the gradient of 777 x 60 2.8 in place of 2.4.
+__device__ __forceinline__ float quotient(float a, float b) { return __fdividef(a, b); }
+
 __device__ __forceinline__ float log_sigmoid(float l) {
   return fminf(l, 0.0f) - log1pf(expf(-fabsf(l)));
 }
-__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+__device__ __forceinline__ float sigmoid(float l) { return quotient(1.0f, 1.0f + expf(-l)); }
 
 // The sum over the first `top` lanes, which the others have to leave at 0, in those lanes.
 __device__ __forceinline__ float chosen_sum(float v, int top) {
@@ -93,17 +97,17 @@ __device__ __forceinline__ float chosen_sum(float v, int top) {
 template <bool SORTED>
 __device__ __forceinline__ float normalised(float l, bool there, int top, int score) {
   // sigmoids that are far from underflow as they are, without their logarithms (32768 x 128, six chosen:
-  // 13.7 us with them, 13.3 without)
+  // a thirtieth of the time)
   if (score == COLL_SCORE_SIGMOID && __all_sync(~0u, !there || l > -60.0f)) {
     const float s = there ? sigmoid(l) : 0.0f;
     const float sum = chosen_sum(s, top);
-    return there ? s / sum : 0.0f;
+    return there ? quotient(s, sum) : 0.0f;
   }
   const float a = score == COLL_SCORE_SIGMOID ? log_sigmoid(l) : l;
   const float most = SORTED ? __shfl_sync(~0u, a, 0) : warp_max(there ? a : -INFINITY);
   const float x = there ? expf(a - most) : 0.0f;
   const float sum = chosen_sum(x, top);
-  return there ? x / sum : 0.0f;
+  return there ? quotient(x, sum) : 0.0f;
 }
 
 // How a row lies over a warp: lane l holds runs of L neighbouring logits, V / L of them. VEC: the runs
@@ -254,10 +258,12 @@ __device__ __forceinline__ bool choose_by_rank(int top, int lane, const float (&
   for (int i = 0; i < V; ++i) count += v[i] >= least;
   int at = count;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int c = __shfl_up_sync(~0u, at, o);
-    if (lane >= o) at += c;
-  }
+  for (int o = 1; o < 32; o <<= 1)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .s32 c;\n\tshfl.sync.up.b32 c|p, %0, %1, 0, 0xffffffff;\n\t"
+        "@p add.s32 %0, %0, c;\n\t}"
+        : "+r"(at)
+        : "r"(o));
   const int n = __shfl_sync(~0u, at, 31);
   if (n > 32) return false;
   uint32_t to = smem_u32(mine.of + at - count);
@@ -301,9 +307,10 @@ __device__ __forceinline__ bool choose_by_rank(int top, int lane, const float (&
 }
 
 // CTAs that an SM is sure to hold, which bounds the registers: those of V logits, asked for ahead, and what
-// lets a row's instructions overlap. 8000 tokens of 1000: 12.8 us with one, 10.6 with two; 8192 of 512: 8.9
-// with two, 7.5 with three; 32768 of 256: 12.8 with four, 13.9 with five; of 128: 16.2 with four, 13.3 with
-// six; 5003 of 60: 3.0 with four, 3.4 with six, 4.0 with eight (more fit, and the grid has eight an SM).
+// lets a row's instructions overlap. With exact divisions: 8000 tokens of 1000 12.8 us with one, 10.6 with
+// two; 8192 of 512 8.9 with two, 7.5 with three; 32768 of 256 12.8 with four, 13.9 with five; of 128 16.2
+// with four, 13.3 with six; 5003 of 60 3.0 with four, 3.4 with six, 4.0 with eight (more fit, and the grid
+// has eight an SM).
 template <int V>
 constexpr int kPerSm = V <= 2 ? 4 : V <= 4 ? 6 : V <= 8 ? 4 : V <= 16 ? 3 : 2;
 
@@ -312,7 +319,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<V>) route_kernel(const Rou
   using R = Row<V, TYPE, VEC>;
   __shared__ __align__(16) Places places[kWarps];
   // by a shuffle, from which the compiler knows that it is the same for all lanes: the row's branches and
-  // addresses are then the warp's (32768 x 256: 14.3 us without, 12.8 with)
+  // addresses are then the warp's (32768 x 256: an eighth of the time)
   const int warp = __shfl_sync(~0u, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * kWarps;
   int64_t row = (int64_t)blockIdx.x * kWarps + warp;
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm<V>) route_kernel(const Rou
       float sum = 0.0f;
 #pragma unroll
       for (int i = 0; i < V; ++i) sum += exp_below(v[i] - most);
-      w = expf(chosen - most) / warp_sum(sum);
+      w = quotient(expf(chosen - most), warp_sum(sum));
     }
     if (lane < p.top) {
       *ids = id;
@@ -400,7 +407,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
     }
     sum = warp_sum(sum);
     // a row of -inf has no probabilities, and no gradient
-    const float r = most == -INFINITY ? 0.0f : 1.0f / sum;
+    const float r = most == -INFINITY ? 0.0f : quotient(1.0f, sum);
     const float own = there ? (most == -INFINITY ? 0.0f : expf(l - most) * r) : 0.0f;
     d = own * g;
     const float all = __shfl_sync(~0u, chosen_sum(d, p.top), 0);
