@@ -190,6 +190,19 @@ def test_odd_rows_among_many_experts(kind, e):
     assert bool(w[nan, 0].isnan().all())
 
 
+@pytest.mark.parametrize("dtype", [F32, BF, HF])
+@pytest.mark.parametrize("e", [40, 128, 256, 1000])
+def test_subnormal_logits(dtype, e):
+    tiny = torch.finfo(dtype).smallest_normal
+    g = torch.Generator(device="cuda").manual_seed(e)
+    logits = (torch.randn(200, e, generator=g, device="cuda") * (tiny / 4)).to(dtype)
+    logits[100:] = -logits[100:].abs()
+    assert bool((logits != 0).any()) and float(logits.abs().max()) < 2 * tiny
+    for kind in KINDS:
+        ids, _ = check_forward(logits, 8, *kind)
+        check_backward(logits, ids, *kind)
+
+
 @pytest.mark.parametrize("normalize", [True, False])
 def test_sigmoids_around_where_their_logarithms_are_taken(normalize):
     rows = [[-58.0, -59.5, -60.0, -60.5], [-59.9, -59.99, -59.0, -59.5], [0.0, -59.9, 3.0, -60.1],
