@@ -85,7 +85,7 @@ def _read(t, m, cols, dtype, dev, what, keep):
     shape = t.shape
     if (len(shape) == 2 and shape[1] == cols and (m is None or shape[0] == m)
             and t.dtype is dtype and t.get_device() == dev):
-        return (t.data_ptr(), *t.stride())
+        return (t.data_ptr(),) + t.stride()
     if t.dtype is not dtype:
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
     if t.get_device() != dev:
@@ -97,13 +97,13 @@ def _read(t, m, cols, dtype, dev, what, keep):
         raise ValueError(f"{what} has {rows} rows, x has {m}")
     t = t.reshape(rows, cols)
     keep.append(t)
-    return (t.data_ptr(), *t.stride())
+    return (t.data_ptr(),) + t.stride()
 
 
 def _write(t, m, cols, dtype, dev, what):
     """An output's address and strides as a matrix; never a copy."""
     if t.shape == (m, cols) and t.dtype is dtype and t.get_device() == dev:
-        return (t.data_ptr(), *t.stride())
+        return (t.data_ptr(),) + t.stride()
     if t.dtype is not dtype:
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
     if t.get_device() != dev:
@@ -111,7 +111,7 @@ def _write(t, m, cols, dtype, dev, what):
     if t.dim() == 0 or t.shape[-1] != cols or t.numel() != m * cols:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {m} rows of {cols}")
     t = t.view(m, cols)
-    return (t.data_ptr(), *t.stride())
+    return (t.data_ptr(),) + t.stride()
 
 
 def _row_count(x):

@@ -41,7 +41,7 @@ dense._MASK["coll_gated_experts"] = _mask("." * 10 + "a.." * 8)
 def _out(t, m, cols, dtype, dev, what):
     """An output's address and strides as a matrix; never a copy."""
     if t.shape == (m, cols) and t.dtype is dtype and t.get_device() == dev:
-        return (t.data_ptr(), *t.stride())
+        return (t.data_ptr(),) + t.stride()
     if t.dtype is not dtype:
         raise ValueError(f"{what} is {t.dtype}, expected {dtype}")
     if t.get_device() != dev:
@@ -49,7 +49,7 @@ def _out(t, m, cols, dtype, dev, what):
     if t.dim() == 0 or t.shape[-1] != cols or t.numel() != m * cols:
         raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {m} rows of {cols}")
     t = t.view(m, cols)
-    return (t.data_ptr(), *t.stride())
+    return (t.data_ptr(),) + t.stride()
 
 
 def _stack(name, w, like=None):
@@ -107,8 +107,8 @@ class Router:
             t = math.prod(shape[:-1])
             rows = logits.reshape(t, e)
             keep.append(rows)
-        return ((t, e, self.top_k, _TYPE[logits.dtype], *self._how),
-                (rows.data_ptr(), *rows.stride()))
+        return ((t, e, self.top_k, _TYPE[logits.dtype]) + self._how,
+                (rows.data_ptr(),) + rows.stride())
 
     @staticmethod
     def _launch(where, packed, dev):
@@ -138,9 +138,9 @@ class Router:
         if weights is None:
             weights = torch.empty(*logits.shape[:-1], top, dtype=torch.float32,
                                   device=logits.device)
-        self._launch("coll_route", _ROUTE.pack(
-            *head, *lm, *_out(ids, t, top, torch.int32, dev, "ids"),
-            *_out(weights, t, top, torch.float32, dev, "weights")), dev)
+        self._launch("coll_route", _ROUTE.pack(*(
+            head + lm + _out(ids, t, top, torch.int32, dev, "ids")
+            + _out(weights, t, top, torch.float32, dev, "weights"))), dev)
         return ids, weights
 
     __call__ = forward
@@ -160,8 +160,7 @@ class Router:
         if dlogits is None:
             dlogits = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
         self._launch("coll_route_backward", _ROUTE_BWD.pack(
-            *head, *gm, *lm, *im,
-            *_out(dlogits, t, e, logits.dtype, dev, "dlogits")), dev)
+            *(head + gm + lm + im + _out(dlogits, t, e, logits.dtype, dev, "dlogits"))), dev)
         return dlogits
 
 
