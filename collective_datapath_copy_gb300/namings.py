@@ -96,7 +96,7 @@ def moe_dispatch(routing: np.ndarray, experts_per_rank: int, hidden: int,
     to every rank hosting one of its experts (expert e lives on rank e // experts_per_rank; an id
     of -1, a choice that was not made, is no expert);
     at a destination, rows are ordered by (source rank, source token). meta["counts"] holds
-    the rows each rank receives.
+    the rows each rank receives, meta["dest"] [R, T, R] which token goes to which rank.
     """
     R, T, k = routing.shape
     dest = np.zeros((R, T, R), dtype=bool)
@@ -159,13 +159,14 @@ def moe_combine(routing: np.ndarray, experts_per_rank: int, hidden: int,
     """Reverse of moe_dispatch with a sum: rank d's input holds, in dispatch order, one row
     per token routed to it; token (s, t) (name s*T+t) receives at rank s the sum of its rows
     over the destination ranks, which the fixed (rank, offset) order visits ascending.
+    A token without an expert (all its ids are -1) receives nothing: its output row is left as it
+    was, and is the caller's to set to zero (its row of meta["dest"] is all False).
     meta["counts"] holds the rows each rank's input has."""
     R, T, k = routing.shape
     disp = moe_dispatch(routing, experts_per_rank, hidden, dtype)
     counts = disp.meta["counts"]
     o_in = disp.out_segs  # dispatch outputs are the combine inputs
-    names = np.arange(R * T)
-    o = _segs_cols(np.repeat(np.arange(R), T), np.tile(np.arange(T), R) * hidden,
-                   np.full(R * T, hidden), names)
+    names = np.nonzero(disp.meta["dest"].any(2).ravel())[0]
+    o = _segs_cols(names // T, names % T * hidden, np.full(len(names), hidden), names)
     return Naming(R, "sum", dtype, list(disp.out_len), o_in.copy(), [T * hidden] * R, o,
                   meta={"counts": counts, "dest": disp.meta["dest"]})
