@@ -107,13 +107,14 @@ def gemv_payloads(wts, xs):
 
 
 def moe_dest_ranks(routing, experts_per_rank):
-    """routing [R, T, k] expert ids -> boolean [R, T, R]: token (s,t) goes to rank d."""
+    """routing [R, T, k] expert ids -> boolean [R, T, R]: token (s,t) goes to rank d. An id of -1
+    is a choice that was not made, and goes nowhere."""
     R = routing.shape[0]
     dest = np.zeros((R, routing.shape[1], R), dtype=bool)
     for s in range(R):
         for j in range(routing.shape[2]):
-            d = routing[s, :, j] // experts_per_rank
-            dest[s, np.arange(routing.shape[1]), d] = True
+            t = np.nonzero(routing[s, :, j] >= 0)[0]
+            dest[s, t, routing[s, t, j] // experts_per_rank] = True
     return dest
 
 
@@ -132,8 +133,8 @@ def moe_dispatch(xs, routing, experts_per_rank):
 
 def moe_combine_sum(ys, routing, experts_per_rank, dtype):
     """Reverse of dispatch with summation: token (s,t) of rank s receives the fixed-order
-    sum, over its destination ranks d ascending, of the row rank d holds for it.
-    ys[d] is [count_d, H] in dispatch order."""
+    sum, over its destination ranks d ascending, of the row rank d holds for it, or nothing
+    (zeros here) where it went to none. ys[d] is [count_d, H] in dispatch order."""
     R = len(ys)
     dest = moe_dest_ranks(routing, experts_per_rank)
     T = routing.shape[1]
@@ -151,6 +152,7 @@ def moe_combine_sum(ys, routing, experts_per_rank, dtype):
         o = np.zeros((T, H), dtype=ys[0].dtype)
         for t in range(T):
             terms = [ys[d][where[(s, t, d)]] for d in range(R) if dest[s, t, d]]
-            o[t] = ordered_sum(terms, dtype)
+            if terms:
+                o[t] = ordered_sum(terms, dtype)
         outs.append(o)
     return outs
