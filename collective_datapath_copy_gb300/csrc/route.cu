@@ -387,9 +387,10 @@ __global__ void __launch_bounds__(kWarps * 32) route_bwd_kernel(const RouteParam
   if (plain) R::load(p, R::row(p, row), lane, v);
   const bool there = (uint32_t)id < (uint32_t)p.e;
   if (there) l = ld_elem(p.logits.p, row * p.logits.rs + id * p.logits.cs, TYPE);
+  else g = 0.0f;  // whatever stands there has no part in the sums
   if (p.norm) {
     const float w = normalised<false>(l, there, p.top, p.score);
-    const float sum = chosen_sum(there ? g * w : 0.0f, p.top);
+    const float sum = chosen_sum(g * w, p.top);
     d = w * (g - sum);
     if (p.score == COLL_SCORE_SIGMOID) d *= sigmoid(-l);
   } else if (p.score == COLL_SCORE_SIGMOID) {

@@ -467,8 +467,9 @@ typedef struct {
 } coll_route_t;
 
 /* dlogits [t][e] of dtype, for the gradient dweights [t][top] (binary32) of the weights and the ids
- * that were chosen (any strides; an id outside 0..e-1 has no part in it). The choice itself has no
- * gradient: with normalize or sigmoid scores, logits that were not chosen get 0. */
+ * that were chosen (any strides; an id outside 0..e-1 and its dweights, whatever they are, have no
+ * part in it). The choice itself has no gradient: with normalize or sigmoid scores, logits that were
+ * not chosen get 0. */
 typedef struct {
   int64_t t, e, top;
   int64_t dtype, score, normalize;

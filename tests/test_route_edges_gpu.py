@@ -1,0 +1,46 @@
+"""Router at the edges of what it documents: gradients of choices that were not made."""
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+import collective_datapath_copy_gb300 as cdc  # noqa: E402
+from collective_datapath_copy_gb300.build import build  # noqa: E402
+
+F32 = torch.float32
+INF = float("inf")
+KINDS = [("softmax", True, 1.0), ("softmax", False, 1.0), ("sigmoid", True, 2.5),
+         ("sigmoid", False, 0.7)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    build()
+    yield
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("e,top", [(9, 6), (60, 4), (256, 8), (700, 20)])
+@pytest.mark.parametrize("value", [float("nan"), INF, -INF])
+def test_the_gradient_of_a_choice_that_was_not_made_is_unread(kind, e, top, value):
+    """An id outside the experts has no part in the gradient, whatever stands in its place."""
+    g = torch.Generator(device="cuda").manual_seed(e)
+    logits = torch.randn(40, e, generator=g, device="cuda")
+    logits[:, 3:] = torch.where(torch.rand(40, 1, generator=g, device="cuda") < 0.5,
+                                logits[:, 3:], torch.full_like(logits[:, 3:], -INF))
+    logits[7] = -INF
+    r = cdc.Router(top, *kind)
+    ids, w = r.forward(logits)
+    assert bool((ids < 0).any())
+    ids[5, 1] = e  # of another table
+    dw = torch.randn(40, top, generator=g, device="cuda")
+    out = (ids < 0) | (ids >= e)
+    want = r.backward(torch.where(out, torch.zeros_like(dw), dw), logits, ids)
+    got = r.backward(torch.where(out, torch.full_like(dw, value), dw), logits, ids)
+    assert bool(want.isfinite().all())
+    assert torch.equal(got, want)
