@@ -1,4 +1,5 @@
-"""Router at the edges of what it documents: gradients of choices that were not made."""
+"""Router at the edges of what it documents: gradients of choices that were not made, scores below
+binary32's normal range."""
 
 import pytest
 
@@ -8,6 +9,7 @@ pytestmark = pytest.mark.gpu
 
 import collective_datapath_copy_gb300 as cdc  # noqa: E402
 from collective_datapath_copy_gb300.build import build  # noqa: E402
+import experts_ref as er  # noqa: E402
 
 F32 = torch.float32
 INF = float("inf")
@@ -44,3 +46,21 @@ def test_the_gradient_of_a_choice_that_was_not_made_is_unread(kind, e, top, valu
     got = r.backward(torch.where(out, torch.full_like(dw, value), dw), logits, ids)
     assert bool(want.isfinite().all())
     assert torch.equal(got, want)
+
+
+def test_sigmoid_scores_below_the_normal_range():
+    """Down to the last subnormal: a score is good to 2^-20 of itself or two steps of 2^-149."""
+    logits = -torch.arange(80.0, 104.0, 0.25, device="cuda").repeat(4, 1)
+    logits[1:] += torch.tensor([[0.1], [0.17], [-0.05]], device="cuda")
+    r = cdc.Router(32, "sigmoid", False)
+    ids, w = r.forward(logits)
+    assert torch.equal(ids.long(), er.choose(logits, 32))
+    for part in (logits[:, :32], logits[:, 32:64], logits[:, 64:]):
+        ids, w = r.forward(part)
+        s = torch.special.expit(torch.gather(part, 1, ids.long()).double())
+        # a product by 1 and the rounding of a subnormal are below a step, expf good to two of them
+        assert bool(((w.double() - s).abs() <= 2.0 ** -20 * s + 2 * 2.0 ** -149).all())
+        # the slope s (1 - s) at -l and at l is the smaller of s and 1 - s
+        for l in (part, -part):
+            dl = torch.gather(r.backward(torch.ones_like(w), l, ids), 1, ids.long()).double()
+            assert bool(((dl - s).abs() <= 2.0 ** -19 * s + 4 * 2.0 ** -149).all())
