@@ -493,7 +493,8 @@ int check_sizes(const T &a) {
     return COLL_EINVAL;
   if (!is_half(a.dtype) && a.dtype != COLL_F32) return COLL_EINVAL;
   if (a.score != COLL_SCORE_SOFTMAX && a.score != COLL_SCORE_SIGMOID) return COLL_EINVAL;
-  return (a.normalize == 0 || a.normalize == 1) && isfinite(a.scale) ? COLL_OK : COLL_EINVAL;
+  // the weights are binary32, and so is what they are multiplied by
+  return (a.normalize == 0 || a.normalize == 1) && fabs(a.scale) <= FLT_MAX ? COLL_OK : COLL_EINVAL;
 }
 
 int check(const coll_route_t &a) {

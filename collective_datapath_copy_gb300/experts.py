@@ -34,6 +34,7 @@ _EXPERTS = struct.Struct("37q")
 _alloc = torch._C._cuda_cudaCachingAllocator_raw_alloc
 _free = torch._C._cuda_cudaCachingAllocator_raw_delete
 _entries = {}
+_MOST = (2.0 - 2.0 ** -23) * 2.0 ** 127  # binary32's largest
 
 dense._MASK["coll_gated_experts"] = _mask("." * 10 + "a.." * 8)
 
@@ -77,8 +78,8 @@ class Router:
             raise ValueError(f"top_k must be 1 to 32, not {top_k}")
         if score not in _lib.SCORE:
             raise ValueError(f"score must be one of {tuple(_lib.SCORE)}, not {score!r}")
-        if not math.isfinite(scale):
-            raise ValueError(f"scale must be finite, not {scale}")
+        if not abs(scale) <= _MOST:
+            raise ValueError(f"scale must be a finite binary32 number, not {scale}")
         self.top_k, self._score = int(top_k), score
         self._how = (_lib.SCORE[score], int(bool(normalize)), float(scale))
 

@@ -457,8 +457,8 @@ int64_t coll_gated_ffn_backward_workspace(const coll_gated_bwd_t *a);
  * index (-0 equals 0; a NaN is the largest), and a weight for each: scale times its score, or with
  * normalize == 1 scale times its score over the chosen scores' sum. A logit of -inf is not chosen:
  * where fewer than `top` others are left, ids ends in -1 with weight 0. 1 <= top <= 32, top <= e
- * <= 1024. logits [t][e] of dtype (COLL_F32, COLL_BF16 or COLL_F16), any strides; ids [t][top]
- * int32; weights [t][top] binary32, as are the sums. */
+ * <= 1024, |scale| at most binary32's largest number. logits [t][e] of dtype (COLL_F32, COLL_BF16
+ * or COLL_F16), any strides; ids [t][top] int32; weights [t][top] binary32, as are the sums. */
 typedef struct {
   int64_t t, e, top;
   int64_t dtype, score, normalize;
