@@ -168,32 +168,43 @@ class Router:
 class GatedExperts(_Dense):
     """y = residual + sum over a token's choices of weight * (act(x w_gate^T) * (x w_up^T)) w_down^T:
     a few tokens through the experts they chose.  w_gate, w_up [E, F, K], w_down [E, N, F],
-    bfloat16 or float16, each one's last dimension contiguous. Updates in place are seen by the next
-    call.
+    bfloat16 or float16, each one's last dimension contiguous. Updates in place and storage that takes
+    the place of a stack's are seen by the next call.
 
     act: "silu", "gelu", "gelu_tanh", "relu" or "sigmoid". first: the id of w_gate[0]; a token's ids
     outside [first, first + E) are passed over."""
 
     def __init__(self, w_gate, w_up, w_down, act="silu", first=0):
-        self._w = (_stack("w_gate", w_gate), _stack("w_up", w_up, w_gate),
-                   _stack("w_down", w_down, w_gate))
-        E, F, K = w_gate.shape
-        if w_up.shape != w_gate.shape or w_down.shape[0] != E or w_down.shape[2] != F:
-            raise ValueError(f"w_up must be {(E, F, K)} and w_down {(E, 'N', F)}, not "
-                             f"{tuple(w_up.shape)} and {tuple(w_down.shape)}")
+        self._w = (_stack("w_gate", w_gate), w_up, w_down)
+        self._start(w_gate.device)
+        self._take(None)
         if act not in GATED_ACTS:
             raise ValueError(f"act must be one of {GATED_ACTS}, not {act!r}")
         if not 0 <= first < 2 ** 31 - 4096:
             raise ValueError(f"first must be the id of an expert, not {first}")
         self.act, self.first = act, int(first)
-        self._sizes = (w_down.shape[1], K, F, E)
-        self._strides = tuple(w.stride()[:2] for w in (w_gate, w_up, w_down))
-        self._start(w_gate.device)
 
-    # one object, one set of stacks: their sizes and strides are taken once
     w_gate = property(lambda self: self._w[0])
     w_up = property(lambda self: self._w[1])
     w_down = property(lambda self: self._w[2])
+
+    def _take(self, now):
+        """The call's view of the stacks, checked: at first, and when `now`, what a call finds of their
+        addresses, shapes, strides and types, is not what the last one found."""
+        wg, wu, wd = self._w
+        _stack("w_gate", wg)
+        _stack("w_up", wu, wg)
+        _stack("w_down", wd, wg)
+        E, F, K = wg.shape
+        if wu.shape != wg.shape or wd.shape[0] != E or wd.shape[2] != F:
+            raise ValueError(f"w_up must be {(E, F, K)} and w_down {(E, 'N', F)}, not "
+                             f"{tuple(wu.shape)} and {tuple(wd.shape)}")
+        if wg.get_device() != self._dev:
+            raise ValueError(f"the weights are on cuda:{wg.get_device()}, the object was made on "
+                             f"cuda:{self._dev}")
+        self._sizes = (wd.shape[1], K, F, E, wg.dtype)
+        self._stacks = tuple(v for w in self._w for v in (w.data_ptr(),) + w.stride()[:2])
+        self._now = now
 
     def _lend(self, fn, pack, fields, need, stream):
         # no tensor around it: making one costs as much as the launches (one token: 14.6 us a call, 10.7 so)
@@ -213,8 +224,11 @@ class GatedExperts(_Dense):
         if stream is not None:
             with _on(stream, dev, (x, ids, weights, residual, out, wg, wu, wd, self._status)):
                 return self.forward(x, ids, weights, residual, out, out_dtype)
-        n, K, F, E = self._sizes
-        dt = wg.dtype
+        now = (wg.data_ptr(), wg.shape, wg.stride(), wg.dtype, wu.data_ptr(), wu.shape, wu.stride(),
+               wu.dtype, wd.data_ptr(), wd.shape, wd.stride(), wd.dtype)
+        if now != self._now:
+            self._take(now)
+        n, K, F, E, dt = self._sizes
         xm = _read(x, None, K, dt, dev, "x", keep)
         m = _row_count(x)
         if ids.dim() == 0:
@@ -234,11 +248,9 @@ class GatedExperts(_Dense):
             if residual.shape != out.shape:
                 residual = residual.expand(out.shape)
             rm = _read(residual, m, n, ot, dev, "residual", keep)
-        gs, us, ds = self._strides
         self._launch("coll_gated_experts", _EXPERTS.pack,
                      (m, n, K, F, E, self.first, top, _TYPE[dt], _TYPE[ot], ACT[self.act],
-                      wg.data_ptr(), *gs, wu.data_ptr(), *us, wd.data_ptr(), *ds, *xm, *im, *sm,
-                      *rm, *ym))
+                      *self._stacks, *xm, *im, *sm, *rm, *ym))
         return out
 
     __call__ = forward
