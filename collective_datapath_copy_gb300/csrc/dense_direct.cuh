@@ -81,7 +81,7 @@ struct Around {
 
 __device__ __forceinline__ void ask16(const uint16_t *p, int k, int len, Around &a) {
   const int off = (int)((uintptr_t)p & 15u);
-  a.whole = 2 * k >= off && k + (48 - off) / 2 <= len;
+  a.whole = k >= off / 2 && k + (48 - off) / 2 <= len;
   const char *q = reinterpret_cast<const char *>(p) - off;
 #pragma unroll
   for (int h = 0; h < 3; ++h) {

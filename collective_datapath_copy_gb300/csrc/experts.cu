@@ -422,11 +422,11 @@ __device__ __forceinline__ void load_weights(const ProductParams &p, const PlanV
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
       const int row = min(4 * j + sub, max(ahead.rows, 1) - 1);
-      word[j] = ((ahead.row + row * pitch) & ~(uintptr_t)127) + ahead.kb * 128 + chunk * 16;
+      word[j] = ((ahead.row + row * pitch) & ~(uintptr_t)127) + (uintptr_t)ahead.kb * 128 + chunk * 16;
     }
     const uintptr_t last = ahead.row + (max(ahead.rows, 1) - 1) * pitch;
     inside = (ahead.row & ~(uintptr_t)127) >= lo &&
-             (last & ~(uintptr_t)127) + (ahead.kb1 + 1) * 128 <= hi;
+             (last & ~(uintptr_t)127) + ((uintptr_t)ahead.kb1 + 1) * 128 <= hi;
   };
   auto ask = [&](uint32_t place) {
     if (lines > 0) {
