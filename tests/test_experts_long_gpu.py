@@ -55,3 +55,48 @@ def test_rows_past_30_bits():
     assert op.status() == _lib.OK
     want = er.experts(x[:, at], ids, s, w[:, :, at], w[:, :, at], wd, "silu", 0, None, BF)
     ref.assert_close(y, want, "y")
+
+
+@pytest.mark.parametrize("n,k", [(512, 8192), (8192, 512)])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_stacks_past_32_bits(n, k, odd):
+    """2^31 elements and more in gate and up, then in down; odd: rows that only loader warps bring."""
+    E, f, m, k = 20, 14336 + odd, 20, k + odd
+    wg = torch.zeros(E, f, k, dtype=BF, device="cuda")
+    wu, wd = torch.zeros_like(wg), torch.zeros(E, n, f, dtype=BF, device="cuda")
+    assert max(wg.numel(), wd.numel()) > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(n + odd)
+    for e in (0, E - 1):
+        for w in (wg, wu):
+            w[e] = normal(g, f, k, scale=k ** -0.5)
+        wd[e] = normal(g, n, f, scale=f ** -0.5)
+    op = cdc.GatedExperts(wg, wu, wd)
+    ids = torch.tensor([[0, E - 1], [E - 1, 5], [7, 3], [E - 1, 0]], dtype=torch.int32, device="cuda")
+    ids = ids.repeat(m // 4, 1)
+    x, s = normal(g, m, k), torch.rand(m, 2, generator=g, device="cuda")
+    y = op.forward(x, ids, s)
+    assert op.status() == _lib.OK
+    at = torch.where(ids == 0, 0, torch.where(ids == E - 1, 1, -1)).int()  # the others' are zero
+    rows = torch.tensor([0, E - 1], device="cuda")
+    want = er.experts(x, at, s, wg[rows], wu[rows], wd[rows], "silu", 0, None, BF)
+    ref.assert_close(y, want, "y")
+    ref.assert_rms(y, want, BF, "y", 2.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("m", [20, 32, 64, 128])  # 32, 64 and 128 columns
+@pytest.mark.parametrize("n,k,f", [(2064, 8192, 4096), (2064, 4099, 2051), (259, 8200, 2049),
+                                   (520, 4097, 8200)])
+def test_long_sums(m, n, k, f, dtype):
+    g = torch.Generator(device="cuda").manual_seed(m + k)
+    E = 2
+    wg, wu = (normal(g, E, f, k, dtype=dtype, scale=k ** -0.5) for _ in range(2))
+    wd = normal(g, E, n, f, dtype=dtype, scale=f ** -0.5)
+    op = cdc.GatedExperts(wg, wu, wd)
+    ids, s = routing(g, m, E, 2)
+    x, r = normal(g, m, k, dtype=dtype), normal(g, m, n, dtype=dtype)
+    y = op.forward(x, ids, s, residual=r)
+    assert op.status() == _lib.OK
+    want = er.experts(x, ids, s, wg, wu, wd, "silu", 0, r, dtype)
+    ref.assert_close(y, want, "y")
+    ref.assert_rms(y, want, dtype, "y", 2.0)
