@@ -85,8 +85,11 @@ cudaError_t dense_pack(DensePack &p, cudaStream_t s);
 // The job's epilogue over accumulators of zero (nothing to sum over).
 cudaError_t dense_empty_sum(const DenseJob &j, cudaStream_t s);
 
-// Launch a kernel that may be set up while its predecessor in the stream still runs; every kernel
-// here waits for it (griddep_wait) before it touches memory.
+// Launch a kernel that may be set up while its predecessor in the stream still runs. A call's first
+// kernel waits for that (griddep_wait) before it touches memory, and every kernel waits before it ends.
+// A later kernel of a call may read before its own wait what an earlier one of the call had waited for
+// before it let its successor start (griddep_launch behind griddep_wait): the caller's arrays, or a plan
+// made two kernels before.
 template <typename... P, typename... A>
 cudaError_t dense_launch(void (*kernel)(P...), dim3 grid, unsigned threads, uint32_t smem,
                          unsigned cluster, cudaStream_t s, A &&...args) {

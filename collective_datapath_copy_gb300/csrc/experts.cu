@@ -512,6 +512,10 @@ __device__ __forceinline__ void load_weights(const ProductParams &p, const PlanV
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
+// The inner value's one rounding, to the operands' type: the sums' matrix instructions take it in no
+// other, and GatedFFN rounds its h alike. (As the sum of two 16-bit numbers it would keep 16 bits or more,
+// for twice the columns in the sums' ring and matrix instructions.) The result is off by 0.0019 to 0.0024
+// of its size in bf16 with it, 0.0017 by its own rounding alone.
 __device__ __forceinline__ void inner_out(const ProductParams &p, int64_t place, int f, int rows,
                                           float (&g)[16], const float (&u)[16]) {
   act_run(g, p.act);
@@ -970,11 +974,16 @@ struct Layout {
 };
 
 // Rows of the inner tiles. 128 and cut where a CTA's length ends, or fewer and whole, which saves the
-// launch that joins them (32 choices of eight experts of 4096 x 1792: 66 us against 68.5; 32 tokens of
-// six, 64 of 2048 x 176: 36.7 against 39.4): whole if that takes less time for as many experts as
-// uniform choices come to, one more and all of them (eight choices of eight experts, six of which were
-// chosen where 5.3 were expected: 61 us whole, 50 cut). A k block takes its bytes at 45 a ns or 300 ns
-// to issue; what cutting costs, 6 us.
+// launch that joins them: whole if that takes less time for as many experts as uniform choices come to,
+// one more and all of them. The times are a model's, a k block its bytes at 45 a ns or 300 ns to issue,
+// cutting 6 us. Both ways measured (us, tokens, choices / experts, sizes):
+//   left whole: 17, 2 / 8, 4096 x 1792 63.8 whole, 68.4 cut; 100 of the same 72.5, 80.8; 32, 6 / 64,
+//   2048 x 176 36.9, 38.2; 64, 8 / 64, 2048 x 704 99.1, 104.5; 32, 8 / 32, 2048 x 768 59.9, 64.4; 40,
+//   2 / 16, 2048 x 1024 43.7, 46.9; 40, 2 / 8, 1024 x 14336 118, 125; but 33, 2 / 8, 1024 x 512 20.3,
+//   19.4 and 20, 4 / 8, 1024 x 1024 23.9, 23.5
+//   cut: 40, 2 / 64, 1024 x 512 36.5, 40.8; 48, 2 / 16, 4096 x 512 45.5, 50.8; 24, 6 / 64, 2048 x 704
+//   85.6, 91.0; 60, 2 / 16, 4096 x 4096 246, 251; 128, 2 / 8, 4096 x 14336 440, 451
+// so it is right to leave tiles whole where it does but for calls of 20 us, and cuts more than it should.
 void inner_tiles(const coll_experts_t &a, Layout &l) {
   ProductParams &p = l.inner;
   const double choices = (double)l.tokens * a.top, e = (double)a.experts;

@@ -13,7 +13,7 @@ constexpr int kExpertsGroup = 128;  // tokens that a launch takes
 // weight in the order of the chunks.
 struct ExpertsPlan {
   int32_t *chunks;   // their number
-  int4 *chunk;       // {expert, first place, choices, 0}
+  int4 *chunk;       // {expert, first place, choices, the expert's first chunk | its chunks << 16}
   int32_t *token;
   float *weight;
 };

@@ -3,8 +3,9 @@
 //   choice      the `top` largest logits of a token, largest first, ties to the lowest index
 //   softmax     p_e = exp(l_e - max) / sum over all e;       sigmoid  s_e = 1 / (1 + exp(-l_e))
 //   weights     scale score_j, or scale score_j / (sum over the chosen): then only the chosen logits
-//               matter, and both scores are taken relative to the largest, exp(a_j - a_0) / sum, with
-//               a = l (softmax) or log s (sigmoid), so that no sum of tiny scores vanishes
+//               matter, and softmax scores are taken relative to the largest, exp(l_j - l_0) / sum;
+//               sigmoids as they are where all chosen logits are above -60, else relative to the
+//               largest too, exp(log s_j - log s_0) / sum, so that no sum of tiny scores vanishes
 //
 // A warp takes a token. Its logits stay in registers, as keys whose unsigned order is that of the
 // numbers, or as they are; choosing is by them alone, so it depends on no computed score. Bound by the
@@ -68,8 +69,9 @@ __device__ __forceinline__ float warp_max(float v) {
   return r;
 }
 
-// exp(d) for d <= 0, off by 2^-22 and d's rounding times log2 e, 2^-23 |d|: for sums and products over
-// all experts, a third of expf's instructions.
+// exp(d) for d <= 0, off by 2^-22 and d's rounding times log2 e, 2^-23 |d|, 0 below 2^-126: for sums and
+// products over all experts, where a term so far below the largest is nothing, a third of expf's
+// instructions.
 __device__ __forceinline__ float exp_below(float d) { return exp2_fast(d * kLog2e); }
 
 // a / b, off by two steps at most, for b up to 2^126 (0 past it). With exact divisions 32768 x 256 took
@@ -314,7 +316,9 @@ __device__ __forceinline__ bool choose_by_rank(int top, int lane, const float (&
 // lets a row's instructions overlap. With exact divisions: 8000 tokens of 1000 12.8 us with one, 10.6 with
 // two; 8192 of 512 8.9 with two, 7.5 with three; 32768 of 256 12.8 with four, 13.9 with five; of 128 16.2
 // with four, 13.3 with six; 5003 of 60 3.0 with four, 3.4 with six, 4.0 with eight (more fit, and the grid
-// has eight an SM).
+// has eight an SM). A row of 1024 and the next one do not fit 128 registers: up to 304 bytes of a thread's
+// go to local memory with two CTAs (168 in 16-byte loads), up to 36 of rows of 512 with three, and that is
+// in these times.
 template <int V>
 constexpr int kPerSm = V <= 2 ? 4 : V <= 4 ? 6 : V <= 8 ? 4 : V <= 16 ? 3 : 2;
 

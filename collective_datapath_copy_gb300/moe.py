@@ -9,7 +9,8 @@ Every rank has all tokens; rank r holds experts [r E/R, (r + 1) E/R):
 
 The shards are views of the whole stacks, so nothing is copied. Prompts go another way: their rows
 through moe_dispatch to the ranks, each expert's through GatedFFN and Linear, back through
-moe_combine. Run as a module for a timing: python -m collective_datapath_copy_gb300.moe [tokens]
+moe_combine, with plans made from that prompt's table (the Router's ids, copied to the host). Run as
+a module for a timing: python -m collective_datapath_copy_gb300.moe [tokens]
 """
 
 from __future__ import annotations
