@@ -64,3 +64,15 @@ def test_sigmoid_scores_below_the_normal_range():
         for l in (part, -part):
             dl = torch.gather(r.backward(torch.ones_like(w), l, ids), 1, ids.long()).double()
             assert bool(((dl - s).abs() <= 2.0 ** -19 * s + 4 * 2.0 ** -149).all())
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+def test_softmax_scores_below_the_normal_range(normalize):
+    """The same for probabilities, next to one of nearly 1."""
+    logits = torch.zeros(60, 32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    logits[:, 1:] = -84 - 20 * torch.rand(60, 31, generator=g, device="cuda")
+    ids, w = cdc.Router(32, normalize=normalize).forward(logits)
+    assert torch.equal(ids.long(), er.choose(logits, 32))
+    p = torch.gather(torch.softmax(logits.double(), 1), 1, ids.long())
+    assert bool(((w.double() - p).abs() <= 2.0 ** -20 * p + 2 * 2.0 ** -149).all())
