@@ -81,10 +81,13 @@ __device__ __forceinline__ float quotient(float a, float b) { return __fdividef(
 __device__ __forceinline__ float log_sigmoid(float l) {
   return fminf(l, 0.0f) - log1pf(expf(-fabsf(l)));
 }
-// Over a number from 1 to 2, so that a score below the normal range is not lost with the quotient.
+// Below -80 the exponential itself, which 1 added to its reciprocal would not change: the quotient over
+// that is 0 from 2^-126 on, where scores still are numbers. Not x / (1 + x) throughout: s and 1 - s, which
+// the gradient multiplies, would then share their errors (9.8e-8 of its size so, 7.2e-8 as they are).
 __device__ __forceinline__ float sigmoid(float l) {
-  const float x = expf(-fabsf(l));
-  return quotient(l < 0.0f ? x : 1.0f, 1.0f + x);
+  const bool far = l < -80.0f;
+  const float x = expf(far ? l : -l);
+  return far ? x : quotient(1.0f, 1.0f + x);
 }
 
 // The sum over the first `top` lanes, which the others have to leave at 0, in those lanes.
