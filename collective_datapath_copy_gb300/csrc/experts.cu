@@ -168,12 +168,15 @@ constexpr uint32_t kTile = 128 * 128;  // bytes of 128 rows of one k block
 constexpr uint32_t kShort = 8;
 
 struct ProductParams {
-  CUtensorMap w[2], b;  // weights {k, rows, experts}; tokens {k, rows}, by four rows or by 16
+  // weights {k, rows, experts}; tokens {k, rows} by four rows, or inner values {k, rows, 2}, by 16 of
+  // them and their rests
+  CUtensorMap w[2], b;
   Choices choices;
   ExpertsPlan plan;     // plan.chunks NULL: every CTA makes its own
   DenseMat res;         // sums only
   void *out;            // inner values [place][out_rs], or y
   int64_t out_rs;
+  int64_t rest;         // inner: elements from a value to its rest
   float *part;          // of cut tiles
   int32_t *status;
   int32_t rows;         // output features of a tile: at most 128
@@ -512,17 +515,13 @@ __device__ __forceinline__ void load_weights(const ProductParams &p, const PlanV
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-// The inner value's one rounding, to the operands' type: the sums' matrix instructions take it in no
-// other, and GatedFFN rounds its h alike. (As the sum of two 16-bit numbers it would keep 16 bits or more,
-// for twice the columns in the sums' ring and matrix instructions.) The result is off by 0.0019 to 0.0024
-// of its size in bf16 with it, 0.0017 by its own rounding alone.
 __device__ __forceinline__ void inner_out(const ProductParams &p, int64_t place, int f, int rows,
                                           float (&g)[16], const float (&u)[16]) {
   act_run(g, p.act);
   uint16_t *o = static_cast<uint16_t *>(p.out) + place * p.out_rs + f;
 #pragma unroll
   for (int i = 0; i < 16; ++i)
-    if (i < rows) o[i * p.out_rs] = f2h(g[i] * u[i], p.type);
+    if (i < rows) split_value(g[i] * u[i], p.type, o[i * p.out_rs], o[i * p.out_rs + p.rest]);
 }
 
 template <bool INNER, bool COPY>
@@ -538,7 +537,7 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
   constexpr int W = INNER ? 2 : 1;
   const uint32_t stages = p.stages, stage_bytes = p.stage_bytes;
   uint32_t tmem_cols = 32;
-  while (tmem_cols < 2u * W * p.cols) tmem_cols *= 2;
+  while (tmem_cols < 4u * p.cols) tmem_cols *= 2;  // two accumulators of g and u, or values and rests
 
   if (threadIdx.x == 0) {
     if (!p.nothing) {
@@ -587,7 +586,7 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
       const uint32_t bar = full0 + 8 * s, at = ring + s * stage_bytes;
       bar_expect(bar, (COPY ? W * (uint32_t)p.rows * 128u : 0u) +
                           (INNER ? (uint32_t)((c.z + 3) / 4) * 512u
-                                 : (uint32_t)((c.z + 15) / 16) * 2048u));
+                                 : (uint32_t)((c.z + 15) / 16) * 4096u));
       if (!COPY) return;
 #pragma unroll
       for (int w = 0; w < W; ++w)
@@ -630,7 +629,7 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
           if (ok && lane < fours) tma_gather4(at + lane * 512u, &p.b, kb * kTileK, tok, bar);
         } else if (elect_one() && ok) {
           for (int i = 0; i < sixteens; ++i)
-            tma_box(at + i * 2048u, &p.b, kb * kTileK, c.y + 16 * i, bar);
+            tma_box3(at + i * 4096u, &p.b, kb * kTileK, c.y + 16 * i, 0, bar);
         }
         __syncwarp();
         if (++s == stages) {
@@ -649,8 +648,9 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
     while (u < end) {
       const Piece q = piece_at<INNER>(p, plan, u, end);
       const uint32_t n = (uint32_t)(plan.chunk[q.chunk].z + 15) & ~15u;
-      const uint32_t idesc = mma_desc(p.type == COLL_BF16, false, false, 128, n);
-      const uint32_t d0 = tmem + d * W * p.cols, d1 = d0 + p.cols;
+      // sums: every 16 columns of values and the 16 of their rests
+      const uint32_t idesc = mma_desc(p.type == COLL_BF16, false, false, 128, INNER ? n : 2 * n);
+      const uint32_t d0 = tmem + d * 2 * p.cols, d1 = d0 + p.cols;
       ok = ok && wait_bar(&sh.abort, free0 + 8 * d, dphase ^ 1u, p.status);
       tc_fence_after();
       uint32_t add = 0;
@@ -723,11 +723,11 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
         const bool live = row < p.rows && f < p.features;
         ok = ok && __all_sync(~0u, wait_bar(&sh.abort, ready0 + 8 * d, dphase, p.status));
         tc_fence_after();
-        const uint32_t from = lanes + d * W * p.cols;
+        const uint32_t from = lanes + d * 2 * p.cols;
         for (int i0 = 0; ok && i0 < c.z; i0 += 16) {
           const int rows = min(16, c.z - i0);
           float v[16];
-          tmem_load16(from + i0, v);
+          tmem_load16(from + (INNER ? i0 : 2 * i0), v);
           if constexpr (INNER) {
             float up[16];
             tmem_load16(from + p.cols + i0, up);
@@ -742,6 +742,10 @@ __global__ void __launch_bounds__(kAllThreads<COPY>, 1)
                 }
             }
           } else {
+            float rest[16];
+            tmem_load16(from + 2 * i0 + 16, rest);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] += rest[i];
             int tok = 0;
             float wt = 0.0f;
             if (lane < rows) {
@@ -846,7 +850,8 @@ __global__ void __launch_bounds__(512) join_kernel(const __grid_constant__ Produ
       const int64_t t = i0 + groups * i;
       if (t >= end) break;
       if constexpr (INNER) {
-        static_cast<uint16_t *>(p.out)[(c.y + t) * p.out_rs + f] = f2h(v[i] * u[i], p.type);
+        uint16_t *h = static_cast<uint16_t *>(p.out) + (c.y + t) * p.out_rs + f;
+        split_value(v[i] * u[i], p.type, h[0], h[p.rest]);
       } else {
         if (p.res.p) v[i] += ld_elem(p.res.p, t * p.res.rs + f * p.res.cs, p.out_type);
         st_elem(p.out, t * p.out_rs + f, v[i], p.out_type);
@@ -914,10 +919,10 @@ bool copied(const coll_mat_t &x, int64_t rows, int64_t k) {
 }
 
 int encode(CUtensorMap *map, int64_t type, int rank, const void *base, const cuuint64_t *dims,
-           const cuuint64_t *strides, uint32_t rows) {
+           const cuuint64_t *strides, uint32_t rows, uint32_t planes = 1) {
   const PFN_cuTensorMapEncodeTiled_v12000 fn = tensor_map_encoder();
   if (!fn) return COLL_ECUDA;
-  const cuuint32_t box[3] = {kTileK, rows, 1}, step[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {kTileK, rows, planes}, step[3] = {1, 1, 1};
   return fn(map,
             type == COLL_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
             (cuuint32_t)rank, const_cast<void *>(base), dims, strides, box, step,
@@ -937,11 +942,20 @@ int encode_stack(CUtensorMap *map, int64_t type, const coll_stack_t &w, int64_t 
   return encode(map, type, 3, w.ptr, dims, strides, (uint32_t)box);
 }
 
+// Rows of tokens, one at a time.
 int encode_rows(CUtensorMap *map, int64_t type, const void *base, int64_t rows, int64_t k,
-                int64_t ld, int box) {
+                int64_t ld) {
   const cuuint64_t dims[2] = {(cuuint64_t)k, (cuuint64_t)rows};
   const cuuint64_t strides[1] = {(cuuint64_t)ld * 2};
-  return encode(map, type, 2, base, dims, strides, (uint32_t)box);
+  return encode(map, type, 2, base, dims, strides, 1);
+}
+
+// Inner values and, behind them all, their rests.
+int encode_pairs(CUtensorMap *map, int64_t type, const void *base, int64_t rows, int64_t k,
+                 int64_t ld) {
+  const cuuint64_t dims[3] = {(cuuint64_t)k, (cuuint64_t)rows, 2};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2, (cuuint64_t)(rows * ld) * 2};
+  return encode(map, type, 3, base, dims, strides, 16, 2);
 }
 
 // The bytes that every row of a stack starts on and is a multiple of: 32, 16, 4 or 2.
@@ -1033,12 +1047,13 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   l.inner_copied = copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f);
   l.outer_copied = copied(a.w_down, a.experts, a.n);
   // columns of a chunk: all tokens, or 64 or 32 where the experts have half as many each at most (100
-  // tokens of two, eight experts of 4096 x 1792: 80 us with 128, 72 with 64, whose ring is deeper)
+  // tokens of two, eight experts of 4096 x 1792: 80 us with 128, 72 with 64, whose ring is deeper); not
+  // more than 64 beside the loader warps' rings
   const bool spread = choices <= 16 * a.experts;
   l.cols = l.direct ? 8
            : l.tokens <= 16 ? 16
            : l.tokens <= 32 || spread ? 32
-           : l.tokens <= 64 || choices <= 32 * a.experts ? 64 : 128;
+           : l.tokens <= 64 || choices <= 32 * a.experts || !l.outer_copied ? 64 : 128;
   l.planned = !l.nothing && !l.direct && (choices > kOwnChoices || !copied(a.x, a.m, a.k));
   l.pack = !l.nothing && !l.direct && !copied(a.x, a.m, a.k);
   l.chunks = chosen + choices / l.cols;
@@ -1080,13 +1095,17 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     q.out_type = (int32_t)a.out_dtype;
     p.act = (int32_t)a.act;
     p.status = q.status = a.status;
-    auto ring = [&](ProductParams &r, int w, uint32_t fixed, uint32_t raw) {
+    // w stacks' rows and b tiles of tokens a stage
+    auto ring = [&](ProductParams &r, int w, int b, uint32_t fixed, uint32_t raw) {
       r.w_bytes = (uint32_t)r.rows * 128u;
-      r.stage_bytes = w * r.w_bytes + (uint32_t)l.cols * 128u;
+      r.stage_bytes = w * r.w_bytes + b * (uint32_t)l.cols * 128u;
       // a matrix instruction reads 128 rows whatever a tile has: slack behind the last stage's
       const uint32_t other = 1024 + kTile - r.w_bytes + fixed + raw;
-      const uint32_t room = raw ? kSmem : kSmem - kJoinSmem;
-      r.stages = room > other ? (int32_t)((room - other) / r.stage_bytes) : 0;
+      auto fit = [&](uint32_t room) {
+        return room > other ? (int32_t)((room - other) / r.stage_bytes) : 0;
+      };
+      r.stages = fit(raw ? kSmem : kSmem - kJoinSmem);
+      if (r.stages < 4) r.stages = fit(kSmem);
       if (r.stages > kMaxStages) r.stages = kMaxStages;
       r.ring = r.stages * r.stage_bytes;
       r.raw = r.ring + fixed;
@@ -1104,9 +1123,9 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     by_hand(q, 0, a.w_down, a.n, a.f);
     const uint32_t sums = (uint32_t)l.tokens * 512u;
     p.lines = 4;
-    ring(p, 2, 0, l.inner_copied ? 0 : 4 * kLineBytes<true>);
+    ring(p, 2, 1, 0, l.inner_copied ? 0 : 4 * kLineBytes<true>);
     for (q.lines = 8; q.lines >= 4; q.lines /= 2) {  // as long as two stages fit beside it
-      ring(q, 1, sums, l.outer_copied ? 0 : q.lines * kLineBytes<false>);
+      ring(q, 1, 2, sums, l.outer_copied ? 0 : q.lines * kLineBytes<false>);
       if (q.stages >= 2) break;
     }
     const uint64_t inner = (uint64_t)2 * l.cols * 512, outer = (uint64_t)l.tokens * 512;
@@ -1153,7 +1172,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     o.weight = reinterpret_cast<float *>(take((uint64_t)l.places * 4));
   }
   d.counters = e.counters = reinterpret_cast<uint32_t *>(take(counters * 4));
-  char *h = take((uint64_t)l.places * l.ld * 2);
+  char *h = take((uint64_t)l.places * l.ld * 4);  // the values, then their rests
   p.part = q.part = e.part = reinterpret_cast<float *>(take(part));
   if (l.pack)
     s.packed = reinterpret_cast<uint16_t *>(take((uint64_t)l.tokens * l.packed_ld * 2));
@@ -1166,6 +1185,7 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   s.out = p.plan = q.plan = o;
   p.out = h;
   p.out_rs = l.ld;
+  p.rest = d.rest = e.rest = l.places * l.ld;
   d.h = reinterpret_cast<uint16_t *>(h);
   d.h_ld = e.x_ld = l.ld;
   e.x = d.h;
@@ -1210,12 +1230,12 @@ int run(const coll_experts_t &a, Layout &l, cudaStream_t s) {
       }
       if (!c && l.outer_copied)
         c = encode_stack(&q.w[0], a.dtype, a.w_down, a.experts, a.n, a.f, q.rows);
-      if (!c) c = encode_rows(&q.b, a.dtype, p.out, l.places, a.f, l.ld, 16);
+      if (!c) c = encode_pairs(&q.b, a.dtype, p.out, l.places, a.f, l.ld);
       // the first group's rows as a trial of them all
       if (!c)
-        c = l.pack ? encode_rows(&p.b, a.dtype, l.plan.packed, l.tokens, a.k, l.packed_ld, 1)
+        c = l.pack ? encode_rows(&p.b, a.dtype, l.plan.packed, l.tokens, a.k, l.packed_ld)
                    : encode_rows(&p.b, a.dtype, a.x.ptr, l.tokens, a.k,
-                                 a.m == 1 ? round_up(a.k, 8) : a.x.rs, 1);
+                                 a.m == 1 ? round_up(a.k, 8) : a.x.rs);
     }
     if (c) return c;
   }
@@ -1232,7 +1252,7 @@ int run(const coll_experts_t &a, Layout &l, cudaStream_t s) {
     const uint16_t *x = static_cast<const uint16_t *>(a.x.ptr) + t * a.x.rs;
     if (l.pack) o.x = DenseMat{x, a.x.rs, a.x.cs};
     else if (!l.direct && t && !l.nothing)
-      c = encode_rows(&p.b, a.dtype, x, tokens, a.k, a.x.rs, 1);
+      c = encode_rows(&p.b, a.dtype, x, tokens, a.k, a.x.rs);
     if (c) return c;
     void *y = static_cast<char *>(a.y.ptr) + t * a.y.rs * oe;
     DenseMat res = {};

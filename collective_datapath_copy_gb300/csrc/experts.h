@@ -2,8 +2,20 @@
 #pragma once
 
 #include "dense.h"
+#include "dense_epi.cuh"
 
 namespace coll {
+
+// An inner value act(g) u as the sum of two numbers of the operands' type, off by 2^-16 of itself in bf16 and
+// 2^-22 in f16: the sums' matrix instructions take 16 bits, and each weight that is read goes into both
+// products. One number alone put the result 0.0019 to 0.0025 of its size off in bf16, where its own rounding is
+// 0.0016 to 0.0017, and took 0 to 4 % less time (one token, 6 of 64 experts of 2048 x 176: 8.0 us, 8.1 with
+// both; 128 of two, eight of 4096 x 14336 452, 463). What is infinite has no rest.
+__device__ __forceinline__ void split_value(float v, int type, uint16_t &value, uint16_t &rest) {
+  value = f2h(v, type);
+  const float r = h2f(value, type);
+  rest = fabsf(r) < INFINITY ? f2h(v - r, type) : (uint16_t)0;
+}
 
 constexpr int kExpertsMost = 1024;  // experts of a call
 constexpr int kChosenMost = 32;     // choices of a token
@@ -35,6 +47,7 @@ struct DirectParams {
   int32_t x_align;       // bytes that rows of x start on and are a multiple of
   uint16_t *h;           // inner: the output
   int64_t h_ld;
+  int64_t rest;          // elements from an inner value to its rest
   uint32_t *counters;    // of the sums' tiles; the inner kernel sets them to 0
   int32_t tiles;
   void *y;               // sums: the output

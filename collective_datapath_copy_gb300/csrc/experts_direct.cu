@@ -173,14 +173,15 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
         v += part[turn][w][n][j];
         u += part[turn][w][n][j + 8];
       }
-      // the one rounding: the sums' matrix instructions take 16 bits
-      p.h[(int64_t)(c.y + n) * p.h_ld + f0 + j] = f2h(act_value(v, p.act) * u, TYPE);
+      uint16_t *h = p.h + (int64_t)(c.y + n) * p.h_ld + f0 + j;
+      split_value(act_value(v, p.act) * u, TYPE, h[0], h[p.rest]);
     }
     // the sums read rows in whole runs of 16
     if (tile == tiles - 1)
       for (int i = threadIdx.x; i < 16 * c.z; i += blockDim.x) {
         const int j = p.features + i % 16;
-        if (j < ((p.features + 15) & ~15)) p.h[(int64_t)(c.y + i / 16) * p.h_ld + j] = 0;
+        uint16_t *h = p.h + (int64_t)(c.y + i / 16) * p.h_ld + j;
+        if (j < ((p.features + 15) & ~15)) h[0] = h[p.rest] = 0;
       }
   }
 }
@@ -189,6 +190,9 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 // neighbouring, and inside a share the warps take steps in turn; each adds its finished products,
 // times their weights, to its own sums in shared memory. The warps join in order, and so do the
 // splits, in the last of their CTAs to arrive.
+//
+// Up to four choices' inner values and their rests are the eight columns of one fragment. More choices
+// take a second fragment for the rests; there are registers for two steps of both at a time.
 template <int TYPE, int ALIGN>
 __global__ void __launch_bounds__(kWarps * 32, 2)
     direct_outer_kernel(const __grid_constant__ DirectParams p) {
@@ -220,6 +224,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   // after the other
   auto flush = [&]() {
     const int4 c = few.chunk[now];
+    if (c.z <= 4) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor_sync(~0u, acc[j], 2);
+    }
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       if (t == q) {
@@ -242,6 +250,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
   while (s < hi) {
     const uint16_t *pa[AHEAD], *pb[AHEAD], *x[AHEAD];
     int at[AHEAD], ka[AHEAD], kb[AHEAD], which[AHEAD], x_len[AHEAD];
+    uint32_t apart = 0;  // steps whose rests are a fragment of their own
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const bool there = s < hi;
@@ -253,8 +262,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
       at[i] = k + 16 * t;
       ka[i] = there ? la : 0;
       kb[i] = there ? lb : 0;
-      x_len[i] = g < c.z ? p.len : 0;
-      x[i] = h + (int64_t)(g < c.z ? c.y + g : 0) * p.x_ld + k;
+      const int choice = c.z <= 4 ? g & 3 : g;
+      x_len[i] = choice < c.z ? p.len : 0;
+      x[i] = h + (int64_t)(choice < c.z ? c.y + choice : 0) * p.x_ld + k;
+      if (c.z > 4) apart |= 1u << i;
+      else if (g >= 4) x[i] += p.rest;
       s += warps;
       at_step += warps;
       while (at_step >= steps) {
@@ -266,19 +278,45 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
     load_rows<ALIGN, AHEAD>(pa, pb, at, ka, kb, r);
     griddep_wait();
     uint32_t xs[AHEAD][8];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) load_x(p, x[i], at[i], x_len[i], xs[i]);
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      if (which[i] < 0) break;
-      if (which[i] != now) {
-        if (now >= 0) flush();
-        now = which[i];
-      }
+    auto begin = [&](int i) {
+      if (which[i] == now) return;
+      if (now >= 0) flush();
+      now = which[i];
+    };
+    auto product = [&](int i, const uint32_t (&b)[8]) {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         mma16816<TYPE>(acc, r.a[i][2 * q], r.b[i][2 * q], r.a[i][2 * q + 1], r.b[i][2 * q + 1],
-                       xs[i][2 * q], xs[i][2 * q + 1]);
+                       b[2 * q], b[2 * q + 1]);
+    };
+    if (apart == 0) {
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) load16<32>(x[i], at[i], x_len[i], xs[i]);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (which[i] < 0) break;
+        begin(i);
+        product(i, xs[i]);
+      }
+    } else {
+      constexpr int HALF = AHEAD / 2;
+#pragma unroll
+      for (int i0 = 0; i0 < AHEAD; i0 += HALF) {
+#pragma unroll
+        for (int j = 0; j < HALF; ++j) {
+          const int i = i0 + j;
+          load16<32>(x[i], at[i], x_len[i], xs[j]);
+          load16<32>(x[i] + p.rest, at[i], apart >> i & 1u ? x_len[i] : 0, xs[HALF + j]);
+        }
+#pragma unroll
+        for (int j = 0; j < HALF; ++j) {
+          const int i = i0 + j;
+          if (which[i] < 0) break;
+          begin(i);
+          product(i, xs[j]);
+          if (apart >> i & 1u) product(i, xs[HALF + j]);
+        }
+      }
     }
   }
   if (now >= 0) flush();

@@ -174,8 +174,8 @@ class GatedExperts(_Dense):
     the place of a stack's are seen by the next call.
 
     act: "silu", "gelu", "gelu_tanh", "relu" or "sigmoid". first: the id of w_gate[0]; a token's ids
-    outside [first, first + E) are passed over. act(...) * (...) is rounded to the weights' type once, and in
-    float16 infinite past 65504; everything else is binary32 until y is rounded."""
+    outside [first, first + E) are passed over. act(...) * (...) is kept to twice the bits of the weights'
+    type, in float16 infinite past 65504; everything else is binary32 until y is rounded."""
 
     def __init__(self, w_gate, w_up, w_down, act="silu", first=0):
         self._w = (_stack("w_gate", w_gate), w_up, w_down)

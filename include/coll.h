@@ -491,9 +491,10 @@ typedef struct {
  * passed over, their weights and experts unread. x [m][k], w_gate and w_up [experts][f][k],
  * w_down [experts][n][f], residual and y [m][n] (y of out_dtype: dtype or COLL_F32, the residual
  * alike), ids [m][top] int32, weights [m][top] binary32; x, ids, weights and residual may have any
- * strides. The inner act(g) u is rounded to dtype once, as coll_gated_ffn rounds its h (in COLL_F16
- * one past 65504 is infinite); everything else is kept in binary32 until y is rounded. An expert
- * chosen twice by a token counts twice.
+ * strides. The inner act(g) u is kept as the sum of two numbers of dtype, to 2^-16 of itself in
+ * COLL_BF16 and 2^-22 in COLL_F16 (2^-25 at least; one past 65504 is infinite there); everything else
+ * is binary32 until y is rounded. Where w_down is infinite, y is infinite or NaN. An expert chosen
+ * twice by a token counts twice.
  * For a few tokens: the weights of every expert that some token chose are read once for every 128
  * tokens. 1 <= experts <= 1024, 1 <= top <= 32. */
 typedef struct {
