@@ -11,9 +11,12 @@
 // 152 equal lengths, because whole tiles would leave SMs idle (8 experts of 2048 inner features are
 // 128 tiles). The shares of a tile that was cut join in a launch behind, in the order of k: nothing
 // waits, and results do not depend on timing. Measured: 128 tokens of two, eight experts of 4096 x 14336
-// (2.8 GB) 451 us, 6.3 TB/s; 32 tokens of eight out of 256, 32 of these experts here, of 7168 x 2048,
-// 280 us, 6.4 TB/s; 16 to 128 tokens over weights of some MB 20 to 25 us, which is the chain of the
+// (2.8 GB) 463 us, 6.1 TB/s; 32 tokens of eight out of 256, 32 of these experts here, of 7168 x 2048,
+// 281 us, 6.4 TB/s; 17 to 128 tokens over weights of some MB 21 to 27 us, which is the chain of the
 // launches: plan 2 us, first weights 3, inner values, join 4, sums, join 4.
+//
+// The sums' columns are inner values and their rests, 16 of each in turn: one tensor copy brings both (two,
+// 33 tokens of two, eight experts of 1024 x 512: 21.9 us, 21.0 so) and one matrix instruction takes them.
 #include <cuda.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -969,8 +972,9 @@ int alignment(const void *base, int64_t es, int64_t e, int64_t rs, int64_t rows,
 // Shared memory for a product's CTA: an SM's. (Half of it, so that the sums' CTAs fit beside the inner
 // values' and bring their weights early, left too few stages: 16 experts of 4096 x 4096, 60 tokens, 265 us
 // against 252; a call of 20 us gained one.) Tensor copies leave room for a CTA of the join, which then makes
-// its plan beside the products (64 experts of 2048 x 704, 16 tokens of six: 86.7 us without, 82.9 with);
-// loader warps need the room themselves (eight of 2001 x 5001, 128 tokens: 137 us, 147 without it).
+// its plan beside the products (64 experts of 2048 x 704, 16 tokens of six: 86.7 us without, 82.9 with), as
+// long as four stages are left; loader warps need the room themselves (eight of 2001 x 5001, 128 tokens: 137
+// us, 147 without it). All three before inner values had their rests.
 constexpr uint32_t kSmem = 227 * 1024 - sizeof(OwnPlan) - sizeof(Shared) - 64;
 constexpr uint32_t kJoinSmem = 1024 + sizeof(OwnPlan) + 512;
 
@@ -991,13 +995,14 @@ struct Layout {
 // launch that joins them: whole if that takes less time for as many experts as uniform choices come to,
 // one more and all of them. The times are a model's, a k block its bytes at 45 a ns or 300 ns to issue,
 // cutting 6 us. Both ways measured (us, tokens, choices / experts, sizes):
-//   left whole: 17, 2 / 8, 4096 x 1792 63.8 whole, 68.4 cut; 100 of the same 72.5, 80.8; 32, 6 / 64,
-//   2048 x 176 36.9, 38.2; 64, 8 / 64, 2048 x 704 99.1, 104.5; 32, 8 / 32, 2048 x 768 59.9, 64.4; 40,
-//   2 / 16, 2048 x 1024 43.7, 46.9; 40, 2 / 8, 1024 x 14336 118, 125; but 33, 2 / 8, 1024 x 512 20.3,
-//   19.4 and 20, 4 / 8, 1024 x 1024 23.9, 23.5
-//   cut: 40, 2 / 64, 1024 x 512 36.5, 40.8; 48, 2 / 16, 4096 x 512 45.5, 50.8; 24, 6 / 64, 2048 x 704
-//   85.6, 91.0; 60, 2 / 16, 4096 x 4096 246, 251; 128, 2 / 8, 4096 x 14336 440, 451
-// so it is right to leave tiles whole where it does but for calls of 20 us, and cuts more than it should.
+//   left whole: 17, 2 / 8, 4096 x 1792 64.6 whole, 67.7 cut; 100 of the same 73.9, 79.9; 32, 6 / 64,
+//   2048 x 176 38.0, 38.2; 64, 8 / 64, 2048 x 704 101, 106; 32, 8 / 32, 2048 x 768 60.7, 64.8; 40,
+//   2 / 16, 2048 x 1024 44.9, 46.6; 40, 2 / 8, 1024 x 14336 120, 126; but 33, 2 / 8, 1024 x 512 21.0,
+//   19.2, 20, 4 / 8, 1024 x 1024 24.5, 23.4 and 12, 4 / 16, 2048 x 512 31.4, 30.9
+//   cut: 40, 2 / 64, 1024 x 512 37.9, 41.5; 48, 2 / 16, 4096 x 512 46.9, 47.6; 24, 6 / 64, 2048 x 704
+//   88.6, 92.9; 60, 2 / 16, 4096 x 4096 249, 253; 128, 2 / 8, 4096 x 14336 455, 463
+// so it is right to leave tiles whole where it does but for calls of 20 to 30 us, and cuts more than it
+// should.
 void inner_tiles(const coll_experts_t &a, Layout &l) {
   ProductParams &p = l.inner;
   const double choices = (double)l.tokens * a.top, e = (double)a.experts;
@@ -1047,8 +1052,8 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
   l.inner_copied = copied(a.w_gate, a.experts, a.f) && copied(a.w_up, a.experts, a.f);
   l.outer_copied = copied(a.w_down, a.experts, a.n);
   // columns of a chunk: all tokens, or 64 or 32 where the experts have half as many each at most (100
-  // tokens of two, eight experts of 4096 x 1792: 80 us with 128, 72 with 64, whose ring is deeper); not
-  // more than 64 beside the loader warps' rings
+  // tokens of two, eight experts of 4096 x 1792: 81 us with 128, 74 with 64, whose ring is deeper; 128 of
+  // 4096 x 14336 468, 462); not more than 64 beside the loader warps' rings, where 128 leave one stage
   const bool spread = choices <= 16 * a.experts;
   l.cols = l.direct ? 8
            : l.tokens <= 16 ? 16

@@ -6,12 +6,13 @@
 // Bound by HBM, and for small experts by latency: two launches, the chunks made by a warp of every CTA
 // from the ids alone, the sums' first weights asked for while the inner values are still being made, the
 // sums' CTAs all on the SMs at once (two waves of them: 24 us where one takes 19, two experts of 4096 x
-// 1792). One token, six of 64 experts of 2048 x 176 (13 MB): 8.0 us, where the tensor-core kernels' cut
-// tiles and joins take 18; two tokens, four of eight experts of 4096 x 14336: 177 us (7 TB/s) against
-// 192; 16 tokens of two, eight of 4096 x 1792: 57 against 63. With more choices a CTA's plan takes
-// longer and an expert's choices fill more chunks: 48 choices within 3 % either way, 96 of 16 experts of
-// 7168 x 2048 224 against 219. The warp's number comes by a shuffle, so that the compiler knows it to be
-// the same for all lanes (one token: 8.3 us without).
+// 1792). One token, six of 64 experts of 2048 x 176 (13 MB): 8.1 us, where the tensor-core kernels' cut
+// tiles and joins take 21; two tokens, four of eight experts of 4096 x 14336: 182 us (6.8 TB/s) against
+// 191; 16 tokens of two, eight of 4096 x 1792: 61 against 64; 32 of one, 16 of 1024 x 512 16.7 against
+// 22.5. With more choices a CTA's plan takes longer and an expert's choices fill more chunks: 48 choices
+// within 3 % either way, 96 of 16 experts of 7168 x 2048 224 against 219 (both before inner values had
+// their rests). The warp's number comes by a shuffle, so that the compiler knows it to be the same for all
+// lanes (one token: 0.3 us more without).
 #include "dense_direct.cuh"
 #include "dense_epi.cuh"
 #include "dense_tc.h"
@@ -68,7 +69,7 @@ __device__ __forceinline__ void make_chunks(const DirectParams &p, Few &few) {
 }
 
 // Tokens off 16 bytes come an element at a time (four tokens of two, eight experts of 4096 x 1792: 49 us,
-// 41.5 on 16 bytes; 16 of them 72, 58; one of six, 64 of 2048 x 176 8.0, 8.0).
+// 42 on 16 bytes; 16 of them 76, 61; one of six, 64 of 2048 x 176 8.1, 8.1).
 __device__ __forceinline__ void load_x(const DirectParams &p, const uint16_t *x, int at, int len,
                                        uint32_t (&r)[8]) {
   if (p.x_align >= 32) load16<32>(x, at, len, r);
@@ -353,8 +354,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 }
 
 // Rows on 4 bytes by eight 4-byte loads a fragment, four steps ahead; through the words around them, as rows
-// on 2 bytes, two ahead (one token, 6 of 64 experts of 2050 x 178: 10.7 us, 13.8 so; two of eight of 4098 x
-// 1790 31.1, 34.2, of 4098 x 14338 173, 184; four tokens of the former 67.7, 71.0, 16 of them 106, 103).
+// on 2 bytes, two ahead (one token, 6 of 64 experts of 2050 x 178: 10.8 us, 14.1 so; two of eight of 4098 x
+// 1790 31.6, 34.3, of 4098 x 14338 173, 185; four tokens of the former 67.7, 71.4, 16 of them 107, 105).
 using Kernel = void (*)(const DirectParams);
 template <bool INNER, int TYPE>
 Kernel pick(int align) {
