@@ -26,7 +26,8 @@ from .plan import Plan
 
 class ExpertParallelMoE:
     """w_router [E, K], w_gate and w_up [E, F, K], w_down [E, K, F], bfloat16 (or float16 with
-    partials="f32"); R divides E; `tokens` rows a call. score, normalize and scale: Router's.
+    partials="f32"); R divides E; `tokens` rows a call. score, normalize and scale: Router's. The
+    ranks hold views of the stacks as they are given: updates in place are seen, other storage is not.
     partials: "bf16" sums rounded partials, "f32" sums them in binary32 and returns y in float32."""
 
     def __init__(self, R, w_router, w_gate, w_up, w_down, top_k, tokens, act="silu",
