@@ -1147,7 +1147,6 @@ int lay_out(const coll_experts_t &a, Layout &l, char *base) {
     d.len = (int32_t)a.k, e.len = (int32_t)a.f;
     d.features = (int32_t)a.f, e.features = (int32_t)a.n;
     d.x_align = alignment(a.x.ptr, 0, 1, a.x.rs, a.m, a.k);
-    e.x_align = 32;
     for (DirectParams *r : {&d, &e}) {
       r->first = (int32_t)a.first, r->experts = (int32_t)a.experts, r->top = (int32_t)a.top;
       r->type = (int32_t)a.dtype, r->out_type = (int32_t)a.out_dtype, r->act = (int32_t)a.act;

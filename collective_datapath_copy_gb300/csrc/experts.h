@@ -44,7 +44,7 @@ struct DirectParams {
   int32_t type, out_type, act;
   int32_t len;           // elements of a row of weights
   int32_t features;      // rows of weights of an expert
-  int32_t x_align;       // bytes that rows of x start on and are a multiple of
+  int32_t x_align;       // inner: bytes that rows of x start on and are a multiple of
   uint16_t *h;           // inner: the output
   int64_t h_ld;
   int64_t rest;          // elements from an inner value to its rest
